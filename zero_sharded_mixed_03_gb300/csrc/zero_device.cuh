@@ -1,0 +1,224 @@
+// zero_device.cuh -- what the device translation units share: element conversions, the AdamW
+// rule, fixed-order sums, bounded mbarrier waits, and a few host helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+#include <string>
+
+#include "zero_internal.h"
+
+namespace zero {
+namespace {
+
+// ------------------------------------------------------------------ host helpers
+
+inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+
+inline int device_sms(int dev)
+{
+    static std::mutex mu;
+    static int cache[64] = {0};
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64) return 0;
+    if (cache[dev] == 0) {
+        int sms = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cache[dev] = sms;
+    }
+    return cache[dev];
+}
+
+inline zero_status_t cuda_fail(cudaError_t e, const char* what)
+{
+    return fail(ZERO_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+// ------------------------------------------------------------------ element helpers
+
+// 16-bit -> fp32 widening (exact).  bf16 is the upper half of an IEEE binary32.
+template <int DT>
+__device__ __forceinline__ float widen1(uint16_t h)
+{
+    if constexpr (DT == ZERO_BF16) return __uint_as_float((uint32_t)h << 16);
+    else return __half2float(__ushort_as_half(h));
+}
+
+template <int DT>
+__device__ __forceinline__ void widen2(uint32_t w, float& lo, float& hi)
+{
+    if constexpr (DT == ZERO_BF16) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+        __half2 h = *reinterpret_cast<const __half2*>(&w);
+        float2 f = __half22float2(h);
+        lo = f.x;
+        hi = f.y;
+    }
+}
+
+// fp32 -> 16-bit, round to nearest even.
+template <int DT>
+__device__ __forceinline__ uint16_t narrow1(float f)
+{
+    if constexpr (DT == ZERO_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    else return __half_as_ushort(__float2half_rn(f));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi)
+{
+    if constexpr (DT == ZERO_BF16) {
+        __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+__device__ __forceinline__ bool nonfinite(float g)
+{
+    return (__float_as_uint(g) & 0x7F800000u) == 0x7F800000u;
+}
+
+// The constants that depend on t, the loss scale and the gradient norm, formed per block.
+struct StepK {
+    float step;   // lr / (1 - beta1^t)
+    float bc2s;   // sqrt(1 - beta2^t)
+    float inv;    // 1 / (N_d * loss_scale)
+    float coef;   // clip mode: min(1, max_norm / (norm + 1e-6)); else 1
+};
+
+// Per-thread sum of the fp32 squares as an unevaluated pair hi + lo of floats, extended by an
+// error-free TwoSum (Knuth) per term: ~48 significant bits from fp32 operations only (GB300's
+// fp64 rate is far below its fp32 rate).  Converted to double once, at the end of the thread.
+struct NormAcc {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float p)
+    {
+        const float s = __fadd_rn(hi, p);
+        const float bp = __fsub_rn(s, hi);
+        const float ap = __fsub_rn(s, bp);
+        const float e = __fadd_rn(__fsub_rn(hi, ap), __fsub_rn(p, bp));
+        hi = s;
+        lo = __fadd_rn(lo, e);
+    }
+    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+};
+
+// AdamW on one element with separately rounded IEEE operations (no contraction):
+//   m = b1 m + (1-b1) g ; v = b2 v + (1-b2) g^2 ; d = sqrt(v)/sqrt(bc2) + eps
+//   p = p - (lr wd) p   ; p = p - (lr/bc1) (m / d)
+// k[0..5] (b1, 1-b1, b2, 1-b2, eps, lr*wd) stay in the kernel parameters.
+__device__ __forceinline__ void adamw1(float g, float& p, float& m, float& v, const float* k,
+                                       const StepK& sk)
+{
+    m = __fadd_rn(__fmul_rn(k[0], m), __fmul_rn(k[1], g));
+    v = __fadd_rn(__fmul_rn(k[2], v), __fmul_rn(k[3], __fmul_rn(g, g)));
+    const float d = __fadd_rn(__fdiv_rn(__fsqrt_rn(v), sk.bc2s), k[4]);
+    p = __fsub_rn(p, __fmul_rn(k[5], p));
+    p = __fsub_rn(p, __fmul_rn(sk.step, __fdiv_rn(m, d)));
+}
+
+__device__ __forceinline__ uint4 ld_stream(const void* p)
+{
+    return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+
+__device__ __forceinline__ uint2 ld_stream8(const void* p)
+{
+    return __ldcs(reinterpret_cast<const uint2*>(p));
+}
+
+// Sum of one double over a block of NT threads in a fixed pattern (shuffle tree per warp,
+// warps in order); the result is valid in thread 0.
+template <int NT>
+__device__ __forceinline__ double block_sum_fixed(double x, double* warp_sum)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xFFFFFFFFu, x, o);
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = x;
+    __syncthreads();
+    double b = 0.0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < NT / 32; ++w) b += warp_sum[w];
+    __syncthreads();
+    return b;
+}
+
+// ------------------------------------------------------------------ bounded barrier waits
+
+constexpr uint32_t kWaitIterCap = 1u << 26;              // polls per wait, whatever the clock
+
+__device__ __forceinline__ uint64_t global_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Non-blocking probe of the same condition.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Wait until the phase of parity `parity` of barrier `bar` has completed.  False when
+// limit_ns of %globaltimer (or kWaitIterCap polls) pass first; limit 0 gives up as soon as
+// the first, non-blocking probe fails.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 0; i < kWaitIterCap; ++i) {
+        if (global_ns() - t0 >= limit_ns) return false;
+        if (mbar_try(bar, parity)) return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+}  // namespace
+}  // namespace zero

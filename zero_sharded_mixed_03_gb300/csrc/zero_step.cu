@@ -11,6 +11,7 @@
 
 #include <cuda.h>
 
+#include "zero_device.cuh"
 #include "zero_kernels.cuh"
 
 namespace zero {
@@ -18,24 +19,8 @@ namespace {
 
 // ------------------------------------------------------------------ host helpers
 
-inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-
 // Elements before the first 16-byte boundary of a 16-bit stream starting at p.
 inline int head16(const void* p) { return (int)(((16 - ((uintptr_t)p % 16)) % 16) / 2); }
-
-int device_sms(int dev)
-{
-    static std::mutex mu;
-    static int cache[64] = {0};
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64) return 0;
-    if (cache[dev] == 0) {
-        int sms = 0;
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cache[dev] = sms;
-    }
-    return cache[dev];
-}
 
 // Resident blocks per SM of one kernel, queried once per kernel.  Kernels of one signature
 // share this template's statics, so the cache is keyed by the kernel's address.
@@ -62,11 +47,6 @@ int grid_for(K kernel, int dev, int64_t work)
     const int64_t cap = (int64_t)device_sms(dev) * blocks_per_sm(kernel);
     const int64_t need = std::max<int64_t>(1, (work + kThreads - 1) / kThreads);
     return (int)std::max<int64_t>(1, std::min(cap, need));
-}
-
-zero_status_t cuda_fail(cudaError_t e, const char* what)
-{
-    return fail(ZERO_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
 DevState* dev_state(const zero_plan* p) { return reinterpret_cast<DevState*>(p->workspace); }
