@@ -63,7 +63,7 @@ typedef enum {
                          call changed nothing it had not finished */
 } zero_status_t;
 
-enum { ZERO_BF16 = 0, ZERO_FP16 = 1 };
+enum { ZERO_BF16 = 0, ZERO_FP16 = 1, ZERO_FP32 = 2 /* zero_adamw gradients only */ };
 
 /* Largest supported N_d (contribution pointers travel in the kernel parameters). */
 #define ZERO_MAX_RANKS 128
@@ -560,6 +560,68 @@ zero_status_t zero_step_range_noalloc(const void* const* grad_contribs, int n_d,
                                       float* v_out, void* out16, const zero_hyper_t* hyper,
                                       int64_t t, double loss_scale, void* stream,
                                       int32_t* nonfinite);
+
+/* ---------------------------------------------------------------------------------------
+ * Operators of a training program around the sharded step: an optimizer for tensors that are not
+ * sharded (zero_adamw).
+ *
+ * Each is asynchronous on `stream`, allocates nothing, may be captured in a CUDA graph and works
+ * on the current device.  Pointers need the alignment of their element type; rows (or tensors)
+ * that start on 16 bytes take the faster path.  ld_* are row strides in elements (0: the rows
+ * follow each other).  Outputs must not overlap inputs or each other except where a call says
+ * so.  Results do not depend on the stream, on other work or on the order blocks finish in.
+ * --------------------------------------------------------------------------------------- */
+
+/* Elements of one tensor that share a pair of 8-bit scales; the moments' buffers hold every
+ * tensor's elements from a multiple of it on, zero-padded. */
+#define ZERO_ADAMW_BLOCK 256
+#define ZERO_ADAMW_MAX_BLOCKS 1073741824
+
+typedef struct zero_adamw zero_adamw_t;
+
+typedef struct {
+    int64_t n_tensors, elems;
+    int64_t n_blocks;        /* blocks of ZERO_ADAMW_BLOCK elements over all tensors */
+    int64_t state_elems;     /* elements of each moment: ZERO_ADAMW_BLOCK * n_blocks */
+    int64_t moment_bytes;    /* bytes of m, and of v */
+    int64_t scale_bytes;     /* 8-bit moments: two bytes a block; else 0 */
+    int64_t workspace_bytes;
+} zero_adamw_info_t;
+
+/* An AdamW optimizer over n_tensors separately held tensors with fp32 parameters, gradients of
+ * grad_type (ZERO_BF16, ZERO_FP16, ZERO_FP32), an optional 16-bit copy (dtype16) of each
+ * parameter, and moments of state_bits (8 or 32) bits.  Host memory only; zero_adamw_destroy. */
+zero_status_t zero_adamw_create(const int64_t* tensor_sizes, int64_t n_tensors, int state_bits, int dtype16,
+                                int grad_type, zero_adamw_t** out);
+zero_status_t zero_adamw_info(const zero_adamw_t* h, zero_adamw_info_t* out);
+
+/* Bind the caller's device buffers: per tensor a parameter (updated in place), a 16-bit copy
+ * (params16 or an entry NULL: none) and a gradient; m, v (info.moment_bytes, 16-byte aligned)
+ * and scales (info.scale_bytes, 8-bit moments), zero at the start of a training run; workspace
+ * (info.workspace_bytes, 16-byte aligned).  t: steps applied so far (0 at the start); -1 with an
+ * earlier bind's workspace keeps its counters, to change tensors' addresses.  Synchronises
+ * `stream`. */
+zero_status_t zero_adamw_bind(zero_adamw_t* h, float* const* params, void* const* params16, const void* const* grads,
+                              void* m, void* v, void* scales, void* workspace, int64_t t, void* stream);
+
+/* One step over every tensor, g = gradient / loss_scale: the rule of zero_step, in place.  With
+ * hyper->max_grad_norm > 0 or ZERO_REPORT_GRAD_NORM a pass over the gradients comes first: their
+ * global norm clips (max_grad_norm), and a step whose gradients' sum of squares is not finite is
+ * skipped whole.  Without, a gradient that is not finite spoils its own element.  8-bit moments:
+ * the update uses the new moments before they are rounded. */
+zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double loss_scale, void* stream);
+
+/* The 8-bit moments as the values that they stand for, in bf16 (which holds each exactly; values
+ * below its range of 2^-133 excepted), info.state_elems each, 16-byte aligned: m, and the root of
+ * v. */
+zero_status_t zero_adamw_export(zero_adamw_t* h, void* m_out, void* root_out, void* stream);
+
+/* t, skipped, skipped_total, finished and grad_norm (-1: none formed; not a number: skipped) after
+ * the work on `stream`, which it synchronises. */
+zero_status_t zero_adamw_read(zero_adamw_t* h, void* stream, zero_step_result_t* out);
+
+/* NULL is ignored. */
+void zero_adamw_destroy(zero_adamw_t* h);
 
 /* Text of the last error of the calling thread (empty if none); valid until its next call. */
 const char* zero_last_error(void);

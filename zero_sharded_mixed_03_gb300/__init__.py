@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libzero.so")
 
 ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ECUDA, ZERO_ESTATE, ZERO_ERANGE, ZERO_ETIMEOUT, ZERO_ENOMEM = range(8)
-ZERO_BF16, ZERO_FP16 = 0, 1
+ZERO_BF16, ZERO_FP16, ZERO_FP32 = 0, 1, 2
 ZERO_MAX_RANKS = 128
 ZERO_REPORT_GRAD_NORM = 1
 (ZERO_OPT_STAGING, ZERO_OPT_WAIT_LIMIT_NS, ZERO_OPT_BULK_TILE, ZERO_OPT_BULK_STAGES,
@@ -28,6 +28,14 @@ ZERO_STAGING_REGISTER_LOADS, ZERO_STAGING_BULK, ZERO_STAGING_AUTO = range(3)
 (ZERO_TABLE_TENSOR_OFFSET, ZERO_TABLE_UNITS, ZERO_TABLE_SHARD_SEGMENTS,
  ZERO_TABLE_BUCKET_SEGMENTS, ZERO_TABLE_STATE_LAYOUT, ZERO_TABLE_PARAM_CHUNKS) = range(6)
 TABLE_COLS = {0: 1, 1: 7, 2: 6, 3: 5, 4: 4, 5: 10}
+ZERO_WEIGHT_OUT_IN, ZERO_WEIGHT_IN_OUT = range(2)
+ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU_TANH, ZERO_ACT_GELU, ZERO_ACT_SILU = range(5)
+ZERO_LINEAR_ACCUMULATE = 1
+ZERO_NORM_RMS, ZERO_NORM_LAYER = range(2)
+ZERO_NORM_PRE, ZERO_NORM_POST = 1, 2
+ZERO_NORM_MAX_DIM = 8192
+ZERO_ADAMW_BLOCK = 256
+ZERO_ADAMW_MAX_BLOCKS = 1073741824
 STATUS_NAMES = {0: "ZERO_OK", 1: "ZERO_EINVAL", 2: "ZERO_EALIGN", 3: "ZERO_ECUDA",
                 4: "ZERO_ESTATE", 5: "ZERO_ERANGE", 6: "ZERO_ETIMEOUT", 7: "ZERO_ENOMEM"}
 
@@ -39,7 +47,9 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_offload_finish", "zero_set_option", "zero_get_option",
             "zero_bind_host_staging", "zero_step_host", "zero_step_host_finish", "zero_grad_norm_host",
             "zero_step_gather_next",
-            "zero_last_error", "zero_plan_destroy", "zero_step_range_noalloc"]
+            "zero_last_error", "zero_plan_destroy", "zero_step_range_noalloc",
+            "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
+            "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
 ZERO_NOALLOC_SCRATCH_BYTES = 256
 
 
@@ -93,6 +103,12 @@ class zero_comm_report_t(ctypes.Structure):
                 ("zero1", ctypes.c_int64), ("zero2", ctypes.c_int64), ("zero3", ctypes.c_int64),
                 ("this_stage", ctypes.c_int64), ("bytes_per_elem", ctypes.c_int64),
                 ("collectives_per_step", ctypes.c_int64)]
+
+
+class zero_adamw_info_t(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in
+                ("n_tensors", "elems", "n_blocks", "state_elems", "moment_bytes", "scale_bytes",
+                 "workspace_bytes")]
 
 
 _lib = None
@@ -177,6 +193,17 @@ def lib() -> ctypes.CDLL:
                                               ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_int32)]
         L.zero_plan_destroy.restype = None
         L.zero_plan_destroy.argtypes = [_vp]
+        L.zero_adamw_create.argtypes = [_vp, _i64, _int, _int, _int, ctypes.POINTER(_vp)]
+        L.zero_adamw_info.argtypes = [_vp, ctypes.POINTER(zero_adamw_info_t)]
+        L.zero_adamw_bind.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+        L.zero_adamw_step.argtypes = [_vp, ctypes.POINTER(zero_hyper_t), ctypes.c_double, _vp]
+        L.zero_adamw_export.argtypes = [_vp, _vp, _vp, _vp]
+        L.zero_adamw_read.argtypes = [_vp, _vp, ctypes.POINTER(zero_step_result_t)]
+        for f in (L.zero_adamw_create, L.zero_adamw_info, L.zero_adamw_bind, L.zero_adamw_step,
+                  L.zero_adamw_export, L.zero_adamw_read):
+            f.restype = st
+        L.zero_adamw_destroy.restype = None
+        L.zero_adamw_destroy.argtypes = [_vp]
         _lib = L
     return _lib
 
@@ -413,6 +440,52 @@ def zero_step_range_noalloc(grad_contribs: Sequence[int], n: int, dtype16: int, 
                                          out16 or None, ctypes.byref(hyper), t, loss_scale,
                                          stream or None, ctypes.byref(flag)))
     return int(flag.value)
+
+
+def zero_adamw_create(tensor_sizes: Sequence[int], state_bits: int, dtype16: int = ZERO_BF16,
+                      grad_type: int = ZERO_BF16) -> int:
+    out = _vp()
+    _check(lib().zero_adamw_create(_i64_array(tensor_sizes), len(tensor_sizes), state_bits, dtype16,
+                                   grad_type, ctypes.byref(out)))
+    return int(out.value)
+
+
+def zero_adamw_info(handle: int) -> zero_adamw_info_t:
+    info = zero_adamw_info_t()
+    _check(lib().zero_adamw_info(handle, ctypes.byref(info)))
+    return info
+
+
+def zero_adamw_bind(handle: int, params: Sequence[int], params16: Optional[Sequence[Optional[int]]],
+                    grads: Sequence[int], m: int, v: int, scales: Optional[int], workspace: int,
+                    t: int = 0, stream: int = 0) -> None:
+    n = zero_adamw_info(handle).n_tensors
+    for ptrs in (params, grads) + ((params16,) if params16 is not None else ()):
+        if len(ptrs) != n:
+            raise ValueError(f"zero_adamw_bind: {len(ptrs)} pointers for {n} tensors")
+    _check(lib().zero_adamw_bind(handle, _ptr_array(params),
+                                 _ptr_array(params16) if params16 is not None else None,
+                                 _ptr_array(grads), m or None, v or None, scales or None,
+                                 workspace or None, t, stream or None))
+
+
+def zero_adamw_step(handle: int, hyper: zero_hyper_t, loss_scale: float = 1.0, stream: int = 0) -> None:
+    _check(lib().zero_adamw_step(handle, ctypes.byref(hyper), loss_scale, stream or None))
+
+
+def zero_adamw_export(handle: int, m_out: int, root_out: int, stream: int = 0) -> None:
+    _check(lib().zero_adamw_export(handle, m_out or None, root_out or None, stream or None))
+
+
+def zero_adamw_read(handle: int, stream: int = 0) -> zero_step_result_t:
+    res = zero_step_result_t()
+    _check(lib().zero_adamw_read(handle, stream or None, ctypes.byref(res)), res)
+    return res
+
+
+def zero_adamw_destroy(handle: int) -> None:
+    if handle:
+        lib().zero_adamw_destroy(handle)
 
 
 def hyper(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, max_grad_norm=0.0,
