@@ -144,7 +144,7 @@ def check(opt, h, t, loss_scale=1.0, max_norm=0.0):
         half = 0.5 * 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(y, 1e-300))), -13) - 4 + e[:, 1] - 127)
         dr = dr + np.where(r1 > 0, half * (1 + 1e-6), 0)
         low = (r1 > 0) & (y < 2.0 ** -17)
-        dr = np.where(low, 2.0 ** (e[:, 1] - 127 - 17), dr)
+        dr = dr + np.where(low, 2.0 ** (e[:, 1] - 127 - 17), 0)
         assert np.all(gr[r1 > 2 * np.sqrt(2.0 ** -148)] > 0)
         # scales follow the block's largest value (a power of two apart only at a boundary)
         top = np.zeros(opt.info.n_blocks)
