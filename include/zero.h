@@ -562,8 +562,9 @@ zero_status_t zero_step_range_noalloc(const void* const* grad_contribs, int n_d,
                                       int32_t* nonfinite);
 
 /* ---------------------------------------------------------------------------------------
- * Operators of a training program around the sharded step: an optimizer for tensors that are not
- * sharded (zero_adamw).
+ * Operators of a training program around the sharded step: what a gathered unit's weights are
+ * used for and what fills the gradient contributions (zero_linear and its gradients), and an
+ * optimizer for tensors that are not sharded (zero_adamw).
  *
  * Each is asynchronous on `stream`, allocates nothing, may be captured in a CUDA graph and works
  * on the current device.  Pointers need the alignment of their element type; rows (or tensors)
@@ -571,6 +572,62 @@ zero_status_t zero_step_range_noalloc(const void* const* grad_contribs, int n_d,
  * follow each other).  Outputs must not overlap inputs or each other except where a call says
  * so.  Results do not depend on the stream, on other work or on the order blocks finish in.
  * --------------------------------------------------------------------------------------- */
+
+/* How a weight is stored: (out_features, in_features) rows, or (in_features, out_features). */
+enum { ZERO_WEIGHT_OUT_IN = 0, ZERO_WEIGHT_IN_OUT = 1 };
+/* Activations: gelu is x Phi(x), gelu_tanh its tanh form, silu x / (1 + exp(-x)). */
+enum { ZERO_ACT_NONE = 0, ZERO_ACT_RELU = 1, ZERO_ACT_GELU_TANH = 2, ZERO_ACT_GELU = 3, ZERO_ACT_SILU = 4 };
+#define ZERO_LINEAR_ACCUMULATE 1
+#define ZERO_LINEAR_MAX_SIZE 1073741824   /* rows, in_features, out_features */
+
+/* One linear layer; 16-bit tensors (dtype16), sums in fp32.  W = the (in, out) matrix `w` stands
+ * for.  NULL pointers leave a part out where that is said.
+ *   forward   z = x W + bias;  y = act(z) + residual          pre: z, kept for the gradient
+ *   backward  dz = dy * act'(pre);  dx = dz W^T;  dw = x^T dz (stored as w is);  dbias = sum of
+ *             dz's rows.  dz is rounded to dtype16 for the two products.  The residual's
+ *             gradient is dy itself. */
+typedef struct {
+    int64_t rows, in_features, out_features;
+    int32_t dtype16;         /* ZERO_BF16 or ZERO_FP16, every tensor */
+    int32_t layout;          /* ZERO_WEIGHT_* */
+    int32_t activation;      /* ZERO_ACT_* */
+    int32_t flags;           /* ZERO_LINEAR_ACCUMULATE: dw and dbias are added to what is there
+                                (one more micro-batch of the same contribution) */
+    int64_t ld_x, ld_w, ld_y, ld_pre, ld_residual, ld_dy, ld_dx, ld_dw;
+    const void* x;           /* rows x in */
+    const void* w;
+    const void* bias;        /* out, or NULL */
+    const void* residual;    /* forward: rows x out, or NULL */
+    void* y;                 /* forward: rows x out; may be `residual` with the same stride */
+    void* pre;               /* rows x out; forward: written unless NULL; backward: read, needed
+                                unless activation is ZERO_ACT_NONE */
+    const void* dy;          /* backward: rows x out */
+    void* dx;                /* backward: rows x in, or NULL */
+    void* dw;                /* backward: as w, or NULL */
+    void* dbias;             /* backward: out, or NULL */
+} zero_linear_t;
+
+/* Bytes of device workspace that zero_linear (backward == 0) or zero_linear_backward needs for
+ * these sizes, strides and pointers (their alignment counts): partial sums of a product split
+ * along its inner dimension, dz, and copies of operands whose rows do not start on 16 bytes.
+ * Host-only.  0 is possible. */
+zero_status_t zero_linear_workspace(const zero_linear_t* a, int backward, int64_t* bytes);
+
+/* Forward of one linear layer.  workspace: at least zero_linear_workspace bytes, 16-byte aligned
+ * (NULL if that is 0); its contents need not survive between calls, but calls that may overlap
+ * on the GPU need one each.  ZERO_EINVAL / ZERO_EALIGN / ZERO_ERANGE (a size beyond
+ * ZERO_LINEAR_MAX_SIZE, or a workspace that is too small) before anything is enqueued.  rows == 0 does nothing;
+ * in_features == 0 gives z = bias. */
+zero_status_t zero_linear(const zero_linear_t* a, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradients of one linear layer (see zero_linear_t); at least one of dx, dw, dbias.  rows == 0
+ * writes zeros to dw and dbias (nothing with ZERO_LINEAR_ACCUMULATE). */
+zero_status_t zero_linear_backward(const zero_linear_t* a, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The matrix-product kernels' only waits are on shared-memory barriers; each is bounded (2 s).
+ * ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
+ * synchronises `stream`. */
+zero_status_t zero_linear_check(void* stream);
 
 /* Elements of one tensor that share a pair of 8-bit scales; the moments' buffers hold every
  * tensor's elements from a multiple of it on, zero-padded. */

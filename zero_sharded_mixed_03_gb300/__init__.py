@@ -31,6 +31,7 @@ TABLE_COLS = {0: 1, 1: 7, 2: 6, 3: 5, 4: 4, 5: 10}
 ZERO_WEIGHT_OUT_IN, ZERO_WEIGHT_IN_OUT = range(2)
 ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU_TANH, ZERO_ACT_GELU, ZERO_ACT_SILU = range(5)
 ZERO_LINEAR_ACCUMULATE = 1
+ZERO_LINEAR_MAX_SIZE = 1073741824
 ZERO_NORM_RMS, ZERO_NORM_LAYER = range(2)
 ZERO_NORM_PRE, ZERO_NORM_POST = 1, 2
 ZERO_NORM_MAX_DIM = 8192
@@ -48,6 +49,7 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_bind_host_staging", "zero_step_host", "zero_step_host_finish", "zero_grad_norm_host",
             "zero_step_gather_next",
             "zero_last_error", "zero_plan_destroy", "zero_step_range_noalloc",
+            "zero_linear_workspace", "zero_linear", "zero_linear_backward", "zero_linear_check",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
             "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
 ZERO_NOALLOC_SCRATCH_BYTES = 256
@@ -103,6 +105,16 @@ class zero_comm_report_t(ctypes.Structure):
                 ("zero1", ctypes.c_int64), ("zero2", ctypes.c_int64), ("zero3", ctypes.c_int64),
                 ("this_stage", ctypes.c_int64), ("bytes_per_elem", ctypes.c_int64),
                 ("collectives_per_step", ctypes.c_int64)]
+
+
+class zero_linear_t(ctypes.Structure):
+    """One linear layer's sizes, strides (0: dense) and device pointers; see include/zero.h."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("rows", "in_features", "out_features")] +
+                [(k, ctypes.c_int32) for k in ("dtype16", "layout", "activation", "flags")] +
+                [(k, ctypes.c_int64) for k in ("ld_x", "ld_w", "ld_y", "ld_pre", "ld_residual", "ld_dy",
+                                               "ld_dx", "ld_dw")] +
+                [(k, ctypes.c_void_p) for k in ("x", "w", "bias", "residual", "y", "pre", "dy", "dx",
+                                                "dw", "dbias")])
 
 
 class zero_adamw_info_t(ctypes.Structure):
@@ -193,6 +205,12 @@ def lib() -> ctypes.CDLL:
                                               ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_int32)]
         L.zero_plan_destroy.restype = None
         L.zero_plan_destroy.argtypes = [_vp]
+        L.zero_linear_workspace.argtypes = [ctypes.POINTER(zero_linear_t), _int, ctypes.POINTER(_i64)]
+        L.zero_linear.argtypes = [ctypes.POINTER(zero_linear_t), _vp, _i64, _vp]
+        L.zero_linear_backward.argtypes = [ctypes.POINTER(zero_linear_t), _vp, _i64, _vp]
+        L.zero_linear_check.argtypes = [_vp]
+        for f in (L.zero_linear_workspace, L.zero_linear, L.zero_linear_backward, L.zero_linear_check):
+            f.restype = st
         L.zero_adamw_create.argtypes = [_vp, _i64, _int, _int, _int, ctypes.POINTER(_vp)]
         L.zero_adamw_info.argtypes = [_vp, ctypes.POINTER(zero_adamw_info_t)]
         L.zero_adamw_bind.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
@@ -440,6 +458,27 @@ def zero_step_range_noalloc(grad_contribs: Sequence[int], n: int, dtype16: int, 
                                          out16 or None, ctypes.byref(hyper), t, loss_scale,
                                          stream or None, ctypes.byref(flag)))
     return int(flag.value)
+
+
+def zero_linear_workspace(args: zero_linear_t, backward: bool = False) -> int:
+    """Bytes of workspace that zero_linear (or zero_linear_backward) needs for these arguments."""
+    n = _i64()
+    _check(lib().zero_linear_workspace(ctypes.byref(args), int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def zero_linear(args: zero_linear_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().zero_linear(ctypes.byref(args), workspace or None, workspace_bytes, stream or None))
+
+
+def zero_linear_backward(args: zero_linear_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().zero_linear_backward(ctypes.byref(args), workspace or None, workspace_bytes,
+                                      stream or None))
+
+
+def zero_linear_check(stream: int = 0) -> None:
+    """Raises ZERO_ETIMEOUT if a matrix product's bounded wait ran out since the last call."""
+    _check(lib().zero_linear_check(stream or None))
 
 
 def zero_adamw_create(tensor_sizes: Sequence[int], state_bits: int, dtype16: int = ZERO_BF16,

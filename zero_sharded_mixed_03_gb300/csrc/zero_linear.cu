@@ -1,0 +1,1023 @@
+// zero_linear.cu -- one linear layer of a training program, forward and backward (zero_linear_*):
+//   z = x W + bias, y = act(z) + residual;  dz = dy act'(z), dx = dz W^T, dw = x^T dz, dbias = sum dz
+//
+// The three products are one kernel, D[M, N] = A[M, K] B[N, K]^T, on the fifth-generation tensor
+// cores: TMA tiles in 128-byte swizzled shared memory, tcgen05.mma with fp32 accumulators in
+// TMEM, and an epilogue that reads them back while the next tile is multiplied.  Either operand
+// may be stored along K or along its own rows (the descriptors' major bit), so no weight and no
+// activation is transposed in memory: dw reads x and dz as they are.
+//
+// Operands whose rows do not start on 16 bytes (the TMA rule) are first copied to rows that do;
+// dz is written there by the activation's gradient anyway.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include <cuda.h>
+
+#include "zero_device.cuh"
+
+namespace zero {
+namespace {
+
+constexpr int kBM = 128;                 // rows of a block's tile (a pair of blocks: 256)
+constexpr int kBK = 64;                  // inner elements a stage: 128 bytes, one swizzle row
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 32 * (4 + kEpiWarps);   // TMA, MMA, TMEM allocation, idle; epilogue
+constexpr uint64_t kGemmWaitNs = 2000000000ull;
+constexpr int kEpiCols = 32;             // columns an epilogue warp takes at a time
+constexpr int kEpiBytes = 32 * kEpiCols * 4;
+
+// Set by a kernel whose bounded wait ran out (zero_linear_check reads and clears it).
+__device__ uint32_t g_linear_error;
+
+enum { kVecOut = 1, kVecPre = 2, kVecRes = 4, kVecBias = 8 };
+
+struct Epilogue {
+    uint16_t* out;
+    uint16_t* pre;               // z, or NULL
+    const uint16_t* bias;        // per column, or NULL
+    const uint16_t* residual;    // or NULL
+    int64_t ld_out, ld_pre, ld_res;
+    int32_t act;
+    int32_t vec;                 // which of them allow 16-byte accesses at multiples of 8 columns
+};
+
+struct GemmParams {
+    CUtensorMap a, b;
+    Epilogue epi;
+    float* partial;              // [split][M][ld_partial], when the inner dimension is split
+    int64_t ld_partial;
+    int32_t M, N, k_blocks;
+    int32_t splits, k_per_split; // k_blocks of one split (the last may have fewer)
+    int32_t tiles_m, tiles_n;
+    int32_t a_mn, b_mn;          // operand stored along its own rows (M or N) instead of along K
+    uint32_t idesc;
+};
+
+// ------------------------------------------------------------------ activations
+
+// The logistic function, accurate relative to its value in both tails.
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// The tanh form of gelu is z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3), and gelu itself
+// z erfc(-z / sqrt 2) / 2: neither loses the left tail as 1 + tanh and 1 + erf do.
+__device__ __forceinline__ float gelu_arg(float z) { return 1.5957691216057308f * z * (1.0f + 0.044715f * z * z); }
+
+__device__ __forceinline__ float act_value(float z, int act)
+{
+    switch (act) {
+    case ZERO_ACT_RELU: return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z);   // not a number stays so
+    case ZERO_ACT_GELU_TANH: return z * logistic(gelu_arg(z));
+    case ZERO_ACT_GELU: return 0.5f * z * erfcf(z * -0.7071067811865476f);
+    case ZERO_ACT_SILU: return z * logistic(z);
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float act_slope(float z, int act)
+{
+    switch (act) {
+    case ZERO_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    case ZERO_ACT_GELU_TANH: {
+        const float s = logistic(gelu_arg(z));
+        return s * (1.0f + z * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z));
+    }
+    case ZERO_ACT_GELU:
+        return 0.5f * erfcf(z * -0.7071067811865476f) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
+    case ZERO_ACT_SILU: {
+        const float s = logistic(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+    }
+}
+
+// ------------------------------------------------------------------ eight columns of one row
+
+template <int DT>
+__device__ __forceinline__ void load8(const uint16_t* p, bool vec, int n, float (&x)[8])
+{
+    if (vec && n == 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        widen2<DT>(w.x, x[0], x[1]);
+        widen2<DT>(w.y, x[2], x[3]);
+        widen2<DT>(w.z, x[4], x[5]);
+        widen2<DT>(w.w, x[6], x[7]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < n ? widen1<DT>(p[j]) : 0.0f;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(uint16_t* p, bool vec, int n, const float (&x)[8])
+{
+    if (vec && n == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]),
+                                                  narrow2<DT>(x[4], x[5]), narrow2<DT>(x[6], x[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = narrow1<DT>(x[j]);
+    }
+}
+
+// z: the product; bias, activation and residual in fp32, each output rounded once.
+template <int DT>
+__device__ __forceinline__ void finish8(const Epilogue& E, int64_t row, int64_t col, int n, float (&z)[8],
+                                        const float (&bias)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] += bias[j];
+    if (E.pre) store8<DT>(E.pre + row * E.ld_pre + col, E.vec & kVecPre, n, z);
+    if (E.act != ZERO_ACT_NONE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = act_value(z[j], E.act);
+    }
+    if (E.residual) {
+        float r[8];
+        load8<DT>(E.residual + row * E.ld_res + col, E.vec & kVecRes, n, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += r[j];
+    }
+    store8<DT>(E.out + row * E.ld_out + col, E.vec & kVecOut, n, z);
+}
+
+template <int DT>
+__device__ __forceinline__ void bias8(const Epilogue& E, int64_t col, int n, float (&b)[8])
+{
+    if (E.bias && n > 0) {
+        load8<DT>(E.bias + col, E.vec & kVecBias, n, b);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------ tensor-core building blocks
+
+template <int CG>
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    if constexpr (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"(accumulate)
+            : "memory");
+}
+
+// Arrive on `bar` (of both blocks of a pair) once every product issued so far is done.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    if constexpr (CG == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t leader_address(uint32_t addr)   // the pair's first block's copy of `addr`
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 32 lanes x 32 columns of fp32 from TMEM: this thread's lane's columns.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&x)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor of a 128-byte swizzled operand tile.
+//   stored along K:  rows of 128 bytes, eight of them an atom of 1 KB; atoms 1 KB apart (stride)
+//   stored along MN: 64 elements of MN in 128 bytes, eight K rows an atom; K groups 1 KB apart
+//                    (stride), the next 64 of MN one box of kBK rows on (leading: 8 KB)
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn)
+{
+    const uint64_t leading = mn ? (kBK * 128) >> 4 : 1, stride = 1024 >> 4;
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (leading << 16) | (stride << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// ------------------------------------------------------------------ the product
+
+// Tile (m, n) of item `t`: groups of 8 tile rows are walked column by column, so that what runs
+// at one time shares its operands in L2.
+__device__ __forceinline__ void tile_at(const GemmParams& P, int t, int& m, int& n)
+{
+    constexpr int kGroup = 8;
+    const int per_group = kGroup * P.tiles_n, g = t / per_group, in = t - g * per_group;
+    const int rows = min(kGroup, P.tiles_m - g * kGroup);
+    n = in / rows;
+    m = g * kGroup + (in - n * rows);
+}
+
+template <int CG, int BN>
+struct GemmShape {
+    static constexpr int kBRows = BN / CG;                       // B rows one block stages
+    static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBRows * kBK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = 6;
+    static constexpr int kTmemCols = 2 * BN;                     // two accumulators
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 256;
+};
+
+// CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2
+// of B, the first one issues products that read both, and each keeps the accumulators of its own
+// 128 rows.  CG = 1: one block, 128 x BN.
+template <int CG, int BN, int DT>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmParams P)
+{
+    using S = GemmShape<CG, BN>;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t epi0 = base + S::kStages * S::kStageBytes;
+    const uint32_t bars = epi0 + kEpiWarps * kEpiBytes;
+    const uint32_t full0 = bars, empty0 = full0 + 8 * S::kStages, acc_full0 = empty0 + 8 * S::kStages,
+                   acc_empty0 = acc_full0 + 16, tmem_slot = acc_empty0 + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const int n_items = P.tiles_m * P.tiles_n * P.splits;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full0 + 8 * i, 1);
+            mbar_init(acc_empty0 + 8 * i, kEpiWarps * CG);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.b) : "memory");
+    }
+    if (warp == 2) {
+        if constexpr (CG == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "n"(S::kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "n"(S::kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    uint32_t tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+
+    bool ok = true;
+    if (warp == 0) {
+        // ---- producer: one thread
+        if (lane == 0) {
+            uint32_t k = 0;
+            for (int item = first; item < n_items && ok; item += step) {
+                const int split = item % P.splits;
+                int m, n;
+                tile_at(P, item / P.splits, m, n);
+                const int row_a = (m * CG + (int)rank) * kBM, row_b = n * BN + (int)rank * S::kBRows;
+                const int kb0 = split * P.k_per_split, kb1 = min(P.k_blocks, kb0 + P.k_per_split);
+                for (int kb = kb0; kb < kb1; ++kb, ++k) {
+                    const uint32_t s = k % S::kStages, use = k / S::kStages;
+                    if (use > 0 && !mbar_wait(empty0 + 8 * s, (use - 1) & 1, kGemmWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a = base + s * S::kStageBytes, b = a + S::kABytes;
+                    uint32_t bar = full0 + 8 * s;
+                    if (rank == 0) mbar_arrive_expect_tx(bar, CG * S::kStageBytes);
+                    if constexpr (CG == 2) bar = leader_address(bar);
+                    if (P.a_mn) {
+                        for (int i = 0; i < kBM / 64; ++i)
+                            tma_load_2d<CG>(a + i * (kBK * 128), &P.a, row_a + 64 * i, kb * kBK, bar);
+                    } else {
+                        tma_load_2d<CG>(a, &P.a, kb * kBK, row_a, bar);
+                    }
+                    if (P.b_mn) {
+                        for (int i = 0; i < S::kBRows / 64; ++i)
+                            tma_load_2d<CG>(b + i * (kBK * 128), &P.b, row_b + 64 * i, kb * kBK, bar);
+                    } else {
+                        tma_load_2d<CG>(b, &P.b, kb * kBK, row_b, bar);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products: one thread of the leading block
+        if (lane == 0 && rank == 0) {
+            uint32_t k = 0, tile = 0;
+            for (int item = first; item < n_items && ok; item += step, ++tile) {
+                const int split = item % P.splits;
+                const int kb0 = split * P.k_per_split, kb1 = min(P.k_blocks, kb0 + P.k_per_split);
+                const uint32_t acc = tile & 1, use = tile >> 1;
+                if (use > 0 && !mbar_wait(acc_empty0 + 8 * acc, (use - 1) & 1, kGemmWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int kb = kb0; kb < kb1; ++kb, ++k) {
+                    const uint32_t s = k % S::kStages;
+                    if (!mbar_wait(full0 + 8 * s, (k / S::kStages) & 1, kGemmWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t a = base + s * S::kStageBytes, b = a + S::kABytes;
+                    const uint64_t da = smem_desc(a, P.a_mn), db = smem_desc(b, P.b_mn);
+                    // 16 inner elements: 32 bytes along K, two groups of eight K rows along MN
+                    const uint64_t sa = P.a_mn ? 2048 >> 4 : 32 >> 4, sb = P.b_mn ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+                    for (int i = 0; i < kBK / 16; ++i)
+                        mma_f16<CG>(tmem + acc * BN, da + sa * i, db + sb * i, P.idesc, kb > kb0 || i > 0);
+                    mma_commit<CG>(empty0 + 8 * s);
+                }
+                if (!ok) break;
+                mma_commit<CG>(acc_full0 + 8 * acc);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue: warp w reads TMEM lanes 32 (w % 4) on; the two warps of a lane group take
+        // alternate column chunks
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t stage = epi0 + (warp - 4) * kEpiBytes;
+        const uint32_t acc_empty_leader = CG == 2 ? leader_address(acc_empty0) : acc_empty0;
+        uint32_t tile = 0;
+        for (int item = first; item < n_items && ok; item += step, ++tile) {
+            const int split = item % P.splits;
+            int m, n;
+            tile_at(P, item / P.splits, m, n);
+            const uint32_t acc = tile & 1, use = tile >> 1;
+            const int64_t row0 = (int64_t)(m * CG + (int)rank) * kBM + quad * 32;
+            ok = mbar_wait(acc_full0 + 8 * acc, use & 1, kGemmWaitNs);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
+                const int64_t col = (int64_t)n * BN + c + (lane & 3) * 8;   // this lane's eight columns
+                if ((int64_t)n * BN + c >= P.N) break;
+                float x[32];
+                tmem_load32(tmem + acc * BN + c + ((uint32_t)(quad * 32) << 16), x);
+                // transposed through shared memory: 16-byte pieces, exchanged within eight rows so
+                // that neither side has bank conflicts
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t at = stage + lane * 128 + ((i ^ (lane & 7)) << 4);
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(x[4 * i]), "f"(x[4 * i + 1]),
+                                 "f"(x[4 * i + 2]), "f"(x[4 * i + 3])
+                                 : "memory");
+                }
+                __syncwarp();
+                const int cols = (int)max((int64_t)0, min((int64_t)8, P.N - col));
+                float bias[8];
+                if (!P.partial) bias8<DT>(P.epi, col, cols, bias);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 8 + (lane >> 2), p = (lane & 3) * 2;
+                    float z[8];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t at = stage + r * 128 + (((p + j) ^ (r & 7)) << 4);
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(z[4 * j]), "=f"(z[4 * j + 1]), "=f"(z[4 * j + 2]), "=f"(z[4 * j + 3])
+                                     : "r"(at)
+                                     : "memory");
+                    }
+                    const int64_t row = row0 + r;
+                    if (row < P.M && cols > 0) {
+                        if (P.partial) {
+                            float4* q = reinterpret_cast<float4*>(P.partial + ((int64_t)split * P.M + row) * P.ld_partial + col);
+                            q[0] = make_float4(z[0], z[1], z[2], z[3]);
+                            q[1] = make_float4(z[4], z[5], z[6], z[7]);
+                        } else {
+                            finish8<DT>(P.epi, row, col, cols, z, bias);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) arrive_cluster(acc_empty_leader + 8 * acc);
+                else mbar_arrive(acc_empty0 + 8 * acc);
+            }
+        }
+    }
+    if (!ok) {
+        // A wait ran out: say so, and give copies and products in flight time to end before the
+        // block's memory is given back.
+        if (lane == 0) atomicOr(&g_linear_error, 1u);
+        const uint64_t t0 = global_ns();
+        for (uint32_t i = 0; i < kWaitIterCap && global_ns() - t0 < 100000000ull; ++i) __nanosleep(1000);
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 2) {
+        if constexpr (CG == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
+    }
+}
+
+// The partial products of a split inner dimension, summed in order, with the epilogue; also the
+// product over an empty inner dimension (no splits: z = 0).
+template <int DT>
+__global__ void __launch_bounds__(256) split_sum_kernel(const float* partial, int64_t ld, int splits, int64_t M,
+                                                        int64_t N, const __grid_constant__ Epilogue E)
+{
+    const int64_t per_row = (N + 7) / 8, total = M * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
+        const int n = (int)min((int64_t)8, N - col);
+        float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, bias[8];
+        for (int s = 0; s < splits; ++s) {
+            const float4* q = reinterpret_cast<const float4*>(partial + ((int64_t)s * M + row) * ld + col);
+            const float4 a = __ldcs(q), b = __ldcs(q + 1);
+            z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+            z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+        }
+        bias8<DT>(E, col, n, bias);
+        finish8<DT>(E, row, col, n, z, bias);
+    }
+}
+
+// ------------------------------------------------------------------ dz, and aligned copies
+
+struct DzParams {
+    const uint16_t* dy;
+    const uint16_t* pre;     // NULL: the activation is none
+    uint16_t* dz;            // rows of ld_dz elements, 16-byte aligned; NULL: only the sums
+    float* sums;             // [row chunk][ld_dz] column sums, or NULL
+    int64_t rows, cols, ld_dy, ld_pre, ld_dz;
+    int32_t act, vec_dy, vec_pre, chunk;   // chunk: rows a block takes
+};
+
+// dz = dy act'(pre), and its column sums: 16 lanes of 8 columns by 16 rows at a time.
+template <int DT>
+__global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams P)
+{
+    __shared__ float part[16][128 + 4];
+    const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+    const int64_t col = (int64_t)blockIdx.x * 128 + cx * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, P.cols - col));
+    const int64_t r0 = (int64_t)blockIdx.y * P.chunk, r1 = min(P.rows, r0 + P.chunk);
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (n > 0) {
+        for (int64_t r = r0 + ry; r < r1; r += 16) {
+            float d[8];
+            load8<DT>(P.dy + r * P.ld_dy + col, P.vec_dy, n, d);
+            if (P.pre) {
+                float z[8];
+                load8<DT>(P.pre + r * P.ld_pre + col, P.vec_pre, n, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] *= act_slope(z[j], P.act);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += j < n ? d[j] : 0.0f;
+            if (P.dz) store8<DT>(P.dz + r * P.ld_dz + col, true, n, d);
+        }
+    }
+    if (!P.sums) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[ry][cx * 8 + j] = sum[j];
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += part[i][threadIdx.x];
+        if (c < P.cols) P.sums[(int64_t)blockIdx.y * P.ld_dz + c] = s;
+    }
+}
+
+// Sums over the row chunks, in order, in fp32.
+template <int DT>
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* sums, int64_t ld, int chunks, int64_t cols,
+                                                         uint16_t* out, int accumulate)
+{
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    float s = 0.0f;
+    for (int i = 0; i < chunks; ++i) s += sums[(int64_t)i * ld + c];
+    if (accumulate) s += widen1<DT>(out[c]);
+    out[c] = narrow1<DT>(s);
+}
+
+// Rows copied to rows of `ld` elements that start on 16 bytes.
+__global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld,
+                                                         int64_t rows, int64_t cols)
+{
+    const int64_t per_row = (cols + 7) / 8, total = rows * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
+        const uint16_t* p = src + row * ld_src + col;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = col + 2 * j < cols ? p[2 * j] : 0u, hi = col + 2 * j + 1 < cols ? p[2 * j + 1] : 0u;
+            w[j] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint4*>(dst + row * ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ------------------------------------------------------------------ host: one product
+
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t up(int64_t a, int64_t b) { return div_up(a, b) * b; }
+
+// A matrix as an operand: `rows` x `inner` (M or N by K) in 16 bits; mn: stored with its rows
+// along memory (inner x rows in memory).
+struct Operand {
+    const void* p;
+    int64_t rows, inner, ld;
+    bool mn;
+};
+
+bool tma_ready(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+// How a product is cut: tile shape and splits of the inner dimension.
+struct Cut {
+    int cg = 2, bn = 256;
+    int splits = 1, per_split = 0;
+    int64_t tiles_m = 0, tiles_n = 0;
+};
+
+constexpr int kGb300Sms = 152;
+
+// The cut with the least estimated time.  A wave of tiles takes its inner blocks at the shape's rate, plus
+// filling and draining; a split product writes and reads its fp32 partial sums once more.
+Cut choose_cut(int64_t M, int64_t N, int64_t K, int sms)
+{
+    struct Shape {
+        int cg, bn;
+        double block_us;   // one inner block of kBK elements of one tile
+    };
+    static const Shape shapes[] = {{2, 256, 0.150}, {1, 128, 0.085}};
+    const int64_t kb = div_up(K, kBK);
+    Cut best;
+    double best_us = 1e30;
+    for (const Shape& s : shapes) {
+        const int64_t tm = div_up(M, kBM * s.cg), tn = div_up(N, s.bn), slots = std::max(1, sms / s.cg);
+        for (int64_t want = 1; want <= std::min<int64_t>(kb, 64); ++want) {
+            const int64_t per = div_up(std::max<int64_t>(kb, 1), want), splits = std::max<int64_t>(1, div_up(kb, per));
+            if (splits != want && want > 1) continue;
+            if (splits > 1 && splits * M * N > ((int64_t)1 << 28)) continue;   // 1 GB of partial sums at most
+            const int64_t waves = div_up(tm * tn * splits, slots);
+            double us = waves * per * s.block_us + 2.0;
+            if (splits > 1) us += 2.5 + (double)(splits * 8 + 2) * M * N / 4.0e6;
+            if (us < best_us) {
+                best_us = us;
+                best.cg = s.cg;
+                best.bn = s.bn;
+                best.splits = (int)splits;
+                best.per_split = (int)per;
+                best.tiles_m = tm;
+                best.tiles_n = tn;
+            }
+        }
+    }
+    return best;
+}
+
+int64_t partial_bytes(const Cut& c, int64_t M, int64_t N) { return c.splits > 1 ? 4 * (int64_t)c.splits * M * up(N, 8) : 0; }
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+zero_status_t encode(CUtensorMap* map, const Operand& o, int dtype16, int box_rows)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return fail(ZERO_ECUDA, "zero_linear: the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[2] = {(cuuint64_t)(o.mn ? o.rows : o.inner), (cuuint64_t)(o.mn ? o.inner : o.rows)};
+    const cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)(o.mn ? kBK : box_rows)};
+    const cuuint32_t unit[2] = {1, 1};
+    const CUresult r = fn(map, dtype16 == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                          const_cast<void*>(o.p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_ECUDA, "zero_linear: a tensor map was refused (" + std::to_string((int)r) + ")");
+}
+
+template <int CG, int BN, int DT>
+zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
+{
+    using S = GemmShape<CG, BN>;
+    static const cudaError_t set =
+        cudaFuncSetAttribute(gemm_kernel<CG, BN, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (set != cudaSuccess) return cuda_fail(set, "zero_linear: shared memory");
+    const int64_t items = (int64_t)P.tiles_m * P.tiles_n * P.splits;
+    const int grid = CG * (int)std::min<int64_t>(std::max(1, sms / CG), items);
+    gemm_kernel<CG, BN, DT><<<grid, kGemmThreads, S::kSmem, s>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+}
+
+inline int grid_of(int64_t items, int sms, int per_sm) { return (int)std::max<int64_t>(1, std::min<int64_t>(div_up(items, 256), (int64_t)sms * per_sm)); }
+
+// D = A B^T with epilogue E; `partial` holds partial_bytes.
+zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epilogue& E, float* partial, int sms, cudaStream_t s)
+{
+    const int64_t M = a.rows, N = b.rows, K = a.inner;
+    if (M == 0 || N == 0) return ZERO_OK;
+    const bool bf = dtype16 == ZERO_BF16;
+    Cut c;
+    if (K > 0) {
+        c = choose_cut(M, N, K, sms);
+        GemmParams P;
+        zero_status_t st = encode(&P.a, a, dtype16, kBM);
+        if (st == ZERO_OK) st = encode(&P.b, b, dtype16, c.bn / c.cg);
+        if (st != ZERO_OK) return st;
+        P.epi = E;
+        P.partial = c.splits > 1 ? partial : nullptr;
+        P.ld_partial = up(N, 8);
+        P.M = (int32_t)M;
+        P.N = (int32_t)N;
+        P.k_blocks = (int32_t)div_up(K, kBK);
+        P.splits = c.splits;
+        P.k_per_split = c.per_split;
+        P.tiles_m = (int32_t)c.tiles_m;
+        P.tiles_n = (int32_t)c.tiles_n;
+        P.a_mn = a.mn;
+        P.b_mn = b.mn;
+        // fp32 accumulators; operand type; which operands lie along their rows; N / 8; M / 16
+        P.idesc = (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((a.mn ? 1u : 0u) << 15) |
+                  ((b.mn ? 1u : 0u) << 16) | ((uint32_t)(c.bn >> 3) << 17) | ((uint32_t)((kBM * c.cg) >> 4) << 24);
+        if (c.cg == 2) st = bf ? launch_shape<2, 256, ZERO_BF16>(P, sms, s) : launch_shape<2, 256, ZERO_FP16>(P, sms, s);
+        else st = bf ? launch_shape<1, 128, ZERO_BF16>(P, sms, s) : launch_shape<1, 128, ZERO_FP16>(P, sms, s);
+        if (st != ZERO_OK || c.splits == 1) return st;
+    } else {
+        c.splits = 0;
+    }
+    const int grid = grid_of(M * div_up(N, 8), sms, 8);
+    if (bf) split_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(partial, up(N, 8), c.splits, M, N, E);
+    else split_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(partial, up(N, 8), c.splits, M, N, E);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+}
+
+// ------------------------------------------------------------------ host: the layer
+
+constexpr int64_t kMaxSize = ZERO_LINEAR_MAX_SIZE;   // tile coordinates stay 32-bit
+
+// Everything a call needs, checked: strides filled in, and where its pieces lie in the workspace.
+struct Layer {
+    zero_linear_t a;
+    bool bf = true;
+    int64_t w_rows = 0, w_cols = 0;        // as stored
+    bool copy_x = false, copy_w = false, make_dz = false;
+    int64_t ld_x8 = 0, ld_w8 = 0, ld_dz = 0;
+    int64_t at_x = 0, at_w = 0, at_dz = 0, at_sums = 0, at_partial = 0, bytes = 0;
+    int chunk = 0, chunks = 0;
+};
+
+// Rows one block of the dz pass takes: enough blocks for the GPU, few enough sums.
+void dz_chunks(int64_t rows, int64_t cols, int* chunk, int* chunks)
+{
+    const int64_t want = std::max<int64_t>(1, 8 * kGb300Sms / std::max<int64_t>(1, div_up(cols, 128)));
+    const int64_t c = std::max<int64_t>(32, up(div_up(std::max<int64_t>(rows, 1), want), 16));
+    *chunk = (int)c;
+    *chunks = (int)div_up(rows, c);
+}
+
+zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* who)
+{
+    const std::string w = std::string(who) + ": ";
+    if (!in) return fail(ZERO_EINVAL, w + "NULL arguments");
+    L->a = *in;
+    zero_linear_t& a = L->a;
+    if (a.rows < 0 || a.in_features < 0 || a.out_features < 0) return fail(ZERO_EINVAL, w + "negative size");
+    if (a.rows > kMaxSize || a.in_features > kMaxSize || a.out_features > kMaxSize)
+        return fail(ZERO_ERANGE, w + "a size beyond ZERO_LINEAR_MAX_SIZE");
+    if (a.dtype16 != ZERO_BF16 && a.dtype16 != ZERO_FP16) return fail(ZERO_EINVAL, w + "bad dtype16");
+    if (a.layout != ZERO_WEIGHT_OUT_IN && a.layout != ZERO_WEIGHT_IN_OUT) return fail(ZERO_EINVAL, w + "bad layout");
+    if (a.activation < ZERO_ACT_NONE || a.activation > ZERO_ACT_SILU) return fail(ZERO_EINVAL, w + "bad activation");
+    if (a.flags & ~(back ? ZERO_LINEAR_ACCUMULATE : 0)) return fail(ZERO_EINVAL, w + "unknown flag");
+    L->bf = a.dtype16 == ZERO_BF16;
+    L->w_rows = a.layout == ZERO_WEIGHT_OUT_IN ? a.out_features : a.in_features;
+    L->w_cols = a.layout == ZERO_WEIGHT_OUT_IN ? a.in_features : a.out_features;
+    struct {
+        int64_t* ld;
+        int64_t cols;
+    } strides[] = {{&a.ld_x, a.in_features}, {&a.ld_w, L->w_cols},         {&a.ld_y, a.out_features},  {&a.ld_pre, a.out_features},
+                   {&a.ld_residual, a.out_features}, {&a.ld_dy, a.out_features}, {&a.ld_dx, a.in_features}, {&a.ld_dw, L->w_cols}};
+    for (auto& s : strides) {
+        if (*s.ld == 0) *s.ld = s.cols;
+        if (*s.ld < s.cols) return fail(ZERO_EINVAL, w + "a row stride is shorter than its row");
+        if (*s.ld > ((int64_t)1 << 38)) return fail(ZERO_ERANGE, w + "a row stride beyond 2^38");
+    }
+    const void* every[] = {a.x, a.w, a.bias, a.residual, a.y, a.pre, a.dy, a.dx, a.dw, a.dbias};
+    for (const void* p : every)
+        if (!aligned(p, 2)) return fail(ZERO_EALIGN, w + "a pointer is not aligned to 2 bytes");
+    const bool any_out = a.rows > 0 && a.out_features > 0;
+    if (!back) {
+        if (any_out && !a.y) return fail(ZERO_EINVAL, w + "y is NULL");
+        if (any_out && a.in_features > 0 && (!a.x || !a.w)) return fail(ZERO_EINVAL, w + "x or w is NULL");
+        if (any_out && a.residual == a.y && a.ld_residual != a.ld_y)
+            return fail(ZERO_EINVAL, w + "y over residual needs its stride");
+        if (any_out && a.pre && a.pre == a.y) return fail(ZERO_EINVAL, w + "pre and y are one buffer");
+    } else {
+        if (!a.dx && !a.dw && !a.dbias) return fail(ZERO_EINVAL, w + "no gradient asked for");
+        if (any_out && !a.dy) return fail(ZERO_EINVAL, w + "dy is NULL");
+        if (any_out && a.activation != ZERO_ACT_NONE && !a.pre) return fail(ZERO_EINVAL, w + "the activation's gradient needs pre");
+        if (any_out && a.in_features > 0 && ((a.dx && !a.w) || (a.dw && !a.x)))
+            return fail(ZERO_EINVAL, w + "x or w is NULL");
+    }
+    // the pieces of the workspace
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    const bool use_x = back ? a.dw != nullptr : true, use_w = back ? a.dx != nullptr : true;
+    const bool product_there = any_out && a.in_features > 0;
+    L->ld_x8 = a.ld_x;
+    L->ld_w8 = a.ld_w;
+    L->ld_dz = a.ld_dy;
+    L->copy_x = product_there && use_x && !tma_ready(a.x, a.ld_x);
+    L->copy_w = product_there && use_w && !tma_ready(a.w, a.ld_w);
+    if (L->copy_x) {
+        L->ld_x8 = up(a.in_features, 8);
+        L->at_x = take(2 * a.rows * L->ld_x8);
+    }
+    if (L->copy_w) {
+        L->ld_w8 = up(L->w_cols, 8);
+        L->at_w = take(2 * L->w_rows * L->ld_w8);
+    }
+    int64_t partial = 0;
+    if (!back) {
+        if (product_there) partial = partial_bytes(choose_cut(a.rows, a.out_features, a.in_features, kGb300Sms), a.rows, a.out_features);
+    } else {
+        const bool products = product_there && (a.dx || a.dw);
+        L->make_dz = products && (a.activation != ZERO_ACT_NONE || !tma_ready(a.dy, a.ld_dy));
+        if (L->make_dz) {
+            L->ld_dz = up(a.out_features, 8);
+            L->at_dz = take(2 * a.rows * L->ld_dz);
+        }
+        dz_chunks(a.rows, a.out_features, &L->chunk, &L->chunks);
+        if (a.dbias && any_out) L->at_sums = take(4 * (int64_t)L->chunks * up(a.out_features, 8));
+        if (product_there && a.dx)
+            partial = std::max(partial, partial_bytes(choose_cut(a.rows, a.in_features, a.out_features, kGb300Sms), a.rows, a.in_features));
+        if (product_there && a.dw)
+            partial = std::max(partial, partial_bytes(choose_cut(L->w_rows, L->w_cols, a.rows, kGb300Sms), L->w_rows, L->w_cols));
+    }
+    L->at_partial = take(partial);
+    L->bytes = at;
+    return ZERO_OK;
+}
+
+zero_status_t check_workspace(const Layer& L, const void* workspace, int64_t bytes, const char* who)
+{
+    if (L.bytes == 0) return ZERO_OK;
+    if (!workspace) return fail(ZERO_EINVAL, std::string(who) + ": workspace is NULL");
+    if (!aligned(workspace, 16)) return fail(ZERO_EALIGN, std::string(who) + ": workspace not 16-byte aligned");
+    if (bytes < L.bytes)
+        return fail(ZERO_ERANGE, std::string(who) + ": workspace of " + std::to_string(bytes) + " bytes, " + std::to_string(L.bytes) + " needed");
+    return ZERO_OK;
+}
+
+int vec_flag(const void* p, int64_t ld, int flag) { return p && aligned(p, 16) && ld % 8 == 0 ? flag : 0; }
+
+zero_status_t align_rows(const void* src, int64_t ld_src, void* dst, int64_t ld, int64_t rows, int64_t cols, cudaStream_t s)
+{
+    align_rows_kernel<<<grid_of(rows * div_up(cols, 8), kGb300Sms, 16), 256, 0, s>>>(
+        static_cast<const uint16_t*>(src), ld_src, static_cast<uint16_t*>(dst), ld, rows, cols);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+}
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+zero_status_t zero_linear_workspace(const zero_linear_t* a, int backward, int64_t* bytes)
+try {
+    if (!bytes) return fail(ZERO_EINVAL, "zero_linear_workspace: NULL argument");
+    Layer L;
+    const zero_status_t st = lay_out(a, backward != 0, &L, "zero_linear_workspace");
+    if (st == ZERO_OK) *bytes = L.bytes;
+    return st;
+}
+catch (...) {
+    return exception_status("zero_linear_workspace");
+}
+
+zero_status_t zero_linear(const zero_linear_t* args, void* workspace, int64_t workspace_bytes, void* stream)
+try {
+    Layer L;
+    zero_status_t st = lay_out(args, false, &L, "zero_linear");
+    if (st == ZERO_OK) st = check_workspace(L, workspace, workspace_bytes, "zero_linear");
+    if (st != ZERO_OK) return st;
+    const zero_linear_t& a = L.a;
+    if (a.rows == 0 || a.out_features == 0) return ZERO_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const void *x = a.x, *w = a.w;
+    if (L.copy_x) {
+        st = align_rows(a.x, a.ld_x, ws + L.at_x, L.ld_x8, a.rows, a.in_features, s);
+        x = ws + L.at_x;
+    }
+    if (st == ZERO_OK && L.copy_w) {
+        st = align_rows(a.w, a.ld_w, ws + L.at_w, L.ld_w8, L.w_rows, L.w_cols, s);
+        w = ws + L.at_w;
+    }
+    if (st != ZERO_OK) return st;
+    Epilogue E;
+    E.out = static_cast<uint16_t*>(a.y);
+    E.pre = static_cast<uint16_t*>(a.pre);
+    E.bias = static_cast<const uint16_t*>(a.bias);
+    E.residual = static_cast<const uint16_t*>(a.residual);
+    E.ld_out = a.ld_y;
+    E.ld_pre = a.ld_pre;
+    E.ld_res = a.ld_residual;
+    E.act = a.activation;
+    E.vec = vec_flag(a.y, a.ld_y, kVecOut) | vec_flag(a.pre, a.ld_pre, kVecPre) |
+            vec_flag(a.residual, a.ld_residual, kVecRes) | vec_flag(a.bias, 0, kVecBias);
+    const Operand A{x, a.rows, a.in_features, L.ld_x8, false};
+    const Operand B{w, a.out_features, a.in_features, L.ld_w8, a.layout == ZERO_WEIGHT_IN_OUT};
+    return product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, s);
+}
+catch (...) {
+    return exception_status("zero_linear");
+}
+
+zero_status_t zero_linear_backward(const zero_linear_t* args, void* workspace, int64_t workspace_bytes, void* stream)
+try {
+    Layer L;
+    zero_status_t st = lay_out(args, true, &L, "zero_linear_backward");
+    if (st == ZERO_OK) st = check_workspace(L, workspace, workspace_bytes, "zero_linear_backward");
+    if (st != ZERO_OK) return st;
+    const zero_linear_t& a = L.a;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const bool accumulate = a.flags & ZERO_LINEAR_ACCUMULATE, any_out = a.rows > 0 && a.out_features > 0;
+    const void *x = a.x, *w = a.w, *dz = a.dy;
+    if (L.copy_x) {
+        st = align_rows(a.x, a.ld_x, ws + L.at_x, L.ld_x8, a.rows, a.in_features, s);
+        x = ws + L.at_x;
+    }
+    if (st == ZERO_OK && L.copy_w) {
+        st = align_rows(a.w, a.ld_w, ws + L.at_w, L.ld_w8, L.w_rows, L.w_cols, s);
+        w = ws + L.at_w;
+    }
+    if (st != ZERO_OK) return st;
+    float* sums = a.dbias && any_out ? reinterpret_cast<float*>(ws + L.at_sums) : nullptr;
+    if (L.make_dz || sums) {
+        DzParams D;
+        D.dy = static_cast<const uint16_t*>(a.dy);
+        D.pre = a.activation != ZERO_ACT_NONE ? static_cast<const uint16_t*>(a.pre) : nullptr;
+        D.dz = L.make_dz ? reinterpret_cast<uint16_t*>(ws + L.at_dz) : nullptr;
+        D.sums = sums;
+        D.rows = a.rows;
+        D.cols = a.out_features;
+        D.ld_dy = a.ld_dy;
+        D.ld_pre = a.ld_pre;
+        D.ld_dz = up(a.out_features, 8);
+        D.act = a.activation;
+        D.vec_dy = vec_flag(a.dy, a.ld_dy, 1);
+        D.vec_pre = vec_flag(a.pre, a.ld_pre, 1);
+        D.chunk = L.chunk;
+        const dim3 grid((unsigned)div_up(a.out_features, 128), (unsigned)L.chunks);
+        if (L.bf) dz_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(D);
+        else dz_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(D);
+        if (L.make_dz) dz = D.dz;
+    }
+    if (a.dbias && a.out_features > 0 && !(a.rows == 0 && accumulate)) {
+        const unsigned grid = (unsigned)div_up(a.out_features, 256);
+        const int chunks = any_out ? L.chunks : 0;
+        uint16_t* db = static_cast<uint16_t*>(a.dbias);
+        if (L.bf) column_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(sums, up(a.out_features, 8), chunks, a.out_features, db, accumulate);
+        else column_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(sums, up(a.out_features, 8), chunks, a.out_features, db, accumulate);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "zero_linear_backward: launch");
+    float* partial = reinterpret_cast<float*>(ws + L.at_partial);
+    Epilogue E;
+    std::memset(&E, 0, sizeof(E));
+    E.act = ZERO_ACT_NONE;
+    if (a.dx) {
+        E.out = static_cast<uint16_t*>(a.dx);
+        E.ld_out = a.ld_dx;
+        E.vec = vec_flag(a.dx, a.ld_dx, kVecOut);
+        const Operand A{dz, a.rows, a.out_features, L.ld_dz, false};
+        const Operand B{w, a.in_features, a.out_features, L.ld_w8, a.layout == ZERO_WEIGHT_OUT_IN};
+        st = product(A, B, a.dtype16, E, partial, kGb300Sms, s);
+        if (st != ZERO_OK) return st;
+    }
+    if (a.dw && !(a.rows == 0 && accumulate)) {
+        E.out = static_cast<uint16_t*>(a.dw);
+        E.ld_out = a.ld_dw;
+        E.residual = accumulate ? E.out : nullptr;
+        E.ld_res = a.ld_dw;
+        E.vec = vec_flag(a.dw, a.ld_dw, kVecOut | kVecRes);
+        const Operand X{x, a.in_features, a.rows, L.ld_x8, true}, Z{dz, a.out_features, a.rows, L.ld_dz, true};
+        if (a.layout == ZERO_WEIGHT_OUT_IN) st = product(Z, X, a.dtype16, E, partial, kGb300Sms, s);
+        else st = product(X, Z, a.dtype16, E, partial, kGb300Sms, s);
+    }
+    return st;
+}
+catch (...) {
+    return exception_status("zero_linear_backward");
+}
+
+zero_status_t zero_linear_check(void* stream)
+try {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint32_t word = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&word, g_linear_error, sizeof(word), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "zero_linear_check");
+    if (word == 0) return ZERO_OK;
+    word = 0;
+    e = cudaMemcpyToSymbolAsync(g_linear_error, &word, sizeof(word), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "zero_linear_check");
+    return fail(ZERO_ETIMEOUT, "zero_linear: a bounded wait ran out; outputs since the last check are not final");
+}
+catch (...) {
+    return exception_status("zero_linear_check");
+}
+
+}  // extern "C"
