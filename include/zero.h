@@ -563,8 +563,8 @@ zero_status_t zero_step_range_noalloc(const void* const* grad_contribs, int n_d,
 
 /* ---------------------------------------------------------------------------------------
  * Operators of a training program around the sharded step: what a gathered unit's weights are
- * used for and what fills the gradient contributions (zero_linear and its gradients), and an
- * optimizer for tensors that are not sharded (zero_adamw).
+ * used for and what fills the gradient contributions (zero_linear, zero_block_norm, with their
+ * gradients), and an optimizer for tensors that are not sharded (zero_adamw).
  *
  * Each is asynchronous on `stream`, allocates nothing, may be captured in a CUDA graph and works
  * on the current device.  Pointers need the alignment of their element type; rows (or tensors)
@@ -628,6 +628,53 @@ zero_status_t zero_linear_backward(const zero_linear_t* a, void* workspace, int6
  * ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
  * synchronises `stream`. */
 zero_status_t zero_linear_check(void* stream);
+
+enum { ZERO_NORM_RMS = 0, ZERO_NORM_LAYER = 1 };
+enum { ZERO_NORM_PRE = 1, ZERO_NORM_POST = 2 };
+#define ZERO_NORM_MAX_DIM 8192
+
+/* The norm after one block and the norm before the next, with the block's gate and residual
+ * scale (post-norm, gated residual sum, pre-norm):
+ *   u = norms & ZERO_NORM_POST ? Norm(h; post_w, post_b) : h
+ *   y = x + residual_scale * gate * u
+ *   z = Norm(y; pre_w, pre_b)                                   (norms & ZERO_NORM_PRE)
+ * Norm(a; w, b) = (a - mean a) / sqrt(var a + eps) * w + b with ZERO_NORM_LAYER, and
+ * a / sqrt(mean a^2 + eps) * w + b with ZERO_NORM_RMS, over the `dim` elements of a row; sums in
+ * fp32, z from the unrounded y.  Row r takes gate row r / rows_per_gate: 1 gate a token,
+ * `rows` one for all, a sequence's length one a sequence (the last group may be short). */
+typedef struct {
+    int64_t rows, dim;       /* dim in 1 .. ZERO_NORM_MAX_DIM */
+    int32_t dtype16;         /* every tensor */
+    int32_t kind;            /* ZERO_NORM_RMS or ZERO_NORM_LAYER */
+    int32_t norms;           /* ZERO_NORM_PRE | ZERO_NORM_POST, or one, or 0 */
+    int32_t reserved;
+    int64_t rows_per_gate;   /* 0 without a gate */
+    double eps, residual_scale;
+    int64_t ld_h, ld_x, ld_y, ld_z, ld_gate, ld_dy, ld_dz, ld_dx, ld_dh, ld_dgate;
+    const void* h;           /* rows x dim */
+    const void* x;           /* rows x dim, or NULL: 0 */
+    const void* gate;        /* ceil(rows / rows_per_gate) x dim, or NULL: 1 */
+    const void *post_w, *post_b, *pre_w, *pre_b;   /* dim, or NULL: 1 (w), 0 (b) */
+    void* y;                 /* forward: written, may be x with the same stride, or NULL;
+                                backward: read (with ZERO_NORM_PRE) */
+    void* z;                 /* forward with ZERO_NORM_PRE: written; may be h with the same stride */
+    const void* dy;          /* backward: the gradient that reaches y past the norm, or NULL: 0 */
+    const void* dz;          /* backward with ZERO_NORM_PRE */
+    void* dx;                /* y's whole gradient, which is x's; or NULL; may be dy with the same stride */
+    void* dh;                /* or NULL */
+    void* dgate;             /* as gate, or NULL */
+    void *dpost_w, *dpost_b, *dpre_w, *dpre_b;     /* dim, or NULL */
+} zero_block_norm_t;
+
+zero_status_t zero_block_norm(const zero_block_norm_t* a, void* stream);
+
+/* Gradients (see zero_block_norm_t): h, gate and the norms' weights as in the forward, y as it
+ * wrote it; the rows' statistics are formed again from h and y.  The gradients of the norms'
+ * weights and of a gate shared by several rows are summed in fp32 in a fixed order through
+ * `workspace` (zero_block_norm_workspace bytes, 16-byte aligned; NULL if that is 0). */
+zero_status_t zero_block_norm_workspace(const zero_block_norm_t* a, int64_t* bytes);
+zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspace, int64_t workspace_bytes,
+                                       void* stream);
 
 /* Elements of one tensor that share a pair of 8-bit scales; the moments' buffers hold every
  * tensor's elements from a multiple of it on, zero-padded. */

@@ -50,6 +50,7 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_step_gather_next",
             "zero_last_error", "zero_plan_destroy", "zero_step_range_noalloc",
             "zero_linear_workspace", "zero_linear", "zero_linear_backward", "zero_linear_check",
+            "zero_block_norm", "zero_block_norm_workspace", "zero_block_norm_backward",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
             "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
 ZERO_NOALLOC_SCRATCH_BYTES = 256
@@ -115,6 +116,19 @@ class zero_linear_t(ctypes.Structure):
                                                "ld_dx", "ld_dw")] +
                 [(k, ctypes.c_void_p) for k in ("x", "w", "bias", "residual", "y", "pre", "dy", "dx",
                                                 "dw", "dbias")])
+
+
+class zero_block_norm_t(ctypes.Structure):
+    """The norms around a block: sizes, strides (0: dense) and device pointers; see include/zero.h."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("rows", "dim")] +
+                [(k, ctypes.c_int32) for k in ("dtype16", "kind", "norms", "reserved")] +
+                [("rows_per_gate", ctypes.c_int64), ("eps", ctypes.c_double),
+                 ("residual_scale", ctypes.c_double)] +
+                [(k, ctypes.c_int64) for k in ("ld_h", "ld_x", "ld_y", "ld_z", "ld_gate", "ld_dy", "ld_dz",
+                                               "ld_dx", "ld_dh", "ld_dgate")] +
+                [(k, ctypes.c_void_p) for k in ("h", "x", "gate", "post_w", "post_b", "pre_w", "pre_b", "y",
+                                                "z", "dy", "dz", "dx", "dh", "dgate", "dpost_w", "dpost_b",
+                                                "dpre_w", "dpre_b")])
 
 
 class zero_adamw_info_t(ctypes.Structure):
@@ -210,6 +224,11 @@ def lib() -> ctypes.CDLL:
         L.zero_linear_backward.argtypes = [ctypes.POINTER(zero_linear_t), _vp, _i64, _vp]
         L.zero_linear_check.argtypes = [_vp]
         for f in (L.zero_linear_workspace, L.zero_linear, L.zero_linear_backward, L.zero_linear_check):
+            f.restype = st
+        L.zero_block_norm.argtypes = [ctypes.POINTER(zero_block_norm_t), _vp]
+        L.zero_block_norm_workspace.argtypes = [ctypes.POINTER(zero_block_norm_t), ctypes.POINTER(_i64)]
+        L.zero_block_norm_backward.argtypes = [ctypes.POINTER(zero_block_norm_t), _vp, _i64, _vp]
+        for f in (L.zero_block_norm, L.zero_block_norm_workspace, L.zero_block_norm_backward):
             f.restype = st
         L.zero_adamw_create.argtypes = [_vp, _i64, _int, _int, _int, ctypes.POINTER(_vp)]
         L.zero_adamw_info.argtypes = [_vp, ctypes.POINTER(zero_adamw_info_t)]
@@ -479,6 +498,23 @@ def zero_linear_backward(args: zero_linear_t, workspace: int, workspace_bytes: i
 def zero_linear_check(stream: int = 0) -> None:
     """Raises ZERO_ETIMEOUT if a matrix product's bounded wait ran out since the last call."""
     _check(lib().zero_linear_check(stream or None))
+
+
+def zero_block_norm(args: zero_block_norm_t, stream: int = 0) -> None:
+    _check(lib().zero_block_norm(ctypes.byref(args), stream or None))
+
+
+def zero_block_norm_workspace(args: zero_block_norm_t) -> int:
+    """Bytes of workspace that zero_block_norm_backward needs for these arguments."""
+    n = _i64()
+    _check(lib().zero_block_norm_workspace(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def zero_block_norm_backward(args: zero_block_norm_t, workspace: int, workspace_bytes: int,
+                             stream: int = 0) -> None:
+    _check(lib().zero_block_norm_backward(ctypes.byref(args), workspace or None, workspace_bytes,
+                                          stream or None))
 
 
 def zero_adamw_create(tensor_sizes: Sequence[int], state_bits: int, dtype16: int = ZERO_BF16,

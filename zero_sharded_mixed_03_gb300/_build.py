@@ -12,7 +12,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 SOURCES = ["zero_plan.cpp", "zero_step.cu", "zero_offload.cpp", "zero_adamw.cu",
-           "zero_linear.cu"]
+           "zero_linear.cu", "zero_norm.cu"]
 # the host AdamW must round every fp32 operation separately, like the GPU kernel; without errno
 # bookkeeping its square root (an exact IEEE operation either way) lets the loop vectorise, and
 # without trapping math the compiler may evaluate the fp16 rounding's one fp32 addition for
