@@ -31,6 +31,9 @@ namespace {
 constexpr int kBlockElems = ZERO_ADAMW_BLOCK;  // elements of one tensor that share a pair of scales
 constexpr int kAdamThreads = 256;
 constexpr int kAdamWarps = kAdamThreads / 32;
+constexpr int kAhead = 2;                       // 8-bit moments: blocks on their way to a warp
+constexpr int kAdamPerSm8 = 2;
+constexpr int kAdamPerSm32 = 3;
 constexpr int kAdamNormSlots = 4096;           // most blocks of a norm launch
 
 // First 128 bytes of the workspace.
@@ -48,7 +51,7 @@ struct AdamState {
 };
 static_assert(sizeof(AdamState) <= 128, "AdamState fits its slot");
 
-// One tensor, as the kernels read it.
+// One tensor, as bound.
 struct AdamTensor {
     float* p;
     uint16_t* p16;        // may be NULL
@@ -59,9 +62,19 @@ struct AdamTensor {
 };
 static_assert(sizeof(AdamTensor) == 40, "AdamTensor layout");
 
+// One block of a tensor, as the kernels read it: 32 bytes for the 4 KB and more that the block moves.
+// (A table of tensors and one from blocks to tensors are smaller, but two reads one after the other.)
+struct alignas(16) AdamBlock {
+    float* p;             // at the block's first element
+    uint16_t* p16;
+    const void* g;
+    int32_t n;            // elements, 1 .. kBlockElems
+    int32_t vec;          // whole, and its pointers start on 16 bytes
+};
+static_assert(sizeof(AdamBlock) == 32, "AdamBlock layout");
+
 struct AdamParams {
-    const AdamTensor* tensors;
-    const int32_t* tensor_of;  // block -> tensor
+    const AdamBlock* blocks;
     void* m;
     void* v;
     uint16_t* scales;          // 8 bits: low byte em, high byte er
@@ -69,7 +82,8 @@ struct AdamParams {
     double* partials;          // norm pass: one slot a launched block
     int32_t n_blocks;
     int32_t checked;           // a norm pass of this step ran: skip on its flag, clip by its norm
-    float k[6];                // b1, 1-b1, b2, 1-b2, eps, lr*wd
+    F2 k[6];                   // b1, 1-b1, b2, 1-b2, eps, -lr*wd, each twice
+    F2 one;                    // 1 (add_apart)
     float inv;                 // 1 / loss scale
     double lr, beta1, beta2, max_norm;
 };
@@ -87,6 +101,22 @@ __device__ __forceinline__ double pow_int(double b, int64_t t)
 
 __device__ __forceinline__ float power_field(uint32_t e) { return __uint_as_float(e << 23); }
 
+// ---------------------------------------------------------------- a warp's block of one tensor
+
+// Which elements of its block a lane holds.  A whole block whose pointers start on 16 bytes: four in a
+// row from 4 lane on, and four from 128 + 4 lane on, so that 32 lanes' 16-byte accesses to fp32 values
+// cover 512 bytes without gaps (eight in a row leave half of every sector to a second access).  Else
+// every 32nd.
+
+__device__ __forceinline__ AdamBlock block_at(const AdamParams& P, int b)
+{
+    AdamBlock B;
+    const uint4* q = reinterpret_cast<const uint4*>(P.blocks + b);
+    reinterpret_cast<uint4*>(&B)[0] = __ldg(q);
+    reinterpret_cast<uint4*>(&B)[1] = __ldg(q + 1);
+    return B;
+}
+
 template <int GT>
 __device__ __forceinline__ float load_grad1(const void* g, int64_t e)
 {
@@ -94,224 +124,419 @@ __device__ __forceinline__ float load_grad1(const void* g, int64_t e)
     else return widen1<GT>(static_cast<const uint16_t*>(g)[e]);
 }
 
-// Eight gradients from element e on; aligned to 16 bytes.
 template <int GT>
-__device__ __forceinline__ void load_grad8(const void* g, int64_t e, float (&x)[8])
+__device__ __forceinline__ void load_grads(const AdamBlock& B, int lane, float (&x)[8])
+{
+    if (B.vec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (GT == ZERO_FP32) {
+                const float4 q = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(B.g) + i * 128 + lane * 4));
+                x[4 * i] = q.x; x[4 * i + 1] = q.y; x[4 * i + 2] = q.z; x[4 * i + 3] = q.w;
+            } else {
+                const uint2 q = ld_stream8(static_cast<const uint16_t*>(B.g) + i * 128 + lane * 4);
+                widen2<GT>(q.x, x[4 * i], x[4 * i + 1]);
+                widen2<GT>(q.y, x[4 * i + 2], x[4 * i + 3]);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j * 32 + lane < B.n ? load_grad1<GT>(B.g, j * 32 + lane) : 0.0f;
+}
+
+// A lane's eight of 256 consecutive fp32 values.
+__device__ __forceinline__ void load8(const float* p, int lane, float (&x)[8])
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p + lane * 4)), b = __ldcs(reinterpret_cast<const float4*>(p + 128 + lane * 4));
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+__device__ __forceinline__ void store8(float* p, int lane, const float (&x)[8])
+{
+    __stcs(reinterpret_cast<float4*>(p + lane * 4), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(p + 128 + lane * 4), make_float4(x[4], x[5], x[6], x[7]));
+}
+
+// ---------------------------------------------------------------- blocks on their way
+
+// With 8-bit moments a warp's aligned blocks come through shared memory of its own, copied
+// asynchronously two blocks ahead (their records four ahead), so that no register waits for memory:
+// the arithmetic needs them.  Measured on GB300 (124M elements, fp16 gradients): loads into
+// registers 361 us, one, two, three, four blocks ahead 348, 335, 343, 373.  With 32-bit moments the
+// arithmetic is less and plain loads with 24 warps an SM are faster (59M elements: 268 us against
+// 288).
+template <int GT>
+struct Ring {
+    static constexpr int kStages = kAhead + 1, kRecords = 2 * kAhead + 1;
+    static constexpr int kG = GT == ZERO_FP32 ? 2 : 1;                              // a lane's pieces of g
+    static constexpr int kStage = kG * 512 + 1024 + 2 * kBlockElems;
+    static constexpr int kWarp = kStages * kStage + kRecords * 32;
+    static constexpr int kBytes = kAdamWarps * kWarp;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint4 shared16(uint32_t at)
+{
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    return q;
+}
+
+__device__ __forceinline__ uint2 shared8(uint32_t at)
+{
+    uint2 q;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(at) : "memory");
+    return q;
+}
+
+__device__ __forceinline__ AdamBlock shared_block(uint32_t at)
+{
+    AdamBlock B;
+    reinterpret_cast<uint4*>(&B)[0] = shared16(at);
+    reinterpret_cast<uint4*>(&B)[1] = shared16(at + 16);
+    return B;
+}
+
+// Start the copies of block b into a stage: g, p, m and v one after the other.
+template <int GT>
+__device__ __forceinline__ void start_block(const AdamParams& P, const AdamBlock& B, int b, int lane, uint32_t stage)
+{
+    using R = Ring<GT>;
+    if (!B.vec) return;
+    const uint32_t own = stage + lane * 16;
+    const char* g = static_cast<const char*>(B.g) + lane * 16;
+    const char* p = reinterpret_cast<const char*>(B.p) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < R::kG; ++i) copy16(own + i * 512, g + i * 512);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) copy16(own + R::kG * 512 + i * 512, p + i * 512);
+    const uint32_t moments = stage + R::kG * 512 + 1024;
+    // m by the first half of the warp, v by the second
+    const uint32_t half = lane >> 4, k = (lane & 15) * 16;
+    const char* m = static_cast<const char*>(half ? P.v : P.m) + (int64_t)b * kBlockElems;
+    copy16(moments + half * kBlockElems + k, m + k);
+}
+
+// A lane's eight values of one of them.
+__device__ __forceinline__ void take_fp32(uint32_t at, int lane, float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 q = shared16(at + i * 512 + lane * 16);
+        x[4 * i] = __uint_as_float(q.x);
+        x[4 * i + 1] = __uint_as_float(q.y);
+        x[4 * i + 2] = __uint_as_float(q.z);
+        x[4 * i + 3] = __uint_as_float(q.w);
+    }
+}
+
+template <int GT>
+__device__ __forceinline__ void take_grads(uint32_t at, int lane, float (&x)[8])
 {
     if constexpr (GT == ZERO_FP32) {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(g) + e);
-        const float4 a = __ldcs(q), b = __ldcs(q + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        take_fp32(at, lane, x);
     } else {
-        const uint4 w = ld_stream(static_cast<const uint16_t*>(g) + e);
-        widen2<GT>(w.x, x[0], x[1]);
-        widen2<GT>(w.y, x[2], x[3]);
-        widen2<GT>(w.z, x[4], x[5]);
-        widen2<GT>(w.w, x[6], x[7]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint2 q = shared8(at + i * 256 + lane * 8);
+            widen2<GT>(q.x, x[4 * i], x[4 * i + 1]);
+            widen2<GT>(q.y, x[4 * i + 2], x[4 * i + 3]);
+        }
     }
 }
 
-// Which elements of its block a lane holds: eight in a row where the tensor's pointers allow
-// 16-byte accesses, else every 32nd (32 lanes then touch neighbouring elements).
-__device__ __forceinline__ int lane_elem(bool vec, int lane, int j) { return vec ? lane * 8 + j : j * 32 + lane; }
+__device__ __forceinline__ uint2 take_codes(uint32_t at, int lane)
+{
+    uint2 c;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.x) : "r"(at + lane * 4) : "memory");
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.y) : "r"(at + 128 + lane * 4) : "memory");
+    return c;
+}
 
 // ---------------------------------------------------------------- 8-bit moments
+//
+// Codes are handled in pairs, one in each half of a word: code << 6 in 16 bits is the half-precision
+// number of half the value in units of the scale (4 of its 5 exponent bits, 4 of its 10 fraction
+// bits; subnormals too), so the conversions between fp16 and fp32 do the work.
 
-__device__ __forceinline__ void decode_m8(uint2 c, float scale, float (&m)[8])
+__device__ __forceinline__ void decode_m2(uint32_t two, F2 scale, float& a, float& b)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    split(mul(pair(f.x, f.y), scale), a, b);
+}
+
+__device__ __forceinline__ uint32_t encode_m2(float a, float b, F2 inv)
+{
+    float2 f;
+    split(mul(pair(a, b), inv), f.x, f.y);
+    return __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+}
+
+// scale2 = twice the root's scale.  two: the codes in the low bytes of the halves.
+__device__ __forceinline__ void decode_root2(uint32_t two, F2 scale2, float& a, float& b)
+{
+    const uint32_t w = two << 6;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    split(mul(pair(f.x, f.y), scale2), a, b);
+}
+
+// inv_half = half of the scale's inverse.  Truncated to fp16, half a code added, truncated to the
+// code: to nearest, a tie upwards.  A root above 0 is at least code 1.
+__device__ __forceinline__ uint32_t encode_root2(float a, float b, F2 inv_half)
+{
+    float x, y;
+    split(mul(pair(a, b), inv_half), x, y);
+    if (a > 0.0f) x = fmaxf(x, 0x1p-18f);
+    if (b > 0.0f) y = fmaxf(y, 0x1p-18f);
+    uint32_t h;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+    return ((h + 0x00200020u) >> 6) & 0x00FF00FFu;
+}
+
+// Whether one of four code bytes is 255, the mark of a root that is not finite.
+__device__ __forceinline__ bool marked(uint32_t c) { return ((c & 0x7F7F7F7Fu) + 0x01010101u) & c & 0x80808080u; }
+
+__device__ __forceinline__ void mark_roots(uint32_t lo, uint32_t hi, float (&r)[8])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_fp8x2_storage_t q = (__nv_fp8x2_storage_t)((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        m[2 * i] = __fmul_rn(f.x, scale);
-        m[2 * i + 1] = __fmul_rn(f.y, scale);
-    }
+    for (int j = 0; j < 8; ++j)
+        if ((((j < 4 ? lo : hi) >> (8 * (j & 3))) & 0xFFu) == 0xFFu) r[j] = __uint_as_float(0x7FC00000u);
 }
 
-__device__ __forceinline__ uint2 encode_m8(const float (&m)[8], float inv)
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(m[2 * i], inv), __fmul_rn(m[2 * i + 1], inv)),
-                                        __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-}
-
-// A code's value: its bits moved to a float's exponent and fraction are the value times 2^-113
-// (field 0 becomes a subnormal, as it should), so one exact product gives it.
-__device__ __forceinline__ float decode_root1(uint32_t c, float scale)
-{
-    const float y = __fmul_rn(__uint_as_float(c << 19), power_field(127 + 113));
-    return c == 255u ? __uint_as_float(0x7FC00000u) : __fmul_rn(y, scale);
-}
-
-__device__ __forceinline__ uint32_t encode_root1(float r, float inv)
-{
-    const float y = __fmul_rn(r, inv);                       // in [0, 2)
-    const uint32_t b = __float_as_uint(y);
-    uint32_t c = ((b + 0x3FFFFu + ((b >> 19) & 1u)) >> 19) - (113u << 4);
-    if (y < 0x1p-13f) c = (uint32_t)__float2int_rn(__fmul_rn(y, 0x1p17f));
-    if (c == 0u && y > 0.0f) c = 1u;
-    return min(c, 255u);
-}
-
-// Largest exponent field of eight magnitudes over the warp; of the finite ones where some are not.
-__device__ __forceinline__ uint32_t warp_top_field(const float (&x)[8])
+// Exponent field of the warp's largest finite magnitude; a value that is not finite becomes not a number
+// (an infinite m would saturate to a finite code).
+__device__ __noinline__ uint32_t top_field_of_finite(float* x)
 {
     uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (top >= 0x7F800000u) {
-        top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (!nonfinite(x[j])) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
+    for (int j = 0; j < 8; ++j) {
+        if (nonfinite(x[j])) x[j] = __uint_as_float(0x7FC00000u);
+        else top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
     }
-    return top >> 23;
+    return __reduce_max_sync(0xFFFFFFFFu, top) >> 23;
+}
+
+// The pair (2 i, 2 i + 1) of a lane's eight code bytes, one in each half; and back.
+__device__ __forceinline__ uint32_t code_pair(uint2 c, int i)
+{
+    return __byte_perm(i < 2 ? c.x : c.y, 0u, (i & 1) ? 0x4342u : 0x4140u);
+}
+
+__device__ __forceinline__ float reciprocal_approx(float d)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return r;
+}
+
+__device__ __forceinline__ float root_approx(float v)
+{
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // ---------------------------------------------------------------- kernels
 
 template <int BITS, int GT, int DT>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamParams P)
+__global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamPerSm32) adamw_kernel(const __grid_constant__ AdamParams P)
 {
     __shared__ float sk_shared[4];
     __shared__ bool skip;
-    const int lane = threadIdx.x & 31;
-    // the constants of this step: two lanes raise the betas to the step's power
+    using R = Ring<GT>;
+    constexpr bool kRing = BITS == 8;
+    extern __shared__ __align__(16) unsigned char ring[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int stride = gridDim.x * kAdamWarps;
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + warp * R::kWarp;
+    const uint32_t records = mine + R::kStages * R::kStage;
+    int b = blockIdx.x * kAdamWarps + warp;
+    auto start_record = [&](int k, int at) {
+        if (lane < 2 && at < P.n_blocks) copy16(records + (k % R::kRecords) * 32 + lane * 16, reinterpret_cast<const char*>(P.blocks + at) + lane * 16);
+    };
+    uint32_t scales0 = 0, scales1 = 0;           // of this block and the next
+    AdamBlock next = {};
+    if constexpr (kRing) {
+        if (b < P.n_blocks) scales0 = P.scales[b];
+        if (b + stride < P.n_blocks) scales1 = P.scales[b + stride];
+        // the first blocks, and the records of as many after them
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (b + k * stride < P.n_blocks) start_block<GT>(P, block_at(P, b + k * stride), b + k * stride, lane, mine + k * R::kStage);
+            start_record(k, b + k * stride);
+            start_record(k + kAhead, b + (k + kAhead) * stride);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    } else {
+        if (b < P.n_blocks) next = block_at(P, b);
+    }
+    // the constants of this step, while the first loads are on their way: two lanes raise the betas
+    // to the step's power
     if (threadIdx.x < 32) {
         const volatile AdamState* st = P.st;
         const int64_t t = st->t + 1;
         const double bc = 1.0 - pow_int(lane == 0 ? P.beta1 : P.beta2, t);
         if (lane == 0) {
             sk_shared[0] = __double2float_rn(__ddiv_rn(P.lr, bc));
-            sk_shared[3] = 1.0f;
+            float coef = 1.0f;
             bool s = false;
             if (P.checked) {
                 s = st->flag != 0;
                 if (P.max_norm > 0.0) {
                     const double c = __ddiv_rn(P.max_norm, __dadd_rn(__dsqrt_rn(st->norm2), 1e-6));
-                    sk_shared[3] = __double2float_rn(c > 1.0 ? 1.0 : c);
+                    coef = __double2float_rn(c > 1.0 ? 1.0 : c);
                 }
             }
+            // the gradient is multiplied by 1 / loss scale, then by the clipping coefficient; where
+            // one of them is 1 that is one product
+            const bool one = P.inv == 1.0f || coef == 1.0f;
+            sk_shared[2] = one ? P.inv * coef : P.inv;
+            sk_shared[3] = one ? 1.0f : coef;
             skip = s;
         } else if (lane == 1) {
-            sk_shared[1] = __double2float_rn(__dsqrt_rn(bc));
+            sk_shared[1] = __double2float_rn(__ddiv_rn(1.0, __dsqrt_rn(bc)));
         }
     }
     __syncthreads();
-    StepK sk;
-    sk.step = sk_shared[0];
-    sk.bc2s = sk_shared[1];
-    sk.inv = P.inv;
-    sk.coef = sk_shared[3];
+    const F2 minus_step = both(-sk_shared[0]), inv_bc2s = both(sk_shared[1]), inv = both(sk_shared[2]), coef = both(sk_shared[3]);
+    const bool twice = sk_shared[3] != 1.0f;
 
-    const int stride = gridDim.x * kAdamWarps;
     if (!skip) {
-        for (int b = blockIdx.x * kAdamWarps + (threadIdx.x >> 5); b < P.n_blocks; b += stride) {
-            const AdamTensor T = P.tensors[__ldg(P.tensor_of + b)];
-            const int64_t e0 = (int64_t)(b - T.first) * kBlockElems;      // in the tensor
-            const int64_t s0 = (int64_t)b * kBlockElems;                  // in the moments
-            const int n = (int)min((int64_t)kBlockElems, T.n - e0);
-            // whole groups of eight only; the lane that holds the tensor's end goes by element
-            const bool vec = T.vec != 0;
-            const bool full = vec && lane * 8 + 8 <= n;
-            float g[8], p[8], m[8], v[8];
-            if (full) {
-                load_grad8<GT>(T.g, e0 + lane * 8, g);
-                const float4* q = reinterpret_cast<const float4*>(T.p + e0 + lane * 8);
-                const float4 a = __ldcs(q), c = __ldcs(q + 1);
-                p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
-                p[4] = c.x; p[5] = c.y; p[6] = c.z; p[7] = c.w;
+        for (int k = 0; b < P.n_blocks; ++k, b += stride) {
+            const int block = b;
+            const int64_t s0 = (int64_t)block * kBlockElems;              // in the moments
+            AdamBlock B;
+            uint32_t scales = 0;
+            if constexpr (kRing) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+                __syncwarp();
+                B = shared_block(records + (k % R::kRecords) * 32);
+                if (b + kAhead * stride < P.n_blocks)
+                    start_block<GT>(P, shared_block(records + ((k + kAhead) % R::kRecords) * 32), b + kAhead * stride, lane,
+                                    mine + ((k + kAhead) % R::kStages) * R::kStage);
+                start_record(k + 2 * kAhead, b + 2 * kAhead * stride);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                scales = scales0;
+                scales0 = scales1;
+                if (b + 2 * stride < P.n_blocks) scales1 = P.scales[b + 2 * stride];
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int e = lane_elem(vec, lane, j);
-                    g[j] = e < n ? load_grad1<GT>(T.g, e0 + e) : 0.0f;
-                    p[j] = e < n ? T.p[e0 + e] : 0.0f;
-                }
+                B = next;
+                if (b + stride < P.n_blocks) next = block_at(P, b + stride);
             }
-            // the moments' block is padded to 256 elements and starts on 16 bytes
-            if constexpr (BITS == 32) {
-                float* mp = static_cast<float*>(P.m) + s0;
-                float* vp = static_cast<float*>(P.v) + s0;
-                if (vec) {
-                    const float4 a = __ldcs(reinterpret_cast<const float4*>(mp + lane * 8));
-                    const float4 c = __ldcs(reinterpret_cast<const float4*>(mp + lane * 8) + 1);
-                    const float4 d = __ldcs(reinterpret_cast<const float4*>(vp + lane * 8));
-                    const float4 f = __ldcs(reinterpret_cast<const float4*>(vp + lane * 8) + 1);
-                    m[0] = a.x; m[1] = a.y; m[2] = a.z; m[3] = a.w;
-                    m[4] = c.x; m[5] = c.y; m[6] = c.z; m[7] = c.w;
-                    v[0] = d.x; v[1] = d.y; v[2] = d.z; v[3] = d.w;
-                    v[4] = f.x; v[5] = f.y; v[6] = f.z; v[7] = f.w;
+            const bool vec = B.vec != 0;
+            float g[8], p[8], m[8], v[8];
+            if (vec) {
+                if constexpr (!kRing) {
+                    load_grads<GT>(B, lane, g);
+                    load8(B.p, lane, p);
+                    load8(static_cast<const float*>(P.m) + s0, lane, m);
+                    load8(static_cast<const float*>(P.v) + s0, lane, v);
+                } else {
+                    const uint32_t stage = mine + (k % R::kStages) * R::kStage, moments = stage + R::kG * 512 + 1024;
+                    take_grads<GT>(stage, lane, g);
+                    take_fp32(stage + R::kG * 512, lane, p);
+                    const F2 ms = both(power_field(scales & 0xFFu)), rs = both(power_field(scales >> 8) * 2.0f);
+                    const uint2 mc = take_codes(moments, lane), vc = take_codes(moments + kBlockElems, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        decode_m2((i < 2 ? mc.x : mc.y) >> (16 * (i & 1)), ms, m[2 * i], m[2 * i + 1]);
+                        decode_root2(code_pair(vc, i), rs, v[2 * i], v[2 * i + 1]);
+                    }
+                    if (marked(vc.x) || marked(vc.y)) mark_roots(vc.x, vc.y, v);
+                }
+            } else {
+                const float* bp = B.p + lane;
+                const char* bg = static_cast<const char*>(B.g) + lane * (GT == ZERO_FP32 ? 4 : 2);
+                if (B.n == kBlockElems) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        g[j] = load_grad1<GT>(bg, j * 32);
+                        p[j] = bp[j * 32];
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        m[j] = mp[j * 32 + lane];
-                        v[j] = vp[j * 32 + lane];
+                        const bool in = j * 32 + lane < B.n;
+                        g[j] = in ? load_grad1<GT>(bg, j * 32) : 0.0f;
+                        p[j] = in ? bp[j * 32] : 0.0f;
                     }
                 }
-            } else {
-                const uint8_t* mp = static_cast<const uint8_t*>(P.m) + s0;
-                const uint8_t* vp = static_cast<const uint8_t*>(P.v) + s0;
-                uint2 mc, vc;
-                if (vec) {
-                    mc = __ldcs(reinterpret_cast<const uint2*>(mp + lane * 8));
-                    vc = __ldcs(reinterpret_cast<const uint2*>(vp + lane * 8));
-                } else {
-                    mc = vc = make_uint2(0u, 0u);
+                if constexpr (BITS == 32) {
+                    const float* mp = static_cast<const float*>(P.m) + s0 + lane;
+                    const float* vp = static_cast<const float*>(P.v) + s0 + lane;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const uint32_t a = mp[j * 32 + lane], c = vp[j * 32 + lane];
-                        if (j < 4) {
-                            mc.x |= a << (8 * j);
-                            vc.x |= c << (8 * j);
-                        } else {
-                            mc.y |= a << (8 * (j - 4));
-                            vc.y |= c << (8 * (j - 4));
+                        m[j] = mp[j * 32];
+                        v[j] = vp[j * 32];
+                    }
+                } else {
+                    const F2 ms = both(power_field(scales & 0xFFu)), rs = both(power_field(scales >> 8) * 2.0f);
+                    const uint8_t* mp = static_cast<const uint8_t*>(P.m) + s0 + lane;
+                    const uint8_t* vp = static_cast<const uint8_t*>(P.v) + s0 + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        decode_m2(mp[i * 64] | ((uint32_t)mp[i * 64 + 32] << 8), ms, m[2 * i], m[2 * i + 1]);
+                        const uint32_t c = vp[i * 64] | ((uint32_t)vp[i * 64 + 32] << 16);
+                        decode_root2(c, rs, v[2 * i], v[2 * i + 1]);
+                        if (marked(c)) {
+                            if ((c & 0xFFu) == 0xFFu) v[2 * i] = __uint_as_float(0x7FC00000u);
+                            if (c >> 16 == 0xFFu) v[2 * i + 1] = __uint_as_float(0x7FC00000u);
                         }
                     }
-                }
-                const uint32_t e = P.scales[b];
-                decode_m8(mc, power_field(e & 0xFFu), m);
-                const float rs = power_field(e >> 8);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float r = decode_root1(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 0xFFu, rs);
-                    v[j] = __fmul_rn(r, r);
                 }
             }
             float root[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float gu = __fmul_rn(__fmul_rn(g[j], sk.inv), sk.coef);
-                m[j] = __fadd_rn(__fmul_rn(P.k[0], m[j]), __fmul_rn(P.k[1], gu));
-                v[j] = __fadd_rn(__fmul_rn(P.k[2], v[j]), __fmul_rn(P.k[3], __fmul_rn(gu, gu)));
-                root[j] = __fsqrt_rn(v[j]);
-                const float d = __fadd_rn(__fdiv_rn(root[j], sk.bc2s), P.k[4]);
-                p[j] = __fsub_rn(p[j], __fmul_rn(P.k[5], p[j]));
-                p[j] = __fsub_rn(p[j], __fmul_rn(sk.step, __fdiv_rn(m[j], d)));
+            for (int i = 0; i < 8; i += 2) {
+                F2 gu = mul(pair(g[i], g[i + 1]), inv);
+                if (twice) gu = mul(gu, coef);
+                F2 v2 = pair(v[i], v[i + 1]);
+                if constexpr (BITS == 8) v2 = mul(v2, v2);
+                // every product and sum rounded by itself: an 8-bit moment is a small whole number of
+                // units, so that exact ties of its next value are common and a last place decides them
+                const F2 m2 = add_apart(mul(P.k[0], pair(m[i], m[i + 1])), mul(P.k[1], gu), P.one);
+                v2 = add_apart(mul(P.k[2], v2), mul(P.k[3], mul(gu, gu)), P.one);
+                split(m2, m[i], m[i + 1]);
+                split(v2, v[i], v[i + 1]);
+                // the root and the quotient within 2 units in the last place, on a step that is a small
+                // part of the parameter it is added to
+                root[i] = root_approx(v[i]);
+                root[i + 1] = root_approx(v[i + 1]);
+                float d0, d1;
+                split(add_apart(mul(pair(root[i], root[i + 1]), inv_bc2s), P.k[4], P.one), d0, d1);
+                F2 p2 = pair(p[i], p[i + 1]);
+                p2 = add_apart(mul(P.k[5], p2), p2, P.one);
+                p2 = add_apart(mul(minus_step, mul(m2, pair(reciprocal_approx(d0), reciprocal_approx(d1)))), p2, P.one);
+                split(p2, p[i], p[i + 1]);
             }
-            if (full) {
-                float4* q = reinterpret_cast<float4*>(T.p + e0 + lane * 8);
-                __stcs(q, make_float4(p[0], p[1], p[2], p[3]));
-                __stcs(q + 1, make_float4(p[4], p[5], p[6], p[7]));
-                if (T.p16)
-                    __stcs(reinterpret_cast<uint4*>(T.p16 + e0 + lane * 8),
-                           make_uint4(narrow2<DT>(p[0], p[1]), narrow2<DT>(p[2], p[3]),
-                                      narrow2<DT>(p[4], p[5]), narrow2<DT>(p[6], p[7])));
+            if (vec) {
+                store8(B.p, lane, p);
+                if (B.p16) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        __stcs(reinterpret_cast<uint2*>(B.p16 + i * 128 + lane * 4),
+                               make_uint2(narrow2<DT>(p[4 * i], p[4 * i + 1]), narrow2<DT>(p[4 * i + 2], p[4 * i + 3])));
+                }
+            } else if (B.n == kBlockElems) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) B.p[j * 32 + lane] = p[j];
+                if (B.p16) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) B.p16[j * 32 + lane] = narrow1<DT>(p[j]);
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int e = lane_elem(vec, lane, j);
-                    if (e < n) {
-                        T.p[e0 + e] = p[j];
-                        if (T.p16) T.p16[e0 + e] = narrow1<DT>(p[j]);
+                    const int e = j * 32 + lane;
+                    if (e < B.n) {
+                        B.p[e] = p[j];
+                        if (B.p16) B.p16[e] = narrow1<DT>(p[j]);
                     } else {
                         m[j] = v[j] = root[j] = 0.0f;      // the moments' padding stays zero
                     }
@@ -321,12 +546,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
                 float* mp = static_cast<float*>(P.m) + s0;
                 float* vp = static_cast<float*>(P.v) + s0;
                 if (vec) {
-                    float4* a = reinterpret_cast<float4*>(mp + lane * 8);
-                    float4* c = reinterpret_cast<float4*>(vp + lane * 8);
-                    __stcs(a, make_float4(m[0], m[1], m[2], m[3]));
-                    __stcs(a + 1, make_float4(m[4], m[5], m[6], m[7]));
-                    __stcs(c, make_float4(v[0], v[1], v[2], v[3]));
-                    __stcs(c + 1, make_float4(v[4], v[5], v[6], v[7]));
+                    store8(mp, lane, m);
+                    store8(vp, lane, v);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -335,36 +556,58 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
                     }
                 }
             } else {
-                // an infinite m would saturate to a finite code: it is kept as not a number
+                // the block's largest magnitudes; m is finite where the root is
+                uint32_t top_r = 0;
+                float top_m = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (nonfinite(m[j])) m[j] = __uint_as_float(0x7FC00000u);
-                const uint32_t fm = warp_top_field(m), er = warp_top_field(root);
+                for (int j = 0; j < 8; ++j) {
+                    top_r = max(top_r, __float_as_uint(root[j]) & 0x7FFFFFFFu);
+                    top_m = fmaxf(top_m, fabsf(m[j]));
+                }
+                top_r = __reduce_max_sync(0xFFFFFFFFu, top_r);
+                uint32_t er = top_r >> 23, fm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_m)) >> 23;
+                const bool finite = er != 0xFFu;
+                if (!finite) {
+                    er = top_field_of_finite(root);
+                    fm = top_field_of_finite(m);
+                }
                 const uint32_t em = fm > 8u ? fm - 7u : 1u;
-                const uint2 mc = encode_m8(m, power_field(254u - em));
-                const float ri = power_field(254u - er);
-                uint2 vc = make_uint2(0u, 0u);
+                const F2 mi = both(power_field(254u - em)), ri = both(power_field(254u - er) * 0.5f);
+                uint32_t mc[4], rc[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    vc.x |= encode_root1(root[j], ri) << (8 * j);
-                    vc.y |= encode_root1(root[j + 4], ri) << (8 * j);
+                for (int i = 0; i < 4; ++i) {
+                    mc[i] = encode_m2(m[2 * i], m[2 * i + 1], mi);
+                    rc[i] = encode_root2(root[2 * i], root[2 * i + 1], ri);
+                }
+                if (!finite) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (nonfinite(root[2 * i])) rc[i] = (rc[i] & 0xFFFF0000u) | 0xFFu;
+                        if (nonfinite(root[2 * i + 1])) rc[i] = (rc[i] & 0x0000FFFFu) | 0x00FF0000u;
+                    }
                 }
                 uint8_t* mp = static_cast<uint8_t*>(P.m) + s0;
                 uint8_t* vp = static_cast<uint8_t*>(P.v) + s0;
                 if (vec) {
-                    __stcs(reinterpret_cast<uint2*>(mp + lane * 8), mc);
-                    __stcs(reinterpret_cast<uint2*>(vp + lane * 8), vc);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        __stcs(reinterpret_cast<uint32_t*>(mp + i * 128 + lane * 4), mc[2 * i] | (mc[2 * i + 1] << 16));
+                        __stcs(reinterpret_cast<uint32_t*>(vp + i * 128 + lane * 4), __byte_perm(rc[2 * i], rc[2 * i + 1], 0x6420u));
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        mp[j * 32 + lane] = (uint8_t)((j < 4 ? mc.x : mc.y) >> (8 * (j & 3)));
-                        vp[j * 32 + lane] = (uint8_t)((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
+                    for (int i = 0; i < 4; ++i) {
+                        mp[i * 64 + lane] = (uint8_t)mc[i];
+                        mp[i * 64 + 32 + lane] = (uint8_t)(mc[i] >> 8);
+                        vp[i * 64 + lane] = (uint8_t)rc[i];
+                        vp[i * 64 + 32 + lane] = (uint8_t)(rc[i] >> 16);
                     }
                 }
-                if (lane == 0) P.scales[b] = (uint16_t)(em | (er << 8));
+                if (lane == 0) P.scales[block] = (uint16_t)(em | (er << 8));
             }
         }
     }
+    if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
     // the last block to finish closes the step: every block has read t by then
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -395,21 +638,15 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     NormAcc acc;
     bool bad = false;
     const int stride = gridDim.x * kAdamWarps;
-    for (int b = blockIdx.x * kAdamWarps + (threadIdx.x >> 5); b < P.n_blocks; b += stride) {
-        const AdamTensor T = P.tensors[__ldg(P.tensor_of + b)];
-        const int64_t e0 = (int64_t)(b - T.first) * kBlockElems;
-        const int n = (int)min((int64_t)kBlockElems, T.n - e0);
-        const bool vec = T.vec != 0;
+    int b = blockIdx.x * kAdamWarps + (threadIdx.x >> 5);
+    AdamBlock next = {};
+    if (b < P.n_blocks) next = block_at(P, b);
+    while (b < P.n_blocks) {
+        const AdamBlock B = next;
         float g[8];
-        if (vec && lane * 8 + 8 <= n) {
-            load_grad8<GT>(T.g, e0 + lane * 8, g);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = lane_elem(vec, lane, j);
-                g[j] = e < n ? load_grad1<GT>(T.g, e0 + e) : 0.0f;
-            }
-        }
+        load_grads<GT>(B, lane, g);
+        b += stride;
+        if (b < P.n_blocks) next = block_at(P, b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = __fmul_rn(g[j], P.inv);
@@ -441,6 +678,26 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     }
 }
 
+// The table of blocks from the table of tensors.
+__global__ void __launch_bounds__(kAdamThreads) adamw_table_kernel(const AdamTensor* tensors, int64_t n, int grad_bytes,
+                                                                   AdamBlock* blocks)
+{
+    for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+        const AdamTensor T = tensors[i];
+        const int64_t count = (T.n + kBlockElems - 1) / kBlockElems;
+        for (int64_t k = threadIdx.x; k < count; k += kAdamThreads) {
+            const int64_t e = k * kBlockElems;
+            AdamBlock B;
+            B.p = T.p + e;
+            B.p16 = T.p16 ? T.p16 + e : nullptr;
+            B.g = static_cast<const char*>(T.g) + e * grad_bytes;
+            B.n = (int32_t)min((int64_t)kBlockElems, T.n - e);
+            B.vec = T.vec && B.n == kBlockElems;
+            blocks[T.first + k] = B;
+        }
+    }
+}
+
 // The 8-bit moments as the values that they stand for; bf16 holds each of them exactly.
 __global__ void __launch_bounds__(kAdamThreads) adamw_export_kernel(const uint8_t* m, const uint8_t* v,
                                                                     const uint16_t* scales, uint16_t* m_out,
@@ -452,11 +709,14 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_export_kernel(const uint8_
         const uint2 mc = __ldcs(reinterpret_cast<const uint2*>(m + at));
         const uint2 vc = __ldcs(reinterpret_cast<const uint2*>(v + at));
         const uint32_t e = scales[b];
+        const F2 ms = both(power_field(e & 0xFFu)), rs = both(power_field(e >> 8) * 2.0f);
         float x[8], r[8];
-        decode_m8(mc, power_field(e & 0xFFu), x);
-        const float rs = power_field(e >> 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = decode_root1(((j < 4 ? vc.x : vc.y) >> (8 * (j & 3))) & 0xFFu, rs);
+        for (int i = 0; i < 4; ++i) {
+            decode_m2((i < 2 ? mc.x : mc.y) >> (16 * (i & 1)), ms, x[2 * i], x[2 * i + 1]);
+            decode_root2(code_pair(vc, i), rs, r[2 * i], r[2 * i + 1]);
+        }
+        if (marked(vc.x) || marked(vc.y)) mark_roots(vc.x, vc.y, r);
         __stcs(reinterpret_cast<uint4*>(m_out + at),
                make_uint4(narrow2<ZERO_BF16>(x[0], x[1]), narrow2<ZERO_BF16>(x[2], x[3]),
                           narrow2<ZERO_BF16>(x[4], x[5]), narrow2<ZERO_BF16>(x[6], x[7])));
@@ -482,21 +742,22 @@ struct zero_adamw {
 namespace zero {
 namespace {
 
-// Workspace: the state's slot, the tensors, the blocks' tensors, the norm pass's slots.
+// Workspace: the state's slot, the tensors, the blocks, the norm pass's slots.
 constexpr int64_t kAdamStateBytes = 256;
 inline int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 int64_t tensors_at() { return kAdamStateBytes; }
-int64_t map_at(const zero_adamw* h) { return tensors_at() + up16((int64_t)sizeof(AdamTensor) * (int64_t)h->sizes.size()); }
-int64_t slots_at(const zero_adamw* h) { return map_at(h) + up16(4 * h->n_blocks); }
+int64_t blocks_at(const zero_adamw* h) { return tensors_at() + up16((int64_t)sizeof(AdamTensor) * (int64_t)h->sizes.size()); }
+int64_t slots_at(const zero_adamw* h) { return blocks_at(h) + (int64_t)sizeof(AdamBlock) * h->n_blocks; }
 int64_t adam_workspace(const zero_adamw* h) { return slots_at(h) + 8 * kAdamNormSlots; }
 
 // A persistent grid: as many blocks as fit the GPU at once, or as the work needs.
-template <auto KERNEL>
+template <auto KERNEL, int SHARED = 0>
 int adam_grid(const zero_adamw* h)
 {
     static const int per_sm = [] {
         int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, kAdamThreads, 0) == cudaSuccess ? std::max(1, n) : 1;
+        if (SHARED > 0) cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, kAdamThreads, SHARED) == cudaSuccess ? std::max(1, n) : 1;
     }();
     const int64_t cap = (int64_t)std::max(1, device_sms(h->device)) * per_sm;
     const int64_t need = (h->n_blocks + kAdamWarps - 1) / kAdamWarps;
@@ -506,10 +767,11 @@ int adam_grid(const zero_adamw* h)
 template <int BITS, int GT>
 void launch_adamw(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
 {
+    constexpr int kShared = BITS == 8 ? Ring<GT>::kBytes : 0;
     if (h->dtype16 == ZERO_BF16)
-        adamw_kernel<BITS, GT, ZERO_BF16><<<adam_grid<adamw_kernel<BITS, GT, ZERO_BF16>>(h), kAdamThreads, 0, s>>>(P);
+        adamw_kernel<BITS, GT, ZERO_BF16><<<adam_grid<adamw_kernel<BITS, GT, ZERO_BF16>, kShared>(h), kAdamThreads, kShared, s>>>(P);
     else
-        adamw_kernel<BITS, GT, ZERO_FP16><<<adam_grid<adamw_kernel<BITS, GT, ZERO_FP16>>(h), kAdamThreads, 0, s>>>(P);
+        adamw_kernel<BITS, GT, ZERO_FP16><<<adam_grid<adamw_kernel<BITS, GT, ZERO_FP16>, kShared>(h), kAdamThreads, kShared, s>>>(P);
 }
 
 template <int BITS>
@@ -610,9 +872,8 @@ try {
     if (!aligned(m, 16) || !aligned(v, 16)) return fail(ZERO_EALIGN, "zero_adamw_bind: moments not 16-byte aligned");
     if (!aligned(scales, 2)) return fail(ZERO_EALIGN, "zero_adamw_bind: scales not 2-byte aligned");
     if (!aligned(workspace, 16)) return fail(ZERO_EALIGN, "zero_adamw_bind: workspace not 16-byte aligned");
-    std::vector<unsigned char> image((size_t)(slots_at(h)), 0);
+    std::vector<unsigned char> image((size_t)(blocks_at(h)), 0);
     AdamTensor* T = reinterpret_cast<AdamTensor*>(image.data() + tensors_at());
-    int32_t* map = reinterpret_cast<int32_t*>(image.data() + map_at(h));
     const uintptr_t gsize = h->grad_type == ZERO_FP32 ? 4 : 2;
     int64_t block = 0;
     for (size_t i = 0; i < n; ++i) {
@@ -626,9 +887,7 @@ try {
         if (!aligned(T[i].p, 4) || !aligned(T[i].p16, 2) || !aligned(T[i].g, gsize))
             return fail(ZERO_EALIGN, "zero_adamw_bind: a tensor is not aligned to its element size");
         T[i].vec = aligned(T[i].p, 16) && aligned(T[i].p16, 16) && aligned(T[i].g, 16);
-        const int64_t blocks = (elems + kBlockElems - 1) / kBlockElems;
-        std::fill(map + block, map + block + blocks, (int32_t)i);
-        block += blocks;
+        block += (elems + kBlockElems - 1) / kBlockElems;
     }
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -641,6 +900,13 @@ try {
     const size_t skip = t == -1 ? (size_t)tensors_at() : 0;       // -1: the state's slot stays
     e = cudaMemcpyAsync(static_cast<char*>(workspace) + skip, image.data() + skip, image.size() - skip,
                         cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess && h->n_blocks > 0) {
+        char* ws = static_cast<char*>(workspace);
+        adamw_table_kernel<<<(unsigned)std::min<int64_t>((int64_t)n, 4096), kAdamThreads, 0, s>>>(
+            reinterpret_cast<const AdamTensor*>(ws + tensors_at()), (int64_t)n, (int)gsize,
+            reinterpret_cast<AdamBlock*>(ws + blocks_at(h)));
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "zero_adamw_bind: the workspace's tables");
     h->m = m;
@@ -672,8 +938,7 @@ try {
     AdamParams P;
     float c[9];
     step_constants(*hyper, 1, loss_scale, 1, c);
-    P.tensors = reinterpret_cast<const AdamTensor*>(ws + tensors_at());
-    P.tensor_of = reinterpret_cast<const int32_t*>(ws + map_at(h));
+    P.blocks = reinterpret_cast<const AdamBlock*>(ws + blocks_at(h));
     P.m = h->m;
     P.v = h->v;
     P.scales = static_cast<uint16_t*>(h->scales);
@@ -681,7 +946,16 @@ try {
     P.partials = reinterpret_cast<double*>(ws + slots_at(h));
     P.n_blocks = (int32_t)h->n_blocks;
     P.checked = hyper->max_grad_norm > 0.0 || (hyper->flags & ZERO_REPORT_GRAD_NORM);
-    for (int i = 0; i < 6; ++i) P.k[i] = c[i];
+    // eps: the smallest normal number at least, so that its reciprocal is finite
+    if (c[4] > 0.0f && c[4] < 0x1p-126f) c[4] = 0x1p-126f;
+    c[5] = -c[5];
+    auto twice = [](float x) {
+        uint32_t w;
+        std::memcpy(&w, &x, 4);
+        return F2{((unsigned long long)w << 32) | w};
+    };
+    for (int i = 0; i < 6; ++i) P.k[i] = twice(c[i]);
+    P.one = twice(1.0f);
     P.inv = c[8];
     P.lr = hyper->lr;
     P.beta1 = hyper->beta1;

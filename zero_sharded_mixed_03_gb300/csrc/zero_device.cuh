@@ -87,6 +87,55 @@ __device__ __forceinline__ bool nonfinite(float g)
     return (__float_as_uint(g) & 0x7F800000u) == 0x7F800000u;
 }
 
+// Two floats in one 64-bit register: one instruction rounds both, each as by itself.
+struct F2 {
+    unsigned long long v;
+};
+
+__device__ __forceinline__ F2 pair(float a, float b)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+
+__device__ __forceinline__ void split(F2 p, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// a + b with a kept a rounded product: `one` is 1 from memory, unknown to the compiler, which would
+// contract the packed product and sum to one rounding.
+__device__ __forceinline__ F2 add_apart(F2 a, F2 b, F2 one)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(one.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // The constants that depend on t, the loss scale and the gradient norm, formed per block.
 struct StepK {
     float step;   // lr / (1 - beta1^t)
