@@ -624,11 +624,6 @@ zero_status_t zero_linear(const zero_linear_t* a, void* workspace, int64_t works
  * writes zeros to dw and dbias (nothing with ZERO_LINEAR_ACCUMULATE). */
 zero_status_t zero_linear_backward(const zero_linear_t* a, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* The matrix-product kernels' only waits are on shared-memory barriers; each is bounded (2 s).
- * ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
- * synchronises `stream`. */
-zero_status_t zero_linear_check(void* stream);
-
 enum { ZERO_NORM_RMS = 0, ZERO_NORM_LAYER = 1 };
 enum { ZERO_NORM_PRE = 1, ZERO_NORM_POST = 2 };
 #define ZERO_NORM_MAX_DIM 8192
@@ -675,6 +670,11 @@ zero_status_t zero_block_norm(const zero_block_norm_t* a, void* stream);
 zero_status_t zero_block_norm_workspace(const zero_block_norm_t* a, int64_t* bytes);
 zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspace, int64_t workspace_bytes,
                                        void* stream);
+
+/* The only waits of the operators' kernels are on shared-memory barriers; each is bounded (2 s).
+ * ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
+ * synchronises `stream`. */
+zero_status_t zero_operators_check(void* stream);
 
 /* Elements of one tensor that share a pair of 8-bit scales; the moments' buffers hold every
  * tensor's elements from a multiple of it on, zero-padded. */

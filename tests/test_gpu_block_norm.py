@@ -25,6 +25,8 @@ def _cuda():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     Z.lib()
+    yield
+    Z.zero_operators_check()
 
 
 def storage(v):

@@ -26,7 +26,7 @@ def _cuda():
         pytest.skip("no CUDA device")
     Z.lib()
     yield
-    Z.zero_linear_check()
+    Z.zero_operators_check()
 
 
 def matrix(rows, cols, dtype, gen, ld=0, shift=0, whole=False, std=1.0):

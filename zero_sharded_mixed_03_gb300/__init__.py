@@ -49,7 +49,7 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_bind_host_staging", "zero_step_host", "zero_step_host_finish", "zero_grad_norm_host",
             "zero_step_gather_next",
             "zero_last_error", "zero_plan_destroy", "zero_step_range_noalloc",
-            "zero_linear_workspace", "zero_linear", "zero_linear_backward", "zero_linear_check",
+            "zero_linear_workspace", "zero_linear", "zero_linear_backward", "zero_operators_check",
             "zero_block_norm", "zero_block_norm_workspace", "zero_block_norm_backward",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
             "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
@@ -222,8 +222,8 @@ def lib() -> ctypes.CDLL:
         L.zero_linear_workspace.argtypes = [ctypes.POINTER(zero_linear_t), _int, ctypes.POINTER(_i64)]
         L.zero_linear.argtypes = [ctypes.POINTER(zero_linear_t), _vp, _i64, _vp]
         L.zero_linear_backward.argtypes = [ctypes.POINTER(zero_linear_t), _vp, _i64, _vp]
-        L.zero_linear_check.argtypes = [_vp]
-        for f in (L.zero_linear_workspace, L.zero_linear, L.zero_linear_backward, L.zero_linear_check):
+        L.zero_operators_check.argtypes = [_vp]
+        for f in (L.zero_linear_workspace, L.zero_linear, L.zero_linear_backward, L.zero_operators_check):
             f.restype = st
         L.zero_block_norm.argtypes = [ctypes.POINTER(zero_block_norm_t), _vp]
         L.zero_block_norm_workspace.argtypes = [ctypes.POINTER(zero_block_norm_t), ctypes.POINTER(_i64)]
@@ -495,9 +495,9 @@ def zero_linear_backward(args: zero_linear_t, workspace: int, workspace_bytes: i
                                       stream or None))
 
 
-def zero_linear_check(stream: int = 0) -> None:
-    """Raises ZERO_ETIMEOUT if a matrix product's bounded wait ran out since the last call."""
-    _check(lib().zero_linear_check(stream or None))
+def zero_operators_check(stream: int = 0) -> None:
+    """Raises ZERO_ETIMEOUT if a bounded wait of an operator's kernel ran out since the last call."""
+    _check(lib().zero_operators_check(stream or None))
 
 
 def zero_block_norm(args: zero_block_norm_t, stream: int = 0) -> None:

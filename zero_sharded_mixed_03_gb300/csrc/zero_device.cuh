@@ -38,6 +38,18 @@ inline zero_status_t cuda_fail(cudaError_t e, const char* what)
     return fail(ZERO_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+// Read and clear a kernel's error word (on a device variable), after the work on `s`.
+template <typename W>
+inline cudaError_t take_error_word(W& symbol, uint32_t* word, cudaStream_t s)
+{
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, symbol, sizeof(*word), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *word == 0) return e;
+    const uint32_t none = 0;
+    e = cudaMemcpyToSymbolAsync(symbol, &none, sizeof(none), 0, cudaMemcpyHostToDevice, s);
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
+
 // ------------------------------------------------------------------ element helpers
 
 // 16-bit -> fp32 widening (exact).  bf16 is the upper half of an IEEE binary32.

@@ -18,6 +18,9 @@
 #include "zero_device.cuh"
 
 namespace zero {
+
+cudaError_t take_norm_error(uint32_t* word, void* stream);   // zero_norm.cu
+
 namespace {
 
 constexpr int kBM = 128;                 // rows of a block's tile (a pair of blocks: 256)
@@ -28,7 +31,7 @@ constexpr uint64_t kGemmWaitNs = 2000000000ull;
 constexpr int kEpiCols = 32;             // columns an epilogue warp takes at a time
 constexpr int kEpiBytes = 32 * kEpiCols * 4;
 
-// Set by a kernel whose bounded wait ran out (zero_linear_check reads and clears it).
+// Set by a kernel whose bounded wait ran out (zero_operators_check reads and clears it).
 __device__ uint32_t g_linear_error;
 
 enum { kVecOut = 1, kVecPre = 2, kVecRes = 4, kVecBias = 8 };
@@ -1002,22 +1005,18 @@ catch (...) {
     return exception_status("zero_linear_backward");
 }
 
-zero_status_t zero_linear_check(void* stream)
+zero_status_t zero_operators_check(void* stream)
 try {
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint32_t word = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&word, g_linear_error, sizeof(word), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return cuda_fail(e, "zero_linear_check");
-    if (word == 0) return ZERO_OK;
-    word = 0;
-    e = cudaMemcpyToSymbolAsync(g_linear_error, &word, sizeof(word), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return cuda_fail(e, "zero_linear_check");
-    return fail(ZERO_ETIMEOUT, "zero_linear: a bounded wait ran out; outputs since the last check are not final");
+    uint32_t linear = 0, norm = 0;
+    cudaError_t e = take_error_word(g_linear_error, &linear, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = take_norm_error(&norm, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "zero_operators_check");
+    if (!linear && !norm) return ZERO_OK;
+    return fail(ZERO_ETIMEOUT, std::string(linear ? "zero_linear" : "zero_block_norm") +
+                                   ": a bounded wait ran out; outputs since the last check are not final");
 }
 catch (...) {
-    return exception_status("zero_linear_check");
+    return exception_status("zero_operators_check");
 }
 
 }  // extern "C"

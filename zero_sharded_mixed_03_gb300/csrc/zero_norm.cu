@@ -34,71 +34,149 @@ struct NormParams {
     float* gate_sums;          // [worker][2][dim]: a gate group's part in the worker's first / last rows
     int64_t chunk;             // backward: consecutive rows a worker takes
     int32_t dim, post, pre;
+    int32_t ragged;            // some thread holds less than the others
+    int32_t bias_sums;         // the biases' gradients are asked for
     float eps, scale, inv_dim;
 };
 
-// Which eight elements of a row a thread holds: neighbours where every row starts on 16 bytes, else
-// every T-th, so that a warp's accesses are to neighbouring elements either way.
-template <bool VEC>
+// Which elements of a row a thread holds: V times eight.  Where every row starts on 16 bytes eight
+// neighbours, else every T-th, so that a warp's accesses are to neighbouring elements either way.
+template <bool VEC, int V>
 struct Lane {
-    int tid, T, n;             // n: elements held
+    int tid, T, n;             // n: elements held (VEC: eights)
     __device__ __forceinline__ Lane(int tid_, int T_, int dim) : tid(tid_), T(T_)
     {
-        if constexpr (VEC) n = tid * 8 < dim ? 8 : 0;
-        else n = tid < dim ? min(8, (dim - tid + T - 1) / T) : 0;
+        if constexpr (VEC) n = tid * 8 < dim ? (dim - tid * 8 + 8 * T - 1) / (8 * T) : 0;
+        else n = tid < dim ? (dim - tid + T - 1) / T : 0;
     }
-    __device__ __forceinline__ int at(int j) const { return VEC ? tid * 8 + j : tid + j * T; }
+    __device__ __forceinline__ bool has(int k) const { return VEC ? (k >> 3) < n : k < n; }
+    __device__ __forceinline__ int at(int k) const { return VEC ? ((k >> 3) * T + tid) * 8 + (k & 7) : tid + k * T; }
 };
 
-// Eight 16-bit elements as loaded.
+// V times eight 16-bit elements as loaded.
+template <int V>
 struct Raw {
-    uint32_t w[4];
+    uint32_t w[4 * V];
 };
 
-template <bool VEC>
-__device__ __forceinline__ Raw load_raw(const uint16_t* p, const Lane<VEC>& L)
+template <bool VEC, int V>
+__device__ __forceinline__ Raw<V> load_raw(const uint16_t* p, const Lane<VEC, V>& L)
 {
-    Raw r;
+    Raw<V> r;
     if constexpr (VEC) {
-        const uint4 q = L.n ? *reinterpret_cast<const uint4*>(p + L.tid * 8) : make_uint4(0u, 0u, 0u, 0u);
-        r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint4 q = v < L.n ? *reinterpret_cast<const uint4*>(p + (v * L.T + L.tid) * 8) : make_uint4(0u, 0u, 0u, 0u);
+            r.w[4 * v] = q.x; r.w[4 * v + 1] = q.y; r.w[4 * v + 2] = q.z; r.w[4 * v + 3] = q.w;
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = 2 * j < L.n ? p[L.at(2 * j)] : 0u, hi = 2 * j + 1 < L.n ? p[L.at(2 * j + 1)] : 0u;
-            r.w[j] = lo | (hi << 16);
+        for (int k = 0; k < 4 * V; ++k) {
+            const uint32_t lo = 2 * k < L.n ? p[L.at(2 * k)] : 0u, hi = 2 * k + 1 < L.n ? p[L.at(2 * k + 1)] : 0u;
+            r.w[k] = lo | (hi << 16);
         }
     }
     return r;
 }
 
 template <int DT>
-__device__ __forceinline__ void widen8(const Raw& r, float (&x)[8])
+__device__ __forceinline__ F2 widen(uint32_t w)
 {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) widen2<DT>(r.w[j], x[2 * j], x[2 * j + 1]);
+    float a, b;
+    widen2<DT>(w, a, b);
+    return pair(a, b);
 }
 
 // An optional vector of weights: `other` where there is none.
-template <int DT, bool VEC>
-__device__ __forceinline__ Raw load_weight(const uint16_t* p, const Lane<VEC>& L, float other)
+template <int DT, bool VEC, int V>
+__device__ __forceinline__ Raw<V> load_weight(const uint16_t* p, const Lane<VEC, V>& L, float other)
 {
-    if (p) return load_raw<VEC>(p, L);
+    if (p) return load_raw<VEC, V>(p, L);
+    Raw<V> r;
     const uint32_t w = narrow2<DT>(other, other);
-    return Raw{{w, w, w, w}};
+#pragma unroll
+    for (int k = 0; k < 4 * V; ++k) r.w[k] = w;
+    return r;
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_row(uint16_t* p, const Lane<VEC>& L, const float (&x)[8])
+template <int DT, bool VEC, int V>
+__device__ __forceinline__ void store_row(uint16_t* p, const Lane<VEC, V>& L, const F2 (&x)[4 * V])
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float a, b;
+            split(x[4 * v + k], a, b);
+            w[k] = narrow2<DT>(a, b);
+        }
+        if constexpr (VEC) {
+            if (v < L.n) *reinterpret_cast<uint4*>(p + (v * L.T + L.tid) * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (8 * v + k < L.n) p[L.at(8 * v + k)] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+        }
+    }
+}
+
+// A worker's fp32 sums: dim floats, not aligned beyond 4 bytes where dim is odd.
+template <bool VEC, int V>
+__device__ __forceinline__ void store_sums(float* p, const Lane<VEC, V>& L, const F2 (&x)[4 * V])
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float t[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split(x[4 * v + k], t[2 * k], t[2 * k + 1]);
+        if constexpr (VEC) {
+            if (v < L.n) {
+                float4* q = reinterpret_cast<float4*>(p + (v * L.T + L.tid) * 8);
+                q[0] = make_float4(t[0], t[1], t[2], t[3]);
+                q[1] = make_float4(t[4], t[5], t[6], t[7]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (8 * v + k < L.n) p[L.at(8 * v + k)] = t[k];
+        }
+    }
+}
+
+__device__ __forceinline__ float total(F2 x)
+{
+    float a, b;
+    split(x, a, b);
+    return a + b;
+}
+
+// What a thread does not hold becomes 0.
+template <bool VEC, int V>
+__device__ __forceinline__ void clear_rest(const Lane<VEC, V>& L, F2 (&x)[4 * V])
+{
+#pragma unroll
+    for (int k = 0; k < 4 * V; ++k) {
+        if constexpr (VEC) {
+            if ((k >> 2) >= L.n) x[k] = both(0.0f);
+        } else {
+            float a, b;
+            split(x[k], a, b);
+            x[k] = pair(2 * k < L.n ? a : 0.0f, 2 * k + 1 < L.n ? b : 0.0f);
+        }
+    }
+}
+
+// One pair of them: 0 where the thread does not hold it.
+template <bool VEC, int V>
+__device__ __forceinline__ F2 held(const Lane<VEC, V>& L, int k, F2 x)
 {
     if constexpr (VEC) {
-        if (L.n)
-            *reinterpret_cast<uint4*>(p + L.tid * 8) = make_uint4(narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]),
-                                                                  narrow2<DT>(x[4], x[5]), narrow2<DT>(x[6], x[7]));
+        return (k >> 2) < L.n ? x : both(0.0f);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < L.n) p[L.at(j)] = narrow1<DT>(x[j]);
+        float a, b;
+        split(x, a, b);
+        return pair(2 * k < L.n ? a : 0.0f, 2 * k + 1 < L.n ? b : 0.0f);
     }
 }
 
@@ -120,246 +198,431 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], int T, float* area, int&
 #pragma unroll
         for (int k = 0; k < NV; ++k) s[k * 32 + warp] = v[k];
     __syncthreads();
+    if (warps == 2) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        v[k] = lane < warps ? s[k * 32 + lane] : 0.0f;
+        for (int k = 0; k < NV; ++k) v[k] = s[k * 32] + s[k * 32 + 1];
+    } else if (warps <= 4) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+        for (int k = 0; k < NV; ++k)
+            v[k] = (s[k * 32] + s[k * 32 + 1]) + (s[k * 32 + 2] + (warps == 4 ? s[k * 32 + 3] : 0.0f));
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            v[k] = lane < warps ? s[k * 32 + lane] : 0.0f;
+            if (warps > 16) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], 16);
+            if (warps > 8) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], 8);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+            v[k] = __shfl_sync(0xFFFFFFFFu, v[k], 0);
+        }
     }
 }
 
 // x centred (LAYER) in place, and 1 / sqrt(mean square + eps).
-template <bool LAYER, bool VEC>
-__device__ __forceinline__ float centre(float (&x)[8], const Lane<VEC>& L, const NormParams& P, int T, float* area, int& turn)
+template <bool LAYER, bool VEC, int V>
+__device__ __forceinline__ float centre(F2 (&x)[4 * V], const Lane<VEC, V>& L, const NormParams& P, int T, float* area, int& turn)
 {
     float s[1];
     if constexpr (LAYER) {
-        s[0] = 0.0f;
+        F2 sum = x[0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += x[j];
+        for (int k = 1; k < 4 * V; ++k) sum = add(sum, x[k]);
+        s[0] = total(sum);
         row_sum(s, T, area, turn);
-        const float mean = s[0] * P.inv_dim;
+        const F2 minus_mean = both(-s[0] * P.inv_dim);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < L.n ? x[j] - mean : 0.0f;
+        for (int k = 0; k < 4 * V; ++k) x[k] = add(x[k], minus_mean);
+        if (P.ragged) clear_rest<VEC, V>(L, x);
     }
-    s[0] = 0.0f;
+    F2 sum = mul(x[0], x[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[0] = fmaf(x[j], x[j], s[0]);
+    for (int k = 1; k < 4 * V; ++k) sum = fma(x[k], x[k], sum);
+    s[0] = total(sum);
     row_sum(s, T, area, turn);
     return rsqrtf(s[0] * P.inv_dim + P.eps);
 }
 
+// The gate row of consecutive or strided rows, without a division a row.
+struct GateRow {
+    int64_t group, rest, step_group, step_rest, rows;
+    __device__ __forceinline__ GateRow(int64_t row, int64_t step, int64_t rows_)
+        : group(row / rows_), rest(row % rows_), step_group(step / rows_), step_rest(step % rows_), rows(rows_)
+    {
+    }
+    __device__ __forceinline__ void next()
+    {
+        group += step_group;
+        rest += step_rest;
+        if (rest >= rows) {
+            rest -= rows;
+            ++group;
+        }
+    }
+};
+
+// ---------------------------------------------------------------- rows on their way
+//
+// Rows of two warps and more whose tensors start on 16 bytes come through shared memory: one thread
+// issues a bulk copy a tensor (TMA) for the row kStages - 1 ahead, all on one mbarrier of that row's
+// stage, and no thread's registers wait for memory.  A stage is free again once every thread has passed
+// the first sum of the next row.  Waits are bounded; one that runs out is reported
+// (zero_operators_check), is the last one that its thread makes, and leaves the control flow as it is.
+constexpr int kRowStages = 3;
+constexpr uint64_t kRowWaitNs = 1000000000ull;
+__device__ uint32_t g_norm_error;
+
+struct RowPipe {
+    uint32_t bars, data, stage_bytes, row_bytes;
+    uint32_t issued = 0;       // thread 0: rows asked for
+    bool dead = false;
+
+    __device__ __forceinline__ void init(unsigned char* shared, int dim, int arrays)
+    {
+        bars = (uint32_t)__cvta_generic_to_shared(shared);
+        data = bars + 64;
+        row_bytes = 2 * dim;
+        stage_bytes = arrays * row_bytes;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kRowStages; ++i) mbar_init(bars + 8 * i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncthreads();
+    }
+    // thread 0: the next row's copies; `rows` holds the arrays' addresses of that row
+    template <int N>
+    __device__ __forceinline__ void issue(const uint16_t* const (&rows)[N])
+    {
+        const uint32_t s = issued % kRowStages, bar = bars + 8 * s;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) bytes += rows[i] ? row_bytes : 0u;
+        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (rows[i])
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 data + s * stage_bytes + i * row_bytes),
+                             "l"(rows[i]), "r"(row_bytes), "r"(bar)
+                             : "memory");
+        ++issued;
+    }
+    __device__ __forceinline__ void wait(uint32_t row)
+    {
+        if (dead) return;
+        if (!mbar_wait(bars + 8 * (row % kRowStages), (row / kRowStages) & 1, kRowWaitNs)) {
+            atomicOr(&g_norm_error, 1u);
+            dead = true;
+        }
+    }
+    // thread 0, at the end: no copy may outlive the block
+    __device__ __forceinline__ void drain(uint32_t done)
+    {
+        for (uint32_t r = done; r < issued; ++r) mbar_wait(bars + 8 * (r % kRowStages), (r / kRowStages) & 1, kRowWaitNs);
+    }
+    template <int V>
+    __device__ __forceinline__ Raw<V> get(uint32_t row, int array, const Lane<true, V>& L) const
+    {
+        Raw<V> r;
+        const uint32_t at = data + (row % kRowStages) * stage_bytes + array * row_bytes;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (v < L.n)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                             : "r"(at + (v * L.T + L.tid) * 16)
+                             : "memory");
+            r.w[4 * v] = q.x; r.w[4 * v + 1] = q.y; r.w[4 * v + 2] = q.z; r.w[4 * v + 3] = q.w;
+        }
+        return r;
+    }
+};
+
+constexpr int pipe_bytes(int64_t dim, int arrays) { return 64 + kRowStages * arrays * 2 * (int)dim; }
+
 // Forward: threads (T, rows a block); a block of more than one row has T = 32.
-template <int DT, bool VEC, bool LAYER, int MOST>
-__global__ void __launch_bounds__(MOST) block_norm_kernel(const __grid_constant__ NormParams P)
+template <int DT, bool VEC, bool LAYER, int V, bool STAGED>
+__global__ void __launch_bounds__(V == 4 ? 256 : 512) block_norm_kernel(const __grid_constant__ NormParams P)
 {
     __shared__ float area[2 * kSumArea];
+    extern __shared__ __align__(128) unsigned char stages[];
     const int T = blockDim.x;
-    const Lane<VEC> L(threadIdx.x, T, P.dim);
+    const Lane<VEC, V> L(threadIdx.x, T, P.dim);
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= P.rows) return;                    // whole blocks, or warps that sum by themselves
-    const Raw post_w = load_weight<DT, VEC>(P.post_w, L, 1.0f), post_b = load_weight<DT, VEC>(P.post_b, L, 0.0f);
-    const Raw pre_w = load_weight<DT, VEC>(P.pre_w, L, 1.0f), pre_b = load_weight<DT, VEC>(P.pre_b, L, 0.0f);
     int turn = 0;
-    Raw h = load_raw<VEC>(P.h + row * P.ld_h, L), x = {}, gate = {};
-    if (P.x) x = load_raw<VEC>(P.x + row * P.ld_x, L);
-    int64_t group = 0;
-    if (P.gate) {
-        group = row / P.gate_rows;
-        gate = load_raw<VEC>(P.gate + group * P.ld_gate, L);
+    RowPipe pipe;
+    const bool own_gates = P.gate && P.gate_rows == 1;
+    auto ask = [&](int64_t r) {
+        const uint16_t* const rows[3] = {P.h + r * P.ld_h, P.x ? P.x + r * P.ld_x : nullptr, own_gates ? P.gate + r * P.ld_gate : nullptr};
+        pipe.issue(rows);
+    };
+    if constexpr (STAGED) {
+        pipe.init(stages, P.dim, own_gates ? 3 : 2);
+        if (threadIdx.x == 0)
+            for (int k = 0; k < kRowStages && row + k * step < P.rows; ++k) ask(row + k * step);
     }
-    for (; row < P.rows; row += step) {
-        float a[8], b[8], w[8];
-        widen8<DT>(h, a);
-        widen8<DT>(x, b);
-        float g[8];
-        if (P.gate) widen8<DT>(gate, g);
-        if (row + step < P.rows) {
-            h = load_raw<VEC>(P.h + (row + step) * P.ld_h, L);
-            if (P.x) x = load_raw<VEC>(P.x + (row + step) * P.ld_x, L);
-            if (P.gate) {
-                const int64_t next = (row + step) / P.gate_rows;
-                if (next != group) gate = load_raw<VEC>(P.gate + next * P.ld_gate, L);
-                group = next;
+    GateRow at(P.gate ? row : 0, step, P.gate ? P.gate_rows : 1);
+    uint32_t n = 0;
+    for (; row < P.rows; row += step, ++n) {
+        F2 a[4 * V];
+        Raw<V> h, x = {};
+        if constexpr (STAGED) {
+            pipe.wait(n);
+            h = pipe.get<V>(n, 0, L);
+        } else {
+            h = load_raw<VEC, V>(P.h + row * P.ld_h, L);
+            if (P.x) x = load_raw<VEC, V>(P.x + row * P.ld_x, L);
+        }
+#pragma unroll
+        for (int k = 0; k < 4 * V; ++k) a[k] = widen<DT>(h.w[k]);
+        // every thread is past the first sum: the row before is done with, its stage is free
+        auto refill = [&]() {
+            if constexpr (STAGED) {
+                const int64_t r = row + (kRowStages - 1) * step;
+                if (threadIdx.x == 0 && n > 0 && r < P.rows) ask(r);
+            }
+        };
+        if (P.post) {
+            const F2 r = both(centre<LAYER, VEC, V>(a, L, P, T, area, turn));
+            refill();
+            const Raw<V> w = load_weight<DT, VEC, V>(P.post_w, L, 1.0f);
+#pragma unroll
+            for (int k = 0; k < 4 * V; ++k) a[k] = mul(mul(a[k], r), widen<DT>(w.w[k]));
+            if (P.post_b) {
+                const Raw<V> c = load_raw<VEC, V>(P.post_b, L);
+#pragma unroll
+                for (int k = 0; k < 4 * V; ++k) a[k] = add(a[k], widen<DT>(c.w[k]));
             }
         }
-        if (P.post) {
-            const float r = centre<LAYER, VEC>(a, L, P, T, area, turn);
-            widen8<DT>(post_w, w);
+        const F2 scale = both(P.scale);
+        if (P.gate) {
+            Raw<V> gate;
+            if constexpr (STAGED) gate = own_gates ? pipe.get<V>(n, 2, L) : load_raw<VEC, V>(P.gate + at.group * P.ld_gate, L);
+            else gate = load_raw<VEC, V>(P.gate + at.group * P.ld_gate, L);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = a[j] * r * w[j];
-            widen8<DT>(post_b, w);
+            for (int k = 0; k < 4 * V; ++k) a[k] = mul(a[k], mul(scale, widen<DT>(gate.w[k])));
+            at.next();
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] += w[j];
+            for (int k = 0; k < 4 * V; ++k) a[k] = mul(a[k], scale);
         }
+        if (P.x) {
+            if constexpr (STAGED) x = pipe.get<V>(n, 1, L);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = fmaf(P.gate ? P.scale * g[j] : P.scale, a[j], b[j]);
-        if (P.y) store_row<DT, VEC>(P.y + row * P.ld_y, L, a);
+            for (int k = 0; k < 4 * V; ++k) a[k] = add(a[k], widen<DT>(x.w[k]));
+        }
+        if (P.y) store_row<DT, VEC, V>(P.y + row * P.ld_y, L, a);
         if (P.pre) {
+            if (P.ragged) clear_rest<VEC, V>(L, a);
+            const F2 r = both(centre<LAYER, VEC, V>(a, L, P, T, area, turn));
+            if (!P.post) refill();
+            const Raw<V> w = load_weight<DT, VEC, V>(P.pre_w, L, 1.0f), c = load_weight<DT, VEC, V>(P.pre_b, L, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = j < L.n ? a[j] : 0.0f;
-            const float r = centre<LAYER, VEC>(a, L, P, T, area, turn);
-            widen8<DT>(pre_w, w);
-            widen8<DT>(pre_b, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = fmaf(a[j] * r, w[j], b[j]);
-            store_row<DT, VEC>(P.z + row * P.ld_z, L, a);
+            for (int k = 0; k < 4 * V; ++k) a[k] = fma(mul(a[k], r), widen<DT>(w.w[k]), widen<DT>(c.w[k]));
+            store_row<DT, VEC, V>(P.z + row * P.ld_z, L, a);
         }
     }
+    if constexpr (STAGED)
+        if (threadIdx.x == 0) pipe.drain(n);
 }
 
-// A worker's sums over its rows, eight columns a thread: registers, or shared memory.
+// A worker's sums over its rows, by column: registers, or shared memory.
 enum { kPreW = 0, kPostW = 1, kGate = 2, kPreB = 3, kPostB = 4 };
-template <bool SHARED, int NACC>
+template <bool SHARED, int NACC, int V>
 struct Acc {
-    float v[SHARED ? 1 : NACC][8];
-    float* s;
+    F2 v[SHARED ? 1 : NACC][4 * V];
+    F2* s;
     int tid, T;
-    __device__ __forceinline__ Acc(float* shared, int tid_, int T_) : s(shared), tid(tid_), T(T_)
+    __device__ __forceinline__ Acc(F2* shared, int tid_, int T_) : s(shared), tid(tid_), T(T_) {}
+    __device__ __forceinline__ F2& at(int k, int j)
     {
-#pragma unroll
-        for (int k = 0; k < NACC; ++k) clear(k);
-    }
-    __device__ __forceinline__ float& at(int k, int j)
-    {
-        if constexpr (SHARED) return s[(k * 8 + j) * T + tid];
+        if constexpr (SHARED) return s[(k * 4 * V + j) * T + tid];
         else return v[k][j];
     }
     __device__ __forceinline__ void clear(int k)
     {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) at(k, j) = 0.0f;
+        for (int j = 0; j < 4 * V; ++j) at(k, j) = both(0.0f);
     }
 };
 
-template <int DT, bool VEC, bool LAYER, bool BIAS, bool SHARED>
-__global__ void __launch_bounds__(SHARED ? 1024 : 512) block_norm_grad_kernel(const __grid_constant__ NormParams P)
+// The sums of the biases' gradients are kept where they may be asked for: with ZERO_NORM_LAYER, and
+// in the variant with shared memory.
+template <int DT, bool VEC, bool LAYER, int V, bool SHARED, bool STAGED>
+__global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHARED ? 2 : 1)
+    block_norm_grad_kernel(const __grid_constant__ NormParams P)
 {
     __shared__ float area[2 * kSumArea];
-    extern __shared__ float acc_shared[];
+    extern __shared__ __align__(128) unsigned char stages[];
+    constexpr bool BIAS = LAYER || SHARED;
     constexpr int NACC = BIAS ? 5 : 3;
     const int T = blockDim.x;
-    const Lane<VEC> L(threadIdx.x, T, P.dim);
+    const Lane<VEC, V> L(threadIdx.x, T, P.dim);
     const int64_t worker = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t r0 = worker * P.chunk, r1 = min(P.rows, r0 + P.chunk);
     if (r0 >= r1) return;                         // whole blocks, or warps that sum by themselves
-    Acc<SHARED, NACC> acc(acc_shared, threadIdx.x, T);
-    const Raw post_w = load_weight<DT, VEC>(P.post_w, L, 1.0f), post_b = load_weight<DT, VEC>(P.post_b, L, 0.0f);
-    const Raw pre_w = load_weight<DT, VEC>(P.pre_w, L, 1.0f);
-    const bool use_h = P.h != nullptr;
+    Acc<SHARED, NACC, V> acc(reinterpret_cast<F2*>(stages), threadIdx.x, T);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) acc.clear(k);
+    if constexpr (BIAS)
+        if (!SHARED || P.bias_sums)
+#pragma unroll
+            for (int k = 3; k < 5; ++k) acc.clear(k);
     int turn = 0;
-    Raw h = {}, y = {}, dy = {}, dz = {}, gate = {};
-    int64_t group = 0, group_first = 0;           // of the current row; the group's first row in the worker
-    auto fetch = [&](int64_t r) {
-        if (use_h) h = load_raw<VEC>(P.h + r * P.ld_h, L);
-        if (P.pre) {
-            y = load_raw<VEC>(P.y_in + r * P.ld_y, L);
-            dz = load_raw<VEC>(P.dz + r * P.ld_dz, L);
-        }
-        if (P.dy) dy = load_raw<VEC>(P.dy + r * P.ld_dy, L);
+    RowPipe pipe;
+    const bool own_gates = P.gate && P.gate_rows == 1;
+    auto ask = [&](int64_t r) {
+        const uint16_t* const rows[5] = {P.pre ? P.y_in + r * P.ld_y : nullptr, P.pre ? P.dz + r * P.ld_dz : nullptr,
+                                         P.h ? P.h + r * P.ld_h : nullptr, P.dy ? P.dy + r * P.ld_dy : nullptr,
+                                         own_gates ? P.gate + r * P.ld_gate : nullptr};
+        pipe.issue(rows);
     };
-    fetch(r0);
-    if (P.gate_rows) {
-        group = r0 / P.gate_rows;
-        group_first = r0;
-        if (P.gate) gate = load_raw<VEC>(P.gate + group * P.ld_gate, L);
+    if constexpr (STAGED) {
+        pipe.init(stages, P.dim, own_gates ? 5 : 4);
+        if (threadIdx.x == 0)
+            for (int k = 0; k < kRowStages && r0 + k < r1; ++k) ask(r0 + k);
     }
+    GateRow at(P.gate_rows ? r0 : 0, 1, P.gate_rows ? P.gate_rows : 1);
+    int64_t group_first = r0;                     // the group's first row in the worker
+    const F2 scale = both(P.scale);
     for (int64_t row = r0; row < r1; ++row) {
-        float a[8], b[8], c[8], d[8], g[8], w[8];
-        widen8<DT>(h, a);
-        widen8<DT>(y, b);
-        widen8<DT>(dz, c);
-        widen8<DT>(dy, d);
-        if (P.gate) widen8<DT>(gate, g);
-        const int64_t this_group = group;
-        if (row + 1 < r1) {
-            fetch(row + 1);
-            if (P.gate_rows) {
-                group = (row + 1) / P.gate_rows;
-                if (P.gate && group != this_group) gate = load_raw<VEC>(P.gate + group * P.ld_gate, L);
-            }
-        }
-        // b, a: centred y and h; their sums, and those of g = dz w_pre
-        widen8<DT>(pre_w, w);
-        if constexpr (LAYER) {
-            float s[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[0] += a[j];
-                s[1] += b[j];
-            }
-            row_sum(s, T, area, turn);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (P.post) a[j] = j < L.n ? a[j] - s[0] * P.inv_dim : 0.0f;
-                b[j] = j < L.n ? b[j] - s[1] * P.inv_dim : 0.0f;
-            }
-        }
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s[0] = fmaf(a[j], a[j], s[0]);
-            s[1] = fmaf(b[j], b[j], s[1]);
-            s[2] = fmaf(c[j] * w[j], b[j], s[2]);
-            if (LAYER) s[3] = fmaf(c[j], w[j], s[3]);
-        }
-        if constexpr (LAYER) {
-            row_sum(s, T, area, turn);
+        const uint32_t n = (uint32_t)(row - r0);
+        Raw<V> hr = {}, yr = {}, zr = {}, dr = {};
+        if constexpr (STAGED) {
+            pipe.wait(n);
         } else {
-            float t[3] = {s[0], s[1], s[2]};
-            row_sum(t, T, area, turn);
-            s[0] = t[0];
-            s[1] = t[1];
-            s[2] = t[2];
+            if (P.pre) {
+                yr = load_raw<VEC, V>(P.y_in + row * P.ld_y, L);
+                zr = load_raw<VEC, V>(P.dz + row * P.ld_dz, L);
+            }
+            if (P.h) hr = load_raw<VEC, V>(P.h + row * P.ld_h, L);
+            if (P.dy) dr = load_raw<VEC, V>(P.dy + row * P.ld_dy, L);
         }
-        const float rh = rsqrtf(s[0] * P.inv_dim + P.eps), ry = rsqrtf(s[1] * P.inv_dim + P.eps);
-        if (P.pre) {
-            const float along = s[2] * P.inv_dim * ry * ry, mean = LAYER ? s[3] * P.inv_dim : 0.0f;
+        auto fetch = [&](int which, const Raw<V>& kept, bool there) {
+            if constexpr (STAGED) return there ? pipe.get<V>(n, which, L) : Raw<V>{};
+            else return kept;
+        };
+        // minus the means of y and h
+        F2 ma = both(0.0f), mb = both(0.0f);
+        auto refill = [&]() {
+            // every thread is past the first sum: the row before is done with, its stage is free
+            if constexpr (STAGED)
+                if (threadIdx.x == 0 && n > 0 && row + kRowStages - 1 < r1) ask(row + kRowStages - 1);
+        };
+        if constexpr (LAYER) {
+            const Raw<V> h = fetch(2, hr, P.h != nullptr), y = fetch(0, yr, P.pre);
+            F2 sa = both(0.0f), sb = sa;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc.at(kPreW, j) += c[j] * (b[j] * ry);
-                if constexpr (BIAS) acc.at(kPreB, j) += c[j];
-                d[j] += ry * (c[j] * w[j] - mean - b[j] * along);
+            for (int k = 0; k < 4 * V; ++k) {
+                sa = add(sa, widen<DT>(h.w[k]));
+                sb = add(sb, widen<DT>(y.w[k]));
+            }
+            float s[2] = {total(sa), total(sb)};
+            row_sum(s, T, area, turn);
+            refill();
+            ma = both(P.post ? -s[0] * P.inv_dim : 0.0f);
+            mb = both(-s[1] * P.inv_dim);
+        }
+        auto centred = [&](uint32_t w, F2 minus_mean, int k) {
+            const F2 x = widen<DT>(w);
+            if constexpr (LAYER) {
+                const F2 c = add(x, minus_mean);
+                return P.ragged ? held<VEC, V>(L, k, c) : c;
+            } else {
+                return x;
+            }
+        };
+        F2 d[4 * V];
+        float rh = 1.0f;
+        {
+            float s[4];
+            {
+                const Raw<V> h = fetch(2, hr, P.h != nullptr), y = fetch(0, yr, P.pre), z = fetch(1, zr, P.pre);
+                const Raw<V> w = load_weight<DT, VEC, V>(P.pre_w, L, 1.0f);
+                F2 s0 = both(0.0f), s1 = s0, s2 = s0, s3 = s0;
+#pragma unroll
+                for (int k = 0; k < 4 * V; ++k) {
+                    const F2 a = centred(h.w[k], ma, k), b = centred(y.w[k], mb, k), g = mul(widen<DT>(z.w[k]), widen<DT>(w.w[k]));
+                    s0 = fma(a, a, s0);
+                    s1 = fma(b, b, s1);
+                    s2 = fma(g, b, s2);
+                    if (LAYER) s3 = add(s3, g);
+                }
+                s[0] = total(s0);
+                s[1] = total(s1);
+                s[2] = total(s2);
+                s[3] = total(s3);
+            }
+            if constexpr (LAYER) {
+                row_sum(s, T, area, turn);
+            } else {
+                float t[3] = {s[0], s[1], s[2]};
+                row_sum(t, T, area, turn);
+                refill();
+                s[0] = t[0];
+                s[1] = t[1];
+                s[2] = t[2];
+            }
+            if (P.post) rh = rsqrtf(s[0] * P.inv_dim + P.eps);
+            const Raw<V> e = fetch(3, dr, P.dy != nullptr);
+#pragma unroll
+            for (int k = 0; k < 4 * V; ++k) d[k] = widen<DT>(e.w[k]);
+            if (P.pre) {
+                const float ry = rsqrtf(s[1] * P.inv_dim + P.eps);
+                const F2 r = both(ry), along = both(-s[2] * P.inv_dim * ry * ry), mean = both(LAYER ? -s[3] * P.inv_dim : 0.0f);
+                const Raw<V> y = fetch(0, yr, true), z = fetch(1, zr, true), w = load_weight<DT, VEC, V>(P.pre_w, L, 1.0f);
+#pragma unroll
+                for (int k = 0; k < 4 * V; ++k) {
+                    const F2 b = centred(y.w[k], mb, k), c = widen<DT>(z.w[k]);
+                    acc.at(kPreW, k) = fma(c, mul(b, r), acc.at(kPreW, k));
+                    if constexpr (BIAS)
+                        if (!SHARED || P.bias_sums) acc.at(kPreB, k) = add(acc.at(kPreB, k), c);
+                    F2 g = fma(c, widen<DT>(w.w[k]), mul(b, along));
+                    if (LAYER) g = add(g, mean);
+                    d[k] = fma(r, g, d[k]);
+                }
             }
         }
-        if (P.dx) store_row<DT, VEC>(P.dx + row * P.ld_dx, L, d);
-        // through the gate: b becomes the normalised h, d becomes du
-        if (P.post) {
-            widen8<DT>(post_w, w);
+        if (P.dx) store_row<DT, VEC, V>(P.dx + row * P.ld_dx, L, d);
+        const int64_t group = at.group;
+        const bool group_ends = row + 1 == r1 || (P.gate_rows && at.rest + 1 == P.gate_rows);
+        at.next();
+        if (!P.dh && !P.sums && !P.dgate) continue;
+        // through the gate: a is the normalised h, d becomes du
+        F2 a[4 * V];
+        {
+            const Raw<V> h = fetch(2, hr, P.h != nullptr);
+            const F2 r = both(rh);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] = a[j] * rh;
+            for (int k = 0; k < 4 * V; ++k) a[k] = mul(centred(h.w[k], ma, k), r);
         }
         if (P.dgate) {
-            float u[8];
+            F2 u[4 * V];
+#pragma unroll
+            for (int k = 0; k < 4 * V; ++k) u[k] = a[k];
             if (P.post) {
-                widen8<DT>(post_b, u);
+                const Raw<V> w = load_weight<DT, VEC, V>(P.post_w, L, 1.0f), e = load_weight<DT, VEC, V>(P.post_b, L, 0.0f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = fmaf(b[j], w[j], u[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = a[j];
+                for (int k = 0; k < 4 * V; ++k) u[k] = fma(a[k], widen<DT>(w.w[k]), widen<DT>(e.w[k]));
             }
             if (P.gate_rows == 1) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = P.scale * d[j] * u[j];
-                store_row<DT, VEC>(P.dgate + row * P.ld_dgate, L, u);
+                for (int k = 0; k < 4 * V; ++k) u[k] = mul(mul(scale, d[k]), u[k]);
+                store_row<DT, VEC, V>(P.dgate + row * P.ld_dgate, L, u);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc.at(kGate, j) += P.scale * d[j] * u[j];
-                if (row + 1 == r1 || group != this_group) {
-                    // the end of the group, or of the worker: whole groups are final
-                    const int64_t first = this_group * P.gate_rows, last = min(P.rows, first + P.gate_rows) - 1;
-                    float t[8];
+                for (int k = 0; k < 4 * V; ++k) acc.at(kGate, k) = fma(mul(scale, d[k]), u[k], acc.at(kGate, k));
+                if (group_ends) {
+                    // whole groups are final; else a part of one, in the worker's first or last slot
+                    const int64_t first = group * P.gate_rows, last = min(P.rows, first + P.gate_rows) - 1;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) t[j] = acc.at(kGate, j);
+                    for (int k = 0; k < 4 * V; ++k) u[k] = acc.at(kGate, k);
                     if (first >= r0 && last < r1) {
-                        store_row<DT, VEC>(P.dgate + this_group * P.ld_dgate, L, t);
+                        store_row<DT, VEC, V>(P.dgate + group * P.ld_dgate, L, u);
                     } else {
-                        float* q = P.gate_sums + (worker * 2 + (group_first == r0 ? 0 : 1)) * P.dim;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j < L.n) q[L.at(j)] = t[j];
+                        store_sums<VEC, V>(P.gate_sums + (worker * 2 + (group_first == r0 ? 0 : 1)) * P.dim, L, u);
                     }
                     acc.clear(kGate);
                     group_first = row + 1;
@@ -367,18 +630,30 @@ __global__ void __launch_bounds__(SHARED ? 1024 : 512) block_norm_grad_kernel(co
             }
         }
         if (!P.dh && !P.sums) continue;
+        if (P.gate) {
+            Raw<V> gate;
+            if constexpr (STAGED) gate = own_gates ? pipe.get<V>(n, 4, L) : load_raw<VEC, V>(P.gate + group * P.ld_gate, L);
+            else gate = load_raw<VEC, V>(P.gate + group * P.ld_gate, L);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= P.gate ? P.scale * g[j] : P.scale;
+            for (int k = 0; k < 4 * V; ++k) d[k] = mul(d[k], mul(scale, widen<DT>(gate.w[k])));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4 * V; ++k) d[k] = mul(d[k], scale);
+        }
         if (P.post) {
-            float t[2] = {0.0f, 0.0f};
+            const Raw<V> w = load_weight<DT, VEC, V>(P.post_w, L, 1.0f);
+            F2 s0 = both(0.0f), s1 = s0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc.at(kPostW, j) += d[j] * b[j];
-                if constexpr (BIAS) acc.at(kPostB, j) += d[j];
-                d[j] = j < L.n ? d[j] * w[j] : 0.0f;
-                t[0] = fmaf(d[j], b[j], t[0]);
-                t[1] += d[j];
+            for (int k = 0; k < 4 * V; ++k) {
+                acc.at(kPostW, k) = fma(d[k], a[k], acc.at(kPostW, k));
+                if constexpr (BIAS)
+                    if (!SHARED || P.bias_sums) acc.at(kPostB, k) = add(acc.at(kPostB, k), d[k]);
+                d[k] = mul(d[k], widen<DT>(w.w[k]));
+                if (P.ragged) d[k] = held<VEC, V>(L, k, d[k]);
+                s0 = fma(d[k], a[k], s0);
+                if (LAYER) s1 = add(s1, d[k]);
             }
+            float t[2] = {total(s0), total(s1)};
             if constexpr (LAYER) {
                 row_sum(t, T, area, turn);
             } else {
@@ -386,27 +661,34 @@ __global__ void __launch_bounds__(SHARED ? 1024 : 512) block_norm_grad_kernel(co
                 row_sum(one, T, area, turn);
                 t[0] = one[0];
             }
-            const float along = t[0] * P.inv_dim, mean = LAYER ? t[1] * P.inv_dim : 0.0f;
+            const F2 along = both(-t[0] * P.inv_dim * rh), mean = both(LAYER ? -t[1] * P.inv_dim * rh : 0.0f), r = both(rh);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = rh * (d[j] - mean - b[j] * along);
+            for (int k = 0; k < 4 * V; ++k) {
+                F2 g = mul(a[k], along);
+                if (LAYER) g = add(g, mean);
+                d[k] = fma(r, d[k], g);
+            }
         }
-        if (P.dh) store_row<DT, VEC>(P.dh + row * P.ld_dh, L, d);
+        if (P.dh) store_row<DT, VEC, V>(P.dh + row * P.ld_dh, L, d);
     }
     if (P.sums) {
         float* q = P.sums + worker * 4 * P.dim;
+        F2 t[4 * V];
+        auto put = [&](int k, int row) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j < L.n) {
-                const int e = L.at(j);
-                q[e] = acc.at(kPreW, j);
-                q[2 * P.dim + e] = acc.at(kPostW, j);
-                if constexpr (BIAS) {
-                    q[P.dim + e] = acc.at(kPreB, j);
-                    q[3 * P.dim + e] = acc.at(kPostB, j);
-                }
+            for (int j = 0; j < 4 * V; ++j) t[j] = acc.at(k, j);
+            store_sums<VEC, V>(q + row * P.dim, L, t);
+        };
+        put(kPreW, 0);
+        put(kPostW, 2);
+        if constexpr (BIAS)
+            if (P.bias_sums) {
+                put(kPreB, 1);
+                put(kPostB, 3);
             }
-        }
     }
+    if constexpr (STAGED)
+        if (threadIdx.x == 0) pipe.drain((uint32_t)(r1 - r0));
 }
 
 struct SumParams {
@@ -420,38 +702,61 @@ struct SumParams {
 };
 
 // Block (column chunk, j): j < 4 adds the workers' sums of one weight; j >= 4 the parts of one gate
-// group that spans workers.  32 columns by 32 workers at a time, in a fixed order.
-template <int DT>
-__global__ void __launch_bounds__(1024) block_norm_sum_kernel(const __grid_constant__ SumParams P)
+// group that spans workers.  32 columns by 8 workers at a time, four columns a thread where dim
+// allows, in a fixed order.
+template <int DT, int C>
+__global__ void __launch_bounds__(256) block_norm_sum_kernel(const __grid_constant__ SumParams P)
 {
-    __shared__ float part[32][33];
-    const int col = blockIdx.x * 32 + threadIdx.x, lane = threadIdx.y;
-    float s = 0.0f;
+    __shared__ float part[8][32 * C + 1];
+    const int col = (blockIdx.x * 32 + threadIdx.x) * C, lane = threadIdx.y;
+    const float* from;
+    int64_t w0, w1, stride;
     uint16_t* out;
+    bool later = false;        // the group starts after its first worker's first row: the second slot
     if (blockIdx.y < 4) {
         out = P.out[blockIdx.y];
         if (!out) return;
-        if (col < P.dim)
-            for (int64_t w = lane; w < P.workers; w += 32) s += P.sums[(w * 4 + blockIdx.y) * P.dim + col];
+        from = P.sums + (int64_t)blockIdx.y * P.dim;
+        stride = 4 * P.dim;
+        w0 = 0;
+        w1 = P.workers - 1;
     } else {
         if (!P.dgate) return;
         const int64_t i = blockIdx.y - 4;
         const int64_t group = P.by_group ? i : (min(P.rows, (i + 1) * P.chunk) - 1) / P.gate_rows;
         const int64_t first = group * P.gate_rows, last = min(P.rows, first + P.gate_rows) - 1;
-        const int64_t w0 = first / P.chunk, w1 = last / P.chunk;
+        w0 = first / P.chunk;
+        w1 = last / P.chunk;
         if (w0 == w1 || (!P.by_group && w0 != i)) return;      // whole in one worker, or another block's
         out = P.dgate + group * P.ld_dgate;
-        if (col < P.dim)
-            for (int64_t w = w0 + lane; w <= w1; w += 32)
-                s += P.gate_sums[(w * 2 + (w == w0 && first > w0 * P.chunk ? 1 : 0)) * P.dim + col];
+        from = P.gate_sums;
+        stride = 2 * P.dim;
+        later = first > w0 * P.chunk;
     }
-    part[lane][threadIdx.x] = s;
-    __syncthreads();
-    if (lane == 0 && col < P.dim) {
-        s = 0.0f;
+    float s[C];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += part[i][threadIdx.x];
-        out[col] = narrow1<DT>(s);
+    for (int c = 0; c < C; ++c) s[c] = 0.0f;
+    if (col < P.dim) {
+#pragma unroll 8
+        for (int64_t w = w0 + lane; w <= w1; w += 8) {
+            const float* q = from + w * stride + (later && w == w0 ? P.dim : 0) + col;
+            if constexpr (C == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(q);
+                s[0] += f.x; s[1] += f.y; s[2] += f.z; s[3] += f.w;
+            } else {
+                s[0] += *q;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[lane][threadIdx.x * C + c] = s[c];
+    __syncthreads();
+    const int i = lane * 32 + threadIdx.x, e = blockIdx.x * 32 * C + i;
+    if (i < 32 * C && e < P.dim) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += part[k][i];
+        out[e] = narrow1<DT>(sum);
     }
 }
 
@@ -459,12 +764,33 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const __grid_const
 
 constexpr int kSms = 152;
 
-// Threads of a row, eight elements each; rows up to 256 elements are one warp, eight a block.
-int row_threads(int64_t dim) { return std::max(32, (int)((dim + 7) / 8 + 31) / 32 * 32); }
+// How a row is held: V eights a thread in T threads.  The sums over a row cost the same instructions
+// whatever a thread holds, so more elements a thread are better while registers last: 32 forward (16
+// where they come one by one), 16 backward (whose column sums take two and a half times as many
+// registers again).
+struct Hold {
+    int V = 1, T = 32;
+    bool even = true;          // every thread holds as much
+};
+
+Hold hold_row(int64_t dim, int most)
+{
+    Hold best;
+    for (int V = most; V >= 1; V /= 2) {
+        Hold h;
+        h.V = V;
+        h.T = (int)((dim + 8 * V * 32 - 1) / (8 * V * 32)) * 32;
+        h.even = (int64_t)h.T * 8 * V == dim;
+        // fewer idle places, in blocks that their kernels are built for
+        if (V == most || (h.T <= 256 && (int64_t)h.T * h.V < (int64_t)best.T * best.V)) best = h;
+    }
+    return best;
+}
 
 // How the backward pass cuts the rows: workers of `chunk` consecutive ones.
 struct Cut {
-    int T = 32, per_block = 1;
+    Hold hold;
+    int per_block = 1;
     bool shared = false;
     int64_t chunk = 1, workers = 0;
 };
@@ -472,10 +798,15 @@ struct Cut {
 Cut cut_rows(const zero_block_norm_t& a)
 {
     Cut c;
-    c.T = row_threads(a.dim);
-    c.per_block = c.T == 32 ? 8 : 1;
-    c.shared = c.T > 512;
-    const int blocks_per_sm = std::max(1, 512 / (c.T * c.per_block));
+    const bool layer = a.kind == ZERO_NORM_LAYER;
+    // five column sums leave registers for eight elements a thread, three for sixteen
+    c.hold = hold_row(a.dim, a.dim <= 256 || (layer && a.dim <= 4096) ? 1 : 2);
+    // more than 4096 elements (their threads' registers do not hold the column sums), and the biases'
+    // gradients of an RMS norm (the register variant keeps none)
+    c.shared = a.dim > 4096 || (!layer && (a.dpre_b || a.dpost_b));
+    if (c.shared) c.hold = hold_row(a.dim, 2);
+    c.per_block = c.hold.T == 32 && !c.shared ? 8 : 1;
+    const int blocks_per_sm = std::max(1, 512 / (c.hold.T * c.per_block));
     const int64_t most = (int64_t)kSms * blocks_per_sm * c.per_block;
     c.chunk = std::max<int64_t>(1, (a.rows + most - 1) / most);
     // chunks that end with gate groups where that costs little balance
@@ -612,59 +943,97 @@ NormParams params_of(const Checked& C, bool back)
     return P;
 }
 
-template <int DT, bool VEC, bool LAYER>
-void launch_forward(const NormParams& P, cudaStream_t s)
+constexpr int kMostShared = 227 * 1024 - 1024;   // beside the kernels' static shared memory
+
+// Dynamic shared memory beyond 48 KB has to be allowed once a kernel.
+template <auto KERNEL>
+zero_status_t allow_shared()
 {
-    const int T = row_threads(P.dim), per_block = T == 32 ? 8 : 1;
-    const int64_t blocks = (P.rows + per_block - 1) / per_block;
-    const int64_t most = (int64_t)kSms * std::max(1, 1536 / (T * per_block));
-    const unsigned grid = (unsigned)std::min(blocks, most);
-    // registers are allotted for the largest block a kernel may have: rows beyond 4096 elements are apart
-    if (T <= 512) block_norm_kernel<DT, VEC, LAYER, 512><<<grid, dim3(T, per_block), 0, s>>>(P);
-    else block_norm_kernel<DT, VEC, LAYER, 1024><<<grid, dim3(T, per_block), 0, s>>>(P);
+    static const cudaError_t set = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    return set == cudaSuccess ? ZERO_OK : cuda_fail(set, "zero_block_norm: shared memory");
 }
 
-template <int DT, bool VEC, bool LAYER, bool BIAS>
-zero_status_t launch_backward(const NormParams& P, const Cut& c, cudaStream_t s)
+template <auto KERNEL>
+zero_status_t launch(unsigned grid, dim3 threads, int64_t bytes, const NormParams& P, cudaStream_t s)
 {
-    const dim3 threads(c.T, c.per_block);
-    const unsigned grid = (unsigned)((c.workers + c.per_block - 1) / c.per_block);
-    if (c.shared) {
-        constexpr int kMost = (BIAS ? 5 : 3) * 8 * 1024 * 4;
-        static const cudaError_t set = cudaFuncSetAttribute(block_norm_grad_kernel<DT, VEC, LAYER, BIAS, true>,
-                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-        if (set != cudaSuccess) return cuda_fail(set, "zero_block_norm_backward: shared memory");
-        const int bytes = (BIAS ? 5 : 3) * 8 * c.T * 4;
-        block_norm_grad_kernel<DT, VEC, LAYER, BIAS, true><<<grid, threads, bytes, s>>>(P);
-    } else {
-        block_norm_grad_kernel<DT, VEC, LAYER, BIAS, false><<<grid, threads, 0, s>>>(P);
+    if (bytes > 48 * 1024) {
+        const zero_status_t st = allow_shared<KERNEL>();
+        if (st != ZERO_OK) return st;
     }
+    KERNEL<<<grid, threads, (size_t)bytes, s>>>(P);
     return ZERO_OK;
 }
 
 template <int DT, bool VEC, bool LAYER>
-zero_status_t launch_backward(const NormParams& P, const Cut& c, bool bias, cudaStream_t s)
+zero_status_t launch_forward(NormParams& P, cudaStream_t s)
 {
-    return bias ? launch_backward<DT, VEC, LAYER, true>(P, c, s) : launch_backward<DT, VEC, LAYER, false>(P, c, s);
+    const Hold h = hold_row(P.dim, VEC ? 4 : 2);
+    P.ragged = !h.even;
+    const int per_block = h.T == 32 ? 8 : 1;
+    const int64_t blocks = (P.rows + per_block - 1) / per_block;
+    const dim3 threads(h.T, per_block);
+    if constexpr (VEC) {
+        // a row of its own a block, and more rows than the GPU holds at once: through shared memory
+        const int64_t bytes = pipe_bytes(P.dim, P.gate && P.gate_rows == 1 ? 3 : 2);
+        if (h.T > 32 && (P.pre || P.post) && P.rows > 4 * kSms) {
+            const int64_t fit = std::min<int64_t>(kMostShared / (bytes + 2048), 2048 / (4 * h.T) * 3);
+            const unsigned grid = (unsigned)std::min<int64_t>(blocks, kSms * std::max<int64_t>(1, fit));
+            if (h.V == 4) return launch<block_norm_kernel<DT, VEC, LAYER, 4, true>>(grid, threads, bytes, P, s);
+            if (h.V == 2) return launch<block_norm_kernel<DT, VEC, LAYER, 2, true>>(grid, threads, bytes, P, s);
+            return launch<block_norm_kernel<DT, VEC, LAYER, 1, true>>(grid, threads, bytes, P, s);
+        }
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)kSms * std::max(1, 768 / (h.T * per_block)));
+    if constexpr (VEC)
+        if (h.V == 4) return launch<block_norm_kernel<DT, VEC, LAYER, 4, false>>(grid, threads, 0, P, s);
+    if (h.V == 2) return launch<block_norm_kernel<DT, VEC, LAYER, 2, false>>(grid, threads, 0, P, s);
+    return launch<block_norm_kernel<DT, VEC, LAYER, 1, false>>(grid, threads, 0, P, s);
+}
+
+template <int DT, bool VEC, bool LAYER>
+zero_status_t launch_backward(NormParams& P, const Cut& c, cudaStream_t s)
+{
+    const dim3 threads(c.hold.T, c.per_block);
+    const unsigned grid = (unsigned)((c.workers + c.per_block - 1) / c.per_block);
+    P.ragged = !c.hold.even;
+    if (c.shared) {
+        const int64_t bytes = (int64_t)(P.bias_sums ? 5 : 3) * 8 * c.hold.V * c.hold.T * 4;
+        if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, VEC, LAYER, 2, true, false>>(grid, threads, bytes, P, s);
+        return launch<block_norm_grad_kernel<DT, VEC, LAYER, 1, true, false>>(grid, threads, bytes, P, s);
+    }
+    if constexpr (VEC) {
+        if (c.hold.T > 32 && (P.pre || P.post) && P.chunk > 1) {
+            const int64_t bytes = pipe_bytes(P.dim, P.gate && P.gate_rows == 1 ? 5 : 4);
+            if constexpr (!LAYER)
+                if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, VEC, LAYER, 2, false, true>>(grid, threads, bytes, P, s);
+            return launch<block_norm_grad_kernel<DT, VEC, LAYER, 1, false, true>>(grid, threads, bytes, P, s);
+        }
+    }
+    if constexpr (!LAYER)
+        if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, VEC, LAYER, 2, false, false>>(grid, threads, 0, P, s);
+    return launch<block_norm_grad_kernel<DT, VEC, LAYER, 1, false, false>>(grid, threads, 0, P, s);
 }
 
 template <int DT>
-zero_status_t launch_backward(const NormParams& P, const Checked& C, bool bias, cudaStream_t s)
+zero_status_t launch_backward(NormParams& P, const Checked& C, cudaStream_t s)
 {
     const bool layer = C.a.kind == ZERO_NORM_LAYER;
-    if (C.vec) return layer ? launch_backward<DT, true, true>(P, C.cut, bias, s) : launch_backward<DT, true, false>(P, C.cut, bias, s);
-    return layer ? launch_backward<DT, false, true>(P, C.cut, bias, s) : launch_backward<DT, false, false>(P, C.cut, bias, s);
+    if (C.vec) return layer ? launch_backward<DT, true, true>(P, C.cut, s) : launch_backward<DT, true, false>(P, C.cut, s);
+    return layer ? launch_backward<DT, false, true>(P, C.cut, s) : launch_backward<DT, false, false>(P, C.cut, s);
 }
 
 template <int DT>
-void launch_forward(const NormParams& P, const Checked& C, cudaStream_t s)
+zero_status_t launch_forward(NormParams& P, const Checked& C, cudaStream_t s)
 {
     const bool layer = C.a.kind == ZERO_NORM_LAYER;
-    if (C.vec) layer ? launch_forward<DT, true, true>(P, s) : launch_forward<DT, true, false>(P, s);
-    else layer ? launch_forward<DT, false, true>(P, s) : launch_forward<DT, false, false>(P, s);
+    if (C.vec) return layer ? launch_forward<DT, true, true>(P, s) : launch_forward<DT, true, false>(P, s);
+    return layer ? launch_forward<DT, false, true>(P, s) : launch_forward<DT, false, false>(P, s);
 }
 
 }  // namespace
+
+cudaError_t take_norm_error(uint32_t* word, void* stream) { return take_error_word(g_norm_error, word, static_cast<cudaStream_t>(stream)); }
+
 }  // namespace zero
 
 using namespace zero;
@@ -674,13 +1043,13 @@ extern "C" {
 zero_status_t zero_block_norm(const zero_block_norm_t* args, void* stream)
 try {
     Checked C;
-    const zero_status_t st = check_norm(args, false, &C, "zero_block_norm");
+    zero_status_t st = check_norm(args, false, &C, "zero_block_norm");
     if (st != ZERO_OK) return st;
     if (C.a.rows == 0) return ZERO_OK;
-    const NormParams P = params_of(C, false);
+    NormParams P = params_of(C, false);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (C.a.dtype16 == ZERO_BF16) launch_forward<ZERO_BF16>(P, C, s);
-    else launch_forward<ZERO_FP16>(P, C, s);
+    st = C.a.dtype16 == ZERO_BF16 ? launch_forward<ZERO_BF16>(P, C, s) : launch_forward<ZERO_FP16>(P, C, s);
+    if (st != ZERO_OK) return st;
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_block_norm: launch");
 }
@@ -717,9 +1086,10 @@ try {
     P.chunk = C.cut.chunk;
     P.sums = C.sums_bytes ? static_cast<float*>(workspace) : nullptr;
     P.gate_sums = C.gate_bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + C.sums_bytes) : nullptr;
-    const bool bias = a.dpre_b || a.dpost_b, bf = a.dtype16 == ZERO_BF16;
+    P.bias_sums = a.dpre_b || a.dpost_b;
+    const bool bf = a.dtype16 == ZERO_BF16;
     if (a.rows > 0) {
-        st = bf ? launch_backward<ZERO_BF16>(P, C, bias, s) : launch_backward<ZERO_FP16>(P, C, bias, s);
+        st = bf ? launch_backward<ZERO_BF16>(P, C, s) : launch_backward<ZERO_FP16>(P, C, s);
         if (st != ZERO_OK) return st;
     }
     const bool weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b, gates = a.rows > 0 && C.gate_bytes > 0;
@@ -740,9 +1110,16 @@ try {
         S.workers = C.cut.workers;
         S.dim = (int32_t)a.dim;
         S.by_group = C.groups <= C.cut.workers;
-        const dim3 grid((unsigned)((a.dim + 31) / 32), (unsigned)(4 + (gates ? std::min(C.groups, C.cut.workers) : 0)));
-        if (bf) block_norm_sum_kernel<ZERO_BF16><<<grid, dim3(32, 32), 0, s>>>(S);
-        else block_norm_sum_kernel<ZERO_FP16><<<grid, dim3(32, 32), 0, s>>>(S);
+        const unsigned rows = (unsigned)(4 + (gates ? std::min(C.groups, C.cut.workers) : 0));
+        const int cols = a.dim % 4 == 0 ? 128 : 32;
+        const dim3 grid((unsigned)((a.dim + cols - 1) / cols), rows), threads(32, 8);
+        if (cols == 128) {
+            if (bf) block_norm_sum_kernel<ZERO_BF16, 4><<<grid, threads, 0, s>>>(S);
+            else block_norm_sum_kernel<ZERO_FP16, 4><<<grid, threads, 0, s>>>(S);
+        } else {
+            if (bf) block_norm_sum_kernel<ZERO_BF16, 1><<<grid, threads, 0, s>>>(S);
+            else block_norm_sum_kernel<ZERO_FP16, 1><<<grid, threads, 0, s>>>(S);
+        }
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_block_norm_backward: launch");
