@@ -24,8 +24,19 @@
 namespace zero {
 namespace {
 
+// A norm's weights.  Where there are none the pointer is to eight ones (or zeros) and the mask takes
+// every element to them: no branch, no selection.
+struct Weights {
+    const uint16_t* p;
+    uint32_t mask;
+};
+__device__ __align__(16) uint16_t g_no_weights[3][8] = {{0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80, 0x3F80},
+                                                        {0x3C00, 0x3C00, 0x3C00, 0x3C00, 0x3C00, 0x3C00, 0x3C00, 0x3C00},
+                                                        {0, 0, 0, 0, 0, 0, 0, 0}};   // ones in bf16, in fp16; zeros
+
 struct NormParams {
-    const uint16_t *h, *x, *gate, *post_w, *post_b, *pre_w, *pre_b, *dy, *dz;
+    const uint16_t *h, *x, *gate, *dy, *dz;
+    Weights post_w, post_b, pre_w, pre_b;
     const uint16_t* y_in;
     uint16_t *y, *z, *dx, *dh, *dgate;
     int64_t rows, ld_h, ld_x, ld_y, ld_z, ld_gate, ld_dy, ld_dz, ld_dx, ld_dh, ld_dgate;
@@ -34,23 +45,26 @@ struct NormParams {
     float* gate_sums;          // [worker][2][dim]: a gate group's part in the worker's first / last rows
     int64_t chunk;             // backward: consecutive rows a worker takes
     int32_t dim, post, pre;
-    int32_t ragged;            // some thread holds less than the others
     int32_t bias_sums;         // the biases' gradients are asked for
     float eps, scale, inv_dim;
 };
 
+// How rows are accessed: every row starts on 16 bytes and all threads hold as much (kEven), or some hold
+// less (kRagged); or elements come one by one (kScalar).
+enum { kEven = 0, kRagged = 1, kScalar = 2 };
+
 // Which elements of a row a thread holds: V times eight.  Where every row starts on 16 bytes eight
 // neighbours, else every T-th, so that a warp's accesses are to neighbouring elements either way.
-template <bool VEC, int V>
+template <int MODE, int V>
 struct Lane {
     int tid, T, n;             // n: elements held (VEC: eights)
     __device__ __forceinline__ Lane(int tid_, int T_, int dim) : tid(tid_), T(T_)
     {
-        if constexpr (VEC) n = tid * 8 < dim ? (dim - tid * 8 + 8 * T - 1) / (8 * T) : 0;
+        if constexpr (MODE == kEven) n = V;
+        else if constexpr (MODE == kRagged) n = tid * 8 < dim ? (dim - tid * 8 + 8 * T - 1) / (8 * T) : 0;
         else n = tid < dim ? (dim - tid + T - 1) / T : 0;
     }
-    __device__ __forceinline__ bool has(int k) const { return VEC ? (k >> 3) < n : k < n; }
-    __device__ __forceinline__ int at(int k) const { return VEC ? ((k >> 3) * T + tid) * 8 + (k & 7) : tid + k * T; }
+    __device__ __forceinline__ int at(int k) const { return MODE != kScalar ? ((k >> 3) * T + tid) * 8 + (k & 7) : tid + k * T; }
 };
 
 // V times eight 16-bit elements as loaded.
@@ -59,14 +73,16 @@ struct Raw {
     uint32_t w[4 * V];
 };
 
-template <bool VEC, int V>
-__device__ __forceinline__ Raw<V> load_raw(const uint16_t* p, const Lane<VEC, V>& L)
+template <int MODE, int V>
+__device__ __forceinline__ Raw<V> load_raw(const uint16_t* p, const Lane<MODE, V>& L)
 {
     Raw<V> r;
-    if constexpr (VEC) {
+    if constexpr (MODE != kScalar) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint4 q = v < L.n ? *reinterpret_cast<const uint4*>(p + (v * L.T + L.tid) * 8) : make_uint4(0u, 0u, 0u, 0u);
+            uint4 q;
+            if (MODE == kEven || v < L.n) q = *reinterpret_cast<const uint4*>(p + (v * L.T + L.tid) * 8);
+            else q = make_uint4(0u, 0u, 0u, 0u);
             r.w[4 * v] = q.x; r.w[4 * v + 1] = q.y; r.w[4 * v + 2] = q.z; r.w[4 * v + 3] = q.w;
         }
     } else {
@@ -87,20 +103,30 @@ __device__ __forceinline__ F2 widen(uint32_t w)
     return pair(a, b);
 }
 
-// An optional vector of weights: `other` where there is none.
-template <int DT, bool VEC, int V>
-__device__ __forceinline__ Raw<V> load_weight(const uint16_t* p, const Lane<VEC, V>& L, float other)
+template <int MODE, int V>
+__device__ __forceinline__ Raw<V> load_weight(const Weights& W, const Lane<MODE, V>& L)
 {
-    if (p) return load_raw<VEC, V>(p, L);
     Raw<V> r;
-    const uint32_t w = narrow2<DT>(other, other);
+    if constexpr (MODE != kScalar) {
 #pragma unroll
-    for (int k = 0; k < 4 * V; ++k) r.w[k] = w;
+        for (int v = 0; v < V; ++v) {
+            uint4 q;
+            if (MODE == kEven || v < L.n) q = __ldg(reinterpret_cast<const uint4*>(W.p + (((v * L.T + L.tid) * 8) & W.mask)));
+            else q = make_uint4(0u, 0u, 0u, 0u);
+            r.w[4 * v] = q.x; r.w[4 * v + 1] = q.y; r.w[4 * v + 2] = q.z; r.w[4 * v + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4 * V; ++k) {
+            const uint32_t lo = 2 * k < L.n ? W.p[L.at(2 * k) & W.mask] : 0u, hi = 2 * k + 1 < L.n ? W.p[L.at(2 * k + 1) & W.mask] : 0u;
+            r.w[k] = lo | (hi << 16);
+        }
+    }
     return r;
 }
 
-template <int DT, bool VEC, int V>
-__device__ __forceinline__ void store_row(uint16_t* p, const Lane<VEC, V>& L, const F2 (&x)[4 * V])
+template <int DT, int MODE, int V>
+__device__ __forceinline__ void store_row(uint16_t* p, const Lane<MODE, V>& L, const F2 (&x)[4 * V])
 {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -111,8 +137,8 @@ __device__ __forceinline__ void store_row(uint16_t* p, const Lane<VEC, V>& L, co
             split(x[4 * v + k], a, b);
             w[k] = narrow2<DT>(a, b);
         }
-        if constexpr (VEC) {
-            if (v < L.n) *reinterpret_cast<uint4*>(p + (v * L.T + L.tid) * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (MODE != kScalar) {
+            if (MODE == kEven || v < L.n) *reinterpret_cast<uint4*>(p + (v * L.T + L.tid) * 8) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -122,16 +148,16 @@ __device__ __forceinline__ void store_row(uint16_t* p, const Lane<VEC, V>& L, co
 }
 
 // A worker's fp32 sums: dim floats, not aligned beyond 4 bytes where dim is odd.
-template <bool VEC, int V>
-__device__ __forceinline__ void store_sums(float* p, const Lane<VEC, V>& L, const F2 (&x)[4 * V])
+template <int MODE, int V>
+__device__ __forceinline__ void store_sums(float* p, const Lane<MODE, V>& L, const F2 (&x)[4 * V])
 {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float t[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) split(x[4 * v + k], t[2 * k], t[2 * k + 1]);
-        if constexpr (VEC) {
-            if (v < L.n) {
+        if constexpr (MODE != kScalar) {
+            if (MODE == kEven || v < L.n) {
                 float4* q = reinterpret_cast<float4*>(p + (v * L.T + L.tid) * 8);
                 q[0] = make_float4(t[0], t[1], t[2], t[3]);
                 q[1] = make_float4(t[4], t[5], t[6], t[7]);
@@ -152,12 +178,12 @@ __device__ __forceinline__ float total(F2 x)
 }
 
 // What a thread does not hold becomes 0.
-template <bool VEC, int V>
-__device__ __forceinline__ void clear_rest(const Lane<VEC, V>& L, F2 (&x)[4 * V])
+template <int MODE, int V>
+__device__ __forceinline__ void clear_rest(const Lane<MODE, V>& L, F2 (&x)[4 * V])
 {
 #pragma unroll
     for (int k = 0; k < 4 * V; ++k) {
-        if constexpr (VEC) {
+        if constexpr (MODE != kScalar) {
             if ((k >> 2) >= L.n) x[k] = both(0.0f);
         } else {
             float a, b;
@@ -168,10 +194,10 @@ __device__ __forceinline__ void clear_rest(const Lane<VEC, V>& L, F2 (&x)[4 * V]
 }
 
 // One pair of them: 0 where the thread does not hold it.
-template <bool VEC, int V>
-__device__ __forceinline__ F2 held(const Lane<VEC, V>& L, int k, F2 x)
+template <int MODE, int V>
+__device__ __forceinline__ F2 held(const Lane<MODE, V>& L, int k, F2 x)
 {
-    if constexpr (VEC) {
+    if constexpr (MODE != kScalar) {
         return (k >> 2) < L.n ? x : both(0.0f);
     } else {
         float a, b;
@@ -183,44 +209,68 @@ __device__ __forceinline__ F2 held(const Lane<VEC, V>& L, int k, F2 x)
 // Sums of NV values over the T threads of a row, the same bits in every thread.  `turn` picks one
 // of two areas, so that one barrier a sum is enough.
 constexpr int kSumArea = 4 * 32;
+
+// Two values summed over lanes whose numbers differ in bit `o`: a in the lanes without it, b in the others.
+__device__ __forceinline__ float fold(float a, float b, int o, int lane)
+{
+    const bool up = lane & o;
+    const float keep = up ? b : a, give = up ? a : b;
+    return keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+}
+
 template <int NV>
 __device__ __forceinline__ void row_sum(float (&v)[NV], int T, float* area, int& turn)
 {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-    if (T <= 32) return;
-    float* s = area + turn * kSumArea;
-    turn ^= 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T >> 5;
-    if (lane == 0)
-#pragma unroll
-        for (int k = 0; k < NV; ++k) s[k * 32 + warp] = v[k];
-    __syncthreads();
-    if (warps == 2) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) v[k] = s[k * 32] + s[k * 32 + 1];
-    } else if (warps <= 4) {
+    const int lane = threadIdx.x & 31;
+    if (T <= 32) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            v[k] = (s[k * 32] + s[k * 32 + 1]) + (s[k * 32 + 2] + (warps == 4 ? s[k * 32 + 3] : 0.0f));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+        return;
+    }
+    // within the warp: lane l ends with value l % 4's sum (l % 2's of two, of one the sum itself)
+    float x;
+    if constexpr (NV == 1) {
+        x = v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+    } else if constexpr (NV == 2) {
+        x = fold(v[0], v[1], 1, lane);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
     } else {
+        x = fold(fold(v[0], v[1], 1, lane), fold(v[2], NV > 3 ? v[NV - 1] : 0.0f, 1, lane), 2, lane);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    float* s = area + turn * kSumArea;
+    turn ^= 1;
+    const int warp = threadIdx.x >> 5, warps = T >> 5;
+    if (lane < NV) s[lane * 32 + warp] = x;
+    __syncthreads();
+    if (warps <= 4) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            v[k] = lane < warps ? s[k * 32 + lane] : 0.0f;
-            if (warps > 16) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], 16);
-            if (warps > 8) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], 8);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-            v[k] = __shfl_sync(0xFFFFFFFFu, v[k], 0);
+            const float4 q = *reinterpret_cast<const float4*>(s + k * 32);
+            v[k] = q.x + q.y;
+            if (warps > 2) v[k] += q.z;
+            if (warps > 3) v[k] += q.w;
         }
+        return;
     }
+    // lane l: value l / 8, warps l % 8, and 8 and 16 and 24 on
+    const int k = lane >> 3;
+    x = 0.0f;
+    if (k < NV)
+        for (int w = lane & 7; w < warps; w += 8) x += s[k * 32 + w];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, x, i * 8);
 }
 
 // x centred (LAYER) in place, and 1 / sqrt(mean square + eps).
-template <bool LAYER, bool VEC, int V>
-__device__ __forceinline__ float centre(F2 (&x)[4 * V], const Lane<VEC, V>& L, const NormParams& P, int T, float* area, int& turn)
+template <bool LAYER, int MODE, int V>
+__device__ __forceinline__ float centre(F2 (&x)[4 * V], const Lane<MODE, V>& L, const NormParams& P, int T, float* area, int& turn)
 {
     float s[1];
     if constexpr (LAYER) {
@@ -232,7 +282,7 @@ __device__ __forceinline__ float centre(F2 (&x)[4 * V], const Lane<VEC, V>& L, c
         const F2 minus_mean = both(-s[0] * P.inv_dim);
 #pragma unroll
         for (int k = 0; k < 4 * V; ++k) x[k] = add(x[k], minus_mean);
-        if (P.ragged) clear_rest<VEC, V>(L, x);
+        if constexpr (MODE != kEven) clear_rest<MODE, V>(L, x);
     }
     F2 sum = mul(x[0], x[0]);
 #pragma unroll
@@ -262,18 +312,22 @@ struct GateRow {
 
 // ---------------------------------------------------------------- rows on their way
 //
-// Rows of two warps and more whose tensors start on 16 bytes come through shared memory: one thread
-// issues a bulk copy a tensor (TMA) for the row kStages - 1 ahead, all on one mbarrier of that row's
+// Even rows of two warps and more come through shared memory: one thread
+// issues a bulk copy a tensor (TMA) for the row STAGES - 1 ahead, all on one mbarrier of that row's
 // stage, and no thread's registers wait for memory.  A stage is free again once every thread has passed
-// the first sum of the next row.  Waits are bounded; one that runs out is reported
+// the first sum of the next row.  Measured on GB300: forward (16384 x 2048, LayerNorm) two stages 57 us,
+// three 55, registers instead 72; backward (16384 x 4096, RMS) two stages 194, three 230 (they leave
+// the weights little L1), registers instead 320.  Waits are bounded; one that runs out is reported
 // (zero_operators_check), is the last one that its thread makes, and leaves the control flow as it is.
-constexpr int kRowStages = 3;
+constexpr int kForwardStages = 3, kBackwardStages = 2;
 constexpr uint64_t kRowWaitNs = 1000000000ull;
 __device__ uint32_t g_norm_error;
 
+template <int STAGES>
 struct RowPipe {
     uint32_t bars, data, stage_bytes, row_bytes;
-    uint32_t issued = 0;       // thread 0: rows asked for
+    uint32_t slot = 0, phase = 0, at = 0;       // the current row's stage, its parity and place
+    uint32_t ask_slot = 0;                      // thread 0: the next row's to ask for
     bool dead = false;
 
     __device__ __forceinline__ void init(unsigned char* shared, int dim, int arrays)
@@ -282,17 +336,22 @@ struct RowPipe {
         data = bars + 64;
         row_bytes = 2 * dim;
         stage_bytes = arrays * row_bytes;
+        at = data;
         if (threadIdx.x == 0) {
-            for (int i = 0; i < kRowStages; ++i) mbar_init(bars + 8 * i, 1);
+            for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
+        // a tensor that is not there reads as zeros
+        for (uint32_t i = threadIdx.x * 16; i < STAGES * stage_bytes; i += blockDim.x * 16)
+            *reinterpret_cast<uint4*>(shared + 64 + i) = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
     }
     // thread 0: the next row's copies; `rows` holds the arrays' addresses of that row
     template <int N>
     __device__ __forceinline__ void issue(const uint16_t* const (&rows)[N])
     {
-        const uint32_t s = issued % kRowStages, bar = bars + 8 * s;
+        const uint32_t bar = bars + 8 * ask_slot, to = data + ask_slot * stage_bytes;
         uint32_t bytes = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) bytes += rows[i] ? row_bytes : 0u;
@@ -301,58 +360,70 @@ struct RowPipe {
         for (int i = 0; i < N; ++i)
             if (rows[i])
                 asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                 data + s * stage_bytes + i * row_bytes),
+                                 to + i * row_bytes),
                              "l"(rows[i]), "r"(row_bytes), "r"(bar)
                              : "memory");
-        ++issued;
+        ask_slot = ask_slot + 1 == STAGES ? 0 : ask_slot + 1;
     }
-    __device__ __forceinline__ void wait(uint32_t row)
+    __device__ __forceinline__ void wait()
     {
-        if (dead) return;
-        if (!mbar_wait(bars + 8 * (row % kRowStages), (row / kRowStages) & 1, kRowWaitNs)) {
+        if (!dead && !mbar_wait(bars + 8 * slot, phase, kRowWaitNs)) {
             atomicOr(&g_norm_error, 1u);
             dead = true;
         }
     }
-    // thread 0, at the end: no copy may outlive the block
-    __device__ __forceinline__ void drain(uint32_t done)
+    __device__ __forceinline__ void next()
     {
-        for (uint32_t r = done; r < issued; ++r) mbar_wait(bars + 8 * (r % kRowStages), (r / kRowStages) & 1, kRowWaitNs);
+        if (++slot == STAGES) {
+            slot = 0;
+            phase ^= 1u;
+            at = data;
+        } else {
+            at += stage_bytes;
+        }
+    }
+    // thread 0, after the last row: a wait that ran out has left copies behind, none may outlive the block
+    __device__ __forceinline__ void drain()
+    {
+        if (!dead) return;
+        for (uint32_t i = 0; i < STAGES; ++i) {
+            mbar_wait(bars + 8 * i, 0, kRowWaitNs);
+            mbar_wait(bars + 8 * i, 1, kRowWaitNs);
+        }
     }
     template <int V>
-    __device__ __forceinline__ Raw<V> get(uint32_t row, int array, const Lane<true, V>& L) const
+    __device__ __forceinline__ Raw<V> get(int array, const Lane<kEven, V>& L) const
     {
         Raw<V> r;
-        const uint32_t at = data + (row % kRowStages) * stage_bytes + array * row_bytes;
+        const uint32_t from = at + array * row_bytes + L.tid * 16;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (v < L.n)
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                             : "r"(at + (v * L.T + L.tid) * 16)
-                             : "memory");
+            uint4 q;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                         : "r"(from + v * L.T * 16)
+                         : "memory");
             r.w[4 * v] = q.x; r.w[4 * v + 1] = q.y; r.w[4 * v + 2] = q.z; r.w[4 * v + 3] = q.w;
         }
         return r;
     }
 };
 
-constexpr int pipe_bytes(int64_t dim, int arrays) { return 64 + kRowStages * arrays * 2 * (int)dim; }
+constexpr int pipe_bytes(int64_t dim, int arrays, int stages) { return 64 + stages * arrays * 2 * (int)dim; }
 
 // Forward: threads (T, rows a block); a block of more than one row has T = 32.
-template <int DT, bool VEC, bool LAYER, int V, bool STAGED>
+template <int DT, int MODE, bool LAYER, int V, bool STAGED>
 __global__ void __launch_bounds__(V == 4 ? 256 : 512) block_norm_kernel(const __grid_constant__ NormParams P)
 {
-    __shared__ float area[2 * kSumArea];
+    __shared__ __align__(16) float area[2 * kSumArea];
     extern __shared__ __align__(128) unsigned char stages[];
     const int T = blockDim.x;
-    const Lane<VEC, V> L(threadIdx.x, T, P.dim);
+    const Lane<MODE, V> L(threadIdx.x, T, P.dim);
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= P.rows) return;                    // whole blocks, or warps that sum by themselves
     int turn = 0;
-    RowPipe pipe;
+    RowPipe<kForwardStages> pipe;
     const bool own_gates = P.gate && P.gate_rows == 1;
     auto ask = [&](int64_t r) {
         const uint16_t* const rows[3] = {P.h + r * P.ld_h, P.x ? P.x + r * P.ld_x : nullptr, own_gates ? P.gate + r * P.ld_gate : nullptr};
@@ -361,46 +432,43 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 512) block_norm_kernel(const __
     if constexpr (STAGED) {
         pipe.init(stages, P.dim, own_gates ? 3 : 2);
         if (threadIdx.x == 0)
-            for (int k = 0; k < kRowStages && row + k * step < P.rows; ++k) ask(row + k * step);
+            for (int k = 0; k < kForwardStages && row + k * step < P.rows; ++k) ask(row + k * step);
     }
     GateRow at(P.gate ? row : 0, step, P.gate ? P.gate_rows : 1);
-    uint32_t n = 0;
-    for (; row < P.rows; row += step, ++n) {
+    bool first = true;
+    for (; row < P.rows; row += step) {
         F2 a[4 * V];
-        Raw<V> h, x = {};
+        Raw<V> h, x;
         if constexpr (STAGED) {
-            pipe.wait(n);
-            h = pipe.get<V>(n, 0, L);
+            pipe.wait();
+            h = pipe.get<V>(0, L);
         } else {
-            h = load_raw<VEC, V>(P.h + row * P.ld_h, L);
-            if (P.x) x = load_raw<VEC, V>(P.x + row * P.ld_x, L);
+            h = load_raw<MODE, V>(P.h + row * P.ld_h, L);
+            if (P.x) x = load_raw<MODE, V>(P.x + row * P.ld_x, L);
         }
 #pragma unroll
         for (int k = 0; k < 4 * V; ++k) a[k] = widen<DT>(h.w[k]);
         // every thread is past the first sum: the row before is done with, its stage is free
         auto refill = [&]() {
             if constexpr (STAGED) {
-                const int64_t r = row + (kRowStages - 1) * step;
-                if (threadIdx.x == 0 && n > 0 && r < P.rows) ask(r);
+                const int64_t r = row + (kForwardStages - 1) * step;
+                if (threadIdx.x == 0 && !first && r < P.rows) ask(r);
+                first = false;
             }
         };
         if (P.post) {
-            const F2 r = both(centre<LAYER, VEC, V>(a, L, P, T, area, turn));
+            // the weights are fetched before the sums that they wait for
+            const Raw<V> w = load_weight<MODE, V>(P.post_w, L), c = load_weight<MODE, V>(P.post_b, L);
+            const F2 r = both(centre<LAYER, MODE, V>(a, L, P, T, area, turn));
             refill();
-            const Raw<V> w = load_weight<DT, VEC, V>(P.post_w, L, 1.0f);
 #pragma unroll
-            for (int k = 0; k < 4 * V; ++k) a[k] = mul(mul(a[k], r), widen<DT>(w.w[k]));
-            if (P.post_b) {
-                const Raw<V> c = load_raw<VEC, V>(P.post_b, L);
-#pragma unroll
-                for (int k = 0; k < 4 * V; ++k) a[k] = add(a[k], widen<DT>(c.w[k]));
-            }
+            for (int k = 0; k < 4 * V; ++k) a[k] = fma(mul(a[k], r), widen<DT>(w.w[k]), widen<DT>(c.w[k]));
         }
         const F2 scale = both(P.scale);
         if (P.gate) {
             Raw<V> gate;
-            if constexpr (STAGED) gate = own_gates ? pipe.get<V>(n, 2, L) : load_raw<VEC, V>(P.gate + at.group * P.ld_gate, L);
-            else gate = load_raw<VEC, V>(P.gate + at.group * P.ld_gate, L);
+            if constexpr (STAGED) gate = own_gates ? pipe.get<V>(2, L) : load_raw<MODE, V>(P.gate + at.group * P.ld_gate, L);
+            else gate = load_raw<MODE, V>(P.gate + at.group * P.ld_gate, L);
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) a[k] = mul(a[k], mul(scale, widen<DT>(gate.w[k])));
             at.next();
@@ -408,24 +476,25 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 512) block_norm_kernel(const __
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) a[k] = mul(a[k], scale);
         }
-        if (P.x) {
-            if constexpr (STAGED) x = pipe.get<V>(n, 1, L);
+        if constexpr (STAGED) x = pipe.get<V>(1, L);
+        if (STAGED || P.x) {
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) a[k] = add(a[k], widen<DT>(x.w[k]));
         }
-        if (P.y) store_row<DT, VEC, V>(P.y + row * P.ld_y, L, a);
+        if (P.y) store_row<DT, MODE, V>(P.y + row * P.ld_y, L, a);
         if (P.pre) {
-            if (P.ragged) clear_rest<VEC, V>(L, a);
-            const F2 r = both(centre<LAYER, VEC, V>(a, L, P, T, area, turn));
+            if constexpr (MODE != kEven) clear_rest<MODE, V>(L, a);
+            const Raw<V> w = load_weight<MODE, V>(P.pre_w, L), c = load_weight<MODE, V>(P.pre_b, L);
+            const F2 r = both(centre<LAYER, MODE, V>(a, L, P, T, area, turn));
             if (!P.post) refill();
-            const Raw<V> w = load_weight<DT, VEC, V>(P.pre_w, L, 1.0f), c = load_weight<DT, VEC, V>(P.pre_b, L, 0.0f);
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) a[k] = fma(mul(a[k], r), widen<DT>(w.w[k]), widen<DT>(c.w[k]));
-            store_row<DT, VEC, V>(P.z + row * P.ld_z, L, a);
+            store_row<DT, MODE, V>(P.z + row * P.ld_z, L, a);
         }
+        if constexpr (STAGED) pipe.next();
     }
     if constexpr (STAGED)
-        if (threadIdx.x == 0) pipe.drain(n);
+        if (threadIdx.x == 0) pipe.drain();
 }
 
 // A worker's sums over its rows, by column: registers, or shared memory.
@@ -450,16 +519,16 @@ struct Acc {
 
 // The sums of the biases' gradients are kept where they may be asked for: with ZERO_NORM_LAYER, and
 // in the variant with shared memory.
-template <int DT, bool VEC, bool LAYER, int V, bool SHARED, bool STAGED>
+template <int DT, int MODE, bool LAYER, int V, bool SHARED, bool STAGED>
 __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHARED ? 2 : 1)
     block_norm_grad_kernel(const __grid_constant__ NormParams P)
 {
-    __shared__ float area[2 * kSumArea];
+    __shared__ __align__(16) float area[2 * kSumArea];
     extern __shared__ __align__(128) unsigned char stages[];
     constexpr bool BIAS = LAYER || SHARED;
     constexpr int NACC = BIAS ? 5 : 3;
     const int T = blockDim.x;
-    const Lane<VEC, V> L(threadIdx.x, T, P.dim);
+    const Lane<MODE, V> L(threadIdx.x, T, P.dim);
     const int64_t worker = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int64_t r0 = worker * P.chunk, r1 = min(P.rows, r0 + P.chunk);
     if (r0 >= r1) return;                         // whole blocks, or warps that sum by themselves
@@ -471,7 +540,7 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
 #pragma unroll
             for (int k = 3; k < 5; ++k) acc.clear(k);
     int turn = 0;
-    RowPipe pipe;
+    RowPipe<kBackwardStages> pipe;
     const bool own_gates = P.gate && P.gate_rows == 1;
     auto ask = [&](int64_t r) {
         const uint16_t* const rows[5] = {P.pre ? P.y_in + r * P.ld_y : nullptr, P.pre ? P.dz + r * P.ld_dz : nullptr,
@@ -482,26 +551,28 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
     if constexpr (STAGED) {
         pipe.init(stages, P.dim, own_gates ? 5 : 4);
         if (threadIdx.x == 0)
-            for (int k = 0; k < kRowStages && r0 + k < r1; ++k) ask(r0 + k);
+            for (int k = 0; k < kBackwardStages && r0 + k < r1; ++k) ask(r0 + k);
     }
     GateRow at(P.gate_rows ? r0 : 0, 1, P.gate_rows ? P.gate_rows : 1);
     int64_t group_first = r0;                     // the group's first row in the worker
     const F2 scale = both(P.scale);
-    for (int64_t row = r0; row < r1; ++row) {
-        const uint32_t n = (uint32_t)(row - r0);
+    auto next_row = [&]() {
+        if constexpr (STAGED) pipe.next();
+    };
+    for (int64_t row = r0; row < r1; ++row, next_row()) {
         Raw<V> hr = {}, yr = {}, zr = {}, dr = {};
         if constexpr (STAGED) {
-            pipe.wait(n);
+            pipe.wait();
         } else {
             if (P.pre) {
-                yr = load_raw<VEC, V>(P.y_in + row * P.ld_y, L);
-                zr = load_raw<VEC, V>(P.dz + row * P.ld_dz, L);
+                yr = load_raw<MODE, V>(P.y_in + row * P.ld_y, L);
+                zr = load_raw<MODE, V>(P.dz + row * P.ld_dz, L);
             }
-            if (P.h) hr = load_raw<VEC, V>(P.h + row * P.ld_h, L);
-            if (P.dy) dr = load_raw<VEC, V>(P.dy + row * P.ld_dy, L);
+            if (P.h) hr = load_raw<MODE, V>(P.h + row * P.ld_h, L);
+            if (P.dy) dr = load_raw<MODE, V>(P.dy + row * P.ld_dy, L);
         }
-        auto fetch = [&](int which, const Raw<V>& kept, bool there) {
-            if constexpr (STAGED) return there ? pipe.get<V>(n, which, L) : Raw<V>{};
+        auto fetch = [&](int which, const Raw<V>& kept) {
+            if constexpr (STAGED) return pipe.get<V>(which, L);
             else return kept;
         };
         // minus the means of y and h
@@ -509,10 +580,10 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
         auto refill = [&]() {
             // every thread is past the first sum: the row before is done with, its stage is free
             if constexpr (STAGED)
-                if (threadIdx.x == 0 && n > 0 && row + kRowStages - 1 < r1) ask(row + kRowStages - 1);
+                if (threadIdx.x == 0 && row > r0 && row + kBackwardStages - 1 < r1) ask(row + kBackwardStages - 1);
         };
         if constexpr (LAYER) {
-            const Raw<V> h = fetch(2, hr, P.h != nullptr), y = fetch(0, yr, P.pre);
+            const Raw<V> h = fetch(2, hr), y = fetch(0, yr);
             F2 sa = both(0.0f), sb = sa;
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) {
@@ -529,7 +600,7 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
             const F2 x = widen<DT>(w);
             if constexpr (LAYER) {
                 const F2 c = add(x, minus_mean);
-                return P.ragged ? held<VEC, V>(L, k, c) : c;
+                return MODE != kEven ? held<MODE, V>(L, k, c) : c;
             } else {
                 return x;
             }
@@ -539,8 +610,8 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
         {
             float s[4];
             {
-                const Raw<V> h = fetch(2, hr, P.h != nullptr), y = fetch(0, yr, P.pre), z = fetch(1, zr, P.pre);
-                const Raw<V> w = load_weight<DT, VEC, V>(P.pre_w, L, 1.0f);
+                const Raw<V> h = fetch(2, hr), y = fetch(0, yr), z = fetch(1, zr);
+                const Raw<V> w = load_weight<MODE, V>(P.pre_w, L);
                 F2 s0 = both(0.0f), s1 = s0, s2 = s0, s3 = s0;
 #pragma unroll
                 for (int k = 0; k < 4 * V; ++k) {
@@ -566,13 +637,13 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
                 s[2] = t[2];
             }
             if (P.post) rh = rsqrtf(s[0] * P.inv_dim + P.eps);
-            const Raw<V> e = fetch(3, dr, P.dy != nullptr);
+            const Raw<V> e = fetch(3, dr);
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) d[k] = widen<DT>(e.w[k]);
             if (P.pre) {
                 const float ry = rsqrtf(s[1] * P.inv_dim + P.eps);
                 const F2 r = both(ry), along = both(-s[2] * P.inv_dim * ry * ry), mean = both(LAYER ? -s[3] * P.inv_dim : 0.0f);
-                const Raw<V> y = fetch(0, yr, true), z = fetch(1, zr, true), w = load_weight<DT, VEC, V>(P.pre_w, L, 1.0f);
+                const Raw<V> y = fetch(0, yr), z = fetch(1, zr), w = load_weight<MODE, V>(P.pre_w, L);
 #pragma unroll
                 for (int k = 0; k < 4 * V; ++k) {
                     const F2 b = centred(y.w[k], mb, k), c = widen<DT>(z.w[k]);
@@ -585,44 +656,37 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
                 }
             }
         }
-        if (P.dx) store_row<DT, VEC, V>(P.dx + row * P.ld_dx, L, d);
+        if (P.dx) store_row<DT, MODE, V>(P.dx + row * P.ld_dx, L, d);
         const int64_t group = at.group;
         const bool group_ends = row + 1 == r1 || (P.gate_rows && at.rest + 1 == P.gate_rows);
         at.next();
         if (!P.dh && !P.sums && !P.dgate) continue;
-        // through the gate: a is the normalised h, d becomes du
-        F2 a[4 * V];
-        {
-            const Raw<V> h = fetch(2, hr, P.h != nullptr);
-            const F2 r = both(rh);
-#pragma unroll
-            for (int k = 0; k < 4 * V; ++k) a[k] = mul(centred(h.w[k], ma, k), r);
-        }
+        // through the gate: a is the normalised h (formed anew where it is used, registers are few), d
+        // becomes du
+        const F2 r_h = both(rh);
+        auto normal_h = [&](const Raw<V>& h, int k) { return mul(centred(h.w[k], ma, k), r_h); };
         if (P.dgate) {
-            F2 u[4 * V];
-#pragma unroll
-            for (int k = 0; k < 4 * V; ++k) u[k] = a[k];
-            if (P.post) {
-                const Raw<V> w = load_weight<DT, VEC, V>(P.post_w, L, 1.0f), e = load_weight<DT, VEC, V>(P.post_b, L, 0.0f);
-#pragma unroll
-                for (int k = 0; k < 4 * V; ++k) u[k] = fma(a[k], widen<DT>(w.w[k]), widen<DT>(e.w[k]));
-            }
+            const Raw<V> h = fetch(2, hr), w = load_weight<MODE, V>(P.post_w, L), e = load_weight<MODE, V>(P.post_b, L);
             if (P.gate_rows == 1) {
+                F2 u[4 * V];
 #pragma unroll
-                for (int k = 0; k < 4 * V; ++k) u[k] = mul(mul(scale, d[k]), u[k]);
-                store_row<DT, VEC, V>(P.dgate + row * P.ld_dgate, L, u);
+                for (int k = 0; k < 4 * V; ++k)
+                    u[k] = mul(mul(scale, d[k]), fma(normal_h(h, k), widen<DT>(w.w[k]), widen<DT>(e.w[k])));
+                store_row<DT, MODE, V>(P.dgate + row * P.ld_dgate, L, u);
             } else {
 #pragma unroll
-                for (int k = 0; k < 4 * V; ++k) acc.at(kGate, k) = fma(mul(scale, d[k]), u[k], acc.at(kGate, k));
+                for (int k = 0; k < 4 * V; ++k)
+                    acc.at(kGate, k) = fma(mul(scale, d[k]), fma(normal_h(h, k), widen<DT>(w.w[k]), widen<DT>(e.w[k])), acc.at(kGate, k));
                 if (group_ends) {
                     // whole groups are final; else a part of one, in the worker's first or last slot
                     const int64_t first = group * P.gate_rows, last = min(P.rows, first + P.gate_rows) - 1;
+                    F2 u[4 * V];
 #pragma unroll
                     for (int k = 0; k < 4 * V; ++k) u[k] = acc.at(kGate, k);
                     if (first >= r0 && last < r1) {
-                        store_row<DT, VEC, V>(P.dgate + group * P.ld_dgate, L, u);
+                        store_row<DT, MODE, V>(P.dgate + group * P.ld_dgate, L, u);
                     } else {
-                        store_sums<VEC, V>(P.gate_sums + (worker * 2 + (group_first == r0 ? 0 : 1)) * P.dim, L, u);
+                        store_sums<MODE, V>(P.gate_sums + (worker * 2 + (group_first == r0 ? 0 : 1)) * P.dim, L, u);
                     }
                     acc.clear(kGate);
                     group_first = row + 1;
@@ -632,8 +696,8 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
         if (!P.dh && !P.sums) continue;
         if (P.gate) {
             Raw<V> gate;
-            if constexpr (STAGED) gate = own_gates ? pipe.get<V>(n, 4, L) : load_raw<VEC, V>(P.gate + group * P.ld_gate, L);
-            else gate = load_raw<VEC, V>(P.gate + group * P.ld_gate, L);
+            if constexpr (STAGED) gate = own_gates ? pipe.get<V>(4, L) : load_raw<MODE, V>(P.gate + group * P.ld_gate, L);
+            else gate = load_raw<MODE, V>(P.gate + group * P.ld_gate, L);
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) d[k] = mul(d[k], mul(scale, widen<DT>(gate.w[k])));
         } else {
@@ -641,17 +705,20 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
             for (int k = 0; k < 4 * V; ++k) d[k] = mul(d[k], scale);
         }
         if (P.post) {
-            const Raw<V> w = load_weight<DT, VEC, V>(P.post_w, L, 1.0f);
             F2 s0 = both(0.0f), s1 = s0;
+            {
+                const Raw<V> h = fetch(2, hr), w = load_weight<MODE, V>(P.post_w, L);
 #pragma unroll
-            for (int k = 0; k < 4 * V; ++k) {
-                acc.at(kPostW, k) = fma(d[k], a[k], acc.at(kPostW, k));
-                if constexpr (BIAS)
-                    if (!SHARED || P.bias_sums) acc.at(kPostB, k) = add(acc.at(kPostB, k), d[k]);
-                d[k] = mul(d[k], widen<DT>(w.w[k]));
-                if (P.ragged) d[k] = held<VEC, V>(L, k, d[k]);
-                s0 = fma(d[k], a[k], s0);
-                if (LAYER) s1 = add(s1, d[k]);
+                for (int k = 0; k < 4 * V; ++k) {
+                    const F2 a = normal_h(h, k);
+                    acc.at(kPostW, k) = fma(d[k], a, acc.at(kPostW, k));
+                    if constexpr (BIAS)
+                        if (!SHARED || P.bias_sums) acc.at(kPostB, k) = add(acc.at(kPostB, k), d[k]);
+                    d[k] = mul(d[k], widen<DT>(w.w[k]));
+                    if constexpr (MODE != kEven) d[k] = held<MODE, V>(L, k, d[k]);
+                    s0 = fma(d[k], a, s0);
+                    if (LAYER) s1 = add(s1, d[k]);
+                }
             }
             float t[2] = {total(s0), total(s1)};
             if constexpr (LAYER) {
@@ -661,15 +728,16 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
                 row_sum(one, T, area, turn);
                 t[0] = one[0];
             }
-            const F2 along = both(-t[0] * P.inv_dim * rh), mean = both(LAYER ? -t[1] * P.inv_dim * rh : 0.0f), r = both(rh);
+            const F2 along = both(-t[0] * P.inv_dim * rh), mean = both(LAYER ? -t[1] * P.inv_dim * rh : 0.0f);
+            const Raw<V> h = fetch(2, hr);
 #pragma unroll
             for (int k = 0; k < 4 * V; ++k) {
-                F2 g = mul(a[k], along);
+                F2 g = mul(normal_h(h, k), along);
                 if (LAYER) g = add(g, mean);
-                d[k] = fma(r, d[k], g);
+                d[k] = fma(r_h, d[k], g);
             }
         }
-        if (P.dh) store_row<DT, VEC, V>(P.dh + row * P.ld_dh, L, d);
+        if (P.dh) store_row<DT, MODE, V>(P.dh + row * P.ld_dh, L, d);
     }
     if (P.sums) {
         float* q = P.sums + worker * 4 * P.dim;
@@ -677,7 +745,7 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
         auto put = [&](int k, int row) {
 #pragma unroll
             for (int j = 0; j < 4 * V; ++j) t[j] = acc.at(k, j);
-            store_sums<VEC, V>(q + row * P.dim, L, t);
+            store_sums<MODE, V>(q + row * P.dim, L, t);
         };
         put(kPreW, 0);
         put(kPostW, 2);
@@ -688,7 +756,7 @@ __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHAR
             }
     }
     if constexpr (STAGED)
-        if (threadIdx.x == 0) pipe.drain((uint32_t)(r1 - r0));
+        if (threadIdx.x == 0) pipe.drain();
 }
 
 struct SumParams {
@@ -763,6 +831,8 @@ __global__ void __launch_bounds__(256) block_norm_sum_kernel(const __grid_consta
 // ------------------------------------------------------------------ host
 
 constexpr int kSms = 152;
+constexpr int kForwardMost = 4;
+constexpr int kForwardThreads = 1024;             // an SM's, of the staged forward kernel
 
 // How a row is held: V eights a thread in T threads.  The sums over a row cost the same instructions
 // whatever a thread holds, so more elements a thread are better while registers last: 32 forward (16
@@ -891,6 +961,19 @@ zero_status_t check_norm(const zero_block_norm_t* in, bool back, Checked* C, con
     return ZERO_OK;
 }
 
+// The address of g_no_weights on the current device.
+const uint16_t* no_weights()
+{
+    static std::mutex mu;
+    static const void* cache[64] = {nullptr};
+    int dev = 0;
+    void* p = nullptr;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cache[dev] && cudaGetSymbolAddress(&p, g_no_weights) == cudaSuccess) cache[dev] = p;
+    return static_cast<const uint16_t*>(cache[dev]);
+}
+
 NormParams params_of(const Checked& C, bool back)
 {
     const zero_block_norm_t& a = C.a;
@@ -902,14 +985,13 @@ NormParams params_of(const Checked& C, bool back)
     P.pre = (a.norms & ZERO_NORM_PRE) != 0;
     P.h = in(a.h);
     P.gate = in(a.gate);
-    if (P.post) {
-        P.post_w = in(a.post_w);
-        P.post_b = in(a.post_b);
-    }
-    if (P.pre) {
-        P.pre_w = in(a.pre_w);
-        P.pre_b = in(a.pre_b);
-    }
+    const uint16_t* none = no_weights();
+    auto weights = [&](const void* p, int which) { return p ? Weights{in(p), 0xFFFFFFFFu} : Weights{none + 8 * which, 0u}; };
+    const int ones = a.dtype16 == ZERO_BF16 ? 0 : 1;
+    P.post_w = weights(P.post ? a.post_w : nullptr, ones);
+    P.post_b = weights(P.post ? a.post_b : nullptr, 2);
+    P.pre_w = weights(P.pre ? a.pre_w : nullptr, ones);
+    P.pre_b = weights(P.pre ? a.pre_b : nullptr, 2);
     if (back) {
         P.y_in = in(a.y);
         P.dy = in(a.dy);
@@ -947,87 +1029,77 @@ constexpr int kMostShared = 227 * 1024 - 1024;   // beside the kernels' static s
 
 // Dynamic shared memory beyond 48 KB has to be allowed once a kernel.
 template <auto KERNEL>
-zero_status_t allow_shared()
-{
-    static const cudaError_t set = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
-    return set == cudaSuccess ? ZERO_OK : cuda_fail(set, "zero_block_norm: shared memory");
-}
-
-template <auto KERNEL>
 zero_status_t launch(unsigned grid, dim3 threads, int64_t bytes, const NormParams& P, cudaStream_t s)
 {
     if (bytes > 48 * 1024) {
-        const zero_status_t st = allow_shared<KERNEL>();
-        if (st != ZERO_OK) return st;
+        static const cudaError_t set = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+        if (set != cudaSuccess) return cuda_fail(set, "zero_block_norm: shared memory");
     }
     KERNEL<<<grid, threads, (size_t)bytes, s>>>(P);
     return ZERO_OK;
 }
 
-template <int DT, bool VEC, bool LAYER>
-zero_status_t launch_forward(NormParams& P, cudaStream_t s)
+template <int DT, int MODE, bool LAYER>
+zero_status_t launch_forward(const NormParams& P, const Hold& h, cudaStream_t s)
 {
-    const Hold h = hold_row(P.dim, VEC ? 4 : 2);
-    P.ragged = !h.even;
     const int per_block = h.T == 32 ? 8 : 1;
     const int64_t blocks = (P.rows + per_block - 1) / per_block;
     const dim3 threads(h.T, per_block);
-    if constexpr (VEC) {
-        // a row of its own a block, and more rows than the GPU holds at once: through shared memory
-        const int64_t bytes = pipe_bytes(P.dim, P.gate && P.gate_rows == 1 ? 3 : 2);
+    if constexpr (MODE == kEven) {
+        // a row of its own a block, and more rows than the GPU takes at once: through shared memory
+        const int64_t bytes = pipe_bytes(P.dim, P.gate && P.gate_rows == 1 ? 3 : 2, kForwardStages);
         if (h.T > 32 && (P.pre || P.post) && P.rows > 4 * kSms) {
-            const int64_t fit = std::min<int64_t>(kMostShared / (bytes + 2048), 2048 / (4 * h.T) * 3);
+            const int64_t fit = std::min<int64_t>(kMostShared / (bytes + 2048), kForwardThreads / h.T);
             const unsigned grid = (unsigned)std::min<int64_t>(blocks, kSms * std::max<int64_t>(1, fit));
-            if (h.V == 4) return launch<block_norm_kernel<DT, VEC, LAYER, 4, true>>(grid, threads, bytes, P, s);
-            if (h.V == 2) return launch<block_norm_kernel<DT, VEC, LAYER, 2, true>>(grid, threads, bytes, P, s);
-            return launch<block_norm_kernel<DT, VEC, LAYER, 1, true>>(grid, threads, bytes, P, s);
+            if (h.V == 4) return launch<block_norm_kernel<DT, MODE, LAYER, 4, true>>(grid, threads, bytes, P, s);
+            if (h.V == 2) return launch<block_norm_kernel<DT, MODE, LAYER, 2, true>>(grid, threads, bytes, P, s);
+            return launch<block_norm_kernel<DT, MODE, LAYER, 1, true>>(grid, threads, bytes, P, s);
         }
     }
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)kSms * std::max(1, 768 / (h.T * per_block)));
-    if constexpr (VEC)
-        if (h.V == 4) return launch<block_norm_kernel<DT, VEC, LAYER, 4, false>>(grid, threads, 0, P, s);
-    if (h.V == 2) return launch<block_norm_kernel<DT, VEC, LAYER, 2, false>>(grid, threads, 0, P, s);
-    return launch<block_norm_kernel<DT, VEC, LAYER, 1, false>>(grid, threads, 0, P, s);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)kSms * std::max(1, 1024 / (h.T * per_block)));
+    if constexpr (MODE != kScalar)
+        if (h.V == 4) return launch<block_norm_kernel<DT, MODE, LAYER, 4, false>>(grid, threads, 0, P, s);
+    if (h.V == 2) return launch<block_norm_kernel<DT, MODE, LAYER, 2, false>>(grid, threads, 0, P, s);
+    return launch<block_norm_kernel<DT, MODE, LAYER, 1, false>>(grid, threads, 0, P, s);
 }
 
-template <int DT, bool VEC, bool LAYER>
-zero_status_t launch_backward(NormParams& P, const Cut& c, cudaStream_t s)
+template <int DT, int MODE, bool LAYER>
+zero_status_t launch_backward(const NormParams& P, const Cut& c, cudaStream_t s)
 {
     const dim3 threads(c.hold.T, c.per_block);
     const unsigned grid = (unsigned)((c.workers + c.per_block - 1) / c.per_block);
-    P.ragged = !c.hold.even;
     if (c.shared) {
         const int64_t bytes = (int64_t)(P.bias_sums ? 5 : 3) * 8 * c.hold.V * c.hold.T * 4;
-        if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, VEC, LAYER, 2, true, false>>(grid, threads, bytes, P, s);
-        return launch<block_norm_grad_kernel<DT, VEC, LAYER, 1, true, false>>(grid, threads, bytes, P, s);
+        if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, MODE, LAYER, 2, true, false>>(grid, threads, bytes, P, s);
+        return launch<block_norm_grad_kernel<DT, MODE, LAYER, 1, true, false>>(grid, threads, bytes, P, s);
     }
-    if constexpr (VEC) {
+    if constexpr (MODE == kEven) {
         if (c.hold.T > 32 && (P.pre || P.post) && P.chunk > 1) {
-            const int64_t bytes = pipe_bytes(P.dim, P.gate && P.gate_rows == 1 ? 5 : 4);
+            const int64_t bytes = pipe_bytes(P.dim, P.gate && P.gate_rows == 1 ? 5 : 4, kBackwardStages);
             if constexpr (!LAYER)
-                if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, VEC, LAYER, 2, false, true>>(grid, threads, bytes, P, s);
-            return launch<block_norm_grad_kernel<DT, VEC, LAYER, 1, false, true>>(grid, threads, bytes, P, s);
+                if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, MODE, LAYER, 2, false, true>>(grid, threads, bytes, P, s);
+            return launch<block_norm_grad_kernel<DT, MODE, LAYER, 1, false, true>>(grid, threads, bytes, P, s);
         }
     }
     if constexpr (!LAYER)
-        if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, VEC, LAYER, 2, false, false>>(grid, threads, 0, P, s);
-    return launch<block_norm_grad_kernel<DT, VEC, LAYER, 1, false, false>>(grid, threads, 0, P, s);
+        if (c.hold.V == 2) return launch<block_norm_grad_kernel<DT, MODE, LAYER, 2, false, false>>(grid, threads, 0, P, s);
+    return launch<block_norm_grad_kernel<DT, MODE, LAYER, 1, false, false>>(grid, threads, 0, P, s);
+}
+
+template <int DT, int MODE>
+zero_status_t launch_norm(const NormParams& P, const Checked& C, bool back, const Hold& h, cudaStream_t s)
+{
+    if (C.a.kind == ZERO_NORM_LAYER)
+        return back ? launch_backward<DT, MODE, true>(P, C.cut, s) : launch_forward<DT, MODE, true>(P, h, s);
+    return back ? launch_backward<DT, MODE, false>(P, C.cut, s) : launch_forward<DT, MODE, false>(P, h, s);
 }
 
 template <int DT>
-zero_status_t launch_backward(NormParams& P, const Checked& C, cudaStream_t s)
+zero_status_t launch_norm(const NormParams& P, const Checked& C, bool back, cudaStream_t s)
 {
-    const bool layer = C.a.kind == ZERO_NORM_LAYER;
-    if (C.vec) return layer ? launch_backward<DT, true, true>(P, C.cut, s) : launch_backward<DT, true, false>(P, C.cut, s);
-    return layer ? launch_backward<DT, false, true>(P, C.cut, s) : launch_backward<DT, false, false>(P, C.cut, s);
-}
-
-template <int DT>
-zero_status_t launch_forward(NormParams& P, const Checked& C, cudaStream_t s)
-{
-    const bool layer = C.a.kind == ZERO_NORM_LAYER;
-    if (C.vec) return layer ? launch_forward<DT, true, true>(P, s) : launch_forward<DT, true, false>(P, s);
-    return layer ? launch_forward<DT, false, true>(P, s) : launch_forward<DT, false, false>(P, s);
+    const Hold h = back ? C.cut.hold : hold_row(P.dim, C.vec ? kForwardMost : 2);
+    if (!C.vec) return launch_norm<DT, kScalar>(P, C, back, h, s);
+    return h.even ? launch_norm<DT, kEven>(P, C, back, h, s) : launch_norm<DT, kRagged>(P, C, back, h, s);
 }
 
 }  // namespace
@@ -1046,9 +1118,10 @@ try {
     zero_status_t st = check_norm(args, false, &C, "zero_block_norm");
     if (st != ZERO_OK) return st;
     if (C.a.rows == 0) return ZERO_OK;
-    NormParams P = params_of(C, false);
+    const NormParams P = params_of(C, false);
+    if (!P.post_w.p) return fail(ZERO_ECUDA, "zero_block_norm: no device");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = C.a.dtype16 == ZERO_BF16 ? launch_forward<ZERO_BF16>(P, C, s) : launch_forward<ZERO_FP16>(P, C, s);
+    st = C.a.dtype16 == ZERO_BF16 ? launch_norm<ZERO_BF16>(P, C, false, s) : launch_norm<ZERO_FP16>(P, C, false, s);
     if (st != ZERO_OK) return st;
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_block_norm: launch");
@@ -1089,7 +1162,8 @@ try {
     P.bias_sums = a.dpre_b || a.dpost_b;
     const bool bf = a.dtype16 == ZERO_BF16;
     if (a.rows > 0) {
-        st = bf ? launch_backward<ZERO_BF16>(P, C, s) : launch_backward<ZERO_FP16>(P, C, s);
+        if (!P.post_w.p) return fail(ZERO_ECUDA, "zero_block_norm_backward: no device");
+        st = bf ? launch_norm<ZERO_BF16>(P, C, true, s) : launch_norm<ZERO_FP16>(P, C, true, s);
         if (st != ZERO_OK) return st;
     }
     const bool weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b, gates = a.rows > 0 && C.gate_bytes > 0;
