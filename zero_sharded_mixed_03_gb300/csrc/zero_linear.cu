@@ -49,12 +49,14 @@ struct Epilogue {
 struct GemmParams {
     CUtensorMap a, b;
     Epilogue epi;
-    float* partial;              // [split][M][ld_partial], when the inner dimension is split
-    int64_t ld_partial;
+    float* partial;              // [split][tail tile][rows][BN] sums of the tiles that are split
     int32_t M, N, k_blocks;
-    int32_t splits, k_per_split; // k_blocks of one split (the last may have fewer)
+    int32_t full;                // tiles done whole; the tail after them is split along K
+    int32_t splits, k_per_split; // k_blocks of one part (the last may have fewer)
     int32_t tiles_m, tiles_n;
+    int32_t a_rows;              // rows of A a copy brings (kBM, or fewer where A has no more)
     int32_t a_mn, b_mn;          // operand stored along its own rows (M or N) instead of along K
+    int32_t rows_vec;            // the outputs and the residual allow 16-byte accesses
     uint32_t idesc;
 };
 
@@ -96,6 +98,31 @@ __device__ __forceinline__ float act_slope(float z, int act)
     }
 }
 
+// Eight at a time: one branch for all.
+__device__ __forceinline__ void act_values(float (&z)[8], int act)
+{
+#define ZERO_EACH(A) case A: _Pragma("unroll") for (int j = 0; j < 8; ++j) z[j] = act_value(z[j], A); break
+    switch (act) {
+        ZERO_EACH(ZERO_ACT_RELU);
+        ZERO_EACH(ZERO_ACT_GELU_TANH);
+        ZERO_EACH(ZERO_ACT_GELU);
+        ZERO_EACH(ZERO_ACT_SILU);
+    }
+#undef ZERO_EACH
+}
+
+__device__ __forceinline__ void act_slopes(float (&z)[8], int act)
+{
+#define ZERO_EACH(A) case A: _Pragma("unroll") for (int j = 0; j < 8; ++j) z[j] = act_slope(z[j], A); break
+    switch (act) {
+        ZERO_EACH(ZERO_ACT_RELU);
+        ZERO_EACH(ZERO_ACT_GELU_TANH);
+        ZERO_EACH(ZERO_ACT_GELU);
+        ZERO_EACH(ZERO_ACT_SILU);
+    }
+#undef ZERO_EACH
+}
+
 // ------------------------------------------------------------------ eight columns of one row
 
 template <int DT>
@@ -134,10 +161,7 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t row, int64_t 
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] += bias[j];
     if (E.pre) store8<DT>(E.pre + row * E.ld_pre + col, E.vec & kVecPre, n, z);
-    if (E.act != ZERO_ACT_NONE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = act_value(z[j], E.act);
-    }
+    if (E.act != ZERO_ACT_NONE) act_values(z, E.act);
     if (E.residual) {
         float r[8];
         load8<DT>(E.residual + row * E.ld_res + col, E.vec & kVecRes, n, r);
@@ -145,6 +169,17 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t row, int64_t 
         for (int j = 0; j < 8; ++j) z[j] += r[j];
     }
     store8<DT>(E.out + row * E.ld_out + col, E.vec & kVecOut, n, z);
+}
+
+// One element.
+template <int DT>
+__device__ __forceinline__ void finish1(const Epilogue& E, int64_t row, int64_t col, float z)
+{
+    if (E.bias) z += widen1<DT>(E.bias[col]);
+    if (E.pre) E.pre[row * E.ld_pre + col] = narrow1<DT>(z);
+    z = act_value(z, E.act);
+    if (E.residual) z += widen1<DT>(E.residual[row * E.ld_res + col]);
+    E.out[row * E.ld_out + col] = narrow1<DT>(z);
 }
 
 template <int DT>
@@ -261,13 +296,35 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn)
 
 // Tile (m, n) of item `t`: groups of 8 tile rows are walked column by column, so that what runs
 // at one time shares its operands in L2.
-__device__ __forceinline__ void tile_at(const GemmParams& P, int t, int& m, int& n)
+__device__ __forceinline__ void tile_at(int tiles_m, int tiles_n, int t, int& m, int& n)
 {
     constexpr int kGroup = 8;
-    const int per_group = kGroup * P.tiles_n, g = t / per_group, in = t - g * per_group;
-    const int rows = min(kGroup, P.tiles_m - g * kGroup);
+    const int per_group = kGroup * tiles_n, g = t / per_group, in = t - g * per_group;
+    const int rows = min(kGroup, tiles_m - g * kGroup);
     n = in / rows;
     m = g * kGroup + (in - n * rows);
+}
+
+// Work item `item`: a tile and its inner blocks [kb0, kb1); part >= 0: its place among the partial sums.
+struct Item {
+    int m, n, kb0, kb1, part;
+};
+
+__device__ __forceinline__ Item item_at(const GemmParams& P, int item)
+{
+    Item I;
+    const int tail = P.tiles_m * P.tiles_n - P.full;
+    int tile = item, split = 0;
+    I.part = -1;
+    if (item >= P.full && P.splits > 1) {
+        I.part = item - P.full;
+        split = I.part / tail;
+        tile = P.full + I.part - split * tail;
+    }
+    tile_at(P.tiles_m, P.tiles_n, tile, I.m, I.n);
+    I.kb0 = I.part >= 0 ? split * P.k_per_split : 0;
+    I.kb1 = I.part >= 0 ? min(P.k_blocks, I.kb0 + P.k_per_split) : P.k_blocks;
+    return I;
 }
 
 template <int CG, int BN>
@@ -297,7 +354,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
                    acc_empty0 = acc_full0 + 16, tmem_slot = acc_empty0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int n_items = P.tiles_m * P.tiles_n * P.splits;
+    const int n_items = P.full + (P.tiles_m * P.tiles_n - P.full) * P.splits;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp == 0 && lane == 0) {
@@ -335,12 +392,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (lane == 0) {
             uint32_t k = 0;
             for (int item = first; item < n_items && ok; item += step) {
-                const int split = item % P.splits;
-                int m, n;
-                tile_at(P, item / P.splits, m, n);
-                const int row_a = (m * CG + (int)rank) * kBM, row_b = n * BN + (int)rank * S::kBRows;
-                const int kb0 = split * P.k_per_split, kb1 = min(P.k_blocks, kb0 + P.k_per_split);
-                for (int kb = kb0; kb < kb1; ++kb, ++k) {
+                const Item I = item_at(P, item);
+                const int row_a = (I.m * CG + (int)rank) * kBM, row_b = I.n * BN + (int)rank * S::kBRows;
+                for (int kb = I.kb0; kb < I.kb1; ++kb, ++k) {
                     const uint32_t s = k % S::kStages, use = k / S::kStages;
                     if (use > 0 && !mbar_wait(empty0 + 8 * s, (use - 1) & 1, kGemmWaitNs)) {
                         ok = false;
@@ -348,7 +402,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     }
                     const uint32_t a = base + s * S::kStageBytes, b = a + S::kABytes;
                     uint32_t bar = full0 + 8 * s;
-                    if (rank == 0) mbar_arrive_expect_tx(bar, CG * S::kStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(bar, CG * (P.a_rows * (kBK * 2) + S::kBBytes));
                     if constexpr (CG == 2) bar = leader_address(bar);
                     if (P.a_mn) {
                         for (int i = 0; i < kBM / 64; ++i)
@@ -370,8 +424,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (lane == 0 && rank == 0) {
             uint32_t k = 0, tile = 0;
             for (int item = first; item < n_items && ok; item += step, ++tile) {
-                const int split = item % P.splits;
-                const int kb0 = split * P.k_per_split, kb1 = min(P.k_blocks, kb0 + P.k_per_split);
+                const Item I = item_at(P, item);
+                const int kb0 = I.kb0, kb1 = I.kb1;
                 const uint32_t acc = tile & 1, use = tile >> 1;
                 if (use > 0 && !mbar_wait(acc_empty0 + 8 * acc, (use - 1) & 1, kGemmWaitNs)) {
                     ok = false;
@@ -406,18 +460,17 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const uint32_t acc_empty_leader = CG == 2 ? leader_address(acc_empty0) : acc_empty0;
         uint32_t tile = 0;
         for (int item = first; item < n_items && ok; item += step, ++tile) {
-            const int split = item % P.splits;
-            int m, n;
-            tile_at(P, item / P.splits, m, n);
+            const Item I = item_at(P, item);
             const uint32_t acc = tile & 1, use = tile >> 1;
-            const int64_t row0 = (int64_t)(m * CG + (int)rank) * kBM + quad * 32;
+            const int row_in = (int)rank * kBM + quad * 32;                     // of the tile
+            const int64_t row0 = (int64_t)I.m * (CG * kBM) + row_in;
             ok = mbar_wait(acc_full0 + 8 * acc, use & 1, kGemmWaitNs);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
-                const int64_t col = (int64_t)n * BN + c + (lane & 3) * 8;   // this lane's eight columns
-                if ((int64_t)n * BN + c >= P.N) break;
+                const int64_t col0 = (int64_t)I.n * BN + c, col = col0 + (lane & 3) * 8;   // this lane's eight columns
+                if (col0 >= P.N || row0 >= P.M) break;
                 float x[32];
                 tmem_load32(tmem + acc * BN + c + ((uint32_t)(quad * 32) << 16), x);
                 // transposed through shared memory: 16-byte pieces, exchanged within eight rows so
@@ -430,9 +483,24 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
                                  : "memory");
                 }
                 __syncwarp();
+                if (I.part < 0 && !P.rows_vec) {
+                    // rows that do not start on 16 bytes: a column a lane, so that a warp writes neighbours
+                    if (col0 + lane < P.N) {
+                        const int rows = (int)min((int64_t)32, P.M - row0);
+#pragma unroll 4
+                        for (int r = 0; r < rows; ++r) {
+                            float z;
+                            const uint32_t at = stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(at) : "memory");
+                            finish1<DT>(P.epi, row0 + r, col0 + lane, z);
+                        }
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 const int cols = (int)max((int64_t)0, min((int64_t)8, P.N - col));
                 float bias[8];
-                if (!P.partial) bias8<DT>(P.epi, col, cols, bias);
+                if (I.part < 0) bias8<DT>(P.epi, col, cols, bias);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = i * 8 + (lane >> 2), p = (lane & 3) * 2;
@@ -447,8 +515,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     }
                     const int64_t row = row0 + r;
                     if (row < P.M && cols > 0) {
-                        if (P.partial) {
-                            float4* q = reinterpret_cast<float4*>(P.partial + ((int64_t)split * P.M + row) * P.ld_partial + col);
+                        if (I.part >= 0) {
+                            float4* q = reinterpret_cast<float4*>(P.partial + ((int64_t)I.part * (CG * kBM) + row_in + r) * BN + c + (lane & 3) * 8);
                             q[0] = make_float4(z[0], z[1], z[2], z[3]);
                             q[1] = make_float4(z[4], z[5], z[6], z[7]);
                         } else {
@@ -486,26 +554,54 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
 }
 
-// The partial products of a split inner dimension, summed in order, with the epilogue; also the
-// product over an empty inner dimension (no splits: z = 0).
+// The partial sums of the split tiles, in order, with the epilogue.  A block takes 8 rows of a tile, a
+// warp one: eight neighbouring columns a lane, or (rows that do not start on 16 bytes) every 32nd.
+struct TailParams {
+    const float* partial;
+    Epilogue epi;
+    int32_t M, N, full, splits, tiles_m, tiles_n, tile_rows, bn, rows_vec;
+};
+
 template <int DT>
-__global__ void __launch_bounds__(256) split_sum_kernel(const float* partial, int64_t ld, int splits, int64_t M,
-                                                        int64_t N, const __grid_constant__ Epilogue E)
+__global__ void __launch_bounds__(256) tail_sum_kernel(const __grid_constant__ TailParams P)
 {
-    const int64_t per_row = (N + 7) / 8, total = M * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-        const int n = (int)min((int64_t)8, N - col);
+    const int lane = threadIdx.x & 31, in = blockIdx.x * 8 + (threadIdx.x >> 5);    // the row in its tile
+    const int tail = gridDim.y, r = blockIdx.y;
+    int m, n;
+    tile_at(P.tiles_m, P.tiles_n, P.full + r, m, n);
+    const int64_t row = (int64_t)m * P.tile_rows + in, col0 = (int64_t)n * P.bn;
+    if (row >= P.M) return;
+    const float* from = P.partial + ((int64_t)r * P.tile_rows + in) * P.bn;
+    const int64_t next = (int64_t)tail * P.tile_rows * P.bn;
+    if (P.rows_vec) {
+        const int c = lane * 8, cols = (int)min((int64_t)8, P.N - col0 - c);
+        if (c >= P.bn || cols <= 0) return;
         float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, bias[8];
-        for (int s = 0; s < splits; ++s) {
-            const float4* q = reinterpret_cast<const float4*>(partial + ((int64_t)s * M + row) * ld + col);
+#pragma unroll 8
+        for (int s = 0; s < P.splits; ++s) {
+            const float4* q = reinterpret_cast<const float4*>(from + s * next + c);
             const float4 a = __ldcs(q), b = __ldcs(q + 1);
             z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
             z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
         }
-        bias8<DT>(E, col, n, bias);
-        finish8<DT>(E, row, col, n, z, bias);
+        bias8<DT>(P.epi, col0 + c, cols, bias);
+        finish8<DT>(P.epi, row, col0 + c, cols, z, bias);
+    } else {
+        for (int c = lane; c < P.bn && col0 + c < P.N; c += 32) {
+            float z = 0.0f;
+#pragma unroll 4
+            for (int s = 0; s < P.splits; ++s) z += __ldcs(from + s * next + c);
+            finish1<DT>(P.epi, row, col0 + c, z);
+        }
     }
+}
+
+// The product over an empty inner dimension: z = 0.
+template <int DT>
+__global__ void __launch_bounds__(256) empty_sum_kernel(int64_t M, int64_t N, const __grid_constant__ Epilogue E)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * 256)
+        finish1<DT>(E, i / N, i % N, 0.0f);
 }
 
 // ------------------------------------------------------------------ dz, and aligned copies
@@ -514,58 +610,101 @@ struct DzParams {
     const uint16_t* dy;
     const uint16_t* pre;     // NULL: the activation is none
     uint16_t* dz;            // rows of ld_dz elements, 16-byte aligned; NULL: only the sums
-    float* sums;             // [row chunk][ld_dz] column sums, or NULL
+    float* sums;             // [worker][ld_dz] column sums, or NULL
     int64_t rows, cols, ld_dy, ld_pre, ld_dz;
-    int32_t act, vec_dy, vec_pre, chunk;   // chunk: rows a block takes
+    int32_t act, vec_dy, vec_pre, chunk;   // chunk: consecutive rows a worker takes
 };
 
-// dz = dy act'(pre), and its column sums: 16 lanes of 8 columns by 16 rows at a time.
-template <int DT>
-__global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams P)
+// FLIGHT rows of a thread's eight columns; FULL: all eight are there, by 16-byte accesses.
+template <int DT, bool FULL, int FLIGHT>
+__device__ __forceinline__ void dz_rows(const DzParams& P, int64_t col, int n, int64_t r, float (&sum)[8])
 {
-    __shared__ float part[16][128 + 4];
-    const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-    const int64_t col = (int64_t)blockIdx.x * 128 + cx * 8;
-    const int n = (int)max((int64_t)0, min((int64_t)8, P.cols - col));
-    const int64_t r0 = (int64_t)blockIdx.y * P.chunk, r1 = min(P.rows, r0 + P.chunk);
-    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (n > 0) {
-        for (int64_t r = r0 + ry; r < r1; r += 16) {
-            float d[8];
-            load8<DT>(P.dy + r * P.ld_dy + col, P.vec_dy, n, d);
-            if (P.pre) {
-                float z[8];
-                load8<DT>(P.pre + r * P.ld_pre + col, P.vec_pre, n, z);
+    uint4 d[FLIGHT], z[FLIGHT];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] *= act_slope(z[j], P.act);
-            }
+    for (int i = 0; i < FLIGHT; ++i) {
+        const int64_t row = r + i;
+        if constexpr (FULL) {
+            d[i] = __ldcs(reinterpret_cast<const uint4*>(P.dy + row * P.ld_dy + col));
+            if (P.pre) z[i] = __ldcs(reinterpret_cast<const uint4*>(P.pre + row * P.ld_pre + col));
+        } else {
+            auto gather = [&](const uint16_t* p) {
+                uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += j < n ? d[j] : 0.0f;
-            if (P.dz) store8<DT>(P.dz + r * P.ld_dz + col, true, n, d);
+                for (int j = 0; j < 4; ++j)
+                    w[j] = (2 * j < n ? p[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)p[2 * j + 1] : 0u) << 16);
+                return make_uint4(w[0], w[1], w[2], w[3]);
+            };
+            d[i] = gather(P.dy + row * P.ld_dy + col);
+            if (P.pre) z[i] = gather(P.pre + row * P.ld_pre + col);
         }
     }
-    if (!P.sums) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[ry][cx * 8 + j] = sum[j];
-    __syncthreads();
-    if (threadIdx.x < 128) {
-        const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
-        float s = 0.0f;
+    for (int i = 0; i < FLIGHT; ++i) {
+        float x[8];
+        widen2<DT>(d[i].x, x[0], x[1]);
+        widen2<DT>(d[i].y, x[2], x[3]);
+        widen2<DT>(d[i].z, x[4], x[5]);
+        widen2<DT>(d[i].w, x[6], x[7]);
+        if (P.pre) {
+            float y[8];
+            widen2<DT>(z[i].x, y[0], y[1]);
+            widen2<DT>(z[i].y, y[2], y[3]);
+            widen2<DT>(z[i].z, y[4], y[5]);
+            widen2<DT>(z[i].w, y[6], y[7]);
+            act_slopes(y, P.act);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += part[i][threadIdx.x];
-        if (c < P.cols) P.sums[(int64_t)blockIdx.y * P.ld_dz + c] = s;
+            for (int j = 0; j < 8; ++j) x[j] *= y[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += FULL || j < n ? x[j] : 0.0f;
+        if (P.dz) store8<DT>(P.dz + (r + i) * P.ld_dz + col, true, n, x);
     }
 }
 
-// Sums over the row chunks, in order, in fp32.
+// dz = dy act'(pre), and its column sums: a thread takes eight columns of a worker's rows (blocks of up to
+// 2048 columns; narrower ones hold several workers), so that the sums need no exchange.
 template <int DT>
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* sums, int64_t ld, int chunks, int64_t cols,
+__global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzParams P)
+{
+    constexpr int kFlight = 2;
+    const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, P.cols - col));
+    const int64_t worker = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
+    const int64_t r1 = min(P.rows, (worker + 1) * P.chunk);
+    int64_t r = worker * P.chunk;
+    if (n == 0 || r >= r1) return;
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (n == 8 && P.vec_dy && (P.vec_pre || !P.pre)) {
+        for (; r + kFlight <= r1; r += kFlight) dz_rows<DT, true, kFlight>(P, col, n, r, sum);
+        for (; r < r1; ++r) dz_rows<DT, true, 1>(P, col, n, r, sum);
+    } else {
+        for (; r + kFlight <= r1; r += kFlight) dz_rows<DT, false, kFlight>(P, col, n, r, sum);
+        for (; r < r1; ++r) dz_rows<DT, false, 1>(P, col, n, r, sum);
+    }
+    if (!P.sums) return;
+    float4* q = reinterpret_cast<float4*>(P.sums + worker * P.ld_dz + col);      // rows of a multiple of 8
+    q[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    q[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+}
+
+// Sums over the workers, in a fixed order, in fp32: 32 columns by 8 workers at a time.
+template <int DT>
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* sums, int64_t ld, int64_t workers, int64_t cols,
                                                          uint16_t* out, int accumulate)
 {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
+    __shared__ float part[8][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
-    for (int i = 0; i < chunks; ++i) s += sums[(int64_t)i * ld + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int64_t w = threadIdx.y; w < workers; w += 8) s += sums[w * ld + c];
+    }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y != 0 || c >= cols) return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
     if (accumulate) s += widen1<DT>(out[c]);
     out[c] = narrow1<DT>(s);
 }
@@ -588,6 +727,157 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* src, in
     }
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Up to kFewRows rows: each weight is used so seldom that reading W at HBM's rate is all there is, and a
+// tile of 128 rows would be idle.  fp32 products on the plain cores, the inner dimension split over a
+// block's threads, one launch.
+constexpr int kFewRows = 8;
+
+struct FewParams {
+    const uint16_t *x, *w;
+    Epilogue epi;
+    int64_t ld_x, ld_w;
+    int32_t M, N, K;
+    int32_t vec_x, vec_w;
+};
+
+// W stored (out, in): a warp takes COLS rows of W and every `warps`-th 256 elements of them.
+template <int DT, int ROWS, int COLS>
+__global__ void __launch_bounds__(256) few_rows_out_in_kernel(const __grid_constant__ FewParams P)
+{
+    __shared__ float part[8][ROWS * COLS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t n0 = (int64_t)blockIdx.x * COLS;
+    F2 acc[ROWS][COLS];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) acc[m][c] = both(0.0f);
+    for (int64_t k = warp * 256 + lane * 8; k < P.K; k += warps * 256) {
+        const int n = (int)min((int64_t)8, P.K - k);
+        F2 w[COLS][4];
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            float f[8];
+            load8<DT>(P.w + (n0 + c) * P.ld_w + k, P.vec_w, n0 + c < P.N ? n : 0, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[c][j] = pair(f[2 * j], f[2 * j + 1]);
+        }
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) {
+            if (m >= P.M) break;
+            float f[8];
+            load8<DT>(P.x + m * P.ld_x + k, P.vec_x, n, f);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][c] = fma(pair(f[2 * j], f[2 * j + 1]), w[c][j], acc[m][c]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            float a, b;
+            split(acc[m][c], a, b);
+            a += b;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            if (lane == 0) part[warp][m * COLS + c] = a;
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * COLS; i += blockDim.x) {
+        const int m = i / COLS, c = i % COLS;
+        if (m >= P.M || n0 + c >= P.N) continue;
+        float z = 0.0f;
+        for (int w = 0; w < warps; ++w) z += part[w][i];
+        finish1<DT>(P.epi, m, n0 + c, z);
+    }
+}
+
+// W stored (in, out): a block takes 64 neighbouring columns, eight a thread, and its 64 thread rows every
+// 64th inner element.
+template <int DT, int ROWS>
+__global__ void __launch_bounds__(512) few_rows_in_out_kernel(const __grid_constant__ FewParams P)
+{
+    __shared__ float part[16][ROWS][64 + 1];
+    const int cx = threadIdx.x & 7, ky = threadIdx.x >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 64 + cx * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, P.N - col));
+    F2 acc[ROWS][4];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = both(0.0f);
+    constexpr int kFlight = ROWS <= 2 ? 8 : 4;
+    const bool vec = P.vec_w && n == 8;
+    for (int64_t k = ky; k < P.K; k += 64 * kFlight) {
+        uint4 q[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int64_t kk = k + 64 * i;
+            const uint16_t* p = P.w + kk * P.ld_w + col;
+            q[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (kk < P.K) {
+                if (vec) {
+                    q[i] = __ldcs(reinterpret_cast<const uint4*>(p));
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = (2 * j < n ? p[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)p[2 * j + 1] : 0u) << 16);
+                    q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int64_t kk = k + 64 * i;
+            if (kk >= P.K) break;
+            float f[8];
+            widen2<DT>(q[i].x, f[0], f[1]);
+            widen2<DT>(q[i].y, f[2], f[3]);
+            widen2<DT>(q[i].z, f[4], f[5]);
+            widen2<DT>(q[i].w, f[6], f[7]);
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                if (m >= P.M) break;
+                const F2 x = both(widen1<DT>(P.x[m * P.ld_x + kk]));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = fma(x, pair(f[2 * j], f[2 * j + 1]), acc[m][j]);
+            }
+        }
+    }
+    // the warp's four thread rows, then the block's sixteen warps in order
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split(acc[m][j], a, b);
+#pragma unroll
+            for (int o = 8; o < 32; o <<= 1) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            if (lane < 8) {
+                part[warp][m][cx * 8 + 2 * j] = a;
+                part[warp][m][cx * 8 + 2 * j + 1] = b;
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * 64; i += 512) {
+        const int m = i >> 6, c = i & 63;
+        const int64_t at = (int64_t)blockIdx.x * 64 + c;
+        if (m >= P.M || at >= P.N) continue;
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) z += part[w][m][c];
+        finish1<DT>(P.epi, m, at, z);
+    }
+}
+
 // ------------------------------------------------------------------ host: one product
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -603,51 +893,56 @@ struct Operand {
 
 bool tma_ready(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
-// How a product is cut: tile shape and splits of the inner dimension.
+// How a product is cut: the tile's shape; tiles done whole, a multiple of what runs at one time; and the
+// parts along K that the rest is split into.
 struct Cut {
     int cg = 2, bn = 256;
     int splits = 1, per_split = 0;
-    int64_t tiles_m = 0, tiles_n = 0;
+    int64_t tiles_m = 0, tiles_n = 0, full = 0;
+    int64_t tail() const { return tiles_m * tiles_n - full; }
+    int64_t tile_elems() const { return (int64_t)kBM * cg * bn; }
 };
 
 constexpr int kGb300Sms = 152;
 
-// The cut with the least estimated time.  A wave of tiles takes its inner blocks at the shape's rate, plus
-// filling and draining; a split product writes and reads its fp32 partial sums once more.
-Cut choose_cut(int64_t M, int64_t N, int64_t K, int sms)
+// The cut with the least estimated time.  One inner block (kBK) of a 256 x 256 tile on a pair of SMs takes
+// 0.336 us, 94 % of the tensor cores' measured rate.  A 128 x 128 tile on one SM is bound by what an SM
+// takes from L2, 117 GB/s measured (64 bytes a clock): the same bytes for half an SM's products.  It serves
+// where there are few rows or few tiles.  Split tiles write and read fp32 partial sums once (L2), in a
+// launch of their own.
+Cut choose_cut(int64_t M, int64_t N, int64_t K)
 {
-    struct Shape {
-        int cg, bn;
-        double block_us;   // one inner block of kBK elements of one tile
-    };
-    static const Shape shapes[] = {{2, 256, 0.150}, {1, 128, 0.085}};
-    const int64_t kb = div_up(K, kBK);
+    const int64_t kb = div_up(std::max<int64_t>(K, 1), kBK);
     Cut best;
     double best_us = 1e30;
-    for (const Shape& s : shapes) {
-        const int64_t tm = div_up(M, kBM * s.cg), tn = div_up(N, s.bn), slots = std::max(1, sms / s.cg);
-        for (int64_t want = 1; want <= std::min<int64_t>(kb, 64); ++want) {
-            const int64_t per = div_up(std::max<int64_t>(kb, 1), want), splits = std::max<int64_t>(1, div_up(kb, per));
-            if (splits != want && want > 1) continue;
-            if (splits > 1 && splits * M * N > ((int64_t)1 << 28)) continue;   // 1 GB of partial sums at most
-            const int64_t waves = div_up(tm * tn * splits, slots);
-            double us = waves * per * s.block_us + 2.0;
-            if (splits > 1) us += 2.5 + (double)(splits * 8 + 2) * M * N / 4.0e6;
+    for (int cg = 2; cg >= 1; --cg) {
+        Cut c;
+        c.cg = cg;
+        c.bn = 128 * cg;
+        c.tiles_m = div_up(M, kBM * cg);
+        c.tiles_n = div_up(N, c.bn);
+        const double block_us = cg == 2 ? 0.336 : (double)(std::min<int64_t>(kBM, up(M, 8)) + 128) * kBK * 2 / 117e3;
+        const int64_t slots = kGb300Sms / cg, tiles = c.tiles_m * c.tiles_n;
+        for (int64_t want = 1; want <= std::min<int64_t>(kb, 76); ++want) {
+            const int64_t per = div_up(kb, want), splits = div_up(kb, per);
+            if (splits != want) continue;
+            c.full = splits == 1 ? tiles : tiles / slots * slots;
+            if (splits > 1 && c.tail() == 0) continue;
+            if (splits * c.tail() * c.tile_elems() > ((int64_t)1 << 28)) continue;   // 1 GB of partial sums at most
+            c.splits = (int)splits;
+            c.per_split = (int)per;
+            double us = div_up(c.full, slots) * kb * block_us;
+            if (splits > 1) us += div_up(c.tail() * splits, slots) * per * block_us + 3.5 + (double)(splits * 8 + 2) * c.tail() * c.tile_elems() / 8.0e6;
             if (us < best_us) {
                 best_us = us;
-                best.cg = s.cg;
-                best.bn = s.bn;
-                best.splits = (int)splits;
-                best.per_split = (int)per;
-                best.tiles_m = tm;
-                best.tiles_n = tn;
+                best = c;
             }
         }
     }
     return best;
 }
 
-int64_t partial_bytes(const Cut& c, int64_t M, int64_t N) { return c.splits > 1 ? 4 * (int64_t)c.splits * M * up(N, 8) : 0; }
+int64_t partial_bytes(const Cut& c) { return c.splits > 1 ? 4 * (int64_t)c.splits * c.tail() * c.tile_elems() : 0; }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -687,7 +982,7 @@ zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
     static const cudaError_t set =
         cudaFuncSetAttribute(gemm_kernel<CG, BN, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (set != cudaSuccess) return cuda_fail(set, "zero_linear: shared memory");
-    const int64_t items = (int64_t)P.tiles_m * P.tiles_n * P.splits;
+    const int64_t items = P.full + ((int64_t)P.tiles_m * P.tiles_n - P.full) * P.splits;
     const int grid = CG * (int)std::min<int64_t>(std::max(1, sms / CG), items);
     gemm_kernel<CG, BN, DT><<<grid, kGemmThreads, S::kSmem, s>>>(P);
     const cudaError_t e = cudaGetLastError();
@@ -702,64 +997,112 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     const int64_t M = a.rows, N = b.rows, K = a.inner;
     if (M == 0 || N == 0) return ZERO_OK;
     const bool bf = dtype16 == ZERO_BF16;
-    Cut c;
-    if (K > 0) {
-        c = choose_cut(M, N, K, sms);
-        GemmParams P;
-        zero_status_t st = encode(&P.a, a, dtype16, kBM);
-        if (st == ZERO_OK) st = encode(&P.b, b, dtype16, c.bn / c.cg);
-        if (st != ZERO_OK) return st;
-        P.epi = E;
-        P.partial = c.splits > 1 ? partial : nullptr;
-        P.ld_partial = up(N, 8);
-        P.M = (int32_t)M;
-        P.N = (int32_t)N;
-        P.k_blocks = (int32_t)div_up(K, kBK);
-        P.splits = c.splits;
-        P.k_per_split = c.per_split;
-        P.tiles_m = (int32_t)c.tiles_m;
-        P.tiles_n = (int32_t)c.tiles_n;
-        P.a_mn = a.mn;
-        P.b_mn = b.mn;
-        // fp32 accumulators; operand type; which operands lie along their rows; N / 8; M / 16
-        P.idesc = (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((a.mn ? 1u : 0u) << 15) |
-                  ((b.mn ? 1u : 0u) << 16) | ((uint32_t)(c.bn >> 3) << 17) | ((uint32_t)((kBM * c.cg) >> 4) << 24);
-        if (c.cg == 2) st = bf ? launch_shape<2, 256, ZERO_BF16>(P, sms, s) : launch_shape<2, 256, ZERO_FP16>(P, sms, s);
-        else st = bf ? launch_shape<1, 128, ZERO_BF16>(P, sms, s) : launch_shape<1, 128, ZERO_FP16>(P, sms, s);
-        if (st != ZERO_OK || c.splits == 1) return st;
-    } else {
-        c.splits = 0;
+    if (K == 0) {
+        const int grid = grid_of(M * N, sms, 8);
+        if (bf) empty_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(M, N, E);
+        else empty_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(M, N, E);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
     }
-    const int grid = grid_of(M * div_up(N, 8), sms, 8);
-    if (bf) split_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(partial, up(N, 8), c.splits, M, N, E);
-    else split_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(partial, up(N, 8), c.splits, M, N, E);
+    const Cut c = choose_cut(M, N, K);
+    GemmParams P;
+    // few rows: no zeros are copied for the rest (the rows of D that they leave undefined are not stored)
+    P.a_rows = c.cg == 1 && !a.mn && M < kBM ? (int32_t)up(M, 8) : kBM;
+    zero_status_t st = encode(&P.a, a, dtype16, P.a_rows);
+    if (st == ZERO_OK) st = encode(&P.b, b, dtype16, c.bn / c.cg);
+    if (st != ZERO_OK) return st;
+    P.epi = E;
+    P.partial = partial;
+    P.M = (int32_t)M;
+    P.N = (int32_t)N;
+    P.k_blocks = (int32_t)div_up(K, kBK);
+    P.full = (int32_t)c.full;
+    P.splits = c.splits;
+    P.k_per_split = c.per_split;
+    P.tiles_m = (int32_t)c.tiles_m;
+    P.tiles_n = (int32_t)c.tiles_n;
+    P.a_mn = a.mn;
+    P.b_mn = b.mn;
+    P.rows_vec = (E.vec & kVecOut) && (!E.pre || (E.vec & kVecPre)) && (!E.residual || (E.vec & kVecRes));
+    // fp32 accumulators; operand type; which operands lie along their rows; N / 8; M / 16
+    P.idesc = (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((a.mn ? 1u : 0u) << 15) |
+              ((b.mn ? 1u : 0u) << 16) | ((uint32_t)(c.bn >> 3) << 17) | ((uint32_t)((kBM * c.cg) >> 4) << 24);
+    if (c.cg == 2) st = bf ? launch_shape<2, 256, ZERO_BF16>(P, sms, s) : launch_shape<2, 256, ZERO_FP16>(P, sms, s);
+    else st = bf ? launch_shape<1, 128, ZERO_BF16>(P, sms, s) : launch_shape<1, 128, ZERO_FP16>(P, sms, s);
+    if (st != ZERO_OK || c.splits == 1) return st;
+    TailParams T;
+    T.partial = partial;
+    T.epi = E;
+    T.M = P.M;
+    T.N = P.N;
+    T.full = P.full;
+    T.splits = c.splits;
+    T.tiles_m = P.tiles_m;
+    T.tiles_n = P.tiles_n;
+    T.tile_rows = kBM * c.cg;
+    T.bn = c.bn;
+    T.rows_vec = P.rows_vec;
+    const dim3 grid((unsigned)(T.tile_rows / 8), (unsigned)c.tail());
+    if (bf) tail_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(T);
+    else tail_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(T);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+}
+
+template <int DT, int ROWS>
+void launch_few(const FewParams& P, bool out_in, cudaStream_t s)
+{
+    if (out_in) {
+        // two outputs a block of eight warps: their parts of K are short enough, and there are blocks for
+        // every SM
+        few_rows_out_in_kernel<DT, ROWS, 2><<<(unsigned)div_up(P.N, 2), P.K > 1024 ? 256 : P.K > 512 ? 128 : 64, 0, s>>>(P);
+    } else {
+        few_rows_in_out_kernel<DT, ROWS><<<(unsigned)div_up(P.N, 64), 512, 0, s>>>(P);
+    }
+}
+
+template <int DT>
+void launch_few(const FewParams& P, bool out_in, cudaStream_t s)
+{
+    if (P.M == 1) launch_few<DT, 1>(P, out_in, s);
+    else if (P.M == 2) launch_few<DT, 2>(P, out_in, s);
+    else if (P.M <= 4) launch_few<DT, 4>(P, out_in, s);
+    else launch_few<DT, 8>(P, out_in, s);
 }
 
 // ------------------------------------------------------------------ host: the layer
 
 constexpr int64_t kMaxSize = ZERO_LINEAR_MAX_SIZE;   // tile coordinates stay 32-bit
 
+// How the dz pass is cut: threads across the columns (eight each) and workers a block, rows a worker.
+// About eight blocks an SM where there are rows for them.
+struct DzCut {
+    int tx = 256, ty = 1, chunk = 1;
+    int64_t workers = 0;
+};
+
+DzCut dz_cut(int64_t rows, int64_t cols)
+{
+    DzCut c;
+    while (c.tx > 32 && (int64_t)c.tx * 4 >= cols) c.tx /= 2;
+    c.ty = 256 / c.tx;
+    const int64_t across = std::max<int64_t>(1, div_up(cols, (int64_t)c.tx * 8));
+    const int64_t want = std::max<int64_t>(1, 8 * kGb300Sms * c.ty / across);
+    c.chunk = (int)std::max<int64_t>(4, div_up(std::max<int64_t>(rows, 1), want));
+    c.workers = div_up(rows, c.chunk);
+    return c;
+}
+
 // Everything a call needs, checked: strides filled in, and where its pieces lie in the workspace.
 struct Layer {
     zero_linear_t a;
     bool bf = true;
     int64_t w_rows = 0, w_cols = 0;        // as stored
-    bool copy_x = false, copy_w = false, make_dz = false;
+    bool copy_x = false, copy_w = false, make_dz = false, few = false;
     int64_t ld_x8 = 0, ld_w8 = 0, ld_dz = 0;
     int64_t at_x = 0, at_w = 0, at_dz = 0, at_sums = 0, at_partial = 0, bytes = 0;
-    int chunk = 0, chunks = 0;
+    DzCut dz;
 };
-
-// Rows one block of the dz pass takes: enough blocks for the GPU, few enough sums.
-void dz_chunks(int64_t rows, int64_t cols, int* chunk, int* chunks)
-{
-    const int64_t want = std::max<int64_t>(1, 8 * kGb300Sms / std::max<int64_t>(1, div_up(cols, 128)));
-    const int64_t c = std::max<int64_t>(32, up(div_up(std::max<int64_t>(rows, 1), want), 16));
-    *chunk = (int)c;
-    *chunks = (int)div_up(rows, c);
-}
 
 zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* who)
 {
@@ -816,8 +1159,9 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
     L->ld_x8 = a.ld_x;
     L->ld_w8 = a.ld_w;
     L->ld_dz = a.ld_dy;
-    L->copy_x = product_there && use_x && !tma_ready(a.x, a.ld_x);
-    L->copy_w = product_there && use_w && !tma_ready(a.w, a.ld_w);
+    L->few = !back && product_there && a.rows <= kFewRows;
+    L->copy_x = product_there && use_x && !L->few && !tma_ready(a.x, a.ld_x);
+    L->copy_w = product_there && use_w && !L->few && !tma_ready(a.w, a.ld_w);
     if (L->copy_x) {
         L->ld_x8 = up(a.in_features, 8);
         L->at_x = take(2 * a.rows * L->ld_x8);
@@ -828,7 +1172,7 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
     }
     int64_t partial = 0;
     if (!back) {
-        if (product_there) partial = partial_bytes(choose_cut(a.rows, a.out_features, a.in_features, kGb300Sms), a.rows, a.out_features);
+        if (product_there && !L->few) partial = partial_bytes(choose_cut(a.rows, a.out_features, a.in_features));
     } else {
         const bool products = product_there && (a.dx || a.dw);
         L->make_dz = products && (a.activation != ZERO_ACT_NONE || !tma_ready(a.dy, a.ld_dy));
@@ -836,12 +1180,12 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
             L->ld_dz = up(a.out_features, 8);
             L->at_dz = take(2 * a.rows * L->ld_dz);
         }
-        dz_chunks(a.rows, a.out_features, &L->chunk, &L->chunks);
-        if (a.dbias && any_out) L->at_sums = take(4 * (int64_t)L->chunks * up(a.out_features, 8));
+        L->dz = dz_cut(a.rows, a.out_features);
+        if (a.dbias && any_out) L->at_sums = take(4 * L->dz.workers * up(a.out_features, 8));
         if (product_there && a.dx)
-            partial = std::max(partial, partial_bytes(choose_cut(a.rows, a.in_features, a.out_features, kGb300Sms), a.rows, a.in_features));
+            partial = std::max(partial, partial_bytes(choose_cut(a.rows, a.in_features, a.out_features)));
         if (product_there && a.dw)
-            partial = std::max(partial, partial_bytes(choose_cut(L->w_rows, L->w_cols, a.rows, kGb300Sms), L->w_rows, L->w_cols));
+            partial = std::max(partial, partial_bytes(choose_cut(L->w_rows, L->w_cols, a.rows)));
     }
     L->at_partial = take(partial);
     L->bytes = at;
@@ -918,6 +1262,23 @@ try {
     E.act = a.activation;
     E.vec = vec_flag(a.y, a.ld_y, kVecOut) | vec_flag(a.pre, a.ld_pre, kVecPre) |
             vec_flag(a.residual, a.ld_residual, kVecRes) | vec_flag(a.bias, 0, kVecBias);
+    if (L.few) {
+        FewParams P;
+        P.x = static_cast<const uint16_t*>(a.x);
+        P.w = static_cast<const uint16_t*>(a.w);
+        P.epi = E;
+        P.ld_x = a.ld_x;
+        P.ld_w = a.ld_w;
+        P.M = (int32_t)a.rows;
+        P.N = (int32_t)a.out_features;
+        P.K = (int32_t)a.in_features;
+        P.vec_x = vec_flag(a.x, a.ld_x, 1);
+        P.vec_w = vec_flag(a.w, a.ld_w, 1);
+        if (L.bf) launch_few<ZERO_BF16>(P, a.layout == ZERO_WEIGHT_OUT_IN, s);
+        else launch_few<ZERO_FP16>(P, a.layout == ZERO_WEIGHT_OUT_IN, s);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+    }
     const Operand A{x, a.rows, a.in_features, L.ld_x8, false};
     const Operand B{w, a.out_features, a.in_features, L.ld_w8, a.layout == ZERO_WEIGHT_IN_OUT};
     return product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, s);
@@ -961,18 +1322,20 @@ try {
         D.act = a.activation;
         D.vec_dy = vec_flag(a.dy, a.ld_dy, 1);
         D.vec_pre = vec_flag(a.pre, a.ld_pre, 1);
-        D.chunk = L.chunk;
-        const dim3 grid((unsigned)div_up(a.out_features, 128), (unsigned)L.chunks);
-        if (L.bf) dz_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(D);
-        else dz_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(D);
+        D.chunk = L.dz.chunk;
+        const dim3 grid((unsigned)div_up(a.out_features, (int64_t)L.dz.tx * 8), (unsigned)div_up(L.dz.workers, L.dz.ty));
+        const dim3 threads(L.dz.tx, L.dz.ty);
+        if (L.bf) dz_kernel<ZERO_BF16><<<grid, threads, 0, s>>>(D);
+        else dz_kernel<ZERO_FP16><<<grid, threads, 0, s>>>(D);
         if (L.make_dz) dz = D.dz;
     }
     if (a.dbias && a.out_features > 0 && !(a.rows == 0 && accumulate)) {
-        const unsigned grid = (unsigned)div_up(a.out_features, 256);
-        const int chunks = any_out ? L.chunks : 0;
+        const unsigned grid = (unsigned)div_up(a.out_features, 32);
+        const dim3 threads(32, 8);
+        const int64_t workers = any_out ? L.dz.workers : 0;
         uint16_t* db = static_cast<uint16_t*>(a.dbias);
-        if (L.bf) column_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(sums, up(a.out_features, 8), chunks, a.out_features, db, accumulate);
-        else column_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(sums, up(a.out_features, 8), chunks, a.out_features, db, accumulate);
+        if (L.bf) column_sum_kernel<ZERO_BF16><<<grid, threads, 0, s>>>(sums, up(a.out_features, 8), workers, a.out_features, db, accumulate);
+        else column_sum_kernel<ZERO_FP16><<<grid, threads, 0, s>>>(sums, up(a.out_features, 8), workers, a.out_features, db, accumulate);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "zero_linear_backward: launch");
