@@ -332,7 +332,7 @@ struct GemmShape {
     static constexpr int kBRows = BN / CG;                       // B rows one block stages
     static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBRows * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = 6;
+    static constexpr int kStages = BN == 64 ? 8 : 6;
     static constexpr int kTmemCols = 2 * BN;                     // two accumulators
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 256;
 };
@@ -729,10 +729,11 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* src, in
 
 // ------------------------------------------------------------------ few rows
 //
-// Up to kFewRows rows: each weight is used so seldom that reading W at HBM's rate is all there is, and a
-// tile of 128 rows would be idle.  fp32 products on the plain cores, the inner dimension split over a
-// block's threads, one launch.
-constexpr int kFewRows = 8;
+// Up to kFewRows rows of x and W stored (out, in): reading W is all there is.  fp32 products on the plain
+// cores straight from the loads, no tiles, one launch: for one row 2048 -> 8192 takes 11.4 us and 8192 ->
+// 2048 9.5, through tiles 14 and 15; for four rows the tiles' 14 are less than this kernel's 22.  W
+// stored (in, out) needs its partial sums exchanged between blocks: 12.8 and 19 us, tiles 14 and 15.
+constexpr int kFewRows = 2;
 
 struct FewParams {
     const uint16_t *x, *w;
@@ -744,7 +745,7 @@ struct FewParams {
 
 // W stored (out, in): a warp takes COLS rows of W and every `warps`-th 256 elements of them.
 template <int DT, int ROWS, int COLS>
-__global__ void __launch_bounds__(256) few_rows_out_in_kernel(const __grid_constant__ FewParams P)
+__global__ void __launch_bounds__(256) few_rows_kernel(const __grid_constant__ FewParams P)
 {
     __shared__ float part[8][ROWS * COLS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -756,23 +757,38 @@ __global__ void __launch_bounds__(256) few_rows_out_in_kernel(const __grid_const
         for (int c = 0; c < COLS; ++c) acc[m][c] = both(0.0f);
     for (int64_t k = warp * 256 + lane * 8; k < P.K; k += warps * 256) {
         const int n = (int)min((int64_t)8, P.K - k);
-        F2 w[COLS][4];
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) {
-            float f[8];
-            load8<DT>(P.w + (n0 + c) * P.ld_w + k, P.vec_w, n0 + c < P.N ? n : 0, f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[c][j] = pair(f[2 * j], f[2 * j + 1]);
-        }
-#pragma unroll
-        for (int m = 0; m < ROWS; ++m) {
-            if (m >= P.M) break;
-            float f[8];
-            load8<DT>(P.x + m * P.ld_x + k, P.vec_x, n, f);
+        if (n == 8 && P.vec_w && P.vec_x) {
+            uint4 w[COLS], x[ROWS];
 #pragma unroll
             for (int c = 0; c < COLS; ++c)
+                w[c] = n0 + c < P.N ? __ldcs(reinterpret_cast<const uint4*>(P.w + (n0 + c) * P.ld_w + k)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][c] = fma(pair(f[2 * j], f[2 * j + 1]), w[c][j], acc[m][c]);
+            for (int m = 0; m < ROWS; ++m) x[m] = *reinterpret_cast<const uint4*>(P.x + m * P.ld_x + k);
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                const uint32_t xs[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a, b, e, f;
+                        widen2<DT>(xs[j], a, b);
+                        widen2<DT>(ws[j], e, f);
+                        acc[m][c] = fma(pair(a, b), pair(e, f), acc[m][c]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                if (n0 + c >= P.N) break;
+                for (int j = 0; j < n; ++j) {
+                    const float w = widen1<DT>(P.w[(n0 + c) * P.ld_w + k + j]);
+#pragma unroll
+                    for (int m = 0; m < ROWS; ++m) acc[m][c] = fma(pair(widen1<DT>(P.x[m * P.ld_x + k + j]), 0.0f), pair(w, 0.0f), acc[m][c]);
+                }
+            }
         }
     }
 #pragma unroll
@@ -793,88 +809,6 @@ __global__ void __launch_bounds__(256) few_rows_out_in_kernel(const __grid_const
         float z = 0.0f;
         for (int w = 0; w < warps; ++w) z += part[w][i];
         finish1<DT>(P.epi, m, n0 + c, z);
-    }
-}
-
-// W stored (in, out): a block takes 64 neighbouring columns, eight a thread, and its 64 thread rows every
-// 64th inner element.
-template <int DT, int ROWS>
-__global__ void __launch_bounds__(512) few_rows_in_out_kernel(const __grid_constant__ FewParams P)
-{
-    __shared__ float part[16][ROWS][64 + 1];
-    const int cx = threadIdx.x & 7, ky = threadIdx.x >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t col = (int64_t)blockIdx.x * 64 + cx * 8;
-    const int n = (int)max((int64_t)0, min((int64_t)8, P.N - col));
-    F2 acc[ROWS][4];
-#pragma unroll
-    for (int m = 0; m < ROWS; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[m][j] = both(0.0f);
-    constexpr int kFlight = ROWS <= 2 ? 8 : 4;
-    const bool vec = P.vec_w && n == 8;
-    for (int64_t k = ky; k < P.K; k += 64 * kFlight) {
-        uint4 q[kFlight];
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const int64_t kk = k + 64 * i;
-            const uint16_t* p = P.w + kk * P.ld_w + col;
-            q[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (kk < P.K) {
-                if (vec) {
-                    q[i] = __ldcs(reinterpret_cast<const uint4*>(p));
-                } else {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = (2 * j < n ? p[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)p[2 * j + 1] : 0u) << 16);
-                    q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const int64_t kk = k + 64 * i;
-            if (kk >= P.K) break;
-            float f[8];
-            widen2<DT>(q[i].x, f[0], f[1]);
-            widen2<DT>(q[i].y, f[2], f[3]);
-            widen2<DT>(q[i].z, f[4], f[5]);
-            widen2<DT>(q[i].w, f[6], f[7]);
-#pragma unroll
-            for (int m = 0; m < ROWS; ++m) {
-                if (m >= P.M) break;
-                const F2 x = both(widen1<DT>(P.x[m * P.ld_x + kk]));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][j] = fma(x, pair(f[2 * j], f[2 * j + 1]), acc[m][j]);
-            }
-        }
-    }
-    // the warp's four thread rows, then the block's sixteen warps in order
-#pragma unroll
-    for (int m = 0; m < ROWS; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float a, b;
-            split(acc[m][j], a, b);
-#pragma unroll
-            for (int o = 8; o < 32; o <<= 1) {
-                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-            }
-            if (lane < 8) {
-                part[warp][m][cx * 8 + 2 * j] = a;
-                part[warp][m][cx * 8 + 2 * j + 1] = b;
-            }
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < ROWS * 64; i += 512) {
-        const int m = i >> 6, c = i & 63;
-        const int64_t at = (int64_t)blockIdx.x * 64 + c;
-        if (m >= P.M || at >= P.N) continue;
-        float z = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) z += part[w][m][c];
-        finish1<DT>(P.epi, m, at, z);
     }
 }
 
@@ -906,8 +840,8 @@ struct Cut {
 constexpr int kGb300Sms = 152;
 
 // The cut with the least estimated time.  One inner block (kBK) of a 256 x 256 tile on a pair of SMs takes
-// 0.336 us, 94 % of the tensor cores' measured rate.  A 128 x 128 tile on one SM is bound by what an SM
-// takes from L2, 117 GB/s measured (64 bytes a clock): the same bytes for half an SM's products.  It serves
+// 0.336 us, 94 % of the tensor cores' measured rate.  A 128 x 128 tile on one SM takes 0.29: the same
+// bytes for a quarter of the products (an SM takes 117 GB/s from L2, 64 bytes a clock).  It serves
 // where there are few rows or few tiles.  Split tiles write and read fp32 partial sums once (L2), in a
 // launch of their own.
 Cut choose_cut(int64_t M, int64_t N, int64_t K)
@@ -915,13 +849,18 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K)
     const int64_t kb = div_up(std::max<int64_t>(K, 1), kBK);
     Cut best;
     double best_us = 1e30;
-    for (int cg = 2; cg >= 1; --cg) {
+    static const struct {
+        int cg, bn;
+        double block_us;
+    } shapes[] = {{2, 256, 0.336}, {1, 128, 0.29}, {1, 64, 0.20}};
+    for (const auto& shape : shapes) {
+        const int cg = shape.cg;
+        const double block_us = shape.block_us;
         Cut c;
         c.cg = cg;
-        c.bn = 128 * cg;
+        c.bn = shape.bn;
         c.tiles_m = div_up(M, kBM * cg);
         c.tiles_n = div_up(N, c.bn);
-        const double block_us = cg == 2 ? 0.336 : (double)(std::min<int64_t>(kBM, up(M, 8)) + 128) * kBK * 2 / 117e3;
         const int64_t slots = kGb300Sms / cg, tiles = c.tiles_m * c.tiles_n;
         for (int64_t want = 1; want <= std::min<int64_t>(kb, 76); ++want) {
             const int64_t per = div_up(kb, want), splits = div_up(kb, per);
@@ -1006,7 +945,7 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     }
     const Cut c = choose_cut(M, N, K);
     GemmParams P;
-    // few rows: no zeros are copied for the rest (the rows of D that they leave undefined are not stored)
+    // few rows: no zeros are copied for the rest, whose results are not stored
     P.a_rows = c.cg == 1 && !a.mn && M < kBM ? (int32_t)up(M, 8) : kBM;
     zero_status_t st = encode(&P.a, a, dtype16, P.a_rows);
     if (st == ZERO_OK) st = encode(&P.b, b, dtype16, c.bn / c.cg);
@@ -1028,7 +967,8 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     P.idesc = (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((a.mn ? 1u : 0u) << 15) |
               ((b.mn ? 1u : 0u) << 16) | ((uint32_t)(c.bn >> 3) << 17) | ((uint32_t)((kBM * c.cg) >> 4) << 24);
     if (c.cg == 2) st = bf ? launch_shape<2, 256, ZERO_BF16>(P, sms, s) : launch_shape<2, 256, ZERO_FP16>(P, sms, s);
-    else st = bf ? launch_shape<1, 128, ZERO_BF16>(P, sms, s) : launch_shape<1, 128, ZERO_FP16>(P, sms, s);
+    else if (c.bn == 128) st = bf ? launch_shape<1, 128, ZERO_BF16>(P, sms, s) : launch_shape<1, 128, ZERO_FP16>(P, sms, s);
+    else st = bf ? launch_shape<1, 64, ZERO_BF16>(P, sms, s) : launch_shape<1, 64, ZERO_FP16>(P, sms, s);
     if (st != ZERO_OK || c.splits == 1) return st;
     TailParams T;
     T.partial = partial;
@@ -1050,24 +990,13 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
 }
 
 template <int DT, int ROWS>
-void launch_few(const FewParams& P, bool out_in, cudaStream_t s)
+zero_status_t launch_few(const FewParams& P, cudaStream_t s)
 {
-    if (out_in) {
-        // two outputs a block of eight warps: their parts of K are short enough, and there are blocks for
-        // every SM
-        few_rows_out_in_kernel<DT, ROWS, 2><<<(unsigned)div_up(P.N, 2), P.K > 1024 ? 256 : P.K > 512 ? 128 : 64, 0, s>>>(P);
-    } else {
-        few_rows_in_out_kernel<DT, ROWS><<<(unsigned)div_up(P.N, 64), 512, 0, s>>>(P);
-    }
-}
-
-template <int DT>
-void launch_few(const FewParams& P, bool out_in, cudaStream_t s)
-{
-    if (P.M == 1) launch_few<DT, 1>(P, out_in, s);
-    else if (P.M == 2) launch_few<DT, 2>(P, out_in, s);
-    else if (P.M <= 4) launch_few<DT, 4>(P, out_in, s);
-    else launch_few<DT, 8>(P, out_in, s);
+    // four outputs a block; as many warps as have 256 inner elements each, eight at most
+    const int warps = (int)std::min<int64_t>(8, std::max<int64_t>(1, div_up(P.K, 256)));
+    few_rows_kernel<DT, ROWS, 4><<<(unsigned)div_up(P.N, 4), 32 * warps, 0, s>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
 
 // ------------------------------------------------------------------ host: the layer
@@ -1159,7 +1088,7 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
     L->ld_x8 = a.ld_x;
     L->ld_w8 = a.ld_w;
     L->ld_dz = a.ld_dy;
-    L->few = !back && product_there && a.rows <= kFewRows;
+    L->few = !back && product_there && a.rows <= kFewRows && a.layout == ZERO_WEIGHT_OUT_IN;
     L->copy_x = product_there && use_x && !L->few && !tma_ready(a.x, a.ld_x);
     L->copy_w = product_there && use_w && !L->few && !tma_ready(a.w, a.ld_w);
     if (L->copy_x) {
@@ -1274,10 +1203,8 @@ try {
         P.K = (int32_t)a.in_features;
         P.vec_x = vec_flag(a.x, a.ld_x, 1);
         P.vec_w = vec_flag(a.w, a.ld_w, 1);
-        if (L.bf) launch_few<ZERO_BF16>(P, a.layout == ZERO_WEIGHT_OUT_IN, s);
-        else launch_few<ZERO_FP16>(P, a.layout == ZERO_WEIGHT_OUT_IN, s);
-        const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+        if (a.rows == 1) return L.bf ? launch_few<ZERO_BF16, 1>(P, s) : launch_few<ZERO_FP16, 1>(P, s);
+        return L.bf ? launch_few<ZERO_BF16, 2>(P, s) : launch_few<ZERO_FP16, 2>(P, s);
     }
     const Operand A{x, a.rows, a.in_features, L.ld_x8, false};
     const Operand B{w, a.out_features, a.in_features, L.ld_w8, a.layout == ZERO_WEIGHT_IN_OUT};
