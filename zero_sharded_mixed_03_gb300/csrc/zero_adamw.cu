@@ -62,6 +62,11 @@ struct AdamTensor {
 };
 static_assert(sizeof(AdamTensor) == 40, "AdamTensor layout");
 
+// How a block's g, p and 16-bit copy are accessed.  kAligned: it is whole and they start on 16 bytes.
+// kInner: it is whole and neither the tensor's first nor its last, so that the 4-byte words around its
+// ends are the tensor's too.  kSingly: element by element.
+enum { kSingly = 0, kAligned = 1, kInner = 2 };
+
 // One block of a tensor, as the kernels read it: 32 bytes for the 4 KB and more that the block moves.
 // (A table of tensors and one from blocks to tensors are smaller, but two reads one after the other.)
 struct alignas(16) AdamBlock {
@@ -69,7 +74,7 @@ struct alignas(16) AdamBlock {
     uint16_t* p16;
     const void* g;
     int32_t n;            // elements, 1 .. kBlockElems
-    int32_t vec;          // whole, and its pointers start on 16 bytes
+    int32_t vec;          // kAligned, kInner or kSingly
 };
 static_assert(sizeof(AdamBlock) == 32, "AdamBlock layout");
 
@@ -103,10 +108,9 @@ __device__ __forceinline__ float power_field(uint32_t e) { return __uint_as_floa
 
 // ---------------------------------------------------------------- a warp's block of one tensor
 
-// Which elements of its block a lane holds.  A whole block whose pointers start on 16 bytes: four in a
-// row from 4 lane on, and four from 128 + 4 lane on, so that 32 lanes' 16-byte accesses to fp32 values
-// cover 512 bytes without gaps (eight in a row leave half of every sector to a second access).  Else
-// every 32nd.
+// Which elements of its block a lane holds: four in a row from 4 lane on, and four from 128 + 4 lane on, so
+// that 32 lanes' 16-byte accesses to fp32 values cover 512 bytes without gaps (eight in a row leave half
+// of every sector to a second access).  In a kSingly block every 32nd.
 
 __device__ __forceinline__ AdamBlock block_at(const AdamParams& P, int b)
 {
@@ -127,7 +131,7 @@ __device__ __forceinline__ float load_grad1(const void* g, int64_t e)
 template <int GT>
 __device__ __forceinline__ void load_grads(const AdamBlock& B, int lane, float (&x)[8])
 {
-    if (B.vec) {
+    if (B.vec == kAligned) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if constexpr (GT == ZERO_FP32) {
@@ -171,7 +175,8 @@ template <int GT>
 struct Ring {
     static constexpr int kStages = kAhead + 1, kRecords = 2 * kAhead + 1;
     static constexpr int kG = GT == ZERO_FP32 ? 2 : 1;                              // a lane's pieces of g
-    static constexpr int kStage = kG * 512 + 1024 + 2 * kBlockElems;
+    static constexpr int kP = kG * 512 + 16, kM = kP + 1024;     // places of p and the moments
+    static constexpr int kStage = kM + 2 * kBlockElems;
     static constexpr int kWarp = kStages * kStage + kRecords * 32;
     static constexpr int kBytes = kAdamWarps * kWarp;
 };
@@ -179,6 +184,18 @@ struct Ring {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint32_t shared4(uint32_t at)
+{
+    uint32_t q;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(q) : "r"(at) : "memory");
+    return q;
 }
 
 __device__ __forceinline__ uint4 shared16(uint32_t at)
@@ -208,15 +225,27 @@ template <int GT>
 __device__ __forceinline__ void start_block(const AdamParams& P, const AdamBlock& B, int b, int lane, uint32_t stage)
 {
     using R = Ring<GT>;
-    if (!B.vec) return;
-    const uint32_t own = stage + lane * 16;
-    const char* g = static_cast<const char*>(B.g) + lane * 16;
-    const char* p = reinterpret_cast<const char*>(B.p) + lane * 16;
+    if (B.vec == kSingly) return;
+    if (B.vec == kAligned) {
+        const uint32_t own = stage + lane * 16;
+        const char* g = static_cast<const char*>(B.g) + lane * 16;
+        const char* p = reinterpret_cast<const char*>(B.p) + lane * 16;
 #pragma unroll
-    for (int i = 0; i < R::kG; ++i) copy16(own + i * 512, g + i * 512);
+        for (int i = 0; i < R::kG; ++i) copy16(own + i * 512, g + i * 512);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) copy16(own + R::kG * 512 + i * 512, p + i * 512);
-    const uint32_t moments = stage + R::kG * 512 + 1024;
+        for (int i = 0; i < 2; ++i) copy16(own + R::kP + i * 512, p + i * 512);
+    } else {
+        // words; 16-bit gradients that start in the middle of one take 129
+        const uint32_t own = stage + lane * 4, off = (uint32_t)(uintptr_t)B.g & 3u;
+        const char* g = static_cast<const char*>(B.g) - off + lane * 4;
+        const char* p = reinterpret_cast<const char*>(B.p) + lane * 4;
+#pragma unroll
+        for (int i = 0; i < 4 * R::kG; ++i) copy4(own + i * 128, g + i * 128);
+        if (off && lane == 0) copy4(own + 512, g + 512);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) copy4(own + R::kP + i * 128, p + i * 128);
+    }
+    const uint32_t moments = stage + R::kM;
     // m by the first half of the warp, v by the second
     const uint32_t half = lane >> 4, k = (lane & 15) * 16;
     const char* m = static_cast<const char*>(half ? P.v : P.m) + (int64_t)b * kBlockElems;
@@ -237,14 +266,19 @@ __device__ __forceinline__ void take_fp32(uint32_t at, int lane, float (&x)[8])
 }
 
 template <int GT>
-__device__ __forceinline__ void take_grads(uint32_t at, int lane, float (&x)[8])
+__device__ __forceinline__ void take_grads(const AdamBlock& B, uint32_t at, int lane, float (&x)[8])
 {
     if constexpr (GT == ZERO_FP32) {
         take_fp32(at, lane, x);
     } else {
+        const bool middle = B.vec == kInner && ((uint32_t)(uintptr_t)B.g & 2u);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint2 q = shared8(at + i * 256 + lane * 8);
+            uint2 q = shared8(at + i * 256 + lane * 8);
+            if (middle) {
+                const uint32_t last = shared4(at + i * 256 + lane * 8 + 8);
+                q = make_uint2(__byte_perm(q.x, q.y, 0x5432u), __byte_perm(q.y, last, 0x5432u));
+            }
             widen2<GT>(q.x, x[4 * i], x[4 * i + 1]);
             widen2<GT>(q.y, x[4 * i + 2], x[4 * i + 3]);
         }
@@ -254,8 +288,8 @@ __device__ __forceinline__ void take_grads(uint32_t at, int lane, float (&x)[8])
 __device__ __forceinline__ uint2 take_codes(uint32_t at, int lane)
 {
     uint2 c;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.x) : "r"(at + lane * 4) : "memory");
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c.y) : "r"(at + 128 + lane * 4) : "memory");
+    c.x = shared4(at + lane * 4);
+    c.y = shared4(at + 128 + lane * 4);
     return c;
 }
 
@@ -429,7 +463,8 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
                 B = next;
                 if (b + stride < P.n_blocks) next = block_at(P, b + stride);
             }
-            const bool vec = B.vec != 0;
+            // with the ring, inner blocks are read as aligned ones are
+            const bool vec = kRing ? B.vec != kSingly : B.vec == kAligned;
             float g[8], p[8], m[8], v[8];
             if (vec) {
                 if constexpr (!kRing) {
@@ -438,9 +473,9 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
                     load8(static_cast<const float*>(P.m) + s0, lane, m);
                     load8(static_cast<const float*>(P.v) + s0, lane, v);
                 } else {
-                    const uint32_t stage = mine + (k % R::kStages) * R::kStage, moments = stage + R::kG * 512 + 1024;
-                    take_grads<GT>(stage, lane, g);
-                    take_fp32(stage + R::kG * 512, lane, p);
+                    const uint32_t stage = mine + (k % R::kStages) * R::kStage, moments = stage + R::kM;
+                    take_grads<GT>(B, stage, lane, g);
+                    take_fp32(stage + R::kP, lane, p);
                     const F2 ms = both(power_field(scales & 0xFFu)), rs = both(power_field(scales >> 8) * 2.0f);
                     const uint2 mc = take_codes(moments, lane), vc = take_codes(moments + kBlockElems, lane);
 #pragma unroll
@@ -515,7 +550,32 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
                 p2 = add_apart(mul(minus_step, mul(m2, pair(reciprocal_approx(d0), reciprocal_approx(d1)))), p2, P.one);
                 split(p2, p[i], p[i + 1]);
             }
-            if (vec) {
+            if (kRing && B.vec == kInner) {
+                // through the stage: four in a row there, 32 lanes' neighbours to memory
+                const uint32_t stage = mine + (k % R::kStages) * R::kStage;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + R::kP + i * 512 + lane * 16), "f"(p[4 * i]),
+                                 "f"(p[4 * i + 1]), "f"(p[4 * i + 2]), "f"(p[4 * i + 3])
+                                 : "memory");
+                    if (B.p16)
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(stage + i * 256 + lane * 8),
+                                     "r"(narrow2<DT>(p[4 * i], p[4 * i + 1])), "r"(narrow2<DT>(p[4 * i + 2], p[4 * i + 3]))
+                                     : "memory");
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) B.p[j * 32 + lane] = __uint_as_float(shared4(stage + R::kP + j * 128 + lane * 4));
+                if (B.p16) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint16_t h;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(stage + j * 64 + lane * 2) : "memory");
+                        B.p16[j * 32 + lane] = h;
+                    }
+                }
+            } else if (vec) {
                 store8(B.p, lane, p);
                 if (B.p16) {
 #pragma unroll
@@ -632,11 +692,10 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
 {
     __shared__ double warp_sum[kAdamWarps];
     __shared__ bool last;
-    __shared__ uint32_t any_bad;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) any_bad = 0;
-    NormAcc acc;
-    bool bad = false;
+    // error-free sums (TwoSum, Knuth) of pairs of squares; a value that is not finite makes them so
+    F2 hi = both(0.0f), lo = both(0.0f);
+    const F2 inv = both(P.inv), minus = both(-1.0f);
     const int stride = gridDim.x * kAdamWarps;
     int b = blockIdx.x * kAdamWarps + (threadIdx.x >> 5);
     AdamBlock next = {};
@@ -648,18 +707,21 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
         b += stride;
         if (b < P.n_blocks) next = block_at(P, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float x = __fmul_rn(g[j], P.inv);
-            bad |= nonfinite(x);
-            acc.add(__fmul_rn(x, x));
+        for (int j = 0; j < 8; j += 2) {
+            const F2 x = mul(pair(g[j], g[j + 1]), inv), p = mul(x, x);
+            const F2 s = add_apart(p, hi, P.one);
+            const F2 bp = fma(hi, minus, s), ap = fma(bp, minus, s);
+            lo = add(lo, add(fma(ap, minus, hi), add_apart(p, fma(bp, minus, both(0.0f)), P.one)));
+            hi = s;
         }
     }
-    __syncthreads();
-    if (bad) any_bad = 1;
-    const double s = block_sum_fixed<kAdamThreads>(acc.value(), warp_sum);
+    float h0, h1, l0, l1;
+    split(hi, h0, h1);
+    split(lo, l0, l1);
+    const double mine = ((double)h0 + (double)h1) + ((double)l0 + (double)l1);
+    const double s = block_sum_fixed<kAdamThreads>(mine, warp_sum);
     if (threadIdx.x == 0) {
-        // a block's slot holds its sum, or not-a-number as the mark of a gradient that is not finite
-        P.partials[blockIdx.x] = any_bad ? __longlong_as_double(0x7FF8000000000000ll) : s;
+        P.partials[blockIdx.x] = s;
         __threadfence();
         last = atomicAdd(&P.st->norm_tickets, 1u) == gridDim.x - 1;
     }
@@ -673,7 +735,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     if (threadIdx.x == 0) {
         volatile AdamState* st = P.st;
         st->norm2 = sum;
-        st->flag = isnan(sum) ? 1u : 0u;
+        st->flag = isfinite(sum) ? 0u : 1u;
         st->norm_tickets = 0;
     }
 }
@@ -692,7 +754,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_table_kernel(const AdamTen
             B.p16 = T.p16 ? T.p16 + e : nullptr;
             B.g = static_cast<const char*>(T.g) + e * grad_bytes;
             B.n = (int32_t)min((int64_t)kBlockElems, T.n - e);
-            B.vec = T.vec && B.n == kBlockElems;
+            B.vec = B.n < kBlockElems ? kSingly : T.vec ? kAligned : k > 0 && k + 1 < count ? kInner : kSingly;
             blocks[T.first + k] = B;
         }
     }
