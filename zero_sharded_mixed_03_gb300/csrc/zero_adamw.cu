@@ -321,17 +321,26 @@ __device__ __forceinline__ void decode_root2(uint32_t two, F2 scale2, float& a, 
     split(mul(pair(f.x, f.y), scale2), a, b);
 }
 
-// inv_half = half of the scale's inverse.  Truncated to fp16, half a code added, truncated to the
-// code: to nearest, a tie upwards.  A root above 0 is at least code 1.
+// The power of two whose last place is x's fifth: x plus it, minus it, is x to four fraction bits (below
+// 2^-14, fp16's and the code's smallest normal number, to a multiple of 2^-18), to nearest, ties to even.
+__device__ __forceinline__ float rounder(float x)
+{
+    return __uint_as_float(max(__float_as_uint(x) & 0x7F800000u, 113u << 23) + (19u << 23));
+}
+
+// inv_half = half of the scale's inverse.  A root above 0 is at least code 1.
 __device__ __forceinline__ uint32_t encode_root2(float a, float b, F2 inv_half)
 {
     float x, y;
     split(mul(pair(a, b), inv_half), x, y);
     if (a > 0.0f) x = fmaxf(x, 0x1p-18f);
     if (b > 0.0f) y = fmaxf(y, 0x1p-18f);
+    const float rx = rounder(x), ry = rounder(y);
+    x = __fsub_rn(__fadd_rn(x, rx), rx);
+    y = __fsub_rn(__fadd_rn(y, ry), ry);
     uint32_t h;
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
-    return ((h + 0x00200020u) >> 6) & 0x00FF00FFu;
+    return (h >> 6) & 0x00FF00FFu;
 }
 
 // Whether one of four code bytes is 255, the mark of a root that is not finite.
@@ -539,10 +548,11 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
                 v2 = add_apart(mul(P.k[2], v2), mul(P.k[3], mul(gu, gu)), P.one);
                 split(m2, m[i], m[i + 1]);
                 split(v2, v[i], v[i + 1]);
-                // the root and the quotient within 2 units in the last place, on a step that is a small
+                // a root that is stored is rounded exactly, as its code has to follow from the values alone;
+                // else it is within 2 units in the last place, as the quotient is, on a step that is a small
                 // part of the parameter it is added to
-                root[i] = root_approx(v[i]);
-                root[i + 1] = root_approx(v[i + 1]);
+                root[i] = BITS == 8 ? __fsqrt_rn(v[i]) : root_approx(v[i]);
+                root[i + 1] = BITS == 8 ? __fsqrt_rn(v[i + 1]) : root_approx(v[i + 1]);
                 float d0, d1;
                 split(add_apart(mul(pair(root[i], root[i + 1]), inv_bc2s), P.k[4], P.one), d0, d1);
                 F2 p2 = pair(p[i], p[i + 1]);
