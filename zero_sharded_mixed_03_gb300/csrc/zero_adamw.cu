@@ -678,10 +678,10 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
         }
     }
     if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
-    // the last block to finish closes the step: every block has read t by then
+    // the last block to finish closes the step: every block has read t by then (and nothing else of
+    // theirs is read here, so that no store has to be waited for)
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();
         if (atomicAdd(&P.st->step_tickets, 1u) == gridDim.x - 1) {
             volatile AdamState* st = P.st;
             st->step_tickets = 0;

@@ -606,7 +606,18 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(int64_t M, int64_t N, co
 
 // ------------------------------------------------------------------ dz, and aligned copies
 
+// Rows copied to rows of `ld` elements that start on 16 bytes (src NULL: nothing to copy).
+struct AlignJob {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t ld_src, ld, rows, cols;
+};
+
+// What precedes the products, one launch: dz, and the copies of x and of w.
 struct DzParams {
+    AlignJob copy[2];
+    int32_t dz_blocks, across;   // blocks of the dz pass, and how many of them share rows
+    int32_t copy_blocks[2];
     const uint16_t* dy;
     const uint16_t* pre;     // NULL: the activation is none
     uint16_t* dz;            // rows of ld_dz elements, 16-byte aligned; NULL: only the sums
@@ -614,6 +625,23 @@ struct DzParams {
     int64_t rows, cols, ld_dy, ld_pre, ld_dz;
     int32_t act, vec_dy, vec_pre, chunk;   // chunk: consecutive rows a worker takes
 };
+
+// Block b of n, 256 threads: eight elements a thread at a time.
+__device__ __forceinline__ void align_rows(const AlignJob& J, int b, int n)
+{
+    const int64_t per_row = (J.cols + 7) / 8, total = J.rows * per_row;
+    for (int64_t i = (int64_t)b * 256 + threadIdx.y * blockDim.x + threadIdx.x; i < total; i += (int64_t)n * 256) {
+        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
+        const uint16_t* p = J.src + row * J.ld_src + col;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = col + 2 * j < J.cols ? p[2 * j] : 0u, hi = col + 2 * j + 1 < J.cols ? p[2 * j + 1] : 0u;
+            w[j] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint4*>(J.dst + row * J.ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
 
 // FLIGHT rows of a thread's eight columns; FULL: all eight are there, by 16-byte accesses.
 template <int DT, bool FULL, int FLIGHT>
@@ -667,9 +695,16 @@ template <int DT>
 __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzParams P)
 {
     constexpr int kFlight = 2;
-    const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    if ((int)blockIdx.x >= P.dz_blocks) {
+        const int b = blockIdx.x - P.dz_blocks;
+        const int which = b >= P.copy_blocks[0];
+        align_rows(P.copy[which], which ? b - P.copy_blocks[0] : b, P.copy_blocks[which]);
+        return;
+    }
+    const int by = blockIdx.x / P.across, bx = blockIdx.x - by * P.across;
+    const int64_t col = ((int64_t)bx * blockDim.x + threadIdx.x) * 8;
     const int n = (int)max((int64_t)0, min((int64_t)8, P.cols - col));
-    const int64_t worker = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
+    const int64_t worker = (int64_t)by * blockDim.y + threadIdx.y;
     const int64_t r1 = min(P.rows, (worker + 1) * P.chunk);
     int64_t r = worker * P.chunk;
     if (n == 0 || r >= r1) return;
@@ -707,24 +742,6 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* sums, int6
     for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
     if (accumulate) s += widen1<DT>(out[c]);
     out[c] = narrow1<DT>(s);
-}
-
-// Rows copied to rows of `ld` elements that start on 16 bytes.
-__global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld,
-                                                         int64_t rows, int64_t cols)
-{
-    const int64_t per_row = (cols + 7) / 8, total = rows * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-        const uint16_t* p = src + row * ld_src + col;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = col + 2 * j < cols ? p[2 * j] : 0u, hi = col + 2 * j + 1 < cols ? p[2 * j + 1] : 0u;
-            w[j] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint4*>(dst + row * ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
 }
 
 // ------------------------------------------------------------------ few rows
@@ -1133,10 +1150,32 @@ zero_status_t check_workspace(const Layer& L, const void* workspace, int64_t byt
 
 int vec_flag(const void* p, int64_t ld, int flag) { return p && aligned(p, 16) && ld % 8 == 0 ? flag : 0; }
 
-zero_status_t align_rows(const void* src, int64_t ld_src, void* dst, int64_t ld, int64_t rows, int64_t cols, cudaStream_t s)
+// The copies of x and w that the layer needs, into D; x and w become theirs.
+void plan_copies(const Layer& L, char* ws, const void** x, const void** w, DzParams* D)
 {
-    align_rows_kernel<<<grid_of(rows * div_up(cols, 8), kGb300Sms, 16), 256, 0, s>>>(
-        static_cast<const uint16_t*>(src), ld_src, static_cast<uint16_t*>(dst), ld, rows, cols);
+    std::memset(D, 0, sizeof(*D));
+    auto job = [&](int i, const void** p, int64_t ld_src, int64_t at, int64_t ld, int64_t rows, int64_t cols) {
+        AlignJob& J = D->copy[i];
+        J.src = static_cast<const uint16_t*>(*p);
+        J.dst = reinterpret_cast<uint16_t*>(ws + at);
+        J.ld_src = ld_src;
+        J.ld = ld;
+        J.rows = rows;
+        J.cols = cols;
+        D->copy_blocks[i] = grid_of(rows * div_up(cols, 8), kGb300Sms, 8);
+        *p = J.dst;
+    };
+    if (L.copy_x) job(0, x, L.a.ld_x, L.at_x, L.ld_x8, L.a.rows, L.a.in_features);
+    if (L.copy_w) job(1, w, L.a.ld_w, L.at_w, L.ld_w8, L.w_rows, L.w_cols);
+}
+
+zero_status_t launch_dz(const Layer& L, const DzParams& D, cudaStream_t s)
+{
+    const int64_t blocks = (int64_t)D.dz_blocks + D.copy_blocks[0] + D.copy_blocks[1];
+    if (blocks == 0) return ZERO_OK;
+    const dim3 threads(L.dz.tx, L.dz.ty);
+    if (L.bf) dz_kernel<ZERO_BF16><<<(unsigned)blocks, threads, 0, s>>>(D);
+    else dz_kernel<ZERO_FP16><<<(unsigned)blocks, threads, 0, s>>>(D);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
@@ -1171,15 +1210,12 @@ try {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const void *x = a.x, *w = a.w;
-    if (L.copy_x) {
-        st = align_rows(a.x, a.ld_x, ws + L.at_x, L.ld_x8, a.rows, a.in_features, s);
-        x = ws + L.at_x;
+    if (L.copy_x || L.copy_w) {
+        DzParams D;
+        plan_copies(L, ws, &x, &w, &D);
+        st = launch_dz(L, D, s);
+        if (st != ZERO_OK) return st;
     }
-    if (st == ZERO_OK && L.copy_w) {
-        st = align_rows(a.w, a.ld_w, ws + L.at_w, L.ld_w8, L.w_rows, L.w_cols, s);
-        w = ws + L.at_w;
-    }
-    if (st != ZERO_OK) return st;
     Epilogue E;
     E.out = static_cast<uint16_t*>(a.y);
     E.pre = static_cast<uint16_t*>(a.pre);
@@ -1225,18 +1261,10 @@ try {
     char* ws = static_cast<char*>(workspace);
     const bool accumulate = a.flags & ZERO_LINEAR_ACCUMULATE, any_out = a.rows > 0 && a.out_features > 0;
     const void *x = a.x, *w = a.w, *dz = a.dy;
-    if (L.copy_x) {
-        st = align_rows(a.x, a.ld_x, ws + L.at_x, L.ld_x8, a.rows, a.in_features, s);
-        x = ws + L.at_x;
-    }
-    if (st == ZERO_OK && L.copy_w) {
-        st = align_rows(a.w, a.ld_w, ws + L.at_w, L.ld_w8, L.w_rows, L.w_cols, s);
-        w = ws + L.at_w;
-    }
-    if (st != ZERO_OK) return st;
+    DzParams D;
+    plan_copies(L, ws, &x, &w, &D);
     float* sums = a.dbias && any_out ? reinterpret_cast<float*>(ws + L.at_sums) : nullptr;
     if (L.make_dz || sums) {
-        DzParams D;
         D.dy = static_cast<const uint16_t*>(a.dy);
         D.pre = a.activation != ZERO_ACT_NONE ? static_cast<const uint16_t*>(a.pre) : nullptr;
         D.dz = L.make_dz ? reinterpret_cast<uint16_t*>(ws + L.at_dz) : nullptr;
@@ -1250,12 +1278,12 @@ try {
         D.vec_dy = vec_flag(a.dy, a.ld_dy, 1);
         D.vec_pre = vec_flag(a.pre, a.ld_pre, 1);
         D.chunk = L.dz.chunk;
-        const dim3 grid((unsigned)div_up(a.out_features, (int64_t)L.dz.tx * 8), (unsigned)div_up(L.dz.workers, L.dz.ty));
-        const dim3 threads(L.dz.tx, L.dz.ty);
-        if (L.bf) dz_kernel<ZERO_BF16><<<grid, threads, 0, s>>>(D);
-        else dz_kernel<ZERO_FP16><<<grid, threads, 0, s>>>(D);
+        D.across = (int32_t)div_up(a.out_features, (int64_t)L.dz.tx * 8);
+        D.dz_blocks = (int32_t)(D.across * div_up(L.dz.workers, L.dz.ty));
         if (L.make_dz) dz = D.dz;
     }
+    st = launch_dz(L, D, s);
+    if (st != ZERO_OK) return st;
     if (a.dbias && a.out_features > 0 && !(a.rows == 0 && accumulate)) {
         const unsigned grid = (unsigned)div_up(a.out_features, 32);
         const dim3 threads(32, 8);
