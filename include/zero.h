@@ -616,8 +616,8 @@ zero_status_t zero_linear_workspace(const zero_linear_t* a, int backward, int64_
 /* Forward of one linear layer.  workspace: at least zero_linear_workspace bytes, 16-byte aligned
  * (NULL if that is 0); its contents need not survive between calls, but calls that may overlap
  * on the GPU need one each.  ZERO_EINVAL / ZERO_EALIGN / ZERO_ERANGE (a size beyond
- * ZERO_LINEAR_MAX_SIZE, or a workspace that is too small) before anything is enqueued.  rows == 0 does nothing;
- * in_features == 0 gives z = bias. */
+ * ZERO_LINEAR_MAX_SIZE, or a workspace that is too small) before anything is enqueued.  rows == 0
+ * does nothing; in_features == 0 gives z = bias. */
 zero_status_t zero_linear(const zero_linear_t* a, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Gradients of one linear layer (see zero_linear_t); at least one of dx, dw, dbias.  rows == 0
@@ -671,8 +671,8 @@ zero_status_t zero_block_norm_workspace(const zero_block_norm_t* a, int64_t* byt
 zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspace, int64_t workspace_bytes,
                                        void* stream);
 
-/* The only waits of the operators' kernels are on shared-memory barriers; each is bounded (2 s).
- * ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
+/* The only waits of the operators' kernels are on shared-memory barriers; each is bounded (at most
+ * 2 s).  ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
  * synchronises `stream`. */
 zero_status_t zero_operators_check(void* stream);
 
@@ -715,9 +715,8 @@ zero_status_t zero_adamw_bind(zero_adamw_t* h, float* const* params, void* const
  * the update uses the new moments before they are rounded. */
 zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double loss_scale, void* stream);
 
-/* The 8-bit moments as the values that they stand for, in bf16 (which holds each exactly; values
- * below its range of 2^-133 excepted), info.state_elems each, 16-byte aligned: m, and the root of
- * v. */
+/* The 8-bit moments as the values that they stand for, in bf16 (which holds each exactly, but for
+ * magnitudes below 2^-126), info.state_elems each, 16-byte aligned: m, and the root of v. */
 zero_status_t zero_adamw_export(zero_adamw_t* h, void* m_out, void* root_out, void* stream);
 
 /* t, skipped, skipped_total, finished and grad_norm (-1: none formed; not a number: skipped) after

@@ -1,9 +1,10 @@
 // zero_adamw.cu -- one AdamW step over many separately held tensors (zero_adamw_*), first and
 // second moments in 8 or 32 bits.
 //
-// The rule is the sharded step's (adamw1): every fp32 operation rounded by itself.  With 8-bit
-// moments each block of 256 elements of one tensor keeps two power-of-two scales, so that scaling
-// is exact and a stored moment is rounded once:
+// The rule is the sharded step's: the moments' operations are each rounded by themselves (their codes
+// hang on a last place, see below), the step's root and quotient are within 2 units in the last place.
+// With 8-bit moments each block of 256 elements of one tensor keeps two power-of-two scales, so that
+// scaling is exact and a stored moment is rounded once:
 //   m         e4m3 times 2^(em - 127), em = max(1, exponent field of the block's largest |m| - 7)
 //   sqrt(v)   an unsigned float of 4 exponent and 4 fraction bits (field 14 = [1, 2)) times
 //             2^(er - 127), er = the exponent field of the block's largest sqrt(v); code 255 is
@@ -15,6 +16,10 @@
 // Bytes per element: gradient 2 or 4, fp32 parameter 4 + 4, 16-bit copy 2, moments 2 + 2 (8 bits) or
 // 8 + 8 (32 bits): bound by HBM.  One warp takes one block of 256 elements, 8 to a lane in
 // registers, so that the block's new maxima are two warp reductions and nothing is read twice.
+// Measured on one GB300, a step after another: 124M elements, fp16 gradients, 8 bits 350 us (5.7 TB/s of the
+// 16 bytes an element), 59M elements, fp32 gradients, 32 bits 285 us (6.2 TB/s); 59M elements in 10,000
+// packed tensors, 8 bits, clipped: 32 us the norm, 230 the step.  Moving the values to bf16 for
+// adamw_export (6 bytes an element): 112 us of 124M.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -826,9 +831,9 @@ int64_t adam_workspace(const zero_adamw* h) { return slots_at(h) + 8 * kAdamNorm
 template <auto KERNEL, int SHARED = 0>
 int adam_grid(const zero_adamw* h)
 {
+    if constexpr (SHARED > 0) allow_shared<KERNEL>(SHARED);      // a refusal shows at the launch
     static const int per_sm = [] {
         int n = 0;
-        if (SHARED > 0) cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SHARED);
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, kAdamThreads, SHARED) == cudaSuccess ? std::max(1, n) : 1;
     }();
     const int64_t cap = (int64_t)std::max(1, device_sms(h->device)) * per_sm;

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <string>
@@ -36,6 +37,22 @@ inline int device_sms(int dev)
 inline zero_status_t cuda_fail(cudaError_t e, const char* what)
 {
     return fail(ZERO_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+// Allow a kernel `bytes` of dynamic shared memory (beyond 48 KB that takes a call) on the current
+// device, once a kernel and device.
+template <auto KERNEL>
+inline cudaError_t allow_shared(int bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load() & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
 }
 
 // Read and clear a kernel's error word (on a device variable), after the work on `s`.

