@@ -67,8 +67,16 @@ struct GemmParams {
 
 // ------------------------------------------------------------------ activations
 
-// The logistic function, accurate relative to its value in both tails.
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// The logistic function, accurate relative to its value in both tails (to 0 where 2^(-z log2 e)
+// overflows): one exponential and one reciprocal, each an instruction; the plain forms' care for
+// subnormal values costs twice as many and shows in nothing that has 16 bits.
+__device__ __forceinline__ float logistic(float z)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 
 // The tanh form of gelu is z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3), and gelu itself
 // z erfc(-z / sqrt 2) / 2: neither loses the left tail as 1 + tanh and 1 + erf do.
@@ -697,7 +705,7 @@ __device__ __forceinline__ void dz_rows(const DzParams& P, int64_t col, int n, i
 // dz = dy act'(pre), and its column sums: a thread takes eight columns of a worker's rows (blocks of up to
 // 2048 columns; narrower ones hold several workers), so that the sums need no exchange.
 template <int DT>
-__global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzParams P)
+__global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzParams P)
 {
     constexpr int kFlight = 2;
     if ((int)blockIdx.x >= P.dz_blocks) {
