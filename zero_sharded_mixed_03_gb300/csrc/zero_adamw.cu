@@ -395,6 +395,7 @@ __device__ __forceinline__ float root_approx(float v)
 template <int BITS, int GT, int DT>
 __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamPerSm32) adamw_kernel(const __grid_constant__ AdamParams P)
 {
+    after_earlier_work();
     __shared__ float sk_shared[4];
     __shared__ bool skip;
     using R = Ring<GT>;
@@ -705,6 +706,7 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
 template <int GT>
 __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamParams P)
 {
+    after_earlier_work();
     __shared__ double warp_sum[kAdamWarps];
     __shared__ bool last;
     const int lane = threadIdx.x & 31;
@@ -759,6 +761,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
 __global__ void __launch_bounds__(kAdamThreads) adamw_table_kernel(const AdamTensor* tensors, int64_t n, int grad_bytes,
                                                                    AdamBlock* blocks)
 {
+    after_earlier_work();
     for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
         const AdamTensor T = tensors[i];
         const int64_t count = (T.n + kBlockElems - 1) / kBlockElems;
@@ -780,6 +783,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_export_kernel(const uint8_
                                                                     const uint16_t* scales, uint16_t* m_out,
                                                                     uint16_t* root_out, int n_blocks)
 {
+    after_earlier_work();
     const int lane = threadIdx.x & 31, stride = gridDim.x * kAdamWarps;
     for (int b = blockIdx.x * kAdamWarps + (threadIdx.x >> 5); b < n_blocks; b += stride) {
         const int64_t at = (int64_t)b * kBlockElems + lane * 8;
@@ -846,9 +850,9 @@ void launch_adamw(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
 {
     constexpr int kShared = BITS == 8 ? Ring<GT>::kBytes : 0;
     if (h->dtype16 == ZERO_BF16)
-        adamw_kernel<BITS, GT, ZERO_BF16><<<adam_grid<adamw_kernel<BITS, GT, ZERO_BF16>, kShared>(h), kAdamThreads, kShared, s>>>(P);
+        launch_after(adamw_kernel<BITS, GT, ZERO_BF16>, adam_grid<adamw_kernel<BITS, GT, ZERO_BF16>, kShared>(h), kAdamThreads, kShared, s, P);
     else
-        adamw_kernel<BITS, GT, ZERO_FP16><<<adam_grid<adamw_kernel<BITS, GT, ZERO_FP16>, kShared>(h), kAdamThreads, kShared, s>>>(P);
+        launch_after(adamw_kernel<BITS, GT, ZERO_FP16>, adam_grid<adamw_kernel<BITS, GT, ZERO_FP16>, kShared>(h), kAdamThreads, kShared, s, P);
 }
 
 template <int BITS>
@@ -862,7 +866,7 @@ void launch_adamw(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
 template <int GT>
 void launch_norm(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
 {
-    adamw_norm_kernel<GT><<<adam_grid<adamw_norm_kernel<GT>>(h), kAdamThreads, 0, s>>>(P);
+    launch_after(adamw_norm_kernel<GT>, adam_grid<adamw_norm_kernel<GT>>(h), kAdamThreads, 0, s, P);
 }
 
 // The bound device has to be current: the launches go to it.
@@ -979,8 +983,7 @@ try {
                         cudaMemcpyHostToDevice, s);
     if (e == cudaSuccess && h->n_blocks > 0) {
         char* ws = static_cast<char*>(workspace);
-        adamw_table_kernel<<<(unsigned)std::min<int64_t>((int64_t)n, 4096), kAdamThreads, 0, s>>>(
-            reinterpret_cast<const AdamTensor*>(ws + tensors_at()), (int64_t)n, (int)gsize,
+        launch_after(adamw_table_kernel, (unsigned)std::min<int64_t>((int64_t)n, 4096), kAdamThreads, 0, s, reinterpret_cast<const AdamTensor*>(ws + tensors_at()), (int64_t)n, (int)gsize,
             reinterpret_cast<AdamBlock*>(ws + blocks_at(h)));
         e = cudaGetLastError();
     }
@@ -1062,8 +1065,7 @@ try {
     const zero_status_t ready = adam_ready(h, "zero_adamw_export");
     if (ready != ZERO_OK) return ready;
     if (h->n_blocks == 0) return ZERO_OK;
-    adamw_export_kernel<<<adam_grid<adamw_export_kernel>(h), kAdamThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint8_t*>(h->m), static_cast<const uint8_t*>(h->v), static_cast<const uint16_t*>(h->scales),
+    launch_after(adamw_export_kernel, adam_grid<adamw_export_kernel>(h), kAdamThreads, 0, static_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(h->m), static_cast<const uint8_t*>(h->v), static_cast<const uint16_t*>(h->scales),
         static_cast<uint16_t*>(m_out), static_cast<uint16_t*>(root_out), (int)h->n_blocks);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_adamw_export: launch");

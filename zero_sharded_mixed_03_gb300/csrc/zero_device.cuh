@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <mutex>
 #include <string>
+#include <utility>
 
 #include "zero_internal.h"
 
@@ -53,6 +54,32 @@ inline cudaError_t allow_shared(int bytes)
     e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.fetch_or(bit);
     return e;
+}
+
+// Launch a kernel that begins with after_earlier_work(): its blocks may be set up while the kernel before
+// it on the stream still runs (programmatic dependent launch), which hides most of a launch's latency.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 threads, size_t shared, cudaStream_t s, Args&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Nothing that an earlier kernel of the stream wrote may be read, and nothing that it reads written, before
+// this; every thread calls it.  The next launch is let in at once: its blocks wait in the same place.
+__device__ __forceinline__ void after_earlier_work()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Read and clear a kernel's error word (on a device variable), after the work on `s`.

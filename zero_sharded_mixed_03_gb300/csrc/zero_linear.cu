@@ -398,6 +398,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+    after_earlier_work();
 
     bool ok = true;
     if (warp == 0) {
@@ -578,6 +579,7 @@ struct TailParams {
 template <int DT>
 __global__ void __launch_bounds__(256) tail_sum_kernel(const __grid_constant__ TailParams P)
 {
+    after_earlier_work();
     const int lane = threadIdx.x & 31, in = blockIdx.x * 8 + (threadIdx.x >> 5);    // the row in its tile
     const int tail = gridDim.y, r = blockIdx.y;
     int m, n;
@@ -613,6 +615,7 @@ __global__ void __launch_bounds__(256) tail_sum_kernel(const __grid_constant__ T
 template <int DT>
 __global__ void __launch_bounds__(256) empty_sum_kernel(int64_t M, int64_t N, const __grid_constant__ Epilogue E)
 {
+    after_earlier_work();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * 256)
         finish1<DT>(E, i / N, i % N, 0.0f);
 }
@@ -707,6 +710,7 @@ __device__ __forceinline__ void dz_rows(const DzParams& P, int64_t col, int n, i
 template <int DT>
 __global__ void __launch_bounds__(256, 4) dz_kernel(const __grid_constant__ DzParams P)
 {
+    after_earlier_work();
     constexpr int kFlight = 2;
     if ((int)blockIdx.x >= P.dz_blocks) {
         const int b = blockIdx.x - P.dz_blocks;
@@ -740,6 +744,7 @@ template <int DT>
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* sums, int64_t ld, int64_t workers, int64_t cols,
                                                          uint16_t* out, int accumulate)
 {
+    after_earlier_work();
     __shared__ float part[8][33];
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
@@ -777,6 +782,7 @@ struct FewParams {
 template <int DT, int ROWS, int COLS>
 __global__ void __launch_bounds__(256) few_rows_kernel(const __grid_constant__ FewParams P)
 {
+    after_earlier_work();
     __shared__ float part[8][ROWS * COLS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t n0 = (int64_t)blockIdx.x * COLS;
@@ -952,7 +958,7 @@ zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
     if (set != cudaSuccess) return cuda_fail(set, "zero_linear: shared memory");
     const int64_t items = P.full + ((int64_t)P.tiles_m * P.tiles_n - P.full) * P.splits;
     const int grid = CG * (int)std::min<int64_t>(std::max(1, sms / CG), items);
-    gemm_kernel<CG, BN, DT><<<grid, kGemmThreads, S::kSmem, s>>>(P);
+    launch_after(gemm_kernel<CG, BN, DT>, grid, kGemmThreads, S::kSmem, s, P);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
@@ -967,8 +973,8 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     const bool bf = dtype16 == ZERO_BF16;
     if (K == 0) {
         const int grid = grid_of(M * N, sms, 8);
-        if (bf) empty_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(M, N, E);
-        else empty_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(M, N, E);
+        if (bf) launch_after(empty_sum_kernel<ZERO_BF16>, grid, 256, 0, s, M, N, E);
+        else launch_after(empty_sum_kernel<ZERO_FP16>, grid, 256, 0, s, M, N, E);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
     }
@@ -1012,8 +1018,8 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     T.bn = c.bn;
     T.rows_vec = P.rows_vec;
     const dim3 grid((unsigned)(T.tile_rows / 8), (unsigned)c.tail());
-    if (bf) tail_sum_kernel<ZERO_BF16><<<grid, 256, 0, s>>>(T);
-    else tail_sum_kernel<ZERO_FP16><<<grid, 256, 0, s>>>(T);
+    if (bf) launch_after(tail_sum_kernel<ZERO_BF16>, grid, 256, 0, s, T);
+    else launch_after(tail_sum_kernel<ZERO_FP16>, grid, 256, 0, s, T);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
@@ -1023,7 +1029,7 @@ zero_status_t launch_few(const FewParams& P, cudaStream_t s)
 {
     // four outputs a block; as many warps as have 256 inner elements each, eight at most
     const int warps = (int)std::min<int64_t>(8, std::max<int64_t>(1, div_up(P.K, 256)));
-    few_rows_kernel<DT, ROWS, 4><<<(unsigned)div_up(P.N, 4), 32 * warps, 0, s>>>(P);
+    launch_after(few_rows_kernel<DT, ROWS, 4>, (unsigned)div_up(P.N, 4), 32 * warps, 0, s, P);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
@@ -1186,8 +1192,8 @@ zero_status_t launch_dz(const Layer& L, const DzParams& D, cudaStream_t s)
     const int64_t blocks = (int64_t)D.dz_blocks + D.copy_blocks[0] + D.copy_blocks[1];
     if (blocks == 0) return ZERO_OK;
     const dim3 threads(L.dz.tx, L.dz.ty);
-    if (L.bf) dz_kernel<ZERO_BF16><<<(unsigned)blocks, threads, 0, s>>>(D);
-    else dz_kernel<ZERO_FP16><<<(unsigned)blocks, threads, 0, s>>>(D);
+    if (L.bf) launch_after(dz_kernel<ZERO_BF16>, (unsigned)blocks, threads, 0, s, D);
+    else launch_after(dz_kernel<ZERO_FP16>, (unsigned)blocks, threads, 0, s, D);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
@@ -1301,8 +1307,8 @@ try {
         const dim3 threads(32, 8);
         const int64_t workers = any_out ? L.dz.workers : 0;
         uint16_t* db = static_cast<uint16_t*>(a.dbias);
-        if (L.bf) column_sum_kernel<ZERO_BF16><<<grid, threads, 0, s>>>(sums, up(a.out_features, 8), workers, a.out_features, db, accumulate);
-        else column_sum_kernel<ZERO_FP16><<<grid, threads, 0, s>>>(sums, up(a.out_features, 8), workers, a.out_features, db, accumulate);
+        if (L.bf) launch_after(column_sum_kernel<ZERO_BF16>, grid, threads, 0, s, sums, up(a.out_features, 8), workers, a.out_features, db, accumulate);
+        else launch_after(column_sum_kernel<ZERO_FP16>, grid, threads, 0, s, sums, up(a.out_features, 8), workers, a.out_features, db, accumulate);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "zero_linear_backward: launch");

@@ -418,6 +418,7 @@ constexpr int pipe_bytes(int64_t dim, int arrays, int stages) { return 64 + stag
 template <int DT, int MODE, bool LAYER, int V, bool STAGED>
 __global__ void __launch_bounds__(V == 4 ? 256 : 512) block_norm_kernel(const __grid_constant__ NormParams P)
 {
+    after_earlier_work();
     __shared__ __align__(16) float area[2 * kSumArea];
     extern __shared__ __align__(128) unsigned char stages[];
     const int T = blockDim.x;
@@ -526,6 +527,7 @@ template <int DT, int MODE, bool LAYER, int V, bool SHARED, bool STAGED>
 __global__ void __launch_bounds__(V == 2 && !SHARED ? 256 : 512, V == 2 && !SHARED ? 2 : 1)
     block_norm_grad_kernel(const __grid_constant__ NormParams P)
 {
+    after_earlier_work();
     __shared__ __align__(16) float area[2 * kSumArea];
     extern __shared__ __align__(128) unsigned char stages[];
     constexpr bool BIAS = LAYER || SHARED;
@@ -778,6 +780,7 @@ struct SumParams {
 template <int DT, int C>
 __global__ void __launch_bounds__(256) block_norm_sum_kernel(const __grid_constant__ SumParams P)
 {
+    after_earlier_work();
     __shared__ float part[8][32 * C + 1];
     const int col = (blockIdx.x * 32 + threadIdx.x) * C, lane = threadIdx.y;
     const float* from;
@@ -1037,7 +1040,7 @@ zero_status_t launch(unsigned grid, dim3 threads, int64_t bytes, const NormParam
         const cudaError_t set = allow_shared<KERNEL>(kMostShared);
         if (set != cudaSuccess) return cuda_fail(set, "zero_block_norm: shared memory");
     }
-    KERNEL<<<grid, threads, (size_t)bytes, s>>>(P);
+    launch_after(KERNEL, grid, threads, (size_t)bytes, s, P);
     return ZERO_OK;
 }
 
@@ -1190,11 +1193,11 @@ try {
         const int cols = a.dim % 4 == 0 ? 128 : 32;
         const dim3 grid((unsigned)((a.dim + cols - 1) / cols), rows), threads(32, 8);
         if (cols == 128) {
-            if (bf) block_norm_sum_kernel<ZERO_BF16, 4><<<grid, threads, 0, s>>>(S);
-            else block_norm_sum_kernel<ZERO_FP16, 4><<<grid, threads, 0, s>>>(S);
+            if (bf) launch_after(block_norm_sum_kernel<ZERO_BF16, 4>, grid, threads, 0, s, S);
+            else launch_after(block_norm_sum_kernel<ZERO_FP16, 4>, grid, threads, 0, s, S);
         } else {
-            if (bf) block_norm_sum_kernel<ZERO_BF16, 1><<<grid, threads, 0, s>>>(S);
-            else block_norm_sum_kernel<ZERO_FP16, 1><<<grid, threads, 0, s>>>(S);
+            if (bf) launch_after(block_norm_sum_kernel<ZERO_BF16, 1>, grid, threads, 0, s, S);
+            else launch_after(block_norm_sum_kernel<ZERO_FP16, 1>, grid, threads, 0, s, S);
         }
     }
     const cudaError_t e = cudaGetLastError();
