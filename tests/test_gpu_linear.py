@@ -207,6 +207,23 @@ def test_few_rows(rows, layout):
     layer.check_backward()
 
 
+@pytest.mark.parametrize("rows", [1, 2])
+@pytest.mark.parametrize("layout", ["out_in", "in_out"])
+@pytest.mark.parametrize("inner,outer", [(8, 8), (8, 1000), (248, 72), (256, 1), (264, 24), (520, 3000), (1032, 6), (2056, 19464),
+                                         (2040, 8), (4104, 136), (8184, 2056), (30000, 64)])
+def test_one_and_two_rows(rows, layout, inner, outer):
+    """Parts of the inner dimension that end anywhere, columns and rows of the weight that do not fill a block."""
+    for dtype, pad in (("bf16", 0), ("fp16", 8)):
+        layer = Layer(rows, inner, outer, dtype=dtype, layout=layout, act="relu", whole=True, pad=pad, seed=inner + outer)
+        layer.check_forward(exact=True)
+        layer.x[-1, inner // 2] = float("inf")        # the last row's own, and no other's
+        first = layer.y[: rows - 1].clone()
+        call(layer.args, False)
+        assert torch.equal(layer.y[: rows - 1], first)
+        want = layer.matrix_w()[inner // 2] * float("inf")
+        assert torch.equal(layer.pre[-1].double().nan_to_num(0.0, 1.0, -1.0)[want != 0], want[want != 0].clamp(-1, 1).nan_to_num(0.0))
+
+
 def test_split_inner_dimension():
     """Few tiles over a long inner dimension, in each of the three products."""
     for shape in ((64, 16384, 128), (64, 128, 16384), (16384, 64, 128)):

@@ -59,19 +59,30 @@ inline cudaError_t allow_shared(int bytes)
 // Launch a kernel that begins with after_earlier_work(): its blocks may be set up while the kernel before
 // it on the stream still runs (programmatic dependent launch), which hides most of a launch's latency.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 threads, size_t shared, cudaStream_t s, Args&&... args)
+inline cudaError_t launch_clusters_after(void (*kernel)(KArgs...), dim3 cluster, dim3 grid, dim3 threads, size_t shared, cudaStream_t s, Args&&... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = shared;
     cfg.stream = s;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster.x;
+    attrs[1].val.clusterDim.y = cluster.y;
+    attrs[1].val.clusterDim.z = cluster.z;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The same without clusters, or with those that the kernel's __cluster_dims__ gives it.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 threads, size_t shared, cudaStream_t s, Args&&... args)
+{
+    return launch_clusters_after(kernel, dim3(1), grid, threads, shared, s, std::forward<Args>(args)...);
 }
 
 // Nothing that an earlier kernel of the stream wrote may be read, and nothing that it reads written, before

@@ -764,88 +764,197 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* sums, int6
 
 // ------------------------------------------------------------------ few rows
 //
-// Up to kFewRows rows of x and W stored (out, in): reading W is all there is.  fp32 products on the plain
-// cores straight from the loads, no tiles, one launch: for one row 2048 -> 8192 takes 11.4 us and 8192 ->
-// 2048 9.5, through tiles 14 and 15; for four rows the tiles' 14 are less than this kernel's 22.  W
-// stored (in, out) needs its partial sums exchanged between blocks: 12.8 and 19 us, tiles 14 and 15.
+// Up to kFewRows rows of x: reading W is all there is.  fp32 products on the plain cores straight from the
+// loads, no tiles and one launch, for operands on the 16-byte grid.  What it costs is not the arithmetic but
+// what stands between the loads: none is behind a branch, sums are joined once a warp, and blocks are as many
+// as run at one time.  Measured on one GB300 in a graph of such calls, W from HBM, one and two rows (tiles
+// need 12.8 us for the first two, 23.6 and 40 for the others):
+//   2048 -> 8192   (out, in) 7.3 and 7.7 us, (in, out) 8.2 and 9.4     (33.5 MB: 4.9 at the copy rate)
+//   8192 -> 2048             7.3 and 7.7               8.6 and 9.8
+//   4096 -> 11008            18.9 and 20.2            16.3 and 18.0
+//   2048 -> 50304            35.0 and 36.7            33.3 and 35.7
+// Four rows take 14 and 27 us for the first of them: the tiles' from three on.
+// (out, in): two loads of two rows a lane and four blocks an SM; four loads and three blocks 8.0 and 9.8 us,
+// eight loads of one row 9.2.  (in, out): 256 threads and two parts of K 8.2, four parts (more blocks than
+// run at one time) 10.4, blocks of 512 threads 10.3.
 constexpr int kFewRows = 2;
+constexpr int kFewWarps = 8, kFewCols = 2;            // (out, in): warps a block, rows of W a warp
+constexpr int kFewDeep = 8, kFewParts = 8;           // (in, out): warps a block, blocks a cluster at most
+constexpr int kFewResident = 3;                       // (in, out): blocks an SM
 
 struct FewParams {
     const uint16_t *x, *w;
     Epilogue epi;
     int64_t ld_x, ld_w;
-    int32_t M, N, K;
-    int32_t vec_x, vec_w;
+    int32_t M, N, K;   // K (and N where W is stored along it) in eights; rows of x and W start on 16 bytes
+    int32_t split;     // (out, in): warps along K
 };
 
-// W stored (out, in): a warp takes COLS rows of W and every `warps`-th 256 elements of them.
-template <int DT, int ROWS, int COLS>
-__global__ void __launch_bounds__(256) few_rows_kernel(const __grid_constant__ FewParams P)
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+
+// acc[m][c] += eight products of row m of x and row c of W, U times.  Loads first, none of them behind a
+// branch.
+template <int DT, int U, int ROWS, int C>
+__device__ __forceinline__ void few_eights(const uint16_t* const (&x)[ROWS], const uint16_t* const (&w)[C], int64_t k, int64_t step, F2 (&acc)[ROWS][C])
 {
-    after_earlier_work();
-    __shared__ float part[8][ROWS * COLS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t n0 = (int64_t)blockIdx.x * COLS;
-    F2 acc[ROWS][COLS];
+    uint4 wv[U][C], xv[U][ROWS];
 #pragma unroll
-    for (int m = 0; m < ROWS; ++m)
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) acc[m][c] = both(0.0f);
-    for (int64_t k = warp * 256 + lane * 8; k < P.K; k += warps * 256) {
-        const int n = (int)min((int64_t)8, P.K - k);
-        if (n == 8 && P.vec_w && P.vec_x) {
-            uint4 w[COLS], x[ROWS];
+        for (int c = 0; c < C; ++c) wv[u][c] = __ldcs(reinterpret_cast<const uint4*>(w[c] + k + u * step));
 #pragma unroll
-            for (int c = 0; c < COLS; ++c)
-                w[c] = n0 + c < P.N ? __ldcs(reinterpret_cast<const uint4*>(P.w + (n0 + c) * P.ld_w + k)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int m = 0; m < ROWS; ++m) x[m] = *reinterpret_cast<const uint4*>(P.x + m * P.ld_x + k);
-#pragma unroll
-            for (int m = 0; m < ROWS; ++m) {
-                const uint32_t xs[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) {
-                    const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a, b, e, f;
-                        widen2<DT>(xs[j], a, b);
-                        widen2<DT>(ws[j], e, f);
-                        acc[m][c] = fma(pair(a, b), pair(e, f), acc[m][c]);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                if (n0 + c >= P.N) break;
-                for (int j = 0; j < n; ++j) {
-                    const float w = widen1<DT>(P.w[(n0 + c) * P.ld_w + k + j]);
-#pragma unroll
-                    for (int m = 0; m < ROWS; ++m) acc[m][c] = fma(pair(widen1<DT>(P.x[m * P.ld_x + k + j]), 0.0f), pair(w, 0.0f), acc[m][c]);
-                }
-            }
-        }
+        for (int m = 0; m < ROWS; ++m) xv[u][m] = *reinterpret_cast<const uint4*>(x[m] + k + u * step);
     }
 #pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            F2 f[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float a, b;
+                widen2<DT>(word(wv[u][c], j), a, b);
+                f[c] = pair(a, b);
+            }
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                float a, b;
+                widen2<DT>(word(xv[u][m], j), a, b);
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[m][c] = fma(pair(a, b), f[c], acc[m][c]);
+            }
+        }
+}
+
+// W stored (out, in): a warp takes kFewCols rows of W and every `split`-th 256 elements of them.
+template <int DT, int ROWS>
+__global__ void __launch_bounds__(32 * kFewWarps, 4) few_rows_kernel(const __grid_constant__ FewParams P)
+{
+    constexpr int C = kFewCols, U = 2;
+    __shared__ float part[kFewWarps][ROWS * C];
+    after_earlier_work();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ways = P.split, sub = warp % ways;
+    const int64_t n0 = ((int64_t)blockIdx.x * (kFewWarps / ways) + warp / ways) * C;
+    const uint16_t *x[ROWS], *w[C];   // the last row again where there are fewer
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) x[m] = P.x + min(m, P.M - 1) * P.ld_x;
+#pragma unroll
+    for (int c = 0; c < C; ++c) w[c] = P.w + min(n0 + c, (int64_t)P.N - 1) * P.ld_w;
+    F2 acc[ROWS][C];
+#pragma unroll
     for (int m = 0; m < ROWS; ++m)
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
+        for (int c = 0; c < C; ++c) acc[m][c] = both(0.0f);
+    const int64_t step = ways * 256;
+    int64_t k = sub * 256 + lane * 8;
+    for (; k + (U - 1) * step < P.K; k += U * step) few_eights<DT, U, ROWS, C>(x, w, k, step, acc);
+    for (; k < P.K; k += step) few_eights<DT, 1, ROWS, C>(x, w, k, step, acc);
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
             float a, b;
             split(acc[m][c], a, b);
             a += b;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            if (lane == 0) part[warp][m * COLS + c] = a;
+            if (lane == 0) part[warp][m * C + c] = a;
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < ROWS * COLS; i += blockDim.x) {
-        const int m = i / COLS, c = i % COLS;
-        if (m >= P.M || n0 + c >= P.N) continue;
-        float z = 0.0f;
-        for (int w = 0; w < warps; ++w) z += part[w][i];
-        finish1<DT>(P.epi, m, n0 + c, z);
+    const int i = threadIdx.x;
+    if (i >= kFewWarps / ways * ROWS * C) return;
+    const int g = i / (ROWS * C), m = i % (ROWS * C) / C, c = i % C;
+    const int64_t n = ((int64_t)blockIdx.x * (kFewWarps / ways) + g) * C + c;
+    if (m >= P.M || n >= P.N) return;
+    float z = 0.0f;
+    for (int v = 0; v < ways; ++v) z += part[g * ways + v][m * C + c];
+    finish1<DT>(P.epi, m, n, z);
+}
+
+// W stored (in, out): a block takes 64 columns and one part of K, a thread eight columns and eight rows of W
+// at a time, so that its eight elements of x are one load; the blocks of a cluster are the parts, summed in
+// order.
+template <int DT, int ROWS>
+__global__ void __launch_bounds__(32 * kFewDeep, kFewResident) few_rows_deep_kernel(const __grid_constant__ FewParams P)
+{
+    __shared__ float part[kFewDeep][ROWS * 64];
+    __shared__ float whole[ROWS * 64];
+    after_earlier_work();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, across = (lane & 7) * 8;
+    // past the last column: that column's eight again
+    const uint16_t* w = P.w + min((int64_t)blockIdx.x * 64 + across, (int64_t)P.N - 8);
+    const int64_t per = (P.K / 8 + gridDim.y - 1) / gridDim.y * 8, end = min((int64_t)P.K, (blockIdx.y + 1) * per);
+    F2 acc[ROWS][4];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = both(0.0f);
+    for (int64_t k = blockIdx.y * per + warp * 32 + (lane >> 3) * 8; k < end; k += kFewDeep * 32) {
+        uint4 wv[8], xv[ROWS];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) wv[u] = __ldcs(reinterpret_cast<const uint4*>(w + (k + u) * P.ld_w));
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) xv[m] = *reinterpret_cast<const uint4*>(P.x + min(m, P.M - 1) * P.ld_x + k);
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+            F2 f[2][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float a, b;
+                widen2<DT>(word(wv[u + j / 4], j % 4), a, b);
+                f[j / 4][j % 4] = pair(a, b);
+            }
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                float a, b;
+                widen2<DT>(word(xv[m], u / 2), a, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = fma(both(a), f[0][j], acc[m][j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = fma(both(b), f[1][j], acc[m][j]);
+            }
+        }
     }
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split(acc[m][j], a, b);
+#pragma unroll
+            for (int o = 8; o < 32; o *= 2) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            if (lane < 8) {
+                part[warp][m * 64 + across + 2 * j] = a;
+                part[warp][m * 64 + across + 2 * j + 1] = b;
+            }
+        }
+    __syncthreads();
+    const int i = threadIdx.x, m = i / 64;
+    const int64_t col = (int64_t)blockIdx.x * 64 + i % 64;
+    const bool mine = i < ROWS * 64 && m < P.M && col < P.N;
+    float z = 0.0f;
+    if (mine) {
+#pragma unroll
+        for (int v = 0; v < kFewDeep; ++v) z += part[v][i];
+    }
+    if (gridDim.y > 1) {
+        if (mine) whole[i] = z;
+        cluster_sync();
+        if (mine && blockIdx.y == 0) {
+            for (uint32_t r = 1; r < gridDim.y; ++r) {
+                uint32_t at;
+                float v;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&whole[i])), "r"(r));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+                z += v;
+            }
+        }
+        cluster_sync();   // a block's shared memory outlives the reads of it
+    }
+    if (mine && blockIdx.y == 0) finish1<DT>(P.epi, m, col, z);
 }
 
 // ------------------------------------------------------------------ host: one product
@@ -1025,13 +1134,29 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
 }
 
 template <int DT, int ROWS>
-zero_status_t launch_few(const FewParams& P, cudaStream_t s)
+zero_status_t launch_few(FewParams P, bool in_out, cudaStream_t s)
 {
-    // four outputs a block; as many warps as have 256 inner elements each, eight at most
-    const int warps = (int)std::min<int64_t>(8, std::max<int64_t>(1, div_up(P.K, 256)));
-    launch_after(few_rows_kernel<DT, ROWS, 4>, (unsigned)div_up(P.N, 4), 32 * warps, 0, s, P);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (!in_out) {
+        // warps along K until there are sixteen an SM; each has at least 256 elements
+        const int64_t groups = div_up(P.N, kFewCols);
+        P.split = 1;
+        while (P.split < kFewWarps && groups * P.split < 16 * kGb300Sms && P.split * 256 < P.K) P.split *= 2;
+        e = launch_after(few_rows_kernel<DT, ROWS>, (unsigned)div_up(groups, kFewWarps / P.split), 32 * kFewWarps, 0, s, P);
+    } else {
+        // as many parts of K as are resident at one time; each has at least 128 rows of W
+        const int64_t blocks = div_up(P.N, 64);
+        int parts = 1;
+        while (parts < kFewParts && 2 * parts * blocks <= kFewResident * kGb300Sms && 256 * parts <= P.K) parts *= 2;
+        e = launch_clusters_after(few_rows_deep_kernel<DT, ROWS>, dim3(1, parts), dim3((unsigned)blocks, parts), 32 * kFewDeep, 0, s, P);
+    }
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
+}
+
+template <int DT>
+zero_status_t launch_few(const FewParams& P, bool in_out, cudaStream_t s)
+{
+    return P.M == 1 ? launch_few<DT, 1>(P, in_out, s) : launch_few<DT, 2>(P, in_out, s);
 }
 
 // ------------------------------------------------------------------ host: the layer
@@ -1123,7 +1248,8 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
     L->ld_x8 = a.ld_x;
     L->ld_w8 = a.ld_w;
     L->ld_dz = a.ld_dy;
-    L->few = !back && product_there && a.rows <= kFewRows && a.layout == ZERO_WEIGHT_OUT_IN;
+    L->few = !back && product_there && a.rows <= kFewRows && a.in_features % 8 == 0 && tma_ready(a.x, a.ld_x) && tma_ready(a.w, a.ld_w) &&
+             (a.layout == ZERO_WEIGHT_OUT_IN || a.out_features % 8 == 0);
     L->copy_x = product_there && use_x && !L->few && !tma_ready(a.x, a.ld_x);
     L->copy_w = product_there && use_w && !L->few && !tma_ready(a.w, a.ld_w);
     if (L->copy_x) {
@@ -1255,10 +1381,8 @@ try {
         P.M = (int32_t)a.rows;
         P.N = (int32_t)a.out_features;
         P.K = (int32_t)a.in_features;
-        P.vec_x = vec_flag(a.x, a.ld_x, 1);
-        P.vec_w = vec_flag(a.w, a.ld_w, 1);
-        if (a.rows == 1) return L.bf ? launch_few<ZERO_BF16, 1>(P, s) : launch_few<ZERO_FP16, 1>(P, s);
-        return L.bf ? launch_few<ZERO_BF16, 2>(P, s) : launch_few<ZERO_FP16, 2>(P, s);
+        const bool in_out = a.layout == ZERO_WEIGHT_IN_OUT;
+        return L.bf ? launch_few<ZERO_BF16>(P, in_out, s) : launch_few<ZERO_FP16>(P, in_out, s);
     }
     const Operand A{x, a.rows, a.in_features, L.ld_x8, false};
     const Operand B{w, a.out_features, a.in_features, L.ld_w8, a.layout == ZERO_WEIGHT_IN_OUT};
