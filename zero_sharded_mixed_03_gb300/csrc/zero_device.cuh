@@ -85,12 +85,19 @@ inline cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 thread
     return launch_clusters_after(kernel, dim3(1), grid, threads, shared, s, std::forward<Args>(args)...);
 }
 
-// Nothing that an earlier kernel of the stream wrote may be read, and nothing that it reads written, before
-// this; every thread calls it.  The next launch is let in at once: its blocks wait in the same place.
+// Every earlier kernel of the stream has ended and its writes are seen.
+__device__ __forceinline__ void wait_for_earlier_work() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The next launch may be set up once every block is here.
+__device__ __forceinline__ void let_next_launch_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// The first statement of a kernel that launch_after starts, for every thread: nothing that an earlier
+// kernel wrote may be read, and nothing that it reads written, before.  The wait comes first, so that a
+// kernel that is let in knows that all before its predecessor has ended.
 __device__ __forceinline__ void after_earlier_work()
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_earlier_work();
+    let_next_launch_in();
 }
 
 // Read and clear a kernel's error word (on a device variable), after the work on `s`.

@@ -62,6 +62,10 @@ struct GemmParams {
     int32_t a_rows;              // rows of A a copy brings (kBM, or fewer where A has no more)
     int32_t a_mn, b_mn;          // operand stored along its own rows (M or N) instead of along K
     int32_t rows_vec;            // the outputs and the residual allow 16-byte accesses
+    // Does not need the kernel just before it on the stream, but only what was before that: the blocks
+    // start at once, beside that kernel's last ones, and wait for its end before they leave, so that the
+    // end of this kernel is the end of both.
+    int32_t beside;
     uint32_t idesc;
 };
 
@@ -398,7 +402,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
-    after_earlier_work();
+    if (P.beside) let_next_launch_in();
+    else after_earlier_work();
 
     bool ok = true;
     if (warp == 0) {
@@ -566,6 +571,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
         else
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
     }
+    if (P.beside) wait_for_earlier_work();
 }
 
 // The partial sums of the split tiles, in order, with the epilogue.  A block takes 8 rows of a tile, a
@@ -1074,9 +1080,11 @@ zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
 
 inline int grid_of(int64_t items, int sms, int per_sm) { return (int)std::max<int64_t>(1, std::min<int64_t>(div_up(items, 256), (int64_t)sms * per_sm)); }
 
-// D = A B^T with epilogue E; `partial` holds partial_bytes.
-zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epilogue& E, float* partial, int sms, cudaStream_t s)
+// D = A B^T with epilogue E but for its split tiles, whose parts are left in `partial` (partial_bytes of
+// it) and described in T; sum_tail ends them.
+zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epilogue& E, float* partial, int sms, bool beside, TailParams* T, cudaStream_t s)
 {
+    T->splits = 1;
     const int64_t M = a.rows, N = b.rows, K = a.inner;
     if (M == 0 || N == 0) return ZERO_OK;
     const bool bf = dtype16 == ZERO_BF16;
@@ -1104,6 +1112,7 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     P.k_per_split = c.per_split;
     P.tiles_m = (int32_t)c.tiles_m;
     P.tiles_n = (int32_t)c.tiles_n;
+    P.beside = beside;
     P.a_mn = a.mn;
     P.b_mn = b.mn;
     P.rows_vec = (E.vec & kVecOut) && (!E.pre || (E.vec & kVecPre)) && (!E.residual || (E.vec & kVecRes));
@@ -1113,23 +1122,26 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     if (c.cg == 2) st = bf ? launch_shape<2, 256, ZERO_BF16>(P, sms, s) : launch_shape<2, 256, ZERO_FP16>(P, sms, s);
     else if (c.bn == 128) st = bf ? launch_shape<1, 128, ZERO_BF16>(P, sms, s) : launch_shape<1, 128, ZERO_FP16>(P, sms, s);
     else st = bf ? launch_shape<1, 64, ZERO_BF16>(P, sms, s) : launch_shape<1, 64, ZERO_FP16>(P, sms, s);
-    if (st != ZERO_OK || c.splits == 1) return st;
-    TailParams T;
-    T.partial = partial;
-    T.epi = E;
-    T.M = P.M;
-    T.N = P.N;
-    T.full = P.full;
-    T.splits = c.splits;
-    T.tiles_m = P.tiles_m;
-    T.tiles_n = P.tiles_n;
-    T.tile_rows = kBM * c.cg;
-    T.bn = c.bn;
-    T.rows_vec = P.rows_vec;
-    const dim3 grid((unsigned)(T.tile_rows / 8), (unsigned)c.tail());
-    if (bf) launch_after(tail_sum_kernel<ZERO_BF16>, grid, 256, 0, s, T);
-    else launch_after(tail_sum_kernel<ZERO_FP16>, grid, 256, 0, s, T);
-    const cudaError_t e = cudaGetLastError();
+    T->partial = partial;
+    T->epi = E;
+    T->M = P.M;
+    T->N = P.N;
+    T->full = P.full;
+    T->splits = c.splits;
+    T->tiles_m = P.tiles_m;
+    T->tiles_n = P.tiles_n;
+    T->tile_rows = kBM * c.cg;
+    T->bn = c.bn;
+    T->rows_vec = P.rows_vec;
+    return st;
+}
+
+zero_status_t sum_tail(const TailParams& T, int dtype16, cudaStream_t s)
+{
+    if (T.splits == 1) return ZERO_OK;
+    const dim3 grid((unsigned)(T.tile_rows / 8), (unsigned)(T.tiles_m * T.tiles_n - T.full));
+    const cudaError_t e = dtype16 == ZERO_BF16 ? launch_after(tail_sum_kernel<ZERO_BF16>, grid, 256, 0, s, T)
+                                               : launch_after(tail_sum_kernel<ZERO_FP16>, grid, 256, 0, s, T);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
 
@@ -1189,7 +1201,7 @@ struct Layer {
     int64_t w_rows = 0, w_cols = 0;        // as stored
     bool copy_x = false, copy_w = false, make_dz = false, few = false;
     int64_t ld_x8 = 0, ld_w8 = 0, ld_dz = 0;
-    int64_t at_x = 0, at_w = 0, at_dz = 0, at_sums = 0, at_partial = 0, bytes = 0;
+    int64_t at_x = 0, at_w = 0, at_dz = 0, at_sums = 0, at_partial = 0, at_partial_w = 0, bytes = 0;
     DzCut dz;
 };
 
@@ -1260,9 +1272,8 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
         L->ld_w8 = up(L->w_cols, 8);
         L->at_w = take(2 * L->w_rows * L->ld_w8);
     }
-    int64_t partial = 0;
     if (!back) {
-        if (product_there && !L->few) partial = partial_bytes(choose_cut(a.rows, a.out_features, a.in_features));
+        if (product_there && !L->few) L->at_partial = take(partial_bytes(choose_cut(a.rows, a.out_features, a.in_features)));
     } else {
         const bool products = product_there && (a.dx || a.dw);
         L->make_dz = products && (a.activation != ZERO_ACT_NONE || !tma_ready(a.dy, a.ld_dy));
@@ -1272,12 +1283,9 @@ zero_status_t lay_out(const zero_linear_t* in, bool back, Layer* L, const char* 
         }
         L->dz = dz_cut(a.rows, a.out_features);
         if (a.dbias && any_out) L->at_sums = take(4 * L->dz.workers * up(a.out_features, 8));
-        if (product_there && a.dx)
-            partial = std::max(partial, partial_bytes(choose_cut(a.rows, a.in_features, a.out_features)));
-        if (product_there && a.dw)
-            partial = std::max(partial, partial_bytes(choose_cut(L->w_rows, L->w_cols, a.rows)));
+        if (product_there && a.dx) L->at_partial = take(partial_bytes(choose_cut(a.rows, a.in_features, a.out_features)));
+        if (product_there && a.dw) L->at_partial_w = take(partial_bytes(choose_cut(L->w_rows, L->w_cols, a.rows)));
     }
-    L->at_partial = take(partial);
     L->bytes = at;
     return ZERO_OK;
 }
@@ -1386,7 +1394,9 @@ try {
     }
     const Operand A{x, a.rows, a.in_features, L.ld_x8, false};
     const Operand B{w, a.out_features, a.in_features, L.ld_w8, a.layout == ZERO_WEIGHT_IN_OUT};
-    return product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, s);
+    TailParams T;
+    st = product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, false, &T, s);
+    return st == ZERO_OK ? sum_tail(T, a.dtype16, s) : st;
 }
 catch (...) {
     return exception_status("zero_linear");
@@ -1426,7 +1436,11 @@ try {
     }
     st = launch_dz(L, D, s);
     if (st != ZERO_OK) return st;
+    // The column sums and dx need dz and not one another, nor does dw need them: each of these kernels starts
+    // beside the one before it.  Both products' split tiles are summed at the end.
+    bool beside = false;
     if (a.dbias && a.out_features > 0 && !(a.rows == 0 && accumulate)) {
+        beside = true;
         const unsigned grid = (unsigned)div_up(a.out_features, 32);
         const dim3 threads(32, 8);
         const int64_t workers = any_out ? L.dz.workers : 0;
@@ -1436,7 +1450,8 @@ try {
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "zero_linear_backward: launch");
-    float* partial = reinterpret_cast<float*>(ws + L.at_partial);
+    TailParams Tx, Tw;
+    Tx.splits = Tw.splits = 1;
     Epilogue E;
     std::memset(&E, 0, sizeof(E));
     E.act = ZERO_ACT_NONE;
@@ -1446,8 +1461,9 @@ try {
         E.vec = vec_flag(a.dx, a.ld_dx, kVecOut);
         const Operand A{dz, a.rows, a.out_features, L.ld_dz, false};
         const Operand B{w, a.in_features, a.out_features, L.ld_w8, a.layout == ZERO_WEIGHT_OUT_IN};
-        st = product(A, B, a.dtype16, E, partial, kGb300Sms, s);
+        st = product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, beside, &Tx, s);
         if (st != ZERO_OK) return st;
+        beside = true;
     }
     if (a.dw && !(a.rows == 0 && accumulate)) {
         E.out = static_cast<uint16_t*>(a.dw);
@@ -1456,10 +1472,12 @@ try {
         E.ld_res = a.ld_dw;
         E.vec = vec_flag(a.dw, a.ld_dw, kVecOut | kVecRes);
         const Operand X{x, a.in_features, a.rows, L.ld_x8, true}, Z{dz, a.out_features, a.rows, L.ld_dz, true};
-        if (a.layout == ZERO_WEIGHT_OUT_IN) st = product(Z, X, a.dtype16, E, partial, kGb300Sms, s);
-        else st = product(X, Z, a.dtype16, E, partial, kGb300Sms, s);
+        const bool out_in = a.layout == ZERO_WEIGHT_OUT_IN;
+        st = product(out_in ? Z : X, out_in ? X : Z, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial_w), kGb300Sms, beside, &Tw, s);
+        if (st != ZERO_OK) return st;
     }
-    return st;
+    st = sum_tail(Tx, a.dtype16, s);
+    return st == ZERO_OK ? sum_tail(Tw, a.dtype16, s) : st;
 }
 catch (...) {
     return exception_status("zero_linear_backward");
