@@ -771,56 +771,72 @@ struct SumParams {
     uint16_t* dgate;
     int64_t rows, ld_dgate, gate_rows, chunk, workers;
     int32_t dim;
-    int32_t by_group;          // gate sums: a block row a group, or a worker
+    int32_t by_group;          // gate sums: one place a group, or a worker
+    int32_t apart;             // kSumLanes places a block row, or one
 };
 
-// Block (column chunk, j): j < 4 adds the workers' sums of one weight; j >= 4 the parts of one gate
-// group that spans workers.  32 columns by 8 workers at a time, four columns a thread where dim
-// allows, in a fixed order.
+constexpr int kSumLanes = 16;
+
+// Block (column chunk, j): j < 4 adds the workers' sums of one weight, kSumLanes workers at a time; then come
+// the gate groups that span workers, kSumLanes a block (`apart`, where a group has no more workers than
+// that: one thread adds them in order) or one a block.  Four columns a thread where dim allows.  The order
+// is fixed.
 template <int DT, int C>
-__global__ void __launch_bounds__(256) block_norm_sum_kernel(const __grid_constant__ SumParams P)
+__global__ void __launch_bounds__(32 * kSumLanes) block_norm_sum_kernel(const __grid_constant__ SumParams P)
 {
     after_earlier_work();
-    __shared__ float part[8][32 * C + 1];
+    __shared__ float part[kSumLanes][32 * C + 1];
     const int col = (blockIdx.x * 32 + threadIdx.x) * C, lane = threadIdx.y;
     const float* from;
     int64_t w0, w1, stride;
-    uint16_t* out;
+    uint16_t* out = nullptr;
     bool later = false;        // the group starts after its first worker's first row: the second slot
-    if (blockIdx.y < 4) {
+    const bool weight = blockIdx.y < 4, apart = !weight && P.apart;
+    if (weight) {
         out = P.out[blockIdx.y];
-        if (!out) return;
         from = P.sums + (int64_t)blockIdx.y * P.dim;
         stride = 4 * P.dim;
         w0 = 0;
         w1 = P.workers - 1;
     } else {
-        if (!P.dgate) return;
-        const int64_t i = blockIdx.y - 4;
+        const int64_t i = apart ? (int64_t)(blockIdx.y - 4) * kSumLanes + lane : blockIdx.y - 4;
         const int64_t group = P.by_group ? i : (min(P.rows, (i + 1) * P.chunk) - 1) / P.gate_rows;
         const int64_t first = group * P.gate_rows, last = min(P.rows, first + P.gate_rows) - 1;
         w0 = first / P.chunk;
         w1 = last / P.chunk;
-        if (w0 == w1 || (!P.by_group && w0 != i)) return;      // whole in one worker, or another block's
-        out = P.dgate + group * P.ld_dgate;
+        // else it is whole in one worker, or another block's
+        if (P.dgate && first < P.rows && w0 != w1 && (P.by_group || w0 == i)) out = P.dgate + group * P.ld_dgate;
         from = P.gate_sums;
         stride = 2 * P.dim;
         later = first > w0 * P.chunk;
     }
+    if (!apart && !out) return;
     float s[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) s[c] = 0.0f;
-    if (col < P.dim) {
-#pragma unroll 8
-        for (int64_t w = w0 + lane; w <= w1; w += 8) {
-            const float* q = from + w * stride + (later && w == w0 ? P.dim : 0) + col;
+    if (col < P.dim && out) {
+        const int64_t step = apart ? 1 : kSumLanes;
+        auto add = [&](const float* q) {
             if constexpr (C == 4) {
                 const float4 f = *reinterpret_cast<const float4*>(q);
                 s[0] += f.x; s[1] += f.y; s[2] += f.z; s[3] += f.w;
             } else {
                 s[0] += *q;
             }
+        };
+        int64_t w = apart ? w0 : w0 + lane;
+        if (later && w == w0) {
+            add(from + w * stride + P.dim + col);
+            w += step;
         }
+#pragma unroll 8
+        for (; w <= w1; w += step) add(from + w * stride + col);
+    }
+    if (apart) {
+        if (col < P.dim && out)
+#pragma unroll
+            for (int c = 0; c < C; ++c) out[col + c] = narrow1<DT>(s[c]);
+        return;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) part[lane][threadIdx.x * C + c] = s[c];
@@ -829,7 +845,7 @@ __global__ void __launch_bounds__(256) block_norm_sum_kernel(const __grid_consta
     if (i < 32 * C && e < P.dim) {
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += part[k][i];
+        for (int k = 0; k < kSumLanes; ++k) sum += part[k][i];
         out[e] = narrow1<DT>(sum);
     }
 }
@@ -1189,9 +1205,12 @@ try {
         S.workers = C.cut.workers;
         S.dim = (int32_t)a.dim;
         S.by_group = C.groups <= C.cut.workers;
-        const unsigned rows = (unsigned)(4 + (gates ? std::min(C.groups, C.cut.workers) : 0));
+        // a group's workers: at most its rows in chunks, and one more
+        S.apart = (a.rows_per_gate + C.cut.chunk - 1) / C.cut.chunk + 1 <= kSumLanes;
+        const int64_t places = gates ? std::min(C.groups, C.cut.workers) : 0;
+        const unsigned rows = (unsigned)(4 + (S.apart ? (places + kSumLanes - 1) / kSumLanes : places));
         const int cols = a.dim % 4 == 0 ? 128 : 32;
-        const dim3 grid((unsigned)((a.dim + cols - 1) / cols), rows), threads(32, 8);
+        const dim3 grid((unsigned)((a.dim + cols - 1) / cols), rows), threads(32, kSumLanes);
         if (cols == 128) {
             if (bf) launch_after(block_norm_sum_kernel<ZERO_BF16, 4>, grid, threads, 0, s, S);
             else launch_after(block_norm_sum_kernel<ZERO_FP16, 4>, grid, threads, 0, s, S);
