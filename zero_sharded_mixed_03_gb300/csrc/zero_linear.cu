@@ -504,15 +504,30 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 }
                 __syncwarp();
                 if (I.part < 0 && !P.rows_vec) {
-                    // rows that do not start on 16 bytes: a column a lane, so that a warp writes neighbours
+                    // rows that do not start on 16 bytes: a column a lane, so that a warp writes neighbours;
+                    // eight rows at a time, as a store may not pass an earlier load of the residual
                     if (col0 + lane < P.N) {
                         const int rows = (int)min((int64_t)32, P.M - row0);
-#pragma unroll 4
-                        for (int r = 0; r < rows; ++r) {
-                            float z;
-                            const uint32_t at = stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(at) : "memory");
-                            finish1<DT>(P.epi, row0 + r, col0 + lane, z);
+                        const Epilogue& E = P.epi;
+                        const float bias = E.bias ? widen1<DT>(E.bias[col0 + lane]) : 0.0f;
+                        for (int r0 = 0; r0 < rows; r0 += 8) {
+                            float z[8], res[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                res[j] = E.residual && r0 + j < rows ? widen1<DT>(E.residual[(row0 + r0 + j) * E.ld_res + col0 + lane]) : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t at = stage + (r0 + j) * 128 + (((lane >> 2) ^ j) << 4) + (lane & 3) * 4;
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z[j]) : "r"(at) : "memory");
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (r0 + j >= rows) break;
+                                const int64_t row = row0 + r0 + j;
+                                z[j] += bias;
+                                if (E.pre) E.pre[row * E.ld_pre + col0 + lane] = narrow1<DT>(z[j]);
+                                E.out[row * E.ld_out + col0 + lane] = narrow1<DT>(act_value(z[j], E.act) + res[j]);
+                            }
                         }
                     }
                     __syncwarp();
