@@ -1010,7 +1010,8 @@ constexpr int kGb300Sms = 152;
 // 0.336 us, 94 % of the tensor cores' measured rate.  A 128 x 128 tile on one SM takes 0.29: the same
 // bytes for a quarter of the products (an SM takes 117 GB/s from L2, 64 bytes a clock).  It serves
 // where there are few rows or few tiles.  Split tiles write and read fp32 partial sums once (L2), in a
-// launch of their own.
+// launch of their own, 2.5 us as it is set up beside the product's (1024 rows, 4096 -> 1024: split 17.3 us,
+// whole 21.9; 512 rows, 2048 -> 2048 stay whole, 12.9).
 Cut choose_cut(int64_t M, int64_t N, int64_t K)
 {
     const int64_t kb = div_up(std::max<int64_t>(K, 1), kBK);
@@ -1038,7 +1039,7 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K)
             c.splits = (int)splits;
             c.per_split = (int)per;
             double us = div_up(c.full, slots) * kb * block_us;
-            if (splits > 1) us += div_up(c.tail() * splits, slots) * per * block_us + 3.5 + (double)(splits * 8 + 2) * c.tail() * c.tile_elems() / 8.0e6;
+            if (splits > 1) us += div_up(c.tail() * splits, slots) * per * block_us + 2.5 + (double)(splits * 8 + 2) * c.tail() * c.tile_elems() / 8.0e6;
             if (us < best_us) {
                 best_us = us;
                 best = c;
