@@ -87,19 +87,13 @@ inline cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 thread
     return launch_clusters_after(kernel, dim3(1), grid, threads, shared, s, std::forward<Args>(args)...);
 }
 
-// Every earlier kernel of the stream has ended and its writes are seen.
-__device__ __forceinline__ void wait_for_earlier_work() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// The next launch may be set up once every block is here.
-__device__ __forceinline__ void let_next_launch_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// The first statement of a kernel that launch_after starts, for every thread: nothing that an earlier
-// kernel wrote may be read, and nothing that it reads written, before.  The wait comes first, so that a
-// kernel that is let in knows that all before its predecessor has ended.
+// In every kernel that launch_after starts, by every thread, before any access to global memory: every earlier
+// kernel of the stream has ended and its writes are seen (PTX promises that to a kernel that waits itself, and
+// to no other); then the next launch may be set up once every block is here.
 __device__ __forceinline__ void after_earlier_work()
 {
-    wait_for_earlier_work();
-    let_next_launch_in();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Read and clear a kernel's error word (on a device variable), after the work on `s`.

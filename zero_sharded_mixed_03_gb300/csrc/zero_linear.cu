@@ -63,10 +63,6 @@ struct GemmParams {
     int32_t a_rows;              // rows of A a copy brings (kBM, or fewer where A has no more)
     int32_t a_mn, b_mn;          // operand stored along its own rows (M or N) instead of along K
     int32_t rows_vec;            // the outputs and the residual allow 16-byte accesses
-    // Does not need the kernel just before it on the stream, but only what was before that: the blocks
-    // start at once, beside that kernel's last ones, and wait for its end before they leave, so that the
-    // end of this kernel is the end of both.
-    int32_t beside;
     uint32_t idesc;
 };
 
@@ -403,8 +399,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
-    if (P.beside) let_next_launch_in();
-    else after_earlier_work();
+    after_earlier_work();
 
     bool ok = true;
     if (warp == 0) {
@@ -587,7 +582,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1)
         else
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
     }
-    if (P.beside) wait_for_earlier_work();
 }
 
 // The partial sums of the split tiles, in order, with the epilogue.  A block takes 8 rows of a tile, a
@@ -1099,7 +1093,7 @@ inline int grid_of(int64_t items, int sms, int per_sm) { return (int)std::max<in
 
 // D = A B^T with epilogue E but for its split tiles, whose parts are left in `partial` (partial_bytes of
 // it) and described in T; sum_tail ends them.
-zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epilogue& E, float* partial, int sms, bool beside, TailParams* T, cudaStream_t s)
+zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epilogue& E, float* partial, int sms, TailParams* T, cudaStream_t s)
 {
     T->splits = 1;
     const int64_t M = a.rows, N = b.rows, K = a.inner;
@@ -1129,7 +1123,6 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     P.k_per_split = c.per_split;
     P.tiles_m = (int32_t)c.tiles_m;
     P.tiles_n = (int32_t)c.tiles_n;
-    P.beside = beside;
     P.a_mn = a.mn;
     P.b_mn = b.mn;
     P.rows_vec = (E.vec & kVecOut) && (!E.pre || (E.vec & kVecPre)) && (!E.residual || (E.vec & kVecRes));
@@ -1413,7 +1406,7 @@ try {
     const Operand A{x, a.rows, a.in_features, L.ld_x8, false};
     const Operand B{w, a.out_features, a.in_features, L.ld_w8, a.layout == ZERO_WEIGHT_IN_OUT};
     TailParams T;
-    st = product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, false, &T, s);
+    st = product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, &T, s);
     return st == ZERO_OK ? sum_tail(T, a.dtype16, s) : st;
 }
 catch (...) {
@@ -1454,12 +1447,10 @@ try {
     }
     st = launch_dz(L, D, s);
     if (st != ZERO_OK) return st;
-    // The column sums and dx need dz and not one another, nor does dw need them: each of these kernels starts
-    // beside the one before it (777 x 1001 x 1603: 45 us, one after another 49; the largest products alike).
-    // Both products' split tiles are summed at the end.
-    bool beside = false;
+    // The column sums and dx need dz and not one another, nor does dw need them; but each waits for the one
+    // before it, as only a kernel's own wait makes what was written before the call, or by its first launch,
+    // visible to it.  Both products' split tiles are summed at the end.
     if (a.dbias && a.out_features > 0 && !(a.rows == 0 && accumulate)) {
-        beside = true;
         const unsigned grid = (unsigned)div_up(a.out_features, 32);
         const dim3 threads(32, 8);
         const int64_t workers = any_out ? L.dz.workers : 0;
@@ -1480,9 +1471,8 @@ try {
         E.vec = vec_flag(a.dx, a.ld_dx, kVecOut);
         const Operand A{dz, a.rows, a.out_features, L.ld_dz, false};
         const Operand B{w, a.in_features, a.out_features, L.ld_w8, a.layout == ZERO_WEIGHT_OUT_IN};
-        st = product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, beside, &Tx, s);
+        st = product(A, B, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial), kGb300Sms, &Tx, s);
         if (st != ZERO_OK) return st;
-        beside = true;
     }
     if (a.dw && !(a.rows == 0 && accumulate)) {
         E.out = static_cast<uint16_t*>(a.dw);
@@ -1492,7 +1482,7 @@ try {
         E.vec = vec_flag(a.dw, a.ld_dw, kVecOut | kVecRes);
         const Operand X{x, a.in_features, a.rows, L.ld_x8, true}, Z{dz, a.out_features, a.rows, L.ld_dz, true};
         const bool out_in = a.layout == ZERO_WEIGHT_OUT_IN;
-        st = product(out_in ? Z : X, out_in ? X : Z, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial_w), kGb300Sms, beside, &Tw, s);
+        st = product(out_in ? Z : X, out_in ? X : Z, a.dtype16, E, reinterpret_cast<float*>(ws + L.at_partial_w), kGb300Sms, &Tw, s);
         if (st != ZERO_OK) return st;
     }
     st = sum_tail(Tx, a.dtype16, s);
