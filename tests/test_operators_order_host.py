@@ -56,3 +56,16 @@ def test_the_next_launch_is_let_in_after_the_wait():
     assert re.findall(r"griddepcontrol\.\w+", text) == ["griddepcontrol.wait", "griddepcontrol.launch_dependents"]
     body = text[text.index("after_earlier_work"):]
     assert body.index("griddepcontrol.wait") < body.index("griddepcontrol.launch_dependents") < body.index("}")
+
+
+def test_constant_loads_are_of_constants():
+    """__ldg is for what no other kernel writes while this one lives, and it lives before the one ahead of it ends:
+    the optimizer's table of blocks is, as its bind waits; a norm's weights and a layer's operands are not."""
+    for name in FILES:
+        text = source(name)
+        found = [m.start() for m in re.finditer(r"__ldg|ld\.global\.nc|__restrict__", text)]
+        if name == "zero_adamw.cu":
+            at = text.index("AdamBlock block_at(")
+            assert all(at < f < text.index("}", at) for f in found)
+        else:
+            assert not found, name

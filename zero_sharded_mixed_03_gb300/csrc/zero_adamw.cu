@@ -117,6 +117,7 @@ __device__ __forceinline__ float power_field(uint32_t e) { return __uint_as_floa
 // that 32 lanes' 16-byte accesses to fp32 values cover 512 bytes without gaps (eight in a row leave half
 // of every sector to a second access).  In a kSingly block every 32nd.
 
+// The table is constant for a kernel's lifetime: zero_adamw_bind waits for the kernel that writes it.
 __device__ __forceinline__ AdamBlock block_at(const AdamParams& P, int b)
 {
     AdamBlock B;

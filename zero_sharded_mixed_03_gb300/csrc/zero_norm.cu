@@ -107,6 +107,8 @@ __device__ __forceinline__ F2 widen(uint32_t w)
     return pair(a, b);
 }
 
+// Plain loads: the kernel just before may be the one that writes the weights, and has not ended when this one
+// is launched, so that they are not constant for its lifetime (what __ldg asks for).
 template <int MODE, int V>
 __device__ __forceinline__ Raw<V> load_weight(const Weights& W, const Lane<MODE, V>& L)
 {
@@ -115,7 +117,7 @@ __device__ __forceinline__ Raw<V> load_weight(const Weights& W, const Lane<MODE,
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             uint4 q;
-            if (MODE == kEven || v < L.n) q = __ldg(reinterpret_cast<const uint4*>(W.p + (((v * L.T + L.tid) * 8) & W.mask)));
+            if (MODE == kEven || v < L.n) q = *reinterpret_cast<const uint4*>(W.p + (((v * L.T + L.tid) * 8) & W.mask));
             else q = make_uint4(0u, 0u, 0u, 0u);
             r.w[4 * v] = q.x; r.w[4 * v + 1] = q.y; r.w[4 * v + 2] = q.z; r.w[4 * v + 3] = q.w;
         }
