@@ -98,3 +98,13 @@ def test_values_that_are_not_finite_stay_in_their_rows(bad):
     n.run(False)
     rows = ~torch.isfinite(n.v["z"].float()).all(1)
     assert rows.nonzero().flatten().tolist() == [77, 4999]
+
+
+@pytest.mark.parametrize("rows_per_gate", [301, 1 << 60, (1 << 63) - 1])
+@pytest.mark.parametrize("layer", [False, True])
+def test_a_gate_row_for_more_rows_than_there_are(rows_per_gate, layer):
+    for rows, dim in ((1, 136), (300, 136), (300, 2048)):
+        n = Norm(rows, dim, layer=layer, gate_rows=rows)
+        n.args.rows_per_gate = rows_per_gate
+        n.check_forward()
+        n.check_backward()

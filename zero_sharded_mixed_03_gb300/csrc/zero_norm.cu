@@ -938,6 +938,8 @@ zero_status_t check_norm(const zero_block_norm_t* in, bool back, Checked* C, con
         return fail(ZERO_EINVAL, w + "bad eps or residual_scale");
     if (a.rows_per_gate < 0 || (a.rows > 0 && (a.rows_per_gate == 0) != (a.gate == nullptr)))
         return fail(ZERO_EINVAL, w + "a gate needs rows_per_gate >= 1, and none 0");
+    // more rows than there are: one gate row for all (rows that share one are added up below)
+    if (a.rows_per_gate > a.rows) a.rows_per_gate = std::max<int64_t>(1, a.rows);
     const bool pre = a.norms & ZERO_NORM_PRE, post = a.norms & ZERO_NORM_POST;
     C->groups = a.rows_per_gate ? (a.rows + a.rows_per_gate - 1) / a.rows_per_gate : 0;
     int64_t* lds[] = {&a.ld_h, &a.ld_x, &a.ld_y, &a.ld_z, &a.ld_gate, &a.ld_dy, &a.ld_dz, &a.ld_dx, &a.ld_dh, &a.ld_dgate};
