@@ -99,8 +99,10 @@ __device__ __forceinline__ float act_slope(float z, int act)
     switch (act) {
     case ZERO_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     case ZERO_ACT_GELU_TANH: {
+        // s (1 - s) first: it is 0 where the polynomial leaves fp32's range, and the square stays in it, so that
+        // finite numbers have finite slopes (in bf16 |z| goes to 3e38)
         const float s = logistic(gelu_arg(z));
-        return s * (1.0f + z * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z));
+        return s + s * (1.0f - s) * z * (1.5957691216057308f * (1.0f + 0.134145f * fminf(z * z, 1e30f)));
     }
     case ZERO_ACT_GELU:
         return 0.5f * erfcf(z * -0.7071067811865476f) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
