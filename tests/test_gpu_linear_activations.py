@@ -125,3 +125,28 @@ def test_not_a_number_stays_so(act):
     ws = torch.empty(max(16, size), dtype=torch.uint8, device="cuda")
     Z.zero_linear_backward(a, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(torch.isnan(db), torch.isnan(pre) if act != "none" else torch.zeros_like(db, dtype=torch.bool))
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,cols", [(1000, 264), (257, 101), (5, 4096)])
+def test_bias_gradients_sum_what_is_not_rounded(act, dtype, rows, cols):
+    """dbias adds dz in fp32, before the rounding that the products' operand takes: random signs leave a sum far below its
+    terms, of which that rounding would be 2^-8.  A term's fp32 part is 2^-17 of its magnitudes (arguments
+    below 2^5), the sum's rows + 64 roundings."""
+    t, kind, u16, _ = DTYPES[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    pre, dy = (torch.randn(rows, cols, generator=gen, device="cuda").to(t) for _ in range(2))
+    pre[:, 0] = pre[:, 0].sign() * 3                       # a column whose slopes are alike, with signs in turn
+    dy[:, 0] = 1 - 2.0 * (torch.arange(rows, device="cuda") % 2).to(t)
+    db = torch.empty(cols, dtype=t, device="cuda")
+    a = Z.zero_linear_t(rows=rows, in_features=8, out_features=cols, dtype16=kind, layout=Z.ZERO_WEIGHT_OUT_IN, activation=ACTS[act],
+                        pre=pre.data_ptr(), dy=dy.data_ptr(), dbias=db.data_ptr())
+    size = Z.zero_linear_workspace(a, True)
+    ws = torch.empty(max(16, size), dtype=torch.uint8, device="cuda")
+    Z.zero_linear_backward(a, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    _, slope, magnitude = value64(pre.double(), act)
+    want, mag = (dy.double() * slope).sum(0), (dy.double().abs() * magnitude).sum(0)
+    bound = (2.0 ** -17 + (rows + 64) * 2.0 ** -24) * mag + u16 * want.abs() + 2.0 ** -25
+    off = (db.double() - want).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
