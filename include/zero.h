@@ -715,6 +715,24 @@ zero_status_t zero_adamw_bind(zero_adamw_t* h, float* const* params, void* const
  * the update uses the new moments before they are rounded. */
 zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double loss_scale, void* stream);
 
+/* A step that h makes together with a plan's, applied or left out as one, with one loss scale and one
+ * norm: for a model of which the plan holds the sharded part and h the rest.  In the plan's step, on its
+ * stream, with hyper->max_grad_norm as in its zero_step calls:
+ *   zero_grad_norm of every bucket/unit        (a clipping step only)
+ *   zero_adamw_check
+ *   zero_step of every bucket/unit
+ *   zero_adamw_step_with
+ *   zero_step_finish
+ * zero_adamw_check reads h's gradients over the plan's loss scale and adds their sum of squares to the plan's norm,
+ * where that is formed; a sum that is not finite marks the plan's step, which is then skipped whole (and its loss
+ * scale backed off) as for a gradient of the plan's that is not.  It may come later, but before
+ * zero_adamw_step_with, in a step that neither clips nor is offloaded.  zero_adamw_step_with applies h's update, gradients over the plan's
+ * loss scale and times its clipping coefficient, unless the plan's step is marked or a bounded wait of it ran out.
+ * zero_adamw_read: grad_norm is -1, the plan's result has the norm of both.  ZERO_ESTATE out of this order.  Not
+ * with zero_step_units_overlapped, which finishes the step itself. */
+zero_status_t zero_adamw_check(zero_adamw_t* h, zero_plan_t* plan, void* stream);
+zero_status_t zero_adamw_step_with(zero_adamw_t* h, zero_plan_t* plan, const zero_hyper_t* hyper, void* stream);
+
 /* The 8-bit moments as the values that they stand for, in bf16 (which holds each exactly, but for
  * magnitudes below 2^-126), info.state_elems each, 16-byte aligned: m, and the root of v. */
 zero_status_t zero_adamw_export(zero_adamw_t* h, void* m_out, void* root_out, void* stream);

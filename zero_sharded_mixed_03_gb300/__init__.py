@@ -52,7 +52,7 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_linear_workspace", "zero_linear", "zero_linear_backward", "zero_operators_check",
             "zero_block_norm", "zero_block_norm_workspace", "zero_block_norm_backward",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
-            "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
+            "zero_adamw_check", "zero_adamw_step_with", "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
 ZERO_NOALLOC_SCRATCH_BYTES = 256
 
 
@@ -234,10 +234,12 @@ def lib() -> ctypes.CDLL:
         L.zero_adamw_info.argtypes = [_vp, ctypes.POINTER(zero_adamw_info_t)]
         L.zero_adamw_bind.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
         L.zero_adamw_step.argtypes = [_vp, ctypes.POINTER(zero_hyper_t), ctypes.c_double, _vp]
+        L.zero_adamw_check.argtypes = [_vp, _vp, _vp]
+        L.zero_adamw_step_with.argtypes = [_vp, _vp, ctypes.POINTER(zero_hyper_t), _vp]
         L.zero_adamw_export.argtypes = [_vp, _vp, _vp, _vp]
         L.zero_adamw_read.argtypes = [_vp, _vp, ctypes.POINTER(zero_step_result_t)]
         for f in (L.zero_adamw_create, L.zero_adamw_info, L.zero_adamw_bind, L.zero_adamw_step,
-                  L.zero_adamw_export, L.zero_adamw_read):
+                  L.zero_adamw_check, L.zero_adamw_step_with, L.zero_adamw_export, L.zero_adamw_read):
             f.restype = st
         L.zero_adamw_destroy.restype = None
         L.zero_adamw_destroy.argtypes = [_vp]
@@ -546,6 +548,16 @@ def zero_adamw_bind(handle: int, params: Sequence[int], params16: Optional[Seque
 
 def zero_adamw_step(handle: int, hyper: zero_hyper_t, loss_scale: float = 1.0, stream: int = 0) -> None:
     _check(lib().zero_adamw_step(handle, ctypes.byref(hyper), loss_scale, stream or None))
+
+
+def zero_adamw_check(handle: int, plan: int, stream: int = 0) -> None:
+    """Make the optimizer's gradients part of the plan's step: its skip decision and its norm."""
+    _check(lib().zero_adamw_check(handle, plan, stream or None))
+
+
+def zero_adamw_step_with(handle: int, plan: int, hyper: zero_hyper_t, stream: int = 0) -> None:
+    """The optimizer's part of the plan's open step, before its finish; see include/zero.h."""
+    _check(lib().zero_adamw_step_with(handle, plan, ctypes.byref(hyper), stream or None))
 
 
 def zero_adamw_export(handle: int, m_out: int, root_out: int, stream: int = 0) -> None:

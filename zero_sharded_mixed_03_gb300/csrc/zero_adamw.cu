@@ -92,6 +92,8 @@ struct AdamParams {
     double* partials;          // norm pass: one slot a launched block
     int32_t n_blocks;
     int32_t checked;           // a norm pass of this step ran: skip on its flag, clip by its norm
+    DevState* plan;            // a sharded step that this one belongs to: skip on its flag, clip by its
+                               // norm, unscale by its loss scale; or NULL
     F2 k[6];                   // b1, 1-b1, b2, 1-b2, eps, -lr*wd, each twice
     F2 one;                    // 1 (add_apart)
     float inv;                 // 1 / loss scale
@@ -393,6 +395,12 @@ __device__ __forceinline__ float root_approx(float v)
 
 // ---------------------------------------------------------------- kernels
 
+// fp32(1 / loss scale), as the sharded step forms it.
+__device__ __forceinline__ float unscale(const volatile DevState* plan)
+{
+    return __double2float_rn(__ddiv_rn(1.0, plan->scale));
+}
+
 template <int BITS, int GT, int DT>
 __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamPerSm32) adamw_kernel(const __grid_constant__ AdamParams P)
 {
@@ -434,19 +442,24 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
         const double bc = 1.0 - pow_int(lane == 0 ? P.beta1 : P.beta2, t);
         if (lane == 0) {
             sk_shared[0] = __double2float_rn(__ddiv_rn(P.lr, bc));
-            float coef = 1.0f;
+            const volatile DevState* plan = P.plan;
+            float coef = 1.0f, inv = P.inv;
             bool s = false;
-            if (P.checked) {
+            if (plan) {
+                s = (plan->flag | plan->error) != 0;
+                inv = unscale(plan);
+            } else if (P.checked) {
                 s = st->flag != 0;
-                if (P.max_norm > 0.0) {
-                    const double c = __ddiv_rn(P.max_norm, __dadd_rn(__dsqrt_rn(st->norm2), 1e-6));
-                    coef = __double2float_rn(c > 1.0 ? 1.0 : c);
-                }
+            }
+            if (P.max_norm > 0.0) {
+                const double norm2 = plan ? plan->norm2 : st->norm2;
+                const double c = __ddiv_rn(P.max_norm, __dadd_rn(__dsqrt_rn(norm2), 1e-6));
+                coef = __double2float_rn(c > 1.0 ? 1.0 : c);
             }
             // the gradient is multiplied by 1 / loss scale, then by the clipping coefficient; where
             // one of them is 1 that is one product
-            const bool one = P.inv == 1.0f || coef == 1.0f;
-            sk_shared[2] = one ? P.inv * coef : P.inv;
+            const bool one = inv == 1.0f || coef == 1.0f;
+            sk_shared[2] = one ? inv * coef : inv;
             sk_shared[3] = one ? 1.0f : coef;
             skip = s;
         } else if (lane == 1) {
@@ -703,8 +716,9 @@ __global__ void __launch_bounds__(kAdamThreads, BITS == 8 ? kAdamPerSm8 : kAdamP
 }
 
 // The sum of squares of the unscaled gradient and whether all of it is finite.  The order of the
-// sum is fixed: lanes, then warps, then blocks in order.
-template <int GT>
+// sum is fixed: lanes, then warps, then blocks in order.  JOINED: both go to a sharded step's state, to what its
+// own passes have found.
+template <int GT, bool JOINED>
 __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamParams P)
 {
     after_earlier_work();
@@ -713,7 +727,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     const int lane = threadIdx.x & 31;
     // error-free sums (TwoSum, Knuth) of pairs of squares; a value that is not finite makes them so
     F2 hi = both(0.0f), lo = both(0.0f);
-    const F2 inv = both(P.inv), minus = both(-1.0f);
+    const F2 inv = both(JOINED ? unscale(P.plan) : P.inv), minus = both(-1.0f);
     const int stride = gridDim.x * kAdamWarps;
     int b = blockIdx.x * kAdamWarps + (threadIdx.x >> 5);
     AdamBlock next = {};
@@ -752,8 +766,14 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     const double sum = block_sum_fixed<kAdamThreads>(x, warp_sum);
     if (threadIdx.x == 0) {
         volatile AdamState* st = P.st;
-        st->norm2 = sum;
-        st->flag = isfinite(sum) ? 0u : 1u;
+        if constexpr (JOINED) {
+            volatile DevState* plan = P.plan;
+            plan->norm2 = plan->norm2 + sum;
+            if (!isfinite(sum)) plan->flag = 1u;
+        } else {
+            st->norm2 = sum;
+            st->flag = isfinite(sum) ? 0u : 1u;
+        }
         st->norm_tickets = 0;
     }
 }
@@ -819,6 +839,8 @@ struct zero_adamw {
     bool bound = false;
     int device = -1;
     void *m = nullptr, *v = nullptr, *scales = nullptr, *workspace = nullptr;
+    // the sharded step (zero_plan::step_no) that zero_adamw_check, zero_adamw_step_with joined last
+    int64_t checked_in = 0, stepped_in = 0;
 };
 
 namespace zero {
@@ -864,10 +886,77 @@ void launch_adamw(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
     else launch_adamw<BITS, ZERO_FP32>(h, P, s);
 }
 
-template <int GT>
+template <int GT, bool JOINED>
 void launch_norm(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
 {
-    launch_after(adamw_norm_kernel<GT>, adam_grid<adamw_norm_kernel<GT>>(h), kAdamThreads, 0, s, P);
+    launch_after(adamw_norm_kernel<GT, JOINED>, adam_grid<adamw_norm_kernel<GT, JOINED>>(h), kAdamThreads, 0, s, P);
+}
+
+template <bool JOINED>
+void launch_norm(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
+{
+    if (h->grad_type == ZERO_BF16) launch_norm<ZERO_BF16, JOINED>(h, P, s);
+    else if (h->grad_type == ZERO_FP16) launch_norm<ZERO_FP16, JOINED>(h, P, s);
+    else launch_norm<ZERO_FP32, JOINED>(h, P, s);
+}
+
+F2 twice(float x)
+{
+    uint32_t w;
+    std::memcpy(&w, &x, 4);
+    return F2{((unsigned long long)w << 32) | w};
+}
+
+// What every pass over the bound tensors needs.
+AdamParams adam_params(const zero_adamw* h)
+{
+    char* ws = static_cast<char*>(h->workspace);
+    AdamParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.blocks = reinterpret_cast<const AdamBlock*>(ws + blocks_at(h));
+    P.m = h->m;
+    P.v = h->v;
+    P.scales = static_cast<uint16_t*>(h->scales);
+    P.st = reinterpret_cast<AdamState*>(ws);
+    P.partials = reinterpret_cast<double*>(ws + slots_at(h));
+    P.n_blocks = (int32_t)h->n_blocks;
+    P.one = twice(1.0f);
+    P.inv = 1.0f;
+    return P;
+}
+
+zero_status_t check_hyper(const zero_hyper_t* hyper, const char* who)
+{
+    const std::string w = std::string(who) + ": ";
+    if (!(hyper->beta1 >= 0.0 && hyper->beta1 < 1.0) || !(hyper->beta2 >= 0.0 && hyper->beta2 < 1.0))
+        return fail(ZERO_EINVAL, w + "betas must be in [0, 1)");
+    if (!(hyper->eps >= 0.0) || !(hyper->max_grad_norm >= 0.0) || !std::isfinite(hyper->lr) ||
+        !std::isfinite(hyper->weight_decay))
+        return fail(ZERO_EINVAL, w + "bad hyperparameter");
+    if (hyper->flags & ~(int64_t)ZERO_REPORT_GRAD_NORM) return fail(ZERO_EINVAL, w + "unknown flag");
+    return ZERO_OK;
+}
+
+// The step's constants into P.
+void set_hyper(AdamParams& P, const zero_hyper_t& hyper, double loss_scale)
+{
+    float c[9];
+    step_constants(hyper, 1, loss_scale, 1, c);
+    // eps: the smallest normal number at least, so that its reciprocal is finite
+    if (c[4] > 0.0f && c[4] < 0x1p-126f) c[4] = 0x1p-126f;
+    c[5] = -c[5];
+    for (int i = 0; i < 6; ++i) P.k[i] = twice(c[i]);
+    P.inv = c[8];
+    P.lr = hyper.lr;
+    P.beta1 = hyper.beta1;
+    P.beta2 = hyper.beta2;
+    P.max_norm = hyper.max_grad_norm;
+}
+
+void launch_adamw(const zero_adamw* h, const AdamParams& P, cudaStream_t s)
+{
+    if (h->bits == 8) launch_adamw<8>(h, P, s);
+    else launch_adamw<32>(h, P, s);
 }
 
 // The bound device has to be current: the launches go to it.
@@ -879,6 +968,17 @@ zero_status_t adam_ready(const zero_adamw* h, const char* who)
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, who);
     if (dev != h->device) return fail(ZERO_EINVAL, std::string(who) + ": the bound buffers live on another device");
+    return ZERO_OK;
+}
+
+// The plan whose step h joins: bound, on h's device.
+zero_status_t plan_ready(const zero_adamw* h, const zero_plan* plan, const char* who)
+{
+    if (!h || !plan) return fail(ZERO_EINVAL, std::string(who) + ": NULL argument");
+    const zero_status_t st = adam_ready(h, who);
+    if (st != ZERO_OK) return st;
+    if (!plan->workspace) return fail(ZERO_ESTATE, std::string(who) + ": no rank of the plan is bound");
+    if (plan->device != h->device) return fail(ZERO_EINVAL, std::string(who) + ": the plan lives on another device");
     return ZERO_OK;
 }
 
@@ -1005,56 +1105,68 @@ catch (...) {
 zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double loss_scale, void* stream)
 try {
     if (!h || !hyper) return fail(ZERO_EINVAL, "zero_adamw_step: NULL argument");
-    if (!(hyper->beta1 >= 0.0 && hyper->beta1 < 1.0) || !(hyper->beta2 >= 0.0 && hyper->beta2 < 1.0))
-        return fail(ZERO_EINVAL, "zero_adamw_step: betas must be in [0, 1)");
-    if (!(hyper->eps >= 0.0) || !(hyper->max_grad_norm >= 0.0) || !std::isfinite(hyper->lr) ||
-        !std::isfinite(hyper->weight_decay))
-        return fail(ZERO_EINVAL, "zero_adamw_step: bad hyperparameter");
-    if (hyper->flags & ~(int64_t)ZERO_REPORT_GRAD_NORM) return fail(ZERO_EINVAL, "zero_adamw_step: unknown flag");
+    zero_status_t st = check_hyper(hyper, "zero_adamw_step");
+    if (st != ZERO_OK) return st;
     if (!(loss_scale > 0.0) || !std::isfinite(loss_scale))
         return fail(ZERO_EINVAL, "zero_adamw_step: loss_scale must be positive");
-    const zero_status_t ready = adam_ready(h, "zero_adamw_step");
-    if (ready != ZERO_OK) return ready;
-    char* ws = static_cast<char*>(h->workspace);
-    AdamParams P;
-    float c[9];
-    step_constants(*hyper, 1, loss_scale, 1, c);
-    P.blocks = reinterpret_cast<const AdamBlock*>(ws + blocks_at(h));
-    P.m = h->m;
-    P.v = h->v;
-    P.scales = static_cast<uint16_t*>(h->scales);
-    P.st = reinterpret_cast<AdamState*>(ws);
-    P.partials = reinterpret_cast<double*>(ws + slots_at(h));
-    P.n_blocks = (int32_t)h->n_blocks;
+    st = adam_ready(h, "zero_adamw_step");
+    if (st != ZERO_OK) return st;
+    AdamParams P = adam_params(h);
+    set_hyper(P, *hyper, loss_scale);
     P.checked = hyper->max_grad_norm > 0.0 || (hyper->flags & ZERO_REPORT_GRAD_NORM);
-    // eps: the smallest normal number at least, so that its reciprocal is finite
-    if (c[4] > 0.0f && c[4] < 0x1p-126f) c[4] = 0x1p-126f;
-    c[5] = -c[5];
-    auto twice = [](float x) {
-        uint32_t w;
-        std::memcpy(&w, &x, 4);
-        return F2{((unsigned long long)w << 32) | w};
-    };
-    for (int i = 0; i < 6; ++i) P.k[i] = twice(c[i]);
-    P.one = twice(1.0f);
-    P.inv = c[8];
-    P.lr = hyper->lr;
-    P.beta1 = hyper->beta1;
-    P.beta2 = hyper->beta2;
-    P.max_norm = hyper->max_grad_norm;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (P.checked) {
-        if (h->grad_type == ZERO_BF16) launch_norm<ZERO_BF16>(h, P, s);
-        else if (h->grad_type == ZERO_FP16) launch_norm<ZERO_FP16>(h, P, s);
-        else launch_norm<ZERO_FP32>(h, P, s);
-    }
-    if (h->bits == 8) launch_adamw<8>(h, P, s);
-    else launch_adamw<32>(h, P, s);
+    if (P.checked) launch_norm<false>(h, P, s);
+    launch_adamw(h, P, s);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_adamw_step: launch");
 }
 catch (...) {
     return exception_status("zero_adamw_step");
+}
+
+zero_status_t zero_adamw_check(zero_adamw_t* h, zero_plan_t* plan, void* stream)
+try {
+    const zero_status_t st = plan_ready(h, plan, "zero_adamw_check");
+    if (st != ZERO_OK) return st;
+    if (h->checked_in == plan->step_no) return fail(ZERO_ESTATE, "zero_adamw_check: already part of this step");
+    if (plan->in_step && (plan->offload || plan->step_hyper.max_grad_norm > 0.0))
+        return fail(ZERO_ESTATE, "zero_adamw_check: must precede the first bucket/unit of a step that clips or is offloaded");
+    AdamParams P = adam_params(h);
+    P.plan = reinterpret_cast<DevState*>(plan->workspace);
+    launch_norm<true>(h, P, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "zero_adamw_check: launch");
+    h->checked_in = plan->step_no;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_adamw_check");
+}
+
+zero_status_t zero_adamw_step_with(zero_adamw_t* h, zero_plan_t* plan, const zero_hyper_t* hyper, void* stream)
+try {
+    if (!hyper) return fail(ZERO_EINVAL, "zero_adamw_step_with: NULL argument");
+    zero_status_t st = check_hyper(hyper, "zero_adamw_step_with");
+    if (st == ZERO_OK) st = plan_ready(h, plan, "zero_adamw_step_with");
+    if (st != ZERO_OK) return st;
+    if (h->checked_in != plan->step_no) return fail(ZERO_ESTATE, "zero_adamw_step_with: needs zero_adamw_check in the same step");
+    if (h->stepped_in == plan->step_no) return fail(ZERO_ESTATE, "zero_adamw_step_with: already part of this step");
+    bool all = plan->in_step;
+    for (int64_t b = 0; b < plan->n_buckets && all; ++b) all = plan->covered[(size_t)b] != 0;
+    if (!all) return fail(ZERO_ESTATE, "zero_adamw_step_with: follows the step of every bucket/unit, before the step's finish");
+    if (hyper->max_grad_norm != plan->step_hyper.max_grad_norm)
+        return fail(ZERO_EINVAL, "zero_adamw_step_with: one step has one max_grad_norm");
+    AdamParams P = adam_params(h);
+    set_hyper(P, *hyper, 1.0);
+    P.plan = reinterpret_cast<DevState*>(plan->workspace);
+    launch_adamw(h, P, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "zero_adamw_step_with: launch");
+    h->stepped_in = plan->step_no;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_adamw_step_with");
 }
 
 zero_status_t zero_adamw_export(zero_adamw_t* h, void* m_out, void* root_out, void* stream)

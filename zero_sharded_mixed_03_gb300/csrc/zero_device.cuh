@@ -1,5 +1,5 @@
-// zero_device.cuh -- what the device translation units share: element conversions, the AdamW
-// rule, fixed-order sums, bounded mbarrier waits, and a few host helpers.
+// zero_device.cuh -- what the device translation units share: the sharded step's device-resident state,
+// element conversions, the AdamW rule, fixed-order sums, bounded mbarrier waits, and a few host helpers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -107,6 +107,35 @@ inline cudaError_t take_error_word(W& symbol, uint32_t* word, cudaStream_t s)
     e = cudaMemcpyToSymbolAsync(symbol, &none, sizeof(none), 0, cudaMemcpyHostToDevice, s);
     return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
+
+// ------------------------------------------------------------------ device-resident step state
+
+// First 96 bytes of the workspace.  Written by the commit (the last re-cast block or
+// commit_kernel), by the host before the first step, and by the kernels' atomics (flag,
+// error, norm tickets); read by the step and re-cast kernels of the following step.
+struct DevState {
+    uint32_t flag;          // OR of the non-finite flags of the open step
+    uint32_t cur;           // current half of every ping-pong pair
+    uint32_t last_skipped;  // 1 if the last finished step was skipped
+    uint32_t blocks_done;   // blocks of the running norm launch that have stored their partial
+    int64_t t;              // applied steps
+    int64_t skipped;        // skipped steps, total
+    int64_t good;           // applied steps since the last change of the loss scale
+    int64_t finished;       // finished steps (applied + skipped)
+    double scale;           // loss scale of the next step
+    double norm2;           // open step: sum of fp32(g*g) so far
+    double last_norm2;      // last finished step's sum
+    uint32_t norm_valid;    // open step computed a norm
+    uint32_t last_norm_valid;
+    uint32_t error;         // bit 0: a barrier wait of the staged step ran out; bit 1: a drain
+                            // ran out; bit 2: a barrier wait of the staged gather ran out
+                            // (sticky until read; every step finished meanwhile is discarded)
+    uint32_t pad32;
+    int64_t pad;
+};
+static_assert(sizeof(DevState) == 96, "DevState layout");
+
+static_assert(sizeof(DevState) <= kStateBytes, "DevState fits its workspace slot");
 
 // ------------------------------------------------------------------ element helpers
 

@@ -106,6 +106,13 @@ constexpr int64_t kWorkspaceBytes = kStateBytes + 16 * (kBiasCap + 1) + 8 * kNor
 
 }  // namespace zero
 
+namespace zero {
+
+// A number that no other step of any plan has.
+int64_t next_step_number();
+
+}  // namespace zero
+
 struct zero_plan {
     int n_d = 0;
     int stage = 0;
@@ -138,6 +145,7 @@ struct zero_plan {
     // and the loss scale live on the device, in the workspace).
     bool in_step = false;
     bool stepped = false;               // a step has been enqueued since the plan was bound
+    int64_t step_no = zero::next_step_number();   // the open or coming step's (zero_adamw_check)
     std::vector<char> covered;          // per bucket / unit in the open step
     std::vector<char> norm_covered;     // per bucket / unit: gradient-norm pre-pass done
     bool norm_open = false;             // a norm pre-pass of the next step has been issued

@@ -6,6 +6,7 @@
 // Page: "Zero Redundancy Optimizer (ZeRO) and Fully Sharded Data Parallelism
 // (FSDP): Mathematical Foundations ..." (llms.blog).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <exception>
@@ -116,6 +117,12 @@ std::vector<Segment> shard_segments_all(const zero_plan* p)
         }
     }
     return segs;
+}
+
+int64_t next_step_number()
+{
+    static std::atomic<int64_t> next{1};
+    return next.fetch_add(1);
 }
 
 void step_constants(const zero_hyper_t& h, int64_t t, double scale, int n_d, float out[9])

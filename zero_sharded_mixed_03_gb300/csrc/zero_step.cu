@@ -1435,6 +1435,7 @@ zero_status_t finish_step(zero_plan_t* p, void* stream, zero_step_result_t* out)
         if (e != cudaSuccess) return cuda_fail(e, "commit launch");
     }
     p->in_step = false;
+    p->step_no = next_step_number();
     p->stepped = true;
     p->norm_open = false;
     std::fill(p->covered.begin(), p->covered.end(), 0);
@@ -1483,6 +1484,7 @@ try {
     cudaError_t e = cudaMemcpyAsync(dev_state(p), &d, sizeof(d), cudaMemcpyHostToDevice, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "zero_restore_state: writing the state");
+    p->step_no = next_step_number();         // marks of an earlier zero_adamw_check are gone
     return ZERO_OK;
 }
 catch (...) {
@@ -1770,6 +1772,7 @@ try {
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "commit launch");
     p->in_step = false;
+    p->step_no = next_step_number();
     p->stepped = true;
     p->norm_open = false;
     std::fill(p->covered.begin(), p->covered.end(), 0);

@@ -22,8 +22,8 @@ from typing import Dict, List
 import torch
 
 from . import (ZERO_ACT_GELU, ZERO_ACT_NONE, ZERO_BF16, ZERO_FP32, ZERO_NORM_POST, ZERO_NORM_PRE,
-               ZERO_NORM_RMS, ZERO_WEIGHT_IN_OUT, hyper, zero_adamw_bind, zero_adamw_create,
-               zero_adamw_destroy, zero_adamw_info, zero_adamw_step, zero_block_norm,
+               ZERO_NORM_RMS, ZERO_WEIGHT_IN_OUT, hyper, zero_adamw_bind, zero_adamw_check,
+               zero_adamw_create, zero_adamw_destroy, zero_adamw_info, zero_adamw_step_with, zero_block_norm,
                zero_block_norm_backward, zero_block_norm_t, zero_block_norm_workspace, zero_linear,
                zero_linear_backward, zero_linear_t, zero_linear_workspace)
 from .emulate import EmulatedGroup
@@ -180,12 +180,18 @@ class ShardedFeedForward:
             zero_block_norm_backward(args, self._room(n), n, s)
 
     def step(self, h) -> None:
-        """One optimizer step from the ranks' gradients (no synchronisation)."""
-        for u in range(self.layers):
-            self.group.step([c.data_ptr() for c in self.contribs[u]], u, h)
-        self.group.finish(wait=False)
+        """One optimizer step from the ranks' gradients (no synchronisation): matrices and vectors are applied or
+        left out together, and clipped by one norm."""
+        contribs = [[c.data_ptr() for c in unit] for unit in self.contribs]
         torch.mean(self.rank_vector_grads.float(), 0, out=self.vector_grads)
-        zero_adamw_step(self.opt, h, 1.0, self._stream())
+        if h.max_grad_norm > 0:
+            for u in range(self.layers):
+                self.group.grad_norm(contribs[u], u)
+        zero_adamw_check(self.opt, self.group.plan, self._stream())
+        for u in range(self.layers):
+            self.group.step(contribs[u], u, h)
+        zero_adamw_step_with(self.opt, self.group.plan, h, self._stream())
+        self.group.finish(wait=False)
 
 
 def train(steps: int = 60, layers: int = 3, dim: int = 256, inner: int = 1024, n_d: int = 4, rows: int = 512,
