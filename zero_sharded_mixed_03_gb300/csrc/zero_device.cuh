@@ -257,7 +257,8 @@ struct NormAcc {
         hi = s;
         lo = __fadd_rn(lo, e);
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    // beyond the range hi is infinite and lo not a number
+    __device__ __forceinline__ double value() const { return isinf(hi) ? (double)hi : (double)hi + (double)lo; }
 };
 
 // AdamW on one element with separately rounded IEEE operations (no contraction):
