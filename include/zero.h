@@ -671,9 +671,13 @@ zero_status_t zero_block_norm_workspace(const zero_block_norm_t* a, int64_t* byt
 zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspace, int64_t workspace_bytes,
                                        void* stream);
 
-/* The only waits of the operators' kernels are on shared-memory barriers; each is bounded (at most
- * 2 s).  ZERO_ETIMEOUT if one ran out on the current device since the last call, and clears that;
- * synchronises `stream`. */
+/* Waits of the operators' kernels.  Those on shared-memory barriers are bounded, each by itself (zero_linear
+ * 2 s, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
+ * product's block then gives its own 0.1 s).  Without a limit of their own are the hardware's: a cluster's barrier, which
+ * every block of it reaches on every path, the allocation of tensor memory while another block on the SM
+ * holds it, and the wait for the earlier work of the stream.  ZERO_ETIMEOUT if a bounded one ran out on the current device
+ * since the last call, and clears that: nothing else tells of outputs that are not final.  Synchronises
+ * `stream`. */
 zero_status_t zero_operators_check(void* stream);
 
 /* Elements of one tensor that share a pair of 8-bit scales; the moments' buffers hold every
@@ -708,11 +712,13 @@ zero_status_t zero_adamw_info(const zero_adamw_t* h, zero_adamw_info_t* out);
 zero_status_t zero_adamw_bind(zero_adamw_t* h, float* const* params, void* const* params16, const void* const* grads,
                               void* m, void* v, void* scales, void* workspace, int64_t t, void* stream);
 
-/* One step over every tensor, g = gradient / loss_scale: the rule of zero_step, in place.  With
+/* One step over every tensor, g = gradient / loss_scale: the rule of zero_step, in place, but that the
+ * step's quotient m / d (and with 32-bit moments the root in d) is within 2 units in the last place where
+ * zero_step rounds it exactly; 32-bit moments are the same bits.  With
  * hyper->max_grad_norm > 0 or ZERO_REPORT_GRAD_NORM a pass over the gradients comes first: their
  * global norm clips (max_grad_norm), and a step whose gradients' sum of squares is not finite is
- * skipped whole.  Without, a gradient that is not finite spoils its own element.  8-bit moments:
- * the update uses the new moments before they are rounded. */
+ * skipped whole.  Without, a gradient that is not finite, or (8-bit moments) whose square is not, spoils its own
+ * element.  8-bit moments: the update uses the new moments before they are rounded. */
 zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double loss_scale, void* stream);
 
 /* A step that h makes together with a plan's, applied or left out as one, with one loss scale and one

@@ -12,10 +12,8 @@ def norm(rows, dim, rows_per_gate, layer):
 
 
 @pytest.mark.parametrize("rows_per_gate", [5001, 1 << 59, (1 << 60) + 1, 1 << 62, (1 << 63) - 1])
-@pytest.mark.parametrize("rows,dim", [(1, 64), (40, 136), (5000, 136), (5000, 8192), (1 << 30, 2048)])
+@pytest.mark.parametrize("rows,dim", [(1, 64), (40, 136), (5000, 136), (5000, 8192)])
 @pytest.mark.parametrize("layer", [False, True])
 def test_a_gate_row_for_more_rows_than_there_are(rows_per_gate, rows, dim, layer):
     """One for all of them, whatever the number: the same cut and the same workspace."""
-    if rows_per_gate < rows:
-        pytest.skip("several gate rows")
     assert Z.zero_block_norm_workspace(norm(rows, dim, rows_per_gate, layer)) == Z.zero_block_norm_workspace(norm(rows, dim, rows, layer))

@@ -18,7 +18,7 @@
 // registers, so that the block's new maxima are two warp reductions and nothing is read twice.
 // Measured on one GB300, a step after another: 124M elements, fp16 gradients, 8 bits 362 us (5.5 TB/s of the
 // 16 bytes an element), 59M elements, fp32 gradients, 32 bits 283 us (6.3 TB/s); 59M elements in 10,000
-// packed tensors, 8 bits, clipped, with the values' export: 317 us, of which 44 are the norm, 219 the step and
+// packed tensors, 8 bits, clipped, with the values' export: 316 us, of which 44 are the norm, 219 the step and
 // 56 the export.  adamw_export (6 bytes an element): 112 us of 124M.  194 gains and biases: 10 us a call.
 #include <algorithm>
 #include <cmath>
@@ -175,8 +175,9 @@ __device__ __forceinline__ void store8(float* p, int lane, const float (&x)[8])
 
 // With 8-bit moments a warp's aligned blocks come through shared memory of its own, copied
 // asynchronously two blocks ahead (their records four ahead), so that no register waits for memory:
-// the arithmetic needs them.  Measured on GB300 (124M elements, fp16 gradients): loads into
-// registers 361 us, one, two, three, four blocks ahead 348, 335, 343, 373.  With 32-bit moments the
+// the arithmetic needs them.  Measured on GB300 (124M elements, fp16 gradients), before the roots were rounded
+// exactly: loads into registers 361 us, one, two, three, four blocks ahead 348, 335, 343, 373.  The exact roots
+// bound the step since (362 us), and the depth shows less: with the export 478, 475, 474 and 479.  With 32-bit moments the
 // arithmetic is less and plain loads with 24 warps an SM are faster (59M elements: 268 us against
 // 288).
 template <int GT>

@@ -11,10 +11,10 @@
 // dz is written there by the activation's gradient anyway.
 //
 // Measured on one GB300 (cuBLAS bf16: 1,947 TFLOP/s in a burst, 1,734 sustained under the power cap):
-// 8192 x 11008 x 4096 alone 405 us, 1,824 TFLOP/s; 8192 x 2048 x 8192 with bias and residual 189 us a pass,
-// 1,454 (3.4 rounds of tiles: the last is split along the inner dimension); the gradients of 4096 -> 11008
-// over 8192 tokens 1,021 us, 1,447 in all, of which 82 are dz; of 1001 -> 1603 over 777 tokens, every row off
-// the 16-byte grid, 40 us.
+// 8192 x 11008 x 4096 alone 405 us, 1,824 TFLOP/s; 8192 x 2048 x 8192 with bias and residual 191 us a pass,
+// 1,440 (3.4 rounds of tiles: the last is split along the inner dimension); the gradients of 4096 -> 11008
+// over 8192 tokens 1,029 to 1,038 us, 1,430 in all, of which 82 are dz; of 1001 -> 1603 over 777 tokens, every row
+// off the 16-byte grid, 46.6 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -68,9 +68,9 @@ struct GemmParams {
 
 // ------------------------------------------------------------------ activations
 
-// The logistic function, accurate relative to its value in both tails (to 0 where 2^(-z log2 e)
-// overflows): one exponential and one reciprocal, each an instruction; the plain forms' care for
-// subnormal values costs twice as many and shows in nothing that has 16 bits.
+// The logistic function, accurate relative to its value in both tails, down to 2^-126 (z = -87.3): below it is
+// 0, as the reciprocal's subnormal results are.  z times it is then off by 2^-119 at most.  One exponential and one
+// reciprocal, each an instruction; the plain forms' care for subnormal values costs twice as many.
 __device__ __forceinline__ float logistic(float z)
 {
     float e, r;
@@ -1162,7 +1162,8 @@ zero_status_t launch_few(FewParams P, bool in_out, cudaStream_t s)
 {
     cudaError_t e;
     if (!in_out) {
-        // warps along K until there are sixteen an SM; each has at least 256 elements
+        // warps along K until there are sixteen an SM, by 256 elements in turn; the last shares may be short or
+        // empty (K = 520 by four: 256, 256, 8 and none)
         const int64_t groups = div_up(P.N, kFewCols);
         P.split = 1;
         while (P.split < kFewWarps && groups * P.split < 16 * kGb300Sms && P.split * 256 < P.K) P.split *= 2;
@@ -1189,7 +1190,7 @@ constexpr int64_t kMaxSize = ZERO_LINEAR_MAX_SIZE;   // tile coordinates stay 32
 
 // How the dz pass is cut: threads across the columns (eight each) and workers a block, rows a worker.
 // About eight blocks an SM where there are rows for them, and two rows a worker at least (the gradients of
-// 777 x 1001 x 1603: 39.8 us, with four rows 44.6, with one 40.1 and without an activation 0.8 more).
+// 777 x 1001 x 1603: 46.6 us, with four rows 49.3, with one 49.8).
 struct DzCut {
     int tx = 256, ty = 1, chunk = 1;
     int64_t workers = 0;

@@ -9,7 +9,7 @@
 // pairs (one instruction for two fp32 operations), a thread holds as many elements as its registers
 // allow, so that a row's sums and addresses are shared by more, and rows come through shared memory.
 // Measured on one GB300: 16384 x 2048, LayerNorm with a gate, 52 us (5.2 TB/s, 0.76 of the copy rate);
-// gradients of 16384 x 4096, RMS with gates, 186.5 us (4.3 TB/s, 0.64), of which 8 are the second kernel's;
+// gradients of 16384 x 4096, RMS with gates, 188.7 us (4.3 TB/s, 0.63), of which 8 are the second kernel's;
 // of 1001 x 1023, LayerNorm, gates of 7 rows, element by element, 23.7 us.
 //
 // Backward, per row (Layer centres h and y; RMS does not):

@@ -8,7 +8,8 @@ Layer l of the residual stream y (a row a token):
 Its matrices and biases are one unit of a stage-3 plan: gathered from the ranks' shards before
 they are used, and the ranks' 16-bit gradients are written by the backward pass straight into the
 contributions that ``zero_step`` reduces.  The norms' gains and the gates are a few thousand
-numbers, replicated, and stepped by ``zero_adamw`` with 8-bit moments.  ``zero_block_norm`` joins a
+numbers, replicated, and stepped by ``zero_adamw`` with 8-bit moments, in one with the matrices: a
+gradient that is not finite leaves out both, and one norm clips both.  ``zero_block_norm`` joins a
 layer's end with the next one's start.
 
     python -m zero_sharded_mixed_03_gb300.feed_forward
@@ -59,7 +60,7 @@ class ShardedFeedForward:
         ptrs = [[t.data_ptr() + i * dim * t.element_size() for i in range(3 * layers)]
                 for t in (self.vectors, self.vectors16, self.vector_grads)]
         zero_adamw_bind(self.opt, *ptrs, *(t.data_ptr() for t in self.moments), 0, self._stream())
-        # gathered units (the next is gathered into one while the other is used), activations of one
+        # gathered units (two buffers in turn, on the one stream: nothing overlaps), activations of one
         # rank's micro-batch, contributions of every rank and unit
         self.full = [new(int(self.group.info.max_unit_pad)) for _ in range(2)]
         self.contribs = [[new(unit[3]).zero_() for _ in range(n_d)] for unit in self.group.units]
