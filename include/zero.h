@@ -563,8 +563,8 @@ zero_status_t zero_step_range_noalloc(const void* const* grad_contribs, int n_d,
 
 /* ---------------------------------------------------------------------------------------
  * Operators of a training program around the sharded step: what a gathered unit's weights are
- * used for and what fills the gradient contributions (zero_linear, zero_block_norm, with their
- * gradients), and an optimizer for tensors that are not sharded (zero_adamw).
+ * used for and what fills the gradient contributions (zero_linear, zero_gated, zero_block_norm, with
+ * their gradients), and an optimizer for tensors that are not sharded (zero_adamw).
  *
  * Each is asynchronous on `stream`, allocates nothing, may be captured in a CUDA graph and works
  * on the current device.  Pointers need the alignment of their element type; rows (or tensors)
@@ -624,6 +624,50 @@ zero_status_t zero_linear(const zero_linear_t* a, void* workspace, int64_t works
  * writes zeros to dw and dbias (nothing with ZERO_LINEAR_ACCUMULATE). */
 zero_status_t zero_linear_backward(const zero_linear_t* a, void* workspace, int64_t workspace_bytes, void* stream);
 
+#define ZERO_GATED_ACCUMULATE 1
+
+/* The first half of a gated feed-forward block; 16-bit tensors (dtype16), sums in fp32.  Wg and Wu = the
+ * (in, out) matrices that `w_gate` and `w_up` stand for (both of one layout; rows of one wider matrix by their
+ * strides).  NULL pointers leave a part out where that is said.
+ *   forward   g = x Wg + bg;  u = x Wu + bu;  h = act(g) * u, from the unrounded g and u
+ *             gate, up: g and u, kept for the gradient
+ *   backward  dg = dh * u * act'(g);  du = dh * act(g), of g and u as kept;  dx = dg Wg^T + du Wu^T;
+ *             dw_gate = x^T dg, dw_up = x^T du (stored as the weights are);  db_gate, db_up = the sums of dg's and
+ *             du's rows.  dg and du are rounded to dtype16 for the products. */
+typedef struct {
+    int64_t rows, in_features, out_features;
+    int32_t dtype16;         /* ZERO_BF16 or ZERO_FP16, every tensor */
+    int32_t layout;          /* ZERO_WEIGHT_* */
+    int32_t activation;      /* ZERO_ACT_* */
+    int32_t flags;           /* ZERO_GATED_ACCUMULATE: the weights' and biases' gradients are added to what is there
+                                (one more micro-batch of the same contribution) */
+    int64_t ld_x, ld_w_gate, ld_w_up, ld_h, ld_gate, ld_up, ld_dh, ld_dx, ld_dw_gate, ld_dw_up;
+    const void* x;           /* rows x in */
+    const void *w_gate, *w_up;
+    const void *b_gate, *b_up;   /* out, or NULL */
+    void* h;                 /* forward: rows x out */
+    void *gate, *up;         /* rows x out; forward: written unless NULL; backward: read */
+    const void* dh;          /* backward: rows x out */
+    void* dx;                /* backward: rows x in, or NULL */
+    void *dw_gate, *dw_up;   /* backward: as the weights, or NULL */
+    void *db_gate, *db_up;   /* backward: out, or NULL */
+} zero_gated_t;
+
+/* Bytes of device workspace that zero_gated (backward == 0) or zero_gated_backward needs for these sizes, strides
+ * and pointers (their alignment counts): dg and du, their sums, and copies of operands whose rows do not start on 16
+ * bytes.  Host-only.  0 is possible. */
+zero_status_t zero_gated_workspace(const zero_gated_t* a, int backward, int64_t* bytes);
+
+/* Forward of one gated block.  workspace: at least zero_gated_workspace bytes, 16-byte aligned (NULL if that is 0);
+ * its contents need not survive between calls, but calls that may overlap on the GPU need one each.  ZERO_EINVAL /
+ * ZERO_EALIGN / ZERO_ERANGE (a size beyond ZERO_LINEAR_MAX_SIZE, or a workspace that is too small) before anything is
+ * enqueued.  rows == 0 does nothing; in_features == 0 gives g = bg and u = bu. */
+zero_status_t zero_gated(const zero_gated_t* a, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradients of one gated block (see zero_gated_t); at least one of dx, dw_gate, dw_up, db_gate, db_up.  rows == 0
+ * writes zeros to the weights' and biases' gradients (nothing with ZERO_GATED_ACCUMULATE). */
+zero_status_t zero_gated_backward(const zero_gated_t* a, void* workspace, int64_t workspace_bytes, void* stream);
+
 enum { ZERO_NORM_RMS = 0, ZERO_NORM_LAYER = 1 };
 enum { ZERO_NORM_PRE = 1, ZERO_NORM_POST = 2 };
 #define ZERO_NORM_MAX_DIM 8192
@@ -672,7 +716,7 @@ zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspa
                                        void* stream);
 
 /* Waits of the operators' kernels.  Those on shared-memory barriers are bounded, each by itself (zero_linear
- * 2 s, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
+ * and zero_gated 2 s, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
  * product's block then gives its own 0.1 s).  Without a limit of their own are the hardware's: a cluster's barrier, which
  * every block of it reaches on every path, the allocation of tensor memory while another block on the SM
  * holds it, and the wait for the earlier work of the stream.  ZERO_ETIMEOUT if a bounded one ran out on the current device

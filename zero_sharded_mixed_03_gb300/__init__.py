@@ -31,6 +31,7 @@ TABLE_COLS = {0: 1, 1: 7, 2: 6, 3: 5, 4: 4, 5: 10}
 ZERO_WEIGHT_OUT_IN, ZERO_WEIGHT_IN_OUT = range(2)
 ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU_TANH, ZERO_ACT_GELU, ZERO_ACT_SILU = range(5)
 ZERO_LINEAR_ACCUMULATE = 1
+ZERO_GATED_ACCUMULATE = 1
 ZERO_LINEAR_MAX_SIZE = 1073741824
 ZERO_NORM_RMS, ZERO_NORM_LAYER = range(2)
 ZERO_NORM_PRE, ZERO_NORM_POST = 1, 2
@@ -50,6 +51,7 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_step_gather_next",
             "zero_last_error", "zero_plan_destroy", "zero_step_range_noalloc",
             "zero_linear_workspace", "zero_linear", "zero_linear_backward", "zero_operators_check",
+            "zero_gated_workspace", "zero_gated", "zero_gated_backward",
             "zero_block_norm", "zero_block_norm_workspace", "zero_block_norm_backward",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
             "zero_adamw_check", "zero_adamw_step_with", "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
@@ -116,6 +118,17 @@ class zero_linear_t(ctypes.Structure):
                                                "ld_dx", "ld_dw")] +
                 [(k, ctypes.c_void_p) for k in ("x", "w", "bias", "residual", "y", "pre", "dy", "dx",
                                                 "dw", "dbias")])
+
+
+class zero_gated_t(ctypes.Structure):
+    """The first half of a gated feed-forward block: sizes, strides (0: dense) and device pointers; see
+    include/zero.h."""
+    _fields_ = ([(k, ctypes.c_int64) for k in ("rows", "in_features", "out_features")] +
+                [(k, ctypes.c_int32) for k in ("dtype16", "layout", "activation", "flags")] +
+                [(k, ctypes.c_int64) for k in ("ld_x", "ld_w_gate", "ld_w_up", "ld_h", "ld_gate", "ld_up", "ld_dh",
+                                               "ld_dx", "ld_dw_gate", "ld_dw_up")] +
+                [(k, ctypes.c_void_p) for k in ("x", "w_gate", "w_up", "b_gate", "b_up", "h", "gate", "up", "dh",
+                                                "dx", "dw_gate", "dw_up", "db_gate", "db_up")])
 
 
 class zero_block_norm_t(ctypes.Structure):
@@ -224,6 +237,11 @@ def lib() -> ctypes.CDLL:
         L.zero_linear_backward.argtypes = [ctypes.POINTER(zero_linear_t), _vp, _i64, _vp]
         L.zero_operators_check.argtypes = [_vp]
         for f in (L.zero_linear_workspace, L.zero_linear, L.zero_linear_backward, L.zero_operators_check):
+            f.restype = st
+        L.zero_gated_workspace.argtypes = [ctypes.POINTER(zero_gated_t), _int, ctypes.POINTER(_i64)]
+        L.zero_gated.argtypes = [ctypes.POINTER(zero_gated_t), _vp, _i64, _vp]
+        L.zero_gated_backward.argtypes = [ctypes.POINTER(zero_gated_t), _vp, _i64, _vp]
+        for f in (L.zero_gated_workspace, L.zero_gated, L.zero_gated_backward):
             f.restype = st
         L.zero_block_norm.argtypes = [ctypes.POINTER(zero_block_norm_t), _vp]
         L.zero_block_norm_workspace.argtypes = [ctypes.POINTER(zero_block_norm_t), ctypes.POINTER(_i64)]
@@ -495,6 +513,22 @@ def zero_linear(args: zero_linear_t, workspace: int, workspace_bytes: int, strea
 def zero_linear_backward(args: zero_linear_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
     _check(lib().zero_linear_backward(ctypes.byref(args), workspace or None, workspace_bytes,
                                       stream or None))
+
+
+def zero_gated_workspace(args: zero_gated_t, backward: bool = False) -> int:
+    """Bytes of workspace that zero_gated (or zero_gated_backward) needs for these arguments."""
+    n = _i64()
+    _check(lib().zero_gated_workspace(ctypes.byref(args), int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def zero_gated(args: zero_gated_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().zero_gated(ctypes.byref(args), workspace or None, workspace_bytes, stream or None))
+
+
+def zero_gated_backward(args: zero_gated_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().zero_gated_backward(ctypes.byref(args), workspace or None, workspace_bytes,
+                                     stream or None))
 
 
 def zero_operators_check(stream: int = 0) -> None:

@@ -1,0 +1,969 @@
+// zero_gated.cu -- the first half of a gated feed-forward block, forward and backward (zero_gated_*):
+//   g = x Wg + bg, u = x Wu + bu, h = act(g) * u
+//   dg = dh u act'(g), du = dh act(g);  dx = dg Wg^T + du Wu^T;  dWg = x^T dg, dWu = x^T du;  db = column sums
+//
+// Both projections are one product on the tensor cores: half of a tile's columns are Wg's and half Wu's, at the same
+// place, so that x is staged once for both and a thread of the epilogue holds g and u of the same elements; h leaves
+// it without g and u having been to memory (they are written where the gradients will want them).  dx is one product
+// too, its inner dimension Wg's columns and then Wu's, and the weights' two gradients are tiles of one launch.
+// dg and du are formed by a pass of their own, as both products need them in two layouts and the biases' gradients
+// their sums.
+#include <cmath>
+#include <cstring>
+
+#include "zero_mma.cuh"
+
+namespace zero {
+namespace {
+
+// Set by a kernel whose bounded wait ran out (zero_operators_check reads and clears it).
+__device__ uint32_t g_gated_error;
+
+// What a launch's tiles are.
+enum { kForward = 0, kInput = 1, kWeights = 2 };   // g and u; dx; dWg and dWu
+
+struct GatedParams {
+    CUtensorMap a[2], b[2];      // forward: x and -, Wg and Wu; dx: dg and du, Wg and Wu; weights: a and b of each
+    Matrix16 out[3];             // forward: h, g, u (p NULL: not kept); dx; dWg, dWu
+    const uint16_t* bias[2];     // forward: of g and u, or NULL
+    int32_t count, tiles_m, tiles_n, per_problem;   // per_problem: tiles of one product
+    int32_t k_blocks, k_first;   // dx: inner blocks in all, and of the first pair
+    int32_t a_rows;              // rows of A that a copy brings (kBM, or fewer where A has no more)
+    int32_t a_mn, b_mn;          // operand stored along its own rows instead of along K
+    int32_t act, accumulate, bias_vec;
+    uint32_t idesc;
+};
+
+// g becomes act(g) u.
+template <int ACT>
+__device__ __forceinline__ void gate_each(float (&g)[32], const float (&u)[32])
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = act_value(g[j], ACT) * u[j];
+}
+
+__device__ __forceinline__ void gate_values(float (&g)[32], const float (&u)[32], int act)
+{
+    switch (act) {
+    case ZERO_ACT_RELU: gate_each<ZERO_ACT_RELU>(g, u); break;
+    case ZERO_ACT_GELU_TANH: gate_each<ZERO_ACT_GELU_TANH>(g, u); break;
+    case ZERO_ACT_GELU: gate_each<ZERO_ACT_GELU>(g, u); break;
+    case ZERO_ACT_SILU: gate_each<ZERO_ACT_SILU>(g, u); break;
+    default: gate_each<ZERO_ACT_NONE>(g, u);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void add_bias(float (&x)[32], const uint16_t* bias, bool vec, int64_t col0, int64_t cols)
+{
+    if (!bias) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = (int)max((int64_t)0, min((int64_t)8, cols - col0 - 8 * i));
+        float b[8];
+        load8<DT>(bias + col0 + 8 * i, vec, n, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[8 * i + j] += b[j];
+    }
+}
+
+template <int CG, int BN, int MODE, int DT>
+struct GatedWork {
+    const GatedParams& P;
+    int count;
+    static constexpr int kBRows = BN / CG;
+    struct Item {
+        int m, n, kb, problem;
+    };
+
+    __device__ __forceinline__ Item item(int i) const
+    {
+        Item I;
+        I.problem = MODE == kWeights && i >= P.per_problem;
+        tile_at(P.tiles_m, P.tiles_n, I.problem ? i - P.per_problem : i, I.m, I.n);
+        I.kb = P.k_blocks;
+        return I;
+    }
+    __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (P.a_rows + kBRows) * (kBK * 2); }
+    __device__ __forceinline__ bool a_mn(const Item&) const { return MODE == kWeights; }
+    __device__ __forceinline__ bool b_mn(const Item&) const { return P.b_mn; }
+    __device__ __forceinline__ uint32_t idesc(const Item&) const { return P.idesc; }
+
+    __device__ __forceinline__ void load(const Item& I, int kb, uint32_t a, uint32_t b, uint32_t bar, int rank) const
+    {
+        const int row_a = (I.m * CG + rank) * kBM;
+        int pair = I.problem;
+        if constexpr (MODE == kInput) {
+            if (kb >= P.k_first) {
+                pair = 1;
+                kb -= P.k_first;
+            }
+        }
+        const int k = kb * kBK;
+        if constexpr (MODE == kWeights) {
+            for (int i = 0; i < kBM / 64; ++i) tma_load_2d<CG>(a + i * (kBK * 128), &P.a[pair], row_a + 64 * i, k, bar);
+        } else {
+            tma_load_2d<CG>(a, &P.a[pair], k, row_a, bar);
+        }
+        if constexpr (MODE == kForward && CG == 2) {
+            // the pair's first block brings Wg's half of the columns and the second Wu's
+            const int row_b = I.n * kBRows;
+            const CUtensorMap* map = &P.b[rank];
+            if (P.b_mn) {
+                for (int i = 0; i < kBRows / 64; ++i) tma_load_2d<CG>(b + i * (kBK * 128), map, row_b + 64 * i, k, bar);
+            } else {
+                tma_load_2d<CG>(b, map, k, row_b, bar);
+            }
+        } else if constexpr (MODE == kForward) {
+            for (int i = 0; i < 2; ++i) {
+                if (P.b_mn) tma_load_2d<CG>(b + i * (kBK * 128), &P.b[i], I.n * 64, k, bar);
+                else tma_load_2d<CG>(b + i * (64 * kBK * 2), &P.b[i], k, I.n * 64, bar);
+            }
+        } else {
+            const int row_b = I.n * BN + rank * kBRows;
+            if (P.b_mn) {
+                for (int i = 0; i < kBRows / 64; ++i) tma_load_2d<CG>(b + i * (kBK * 128), &P.b[pair], row_b + 64 * i, k, bar);
+            } else {
+                tma_load_2d<CG>(b, &P.b[pair], k, row_b, bar);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish(const Item& I, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    {
+        const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
+        if constexpr (MODE == kForward) {
+            constexpr int kWidth = BN / 2;
+            const Matrix16& H = P.out[0];
+            for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols) {
+                const int64_t col0 = (int64_t)I.n * kWidth + c;
+                if (col0 >= H.cols || row0 >= H.rows) break;
+                float g[32], u[32];
+                tmem_load32(acc + c, g);
+                tmem_load32(acc + kWidth + c, u);
+                add_bias<DT>(g, P.bias[0], P.bias_vec & 1, col0, H.cols);
+                add_bias<DT>(u, P.bias[1], P.bias_vec & 2, col0, H.cols);
+                if (P.out[1].p) put_tile<DT>(stage, lane, g, P.out[1], row0, col0);
+                if (P.out[2].p) put_tile<DT>(stage + kTile16Bytes, lane, u, P.out[2], row0, col0);
+                gate_values(g, u, P.act);
+                put_tile<DT>(stage, lane, g, H, row0, col0);
+            }
+        } else {
+            const Matrix16& D = P.out[I.problem];
+            for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
+                const int64_t col0 = (int64_t)I.n * BN + c;
+                if (col0 >= D.cols || row0 >= D.rows) break;
+                float x[32];
+                tmem_load32(acc + c, x);
+                if (MODE == kWeights && P.accumulate) add_tile<DT>(stage + kTile16Bytes, lane, 1.0f, x, D, row0, col0);
+                put_tile<DT>(stage, lane, x, D, row0, col0);
+            }
+        }
+    }
+};
+
+template <int CG, int BN, int MODE, int DT>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) gated_kernel(const __grid_constant__ GatedParams P)
+{
+    extern __shared__ unsigned char smem_raw[];
+    Tiles<CG, BN> T;
+    T.open(smem_raw);
+    after_earlier_work();
+    T.run(GatedWork<CG, BN, MODE, DT>{P, P.count}, &g_gated_error);
+}
+
+// The block over an empty inner dimension: g = bg, u = bu.
+template <int DT>
+__global__ void __launch_bounds__(256) gated_empty_kernel(const __grid_constant__ GatedParams P)
+{
+    after_earlier_work();
+    const Matrix16 &H = P.out[0], &G = P.out[1], &U = P.out[2];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < H.rows * H.cols; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / H.cols, col = i - row * H.cols;
+        const float g = P.bias[0] ? widen1<DT>(P.bias[0][col]) : 0.0f, u = P.bias[1] ? widen1<DT>(P.bias[1][col]) : 0.0f;
+        if (G.p) G.p[row * G.ld + col] = narrow1<DT>(g);
+        if (U.p) U.p[row * U.ld + col] = narrow1<DT>(u);
+        H.p[row * H.ld + col] = narrow1<DT>(act_value(g, P.act) * u);
+    }
+}
+
+// ------------------------------------------------------------------ dg and du, and aligned copies
+
+// What precedes the products, one launch: dg and du with their column sums, and the copies of x and the weights.
+struct SplitParams {
+    AlignJob copy[3];
+    int32_t blocks, across;      // blocks of the pass, and how many of them share rows
+    int32_t copy_blocks[3];
+    const uint16_t *dh, *gate, *up;
+    uint16_t *dg, *du;           // rows of ld elements, 16-byte aligned; NULL: only the sums
+    float* sums;                 // [worker][2][ld] column sums, or NULL
+    int64_t rows, cols, ld_dh, ld_gate, ld_up, ld;
+    int32_t act, vec, chunk;     // vec: every row starts on 16 bytes; chunk: consecutive rows a worker takes
+};
+
+template <int ACT>
+__device__ __forceinline__ void split_each(const float (&d)[8], float (&g)[8], float (&u)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = act_value(g[j], ACT), s = act_slope(g[j], ACT), up = u[j];
+        u[j] = d[j] * a;
+        g[j] = d[j] * up * s;
+    }
+}
+
+// g and u become dg and du.
+__device__ __forceinline__ void split_values(const float (&d)[8], float (&g)[8], float (&u)[8], int act)
+{
+    switch (act) {
+    case ZERO_ACT_RELU: split_each<ZERO_ACT_RELU>(d, g, u); break;
+    case ZERO_ACT_GELU_TANH: split_each<ZERO_ACT_GELU_TANH>(d, g, u); break;
+    case ZERO_ACT_GELU: split_each<ZERO_ACT_GELU>(d, g, u); break;
+    case ZERO_ACT_SILU: split_each<ZERO_ACT_SILU>(d, g, u); break;
+    default: split_each<ZERO_ACT_NONE>(d, g, u);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8])
+{
+    widen2<DT>(w.x, x[0], x[1]);
+    widen2<DT>(w.y, x[2], x[3]);
+    widen2<DT>(w.z, x[4], x[5]);
+    widen2<DT>(w.w, x[6], x[7]);
+}
+
+// FULL: all eight columns are there, by 16-byte accesses; else `n` of them, and zeros.
+template <bool FULL>
+__device__ __forceinline__ uint4 fetch8(const uint16_t* p, int n)
+{
+    if constexpr (FULL) {
+        return __ldcs(reinterpret_cast<const uint4*>(p));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = (2 * j < n ? p[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)p[2 * j + 1] : 0u) << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int DT, bool FULL, int FLIGHT>
+__device__ __forceinline__ void split_rows(const SplitParams& P, int64_t col, int n, int64_t r, float (&sg)[8], float (&su)[8])
+{
+    uint4 d[FLIGHT], g[FLIGHT], u[FLIGHT];
+#pragma unroll
+    for (int i = 0; i < FLIGHT; ++i) {
+        d[i] = fetch8<FULL>(P.dh + (r + i) * P.ld_dh + col, n);
+        g[i] = fetch8<FULL>(P.gate + (r + i) * P.ld_gate + col, n);
+        u[i] = fetch8<FULL>(P.up + (r + i) * P.ld_up + col, n);
+    }
+#pragma unroll
+    for (int i = 0; i < FLIGHT; ++i) {
+        float x[8], y[8], z[8];
+        widen8<DT>(d[i], x);
+        widen8<DT>(g[i], y);
+        widen8<DT>(u[i], z);
+        split_values(x, y, z, P.act);
+        if (P.sums) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sg[j] += FULL || j < n ? y[j] : 0.0f;
+                su[j] += FULL || j < n ? z[j] : 0.0f;
+            }
+        }
+        if (P.dg) {
+            store8<DT>(P.dg + (r + i) * P.ld + col, true, 8, y);      // rows of a multiple of 8
+            store8<DT>(P.du + (r + i) * P.ld + col, true, 8, z);
+        }
+    }
+}
+
+// A thread takes eight columns of a worker's rows (blocks of up to 2048 columns; narrower ones hold several
+// workers), so that the sums need no exchange.
+template <int DT>
+__global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ SplitParams P)
+{
+    after_earlier_work();
+    constexpr int kFlight = 2;
+    if ((int)blockIdx.x >= P.blocks) {
+        int b = blockIdx.x - P.blocks, which = 0;
+        while (b >= P.copy_blocks[which]) b -= P.copy_blocks[which++];
+        align_rows(P.copy[which], b, P.copy_blocks[which]);
+        return;
+    }
+    const int by = blockIdx.x / P.across, bx = blockIdx.x - by * P.across;
+    const int64_t col = ((int64_t)bx * blockDim.x + threadIdx.x) * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, P.cols - col));
+    const int64_t worker = (int64_t)by * blockDim.y + threadIdx.y;
+    const int64_t r1 = min(P.rows, (worker + 1) * P.chunk);
+    int64_t r = worker * P.chunk;
+    if (n == 0 || r >= r1) return;
+    float sg[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, su[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (n == 8 && P.vec) {
+        for (; r + kFlight <= r1; r += kFlight) split_rows<DT, true, kFlight>(P, col, n, r, sg, su);
+        for (; r < r1; ++r) split_rows<DT, true, 1>(P, col, n, r, sg, su);
+    } else {
+        for (; r < r1; ++r) split_rows<DT, false, 1>(P, col, n, r, sg, su);
+    }
+    if (!P.sums) return;
+    float4* q = reinterpret_cast<float4*>(P.sums + worker * 2 * P.ld + col);
+    q[0] = make_float4(sg[0], sg[1], sg[2], sg[3]);
+    q[1] = make_float4(sg[4], sg[5], sg[6], sg[7]);
+    q = reinterpret_cast<float4*>(P.sums + (worker * 2 + 1) * P.ld + col);
+    q[0] = make_float4(su[0], su[1], su[2], su[3]);
+    q[1] = make_float4(su[4], su[5], su[6], su[7]);
+}
+
+// Sums over the workers, in a fixed order, in fp32: 32 columns by 8 workers at a time; the second half of the grid
+// is du's.
+template <int DT>
+__global__ void __launch_bounds__(256) gated_bias_kernel(const float* sums, int64_t ld, int64_t workers, int64_t cols,
+                                                         uint16_t* db_gate, uint16_t* db_up, int accumulate)
+{
+    after_earlier_work();
+    __shared__ float part[8][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    uint16_t* out = blockIdx.y ? db_up : db_gate;
+    const float* from = sums + blockIdx.y * ld;
+    float s = 0.0f;
+    if (c < cols && out) {
+#pragma unroll 8
+        for (int64_t w = threadIdx.y; w < workers; w += 8) s += from[w * 2 * ld + c];
+    }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y != 0 || c >= cols || !out) return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+    if (accumulate) s += widen1<DT>(out[c]);
+    out[c] = narrow1<DT>(s);
+}
+
+// ------------------------------------------------------------------ few rows
+//
+// Up to kFewRows rows of x: reading both weights is all there is.  fp32 products on the plain cores straight from
+// the loads, no tiles and one launch, for operands on the 16-byte grid.
+constexpr int kFewRows = 2;
+constexpr int kFewWarps = 8;                          // warps a block
+constexpr int kFewParts = 8;                          // (in, out): blocks a cluster at most
+constexpr int kFewResident = 3;                       // (in, out): blocks an SM
+
+struct FewParams {
+    const uint16_t *x, *w[2];
+    const uint16_t* bias[2];
+    uint16_t *h, *gate, *up;
+    int64_t ld_x, ld_w[2], ld_h, ld_gate, ld_up;
+    int32_t M, N, K;   // K (and N where the weights are stored along it) in eights; rows of x and W start on 16 bytes
+    int32_t act, split;   // split: (out, in): warps along K
+};
+
+template <int DT>
+__device__ __forceinline__ void few_finish(const FewParams& P, int64_t row, int64_t col, float g, float u)
+{
+    if (P.bias[0]) g += widen1<DT>(P.bias[0][col]);
+    if (P.bias[1]) u += widen1<DT>(P.bias[1][col]);
+    if (P.gate) P.gate[row * P.ld_gate + col] = narrow1<DT>(g);
+    if (P.up) P.up[row * P.ld_up + col] = narrow1<DT>(u);
+    P.h[row * P.ld_h + col] = narrow1<DT>(act_value(g, P.act) * u);
+}
+
+// Weights stored (out, in): a warp takes a row of each and every `split`-th 256 elements of them.
+template <int DT, int ROWS>
+__global__ void __launch_bounds__(32 * kFewWarps, 4) gated_few_kernel(const __grid_constant__ FewParams P)
+{
+    constexpr int U = 2;
+    __shared__ float part[kFewWarps][ROWS * 2];
+    after_earlier_work();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ways = P.split, sub = warp % ways;
+    const int64_t n = (int64_t)blockIdx.x * (kFewWarps / ways) + warp / ways, nc = min(n, (int64_t)P.N - 1);
+    const uint16_t *x[ROWS], *w[2];   // the last row again where there are fewer
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) x[m] = P.x + min(m, P.M - 1) * P.ld_x;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) w[c] = P.w[c] + nc * P.ld_w[c];
+    F2 acc[ROWS][2];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[m][c] = both(0.0f);
+    const int64_t step = ways * 256;
+    int64_t k = sub * 256 + lane * 8;
+    for (; k + (U - 1) * step < P.K; k += U * step) few_eights<DT, U, ROWS, 2>(x, w, k, step, acc);
+    for (; k < P.K; k += step) few_eights<DT, 1, ROWS, 2>(x, w, k, step, acc);
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float a, b;
+            split(acc[m][c], a, b);
+            a += b;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            if (lane == 0) part[warp][m * 2 + c] = a;
+        }
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i >= kFewWarps / ways * ROWS) return;
+    const int g = i / ROWS, m = i % ROWS;
+    const int64_t col = (int64_t)blockIdx.x * (kFewWarps / ways) + g;
+    if (m >= P.M || col >= P.N) return;
+    float a = 0.0f, b = 0.0f;
+    for (int v = 0; v < ways; ++v) {
+        a += part[g * ways + v][m * 2];
+        b += part[g * ways + v][m * 2 + 1];
+    }
+    few_finish<DT>(P, m, col, a, b);
+}
+
+// Weights stored (in, out): a block takes 64 columns of both and one part of K, half of its warps each weight, a
+// thread eight columns and eight rows at a time, so that its eight elements of x are one load; the blocks of a
+// cluster are the parts, summed in order.
+template <int DT, int ROWS>
+__global__ void __launch_bounds__(32 * kFewWarps, kFewResident) gated_few_deep_kernel(const __grid_constant__ FewParams P)
+{
+    constexpr int kDeep = kFewWarps / 2;              // warps along K
+    __shared__ float part[kFewWarps][ROWS * 64];
+    __shared__ float whole[2 * ROWS * 64];
+    after_earlier_work();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, across = (lane & 7) * 8, which = warp / kDeep;
+    // past the last column: that column's eight again
+    const int64_t ld = P.ld_w[which];
+    const uint16_t* w = P.w[which] + min((int64_t)blockIdx.x * 64 + across, (int64_t)P.N - 8);
+    const int64_t per = (P.K / 8 + gridDim.y - 1) / gridDim.y * 8, end = min((int64_t)P.K, (blockIdx.y + 1) * per);
+    F2 acc[ROWS][4];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = both(0.0f);
+    for (int64_t k = blockIdx.y * per + warp % kDeep * 32 + (lane >> 3) * 8; k < end; k += kDeep * 32) {
+        uint4 wv[8], xv[ROWS];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) wv[u] = __ldcs(reinterpret_cast<const uint4*>(w + (k + u) * ld));
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) xv[m] = *reinterpret_cast<const uint4*>(P.x + min(m, P.M - 1) * P.ld_x + k);
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+            F2 f[2][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float a, b;
+                widen2<DT>(word(wv[u + j / 4], j % 4), a, b);
+                f[j / 4][j % 4] = pair(a, b);
+            }
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                float a, b;
+                widen2<DT>(word(xv[m], u / 2), a, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = fma(both(a), f[0][j], acc[m][j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = fma(both(b), f[1][j], acc[m][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split(acc[m][j], a, b);
+#pragma unroll
+            for (int o = 8; o < 32; o *= 2) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            if (lane < 8) {
+                part[warp][m * 64 + across + 2 * j] = a;
+                part[warp][m * 64 + across + 2 * j + 1] = b;
+            }
+        }
+    __syncthreads();
+    const int i = threadIdx.x, m = i / 64;
+    const int64_t col = (int64_t)blockIdx.x * 64 + i % 64;
+    const bool mine = i < ROWS * 64 && m < P.M && col < P.N;
+    float z[2] = {0.0f, 0.0f};
+    if (mine) {
+#pragma unroll
+        for (int v = 0; v < kDeep; ++v) {
+            z[0] += part[v][i];
+            z[1] += part[kDeep + v][i];
+        }
+    }
+    if (gridDim.y > 1) {
+        if (mine) {
+            whole[i] = z[0];
+            whole[ROWS * 64 + i] = z[1];
+        }
+        cluster_sync();
+        if (mine && blockIdx.y == 0) {
+            for (uint32_t r = 1; r < gridDim.y; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t at;
+                    float v;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&whole[c * ROWS * 64 + i])), "r"(r));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+                    z[c] += v;
+                }
+        }
+        cluster_sync();   // a block's shared memory outlives the reads of it
+    }
+    if (mine && blockIdx.y == 0) few_finish<DT>(P, m, col, z[0], z[1]);
+}
+
+// ------------------------------------------------------------------ host
+
+// The shape of a product's tiles: 256 x 256 on a pair of SMs, an inner block of which takes 0.336 us (94 % of the tensor
+// cores' measured rate), or 128 x 128 on one (0.29, what the loads into an SM take), whichever is sooner done.
+struct Shape {
+    int cg = 2, bn = 256;
+    int64_t tiles_m = 0, tiles_n = 0;
+};
+
+Shape choose_shape(int64_t M, int64_t N, int64_t products)
+{
+    Shape best;
+    double best_us = 1e30;
+    static const struct {
+        int cg, bn;
+        double block_us;
+    } shapes[] = {{2, 256, 0.336}, {1, 128, 0.29}};
+    for (const auto& c : shapes) {
+        Shape s;
+        s.cg = c.cg;
+        s.bn = c.bn;
+        s.tiles_m = div_up(M, kBM * c.cg);
+        s.tiles_n = div_up(N, c.bn);
+        const double us = div_up(products * s.tiles_m * s.tiles_n, kGb300Sms / c.cg) * c.block_us;
+        if (us < best_us) {
+            best_us = us;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <int CG, int BN, int MODE, int DT>
+zero_status_t launch_gated(const GatedParams& P, cudaStream_t s)
+{
+    using S = GemmShape<CG, BN>;
+    const cudaError_t set = allow_shared<gated_kernel<CG, BN, MODE, DT>>(S::kSmem);
+    if (set != cudaSuccess) return cuda_fail(set, "zero_gated: shared memory");
+    const int grid = CG * (int)std::min<int64_t>(kGb300Sms / CG, P.count);
+    const cudaError_t e = launch_after(gated_kernel<CG, BN, MODE, DT>, grid, kGemmThreads, S::kSmem, s, P);
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
+}
+
+template <int MODE>
+zero_status_t launch_gated(const GatedParams& P, const Shape& c, bool bf, cudaStream_t s)
+{
+    if (c.cg == 2) return bf ? launch_gated<2, 256, MODE, ZERO_BF16>(P, s) : launch_gated<2, 256, MODE, ZERO_FP16>(P, s);
+    return bf ? launch_gated<1, 128, MODE, ZERO_BF16>(P, s) : launch_gated<1, 128, MODE, ZERO_FP16>(P, s);
+}
+
+// fp32 accumulators; operand type; which operands lie along their rows; N / 8; M / 16
+uint32_t product_desc(bool bf, bool a_mn, bool b_mn, const Shape& c)
+{
+    return (1u << 4) | ((bf ? 1u : 0u) << 7) | ((bf ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(c.bn >> 3) << 17) | ((uint32_t)((kBM * c.cg) >> 4) << 24);
+}
+
+template <int DT, int ROWS>
+zero_status_t launch_few(FewParams P, bool in_out, cudaStream_t s)
+{
+    cudaError_t e;
+    if (!in_out) {
+        // warps along K until there are sixteen an SM, by 256 elements in turn; the last shares may be short or empty
+        P.split = 1;
+        while (P.split < kFewWarps && (int64_t)P.N * P.split < 16 * kGb300Sms && P.split * 256 < P.K) P.split *= 2;
+        e = launch_after(gated_few_kernel<DT, ROWS>, (unsigned)div_up(P.N, kFewWarps / P.split), 32 * kFewWarps, 0, s, P);
+    } else {
+        // as many parts of K as are resident at one time; each has at least 128 rows of the weights
+        const int64_t blocks = div_up(P.N, 64);
+        int parts = 1;
+        while (parts < kFewParts && 2 * parts * blocks <= kFewResident * kGb300Sms && 256 * parts <= P.K) parts *= 2;
+        e = launch_clusters_after(gated_few_deep_kernel<DT, ROWS>, dim3(1, parts), dim3((unsigned)blocks, parts), 32 * kFewWarps, 0, s, P);
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
+}
+
+template <int DT>
+zero_status_t launch_few(const FewParams& P, bool in_out, cudaStream_t s)
+{
+    return P.M == 1 ? launch_few<DT, 1>(P, in_out, s) : launch_few<DT, 2>(P, in_out, s);
+}
+
+// How the pass over dh, g and u is cut: threads across the columns (eight each) and workers a block, rows a worker:
+// about six blocks an SM where there are rows for them, and two rows a worker at least.
+struct SplitCut {
+    int tx = 256, ty = 1, chunk = 1;
+    int64_t workers = 0;
+};
+
+SplitCut split_cut(int64_t rows, int64_t cols)
+{
+    SplitCut c;
+    while (c.tx > 32 && (int64_t)c.tx * 4 >= cols) c.tx /= 2;
+    c.ty = 256 / c.tx;
+    const int64_t across = std::max<int64_t>(1, div_up(cols, (int64_t)c.tx * 8));
+    const int64_t want = std::max<int64_t>(1, 6 * kGb300Sms * c.ty / across);
+    c.chunk = (int)std::max<int64_t>(2, div_up(std::max<int64_t>(rows, 1), want));
+    c.workers = div_up(rows, c.chunk);
+    return c;
+}
+
+constexpr int64_t kMaxSize = ZERO_LINEAR_MAX_SIZE;   // tile coordinates stay 32-bit
+
+// Everything a call needs, checked: strides filled in, and where its pieces lie in the workspace.
+struct Gated {
+    zero_gated_t a;
+    bool bf = true, few = false, copy[3] = {false, false, false};   // x, Wg, Wu
+    int64_t w_rows = 0, w_cols = 0;        // as stored
+    int64_t ld8[3] = {0, 0, 0}, at_copy[3] = {0, 0, 0};
+    int64_t ld_d = 0, at_dg = 0, at_du = 0, at_sums = 0, bytes = 0;
+    bool make_d = false, make_sums = false;
+    SplitCut cut;
+};
+
+zero_status_t lay_out(const zero_gated_t* in, bool back, Gated* L, const char* who)
+{
+    const std::string w = std::string(who) + ": ";
+    if (!in) return fail(ZERO_EINVAL, w + "NULL arguments");
+    L->a = *in;
+    zero_gated_t& a = L->a;
+    if (a.rows < 0 || a.in_features < 0 || a.out_features < 0) return fail(ZERO_EINVAL, w + "negative size");
+    if (a.rows > kMaxSize || a.in_features > kMaxSize || a.out_features > kMaxSize)
+        return fail(ZERO_ERANGE, w + "a size beyond ZERO_LINEAR_MAX_SIZE");
+    if (a.dtype16 != ZERO_BF16 && a.dtype16 != ZERO_FP16) return fail(ZERO_EINVAL, w + "bad dtype16");
+    if (a.layout != ZERO_WEIGHT_OUT_IN && a.layout != ZERO_WEIGHT_IN_OUT) return fail(ZERO_EINVAL, w + "bad layout");
+    if (a.activation < ZERO_ACT_NONE || a.activation > ZERO_ACT_SILU) return fail(ZERO_EINVAL, w + "bad activation");
+    if (a.flags & ~(back ? ZERO_GATED_ACCUMULATE : 0)) return fail(ZERO_EINVAL, w + "unknown flag");
+    L->bf = a.dtype16 == ZERO_BF16;
+    const bool out_in = a.layout == ZERO_WEIGHT_OUT_IN;
+    L->w_rows = out_in ? a.out_features : a.in_features;
+    L->w_cols = out_in ? a.in_features : a.out_features;
+    struct {
+        int64_t* ld;
+        int64_t cols;
+    } strides[] = {{&a.ld_x, a.in_features},   {&a.ld_w_gate, L->w_cols}, {&a.ld_w_up, L->w_cols},   {&a.ld_h, a.out_features}, {&a.ld_gate, a.out_features},
+                   {&a.ld_up, a.out_features}, {&a.ld_dh, a.out_features}, {&a.ld_dx, a.in_features}, {&a.ld_dw_gate, L->w_cols}, {&a.ld_dw_up, L->w_cols}};
+    for (auto& s : strides) {
+        if (*s.ld == 0) *s.ld = s.cols;
+        if (*s.ld < s.cols) return fail(ZERO_EINVAL, w + "a row stride is shorter than its row");
+        if (*s.ld > ((int64_t)1 << 38)) return fail(ZERO_ERANGE, w + "a row stride beyond 2^38");
+    }
+    const void* every[] = {a.x, a.w_gate, a.w_up, a.b_gate, a.b_up, a.h, a.gate, a.up, a.dh, a.dx, a.dw_gate, a.dw_up, a.db_gate, a.db_up};
+    for (const void* p : every)
+        if (!aligned(p, 2)) return fail(ZERO_EALIGN, w + "a pointer is not aligned to 2 bytes");
+    const bool any_out = a.rows > 0 && a.out_features > 0, any_in = any_out && a.in_features > 0;
+    if (!back) {
+        if (any_out && !a.h) return fail(ZERO_EINVAL, w + "h is NULL");
+        if (any_in && (!a.x || !a.w_gate || !a.w_up)) return fail(ZERO_EINVAL, w + "x, w_gate or w_up is NULL");
+        if (any_out && ((a.gate && (a.gate == a.h || a.gate == a.up)) || (a.up && a.up == a.h)))
+            return fail(ZERO_EINVAL, w + "two outputs are one buffer");
+    } else {
+        if (!a.dx && !a.dw_gate && !a.dw_up && !a.db_gate && !a.db_up) return fail(ZERO_EINVAL, w + "no gradient asked for");
+        if (any_out && (!a.dh || !a.gate || !a.up)) return fail(ZERO_EINVAL, w + "dh, gate or up is NULL");
+        if (any_in && ((a.dx && (!a.w_gate || !a.w_up)) || ((a.dw_gate || a.dw_up) && !a.x)))
+            return fail(ZERO_EINVAL, w + "x, w_gate or w_up is NULL");
+        if ((a.dw_gate && a.dw_gate == a.dw_up) || (a.db_gate && a.db_gate == a.db_up))
+            return fail(ZERO_EINVAL, w + "two gradients are one buffer");
+    }
+    // the pieces of the workspace
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    const void* source[3] = {a.x, a.w_gate, a.w_up};
+    const int64_t ld[3] = {a.ld_x, a.ld_w_gate, a.ld_w_up};
+    const int64_t rows[3] = {a.rows, L->w_rows, L->w_rows}, cols[3] = {a.in_features, L->w_cols, L->w_cols};
+    const bool weights = !back || a.dx, input = !back || a.dw_gate || a.dw_up;
+    const bool use[3] = {input, weights, weights};
+    bool ready = true;
+    for (int i = 0; i < 3; ++i) ready = ready && tma_ready(source[i], ld[i]);
+    L->few = !back && any_in && a.rows <= kFewRows && a.in_features % 8 == 0 && ready && (out_in || a.out_features % 8 == 0);
+    for (int i = 0; i < 3; ++i) {
+        L->ld8[i] = ld[i];
+        L->copy[i] = any_in && use[i] && !L->few && !tma_ready(source[i], ld[i]);
+        if (L->copy[i]) {
+            L->ld8[i] = up(cols[i], 8);
+            L->at_copy[i] = take(2 * rows[i] * L->ld8[i]);
+        }
+    }
+    if (back && any_out) {
+        L->make_d = any_in && (a.dx || a.dw_gate || a.dw_up);
+        L->make_sums = a.db_gate || a.db_up;
+        L->ld_d = up(a.out_features, 8);
+        L->cut = split_cut(a.rows, a.out_features);
+        if (L->make_d) {
+            L->at_dg = take(2 * a.rows * L->ld_d);
+            L->at_du = take(2 * a.rows * L->ld_d);
+        }
+        if (L->make_sums) L->at_sums = take(8 * L->cut.workers * L->ld_d);
+    }
+    L->bytes = at;
+    return ZERO_OK;
+}
+
+zero_status_t check_workspace(const Gated& L, const void* workspace, int64_t bytes, const char* who)
+{
+    if (L.bytes == 0) return ZERO_OK;
+    if (!workspace) return fail(ZERO_EINVAL, std::string(who) + ": workspace is NULL");
+    if (!aligned(workspace, 16)) return fail(ZERO_EALIGN, std::string(who) + ": workspace not 16-byte aligned");
+    if (bytes < L.bytes)
+        return fail(ZERO_ERANGE, std::string(who) + ": workspace of " + std::to_string(bytes) + " bytes, " + std::to_string(L.bytes) + " needed");
+    return ZERO_OK;
+}
+
+// The copies that the call needs, into S; the operands become theirs.
+void plan_copies(const Gated& L, char* ws, const void* (&operand)[3], SplitParams* S)
+{
+    const zero_gated_t& a = L.a;
+    std::memset(S, 0, sizeof(*S));
+    const int64_t ld[3] = {a.ld_x, a.ld_w_gate, a.ld_w_up};
+    const void* source[3] = {a.x, a.w_gate, a.w_up};
+    for (int i = 0; i < 3; ++i) {
+        operand[i] = source[i];
+        if (!L.copy[i]) continue;
+        AlignJob& J = S->copy[i];
+        J.src = static_cast<const uint16_t*>(source[i]);
+        J.dst = reinterpret_cast<uint16_t*>(ws + L.at_copy[i]);
+        J.ld_src = ld[i];
+        J.ld = L.ld8[i];
+        J.rows = i == 0 ? a.rows : L.w_rows;
+        J.cols = i == 0 ? a.in_features : L.w_cols;
+        S->copy_blocks[i] = grid_of(J.rows * div_up(J.cols, 8), kGb300Sms, 8);
+        operand[i] = J.dst;
+    }
+}
+
+zero_status_t launch_split(const Gated& L, const SplitParams& S, cudaStream_t s)
+{
+    const int64_t blocks = (int64_t)S.blocks + S.copy_blocks[0] + S.copy_blocks[1] + S.copy_blocks[2];
+    if (blocks == 0) return ZERO_OK;
+    const dim3 threads(L.cut.tx, L.cut.ty);
+    const cudaError_t e = L.bf ? launch_after(split_kernel<ZERO_BF16>, (unsigned)blocks, threads, 0, s, S)
+                               : launch_after(split_kernel<ZERO_FP16>, (unsigned)blocks, threads, 0, s, S);
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
+}
+
+Matrix16 matrix(void* p, int64_t ld, int64_t rows, int64_t cols)
+{
+    return Matrix16{static_cast<uint16_t*>(p), ld, rows, cols, vec_flag(p, ld, 1)};
+}
+
+// Zeros for a gradient that sums over nothing.
+cudaError_t zeros(void* p, int64_t ld, int64_t rows, int64_t cols, cudaStream_t s)
+{
+    return p && rows > 0 && cols > 0 ? cudaMemset2DAsync(p, (size_t)ld * 2, 0, (size_t)cols * 2, (size_t)rows, s) : cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t take_gated_error(uint32_t* word, void* stream) { return take_error_word(g_gated_error, word, static_cast<cudaStream_t>(stream)); }
+
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+zero_status_t zero_gated_workspace(const zero_gated_t* a, int backward, int64_t* bytes)
+try {
+    if (!bytes) return fail(ZERO_EINVAL, "zero_gated_workspace: NULL argument");
+    Gated L;
+    const zero_status_t st = lay_out(a, backward != 0, &L, "zero_gated_workspace");
+    if (st == ZERO_OK) *bytes = L.bytes;
+    return st;
+}
+catch (...) {
+    return exception_status("zero_gated_workspace");
+}
+
+zero_status_t zero_gated(const zero_gated_t* args, void* workspace, int64_t workspace_bytes, void* stream)
+try {
+    Gated L;
+    zero_status_t st = lay_out(args, false, &L, "zero_gated");
+    if (st == ZERO_OK) st = check_workspace(L, workspace, workspace_bytes, "zero_gated");
+    if (st != ZERO_OK) return st;
+    const zero_gated_t& a = L.a;
+    if (a.rows == 0 || a.out_features == 0) return ZERO_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool in_out = a.layout == ZERO_WEIGHT_IN_OUT;
+    if (L.few) {
+        FewParams P;
+        std::memset(&P, 0, sizeof(P));
+        P.x = static_cast<const uint16_t*>(a.x);
+        P.w[0] = static_cast<const uint16_t*>(a.w_gate);
+        P.w[1] = static_cast<const uint16_t*>(a.w_up);
+        P.bias[0] = static_cast<const uint16_t*>(a.b_gate);
+        P.bias[1] = static_cast<const uint16_t*>(a.b_up);
+        P.h = static_cast<uint16_t*>(a.h);
+        P.gate = static_cast<uint16_t*>(a.gate);
+        P.up = static_cast<uint16_t*>(a.up);
+        P.ld_x = a.ld_x;
+        P.ld_w[0] = a.ld_w_gate;
+        P.ld_w[1] = a.ld_w_up;
+        P.ld_h = a.ld_h;
+        P.ld_gate = a.ld_gate;
+        P.ld_up = a.ld_up;
+        P.M = (int32_t)a.rows;
+        P.N = (int32_t)a.out_features;
+        P.K = (int32_t)a.in_features;
+        P.act = a.activation;
+        return L.bf ? launch_few<ZERO_BF16>(P, in_out, s) : launch_few<ZERO_FP16>(P, in_out, s);
+    }
+    GatedParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.out[0] = matrix(a.h, a.ld_h, a.rows, a.out_features);
+    P.out[1] = matrix(a.gate, a.ld_gate, a.rows, a.out_features);
+    P.out[2] = matrix(a.up, a.ld_up, a.rows, a.out_features);
+    P.bias[0] = static_cast<const uint16_t*>(a.b_gate);
+    P.bias[1] = static_cast<const uint16_t*>(a.b_up);
+    P.bias_vec = vec_flag(a.b_gate, 0, 1) | vec_flag(a.b_up, 0, 2);
+    P.act = a.activation;
+    if (a.in_features == 0) {
+        const int grid = grid_of(a.rows * a.out_features, kGb300Sms, 8);
+        const cudaError_t e = L.bf ? launch_after(gated_empty_kernel<ZERO_BF16>, grid, 256, 0, s, P) : launch_after(gated_empty_kernel<ZERO_FP16>, grid, 256, 0, s, P);
+        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
+    }
+    const void* operand[3];
+    SplitParams S;
+    plan_copies(L, static_cast<char*>(workspace), operand, &S);
+    st = launch_split(L, S, s);
+    if (st != ZERO_OK) return st;
+    const Shape c = choose_shape(a.rows, 2 * a.out_features, 1);
+    // few rows: no zeros are copied for the rest, whose results are not stored
+    P.a_rows = c.cg == 1 && a.rows < kBM ? (int32_t)up(a.rows, 8) : kBM;
+    st = encode(&P.a[0], Operand{operand[0], a.rows, a.in_features, L.ld8[0], false}, a.dtype16, P.a_rows, "zero_gated");
+    for (int i = 0; i < 2 && st == ZERO_OK; ++i)
+        st = encode(&P.b[i], Operand{operand[1 + i], a.out_features, a.in_features, L.ld8[1 + i], in_out}, a.dtype16, c.cg == 2 ? kBM : kBM / 2, "zero_gated");
+    if (st != ZERO_OK) return st;
+    P.tiles_m = (int32_t)c.tiles_m;
+    P.tiles_n = (int32_t)div_up(a.out_features, c.bn / 2);
+    P.count = P.per_problem = P.tiles_m * P.tiles_n;
+    P.k_blocks = (int32_t)div_up(a.in_features, kBK);
+    P.b_mn = in_out;
+    P.idesc = product_desc(L.bf, false, in_out, c);
+    return launch_gated<kForward>(P, c, L.bf, s);
+}
+catch (...) {
+    return exception_status("zero_gated");
+}
+
+zero_status_t zero_gated_backward(const zero_gated_t* args, void* workspace, int64_t workspace_bytes, void* stream)
+try {
+    Gated L;
+    zero_status_t st = lay_out(args, true, &L, "zero_gated_backward");
+    if (st == ZERO_OK) st = check_workspace(L, workspace, workspace_bytes, "zero_gated_backward");
+    if (st != ZERO_OK) return st;
+    const zero_gated_t& a = L.a;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const bool accumulate = a.flags & ZERO_GATED_ACCUMULATE, out_in = a.layout == ZERO_WEIGHT_OUT_IN;
+    const int64_t m = a.rows, k = a.in_features, n = a.out_features;
+    if (m == 0 || n == 0) {
+        // sums over nothing
+        cudaError_t e = zeros(a.dx, a.ld_dx, m, k, s);
+        if (!accumulate) {
+            if (e == cudaSuccess) e = zeros(a.dw_gate, a.ld_dw_gate, L.w_rows, L.w_cols, s);
+            if (e == cudaSuccess) e = zeros(a.dw_up, a.ld_dw_up, L.w_rows, L.w_cols, s);
+            if (e == cudaSuccess) e = zeros(a.db_gate, n, 1, n, s);
+            if (e == cudaSuccess) e = zeros(a.db_up, n, 1, n, s);
+        }
+        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated_backward: memset");
+    }
+    const void* operand[3];
+    SplitParams S;
+    plan_copies(L, ws, operand, &S);
+    float* sums = L.make_sums ? reinterpret_cast<float*>(ws + L.at_sums) : nullptr;
+    if (L.make_d || L.make_sums) {
+        S.dh = static_cast<const uint16_t*>(a.dh);
+        S.gate = static_cast<const uint16_t*>(a.gate);
+        S.up = static_cast<const uint16_t*>(a.up);
+        S.dg = L.make_d ? reinterpret_cast<uint16_t*>(ws + L.at_dg) : nullptr;
+        S.du = L.make_d ? reinterpret_cast<uint16_t*>(ws + L.at_du) : nullptr;
+        S.sums = sums;
+        S.rows = m;
+        S.cols = n;
+        S.ld_dh = a.ld_dh;
+        S.ld_gate = a.ld_gate;
+        S.ld_up = a.ld_up;
+        S.ld = L.ld_d;
+        S.act = a.activation;
+        S.vec = vec_flag(a.dh, a.ld_dh, 1) && vec_flag(a.gate, a.ld_gate, 1) && vec_flag(a.up, a.ld_up, 1);
+        S.chunk = L.cut.chunk;
+        S.across = (int32_t)div_up(n, (int64_t)L.cut.tx * 8);
+        S.blocks = (int32_t)(S.across * div_up(L.cut.workers, L.cut.ty));
+    }
+    st = launch_split(L, S, s);
+    if (st != ZERO_OK) return st;
+    if (L.make_sums) {
+        const dim3 grid((unsigned)div_up(n, 32), 2), threads(32, 8);
+        uint16_t *dbg = static_cast<uint16_t*>(a.db_gate), *dbu = static_cast<uint16_t*>(a.db_up);
+        const cudaError_t e = L.bf ? launch_after(gated_bias_kernel<ZERO_BF16>, grid, threads, 0, s, sums, L.ld_d, L.cut.workers, n, dbg, dbu, (int)accumulate)
+                                   : launch_after(gated_bias_kernel<ZERO_FP16>, grid, threads, 0, s, sums, L.ld_d, L.cut.workers, n, dbg, dbu, (int)accumulate);
+        if (e != cudaSuccess) return cuda_fail(e, "zero_gated_backward: launch");
+    }
+    if (!L.make_d) return ZERO_OK;
+    const Operand dg{ws + L.at_dg, m, n, L.ld_d, false}, du{ws + L.at_du, m, n, L.ld_d, false};
+    if (a.dx) {
+        const Shape c = choose_shape(m, k, 1);
+        GatedParams P;
+        std::memset(&P, 0, sizeof(P));
+        P.out[0] = matrix(a.dx, a.ld_dx, m, k);
+        P.a_rows = c.cg == 1 && m < kBM ? (int32_t)up(m, 8) : kBM;
+        const Operand* d[2] = {&dg, &du};
+        for (int i = 0; i < 2 && st == ZERO_OK; ++i) {
+            st = encode(&P.a[i], *d[i], a.dtype16, P.a_rows, "zero_gated_backward");
+            if (st == ZERO_OK) st = encode(&P.b[i], Operand{operand[1 + i], k, n, L.ld8[1 + i], out_in}, a.dtype16, c.bn / c.cg, "zero_gated_backward");
+        }
+        if (st != ZERO_OK) return st;
+        P.tiles_m = (int32_t)c.tiles_m;
+        P.tiles_n = (int32_t)c.tiles_n;
+        P.count = P.per_problem = P.tiles_m * P.tiles_n;
+        P.k_first = (int32_t)div_up(n, kBK);
+        P.k_blocks = 2 * P.k_first;
+        P.b_mn = out_in;
+        P.idesc = product_desc(L.bf, false, out_in, c);
+        st = launch_gated<kInput>(P, c, L.bf, s);
+        if (st != ZERO_OK) return st;
+    }
+    if (a.dw_gate || a.dw_up) {
+        GatedParams P;
+        std::memset(&P, 0, sizeof(P));
+        const int problems = (a.dw_gate != nullptr) + (a.dw_up != nullptr);
+        const Shape c = choose_shape(L.w_rows, L.w_cols, problems);
+        const Operand x{operand[0], k, m, L.ld8[0], true};
+        int i = 0;
+        for (int which = 0; which < 2; ++which) {
+            void* dw = which ? a.dw_up : a.dw_gate;
+            if (!dw) continue;
+            const Operand z{ws + (which ? L.at_du : L.at_dg), n, m, L.ld_d, true};
+            P.out[i] = matrix(dw, which ? a.ld_dw_up : a.ld_dw_gate, L.w_rows, L.w_cols);
+            st = encode(&P.a[i], out_in ? z : x, a.dtype16, kBM, "zero_gated_backward");
+            if (st == ZERO_OK) st = encode(&P.b[i], out_in ? x : z, a.dtype16, kBM, "zero_gated_backward");
+            if (st != ZERO_OK) return st;
+            ++i;
+        }
+        P.a_rows = kBM;
+        P.tiles_m = (int32_t)c.tiles_m;
+        P.tiles_n = (int32_t)c.tiles_n;
+        P.per_problem = P.tiles_m * P.tiles_n;
+        P.count = problems * P.per_problem;
+        P.k_blocks = (int32_t)div_up(m, kBK);
+        P.b_mn = 1;
+        P.accumulate = accumulate;
+        P.idesc = product_desc(L.bf, true, true, c);
+        st = launch_gated<kWeights>(P, c, L.bf, s);
+    }
+    return st;
+}
+catch (...) {
+    return exception_status("zero_gated_backward");
+}
+
+}  // extern "C"

@@ -19,23 +19,14 @@
 #include <cmath>
 #include <cstring>
 
-#include <cuda.h>
-
-#include "zero_device.cuh"
+#include "zero_mma.cuh"
 
 namespace zero {
 
-cudaError_t take_norm_error(uint32_t* word, void* stream);   // zero_norm.cu
+cudaError_t take_norm_error(uint32_t* word, void* stream);    // zero_norm.cu
+cudaError_t take_gated_error(uint32_t* word, void* stream);   // zero_gated.cu
 
 namespace {
-
-constexpr int kBM = 128;                 // rows of a block's tile (a pair of blocks: 256)
-constexpr int kBK = 64;                  // inner elements a stage: 128 bytes, one swizzle row
-constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = 32 * (4 + kEpiWarps);   // TMA, MMA, TMEM allocation, idle; epilogue
-constexpr uint64_t kGemmWaitNs = 2000000000ull;
-constexpr int kEpiCols = 32;             // columns an epilogue warp takes at a time
-constexpr int kEpiBytes = 32 * kEpiCols * 4;
 
 // Set by a kernel whose bounded wait ran out (zero_operators_check reads and clears it).
 __device__ uint32_t g_linear_error;
@@ -65,109 +56,6 @@ struct GemmParams {
     int32_t rows_vec;            // the outputs and the residual allow 16-byte accesses
     uint32_t idesc;
 };
-
-// ------------------------------------------------------------------ activations
-
-// The logistic function, accurate relative to its value in both tails, down to 2^-126 (z = -87.3): below it is
-// 0, as the reciprocal's subnormal results are.  z times it is then off by 2^-119 at most.  One exponential and one
-// reciprocal, each an instruction; the plain forms' care for subnormal values costs twice as many.
-__device__ __forceinline__ float logistic(float z)
-{
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
-}
-
-// The tanh form of gelu is z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3), and gelu itself
-// z erfc(-z / sqrt 2) / 2: neither loses the left tail as 1 + tanh and 1 + erf do.
-__device__ __forceinline__ float gelu_arg(float z) { return 1.5957691216057308f * z * (1.0f + 0.044715f * z * z); }
-
-__device__ __forceinline__ float act_value(float z, int act)
-{
-    switch (act) {
-    case ZERO_ACT_RELU: return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z);   // not a number stays so
-    case ZERO_ACT_GELU_TANH: return z * logistic(gelu_arg(z));
-    case ZERO_ACT_GELU: return 0.5f * z * erfcf(z * -0.7071067811865476f);
-    case ZERO_ACT_SILU: return z * logistic(z);
-    default: return z;
-    }
-}
-
-__device__ __forceinline__ float act_slope(float z, int act)
-{
-    switch (act) {
-    case ZERO_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    case ZERO_ACT_GELU_TANH: {
-        // s (1 - s) first: it is 0 where the polynomial leaves fp32's range, and the square stays in it, so that
-        // finite numbers have finite slopes (in bf16 |z| goes to 3e38)
-        const float s = logistic(gelu_arg(z));
-        return s + s * (1.0f - s) * z * (1.5957691216057308f * (1.0f + 0.134145f * fminf(z * z, 1e30f)));
-    }
-    case ZERO_ACT_GELU:
-        return 0.5f * erfcf(z * -0.7071067811865476f) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
-    case ZERO_ACT_SILU: {
-        const float s = logistic(z);
-        return s * (1.0f + z * (1.0f - s));
-    }
-    default: return 1.0f;
-    }
-}
-
-// Eight at a time: one branch for all.
-__device__ __forceinline__ void act_values(float (&z)[8], int act)
-{
-#define ZERO_EACH(A) case A: _Pragma("unroll") for (int j = 0; j < 8; ++j) z[j] = act_value(z[j], A); break
-    switch (act) {
-        ZERO_EACH(ZERO_ACT_RELU);
-        ZERO_EACH(ZERO_ACT_GELU_TANH);
-        ZERO_EACH(ZERO_ACT_GELU);
-        ZERO_EACH(ZERO_ACT_SILU);
-    }
-#undef ZERO_EACH
-}
-
-__device__ __forceinline__ void act_slopes(float (&z)[8], int act)
-{
-#define ZERO_EACH(A) case A: _Pragma("unroll") for (int j = 0; j < 8; ++j) z[j] = act_slope(z[j], A); break
-    switch (act) {
-        ZERO_EACH(ZERO_ACT_RELU);
-        ZERO_EACH(ZERO_ACT_GELU_TANH);
-        ZERO_EACH(ZERO_ACT_GELU);
-        ZERO_EACH(ZERO_ACT_SILU);
-    }
-#undef ZERO_EACH
-}
-
-// ------------------------------------------------------------------ eight columns of one row
-
-template <int DT>
-__device__ __forceinline__ void load8(const uint16_t* p, bool vec, int n, float (&x)[8])
-{
-    if (vec && n == 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        widen2<DT>(w.x, x[0], x[1]);
-        widen2<DT>(w.y, x[2], x[3]);
-        widen2<DT>(w.z, x[4], x[5]);
-        widen2<DT>(w.w, x[6], x[7]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < n ? widen1<DT>(p[j]) : 0.0f;
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(uint16_t* p, bool vec, int n, const float (&x)[8])
-{
-    if (vec && n == 8) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]),
-                                                  narrow2<DT>(x[4], x[5]), narrow2<DT>(x[6], x[7]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = narrow1<DT>(x[j]);
-    }
-}
 
 // z: the product; bias, activation and residual in fp32, each output rounded once.
 template <int DT>
@@ -209,117 +97,7 @@ __device__ __forceinline__ void bias8(const Epilogue& E, int64_t col, int n, flo
     }
 }
 
-// ------------------------------------------------------------------ tensor-core building blocks
-
-template <int CG>
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
-{
-    if constexpr (CG == 2)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
-{
-    if constexpr (CG == 2)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-            "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-            "r"(accumulate)
-            : "memory");
-}
-
-// Arrive on `bar` (of both blocks of a pair) once every product issued so far is done.
-template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    if constexpr (CG == 2)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3)
-            : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ uint32_t leader_address(uint32_t addr)   // the pair's first block's copy of `addr`
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// 32 lanes x 32 columns of fp32 from TMEM: this thread's lane's columns.
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&x)[32])
-{
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-}
-
-// Shared-memory descriptor of a 128-byte swizzled operand tile.
-//   stored along K:  rows of 128 bytes, eight of them an atom of 1 KB; atoms 1 KB apart (stride)
-//   stored along MN: 64 elements of MN in 128 bytes, eight K rows an atom; K groups 1 KB apart
-//                    (stride), the next 64 of MN one box of kBK rows on (leading: 8 KB)
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn)
-{
-    const uint64_t leading = mn ? (kBK * 128) >> 4 : 1, stride = 1024 >> 4;
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (leading << 16) | (stride << 32) | (1ull << 46) | (2ull << 61);
-}
-
 // ------------------------------------------------------------------ the product
-
-// Tile (m, n) of item `t`: groups of 8 tile rows are walked column by column, so that what runs
-// at one time shares its operands in L2.
-__device__ __forceinline__ void tile_at(int tiles_m, int tiles_n, int t, int& m, int& n)
-{
-    constexpr int kGroup = 8;
-    const int per_group = kGroup * tiles_n, g = t / per_group, in = t - g * per_group;
-    const int rows = min(kGroup, tiles_m - g * kGroup);
-    n = in / rows;
-    m = g * kGroup + (in - n * rows);
-}
 
 // Work item `item`: a tile and its inner blocks [kb0, kb1); part >= 0: its place among the partial sums.
 struct Item {
@@ -342,16 +120,6 @@ __device__ __forceinline__ Item item_at(const GemmParams& P, int item)
     I.kb1 = I.part >= 0 ? min(P.k_blocks, I.kb0 + P.k_per_split) : P.k_blocks;
     return I;
 }
-
-template <int CG, int BN>
-struct GemmShape {
-    static constexpr int kBRows = BN / CG;                       // B rows one block stages
-    static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBRows * kBK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = BN == 64 ? 8 : 6;
-    static constexpr int kTmemCols = 2 * BN;                     // two accumulators
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 256;
-};
 
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2
 // of B, the first one issues products that read both, and each keeps the accumulators of its own
@@ -640,13 +408,6 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(int64_t M, int64_t N, co
 
 // ------------------------------------------------------------------ dz, and aligned copies
 
-// Rows copied to rows of `ld` elements that start on 16 bytes (src NULL: nothing to copy).
-struct AlignJob {
-    const uint16_t* src;
-    uint16_t* dst;
-    int64_t ld_src, ld, rows, cols;
-};
-
 // What precedes the products, one launch: dz, and the copies of x and of w.
 struct DzParams {
     AlignJob copy[2];
@@ -659,23 +420,6 @@ struct DzParams {
     int64_t rows, cols, ld_dy, ld_pre, ld_dz;
     int32_t act, vec_dy, vec_pre, chunk;   // chunk: consecutive rows a worker takes
 };
-
-// Block b of n, 256 threads: eight elements a thread at a time.
-__device__ __forceinline__ void align_rows(const AlignJob& J, int b, int n)
-{
-    const int64_t per_row = (J.cols + 7) / 8, total = J.rows * per_row;
-    for (int64_t i = (int64_t)b * 256 + threadIdx.y * blockDim.x + threadIdx.x; i < total; i += (int64_t)n * 256) {
-        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-        const uint16_t* p = J.src + row * J.ld_src + col;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = col + 2 * j < J.cols ? p[2 * j] : 0u, hi = col + 2 * j + 1 < J.cols ? p[2 * j + 1] : 0u;
-            w[j] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint4*>(J.dst + row * J.ld + col) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
 
 // FLIGHT rows of a thread's eight columns; FULL: all eight are there, by 16-byte accesses.
 template <int DT, bool FULL, int FLIGHT>
@@ -807,42 +551,6 @@ struct FewParams {
     int32_t M, N, K;   // K (and N where W is stored along it) in eights; rows of x and W start on 16 bytes
     int32_t split;     // (out, in): warps along K
 };
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
-
-// acc[m][c] += eight products of row m of x and row c of W, U times.  Loads first, none of them behind a
-// branch.
-template <int DT, int U, int ROWS, int C>
-__device__ __forceinline__ void few_eights(const uint16_t* const (&x)[ROWS], const uint16_t* const (&w)[C], int64_t k, int64_t step, F2 (&acc)[ROWS][C])
-{
-    uint4 wv[U][C], xv[U][ROWS];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) wv[u][c] = __ldcs(reinterpret_cast<const uint4*>(w[c] + k + u * step));
-#pragma unroll
-        for (int m = 0; m < ROWS; ++m) xv[u][m] = *reinterpret_cast<const uint4*>(x[m] + k + u * step);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            F2 f[C];
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float a, b;
-                widen2<DT>(word(wv[u][c], j), a, b);
-                f[c] = pair(a, b);
-            }
-#pragma unroll
-            for (int m = 0; m < ROWS; ++m) {
-                float a, b;
-                widen2<DT>(word(xv[u][m], j), a, b);
-#pragma unroll
-                for (int c = 0; c < C; ++c) acc[m][c] = fma(pair(a, b), f[c], acc[m][c]);
-            }
-        }
-}
 
 // W stored (out, in): a warp takes kFewCols rows of W and every `split`-th 256 elements of them.
 template <int DT, int ROWS>
@@ -977,19 +685,6 @@ __global__ void __launch_bounds__(32 * kFewDeep, kFewResident) few_rows_deep_ker
 
 // ------------------------------------------------------------------ host: one product
 
-inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t up(int64_t a, int64_t b) { return div_up(a, b) * b; }
-
-// A matrix as an operand: `rows` x `inner` (M or N by K) in 16 bits; mn: stored with its rows
-// along memory (inner x rows in memory).
-struct Operand {
-    const void* p;
-    int64_t rows, inner, ld;
-    bool mn;
-};
-
-bool tma_ready(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
-
 // How a product is cut: the tile's shape; tiles done whole, a multiple of what runs at one time; and the
 // parts along K that the rest is split into.
 struct Cut {
@@ -999,8 +694,6 @@ struct Cut {
     int64_t tail() const { return tiles_m * tiles_n - full; }
     int64_t tile_elems() const { return (int64_t)kBM * cg * bn; }
 };
-
-constexpr int kGb300Sms = 152;
 
 // The cut with the least estimated time.  One inner block (kBK) of a 256 x 256 tile on a pair of SMs takes
 // 0.336 us, 94 % of the tensor cores' measured rate.  A 128 x 128 tile on one SM takes 0.29: the same
@@ -1047,37 +740,6 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K)
 
 int64_t partial_bytes(const Cut& c) { return c.splits > 1 ? 4 * (int64_t)c.splits * c.tail() * c.tile_elems() : 0; }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
-{
-    static EncodeFn fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeFn>(f);
-    }();
-    return fn;
-}
-
-zero_status_t encode(CUtensorMap* map, const Operand& o, int dtype16, int box_rows)
-{
-    EncodeFn fn = encode_fn();
-    if (!fn) return fail(ZERO_ECUDA, "zero_linear: the driver has no cuTensorMapEncodeTiled");
-    const cuuint64_t dims[2] = {(cuuint64_t)(o.mn ? o.rows : o.inner), (cuuint64_t)(o.mn ? o.inner : o.rows)};
-    const cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)(o.mn ? kBK : box_rows)};
-    const cuuint32_t unit[2] = {1, 1};
-    const CUresult r = fn(map, dtype16 == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                          const_cast<void*>(o.p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_ECUDA, "zero_linear: a tensor map was refused (" + std::to_string((int)r) + ")");
-}
-
 template <int CG, int BN, int DT>
 zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
 {
@@ -1090,8 +752,6 @@ zero_status_t launch_shape(const GemmParams& P, int sms, cudaStream_t s)
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_linear: launch");
 }
-
-inline int grid_of(int64_t items, int sms, int per_sm) { return (int)std::max<int64_t>(1, std::min<int64_t>(div_up(items, 256), (int64_t)sms * per_sm)); }
 
 // D = A B^T with epilogue E but for its split tiles, whose parts are left in `partial` (partial_bytes of
 // it) and described in T; sum_tail ends them.
@@ -1112,8 +772,8 @@ zero_status_t product(const Operand& a, const Operand& b, int dtype16, const Epi
     GemmParams P;
     // few rows: no zeros are copied for the rest, whose results are not stored
     P.a_rows = c.cg == 1 && !a.mn && M < kBM ? (int32_t)up(M, 8) : kBM;
-    zero_status_t st = encode(&P.a, a, dtype16, P.a_rows);
-    if (st == ZERO_OK) st = encode(&P.b, b, dtype16, c.bn / c.cg);
+    zero_status_t st = encode(&P.a, a, dtype16, P.a_rows, "zero_linear");
+    if (st == ZERO_OK) st = encode(&P.b, b, dtype16, c.bn / c.cg, "zero_linear");
     if (st != ZERO_OK) return st;
     P.epi = E;
     P.partial = partial;
@@ -1314,8 +974,6 @@ zero_status_t check_workspace(const Layer& L, const void* workspace, int64_t byt
     return ZERO_OK;
 }
 
-int vec_flag(const void* p, int64_t ld, int flag) { return p && aligned(p, 16) && ld % 8 == 0 ? flag : 0; }
-
 // The copies of x and w that the layer needs, into D; x and w become theirs.
 void plan_copies(const Layer& L, char* ws, const void** x, const void** w, DzParams* D)
 {
@@ -1497,12 +1155,13 @@ catch (...) {
 
 zero_status_t zero_operators_check(void* stream)
 try {
-    uint32_t linear = 0, norm = 0;
+    uint32_t linear = 0, norm = 0, gated = 0;
     cudaError_t e = take_error_word(g_linear_error, &linear, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = take_norm_error(&norm, stream);
+    if (e == cudaSuccess) e = take_gated_error(&gated, stream);
     if (e != cudaSuccess) return cuda_fail(e, "zero_operators_check");
-    if (!linear && !norm) return ZERO_OK;
-    return fail(ZERO_ETIMEOUT, std::string(linear ? "zero_linear" : "zero_block_norm") +
+    if (!linear && !norm && !gated) return ZERO_OK;
+    return fail(ZERO_ETIMEOUT, std::string(linear ? "zero_linear" : norm ? "zero_block_norm" : "zero_gated") +
                                    ": a bounded wait ran out; outputs since the last check are not final");
 }
 catch (...) {
