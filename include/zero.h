@@ -564,7 +564,7 @@ zero_status_t zero_step_range_noalloc(const void* const* grad_contribs, int n_d,
 /* ---------------------------------------------------------------------------------------
  * Operators of a training program around the sharded step: what a gathered unit's weights are
  * used for and what fills the gradient contributions (zero_linear, zero_gated, zero_block_norm, with
- * their gradients), and an optimizer for tensors that are not sharded (zero_adamw).
+ * their gradients), and optimizers for tensors that are not sharded (zero_adamw, zero_muon).
  *
  * Each is asynchronous on `stream`, allocates nothing, may be captured in a CUDA graph and works
  * on the current device.  Pointers need the alignment of their element type; rows (or tensors)
@@ -715,8 +715,8 @@ zero_status_t zero_block_norm_workspace(const zero_block_norm_t* a, int64_t* byt
 zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspace, int64_t workspace_bytes,
                                        void* stream);
 
-/* Waits of the operators' kernels.  Those on shared-memory barriers are bounded, each by itself (zero_linear
- * and zero_gated 2 s, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
+/* Waits of the operators' kernels.  Those on shared-memory barriers are bounded, each by itself (zero_linear,
+ * zero_gated and zero_muon 2 s, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
  * product's block then gives its own 0.1 s).  Without a limit of their own are the hardware's: a cluster's barrier, which
  * every block of it reaches on every path, the allocation of tensor memory while another block on the SM
  * holds it, and the wait for the earlier work of the stream.  ZERO_ETIMEOUT if a bounded one ran out on the current device
@@ -793,6 +793,78 @@ zero_status_t zero_adamw_read(zero_adamw_t* h, void* stream, zero_step_result_t*
 
 /* NULL is ignored. */
 void zero_adamw_destroy(zero_adamw_t* h);
+
+/* How far an orthogonalised update moves the parameters, beside the learning rate: as it is; times
+ * sqrt(max(1, rows / cols)); times 0.2 sqrt(max(rows, cols)), which gives it AdamW's usual root mean square. */
+enum { ZERO_MUON_SCALE_NONE = 0, ZERO_MUON_SCALE_ASPECT = 1, ZERO_MUON_SCALE_RMS = 2 };
+#define ZERO_MUON_NESTEROV 1
+#define ZERO_MUON_MAX_STEPS 8
+#define ZERO_MUON_MAX_MATRICES 65536
+#define ZERO_MUON_MAX_SIZE 4194304       /* rows, cols */
+#define ZERO_MUON_MAX_SIDE 65536         /* the smaller of them */
+#define ZERO_MUON_BLOCK 256              /* each matrix's momentum starts on a multiple of it */
+
+typedef struct zero_muon zero_muon_t;
+
+typedef struct {
+    double lr, momentum, weight_decay, eps;      /* eps >= 1e-12 */
+    double coefficients[ZERO_MUON_MAX_STEPS][3]; /* a, b, c of each step; (3.4445, -4.7750, 2.0315) is usual */
+    int32_t steps;                               /* 1 .. ZERO_MUON_MAX_STEPS; 5 is usual */
+    int32_t scale;                               /* ZERO_MUON_SCALE_* */
+    int64_t flags;                               /* ZERO_MUON_NESTEROV */
+} zero_muon_hyper_t;
+
+typedef struct {
+    int64_t n_matrices, n_contribs, elems;
+    int64_t state_elems;     /* elements of each half of the momentum: every matrix's rounded up to ZERO_MUON_BLOCK */
+    int64_t workspace_bytes;
+} zero_muon_info_t;
+
+/* An optimizer whose update of a matrix is its momentum brought near the closest matrix with orthonormal rows or
+ * columns, for matrices that are whole on this GPU (a rank's own of a model whose matrices are dealt out whole):
+ *   g = sum of the n_contribs contributions / (n_contribs * loss_scale);  m' = mu m + (1 - mu) g
+ *   u = mu m' + (1 - mu) g  (ZERO_MUON_NESTEROV; else m');  X = u / (||u||_F + eps)
+ *   `steps` times:  X <- (a I + b G + c G^2) X,  G = X X^T   (from the right, X^T X, where rows > cols)
+ *   p <- p - lr weight_decay p;  p <- p - lr s X            (s: ZERO_MUON_SCALE_*)
+ * fp32 parameters, row-major and dense, and momentum; contributions, an optional copy of each parameter and an
+ * optional copy of X in dtype16.  The products' operands are fp16 whatever dtype16 is, in its range by powers of two,
+ * with fp32 sums: X is within about 0.3 % (2-norm) of the formula's where its smallest singular values are not far
+ * below rounding.  Host memory only; zero_muon_destroy. */
+zero_status_t zero_muon_create(const int64_t* rows, const int64_t* cols, int64_t n_matrices, int n_contribs, int dtype16,
+                               zero_muon_t** out);
+zero_status_t zero_muon_info(const zero_muon_t* h, zero_muon_info_t* out);
+
+/* Bind the caller's device buffers: per matrix the parameters (updated in place; params or an entry NULL: none), a
+ * 16-bit copy (params16 or an entry NULL: none) and where X goes (updates or an entry NULL: nowhere; one of
+ * parameters and update is needed); grads[r * n_matrices + i]: contribution r of matrix i; the momentum's two halves
+ * (info.state_elems floats each, 16-byte aligned, not overlapping; the first zero at the start of a training run):
+ * a step reads one and writes the other, and which one is current afterwards is zero_muon_read's `current`;
+ * workspace (info.workspace_bytes, 256-byte aligned).  t: steps applied so far (0 at the start; the first half is
+ * current); -1 with an earlier bind's workspace and momentum keeps its counters and half, to change the other
+ * addresses.  Synchronises `stream`. */
+zero_status_t zero_muon_bind(zero_muon_t* h, float* const* params, void* const* params16, void* const* updates,
+                             const void* const* grads, float* const momentum[2], void* workspace, int64_t t, void* stream);
+
+/* One step over every matrix.  Where the sum of squares of a matrix's u is not finite (a contribution is not, or fp32's
+ * range is left) the whole step is left out: parameters, copies, updates and the current momentum stay.  ZERO_ERANGE
+ * for coefficients that let singular values of at most 1 grow beyond 8. */
+zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, double loss_scale, void* stream);
+
+/* A step that h makes together with a plan's, applied or left out as one, with the plan's loss scale (as
+ * zero_adamw_check and zero_adamw_step_with, of which both may be part of the same step).  In the plan's step, on its
+ * stream: zero_muon_check, then zero_step of every bucket/unit, then zero_muon_step_with, then zero_step_finish.
+ * zero_muon_check forms the momentum and marks the plan's step where it is not finite; it may come later, but before
+ * zero_muon_step_with, in a step that is not offloaded.  The matrices' gradients are no part of the plan's norm and
+ * are not clipped: a common factor of the gradients leaves X as it is.  ZERO_ESTATE out of this order; ZERO_EINVAL
+ * where the two calls differ in momentum or flags. */
+zero_status_t zero_muon_check(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);
+zero_status_t zero_muon_step_with(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);
+
+/* t, skipped, skipped_total, finished and current after the work on `stream`, which it synchronises; grad_norm is -1. */
+zero_status_t zero_muon_read(zero_muon_t* h, void* stream, zero_step_result_t* out);
+
+/* NULL is ignored. */
+void zero_muon_destroy(zero_muon_t* h);
 
 /* Text of the last error of the calling thread (empty if none); valid until its next call. */
 const char* zero_last_error(void);

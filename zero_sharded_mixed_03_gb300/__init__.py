@@ -38,6 +38,13 @@ ZERO_NORM_PRE, ZERO_NORM_POST = 1, 2
 ZERO_NORM_MAX_DIM = 8192
 ZERO_ADAMW_BLOCK = 256
 ZERO_ADAMW_MAX_BLOCKS = 1073741824
+ZERO_MUON_SCALE_NONE, ZERO_MUON_SCALE_ASPECT, ZERO_MUON_SCALE_RMS = range(3)
+ZERO_MUON_NESTEROV = 1
+ZERO_MUON_MAX_STEPS = 8
+ZERO_MUON_MAX_MATRICES = 65536
+ZERO_MUON_MAX_SIZE = 4194304
+ZERO_MUON_MAX_SIDE = 65536
+ZERO_MUON_BLOCK = 256
 STATUS_NAMES = {0: "ZERO_OK", 1: "ZERO_EINVAL", 2: "ZERO_EALIGN", 3: "ZERO_ECUDA",
                 4: "ZERO_ESTATE", 5: "ZERO_ERANGE", 6: "ZERO_ETIMEOUT", 7: "ZERO_ENOMEM"}
 
@@ -54,7 +61,9 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_gated_workspace", "zero_gated", "zero_gated_backward",
             "zero_block_norm", "zero_block_norm_workspace", "zero_block_norm_backward",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
-            "zero_adamw_check", "zero_adamw_step_with", "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy"]
+            "zero_adamw_check", "zero_adamw_step_with", "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy",
+            "zero_muon_create", "zero_muon_info", "zero_muon_bind", "zero_muon_step", "zero_muon_check",
+            "zero_muon_step_with", "zero_muon_read", "zero_muon_destroy"]
 ZERO_NOALLOC_SCRATCH_BYTES = 256
 
 
@@ -148,6 +157,16 @@ class zero_adamw_info_t(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int64) for k in
                 ("n_tensors", "elems", "n_blocks", "state_elems", "moment_bytes", "scale_bytes",
                  "workspace_bytes")]
+
+
+class zero_muon_hyper_t(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_double) for k in ("lr", "momentum", "weight_decay", "eps")] +
+                [("coefficients", (ctypes.c_double * 3) * ZERO_MUON_MAX_STEPS), ("steps", ctypes.c_int32),
+                 ("scale", ctypes.c_int32), ("flags", ctypes.c_int64)])
+
+
+class zero_muon_info_t(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("n_matrices", "n_contribs", "elems", "state_elems", "workspace_bytes")]
 
 
 _lib = None
@@ -261,6 +280,18 @@ def lib() -> ctypes.CDLL:
             f.restype = st
         L.zero_adamw_destroy.restype = None
         L.zero_adamw_destroy.argtypes = [_vp]
+        L.zero_muon_create.argtypes = [_vp, _vp, _i64, _int, _int, ctypes.POINTER(_vp)]
+        L.zero_muon_info.argtypes = [_vp, ctypes.POINTER(zero_muon_info_t)]
+        L.zero_muon_bind.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+        L.zero_muon_step.argtypes = [_vp, ctypes.POINTER(zero_muon_hyper_t), ctypes.c_double, _vp]
+        L.zero_muon_check.argtypes = [_vp, _vp, ctypes.POINTER(zero_muon_hyper_t), _vp]
+        L.zero_muon_step_with.argtypes = [_vp, _vp, ctypes.POINTER(zero_muon_hyper_t), _vp]
+        L.zero_muon_read.argtypes = [_vp, _vp, ctypes.POINTER(zero_step_result_t)]
+        for f in (L.zero_muon_create, L.zero_muon_info, L.zero_muon_bind, L.zero_muon_step, L.zero_muon_check,
+                  L.zero_muon_step_with, L.zero_muon_read):
+            f.restype = st
+        L.zero_muon_destroy.restype = None
+        L.zero_muon_destroy.argtypes = [_vp]
         _lib = L
     return _lib
 
@@ -607,6 +638,78 @@ def zero_adamw_read(handle: int, stream: int = 0) -> zero_step_result_t:
 def zero_adamw_destroy(handle: int) -> None:
     if handle:
         lib().zero_adamw_destroy(handle)
+
+
+def zero_muon_create(rows: Sequence[int], cols: Sequence[int], n_contribs: int = 1, dtype16: int = ZERO_BF16) -> int:
+    if len(rows) != len(cols):
+        raise ValueError(f"zero_muon_create: {len(rows)} row counts for {len(cols)} column counts")
+    out = _vp()
+    _check(lib().zero_muon_create(_i64_array(rows), _i64_array(cols), len(rows), n_contribs, dtype16, ctypes.byref(out)))
+    return int(out.value)
+
+
+def zero_muon_info(handle: int) -> zero_muon_info_t:
+    info = zero_muon_info_t()
+    _check(lib().zero_muon_info(handle, ctypes.byref(info)))
+    return info
+
+
+def zero_muon_bind(handle: int, params: Optional[Sequence[Optional[int]]], params16: Optional[Sequence[Optional[int]]],
+                   updates: Optional[Sequence[Optional[int]]], grads: Sequence[int], momentum: Sequence[int],
+                   workspace: int, t: int = 0, stream: int = 0) -> None:
+    """grads: contribution r of matrix i at r * n_matrices + i; see include/zero.h."""
+    info = zero_muon_info(handle)
+    n = info.n_matrices
+    for ptrs in (params, params16, updates):
+        if ptrs is not None and len(ptrs) != n:
+            raise ValueError(f"zero_muon_bind: {len(ptrs)} pointers for {n} matrices")
+    if len(momentum) != 2:
+        raise ValueError("zero_muon_bind: the momentum has two halves")
+    if len(grads) != n * info.n_contribs:
+        raise ValueError(f"zero_muon_bind: {len(grads)} pointers for {info.n_contribs} contributions of {n} matrices")
+    lists = [_ptr_array(ptrs) if ptrs is not None else None for ptrs in (params, params16, updates)]
+    _check(lib().zero_muon_bind(handle, *lists, _ptr_array(grads), _ptr_array(momentum), workspace or None, t,
+                                stream or None))
+
+
+def zero_muon_step(handle: int, hyper: zero_muon_hyper_t, loss_scale: float = 1.0, stream: int = 0) -> None:
+    _check(lib().zero_muon_step(handle, ctypes.byref(hyper), loss_scale, stream or None))
+
+
+def zero_muon_check(handle: int, plan: int, hyper: zero_muon_hyper_t, stream: int = 0) -> None:
+    """Form the momentum as part of the plan's step: its loss scale and its skip decision."""
+    _check(lib().zero_muon_check(handle, plan, ctypes.byref(hyper), stream or None))
+
+
+def zero_muon_step_with(handle: int, plan: int, hyper: zero_muon_hyper_t, stream: int = 0) -> None:
+    """The optimizer's part of the plan's open step, before its finish; see include/zero.h."""
+    _check(lib().zero_muon_step_with(handle, plan, ctypes.byref(hyper), stream or None))
+
+
+def zero_muon_read(handle: int, stream: int = 0) -> zero_step_result_t:
+    res = zero_step_result_t()
+    _check(lib().zero_muon_read(handle, stream or None, ctypes.byref(res)), res)
+    return res
+
+
+def zero_muon_destroy(handle: int) -> None:
+    if handle:
+        lib().zero_muon_destroy(handle)
+
+
+def muon_hyper(lr=2e-4, momentum=0.95, weight_decay=0.1, eps=1e-7, steps=5, coefficients=(3.4445, -4.7750, 2.0315),
+               nesterov=True, scale=ZERO_MUON_SCALE_RMS) -> zero_muon_hyper_t:
+    """coefficients: a, b, c, or one such triple for each step."""
+    h = zero_muon_hyper_t(lr, momentum, weight_decay, eps, steps=steps, scale=scale,
+                          flags=ZERO_MUON_NESTEROV if nesterov else 0)
+    each = list(coefficients)
+    if each and not hasattr(each[0], "__len__"):
+        each = [each] * ZERO_MUON_MAX_STEPS
+    if len(each) < steps:
+        raise ValueError(f"muon_hyper: coefficients of {len(each)} steps for {steps}")
+    for k, abc in enumerate(each[:ZERO_MUON_MAX_STEPS]):
+        h.coefficients[k][:] = tuple(abc)
+    return h
 
 
 def hyper(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, max_grad_norm=0.0,

@@ -84,6 +84,7 @@ struct GatedWork {
         I.kb = P.k_blocks;
         return I;
     }
+    __device__ __forceinline__ void begin(const Item&) const {}
     __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (P.a_rows + kBRows) * (kBK * 2); }
     __device__ __forceinline__ bool a_mn(const Item&) const { return MODE == kWeights; }
     __device__ __forceinline__ bool b_mn(const Item&) const { return P.b_mn; }

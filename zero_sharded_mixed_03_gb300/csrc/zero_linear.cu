@@ -25,6 +25,7 @@ namespace zero {
 
 cudaError_t take_norm_error(uint32_t* word, void* stream);    // zero_norm.cu
 cudaError_t take_gated_error(uint32_t* word, void* stream);   // zero_gated.cu
+cudaError_t take_muon_error(uint32_t* word, void* stream);    // zero_muon.cu
 
 namespace {
 
@@ -1155,13 +1156,14 @@ catch (...) {
 
 zero_status_t zero_operators_check(void* stream)
 try {
-    uint32_t linear = 0, norm = 0, gated = 0;
+    uint32_t linear = 0, norm = 0, gated = 0, muon = 0;
     cudaError_t e = take_error_word(g_linear_error, &linear, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = take_norm_error(&norm, stream);
     if (e == cudaSuccess) e = take_gated_error(&gated, stream);
+    if (e == cudaSuccess) e = take_muon_error(&muon, stream);
     if (e != cudaSuccess) return cuda_fail(e, "zero_operators_check");
-    if (!linear && !norm && !gated) return ZERO_OK;
-    return fail(ZERO_ETIMEOUT, std::string(linear ? "zero_linear" : norm ? "zero_block_norm" : "zero_gated") +
+    if (!linear && !norm && !gated && !muon) return ZERO_OK;
+    return fail(ZERO_ETIMEOUT, std::string(linear ? "zero_linear" : norm ? "zero_block_norm" : gated ? "zero_gated" : "zero_muon") +
                                    ": a bounded wait ran out; outputs since the last check are not final");
 }
 catch (...) {

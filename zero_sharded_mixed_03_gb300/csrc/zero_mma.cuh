@@ -251,7 +251,7 @@ struct GemmShape {
 //   int count                               tiles, walked with the grid's stride
 //   Item item(int)                          where a tile is; Item::kb: its inner blocks, at least one
 //   uint32_t bytes(Item)                    what a stage's copies bring, to both blocks of a pair
-//   load(Item, kb, a, b, bar, rank)         those copies
+//   begin(Item); load(Item, kb, a, b, bar, rank)   those copies: what precedes a tile's, and a stage's
 //   a_mn(Item), b_mn(Item), idesc(Item)     how the operands lie, and the product's descriptor
 //   finish(Item, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
@@ -314,6 +314,7 @@ struct Tiles {
                 for (int i = first; i < work.count && ok; i += step) {
                     const typename W::Item I = work.item(i);
                     const uint32_t bytes = work.bytes(I);
+                    work.begin(I);
                     for (int kb = 0; kb < I.kb; ++kb, ++k) {
                         const uint32_t s = k % S::kStages, use = k / S::kStages;
                         if (use > 0 && !mbar_wait(empty0 + 8 * s, (use - 1) & 1, kGemmWaitNs)) {

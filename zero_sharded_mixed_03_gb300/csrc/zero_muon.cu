@@ -1,0 +1,998 @@
+// zero_muon.cu -- an optimizer whose update of a matrix is orthogonalised (zero_muon_*):
+//   g = sum of the ranks' contributions / (N_d loss_scale);  m' = mu m + (1 - mu) g
+//   u = mu m' + (1 - mu) g (nesterov), or m';  X = u / (||u||_F + eps)
+//   X <- (a I + b G + c G^2) X, G = X X^T, `steps` times (a Newton-Schulz iteration for the polar factor; X^T X from
+//   the right where X has more rows than columns)
+//   p <- p - lr wd p;  p <- p - lr s X
+//
+// A pass over the contributions forms m' and the norms, one over the momentum the first X; then each iteration is three
+// products on the tensor cores, each of them one launch for the tiles of every matrix: G and the polynomial of it, of
+// which the upper triangle's tiles are multiplied and written twice, and the polynomial times X.  Nothing is
+// transposed in memory: a tensor map takes X along its rows or along its columns.
+//
+// Operands are fp16 whatever the gradients' type, times powers of two that keep them in its range (the iterates' are
+// bounded: ||X||_2 <= 1 at first, and the coefficients give the rest).  Rounding to bf16's 8 bits costs 1 to 3 % of the
+// result, as small singular values grow by a^steps (485) and what rounding adds to them grows with them; fp16's 11 bits
+// 0.13 to 0.4 %, and with the first iterates as sums of two fp16 numbers (the products take the first; a X, which is
+// nearly all of small singular values' growth, both) 0.1 to 0.3 %.  Sums are fp32.
+#include <cmath>
+#include <cstring>
+#include <memory>
+#include <vector>
+
+#include "zero_mma.cuh"
+
+namespace zero {
+namespace {
+
+// Set by a kernel whose bounded wait ran out (zero_operators_check reads and clears it).
+__device__ uint32_t g_muon_error;
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 8192;              // elements of a matrix that a block takes at a time
+constexpr int kStateBlock = 256;          // each matrix's momentum starts on a multiple of it
+constexpr int kTwice = 2;                 // iterations whose X is the sum of two fp16 numbers
+constexpr float kLow = 2048.0f;           // the second of them is stored times this
+
+struct MuonState {
+    uint32_t flag;          // the open step's gradients are not finite
+    uint32_t cur;           // the momentum's current half
+    uint32_t last_skipped;
+    uint32_t closed;        // blocks of the last pass that are done
+    int64_t t, skipped, finished;
+};
+static_assert(sizeof(MuonState) <= 256, "MuonState fits its slot");
+
+struct alignas(128) MuonTensor {
+    CUtensorMap xk[2], xm[2];    // X's two buffers, taken along their rows and along their columns
+    CUtensorMap ak, bk;          // G, and the polynomial
+    uint16_t *x[2], *low;        // rows x ldx
+    uint16_t *a, *b;             // m x ldm
+    float* p;                    // NULL: no parameters
+    uint16_t *p16, *update;      // may be NULL
+    int64_t at;                  // its first momentum
+    float aspect, rms;           // factors of the update
+    int32_t rows, cols, m, ldx, ldm;
+    int32_t wide;                // rows <= cols: G = X X^T
+    int32_t vec_g, vec_p;        // 16-byte accesses to the contributions; to p, p16 and update
+    int32_t chunks;              // of the first pass
+};
+
+// A piece of a matrix's elements, or a tile of it (m << 16 | n).
+struct Piece {
+    int32_t tensor, at;
+};
+
+struct MuonParams {
+    MuonTensor* tensors;
+    const Piece* pieces;
+    const void* const* grads;    // [tensor][n_d]
+    float* momentum[2];
+    MuonState* st;
+    DevState* plan;              // a sharded step that this one is part of, or NULL
+    double* slots;               // [piece of the first pass] sums of squares
+    float* scale;                // [tensor] 1 / (norm + eps)
+    uint32_t* tickets;           // [tensor]
+    int32_t count, n_d, nesterov, src, how;
+    float inv, mu, nu, sigma, lr, decay;   // nu = 1 - mu; sigma: X's factor in fp16
+    double eps;
+};
+
+__device__ __forceinline__ float contribution_scale(const MuonParams& P)
+{
+    if (!P.plan) return P.inv;
+    const volatile DevState* plan = P.plan;
+    return __double2float_rn(__ddiv_rn(1.0, (double)P.n_d * plan->scale));
+}
+
+__device__ __forceinline__ float ahead(float m0, float m1, const MuonParams& P)
+{
+    // mu m' + (1 - mu) g, (1 - mu) g = m' - mu m
+    return P.nesterov ? fmaf(P.mu, m1, fmaf(-P.mu, m0, m1)) : m1;
+}
+
+// ------------------------------------------------------------------ the contributions into the momentum
+
+// Eight elements from e on (n of them there): the sum of the contributions.
+template <int DT>
+__device__ __forceinline__ void sum_contributions(const void* const* grads, int n_d, int64_t e, int n, bool vec, float (&g)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = 0.0f;
+    auto add8 = [&](const uint4& w) {
+        float x[8];
+        widen2<DT>(w.x, x[0], x[1]);
+        widen2<DT>(w.y, x[2], x[3]);
+        widen2<DT>(w.z, x[4], x[5]);
+        widen2<DT>(w.w, x[6], x[7]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] += x[j];
+    };
+    int r = 0;
+    if (vec && n == 8) {
+        for (; r + 4 <= n_d; r += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(grads[r + i]) + e));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add8(w[i]);
+        }
+        for (; r < n_d; ++r) add8(__ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(grads[r]) + e)));
+    } else {
+        for (; r < n_d; ++r) {
+            const uint16_t* p = static_cast<const uint16_t*>(grads[r]) + e;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) g[j] += widen1<DT>(p[j]);
+        }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) muon_reduce_kernel(const __grid_constant__ MuonParams P)
+{
+    after_earlier_work();
+    __shared__ double warp_sum[kThreads / 32];
+    __shared__ bool last;
+    const uint32_t cur = *(const volatile uint32_t*)&P.st->cur;
+    const float *from = P.momentum[cur & 1];
+    float* to = P.momentum[(cur & 1) ^ 1];
+    const float inv = contribution_scale(P);
+    for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
+        const Piece piece = P.pieces[i];
+        const MuonTensor& T = P.tensors[piece.tensor];
+        const int64_t elems = (int64_t)T.rows * T.cols, e0 = (int64_t)piece.at * kChunk;
+        const void* const* grads = P.grads + (int64_t)piece.tensor * P.n_d;
+        float sum = 0.0f;
+#pragma unroll 2
+        for (int k = 0; k < kChunk / (8 * kThreads); ++k) {
+            const int64_t e = e0 + ((int64_t)k * kThreads + threadIdx.x) * 8;
+            const int n = (int)min((int64_t)8, elems - e);
+            if (n <= 0) break;
+            float g[8];
+            sum_contributions<DT>(grads, P.n_d, e, n, T.vec_g, g);
+            // the momentum's rows of eight are whole: it is padded
+            const float4* q = reinterpret_cast<const float4*>(from + T.at + e);
+            const float4 a = __ldcs(q), b = __ldcs(q + 1);
+            const float m0[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            float m1[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m1[j] = j < n ? fmaf(P.mu, m0[j], P.nu * (g[j] * inv)) : 0.0f;
+                const float u = j < n ? ahead(m0[j], m1[j], P) : 0.0f;
+                sum = fmaf(u, u, sum);
+            }
+            float4* o = reinterpret_cast<float4*>(to + T.at + e);
+            o[0] = make_float4(m1[0], m1[1], m1[2], m1[3]);
+            o[1] = make_float4(m1[4], m1[5], m1[6], m1[7]);
+        }
+        const double s = block_sum_fixed<kThreads>((double)sum, warp_sum);
+        const int first = i - piece.at;          // a matrix's pieces follow one another
+        if (threadIdx.x == 0) {
+            P.slots[i] = s;
+            __threadfence();
+            last = atomicAdd(&P.tickets[piece.tensor], 1u) == (uint32_t)T.chunks - 1;
+        }
+        __syncthreads();
+        if (!last) continue;
+        __threadfence();
+        const volatile double* slots = P.slots + first;
+        double x = 0.0;
+        for (int k = threadIdx.x; k < T.chunks; k += kThreads) x += slots[k];
+        const double norm2 = block_sum_fixed<kThreads>(x, warp_sum);
+        if (threadIdx.x == 0) {
+            P.tickets[piece.tensor] = 0;
+            P.scale[piece.tensor] = (float)(1.0 / (sqrt(norm2) + P.eps));
+            if (!isfinite(norm2)) {
+                atomicOr(P.plan ? &P.plan->flag : &P.st->flag, 1u);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ the first X
+
+__device__ __forceinline__ void two_halves(const float (&x)[8], uint32_t (&hi)[4], uint32_t (&low)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a, b;
+        hi[j] = narrow2<ZERO_FP16>(x[2 * j], x[2 * j + 1]);
+        widen2<ZERO_FP16>(hi[j], a, b);
+        low[j] = narrow2<ZERO_FP16>((x[2 * j] - a) * kLow, (x[2 * j + 1] - b) * kLow);
+    }
+}
+
+// Piece `at` of the matrix in groups of eight columns: f(row, column, columns there, group's place in X).
+template <typename F>
+__device__ __forceinline__ void for_groups(const MuonTensor& T, int at, F&& f)
+{
+    const int groups = T.ldx / 8;
+    const int64_t total = (int64_t)T.rows * groups;
+#pragma unroll 2
+    for (int k = 0; k < kChunk / (8 * kThreads); ++k) {
+        const int64_t i = (int64_t)at * (kChunk / 8) + (int64_t)k * kThreads + threadIdx.x;
+        if (i >= total) break;
+        int64_t row = 0;
+        int col = 0;
+        if (T.cols == T.ldx) {
+            f(i * 8, 8, i * 8);          // the matrix is as X is laid out
+        } else {
+            row = i / groups;
+            col = (int)(i - row * groups) * 8;
+            f(row * T.cols + col, min(8, T.cols - col), i * 8);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_constant__ MuonParams P)
+{
+    after_earlier_work();
+    const uint32_t cur = *(const volatile uint32_t*)&P.st->cur;
+    for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
+        const Piece piece = P.pieces[i];
+        const MuonTensor& T = P.tensors[piece.tensor];
+        const float scale = P.scale[piece.tensor];
+        const float *old = P.momentum[cur & 1] + T.at, *now = P.momentum[(cur & 1) ^ 1] + T.at;
+        for_groups(T, piece.at, [&](int64_t e, int n, int64_t out) {
+            float m0[8], m1[8], x[8];
+            if (T.cols == T.ldx) {
+                const float4* q = reinterpret_cast<const float4*>(now + e);
+                const float4 a = q[0], b = q[1];
+                m1[0] = a.x; m1[1] = a.y; m1[2] = a.z; m1[3] = a.w;
+                m1[4] = b.x; m1[5] = b.y; m1[6] = b.z; m1[7] = b.w;
+                if (P.nesterov) {
+                    const float4* r = reinterpret_cast<const float4*>(old + e);
+                    const float4 c = r[0], d = r[1];
+                    m0[0] = c.x; m0[1] = c.y; m0[2] = c.z; m0[3] = c.w;
+                    m0[4] = d.x; m0[5] = d.y; m0[6] = d.z; m0[7] = d.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    m1[j] = j < n ? now[e + j] : 0.0f;
+                    m0[j] = j < n && P.nesterov ? old[e + j] : 0.0f;
+                }
+            }
+            uint32_t hi[4], low[4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (ahead(m0[j], m1[j], P) * scale) * P.sigma;
+            two_halves(x, hi, low);
+            *reinterpret_cast<uint4*>(T.x[0] + out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(T.low + out) = make_uint4(low[0], low[1], low[2], low[3]);
+        });
+    }
+}
+
+// ------------------------------------------------------------------ the products
+
+enum { kGram = 0, kPoly = 1, kNext = 2 };
+
+struct ProductParams {
+    const MuonTensor* tensors;
+    const Piece* tiles;
+    int32_t count, src;          // src: X's buffer that is read
+    int32_t twice, keep_low;     // kNext: X is a sum of two; its successor is to be
+    float scale;                 // of the accumulator
+    float lin, diag;             // kPoly: of G, of I; kNext: lin: of X
+};
+
+// row `lane` of a tile: x, written as its transpose at (col0, row0)
+__device__ __forceinline__ void put_tile_across(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile16_at(stage, j, lane >> 3) + (lane & 7) * 2), "h"(narrow1<ZERO_FP16>(x[j])) : "memory");
+    __syncwarp();
+    store_tile16(stage, lane, D, col0, row0);
+    __syncwarp();
+}
+
+template <int CG, int BN, int KIND>
+struct MuonWork {
+    const ProductParams& P;
+    int count;
+    struct Item {
+        const MuonTensor* T;
+        int m, n, kb;
+        bool wide;
+    };
+
+    // The tensor maps that a tile's copies take, written by the host into memory that may have held others.
+    __device__ __forceinline__ static void see(const CUtensorMap* map)
+    {
+        asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+    }
+    __device__ __forceinline__ void begin(const Item& I) const
+    {
+        const MuonTensor& T = *I.T;
+        if constexpr (KIND == kGram) {
+            see(I.wide ? &T.xk[P.src] : &T.xm[P.src]);
+        } else if constexpr (KIND == kPoly) {
+            see(&T.ak);
+        } else {
+            see(&T.bk);
+            see(I.wide ? &T.xm[P.src] : &T.xk[P.src]);
+        }
+    }
+
+    __device__ __forceinline__ Item item(int i) const
+    {
+        const Piece t = P.tiles[i];
+        Item I;
+        I.T = P.tensors + t.tensor;
+        I.m = t.at >> 16;
+        I.n = t.at & 0xFFFF;
+        I.wide = I.T->wide;
+        const int inner = KIND == kGram ? (I.wide ? I.T->cols : I.T->rows) : I.T->m;
+        I.kb = (inner + kBK - 1) / kBK;
+        return I;
+    }
+    __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (kBM + BN / CG) * (kBK * 2); }
+    __device__ __forceinline__ bool a_mn(const Item& I) const { return KIND == kGram && !I.wide; }
+    __device__ __forceinline__ bool b_mn(const Item& I) const { return (KIND == kGram && !I.wide) || (KIND == kNext && I.wide); }
+    __device__ __forceinline__ uint32_t idesc(const Item& I) const
+    {
+        return (1u << 4) | ((a_mn(I) ? 1u : 0u) << 15) | ((b_mn(I) ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((kBM * CG) >> 4) << 24);
+    }
+
+    // 128 rows of an operand: along K in one box, along its own rows in two
+    __device__ __forceinline__ static void bring(const CUtensorMap* map, bool mn, uint32_t at, int row, int k, uint32_t bar)
+    {
+        if (mn) {
+            tma_load_2d<CG>(at, map, row, k, bar);
+            tma_load_2d<CG>(at + kBK * 128, map, row + 64, k, bar);
+        } else {
+            tma_load_2d<CG>(at, map, k, row, bar);
+        }
+    }
+
+    __device__ __forceinline__ void load(const Item& I, int kb, uint32_t a, uint32_t b, uint32_t bar, int rank) const
+    {
+        const int row_a = (I.m * CG + rank) * kBM, row_b = I.n * BN + rank * (BN / CG), k = kb * kBK;
+        const MuonTensor& T = *I.T;
+        if constexpr (KIND == kGram) {
+            const CUtensorMap* map = I.wide ? &T.xk[P.src] : &T.xm[P.src];
+            bring(map, !I.wide, a, row_a, k, bar);
+            bring(map, !I.wide, b, row_b, k, bar);
+        } else if constexpr (KIND == kPoly) {
+            bring(&T.ak, false, a, row_a, k, bar);
+            bring(&T.ak, false, b, row_b, k, bar);
+        } else {
+            bring(I.wide ? &T.bk : &T.xk[P.src], false, a, row_a, k, bar);
+            bring(I.wide ? &T.xm[P.src] : &T.bk, I.wide, b, row_b, k, bar);
+        }
+    }
+
+    __device__ __forceinline__ void finish(const Item& I, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    {
+        const MuonTensor& T = *I.T;
+        const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
+        Matrix16 D;
+        if constexpr (KIND == kNext) D = Matrix16{T.x[P.src ^ 1], T.ldx, T.rows, T.ldx, 1};
+        else D = Matrix16{KIND == kGram ? T.a : T.b, T.ldm, T.m, T.ldm, 1};
+        for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
+            const int64_t col0 = (int64_t)I.n * BN + c;
+            if (col0 >= D.cols || row0 >= D.rows) break;
+            float x[32];
+            tmem_load32(acc + c, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] *= P.scale;
+            if constexpr (KIND == kPoly) {
+                add_tile<ZERO_FP16>(stage, lane, P.lin, x, Matrix16{T.a, T.ldm, T.m, T.ldm, 1}, row0, col0);
+                if (row0 == col0) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] += j == lane ? P.diag : 0.0f;
+                }
+            }
+            if constexpr (KIND == kNext) {
+                const Matrix16 low{T.low, T.ldx, T.rows, T.ldx, 1};
+                if (P.twice) {
+                    add_tile<ZERO_FP16>(stage, lane, P.lin, x, Matrix16{T.x[P.src], T.ldx, T.rows, T.ldx, 1}, row0, col0);
+                    add_tile<ZERO_FP16>(stage + kTile16Bytes, lane, P.lin * (1.0f / kLow), x, low, row0, col0);
+                }
+                put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
+                if (P.keep_low) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
+                    put_tile<ZERO_FP16>(stage + kTile16Bytes, lane, x, low, row0, col0);
+                }
+            } else {
+                put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
+                // the tile on the other side of the diagonal is this one's transpose
+                if (I.m != I.n) put_tile_across(stage + kTile16Bytes, lane, x, D, row0, col0);
+            }
+        }
+    }
+};
+
+template <int CG, int BN, int KIND>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) muon_product_kernel(const __grid_constant__ ProductParams P)
+{
+    extern __shared__ unsigned char smem_raw[];
+    Tiles<CG, BN> T;
+    T.open(smem_raw);
+    after_earlier_work();
+    T.run(MuonWork<CG, BN, KIND>{P, P.count}, &g_muon_error);
+}
+
+// ------------------------------------------------------------------ the parameters
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) muon_apply_kernel(const __grid_constant__ MuonParams P)
+{
+    after_earlier_work();
+    bool skip = (*(const volatile uint32_t*)&P.st->flag) != 0;
+    if (P.plan) {
+        const volatile DevState* plan = P.plan;
+        skip = (plan->flag | plan->error) != 0;
+    }
+    if (!skip) {
+        for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
+            const Piece piece = P.pieces[i];
+            const MuonTensor& T = P.tensors[piece.tensor];
+            const float step = P.lr * (P.how == ZERO_MUON_SCALE_RMS ? T.rms : P.how == ZERO_MUON_SCALE_ASPECT ? T.aspect : 1.0f);
+            const float unit = 1.0f / P.sigma;      // a power of two
+            const uint16_t* x16 = T.x[P.src];
+            for_groups(T, piece.at, [&](int64_t e, int n, int64_t at) {
+                const uint4 w = *reinterpret_cast<const uint4*>(x16 + at);
+                float x[8];
+                widen2<ZERO_FP16>(w.x, x[0], x[1]);
+                widen2<ZERO_FP16>(w.y, x[2], x[3]);
+                widen2<ZERO_FP16>(w.z, x[4], x[5]);
+                widen2<ZERO_FP16>(w.w, x[6], x[7]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= unit;
+                if (T.update) store8<DT>(T.update + e, T.vec_p, n, x);
+                if (!T.p) return;
+                float p[8];
+                if (T.vec_p) {
+                    const float4* q = reinterpret_cast<const float4*>(T.p + e);
+                    const float4 a = q[0], b = q[1];
+                    p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
+                    p[4] = b.x; p[5] = b.y; p[6] = b.z; p[7] = b.w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[j] = j < n ? T.p[e + j] : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = fmaf(-step, x[j], fmaf(-P.decay, p[j], p[j]));
+                if (T.vec_p) {
+                    float4* q = reinterpret_cast<float4*>(T.p + e);
+                    q[0] = make_float4(p[0], p[1], p[2], p[3]);
+                    q[1] = make_float4(p[4], p[5], p[6], p[7]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < n) T.p[e + j] = p[j];
+                }
+                if (T.p16) store8<DT>(T.p16 + e, T.vec_p, n, p);
+            });
+        }
+    }
+    // the last block to finish closes the step: every block has read the flag by then
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (atomicAdd(&P.st->closed, 1u) == gridDim.x - 1) {
+            volatile MuonState* st = P.st;
+            st->closed = 0;
+            st->flag = 0;
+            st->finished = st->finished + 1;
+            st->last_skipped = skip ? 1u : 0u;
+            if (skip) {
+                st->skipped = st->skipped + 1;
+            } else {
+                st->t = st->t + 1;
+                st->cur = (st->cur & 1) ^ 1;
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t take_muon_error(uint32_t* word, void* stream) { return take_error_word(g_muon_error, word, static_cast<cudaStream_t>(stream)); }
+
+}  // namespace zero
+
+struct zero_muon {
+    int n_d = 0, dtype16 = 0;
+    std::vector<int64_t> rows, cols;
+    int64_t elems = 0, state_elems = 0;
+    // tiles of 128 or 256 for the symmetric products and for the others
+    int cg[2] = {1, 1};
+    std::vector<zero::Piece> chunks, groups, tiles[2];
+    // the workspace's pieces
+    int64_t at_tensors = 0, at_grads = 0, at_chunks = 0, at_groups = 0, at_tiles[2] = {0, 0}, at_slots = 0, at_scale = 0, at_tickets = 0,
+            at_data = 0, bytes = 0;
+    // bound buffers (caller-owned)
+    bool bound = false;
+    int device = -1;
+    float* momentum[2] = {nullptr, nullptr};
+    void* workspace = nullptr;
+    // the sharded step (zero_plan::step_no) that zero_muon_check, zero_muon_step_with joined last
+    int64_t checked_in = 0, stepped_in = 0;
+    double checked_mu = 0.0;
+    int64_t checked_flags = 0;
+};
+
+namespace zero {
+namespace {
+
+// What X, G and the polynomial are multiplied by in fp16: powers of two that leave room for rounding below 65504.
+struct Range {
+    double sigma = 1.0, alpha = 1.0, beta = 1.0;
+};
+
+double power_below(double limit) { return std::exp2(std::floor(std::log2(limit))); }
+
+// Bounds of the iterates' singular values from the coefficients, by sampling s -> |a s + b s^3 + c s^5| and the
+// polynomial itself with slack for what lies between the samples and for rounding.  False: they grow too far.
+bool find_range(const zero_muon_hyper_t& hyper, Range* r)
+{
+    constexpr int kSamples = 4096;
+    double hi = 1.0, x = 1.0, g = 1.0, q = 0.0;
+    for (int k = 0; k < hyper.steps; ++k) {
+        const double* c = hyper.coefficients[k];
+        double next = 0.0;
+        for (int i = 0; i <= kSamples; ++i) {
+            const double s = hi * i / kSamples, s2 = s * s, rest = c[1] * s2 + c[2] * s2 * s2, poly = c[0] + rest;
+            next = std::max(next, std::fabs(s * poly));
+            q = std::max(q, std::max(std::fabs(poly), std::fabs(rest)));
+        }
+        hi = std::max(1.01 * next, 1e-6);
+        if (!(hi <= 8.0) || !(q <= 1024.0)) return false;
+        x = std::max(x, hi);
+        g = std::max(g, hi * hi);
+    }
+    r->sigma = power_below(24000.0 / x);
+    r->alpha = power_below(24000.0 / g);
+    r->beta = power_below(24000.0 / std::max(q, 1e-3));
+    return true;
+}
+
+// Tiles of every matrix for both kinds of product, longest inner dimension first, so that the last ones are short.
+void cut_tiles(zero_muon* h, int which, int cg, std::vector<Piece>* out, double* us)
+{
+    const int tile = 128 * cg;
+    std::vector<size_t> order(h->rows.size());
+    for (size_t i = 0; i < order.size(); ++i) order[i] = i;
+    auto inner = [&](size_t i) { return which == 0 ? std::max(h->rows[i], h->cols[i]) : std::min(h->rows[i], h->cols[i]); };
+    std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return inner(a) > inner(b); });
+    double work = 0.0, longest = 0.0;
+    const double block_us = cg == 2 ? 0.336 : 0.29;
+    for (const size_t i : order) {
+        const int64_t rows = h->rows[i], cols = h->cols[i], m = std::min(rows, cols);
+        if (m == 0) continue;
+        const int64_t tm = div_up(which == 0 ? m : rows, tile), tn = div_up(which == 0 ? m : cols, tile);
+        const double each = div_up(inner(i), kBK) * block_us;
+        longest = std::max(longest, each);
+        // groups of eight tile rows, column by column, so that what runs at one time shares its operands
+        for (int64_t g = 0; g < tm; g += 8)
+            for (int64_t n = 0; n < tn; ++n)
+                for (int64_t k = g; k < std::min(tm, g + 8); ++k) {
+                    if (which == 0 && k > n) continue;
+                    out->push_back(Piece{(int32_t)i, (int32_t)(k << 16 | n)});
+                    work += each;
+                }
+    }
+    const double slots = kGb300Sms / cg;
+    *us = std::max(longest, work / slots) + 0.5 * longest;
+}
+
+zero_status_t check_hyper(const zero_muon_hyper_t* hyper, Range* range, const char* who)
+{
+    const std::string w = std::string(who) + ": ";
+    if (!hyper) return fail(ZERO_EINVAL, w + "NULL argument");
+    if (!(hyper->momentum >= 0.0 && hyper->momentum < 1.0)) return fail(ZERO_EINVAL, w + "momentum must be in [0, 1)");
+    if (!std::isfinite(hyper->lr) || !std::isfinite(hyper->weight_decay) || !(hyper->eps >= 1e-12) || !std::isfinite(hyper->eps))
+        return fail(ZERO_EINVAL, w + "bad hyperparameter");
+    if (hyper->steps < 1 || hyper->steps > ZERO_MUON_MAX_STEPS) return fail(ZERO_EINVAL, w + "steps must be in 1 .. ZERO_MUON_MAX_STEPS");
+    if (hyper->scale < ZERO_MUON_SCALE_NONE || hyper->scale > ZERO_MUON_SCALE_RMS) return fail(ZERO_EINVAL, w + "bad scale");
+    if (hyper->flags & ~(int64_t)ZERO_MUON_NESTEROV) return fail(ZERO_EINVAL, w + "unknown flag");
+    for (int k = 0; k < hyper->steps; ++k)
+        for (int j = 0; j < 3; ++j)
+            if (!std::isfinite(hyper->coefficients[k][j])) return fail(ZERO_EINVAL, w + "a coefficient is not finite");
+    if (!find_range(*hyper, range)) return fail(ZERO_ERANGE, w + "the coefficients let singular values of at most 1 grow beyond 8");
+    return ZERO_OK;
+}
+
+zero_status_t ready(const zero_muon* h, const char* who)
+{
+    if (!h) return fail(ZERO_EINVAL, std::string(who) + ": NULL handle");
+    if (!h->bound) return fail(ZERO_ESTATE, std::string(who) + ": nothing bound (zero_muon_bind)");
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    if (dev != h->device) return fail(ZERO_EINVAL, std::string(who) + ": the bound buffers live on another device");
+    return ZERO_OK;
+}
+
+MuonParams params(const zero_muon* h, const zero_muon_hyper_t& hyper, double loss_scale, const Range& range)
+{
+    char* ws = static_cast<char*>(h->workspace);
+    MuonParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.tensors = reinterpret_cast<MuonTensor*>(ws + h->at_tensors);
+    P.grads = reinterpret_cast<const void* const*>(ws + h->at_grads);
+    P.momentum[0] = h->momentum[0];
+    P.momentum[1] = h->momentum[1];
+    P.st = reinterpret_cast<MuonState*>(ws);
+    P.slots = reinterpret_cast<double*>(ws + h->at_slots);
+    P.scale = reinterpret_cast<float*>(ws + h->at_scale);
+    P.tickets = reinterpret_cast<uint32_t*>(ws + h->at_tickets);
+    P.n_d = h->n_d;
+    P.nesterov = (hyper.flags & ZERO_MUON_NESTEROV) != 0;
+    P.how = hyper.scale;
+    P.inv = (float)(1.0 / ((double)h->n_d * loss_scale));
+    P.mu = (float)hyper.momentum;
+    P.nu = (float)(1.0 - hyper.momentum);
+    P.sigma = (float)range.sigma;
+    P.lr = (float)hyper.lr;
+    P.decay = (float)(hyper.lr * hyper.weight_decay);
+    P.eps = hyper.eps;
+    return P;
+}
+
+int pass_grid(int64_t pieces) { return (int)std::max<int64_t>(1, std::min<int64_t>(pieces, 6 * kGb300Sms)); }
+
+zero_status_t launch_reduce(const zero_muon* h, MuonParams P, cudaStream_t s)
+{
+    if (h->chunks.empty()) return ZERO_OK;
+    P.pieces = reinterpret_cast<const Piece*>(static_cast<char*>(h->workspace) + h->at_chunks);
+    P.count = (int32_t)h->chunks.size();
+    const cudaError_t e = h->dtype16 == ZERO_BF16 ? launch_after(muon_reduce_kernel<ZERO_BF16>, pass_grid(P.count), kThreads, 0, s, P)
+                                                  : launch_after(muon_reduce_kernel<ZERO_FP16>, pass_grid(P.count), kThreads, 0, s, P);
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
+}
+
+template <int CG, int BN, int KIND>
+zero_status_t launch_product(const ProductParams& P, cudaStream_t s)
+{
+    using S = GemmShape<CG, BN>;
+    const cudaError_t set = allow_shared<muon_product_kernel<CG, BN, KIND>>(S::kSmem);
+    if (set != cudaSuccess) return cuda_fail(set, "zero_muon: shared memory");
+    const int grid = CG * (int)std::min<int64_t>(kGb300Sms / CG, P.count);
+    const cudaError_t e = launch_after(muon_product_kernel<CG, BN, KIND>, grid, kGemmThreads, S::kSmem, s, P);
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
+}
+
+template <int KIND>
+zero_status_t launch_product(const zero_muon* h, ProductParams P, cudaStream_t s)
+{
+    constexpr int which = KIND == kNext;
+    P.tiles = reinterpret_cast<const Piece*>(static_cast<char*>(h->workspace) + h->at_tiles[which]);
+    P.count = (int32_t)h->tiles[which].size();
+    return h->cg[which] == 2 ? launch_product<2, 256, KIND>(P, s) : launch_product<1, 128, KIND>(P, s);
+}
+
+// The first X, the iterations and the parameters.
+zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hyper_t& hyper, const Range& R, cudaStream_t s)
+{
+    P.pieces = reinterpret_cast<const Piece*>(static_cast<char*>(h->workspace) + h->at_groups);
+    P.count = (int32_t)h->groups.size();
+    const int grid = pass_grid(P.count);
+    cudaError_t e = cudaSuccess;
+    if (P.count > 0) {
+        e = launch_after(muon_start_kernel, grid, kThreads, 0, s, P);
+        if (e != cudaSuccess) return cuda_fail(e, "zero_muon: launch");
+        for (int k = 0; k < hyper.steps; ++k) {
+            const double *c = hyper.coefficients[k], a2 = R.alpha * R.alpha;
+            const bool twice = k < kTwice;
+            ProductParams Q;
+            std::memset(&Q, 0, sizeof(Q));
+            Q.tensors = P.tensors;
+            Q.src = k & 1;
+            Q.scale = (float)(R.alpha / (R.sigma * R.sigma));
+            zero_status_t st = launch_product<kGram>(h, Q, s);
+            if (st != ZERO_OK) return st;
+            Q.scale = (float)(c[2] * R.beta / a2);
+            Q.lin = (float)(c[1] * R.beta / R.alpha);
+            Q.diag = twice ? 0.0f : (float)(c[0] * R.beta);
+            st = launch_product<kPoly>(h, Q, s);
+            if (st != ZERO_OK) return st;
+            Q.scale = (float)(1.0 / R.beta);
+            Q.lin = (float)c[0];
+            Q.twice = twice;
+            Q.keep_low = k + 1 < kTwice && k + 1 < hyper.steps;
+            st = launch_product<kNext>(h, Q, s);
+            if (st != ZERO_OK) return st;
+        }
+    }
+    P.src = hyper.steps & 1;
+    e = h->dtype16 == ZERO_BF16 ? launch_after(muon_apply_kernel<ZERO_BF16>, grid, kThreads, 0, s, P)
+                                : launch_after(muon_apply_kernel<ZERO_FP16>, grid, kThreads, 0, s, P);
+    return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
+}
+
+zero_status_t plan_ready(const zero_muon* h, const zero_plan* plan, const char* who)
+{
+    if (!h || !plan) return fail(ZERO_EINVAL, std::string(who) + ": NULL argument");
+    const zero_status_t st = ready(h, who);
+    if (st != ZERO_OK) return st;
+    if (!plan->workspace) return fail(ZERO_ESTATE, std::string(who) + ": no rank of the plan is bound");
+    if (plan->device != h->device) return fail(ZERO_EINVAL, std::string(who) + ": the plan lives on another device");
+    return ZERO_OK;
+}
+
+// Elements of X, and of G, in the workspace: each buffer starts on 256 bytes.
+int64_t x_elems(int64_t rows, int64_t cols) { return up(rows * up(cols, 8), 128); }
+int64_t g_elems(int64_t m) { return up(m * up(m, 8), 128); }
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+zero_status_t zero_muon_create(const int64_t* rows, const int64_t* cols, int64_t n_matrices, int n_contribs, int dtype16, zero_muon_t** out)
+try {
+    if (!out || ((!rows || !cols) && n_matrices > 0)) return fail(ZERO_EINVAL, "zero_muon_create: NULL argument");
+    *out = nullptr;
+    if (n_matrices < 0) return fail(ZERO_EINVAL, "zero_muon_create: negative count");
+    if (n_matrices > ZERO_MUON_MAX_MATRICES) return fail(ZERO_ERANGE, "zero_muon_create: more than ZERO_MUON_MAX_MATRICES matrices");
+    if (n_contribs < 1) return fail(ZERO_EINVAL, "zero_muon_create: n_contribs must be at least 1");
+    if (n_contribs > ZERO_MAX_RANKS) return fail(ZERO_ERANGE, "zero_muon_create: more than ZERO_MAX_RANKS contributions");
+    if (dtype16 != ZERO_BF16 && dtype16 != ZERO_FP16) return fail(ZERO_EINVAL, "zero_muon_create: bad dtype16");
+    std::unique_ptr<zero_muon> h(new zero_muon);
+    h->n_d = n_contribs;
+    h->dtype16 = dtype16;
+    int64_t at = 0, pieces = 0;
+    for (int64_t i = 0; i < n_matrices; ++i) {
+        const int64_t r = rows[i], c = cols[i];
+        if (r < 0 || c < 0) return fail(ZERO_EINVAL, "zero_muon_create: negative size");
+        if (r > ZERO_MUON_MAX_SIZE || c > ZERO_MUON_MAX_SIZE || std::min(r, c) > ZERO_MUON_MAX_SIDE)
+            return fail(ZERO_ERANGE, "zero_muon_create: a matrix beyond ZERO_MUON_MAX_SIZE, or its smaller side beyond ZERO_MUON_MAX_SIDE");
+        pieces += div_up(r * c, kChunk);
+        if (pieces > INT32_MAX / 16) return fail(ZERO_ERANGE, "zero_muon_create: the matrices have too many elements");
+        h->elems += r * c;
+        h->state_elems += up(r * c, kStateBlock);
+    }
+    h->rows.assign(rows, rows + n_matrices);
+    h->cols.assign(cols, cols + n_matrices);
+    for (int64_t i = 0; i < n_matrices; ++i) {
+        const int64_t r = rows[i], c = cols[i];
+        for (int64_t k = 0; k < div_up(r * c, kChunk); ++k) h->chunks.push_back(Piece{(int32_t)i, (int32_t)k});
+        for (int64_t k = 0; k < div_up(r * up(c, 8), kChunk); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
+    }
+    for (int which = 0; which < 2; ++which) {
+        std::vector<Piece> small, large;
+        double us1 = 0.0, us2 = 0.0;
+        cut_tiles(h.get(), which, 1, &small, &us1);
+        cut_tiles(h.get(), which, 2, &large, &us2);
+        h->cg[which] = us2 < us1 ? 2 : 1;
+        h->tiles[which] = us2 < us1 ? std::move(large) : std::move(small);
+    }
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    take(sizeof(MuonState));
+    h->at_tensors = take((int64_t)sizeof(MuonTensor) * n_matrices);
+    h->at_grads = take(8 * n_matrices * n_contribs);
+    h->at_chunks = take(8 * (int64_t)h->chunks.size());
+    h->at_groups = take(8 * (int64_t)h->groups.size());
+    for (int which = 0; which < 2; ++which) h->at_tiles[which] = take(8 * (int64_t)h->tiles[which].size());
+    h->at_slots = take(8 * (int64_t)h->chunks.size());
+    h->at_scale = take(4 * n_matrices);
+    h->at_tickets = take(4 * n_matrices);
+    h->at_data = at;
+    for (int64_t i = 0; i < n_matrices; ++i)
+        if (rows[i] * cols[i] > 0) at += 2 * (3 * x_elems(rows[i], cols[i]) + 2 * g_elems(std::min(rows[i], cols[i])));
+    h->bytes = at;
+    *out = h.release();
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_muon_create");
+}
+
+zero_status_t zero_muon_info(const zero_muon_t* h, zero_muon_info_t* out)
+try {
+    if (!h || !out) return fail(ZERO_EINVAL, "zero_muon_info: NULL argument");
+    out->n_matrices = (int64_t)h->rows.size();
+    out->n_contribs = h->n_d;
+    out->elems = h->elems;
+    out->state_elems = h->state_elems;
+    out->workspace_bytes = h->bytes;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_muon_info");
+}
+
+zero_status_t zero_muon_bind(zero_muon_t* h, float* const* params, void* const* params16, void* const* updates, const void* const* grads,
+                             float* const momentum[2], void* workspace, int64_t t, void* stream)
+try {
+    if (!h) return fail(ZERO_EINVAL, "zero_muon_bind: NULL handle");
+    const size_t n = h->rows.size();
+    if (n > 0 && !grads) return fail(ZERO_EINVAL, "zero_muon_bind: NULL argument");
+    if (!workspace) return fail(ZERO_EINVAL, "zero_muon_bind: workspace is NULL");
+    if (!aligned(workspace, 256)) return fail(ZERO_EALIGN, "zero_muon_bind: workspace not 256-byte aligned");
+    if (t < -1 || (t == -1 && (!h->bound || workspace != h->workspace)))
+        return fail(ZERO_EINVAL, "zero_muon_bind: t must be >= 0 (-1 keeps an earlier bind's, with its workspace)");
+    if (h->state_elems > 0) {
+        if (!momentum || !momentum[0] || !momentum[1]) return fail(ZERO_EINVAL, "zero_muon_bind: NULL momentum");
+        if (momentum[0] == momentum[1]) return fail(ZERO_EINVAL, "zero_muon_bind: the momentum's halves are one buffer");
+        if (!aligned(momentum[0], 16) || !aligned(momentum[1], 16)) return fail(ZERO_EALIGN, "zero_muon_bind: momentum not 16-byte aligned");
+        if (t == -1 && (momentum[0] != h->momentum[0] || momentum[1] != h->momentum[1]))
+            return fail(ZERO_EINVAL, "zero_muon_bind: t = -1 keeps the momentum too");
+    }
+    char* ws = static_cast<char*>(workspace);
+    std::vector<unsigned char> image((size_t)h->at_data, 0);
+    MuonState init;
+    std::memset(&init, 0, sizeof(init));
+    init.t = t;
+    std::memcpy(image.data(), &init, sizeof(init));
+    const void** table = reinterpret_cast<const void**>(image.data() + h->at_grads);
+    int64_t data = h->at_data, at = 0;
+    for (size_t i = 0; i < n; ++i) {
+        const int64_t r = h->rows[i], c = h->cols[i], m = std::min(r, c);
+        MuonTensor T;
+        std::memset(&T, 0, sizeof(T));
+        T.rows = (int32_t)r;
+        T.cols = (int32_t)c;
+        T.m = (int32_t)m;
+        if (m > 0) {
+            T.ldx = (int32_t)up(c, 8);
+            T.ldm = (int32_t)up(m, 8);
+            T.wide = r <= c;
+            T.at = at;
+            T.chunks = (int32_t)div_up(r * c, kChunk);
+            T.aspect = (float)std::sqrt(std::max(1.0, (double)r / (double)c));
+            T.rms = (float)(0.2 * std::sqrt((double)std::max(r, c)));
+            T.p = params ? params[i] : nullptr;
+            T.p16 = params16 ? static_cast<uint16_t*>(params16[i]) : nullptr;
+            T.update = updates ? static_cast<uint16_t*>(updates[i]) : nullptr;
+            if (!T.p && T.p16) return fail(ZERO_EINVAL, "zero_muon_bind: a 16-bit copy without its parameters");
+            if (!T.p && !T.update) return fail(ZERO_EINVAL, "zero_muon_bind: a matrix with neither parameters nor update");
+            if (!aligned(T.p, 4) || !aligned(T.p16, 2) || !aligned(T.update, 2))
+                return fail(ZERO_EALIGN, "zero_muon_bind: a matrix is not aligned to its element size");
+            T.vec_g = 1;
+            for (int k = 0; k < h->n_d; ++k) {
+                const void* g = grads[(size_t)k * n + i];
+                if (!g) return fail(ZERO_EINVAL, "zero_muon_bind: NULL contribution");
+                if (!aligned(g, 2)) return fail(ZERO_EALIGN, "zero_muon_bind: a contribution is not aligned to 2 bytes");
+                T.vec_g = T.vec_g && aligned(g, 16);
+                table[i * (size_t)h->n_d + (size_t)k] = g;
+            }
+            T.vec_p = c % 8 == 0 && aligned(T.p, 16) && aligned(T.p16, 16) && aligned(T.update, 16);
+            uint16_t* q = reinterpret_cast<uint16_t*>(ws + data);
+            const int64_t x = x_elems(r, c), g = g_elems(m);
+            T.x[0] = q;
+            T.x[1] = q + x;
+            T.low = q + 2 * x;
+            T.a = q + 3 * x;
+            T.b = T.a + g;
+            data += 2 * (3 * x + 2 * g);
+            zero_status_t st = ZERO_OK;
+            for (int k = 0; k < 2 && st == ZERO_OK; ++k) {
+                st = encode(&T.xk[k], Operand{T.x[k], r, c, T.ldx, false}, ZERO_FP16, kBM, "zero_muon_bind");
+                if (st == ZERO_OK) st = encode(&T.xm[k], Operand{T.x[k], c, r, T.ldx, true}, ZERO_FP16, kBM, "zero_muon_bind");
+            }
+            if (st == ZERO_OK) st = encode(&T.ak, Operand{T.a, m, m, T.ldm, false}, ZERO_FP16, kBM, "zero_muon_bind");
+            if (st == ZERO_OK) st = encode(&T.bk, Operand{T.b, m, m, T.ldm, false}, ZERO_FP16, kBM, "zero_muon_bind");
+            if (st != ZERO_OK) return st;
+            at += up(r * c, kStateBlock);
+        }
+        std::memcpy(image.data() + h->at_tensors + (int64_t)sizeof(T) * (int64_t)i, &T, sizeof(T));
+    }
+    auto put = [&](int64_t where, const std::vector<Piece>& v) {
+        if (!v.empty()) std::memcpy(image.data() + where, v.data(), v.size() * sizeof(Piece));
+    };
+    put(h->at_chunks, h->chunks);
+    put(h->at_groups, h->groups);
+    for (int which = 0; which < 2; ++which) put(h->at_tiles[which], h->tiles[which]);
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "zero_muon_bind: cudaGetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t skip = t == -1 ? 256 : 0;       // -1: the state's slot stays
+    e = cudaMemcpyAsync(ws + skip, image.data() + skip, image.size() - skip, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "zero_muon_bind: the workspace's tables");
+    for (int k = 0; k < 2; ++k) h->momentum[k] = momentum ? momentum[k] : nullptr;
+    h->workspace = workspace;
+    h->device = dev;
+    h->bound = true;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_muon_bind");
+}
+
+zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, double loss_scale, void* stream)
+try {
+    if (!h) return fail(ZERO_EINVAL, "zero_muon_step: NULL handle");
+    Range R;
+    zero_status_t st = check_hyper(hyper, &R, "zero_muon_step");
+    if (st != ZERO_OK) return st;
+    if (!(loss_scale > 0.0) || !std::isfinite(loss_scale)) return fail(ZERO_EINVAL, "zero_muon_step: loss_scale must be positive");
+    st = ready(h, "zero_muon_step");
+    if (st != ZERO_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const MuonParams P = params(h, *hyper, loss_scale, R);
+    st = launch_reduce(h, P, s);
+    return st == ZERO_OK ? launch_rest(h, P, *hyper, R, s) : st;
+}
+catch (...) {
+    return exception_status("zero_muon_step");
+}
+
+zero_status_t zero_muon_check(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream)
+try {
+    Range R;
+    zero_status_t st = check_hyper(hyper, &R, "zero_muon_check");
+    if (st == ZERO_OK) st = plan_ready(h, plan, "zero_muon_check");
+    if (st != ZERO_OK) return st;
+    if (h->checked_in == plan->step_no) return fail(ZERO_ESTATE, "zero_muon_check: already part of this step");
+    if (plan->in_step && plan->offload)
+        return fail(ZERO_ESTATE, "zero_muon_check: must precede the first bucket/unit of a step that is offloaded");
+    MuonParams P = params(h, *hyper, 1.0, R);
+    P.plan = reinterpret_cast<DevState*>(plan->workspace);
+    st = launch_reduce(h, P, static_cast<cudaStream_t>(stream));
+    if (st != ZERO_OK) return st;
+    h->checked_in = plan->step_no;
+    h->checked_mu = hyper->momentum;
+    h->checked_flags = hyper->flags;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_muon_check");
+}
+
+zero_status_t zero_muon_step_with(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream)
+try {
+    Range R;
+    zero_status_t st = check_hyper(hyper, &R, "zero_muon_step_with");
+    if (st == ZERO_OK) st = plan_ready(h, plan, "zero_muon_step_with");
+    if (st != ZERO_OK) return st;
+    if (h->checked_in != plan->step_no) return fail(ZERO_ESTATE, "zero_muon_step_with: needs zero_muon_check in the same step");
+    if (h->stepped_in == plan->step_no) return fail(ZERO_ESTATE, "zero_muon_step_with: already part of this step");
+    bool all = plan->in_step;
+    for (int64_t b = 0; b < plan->n_buckets && all; ++b) all = plan->covered[(size_t)b] != 0;
+    if (!all) return fail(ZERO_ESTATE, "zero_muon_step_with: follows the step of every bucket/unit, before the step's finish");
+    if (hyper->momentum != h->checked_mu || hyper->flags != h->checked_flags)
+        return fail(ZERO_EINVAL, "zero_muon_step_with: one step has one momentum and one set of flags");
+    MuonParams P = params(h, *hyper, 1.0, R);
+    P.plan = reinterpret_cast<DevState*>(plan->workspace);
+    st = launch_rest(h, P, *hyper, R, static_cast<cudaStream_t>(stream));
+    if (st != ZERO_OK) return st;
+    h->stepped_in = plan->step_no;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_muon_step_with");
+}
+
+zero_status_t zero_muon_read(zero_muon_t* h, void* stream, zero_step_result_t* out)
+try {
+    if (!h || !out) return fail(ZERO_EINVAL, "zero_muon_read: NULL argument");
+    const zero_status_t st = ready(h, "zero_muon_read");
+    if (st != ZERO_OK) return st;
+    MuonState state;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(&state, h->workspace, sizeof(state), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "zero_muon_read");
+    std::memset(out, 0, sizeof(*out));
+    out->skipped = (int32_t)state.last_skipped;
+    out->current = (int32_t)state.cur;
+    out->t = state.t;
+    out->scale = 1.0;
+    out->good_steps = state.t;
+    out->skipped_total = state.skipped;
+    out->finished = state.finished;
+    out->grad_norm = -1.0;
+    return ZERO_OK;
+}
+catch (...) {
+    return exception_status("zero_muon_read");
+}
+
+void zero_muon_destroy(zero_muon_t* h) { delete h; }
+
+}  // extern "C"
