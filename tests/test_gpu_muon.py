@@ -94,29 +94,40 @@ class Muon:
         Z.zero_muon_destroy(self.h)
 
 
-def iterate(u, eps, abc, move=None):
-    """The definition in float64; move(x): x with every entry a half step of fp16 off."""
+def iterate(u, eps, abc, move=None, pair=False):
+    """The definition in float64; move(x): x with every entry a half step of fp16 off, at the places where the kernels
+    round (pair: the first two iterations made at once, as they are where every smaller side is at least 128)."""
     off = move or (lambda v: v)
     x = u / (torch.linalg.matrix_norm(u) + eps)
     wide = x.shape[0] <= x.shape[1]
+    gram = lambda h: off(h @ h.t() if wide else h.t() @ h)  # noqa: E731
+    times = lambda p, h: p @ h if wide else h @ p  # noqa: E731
+    eye = torch.eye(min(x.shape), dtype=torch.float64, device=x.device)
     h = off(x)                              # the first of the two numbers that X is kept as
-    for k, (a, b, c) in enumerate(abc):
-        g = h @ h.t() if wide else h.t() @ h
-        g = off(g)
-        poly, eye = b * g + c * (g @ g), a * torch.eye(len(g), dtype=torch.float64, device=g.device)
-        if k < 2:
-            poly = off(poly)
-            x = (poly @ h if wide else h @ poly) + a * x
+    first = 0
+    if pair and len(abc) > 1:
+        (a, b, c), (a2, b2, c2) = abc[:2]
+        g = gram(h)
+        r = off(b * g + c * (g @ g))
+        w = off(r @ g)
+        g = off(a * a * g + 2 * a * w + r @ w)
+        s = off(b2 * g + c2 * (g @ g))
+        h = off(times(off(a2 * r + a * s + s @ r), h) + a * a2 * x)
+        first = 2
+    for k, (a, b, c) in enumerate(abc[first:], first):
+        g = gram(h)
+        poly = b * g + c * (g @ g)
+        if k < 2 and not pair:
+            x = times(off(poly), h) + a * x
         else:
-            poly = off(poly + eye)
-            x = poly @ h if wide else h @ poly
+            x = times(off(poly + a * eye), h)
         h = off(x)
-        if k >= 1:
+        if k >= 1 or pair:
             x = h
     return h if move else x
 
 
-def tolerance(u, eps, abc, want):
+def tolerance(u, eps, abc, want, pair):
     gen = torch.Generator(device="cuda").manual_seed(1)
 
     def move(v):
@@ -125,7 +136,7 @@ def tolerance(u, eps, abc, want):
             sign = torch.triu(sign) + torch.triu(sign, 1).t()
         return v * (1 + 2.0 ** -11 * sign)
 
-    worst = max(float((iterate(u, eps, abc, move) - want).norm()) for _ in range(8))
+    worst = max(float((iterate(u, eps, abc, move, pair) - want).norm()) for _ in range(8))
     return 2 * worst + 2.0 ** -13 * float(want.norm()) + 1e-30
 
 
@@ -156,7 +167,7 @@ def check(mu, hyper, half=0, loss_scale=1.0):
         _g, m, u, err = want[i]
         assert bool(((mu.m(half ^ 1, i).double() - m).abs() <= err).all())
         x = iterate(u, hyper.eps, coefficients(hyper))
-        tol = tolerance(u, hyper.eps, coefficients(hyper), x)
+        tol = tolerance(u, hyper.eps, coefficients(hyper), x, min(min(s) for s in mu.shapes if min(s)) >= 128)
         if mu.ptrs[2][i]:
             got = mu.x[i].double()
             off = float((got - x).norm())
@@ -250,6 +261,19 @@ def test_exact(r, c, k):
         assert torch.equal(mu.x[0], x.to(torch.bfloat16))
         mu.guards_stand()
         mu.close()
+
+
+@pytest.mark.parametrize("r,c", [(128, 128), (300, 257), (257, 1100), (2050, 2050)])
+def test_exact_two_at_once(r, c):
+    v = partial_permutation(r, c, 1, torch.Generator().manual_seed(r))
+    mu = Muon([(r, c)], 1, "bf16")
+    mu.g[0][0].copy_(v)
+    mu.p[0].zero_()
+    # singular values 1/2: G 1/4, R1 1/8, W 1/32, the second G 81/256 and R 81/512, Q 1241/4096
+    mu.step(Z.muon_hyper(lr=1.0, weight_decay=0.0, momentum=0.0, eps=1e-12, steps=2, coefficients=(1.0, 0.5, 0.0), scale=0))
+    x = (v.double().cuda() / 16 * (5337 / 4096)).to(torch.float16).double()
+    assert torch.equal(mu.p[0].double(), -x)
+    mu.close()
 
 
 def test_zero_gradients_and_small_ones():

@@ -75,6 +75,8 @@ struct GatedWork {
     struct Item {
         int m, n, kb, problem;
     };
+    struct Ahead {};
+    __device__ __forceinline__ void prepare(const Item&, int, int, int, int, Ahead&) const {}
 
     __device__ __forceinline__ Item item(int i) const
     {
@@ -130,7 +132,7 @@ struct GatedWork {
         }
     }
 
-    __device__ __forceinline__ void finish(const Item& I, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    __device__ __forceinline__ void finish(const Item& I, Ahead&, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
         if constexpr (MODE == kForward) {

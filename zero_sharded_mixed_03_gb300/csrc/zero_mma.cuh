@@ -253,7 +253,8 @@ struct GemmShape {
 //   uint32_t bytes(Item)                    what a stage's copies bring, to both blocks of a pair
 //   begin(Item); load(Item, kb, a, b, bar, rank)   those copies: what precedes a tile's, and a stage's
 //   a_mn(Item), b_mn(Item), idesc(Item)     how the operands lie, and the product's descriptor
-//   finish(Item, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
+//   prepare(Item, quad, half, rank, lane, Ahead&)      what a tile's end may load before its products are done
+//   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
 template <int CG, int BN>
@@ -372,11 +373,13 @@ struct Tiles {
             for (int i = first; i < work.count && ok; i += step, ++tile) {
                 const typename W::Item I = work.item(i);
                 const uint32_t acc = tile & 1, use = tile >> 1;
+                typename W::Ahead ahead;
+                work.prepare(I, quad, half, (int)rank, lane, ahead);
                 ok = mbar_wait(acc_full0 + 8 * acc, use & 1, kGemmWaitNs);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                work.finish(I, tmem + acc * BN + ((uint32_t)(quad * 32) << 16), quad, half, stage, (int)rank, lane);
+                work.finish(I, ahead, tmem + acc * BN + ((uint32_t)(quad * 32) << 16), quad, half, stage, (int)rank, lane);
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {

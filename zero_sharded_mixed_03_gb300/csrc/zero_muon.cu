@@ -17,7 +17,9 @@
 // nearly all of small singular values' growth, both) 0.1 to 0.3 %.  Sums are fp32.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <memory>
+#include <utility>
 #include <vector>
 
 #include "zero_mma.cuh"
@@ -29,9 +31,12 @@ namespace {
 __device__ uint32_t g_muon_error;
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;              // elements of a matrix that a block takes at a time
+constexpr int kChunk = 8 * kThreads;      // elements of a matrix that a block takes at a time, or a multiple of them
+constexpr int kPassBlocks = 6;            // blocks an SM of a pass over the elements
 constexpr int kStateBlock = 256;          // each matrix's momentum starts on a multiple of it
+constexpr int kSquares = 4;               // symmetric matrices beside each X
 constexpr int kTwice = 2;                 // iterations whose X is the sum of two fp16 numbers
+constexpr int kPairSide = 128;            // smaller sides from which the first two iterations are one
 constexpr float kLow = 2048.0f;           // the second of them is stored times this
 
 struct MuonState {
@@ -45,9 +50,9 @@ static_assert(sizeof(MuonState) <= 256, "MuonState fits its slot");
 
 struct alignas(128) MuonTensor {
     CUtensorMap xk[2], xm[2];    // X's two buffers, taken along their rows and along their columns
-    CUtensorMap ak, bk;          // G, and the polynomial
+    CUtensorMap sq[kSquares];    // the symmetric matrices
     uint16_t *x[2], *low;        // rows x ldx
-    uint16_t *a, *b;             // m x ldm
+    uint16_t* square[kSquares];  // m x ldm
     float* p;                    // NULL: no parameters
     uint16_t *p16, *update;      // may be NULL
     int64_t at;                  // its first momentum
@@ -73,7 +78,7 @@ struct MuonParams {
     double* slots;               // [piece of the first pass] sums of squares
     float* scale;                // [tensor] 1 / (norm + eps)
     uint32_t* tickets;           // [tensor]
-    int32_t count, n_d, nesterov, src, how;
+    int32_t count, rounds, n_d, nesterov, src, how;   // rounds: multiples of kChunk in a piece
     float inv, mu, nu, sigma, lr, decay;   // nu = 1 - mu; sigma: X's factor in fp16
     double eps;
 };
@@ -110,12 +115,20 @@ __device__ __forceinline__ void sum_contributions(const void* const* grads, int 
     };
     int r = 0;
     if (vec && n == 8) {
-        for (; r + 4 <= n_d; r += 4) {
+        for (; r + 8 <= n_d; r += 8) {
+            uint4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(grads[r + i]) + e));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add8(w[i]);
+        }
+        if (r + 4 <= n_d) {
             uint4 w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(grads[r + i]) + e));
 #pragma unroll
             for (int i = 0; i < 4; ++i) add8(w[i]);
+            r += 4;
         }
         for (; r < n_d; ++r) add8(__ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(grads[r]) + e)));
     } else {
@@ -141,19 +154,18 @@ __global__ void __launch_bounds__(kThreads) muon_reduce_kernel(const __grid_cons
     for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
         const Piece piece = P.pieces[i];
         const MuonTensor& T = P.tensors[piece.tensor];
-        const int64_t elems = (int64_t)T.rows * T.cols, e0 = (int64_t)piece.at * kChunk;
+        const int64_t elems = (int64_t)T.rows * T.cols, e0 = (int64_t)piece.at * P.rounds * kChunk;
         const void* const* grads = P.grads + (int64_t)piece.tensor * P.n_d;
         float sum = 0.0f;
-#pragma unroll 2
-        for (int k = 0; k < kChunk / (8 * kThreads); ++k) {
+        for (int k = 0; k < P.rounds; ++k) {
             const int64_t e = e0 + ((int64_t)k * kThreads + threadIdx.x) * 8;
             const int n = (int)min((int64_t)8, elems - e);
             if (n <= 0) break;
-            float g[8];
-            sum_contributions<DT>(grads, P.n_d, e, n, T.vec_g, g);
             // the momentum's rows of eight are whole: it is padded
             const float4* q = reinterpret_cast<const float4*>(from + T.at + e);
             const float4 a = __ldcs(q), b = __ldcs(q + 1);
+            float g[8];
+            sum_contributions<DT>(grads, P.n_d, e, n, T.vec_g, g);
             const float m0[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             float m1[8];
 #pragma unroll
@@ -206,13 +218,13 @@ __device__ __forceinline__ void two_halves(const float (&x)[8], uint32_t (&hi)[4
 
 // Piece `at` of the matrix in groups of eight columns: f(row, column, columns there, group's place in X).
 template <typename F>
-__device__ __forceinline__ void for_groups(const MuonTensor& T, int at, F&& f)
+__device__ __forceinline__ void for_groups(const MuonTensor& T, int at, int rounds, F&& f)
 {
     const int groups = T.ldx / 8;
     const int64_t total = (int64_t)T.rows * groups;
 #pragma unroll 2
-    for (int k = 0; k < kChunk / (8 * kThreads); ++k) {
-        const int64_t i = (int64_t)at * (kChunk / 8) + (int64_t)k * kThreads + threadIdx.x;
+    for (int k = 0; k < rounds; ++k) {
+        const int64_t i = ((int64_t)at * rounds + k) * kThreads + threadIdx.x;
         if (i >= total) break;
         int64_t row = 0;
         int col = 0;
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
         const MuonTensor& T = P.tensors[piece.tensor];
         const float scale = P.scale[piece.tensor];
         const float *old = P.momentum[cur & 1] + T.at, *now = P.momentum[(cur & 1) ^ 1] + T.at;
-        for_groups(T, piece.at, [&](int64_t e, int n, int64_t out) {
+        for_groups(T, piece.at, P.rounds, [&](int64_t e, int n, int64_t out) {
             float m0[8], m1[8], x[8];
             if (T.cols == T.ldx) {
                 const float4* q = reinterpret_cast<const float4*>(now + e);
@@ -267,15 +279,19 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
 
 // ------------------------------------------------------------------ the products
 
-enum { kGram = 0, kPoly = 1, kNext = 2 };
+// X X^T (or X^T X); a product of two symmetric matrices that commute, so that it is one too; one times X.
+enum { kGram = 0, kSquare = 1, kNext = 2 };
 
+// out = scale acc + lin[0] add0 + lin[1] add1 + diag I.  Symmetric matrices by their numbers; kNext's addends are X
+// and its low part.
 struct ProductParams {
     const MuonTensor* tensors;
     const Piece* tiles;
     int32_t count, src;          // src: X's buffer that is read
-    int32_t twice, keep_low;     // kNext: X is a sum of two; its successor is to be
-    float scale;                 // of the accumulator
-    float lin, diag;             // kPoly: of G, of I; kNext: lin: of X
+    int32_t left, right, out;    // operands and result; kNext: left is the polynomial
+    int32_t adds, add[2];
+    int32_t keep_low;            // kNext: the successor's low part is wanted
+    float scale, lin[2], diag;
 };
 
 // row `lane` of a tile: x, written as its transpose at (col0, row0)
@@ -309,10 +325,11 @@ struct MuonWork {
         const MuonTensor& T = *I.T;
         if constexpr (KIND == kGram) {
             see(I.wide ? &T.xk[P.src] : &T.xm[P.src]);
-        } else if constexpr (KIND == kPoly) {
-            see(&T.ak);
+        } else if constexpr (KIND == kSquare) {
+            see(&T.sq[P.left]);
+            if (P.right != P.left) see(&T.sq[P.right]);
         } else {
-            see(&T.bk);
+            see(&T.sq[P.left]);
             see(I.wide ? &T.xm[P.src] : &T.xk[P.src]);
         }
     }
@@ -356,49 +373,120 @@ struct MuonWork {
             const CUtensorMap* map = I.wide ? &T.xk[P.src] : &T.xm[P.src];
             bring(map, !I.wide, a, row_a, k, bar);
             bring(map, !I.wide, b, row_b, k, bar);
-        } else if constexpr (KIND == kPoly) {
-            bring(&T.ak, false, a, row_a, k, bar);
-            bring(&T.ak, false, b, row_b, k, bar);
+        } else if constexpr (KIND == kSquare) {
+            bring(&T.sq[P.left], false, a, row_a, k, bar);
+            bring(&T.sq[P.right], false, b, row_b, k, bar);
         } else {
-            bring(I.wide ? &T.bk : &T.xk[P.src], false, a, row_a, k, bar);
-            bring(I.wide ? &T.xm[P.src] : &T.bk, I.wide, b, row_b, k, bar);
+            bring(I.wide ? &T.sq[P.left] : &T.xk[P.src], false, a, row_a, k, bar);
+            bring(I.wide ? &T.xm[P.src] : &T.sq[P.left], I.wide, b, row_b, k, bar);
         }
     }
 
-    __device__ __forceinline__ void finish(const Item& I, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    // ---- a tile's end.  The addends of a 32 x 32 part are loaded while the one before it is finished, the first
+    // ones' while the products run: their latency, a microsecond, is otherwise most of a part's time.
+    struct Ahead {
+        uint4 v[2][4];
+    };
+    struct Place {
+        uint16_t *out, *add[2];
+        int32_t ld, rows, cols;
+    };
+
+    __device__ __forceinline__ Place place(const Item& I) const
     {
         const MuonTensor& T = *I.T;
+        Place L;
+        if constexpr (KIND == kNext) {
+            L.out = T.x[P.src ^ 1];
+            L.add[0] = T.x[P.src];
+            L.add[1] = T.low;
+            L.ld = L.cols = T.ldx;
+            L.rows = T.rows;
+        } else {
+            L.out = T.square[P.out];
+            L.add[0] = T.square[P.add[0]];
+            L.add[1] = T.square[P.add[1]];
+            L.ld = L.cols = T.ldm;
+            L.rows = T.m;
+        }
+        return L;
+    }
+
+    // Rows of a multiple of eight columns that start on 16 bytes: all eight of a piece are there, or none.
+    __device__ __forceinline__ static void fetch(uint4 (&v)[4], const uint16_t* p, const Place& L, int64_t row0, int64_t col0, int lane)
+    {
+        const int64_t col = col0 + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = row0 + i * 8 + (lane >> 2);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < L.rows && col < L.cols) v[i] = *reinterpret_cast<const uint4*>(p + row * L.ld + col);
+        }
+    }
+    __device__ __forceinline__ static void stash(uint32_t stage, const uint4 (&v)[4], int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile16_at(stage, i * 8 + (lane >> 2), lane & 3)), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
+    }
+    __device__ __forceinline__ static void add_row(uint32_t stage, float lin, float (&x)[32], int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tile16_at(stage, lane, i)) : "memory");
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a, b;
+                widen2<ZERO_FP16>(w[j], a, b);
+                x[8 * i + 2 * j] = fmaf(lin, a, x[8 * i + 2 * j]);
+                x[8 * i + 2 * j + 1] = fmaf(lin, b, x[8 * i + 2 * j + 1]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void fetch_adds(const Item& I, const Place& L, Ahead& A, int64_t row0, int c, int lane) const
+    {
+        if (P.adds > 0) fetch(A.v[0], L.add[0], L, row0, (int64_t)I.n * BN + c, lane);
+        if (P.adds > 1) fetch(A.v[1], L.add[1], L, row0, (int64_t)I.n * BN + c, lane);
+    }
+
+    __device__ __forceinline__ void prepare(const Item& I, int quad, int half, int rank, int lane, Ahead& A) const
+    {
+        if (P.adds > 0) fetch_adds(I, place(I), A, ((int64_t)I.m * CG + rank) * kBM + quad * 32, half * kEpiCols, lane);
+    }
+
+    __device__ __forceinline__ void finish(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    {
+        const Place L = place(I);
+        const Matrix16 D{L.out, L.ld, L.rows, L.cols, 1};
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
-        Matrix16 D;
-        if constexpr (KIND == kNext) D = Matrix16{T.x[P.src ^ 1], T.ldx, T.rows, T.ldx, 1};
-        else D = Matrix16{KIND == kGram ? T.a : T.b, T.ldm, T.m, T.ldm, 1};
         for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
             const int64_t col0 = (int64_t)I.n * BN + c;
             if (col0 >= D.cols || row0 >= D.rows) break;
+            if (P.adds > 0) stash(stage, A.v[0], lane);
+            if (P.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
+            __syncwarp();
+            if (c + 2 * kEpiCols < BN) fetch_adds(I, L, A, row0, c + 2 * kEpiCols, lane);
             float x[32];
             tmem_load32(acc + c, x);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] *= P.scale;
-            if constexpr (KIND == kPoly) {
-                add_tile<ZERO_FP16>(stage, lane, P.lin, x, Matrix16{T.a, T.ldm, T.m, T.ldm, 1}, row0, col0);
-                if (row0 == col0) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] += j == lane ? P.diag : 0.0f;
-                }
-            }
+            if (P.adds > 0) add_row(stage, P.lin[0], x, lane);
+            if (P.adds > 1) add_row(stage + kTile16Bytes, P.lin[1], x, lane);
+            __syncwarp();
             if constexpr (KIND == kNext) {
-                const Matrix16 low{T.low, T.ldx, T.rows, T.ldx, 1};
-                if (P.twice) {
-                    add_tile<ZERO_FP16>(stage, lane, P.lin, x, Matrix16{T.x[P.src], T.ldx, T.rows, T.ldx, 1}, row0, col0);
-                    add_tile<ZERO_FP16>(stage + kTile16Bytes, lane, P.lin * (1.0f / kLow), x, low, row0, col0);
-                }
                 put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
                 if (P.keep_low) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
-                    put_tile<ZERO_FP16>(stage + kTile16Bytes, lane, x, low, row0, col0);
+                    put_tile<ZERO_FP16>(stage + kTile16Bytes, lane, x, Matrix16{L.add[1], L.ld, L.rows, L.cols, 1}, row0, col0);
                 }
             } else {
+                if (row0 == col0) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] += j == lane ? P.diag : 0.0f;
+                }
                 put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
                 // the tile on the other side of the diagonal is this one's transpose
                 if (I.m != I.n) put_tile_across(stage + kTile16Bytes, lane, x, D, row0, col0);
@@ -435,7 +523,7 @@ __global__ void __launch_bounds__(kThreads) muon_apply_kernel(const __grid_const
             const float step = P.lr * (P.how == ZERO_MUON_SCALE_RMS ? T.rms : P.how == ZERO_MUON_SCALE_ASPECT ? T.aspect : 1.0f);
             const float unit = 1.0f / P.sigma;      // a power of two
             const uint16_t* x16 = T.x[P.src];
-            for_groups(T, piece.at, [&](int64_t e, int n, int64_t at) {
+            for_groups(T, piece.at, P.rounds, [&](int64_t e, int n, int64_t at) {
                 const uint4 w = *reinterpret_cast<const uint4*>(x16 + at);
                 float x[8];
                 widen2<ZERO_FP16>(w.x, x[0], x[1]);
@@ -502,6 +590,8 @@ struct zero_muon {
     int64_t elems = 0, state_elems = 0;
     // tiles of 128 or 256 for the symmetric products and for the others
     int cg[2] = {1, 1};
+    bool pair = false;
+    int rounds = 1;              // of kChunk elements in a piece of the passes
     std::vector<zero::Piece> chunks, groups, tiles[2];
     // the workspace's pieces
     int64_t at_tensors = 0, at_grads = 0, at_chunks = 0, at_groups = 0, at_tiles[2] = {0, 0}, at_slots = 0, at_scale = 0, at_tickets = 0,
@@ -520,35 +610,55 @@ struct zero_muon {
 namespace zero {
 namespace {
 
-// What X, G and the polynomial are multiplied by in fp16: powers of two that leave room for rounding below 65504.
+// The symmetric matrices of an iteration, and where each is kept: G and the polynomial; for two iterations at once R1 =
+// b G + c G^2, W = R1 G, the second's G and R, and Q = (a I + R1)(a' I + R2) - a a' I.
+enum Role { kG, kPoly, kR1, kW, kG2, kR2, kQ, kRoles };
+constexpr int kSlot[kRoles] = {0, 1, 1, 2, 3, 0, 2};
+
+// What X and the symmetric matrices are multiplied by in fp16: powers of two that leave room below 65504.
 struct Range {
-    double sigma = 1.0, alpha = 1.0, beta = 1.0;
+    double sigma = 1.0, factor[kRoles];
+    double of(Role r) const { return factor[r]; }
 };
 
 double power_below(double limit) { return std::exp2(std::floor(std::log2(limit))); }
 
-// Bounds of the iterates' singular values from the coefficients, by sampling s -> |a s + b s^3 + c s^5| and the
-// polynomial itself with slack for what lies between the samples and for rounding.  False: they grow too far.
-bool find_range(const zero_muon_hyper_t& hyper, Range* r)
+// Bounds of the singular values of all of them from the coefficients, by sampling the functions of one singular value
+// that they are, with slack for what lies between the samples and for rounding.  False: they grow too far.
+bool find_range(const zero_muon_hyper_t& hyper, bool pair, Range* r)
 {
     constexpr int kSamples = 4096;
-    double hi = 1.0, x = 1.0, g = 1.0, q = 0.0;
+    double hi = 1.0, x = 1.0, most[kRoles];
+    for (double& m : most) m = 1e-6;
+    auto see = [&](Role role, double v) { most[role] = std::max(most[role], std::fabs(v)); };
     for (int k = 0; k < hyper.steps; ++k) {
         const double* c = hyper.coefficients[k];
         double next = 0.0;
         for (int i = 0; i <= kSamples; ++i) {
-            const double s = hi * i / kSamples, s2 = s * s, rest = c[1] * s2 + c[2] * s2 * s2, poly = c[0] + rest;
+            const double s = hi * i / kSamples, g = s * s, rest = c[1] * g + c[2] * g * g, poly = c[0] + rest;
             next = std::max(next, std::fabs(s * poly));
-            q = std::max(q, std::max(std::fabs(poly), std::fabs(rest)));
+            see(kG, g);
+            see(kPoly, poly);
+            see(kPoly, rest);
+            if (k == 0 && pair && hyper.steps > 1) {
+                const double* e = hyper.coefficients[1];
+                const double g2 = g * poly * poly, rest2 = e[1] * g2 + e[2] * g2 * g2;
+                see(kR1, rest);
+                see(kW, rest * g);
+                see(kG2, g2);
+                see(kR2, rest2);
+                see(kQ, poly * (e[0] + rest2) - c[0] * e[0]);
+            }
         }
         hi = std::max(1.01 * next, 1e-6);
-        if (!(hi <= 8.0) || !(q <= 1024.0)) return false;
+        if (!(hi <= 8.0)) return false;
         x = std::max(x, hi);
-        g = std::max(g, hi * hi);
     }
     r->sigma = power_below(24000.0 / x);
-    r->alpha = power_below(24000.0 / g);
-    r->beta = power_below(24000.0 / std::max(q, 1e-3));
+    for (int i = 0; i < kRoles; ++i) {
+        if (!(most[i] <= 16384.0)) return false;
+        r->factor[i] = power_below(24000.0 / most[i]);
+    }
     return true;
 }
 
@@ -581,7 +691,7 @@ void cut_tiles(zero_muon* h, int which, int cg, std::vector<Piece>* out, double*
     *us = std::max(longest, work / slots) + 0.5 * longest;
 }
 
-zero_status_t check_hyper(const zero_muon_hyper_t* hyper, Range* range, const char* who)
+zero_status_t check_hyper(const zero_muon* h, const zero_muon_hyper_t* hyper, Range* range, const char* who)
 {
     const std::string w = std::string(who) + ": ";
     if (!hyper) return fail(ZERO_EINVAL, w + "NULL argument");
@@ -594,7 +704,7 @@ zero_status_t check_hyper(const zero_muon_hyper_t* hyper, Range* range, const ch
     for (int k = 0; k < hyper->steps; ++k)
         for (int j = 0; j < 3; ++j)
             if (!std::isfinite(hyper->coefficients[k][j])) return fail(ZERO_EINVAL, w + "a coefficient is not finite");
-    if (!find_range(*hyper, range)) return fail(ZERO_ERANGE, w + "the coefficients let singular values of at most 1 grow beyond 8");
+    if (!find_range(*hyper, h && h->pair, range)) return fail(ZERO_ERANGE, w + "the coefficients let singular values of at most 1 grow beyond 8");
     return ZERO_OK;
 }
 
@@ -623,6 +733,7 @@ MuonParams params(const zero_muon* h, const zero_muon_hyper_t& hyper, double los
     P.scale = reinterpret_cast<float*>(ws + h->at_scale);
     P.tickets = reinterpret_cast<uint32_t*>(ws + h->at_tickets);
     P.n_d = h->n_d;
+    P.rounds = h->rounds;
     P.nesterov = (hyper.flags & ZERO_MUON_NESTEROV) != 0;
     P.how = hyper.scale;
     P.inv = (float)(1.0 / ((double)h->n_d * loss_scale));
@@ -635,7 +746,7 @@ MuonParams params(const zero_muon* h, const zero_muon_hyper_t& hyper, double los
     return P;
 }
 
-int pass_grid(int64_t pieces) { return (int)std::max<int64_t>(1, std::min<int64_t>(pieces, 6 * kGb300Sms)); }
+int pass_grid(int64_t pieces) { return (int)std::max<int64_t>(1, std::min<int64_t>(pieces, kPassBlocks * kGb300Sms)); }
 
 zero_status_t launch_reduce(const zero_muon* h, MuonParams P, cudaStream_t s)
 {
@@ -677,30 +788,72 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
     if (P.count > 0) {
         e = launch_after(muon_start_kernel, grid, kThreads, 0, s, P);
         if (e != cudaSuccess) return cuda_fail(e, "zero_muon: launch");
-        for (int k = 0; k < hyper.steps; ++k) {
-            const double *c = hyper.coefficients[k], a2 = R.alpha * R.alpha;
-            const bool twice = k < kTwice;
-            ProductParams Q;
-            std::memset(&Q, 0, sizeof(Q));
-            Q.tensors = P.tensors;
-            Q.src = k & 1;
-            Q.scale = (float)(R.alpha / (R.sigma * R.sigma));
-            zero_status_t st = launch_product<kGram>(h, Q, s);
-            if (st != ZERO_OK) return st;
-            Q.scale = (float)(c[2] * R.beta / a2);
-            Q.lin = (float)(c[1] * R.beta / R.alpha);
-            Q.diag = twice ? 0.0f : (float)(c[0] * R.beta);
-            st = launch_product<kPoly>(h, Q, s);
-            if (st != ZERO_OK) return st;
-            Q.scale = (float)(1.0 / R.beta);
-            Q.lin = (float)c[0];
-            Q.twice = twice;
-            Q.keep_low = k + 1 < kTwice && k + 1 < hyper.steps;
-            st = launch_product<kNext>(h, Q, s);
-            if (st != ZERO_OK) return st;
+        zero_status_t st = ZERO_OK;
+        ProductParams Q;
+        std::memset(&Q, 0, sizeof(Q));
+        Q.tensors = P.tensors;
+        // one symmetric product: out = f left right + l0 add0 + l1 add1 + d I, of values (their factors in fp16 are
+        // range's)
+        auto square = [&](Role left, Role right, Role out, double f, double d, std::initializer_list<std::pair<Role, double>> adds) {
+            if (st != ZERO_OK) return;
+            ProductParams S = Q;
+            S.left = kSlot[left];
+            S.right = kSlot[right];
+            S.out = kSlot[out];
+            S.scale = (float)(f * R.of(out) / (R.of(left) * R.of(right)));
+            S.diag = (float)(d * R.of(out));
+            for (const auto& a : adds) {
+                S.add[S.adds] = kSlot[a.first];
+                S.lin[S.adds++] = (float)(a.second * R.of(out) / R.of(a.first));
+            }
+            st = launch_product<kSquare>(h, S, s);
+        };
+        auto gram = [&]() {
+            if (st != ZERO_OK) return;
+            ProductParams S = Q;
+            S.out = kSlot[kG];
+            S.scale = (float)(R.of(kG) / (R.sigma * R.sigma));
+            st = launch_product<kGram>(h, S, s);
+        };
+        // X <- poly X (+ d X where the polynomial is without d I, X with its low part)
+        auto next = [&](Role poly, double d, bool keep_low) {
+            if (st != ZERO_OK) return;
+            ProductParams S = Q;
+            S.left = kSlot[poly];
+            S.scale = (float)(1.0 / R.of(poly));
+            if (d != 0.0) {
+                S.adds = 2;
+                S.lin[0] = (float)d;
+                S.lin[1] = (float)(d / kLow);
+            }
+            S.keep_low = keep_low;
+            st = launch_product<kNext>(h, S, s);
+            Q.src ^= 1;
+        };
+        int k = 0;
+        if (h->pair && hyper.steps >= 2) {
+            // Two iterations at once.  The second's G is (a I + R1) G (a I + R1), R1 = b G + c G^2, as polynomials of G
+            // commute: products of the smaller side instead of two passes over X, and nothing rounds the X between.
+            const double *c = hyper.coefficients[0], *e = hyper.coefficients[1];
+            gram();
+            square(kG, kG, kR1, c[2], 0.0, {{kG, c[1]}});
+            square(kR1, kG, kW, 1.0, 0.0, {});
+            square(kR1, kW, kG2, 1.0, 0.0, {{kG, c[0] * c[0]}, {kW, 2.0 * c[0]}});
+            square(kG2, kG2, kR2, e[2], 0.0, {{kG2, e[1]}});
+            square(kR2, kR1, kQ, 1.0, 0.0, {{kR1, e[0]}, {kR2, c[0]}});
+            next(kQ, c[0] * e[0], false);
+            k = 2;
         }
+        for (; k < hyper.steps && st == ZERO_OK; ++k) {
+            const double* c = hyper.coefficients[k];
+            const bool twice = !h->pair && k < kTwice;
+            gram();
+            square(kG, kG, kPoly, c[2], twice ? 0.0 : c[0], {{kG, c[1]}});
+            next(kPoly, twice ? c[0] : 0.0, twice && k + 1 < kTwice && k + 1 < hyper.steps);
+        }
+        if (st != ZERO_OK) return st;
+        P.src = Q.src;
     }
-    P.src = hyper.steps & 1;
     e = h->dtype16 == ZERO_BF16 ? launch_after(muon_apply_kernel<ZERO_BF16>, grid, kThreads, 0, s, P)
                                 : launch_after(muon_apply_kernel<ZERO_FP16>, grid, kThreads, 0, s, P);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
@@ -739,24 +892,31 @@ try {
     std::unique_ptr<zero_muon> h(new zero_muon);
     h->n_d = n_contribs;
     h->dtype16 = dtype16;
-    int64_t at = 0, pieces = 0;
+    int64_t at = 0;
     for (int64_t i = 0; i < n_matrices; ++i) {
         const int64_t r = rows[i], c = cols[i];
         if (r < 0 || c < 0) return fail(ZERO_EINVAL, "zero_muon_create: negative size");
         if (r > ZERO_MUON_MAX_SIZE || c > ZERO_MUON_MAX_SIZE || std::min(r, c) > ZERO_MUON_MAX_SIDE)
             return fail(ZERO_ERANGE, "zero_muon_create: a matrix beyond ZERO_MUON_MAX_SIZE, or its smaller side beyond ZERO_MUON_MAX_SIDE");
-        pieces += div_up(r * c, kChunk);
-        if (pieces > INT32_MAX / 16) return fail(ZERO_ERANGE, "zero_muon_create: the matrices have too many elements");
         h->elems += r * c;
+        if (h->elems > (int64_t)1 << 40) return fail(ZERO_ERANGE, "zero_muon_create: more than 2^40 elements");
         h->state_elems += up(r * c, kStateBlock);
     }
     h->rows.assign(rows, rows + n_matrices);
     h->cols.assign(cols, cols + n_matrices);
+    // four pieces a block of the passes, so that few wait for the last; at most 32768 elements, at least 2048
+    h->rounds = (int)std::min<int64_t>(16, std::max<int64_t>(1, h->elems / ((int64_t)4 * kPassBlocks * kGb300Sms * kChunk)));
+    const int64_t piece = (int64_t)h->rounds * kChunk;
     for (int64_t i = 0; i < n_matrices; ++i) {
         const int64_t r = rows[i], c = cols[i];
-        for (int64_t k = 0; k < div_up(r * c, kChunk); ++k) h->chunks.push_back(Piece{(int32_t)i, (int32_t)k});
-        for (int64_t k = 0; k < div_up(r * up(c, 8), kChunk); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
+        for (int64_t k = 0; k < div_up(r * c, piece); ++k) h->chunks.push_back(Piece{(int32_t)i, (int32_t)k});
+        for (int64_t k = 0; k < div_up(r * up(c, 8), piece); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
     }
+    // Two iterations at once replace two passes over X by products of the smaller side, and are as exact from sides of
+    // 64 on; for small sides the second G's largest values, differences of larger terms, are not.
+    h->pair = h->elems > 0;
+    for (int64_t i = 0; i < n_matrices; ++i)
+        if (rows[i] * cols[i] > 0 && std::min(rows[i], cols[i]) < kPairSide) h->pair = false;
     for (int which = 0; which < 2; ++which) {
         std::vector<Piece> small, large;
         double us1 = 0.0, us2 = 0.0;
@@ -781,7 +941,7 @@ try {
     h->at_tickets = take(4 * n_matrices);
     h->at_data = at;
     for (int64_t i = 0; i < n_matrices; ++i)
-        if (rows[i] * cols[i] > 0) at += 2 * (3 * x_elems(rows[i], cols[i]) + 2 * g_elems(std::min(rows[i], cols[i])));
+        if (rows[i] * cols[i] > 0) at += 2 * (3 * x_elems(rows[i], cols[i]) + kSquares * g_elems(std::min(rows[i], cols[i])));
     h->bytes = at;
     *out = h.release();
     return ZERO_OK;
@@ -841,7 +1001,7 @@ try {
             T.ldm = (int32_t)up(m, 8);
             T.wide = r <= c;
             T.at = at;
-            T.chunks = (int32_t)div_up(r * c, kChunk);
+            T.chunks = (int32_t)div_up(r * c, (int64_t)h->rounds * kChunk);
             T.aspect = (float)std::sqrt(std::max(1.0, (double)r / (double)c));
             T.rms = (float)(0.2 * std::sqrt((double)std::max(r, c)));
             T.p = params ? params[i] : nullptr;
@@ -865,16 +1025,15 @@ try {
             T.x[0] = q;
             T.x[1] = q + x;
             T.low = q + 2 * x;
-            T.a = q + 3 * x;
-            T.b = T.a + g;
-            data += 2 * (3 * x + 2 * g);
+            for (int k = 0; k < kSquares; ++k) T.square[k] = q + 3 * x + k * g;
+            data += 2 * (3 * x + kSquares * g);
             zero_status_t st = ZERO_OK;
             for (int k = 0; k < 2 && st == ZERO_OK; ++k) {
                 st = encode(&T.xk[k], Operand{T.x[k], r, c, T.ldx, false}, ZERO_FP16, kBM, "zero_muon_bind");
                 if (st == ZERO_OK) st = encode(&T.xm[k], Operand{T.x[k], c, r, T.ldx, true}, ZERO_FP16, kBM, "zero_muon_bind");
             }
-            if (st == ZERO_OK) st = encode(&T.ak, Operand{T.a, m, m, T.ldm, false}, ZERO_FP16, kBM, "zero_muon_bind");
-            if (st == ZERO_OK) st = encode(&T.bk, Operand{T.b, m, m, T.ldm, false}, ZERO_FP16, kBM, "zero_muon_bind");
+            for (int k = 0; k < kSquares && st == ZERO_OK; ++k)
+                st = encode(&T.sq[k], Operand{T.square[k], m, m, T.ldm, false}, ZERO_FP16, kBM, "zero_muon_bind");
             if (st != ZERO_OK) return st;
             at += up(r * c, kStateBlock);
         }
@@ -908,7 +1067,7 @@ zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, dou
 try {
     if (!h) return fail(ZERO_EINVAL, "zero_muon_step: NULL handle");
     Range R;
-    zero_status_t st = check_hyper(hyper, &R, "zero_muon_step");
+    zero_status_t st = check_hyper(h, hyper, &R, "zero_muon_step");
     if (st != ZERO_OK) return st;
     if (!(loss_scale > 0.0) || !std::isfinite(loss_scale)) return fail(ZERO_EINVAL, "zero_muon_step: loss_scale must be positive");
     st = ready(h, "zero_muon_step");
@@ -925,7 +1084,7 @@ catch (...) {
 zero_status_t zero_muon_check(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream)
 try {
     Range R;
-    zero_status_t st = check_hyper(hyper, &R, "zero_muon_check");
+    zero_status_t st = check_hyper(h, hyper, &R, "zero_muon_check");
     if (st == ZERO_OK) st = plan_ready(h, plan, "zero_muon_check");
     if (st != ZERO_OK) return st;
     if (h->checked_in == plan->step_no) return fail(ZERO_ESTATE, "zero_muon_check: already part of this step");
@@ -947,7 +1106,7 @@ catch (...) {
 zero_status_t zero_muon_step_with(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream)
 try {
     Range R;
-    zero_status_t st = check_hyper(hyper, &R, "zero_muon_step_with");
+    zero_status_t st = check_hyper(h, hyper, &R, "zero_muon_step_with");
     if (st == ZERO_OK) st = plan_ready(h, plan, "zero_muon_step_with");
     if (st != ZERO_OK) return st;
     if (h->checked_in != plan->step_no) return fail(ZERO_ESTATE, "zero_muon_step_with: needs zero_muon_check in the same step");
