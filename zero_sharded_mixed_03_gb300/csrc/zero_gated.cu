@@ -70,7 +70,6 @@ __device__ __forceinline__ void add_bias(float (&x)[32], const uint16_t* bias, b
 template <int CG, int BN, int MODE, int DT>
 struct GatedWork {
     const GatedParams& P;
-    int count;
     static constexpr int kBRows = BN / CG;
     struct Item {
         int m, n, kb, problem;
@@ -86,7 +85,14 @@ struct GatedWork {
         I.kb = P.k_blocks;
         return I;
     }
-    __device__ __forceinline__ void begin(const Item&) const {}
+    __device__ __forceinline__ void range(int worker, int workers, int& i, int& end, int& step) const
+    {
+        i = worker;
+        end = P.count;
+        step = workers;
+    }
+    __device__ __forceinline__ bool begin(const Item&) const { return true; }
+    __device__ __forceinline__ void done(const Item&, int) const {}
     __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (P.a_rows + kBRows) * (kBK * 2); }
     __device__ __forceinline__ bool a_mn(const Item&) const { return MODE == kWeights; }
     __device__ __forceinline__ bool b_mn(const Item&) const { return P.b_mn; }
@@ -172,7 +178,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) ga
     Tiles<CG, BN> T;
     T.open(smem_raw);
     after_earlier_work();
-    T.run(GatedWork<CG, BN, MODE, DT>{P, P.count}, &g_gated_error);
+    T.run(GatedWork<CG, BN, MODE, DT>{P}, &g_gated_error);
 }
 
 // The block over an empty inner dimension: g = bg, u = bu.

@@ -248,12 +248,14 @@ struct GemmShape {
 //
 // One thread copies operand tiles into the ring, one issues the products, eight warps finish a tile while the next
 // is multiplied: the frame of a persistent kernel whose tiles W describes:
-//   int count                               tiles, walked with the grid's stride
+//   range(worker, workers, i, end, step)    the tiles of a block or pair
 //   Item item(int)                          where a tile is; Item::kb: its inner blocks, at least one
 //   uint32_t bytes(Item)                    what a stage's copies bring, to both blocks of a pair
-//   begin(Item); load(Item, kb, a, b, bar, rank)   those copies: what precedes a tile's, and a stage's
+//   bool begin(Item)                        before its copies: what they wait for; false: given up
+//   load(Item, kb, a, b, bar, rank)      those copies
 //   a_mn(Item), b_mn(Item), idesc(Item)     how the operands lie, and the product's descriptor
 //   prepare(Item, quad, half, rank, lane, Ahead&)      what a tile's end may load before its products are done
+//   done(Item, lane)                                   by each of those warps once its part is stored
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
@@ -306,16 +308,18 @@ struct Tiles {
     template <class W>
     __device__ __forceinline__ void run(const W& work, uint32_t* error)
     {
-        const int first = blockIdx.x / CG, step = gridDim.x / CG;
+        int first, end, step;
+        work.range((int)(blockIdx.x / CG), (int)(gridDim.x / CG), first, end, step);
         bool ok = true;
         if (warp == 0) {
             // ---- producer: one thread
             if (lane == 0) {
                 uint32_t k = 0;
-                for (int i = first; i < work.count && ok; i += step) {
+                for (int i = first; i < end && ok; i += step) {
                     const typename W::Item I = work.item(i);
                     const uint32_t bytes = work.bytes(I);
-                    work.begin(I);
+                    ok = work.begin(I);
+                    if (!ok) break;
                     for (int kb = 0; kb < I.kb; ++kb, ++k) {
                         const uint32_t s = k % S::kStages, use = k / S::kStages;
                         if (use > 0 && !mbar_wait(empty0 + 8 * s, (use - 1) & 1, kGemmWaitNs)) {
@@ -334,7 +338,7 @@ struct Tiles {
             // ---- products: one thread of the leading block
             if (lane == 0 && rank == 0) {
                 uint32_t k = 0, tile = 0;
-                for (int i = first; i < work.count && ok; i += step, ++tile) {
+                for (int i = first; i < end && ok; i += step, ++tile) {
                     const typename W::Item I = work.item(i);
                     const bool a_mn = work.a_mn(I), b_mn = work.b_mn(I);
                     const uint32_t idesc = work.idesc(I), acc = tile & 1, use = tile >> 1;
@@ -370,7 +374,7 @@ struct Tiles {
             const uint32_t stage = epi0 + (warp - 4) * kEpiBytes;
             const uint32_t acc_empty_leader = CG == 2 ? leader_address(acc_empty0) : acc_empty0;
             uint32_t tile = 0;
-            for (int i = first; i < work.count && ok; i += step, ++tile) {
+            for (int i = first; i < end && ok; i += step, ++tile) {
                 const typename W::Item I = work.item(i);
                 const uint32_t acc = tile & 1, use = tile >> 1;
                 typename W::Ahead ahead;
@@ -386,6 +390,7 @@ struct Tiles {
                     if constexpr (CG == 2) arrive_cluster(acc_empty_leader + 8 * acc);
                     else mbar_arrive(acc_empty0 + 8 * acc);
                 }
+                work.done(I, lane);
             }
         }
         if (!ok) {

@@ -6,9 +6,10 @@
 //   p <- p - lr wd p;  p <- p - lr s X
 //
 // A pass over the contributions forms m' and the norms, one over the momentum the first X; then each iteration is three
-// products on the tensor cores, each of them one launch for the tiles of every matrix: G and the polynomial of it, of
-// which the upper triangle's tiles are multiplied and written twice, and the polynomial times X.  Nothing is
-// transposed in memory: a tensor map takes X along its rows or along its columns.
+// products on the tensor cores: G and the polynomial of it, of which the upper triangle's tiles are multiplied and
+// written twice, and the polynomial times X.  Nothing is transposed in memory: a tensor map takes X along its rows or
+// along its columns.  All products of all matrices are one cooperative launch: a matrix's next product begins when
+// the one before it is complete, whatever the other matrices do, so that no round of tiles has to be full.
 //
 // Operands are fp16 whatever the gradients' type, times powers of two that keep them in its range (the iterates' are
 // bounded: ||X||_2 <= 1 at first, and the coefficients give the rest).  Rounding to bf16's 8 bits costs 1 to 3 % of the
@@ -17,6 +18,7 @@
 // nearly all of small singular values' growth, both) 0.1 to 0.3 %.  Sums are fp32.
 #include <cmath>
 #include <cstring>
+#include <functional>
 #include <initializer_list>
 #include <memory>
 #include <utility>
@@ -31,10 +33,14 @@ namespace {
 __device__ uint32_t g_muon_error;
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8 * kThreads;      // elements of a matrix that a block takes at a time, or a multiple of them
+// Elements of a matrix that a block takes at a time, eight a thread.  Blocks take neighbouring ones in turn, so that
+// what runs at one time reads a few MB of each contribution: with 32768 in a row the contributions' pages are too many
+// (16 of 100M elements: 895 us; with 8192 816).
+constexpr int kChunk = 8 * kThreads;
 constexpr int kPassBlocks = 6;            // blocks an SM of a pass over the elements
 constexpr int kStateBlock = 256;          // each matrix's momentum starts on a multiple of it
 constexpr int kSquares = 4;               // symmetric matrices beside each X
+constexpr int kMaxPhases = 32;            // products of a step, at most 25
 constexpr int kTwice = 2;                 // iterations whose X is the sum of two fp16 numbers
 constexpr int kPairSide = 128;            // smaller sides from which the first two iterations are one
 constexpr float kLow = 2048.0f;           // the second of them is stored times this
@@ -61,6 +67,7 @@ struct alignas(128) MuonTensor {
     int32_t wide;                // rows <= cols: G = X X^T
     int32_t vec_g, vec_p;        // 16-byte accesses to the contributions; to p, p16 and update
     int32_t chunks;              // of the first pass
+    int32_t tiles[2];            // of a symmetric product, and of one with X
 };
 
 // A piece of a matrix's elements, or a tile of it (m << 16 | n).
@@ -78,7 +85,9 @@ struct MuonParams {
     double* slots;               // [piece of the first pass] sums of squares
     float* scale;                // [tensor] 1 / (norm + eps)
     uint32_t* tickets;           // [tensor]
-    int32_t count, rounds, n_d, nesterov, src, how;   // rounds: multiples of kChunk in a piece
+    uint32_t* counters;          // [tensor][kMaxPhases]: warps that have stored their part of a product's tile
+    int32_t n_counters;
+    int32_t count, n_d, nesterov, src, how;
     float inv, mu, nu, sigma, lr, decay;   // nu = 1 - mu; sigma: X's factor in fp16
     double eps;
 };
@@ -141,31 +150,43 @@ __device__ __forceinline__ void sum_contributions(const void* const* grads, int 
     }
 }
 
+// A block's sum of squares of a matrix goes to the slot of its first piece of it; the last of the blocks that have any
+// sums them, in order.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) muon_reduce_kernel(const __grid_constant__ MuonParams P)
+__global__ void __launch_bounds__(kThreads, 5) muon_reduce_kernel(const __grid_constant__ MuonParams P)
 {
     after_earlier_work();
     __shared__ double warp_sum[kThreads / 32];
+    __shared__ const void* grads[ZERO_MAX_RANKS];
     __shared__ bool last;
     const uint32_t cur = *(const volatile uint32_t*)&P.st->cur;
     const float *from = P.momentum[cur & 1];
     float* to = P.momentum[(cur & 1) ^ 1];
     const float inv = contribution_scale(P);
-    for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
-        const Piece piece = P.pieces[i];
-        const MuonTensor& T = P.tensors[piece.tensor];
-        const int64_t elems = (int64_t)T.rows * T.cols, e0 = (int64_t)piece.at * P.rounds * kChunk;
-        const void* const* grads = P.grads + (int64_t)piece.tensor * P.n_d;
+    int i = blockIdx.x;
+    Piece next = P.pieces[min(i, P.count - 1)];
+    while (i < P.count) {
+        // every piece of this block of one matrix
+        const int tensor = next.tensor, first = i;
+        const MuonTensor& T = P.tensors[tensor];
+        const int64_t elems = (int64_t)T.rows * T.cols, at = T.at;
+        const int chunks = T.chunks, head = i - next.at;
+        const bool vec = T.vec_g;
+        __syncthreads();
+        for (int r = threadIdx.x; r < P.n_d; r += kThreads) grads[r] = P.grads[(int64_t)tensor * P.n_d + r];
+        __syncthreads();
         float sum = 0.0f;
-        for (int k = 0; k < P.rounds; ++k) {
-            const int64_t e = e0 + ((int64_t)k * kThreads + threadIdx.x) * 8;
-            const int n = (int)min((int64_t)8, elems - e);
-            if (n <= 0) break;
+        while (i < P.count && next.tensor == tensor) {
+            const int64_t e = (int64_t)next.at * kChunk + threadIdx.x * 8;
+            const int n = (int)max((int64_t)0, min((int64_t)8, elems - e));
+            i += gridDim.x;
+            next = P.pieces[min(i, P.count - 1)];
+            if (n <= 0) continue;
             // the momentum's rows of eight are whole: it is padded
-            const float4* q = reinterpret_cast<const float4*>(from + T.at + e);
+            const float4* q = reinterpret_cast<const float4*>(from + at + e);
             const float4 a = __ldcs(q), b = __ldcs(q + 1);
             float g[8];
-            sum_contributions<DT>(grads, P.n_d, e, n, T.vec_g, g);
+            sum_contributions<DT>(grads, P.n_d, e, n, vec, g);
             const float m0[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             float m1[8];
 #pragma unroll
@@ -174,36 +195,40 @@ __global__ void __launch_bounds__(kThreads) muon_reduce_kernel(const __grid_cons
                 const float u = j < n ? ahead(m0[j], m1[j], P) : 0.0f;
                 sum = fmaf(u, u, sum);
             }
-            float4* o = reinterpret_cast<float4*>(to + T.at + e);
+            float4* o = reinterpret_cast<float4*>(to + at + e);
             o[0] = make_float4(m1[0], m1[1], m1[2], m1[3]);
             o[1] = make_float4(m1[4], m1[5], m1[6], m1[7]);
         }
+        const int sharers = min(chunks, (int)gridDim.x);
         const double s = block_sum_fixed<kThreads>((double)sum, warp_sum);
-        const int first = i - piece.at;          // a matrix's pieces follow one another
         if (threadIdx.x == 0) {
-            P.slots[i] = s;
+            P.slots[first] = s;
             __threadfence();
-            last = atomicAdd(&P.tickets[piece.tensor], 1u) == (uint32_t)T.chunks - 1;
+            last = atomicAdd(&P.tickets[tensor], 1u) == (uint32_t)sharers - 1;
         }
         __syncthreads();
         if (!last) continue;
         __threadfence();
-        const volatile double* slots = P.slots + first;
+        const volatile double* slots = P.slots + head;
         double x = 0.0;
-        for (int k = threadIdx.x; k < T.chunks; k += kThreads) x += slots[k];
+        for (int k = threadIdx.x; k < sharers; k += kThreads) x += slots[k];
         const double norm2 = block_sum_fixed<kThreads>(x, warp_sum);
         if (threadIdx.x == 0) {
-            P.tickets[piece.tensor] = 0;
-            P.scale[piece.tensor] = (float)(1.0 / (sqrt(norm2) + P.eps));
-            if (!isfinite(norm2)) {
-                atomicOr(P.plan ? &P.plan->flag : &P.st->flag, 1u);
-            }
+            P.tickets[tensor] = 0;
+            P.scale[tensor] = (float)(1.0 / (sqrt(norm2) + P.eps));
+            if (!isfinite(norm2)) atomicOr(P.plan ? &P.plan->flag : &P.st->flag, 1u);
         }
-        __syncthreads();
     }
 }
 
 // ------------------------------------------------------------------ the first X
+
+__device__ __forceinline__ void load_floats(const float* p, float (&x)[8])
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
 
 __device__ __forceinline__ void two_halves(const float (&x)[8], uint32_t (&hi)[4], uint32_t (&low)[4])
 {
@@ -216,64 +241,58 @@ __device__ __forceinline__ void two_halves(const float (&x)[8], uint32_t (&hi)[4
     }
 }
 
-// Piece `at` of the matrix in groups of eight columns: f(row, column, columns there, group's place in X).
-template <typename F>
-__device__ __forceinline__ void for_groups(const MuonTensor& T, int at, int rounds, F&& f)
+// This thread's eight columns in piece `at` of a matrix, cut as X is laid out: where they are in the matrix and in X,
+// and how many are there (0: none of it).
+struct Eight {
+    int64_t e, x;
+    int n;
+};
+
+__device__ __forceinline__ Eight eight_at(const MuonTensor& T, int at)
 {
-    const int groups = T.ldx / 8;
-    const int64_t total = (int64_t)T.rows * groups;
-#pragma unroll 2
-    for (int k = 0; k < rounds; ++k) {
-        const int64_t i = ((int64_t)at * rounds + k) * kThreads + threadIdx.x;
-        if (i >= total) break;
-        int64_t row = 0;
-        int col = 0;
-        if (T.cols == T.ldx) {
-            f(i * 8, 8, i * 8);          // the matrix is as X is laid out
-        } else {
-            row = i / groups;
-            col = (int)(i - row * groups) * 8;
-            f(row * T.cols + col, min(8, T.cols - col), i * 8);
-        }
+    const int64_t groups = T.ldx / 8, i = (int64_t)at * kThreads + threadIdx.x;
+    Eight E{i * 8, i * 8, 8};
+    if (i >= T.rows * groups) {
+        E.n = 0;
+    } else if (T.cols != T.ldx) {
+        const int64_t row = i / groups, col = (i - row * groups) * 8;
+        E.e = row * T.cols + col;
+        E.n = (int)min((int64_t)8, T.cols - col);
     }
+    return E;
 }
 
-__global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_constant__ MuonParams P)
+__global__ void __launch_bounds__(kThreads, 6) muon_start_kernel(const __grid_constant__ MuonParams P)
 {
     after_earlier_work();
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < P.n_counters; i += gridDim.x * kThreads) P.counters[i] = 0;
     const uint32_t cur = *(const volatile uint32_t*)&P.st->cur;
+    Piece next = P.pieces[min((int)blockIdx.x, P.count - 1)];
     for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
-        const Piece piece = P.pieces[i];
+        const Piece piece = next;
+        next = P.pieces[min(i + (int)gridDim.x, P.count - 1)];
         const MuonTensor& T = P.tensors[piece.tensor];
+        const Eight E = eight_at(T, piece.at);
+        if (E.n == 0) continue;
         const float scale = P.scale[piece.tensor];
-        const float *old = P.momentum[cur & 1] + T.at, *now = P.momentum[(cur & 1) ^ 1] + T.at;
-        for_groups(T, piece.at, P.rounds, [&](int64_t e, int n, int64_t out) {
-            float m0[8], m1[8], x[8];
-            if (T.cols == T.ldx) {
-                const float4* q = reinterpret_cast<const float4*>(now + e);
-                const float4 a = q[0], b = q[1];
-                m1[0] = a.x; m1[1] = a.y; m1[2] = a.z; m1[3] = a.w;
-                m1[4] = b.x; m1[5] = b.y; m1[6] = b.z; m1[7] = b.w;
-                if (P.nesterov) {
-                    const float4* r = reinterpret_cast<const float4*>(old + e);
-                    const float4 c = r[0], d = r[1];
-                    m0[0] = c.x; m0[1] = c.y; m0[2] = c.z; m0[3] = c.w;
-                    m0[4] = d.x; m0[5] = d.y; m0[6] = d.z; m0[7] = d.w;
-                }
-            } else {
+        const float *old = P.momentum[cur & 1] + T.at + E.e, *now = P.momentum[(cur & 1) ^ 1] + T.at + E.e;
+        float m0[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, m1[8], x[8];
+        if (T.cols == T.ldx) {
+            load_floats(now, m1);
+            if (P.nesterov) load_floats(old, m0);
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    m1[j] = j < n ? now[e + j] : 0.0f;
-                    m0[j] = j < n && P.nesterov ? old[e + j] : 0.0f;
-                }
+            for (int j = 0; j < 8; ++j) {
+                m1[j] = j < E.n ? now[j] : 0.0f;
+                m0[j] = j < E.n && P.nesterov ? old[j] : 0.0f;
             }
-            uint32_t hi[4], low[4];
+        }
+        uint32_t hi[4], low[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (ahead(m0[j], m1[j], P) * scale) * P.sigma;
-            two_halves(x, hi, low);
-            *reinterpret_cast<uint4*>(T.x[0] + out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(T.low + out) = make_uint4(low[0], low[1], low[2], low[3]);
-        });
+        for (int j = 0; j < 8; ++j) x[j] = (ahead(m0[j], m1[j], P) * scale) * P.sigma;
+        two_halves(x, hi, low);
+        *reinterpret_cast<uint4*>(T.x[0] + E.x) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(T.low + E.x) = make_uint4(low[0], low[1], low[2], low[3]);
     }
 }
 
@@ -282,17 +301,31 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
 // X X^T (or X^T X); a product of two symmetric matrices that commute, so that it is one too; one times X.
 enum { kGram = 0, kSquare = 1, kNext = 2 };
 
-// out = scale acc + lin[0] add0 + lin[1] add1 + diag I.  Symmetric matrices by their numbers; kNext's addends are X
-// and its low part.
-struct ProductParams {
-    const MuonTensor* tensors;
-    const Piece* tiles;
-    int32_t count, src;          // src: X's buffer that is read
+// One product of every matrix: out = scale acc + lin[0] add0 + lin[1] add1 + diag I.  Symmetric matrices by their
+// slots; kNext's addends are X and its low part.
+struct Op {
+    int32_t kind, src;           // src: X's buffer that is read
     int32_t left, right, out;    // operands and result; kNext: left is the polynomial
     int32_t adds, add[2];
     int32_t keep_low;            // kNext: the successor's low part is wanted
     float scale, lin[2], diag;
 };
+
+struct ProductParams {
+    const MuonTensor* tensors;
+    const Piece* tiles;          // each worker's, in the order of the products: tensor | product << 16
+    const int32_t* bounds;       // [worker][kMaxPhases]: where its tiles of each product begin
+    uint32_t* counters;
+    int32_t first, last;         // products that are made
+    Op ops[kMaxPhases];          // ops[i - first] is product i
+};
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p)
+{
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // row `lane` of a tile: x, written as its transpose at (col0, row0)
 __device__ __forceinline__ void put_tile_across(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
@@ -305,53 +338,101 @@ __device__ __forceinline__ void put_tile_across(uint32_t stage, int lane, const 
     __syncwarp();
 }
 
-template <int CG, int BN, int KIND>
+template <int CG, int BN>
 struct MuonWork {
     const ProductParams& P;
-    int count;
     struct Item {
         const MuonTensor* T;
-        int m, n, kb;
-        bool wide;
+        const Op* op;
+        const uint32_t* before;  // the matrix's counter of the product before, or NULL
+        uint32_t* counter;       // and of this one
+        const CUtensorMap *map_a, *map_b;
+        int m, n, kb, kind;
+        uint32_t want;           // of `before`
+        bool a_along, b_along;   // operands taken along their own rows
     };
+
+    __device__ __forceinline__ void range(int worker, int, int& i, int& end, int& step) const
+    {
+        i = P.bounds[worker * kMaxPhases + P.first];
+        end = P.bounds[worker * kMaxPhases + P.last];
+        step = 1;
+    }
+
+    __device__ __forceinline__ Item item(int i) const
+    {
+        const Piece t = P.tiles[i];
+        const int tensor = t.tensor & 0xFFFF, phase = (t.tensor >> 16) - P.first;
+        Item I;
+        I.T = P.tensors + tensor;
+        I.op = &P.ops[phase];
+        I.m = t.at >> 16;
+        I.n = t.at & 0xFFFF;
+        I.kind = I.op->kind;
+        I.counter = P.counters + tensor * kMaxPhases + phase;
+        I.before = phase > 0 ? I.counter - 1 : nullptr;
+        I.want = 0;
+        if (phase > 0) I.want = (uint32_t)I.T->tiles[P.ops[phase - 1].kind == kNext] * (kEpiWarps * CG);
+        const MuonTensor& T = *I.T;
+        const Op& O = *I.op;
+        const bool wide = T.wide;
+        int inner = T.m;
+        if (I.kind == kGram) {
+            I.map_a = I.map_b = wide ? &T.xk[O.src] : &T.xm[O.src];
+            I.a_along = I.b_along = !wide;
+            inner = wide ? T.cols : T.rows;
+        } else if (I.kind == kSquare) {
+            I.map_a = &T.sq[O.left];
+            I.map_b = &T.sq[O.right];
+            I.a_along = I.b_along = false;
+        } else {
+            I.map_a = wide ? &T.sq[O.left] : &T.xk[O.src];
+            I.map_b = wide ? &T.xm[O.src] : &T.sq[O.left];
+            I.a_along = false;
+            I.b_along = wide;
+        }
+        I.kb = (inner + kBK - 1) / kBK;
+        return I;
+    }
+
+    // Until every part of the product before is stored: a bounded wait.
+    __device__ __forceinline__ static bool wait_before(const Item& I)
+    {
+        if (!I.before || load_acquire(I.before) >= I.want) return true;
+        const uint64_t t0 = global_ns();
+        for (uint32_t i = 0; i < kWaitIterCap && global_ns() - t0 < kGemmWaitNs; ++i)
+            if (load_acquire(I.before) >= I.want) return true;
+        return false;
+    }
 
     // The tensor maps that a tile's copies take, written by the host into memory that may have held others.
     __device__ __forceinline__ static void see(const CUtensorMap* map)
     {
         asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
     }
-    __device__ __forceinline__ void begin(const Item& I) const
+    __device__ __forceinline__ bool begin(const Item& I) const
     {
-        const MuonTensor& T = *I.T;
-        if constexpr (KIND == kGram) {
-            see(I.wide ? &T.xk[P.src] : &T.xm[P.src]);
-        } else if constexpr (KIND == kSquare) {
-            see(&T.sq[P.left]);
-            if (P.right != P.left) see(&T.sq[P.right]);
-        } else {
-            see(&T.sq[P.left]);
-            see(I.wide ? &T.xm[P.src] : &T.xk[P.src]);
-        }
+        see(I.map_a);
+        see(I.map_b);
+        if (!wait_before(I)) return false;
+        // what other blocks stored is read by copies from here on
+        asm volatile("fence.proxy.async;" ::: "memory");
+        return true;
+    }
+    // Each lane's stores, then the warp's one release of them all.
+    __device__ __forceinline__ void done(const Item& I, int lane) const
+    {
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
     }
 
-    __device__ __forceinline__ Item item(int i) const
-    {
-        const Piece t = P.tiles[i];
-        Item I;
-        I.T = P.tensors + t.tensor;
-        I.m = t.at >> 16;
-        I.n = t.at & 0xFFFF;
-        I.wide = I.T->wide;
-        const int inner = KIND == kGram ? (I.wide ? I.T->cols : I.T->rows) : I.T->m;
-        I.kb = (inner + kBK - 1) / kBK;
-        return I;
-    }
     __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (kBM + BN / CG) * (kBK * 2); }
-    __device__ __forceinline__ bool a_mn(const Item& I) const { return KIND == kGram && !I.wide; }
-    __device__ __forceinline__ bool b_mn(const Item& I) const { return (KIND == kGram && !I.wide) || (KIND == kNext && I.wide); }
+    __device__ __forceinline__ bool a_mn(const Item& I) const { return I.a_along; }
+    __device__ __forceinline__ bool b_mn(const Item& I) const { return I.b_along; }
     __device__ __forceinline__ uint32_t idesc(const Item& I) const
     {
-        return (1u << 4) | ((a_mn(I) ? 1u : 0u) << 15) | ((b_mn(I) ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((kBM * CG) >> 4) << 24);
+        return (1u << 4) | ((I.a_along ? 1u : 0u) << 15) | ((I.b_along ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((kBM * CG) >> 4) << 24);
     }
 
     // 128 rows of an operand: along K in one box, along its own rows in two
@@ -367,19 +448,8 @@ struct MuonWork {
 
     __device__ __forceinline__ void load(const Item& I, int kb, uint32_t a, uint32_t b, uint32_t bar, int rank) const
     {
-        const int row_a = (I.m * CG + rank) * kBM, row_b = I.n * BN + rank * (BN / CG), k = kb * kBK;
-        const MuonTensor& T = *I.T;
-        if constexpr (KIND == kGram) {
-            const CUtensorMap* map = I.wide ? &T.xk[P.src] : &T.xm[P.src];
-            bring(map, !I.wide, a, row_a, k, bar);
-            bring(map, !I.wide, b, row_b, k, bar);
-        } else if constexpr (KIND == kSquare) {
-            bring(&T.sq[P.left], false, a, row_a, k, bar);
-            bring(&T.sq[P.right], false, b, row_b, k, bar);
-        } else {
-            bring(I.wide ? &T.sq[P.left] : &T.xk[P.src], false, a, row_a, k, bar);
-            bring(I.wide ? &T.xm[P.src] : &T.sq[P.left], I.wide, b, row_b, k, bar);
-        }
+        bring(I.map_a, I.a_along, a, (I.m * CG + rank) * kBM, kb * kBK, bar);
+        bring(I.map_b, I.b_along, b, I.n * BN + rank * (BN / CG), kb * kBK, bar);
     }
 
     // ---- a tile's end.  The addends of a 32 x 32 part are loaded while the one before it is finished, the first
@@ -395,24 +465,26 @@ struct MuonWork {
     __device__ __forceinline__ Place place(const Item& I) const
     {
         const MuonTensor& T = *I.T;
+        const Op& O = *I.op;
         Place L;
-        if constexpr (KIND == kNext) {
-            L.out = T.x[P.src ^ 1];
-            L.add[0] = T.x[P.src];
+        if (I.kind == kNext) {
+            L.out = T.x[O.src ^ 1];
+            L.add[0] = T.x[O.src];
             L.add[1] = T.low;
             L.ld = L.cols = T.ldx;
             L.rows = T.rows;
         } else {
-            L.out = T.square[P.out];
-            L.add[0] = T.square[P.add[0]];
-            L.add[1] = T.square[P.add[1]];
+            L.out = T.square[O.out];
+            L.add[0] = T.square[O.add[0]];
+            L.add[1] = T.square[O.add[1]];
             L.ld = L.cols = T.ldm;
             L.rows = T.m;
         }
         return L;
     }
 
-    // Rows of a multiple of eight columns that start on 16 bytes: all eight of a piece are there, or none.
+    // Rows of a multiple of eight columns that start on 16 bytes: all eight of a piece are there, or none.  From L2:
+    // other blocks write these buffers while this kernel runs.
     __device__ __forceinline__ static void fetch(uint4 (&v)[4], const uint16_t* p, const Place& L, int64_t row0, int64_t col0, int lane)
     {
         const int64_t col = col0 + (lane & 3) * 8;
@@ -420,7 +492,7 @@ struct MuonWork {
         for (int i = 0; i < 4; ++i) {
             const int64_t row = row0 + i * 8 + (lane >> 2);
             v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < L.rows && col < L.cols) v[i] = *reinterpret_cast<const uint4*>(p + row * L.ld + col);
+            if (row < L.rows && col < L.cols) v[i] = __ldcg(reinterpret_cast<const uint4*>(p + row * L.ld + col));
         }
     }
     __device__ __forceinline__ static void stash(uint32_t stage, const uint4 (&v)[4], int lane)
@@ -447,37 +519,43 @@ struct MuonWork {
 
     __device__ __forceinline__ void fetch_adds(const Item& I, const Place& L, Ahead& A, int64_t row0, int c, int lane) const
     {
-        if (P.adds > 0) fetch(A.v[0], L.add[0], L, row0, (int64_t)I.n * BN + c, lane);
-        if (P.adds > 1) fetch(A.v[1], L.add[1], L, row0, (int64_t)I.n * BN + c, lane);
+        const int adds = I.op->adds;
+        if (adds > 0) fetch(A.v[0], L.add[0], L, row0, (int64_t)I.n * BN + c, lane);
+        if (adds > 1) fetch(A.v[1], L.add[1], L, row0, (int64_t)I.n * BN + c, lane);
     }
 
     __device__ __forceinline__ void prepare(const Item& I, int quad, int half, int rank, int lane, Ahead& A) const
     {
-        if (P.adds > 0) fetch_adds(I, place(I), A, ((int64_t)I.m * CG + rank) * kBM + quad * 32, half * kEpiCols, lane);
+        if (I.op->adds == 0) return;
+        // a wait that runs out here does so for the copies too, which say so
+        wait_before(I);
+        __syncwarp();
+        fetch_adds(I, place(I), A, ((int64_t)I.m * CG + rank) * kBM + quad * 32, half * kEpiCols, lane);
     }
 
     __device__ __forceinline__ void finish(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
         const Place L = place(I);
+        const Op& O = *I.op;
         const Matrix16 D{L.out, L.ld, L.rows, L.cols, 1};
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
         for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
             const int64_t col0 = (int64_t)I.n * BN + c;
             if (col0 >= D.cols || row0 >= D.rows) break;
-            if (P.adds > 0) stash(stage, A.v[0], lane);
-            if (P.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
+            if (O.adds > 0) stash(stage, A.v[0], lane);
+            if (O.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
             __syncwarp();
             if (c + 2 * kEpiCols < BN) fetch_adds(I, L, A, row0, c + 2 * kEpiCols, lane);
             float x[32];
             tmem_load32(acc + c, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] *= P.scale;
-            if (P.adds > 0) add_row(stage, P.lin[0], x, lane);
-            if (P.adds > 1) add_row(stage + kTile16Bytes, P.lin[1], x, lane);
+            for (int j = 0; j < 32; ++j) x[j] *= O.scale;
+            if (O.adds > 0) add_row(stage, O.lin[0], x, lane);
+            if (O.adds > 1) add_row(stage + kTile16Bytes, O.lin[1], x, lane);
             __syncwarp();
-            if constexpr (KIND == kNext) {
+            if (I.kind == kNext) {
                 put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
-                if (P.keep_low) {
+                if (O.keep_low) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
                     put_tile<ZERO_FP16>(stage + kTile16Bytes, lane, x, Matrix16{L.add[1], L.ld, L.rows, L.cols, 1}, row0, col0);
@@ -485,7 +563,7 @@ struct MuonWork {
             } else {
                 if (row0 == col0) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] += j == lane ? P.diag : 0.0f;
+                    for (int j = 0; j < 32; ++j) x[j] += j == lane ? O.diag : 0.0f;
                 }
                 put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
                 // the tile on the other side of the diagonal is this one's transpose
@@ -495,20 +573,21 @@ struct MuonWork {
     }
 };
 
-template <int CG, int BN, int KIND>
+// Blocks wait for one another: a cooperative launch.
+template <int CG, int BN>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) muon_product_kernel(const __grid_constant__ ProductParams P)
 {
     extern __shared__ unsigned char smem_raw[];
     Tiles<CG, BN> T;
     T.open(smem_raw);
     after_earlier_work();
-    T.run(MuonWork<CG, BN, KIND>{P, P.count}, &g_muon_error);
+    T.run(MuonWork<CG, BN>{P}, &g_muon_error);
 }
 
 // ------------------------------------------------------------------ the parameters
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) muon_apply_kernel(const __grid_constant__ MuonParams P)
+__global__ void __launch_bounds__(kThreads, 5) muon_apply_kernel(const __grid_constant__ MuonParams P)
 {
     after_earlier_work();
     bool skip = (*(const volatile uint32_t*)&P.st->flag) != 0;
@@ -517,46 +596,46 @@ __global__ void __launch_bounds__(kThreads) muon_apply_kernel(const __grid_const
         skip = (plan->flag | plan->error) != 0;
     }
     if (!skip) {
+        const float unit = 1.0f / P.sigma;      // a power of two
+        Piece next = P.count > 0 ? P.pieces[min((int)blockIdx.x, P.count - 1)] : Piece{0, 0};
         for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
-            const Piece piece = P.pieces[i];
+            const Piece piece = next;
+            next = P.pieces[min(i + (int)gridDim.x, P.count - 1)];
             const MuonTensor& T = P.tensors[piece.tensor];
+            const Eight E = eight_at(T, piece.at);
+            if (E.n == 0) continue;
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(T.x[P.src] + E.x));
+            float* const q = T.p ? T.p + E.e : nullptr;
+            uint16_t *const q16 = T.p16 ? T.p16 + E.e : nullptr, *const update = T.update ? T.update + E.e : nullptr;
+            const bool vec = T.vec_p;
             const float step = P.lr * (P.how == ZERO_MUON_SCALE_RMS ? T.rms : P.how == ZERO_MUON_SCALE_ASPECT ? T.aspect : 1.0f);
-            const float unit = 1.0f / P.sigma;      // a power of two
-            const uint16_t* x16 = T.x[P.src];
-            for_groups(T, piece.at, P.rounds, [&](int64_t e, int n, int64_t at) {
-                const uint4 w = *reinterpret_cast<const uint4*>(x16 + at);
-                float x[8];
-                widen2<ZERO_FP16>(w.x, x[0], x[1]);
-                widen2<ZERO_FP16>(w.y, x[2], x[3]);
-                widen2<ZERO_FP16>(w.z, x[4], x[5]);
-                widen2<ZERO_FP16>(w.w, x[6], x[7]);
+            float x[8], p[8];
+            if (q && vec) {
+                load_floats(q, p);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= unit;
-                if (T.update) store8<DT>(T.update + e, T.vec_p, n, x);
-                if (!T.p) return;
-                float p[8];
-                if (T.vec_p) {
-                    const float4* q = reinterpret_cast<const float4*>(T.p + e);
-                    const float4 a = q[0], b = q[1];
-                    p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
-                    p[4] = b.x; p[5] = b.y; p[6] = b.z; p[7] = b.w;
-                } else {
+                for (int j = 0; j < 8; ++j) p[j] = q && j < E.n ? q[j] : 0.0f;
+            }
+            widen2<ZERO_FP16>(w.x, x[0], x[1]);
+            widen2<ZERO_FP16>(w.y, x[2], x[3]);
+            widen2<ZERO_FP16>(w.z, x[4], x[5]);
+            widen2<ZERO_FP16>(w.w, x[6], x[7]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] = j < n ? T.p[e + j] : 0.0f;
-                }
+            for (int j = 0; j < 8; ++j) {
+                x[j] *= unit;
+                p[j] = fmaf(-step, x[j], fmaf(-P.decay, p[j], p[j]));
+            }
+            if (update) store8<DT>(update, vec, E.n, x);
+            if (!q) continue;
+            if (vec) {
+                reinterpret_cast<float4*>(q)[0] = make_float4(p[0], p[1], p[2], p[3]);
+                reinterpret_cast<float4*>(q)[1] = make_float4(p[4], p[5], p[6], p[7]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = fmaf(-step, x[j], fmaf(-P.decay, p[j], p[j]));
-                if (T.vec_p) {
-                    float4* q = reinterpret_cast<float4*>(T.p + e);
-                    q[0] = make_float4(p[0], p[1], p[2], p[3]);
-                    q[1] = make_float4(p[4], p[5], p[6], p[7]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < n) T.p[e + j] = p[j];
-                }
-                if (T.p16) store8<DT>(T.p16 + e, T.vec_p, n, p);
-            });
+                for (int j = 0; j < 8; ++j)
+                    if (j < E.n) q[j] = p[j];
+            }
+            if (q16) store8<DT>(q16, vec, E.n, p);
         }
     }
     // the last block to finish closes the step: every block has read the flag by then
@@ -588,13 +667,13 @@ struct zero_muon {
     int n_d = 0, dtype16 = 0;
     std::vector<int64_t> rows, cols;
     int64_t elems = 0, state_elems = 0;
-    // tiles of 128 or 256 for the symmetric products and for the others
-    int cg[2] = {1, 1};
+    int cg = 1;                  // tiles of 128 on a block, or of 256 on a pair
     bool pair = false;
-    int rounds = 1;              // of kChunk elements in a piece of the passes
-    std::vector<zero::Piece> chunks, groups, tiles[2];
+    std::vector<zero::Piece> chunks, groups, tiles;   // tiles: each worker's, in the order of the products
+    std::vector<int32_t> bounds;
+    int workers = 0;
     // the workspace's pieces
-    int64_t at_tensors = 0, at_grads = 0, at_chunks = 0, at_groups = 0, at_tiles[2] = {0, 0}, at_slots = 0, at_scale = 0, at_tickets = 0,
+    int64_t at_tensors = 0, at_grads = 0, at_chunks = 0, at_groups = 0, at_tiles = 0, at_bounds = 0, at_counters = 0, at_slots = 0, at_scale = 0, at_tickets = 0,
             at_data = 0, bytes = 0;
     // bound buffers (caller-owned)
     bool bound = false;
@@ -662,33 +741,80 @@ bool find_range(const zero_muon_hyper_t& hyper, bool pair, Range* r)
     return true;
 }
 
-// Tiles of every matrix for both kinds of product, longest inner dimension first, so that the last ones are short.
-void cut_tiles(zero_muon* h, int which, int cg, std::vector<Piece>* out, double* us)
+// The products of a step, in order: the first two iterations at once (a Gram matrix, five products of symmetric ones,
+// one with X), where the handle makes them so, and single ones (Gram, polynomial, X).
+constexpr int kPairPhases = 7;
+int phase_kind(bool pair, int phase)
 {
-    const int tile = 128 * cg;
-    std::vector<size_t> order(h->rows.size());
-    for (size_t i = 0; i < order.size(); ++i) order[i] = i;
-    auto inner = [&](size_t i) { return which == 0 ? std::max(h->rows[i], h->cols[i]) : std::min(h->rows[i], h->cols[i]); };
-    std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return inner(a) > inner(b); });
-    double work = 0.0, longest = 0.0;
-    const double block_us = cg == 2 ? 0.336 : 0.29;
-    for (const size_t i : order) {
-        const int64_t rows = h->rows[i], cols = h->cols[i], m = std::min(rows, cols);
-        if (m == 0) continue;
-        const int64_t tm = div_up(which == 0 ? m : rows, tile), tn = div_up(which == 0 ? m : cols, tile);
-        const double each = div_up(inner(i), kBK) * block_us;
-        longest = std::max(longest, each);
-        // groups of eight tile rows, column by column, so that what runs at one time shares its operands
-        for (int64_t g = 0; g < tm; g += 8)
-            for (int64_t n = 0; n < tn; ++n)
-                for (int64_t k = g; k < std::min(tm, g + 8); ++k) {
-                    if (which == 0 && k > n) continue;
-                    out->push_back(Piece{(int32_t)i, (int32_t)(k << 16 | n)});
-                    work += each;
-                }
+    if (pair && phase < kPairPhases) return phase == 0 ? kGram : phase == kPairPhases - 1 ? kNext : kSquare;
+    const int k = (pair ? phase - kPairPhases : phase) % 3;
+    return k == 0 ? kGram : k == 1 ? kSquare : kNext;
+}
+int phase_count(bool pair, int steps) { return pair ? kPairPhases + 3 * (steps - 2) : 3 * steps; }
+
+// Tiles along a side.
+int64_t tiles_of(int64_t side, int cg) { return div_up(side, 128 * cg); }
+
+// Every product's tiles dealt to the workers (blocks, or pairs), each to the one that is free first once the product
+// before is complete: as many whole steps as a call may ask for, since the list of fewer is its beginning.  The
+// estimated time of an inner block is zero_linear's; what a tile costs besides, and the wait for the product before, were
+// measured at sides of 256.  Returns the time that five steps take.
+double deal_tiles(const zero_muon* h, int cg, std::vector<Piece>* out, std::vector<int32_t>* bounds)
+{
+    const double block_us = cg == 2 ? 0.336 : 0.29, tile_us = 1.0, join_us = 3.0;
+    const size_t n = h->rows.size();
+    std::vector<size_t> order;                // longest inner dimension first
+    int64_t most = 0;
+    for (size_t i = 0; i < n; ++i) {
+        if (h->rows[i] * h->cols[i] == 0) continue;
+        order.push_back(i);
+        most += tiles_of(h->rows[i], cg) * tiles_of(h->cols[i], cg);
     }
-    const double slots = kGb300Sms / cg;
-    *us = std::max(longest, work / slots) + 0.5 * longest;
+    std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return std::max(h->rows[a], h->cols[a]) > std::max(h->rows[b], h->cols[b]); });
+    const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(kGb300Sms / cg, most));
+    std::vector<std::vector<Piece>> mine((size_t)workers);
+    using Free = std::pair<double, int>;
+    std::vector<Free> heap;
+    for (int w = 0; w < workers; ++w) heap.push_back(Free(0.0, w));
+    std::vector<double> complete(n, 0.0);
+    double at_five = 0.0, end = 0.0;
+    const int phases = phase_count(h->pair, ZERO_MUON_MAX_STEPS), five = phase_count(h->pair, 5);
+    for (int phase = 0; phase < phases; ++phase) {
+        const int kind = phase_kind(h->pair, phase);
+        for (const size_t i : order) {
+            const int64_t r = h->rows[i], c = h->cols[i], m = std::min(r, c), inner = kind == kGram ? std::max(r, c) : m;
+            const int64_t tm = tiles_of(kind == kNext ? r : m, cg), tn = tiles_of(kind == kNext ? c : m, cg);
+            const double each = div_up(inner, kBK) * block_us + tile_us;
+            double last = 0.0;
+            // groups of eight tile rows, column by column, so that what runs at one time shares its operands
+            for (int64_t g = 0; g < tm; g += 8)
+                for (int64_t b = 0; b < tn; ++b)
+                    for (int64_t a = g; a < std::min(tm, g + 8); ++a) {
+                        if (kind != kNext && a > b) continue;
+                        std::pop_heap(heap.begin(), heap.end(), std::greater<Free>());
+                        Free& f = heap.back();
+                        f.first = std::max(f.first, complete[i]) + each;
+                        last = std::max(last, f.first);
+                        mine[(size_t)f.second].push_back(Piece{(int32_t)((int64_t)i | (int64_t)phase << 16), (int32_t)(a << 16 | b)});
+                        std::push_heap(heap.begin(), heap.end(), std::greater<Free>());
+                    }
+            complete[i] = last + join_us;
+            end = std::max(end, complete[i]);
+        }
+        if (phase == five - 1) at_five = end;
+    }
+    out->clear();
+    bounds->assign((size_t)workers * kMaxPhases, 0);
+    for (int w = 0; w < workers; ++w) {
+        int32_t* b = bounds->data() + (size_t)w * kMaxPhases;
+        size_t k = 0;
+        for (int phase = 0; phase < kMaxPhases; ++phase) {
+            while (k < mine[(size_t)w].size() && (mine[(size_t)w][k].tensor >> 16) < phase) ++k;
+            b[phase] = (int32_t)(out->size() + k);
+        }
+        out->insert(out->end(), mine[(size_t)w].begin(), mine[(size_t)w].end());
+    }
+    return at_five;
 }
 
 zero_status_t check_hyper(const zero_muon* h, const zero_muon_hyper_t* hyper, Range* range, const char* who)
@@ -732,8 +858,9 @@ MuonParams params(const zero_muon* h, const zero_muon_hyper_t& hyper, double los
     P.slots = reinterpret_cast<double*>(ws + h->at_slots);
     P.scale = reinterpret_cast<float*>(ws + h->at_scale);
     P.tickets = reinterpret_cast<uint32_t*>(ws + h->at_tickets);
+    P.counters = reinterpret_cast<uint32_t*>(ws + h->at_counters);
+    P.n_counters = (int32_t)h->rows.size() * kMaxPhases;
     P.n_d = h->n_d;
-    P.rounds = h->rounds;
     P.nesterov = (hyper.flags & ZERO_MUON_NESTEROV) != 0;
     P.how = hyper.scale;
     P.inv = (float)(1.0 / ((double)h->n_d * loss_scale));
@@ -758,24 +885,24 @@ zero_status_t launch_reduce(const zero_muon* h, MuonParams P, cudaStream_t s)
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
 }
 
-template <int CG, int BN, int KIND>
-zero_status_t launch_product(const ProductParams& P, cudaStream_t s)
+template <int CG, int BN>
+zero_status_t launch_products(const zero_muon* h, const ProductParams& P, cudaStream_t s)
 {
     using S = GemmShape<CG, BN>;
-    const cudaError_t set = allow_shared<muon_product_kernel<CG, BN, KIND>>(S::kSmem);
+    const cudaError_t set = allow_shared<muon_product_kernel<CG, BN>>(S::kSmem);
     if (set != cudaSuccess) return cuda_fail(set, "zero_muon: shared memory");
-    const int grid = CG * (int)std::min<int64_t>(kGb300Sms / CG, P.count);
-    const cudaError_t e = launch_after(muon_product_kernel<CG, BN, KIND>, grid, kGemmThreads, S::kSmem, s, P);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CG * h->workers));
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, muon_product_kernel<CG, BN>, P);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
-}
-
-template <int KIND>
-zero_status_t launch_product(const zero_muon* h, ProductParams P, cudaStream_t s)
-{
-    constexpr int which = KIND == kNext;
-    P.tiles = reinterpret_cast<const Piece*>(static_cast<char*>(h->workspace) + h->at_tiles[which]);
-    P.count = (int32_t)h->tiles[which].size();
-    return h->cg[which] == 2 ? launch_product<2, 256, KIND>(P, s) : launch_product<1, 128, KIND>(P, s);
 }
 
 // The first X, the iterations and the parameters.
@@ -788,50 +915,58 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
     if (P.count > 0) {
         e = launch_after(muon_start_kernel, grid, kThreads, 0, s, P);
         if (e != cudaSuccess) return cuda_fail(e, "zero_muon: launch");
-        zero_status_t st = ZERO_OK;
+        char* ws = static_cast<char*>(h->workspace);
         ProductParams Q;
         std::memset(&Q, 0, sizeof(Q));
         Q.tensors = P.tensors;
+        Q.tiles = reinterpret_cast<const Piece*>(ws + h->at_tiles);
+        Q.bounds = reinterpret_cast<const int32_t*>(ws + h->at_bounds);
+        Q.counters = P.counters;
+        // one step alone of a handle that makes two at once is the first of the single ones
+        const bool pair = h->pair && hyper.steps >= 2;
+        Q.first = h->pair && !pair ? kPairPhases : 0;
+        Q.last = Q.first + phase_count(pair, hyper.steps);
+        int ops = 0, src = 0;
+        auto op = [&](int kind) -> Op& {
+            Op& o = Q.ops[ops++];
+            o.kind = kind;
+            o.src = src;
+            return o;
+        };
         // one symmetric product: out = f left right + l0 add0 + l1 add1 + d I, of values (their factors in fp16 are
         // range's)
         auto square = [&](Role left, Role right, Role out, double f, double d, std::initializer_list<std::pair<Role, double>> adds) {
-            if (st != ZERO_OK) return;
-            ProductParams S = Q;
-            S.left = kSlot[left];
-            S.right = kSlot[right];
-            S.out = kSlot[out];
-            S.scale = (float)(f * R.of(out) / (R.of(left) * R.of(right)));
-            S.diag = (float)(d * R.of(out));
+            Op& o = op(kSquare);
+            o.left = kSlot[left];
+            o.right = kSlot[right];
+            o.out = kSlot[out];
+            o.scale = (float)(f * R.of(out) / (R.of(left) * R.of(right)));
+            o.diag = (float)(d * R.of(out));
             for (const auto& a : adds) {
-                S.add[S.adds] = kSlot[a.first];
-                S.lin[S.adds++] = (float)(a.second * R.of(out) / R.of(a.first));
+                o.add[o.adds] = kSlot[a.first];
+                o.lin[o.adds++] = (float)(a.second * R.of(out) / R.of(a.first));
             }
-            st = launch_product<kSquare>(h, S, s);
         };
         auto gram = [&]() {
-            if (st != ZERO_OK) return;
-            ProductParams S = Q;
-            S.out = kSlot[kG];
-            S.scale = (float)(R.of(kG) / (R.sigma * R.sigma));
-            st = launch_product<kGram>(h, S, s);
+            Op& o = op(kGram);
+            o.out = kSlot[kG];
+            o.scale = (float)(R.of(kG) / (R.sigma * R.sigma));
         };
         // X <- poly X (+ d X where the polynomial is without d I, X with its low part)
         auto next = [&](Role poly, double d, bool keep_low) {
-            if (st != ZERO_OK) return;
-            ProductParams S = Q;
-            S.left = kSlot[poly];
-            S.scale = (float)(1.0 / R.of(poly));
+            Op& o = op(kNext);
+            o.left = kSlot[poly];
+            o.scale = (float)(1.0 / R.of(poly));
             if (d != 0.0) {
-                S.adds = 2;
-                S.lin[0] = (float)d;
-                S.lin[1] = (float)(d / kLow);
+                o.adds = 2;
+                o.lin[0] = (float)d;
+                o.lin[1] = (float)(d / kLow);
             }
-            S.keep_low = keep_low;
-            st = launch_product<kNext>(h, S, s);
-            Q.src ^= 1;
+            o.keep_low = keep_low;
+            src ^= 1;
         };
         int k = 0;
-        if (h->pair && hyper.steps >= 2) {
+        if (pair) {
             // Two iterations at once.  The second's G is (a I + R1) G (a I + R1), R1 = b G + c G^2, as polynomials of G
             // commute: products of the smaller side instead of two passes over X, and nothing rounds the X between.
             const double *c = hyper.coefficients[0], *e = hyper.coefficients[1];
@@ -844,15 +979,16 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
             next(kQ, c[0] * e[0], false);
             k = 2;
         }
-        for (; k < hyper.steps && st == ZERO_OK; ++k) {
+        for (; k < hyper.steps; ++k) {
             const double* c = hyper.coefficients[k];
-            const bool twice = !h->pair && k < kTwice;
+            const bool twice = !pair && k < kTwice;
             gram();
             square(kG, kG, kPoly, c[2], twice ? 0.0 : c[0], {{kG, c[1]}});
             next(kPoly, twice ? c[0] : 0.0, twice && k + 1 < kTwice && k + 1 < hyper.steps);
         }
+        const zero_status_t st = h->cg == 2 ? launch_products<2, 256>(h, Q, s) : launch_products<1, 128>(h, Q, s);
         if (st != ZERO_OK) return st;
-        P.src = Q.src;
+        P.src = src;
     }
     e = h->dtype16 == ZERO_BF16 ? launch_after(muon_apply_kernel<ZERO_BF16>, grid, kThreads, 0, s, P)
                                 : launch_after(muon_apply_kernel<ZERO_FP16>, grid, kThreads, 0, s, P);
@@ -899,31 +1035,32 @@ try {
         if (r > ZERO_MUON_MAX_SIZE || c > ZERO_MUON_MAX_SIZE || std::min(r, c) > ZERO_MUON_MAX_SIDE)
             return fail(ZERO_ERANGE, "zero_muon_create: a matrix beyond ZERO_MUON_MAX_SIZE, or its smaller side beyond ZERO_MUON_MAX_SIDE");
         h->elems += r * c;
-        if (h->elems > (int64_t)1 << 40) return fail(ZERO_ERANGE, "zero_muon_create: more than 2^40 elements");
+        if (h->elems > (int64_t)1 << 40) return fail(ZERO_ERANGE, "zero_muon_create: more than 2^40 elements");   // pieces stay 32-bit
         h->state_elems += up(r * c, kStateBlock);
     }
     h->rows.assign(rows, rows + n_matrices);
     h->cols.assign(cols, cols + n_matrices);
-    // four pieces a block of the passes, so that few wait for the last; at most 32768 elements, at least 2048
-    h->rounds = (int)std::min<int64_t>(16, std::max<int64_t>(1, h->elems / ((int64_t)4 * kPassBlocks * kGb300Sms * kChunk)));
-    const int64_t piece = (int64_t)h->rounds * kChunk;
     for (int64_t i = 0; i < n_matrices; ++i) {
         const int64_t r = rows[i], c = cols[i];
-        for (int64_t k = 0; k < div_up(r * c, piece); ++k) h->chunks.push_back(Piece{(int32_t)i, (int32_t)k});
-        for (int64_t k = 0; k < div_up(r * up(c, 8), piece); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
+        for (int64_t k = 0; k < div_up(r * c, kChunk); ++k) h->chunks.push_back(Piece{(int32_t)i, (int32_t)k});
+        for (int64_t k = 0; k < div_up(r * up(c, 8), kChunk); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
     }
     // Two iterations at once replace two passes over X by products of the smaller side, and are as exact from sides of
     // 64 on; for small sides the second G's largest values, differences of larger terms, are not.
     h->pair = h->elems > 0;
     for (int64_t i = 0; i < n_matrices; ++i)
         if (rows[i] * cols[i] > 0 && std::min(rows[i], cols[i]) < kPairSide) h->pair = false;
-    for (int which = 0; which < 2; ++which) {
-        std::vector<Piece> small, large;
-        double us1 = 0.0, us2 = 0.0;
-        cut_tiles(h.get(), which, 1, &small, &us1);
-        cut_tiles(h.get(), which, 2, &large, &us2);
-        h->cg[which] = us2 < us1 ? 2 : 1;
-        h->tiles[which] = us2 < us1 ? std::move(large) : std::move(small);
+    if (h->elems > 0) {
+        std::vector<Piece> tiles;
+        std::vector<int32_t> bounds;
+        const double us1 = deal_tiles(h.get(), 1, &h->tiles, &h->bounds), us2 = deal_tiles(h.get(), 2, &tiles, &bounds);
+        if (us2 < us1) {
+            h->cg = 2;
+            h->tiles.swap(tiles);
+            h->bounds.swap(bounds);
+        }
+        if (h->tiles.size() > (size_t)INT32_MAX) return fail(ZERO_ERANGE, "zero_muon_create: too many tiles");
+        h->workers = (int)(h->bounds.size() / kMaxPhases);
     }
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -935,7 +1072,9 @@ try {
     h->at_grads = take(8 * n_matrices * n_contribs);
     h->at_chunks = take(8 * (int64_t)h->chunks.size());
     h->at_groups = take(8 * (int64_t)h->groups.size());
-    for (int which = 0; which < 2; ++which) h->at_tiles[which] = take(8 * (int64_t)h->tiles[which].size());
+    h->at_tiles = take(8 * (int64_t)h->tiles.size());
+    h->at_bounds = take(4 * (int64_t)h->bounds.size());
+    h->at_counters = take(4 * n_matrices * kMaxPhases);
     h->at_slots = take(8 * (int64_t)h->chunks.size());
     h->at_scale = take(4 * n_matrices);
     h->at_tickets = take(4 * n_matrices);
@@ -1001,7 +1140,10 @@ try {
             T.ldm = (int32_t)up(m, 8);
             T.wide = r <= c;
             T.at = at;
-            T.chunks = (int32_t)div_up(r * c, (int64_t)h->rounds * kChunk);
+            const int64_t side = tiles_of(m, h->cg);
+            T.tiles[0] = (int32_t)(side * (side + 1) / 2);
+            T.tiles[1] = (int32_t)(tiles_of(r, h->cg) * tiles_of(c, h->cg));
+            T.chunks = (int32_t)div_up(r * c, kChunk);
             T.aspect = (float)std::sqrt(std::max(1.0, (double)r / (double)c));
             T.rms = (float)(0.2 * std::sqrt((double)std::max(r, c)));
             T.p = params ? params[i] : nullptr;
@@ -1044,7 +1186,8 @@ try {
     };
     put(h->at_chunks, h->chunks);
     put(h->at_groups, h->groups);
-    for (int which = 0; which < 2; ++which) put(h->at_tiles[which], h->tiles[which]);
+    put(h->at_tiles, h->tiles);
+    if (!h->bounds.empty()) std::memcpy(image.data() + h->at_bounds, h->bounds.data(), h->bounds.size() * sizeof(int32_t));
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "zero_muon_bind: cudaGetDevice");
