@@ -91,12 +91,12 @@ struct GatedWork {
         end = P.count;
         step = workers;
     }
-    __device__ __forceinline__ bool begin(const Item&) const { return true; }
+    static constexpr bool kScout = false;
     __device__ __forceinline__ void done(const Item&, int) const {}
     __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (P.a_rows + kBRows) * (kBK * 2); }
-    __device__ __forceinline__ bool a_mn(const Item&) const { return MODE == kWeights; }
-    __device__ __forceinline__ bool b_mn(const Item&) const { return P.b_mn; }
-    __device__ __forceinline__ uint32_t idesc(const Item&) const { return P.idesc; }
+    __device__ __forceinline__ bool a_mn(const Item&, int) const { return MODE == kWeights; }
+    __device__ __forceinline__ bool b_mn(const Item&, int) const { return P.b_mn; }
+    __device__ __forceinline__ uint32_t idesc(const Item&, int) const { return P.idesc; }
 
     __device__ __forceinline__ void load(const Item& I, int kb, uint32_t a, uint32_t b, uint32_t bar, int rank) const
     {

@@ -251,9 +251,10 @@ struct GemmShape {
 //   range(worker, workers, i, end, step)    the tiles of a block or pair
 //   Item item(int)                          where a tile is; Item::kb: its inner blocks, at least one
 //   uint32_t bytes(Item)                    what a stage's copies bring, to both blocks of a pair
-//   bool begin(Item)                        before its copies: what they wait for; false: given up
+//   kScout, bool begin(Item, Seen&)         true: a warp of its own finds the items and waits for what they wait for
+//                                           (false: given up), ahead of the others, which take them from a queue
 //   load(Item, kb, a, b, bar, rank)      those copies
-//   a_mn(Item), b_mn(Item), idesc(Item)     how the operands lie, and the product's descriptor
+//   a_mn(Item, kb), b_mn(Item, kb), idesc(Item, kb)   how a stage's operands lie, and the product's descriptor
 //   prepare(Item, quad, half, rank, lane, Ahead&)      what a tile's end may load before its products are done
 //   done(Item, lane)                                   by each of those warps once its part is stored
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
@@ -262,9 +263,12 @@ struct GemmShape {
 template <int CG, int BN>
 struct Tiles {
     using S = GemmShape<CG, BN>;
-    uint32_t base, epi0, full0, empty0, acc_full0, acc_empty0, tmem, rank;
+    uint32_t base, epi0, full0, empty0, acc_full0, acc_empty0, queue_full0, queue_empty0, queue0, tmem, rank;
     int warp, lane;
+    static constexpr int kQueue = 4, kItemBytes = 112;
+    static constexpr int kScoutSmem = S::kSmem + kQueue * (kItemBytes + 16);     // with the queue
 
+    template <bool SCOUT = false>
     __device__ __forceinline__ void open(unsigned char* smem_raw)
     {
         const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
@@ -275,6 +279,9 @@ struct Tiles {
         acc_full0 = empty0 + 8 * S::kStages;
         acc_empty0 = acc_full0 + 16;
         const uint32_t tmem_slot = acc_empty0 + 16;
+        queue0 = (full0 + 256 + 15) & ~15u;
+        queue_full0 = queue0 + kQueue * kItemBytes;
+        queue_empty0 = queue_full0 + 8 * kQueue;
         warp = threadIdx.x >> 5;
         lane = threadIdx.x & 31;
         rank = CG == 2 ? cluster_rank() : 0;
@@ -286,6 +293,12 @@ struct Tiles {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(acc_full0 + 8 * i, 1);
                 mbar_init(acc_empty0 + 8 * i, kEpiWarps * CG);
+            }
+            if constexpr (SCOUT) {
+                for (int i = 0; i < kQueue; ++i) {
+                    mbar_init(queue_full0 + 8 * i, 1);
+                    mbar_init(queue_empty0 + 8 * i, kEpiWarps + 1 + (rank == 0));
+                }
             }
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -305,6 +318,27 @@ struct Tiles {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
     }
 
+    // Item number `tile` of this block; every lane that `reads` it. One lane says that the warp has it.
+    template <class W>
+    __device__ __forceinline__ bool take(const W& work, int i, uint32_t tile, typename W::Item& I, bool whole_warp) const
+    {
+        if constexpr (W::kScout) {
+            const uint32_t slot = tile % kQueue, at = queue0 + slot * kItemBytes;
+            if (!mbar_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1, kGemmWaitNs)) return false;
+            uint32_t w[kItemBytes / 4];
+#pragma unroll
+            for (int j = 0; j < kItemBytes / 16; ++j)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4 * j]), "=r"(w[4 * j + 1]), "=r"(w[4 * j + 2]), "=r"(w[4 * j + 3]) : "r"(at + 16 * j) : "memory");
+            static_assert(sizeof(I) == kItemBytes, "an item's size");
+            memcpy(&I, w, sizeof(I));
+            if (whole_warp) __syncwarp();
+            if (!whole_warp || lane == 0) mbar_arrive(queue_empty0 + 8 * slot);
+        } else {
+            I = work.item(i);
+        }
+        return true;
+    }
+
     template <class W>
     __device__ __forceinline__ void run(const W& work, uint32_t* error)
     {
@@ -314,12 +348,12 @@ struct Tiles {
         if (warp == 0) {
             // ---- producer: one thread
             if (lane == 0) {
-                uint32_t k = 0;
-                for (int i = first; i < end && ok; i += step) {
-                    const typename W::Item I = work.item(i);
-                    const uint32_t bytes = work.bytes(I);
-                    ok = work.begin(I);
+                uint32_t k = 0, tile = 0;
+                for (int i = first; i < end && ok; i += step, ++tile) {
+                    typename W::Item I;
+                    ok = take(work, i, tile, I, false);
                     if (!ok) break;
+                    const uint32_t bytes = work.bytes(I);
                     for (int kb = 0; kb < I.kb; ++kb, ++k) {
                         const uint32_t s = k % S::kStages, use = k / S::kStages;
                         if (use > 0 && !mbar_wait(empty0 + 8 * s, (use - 1) & 1, kGemmWaitNs)) {
@@ -339,11 +373,10 @@ struct Tiles {
             if (lane == 0 && rank == 0) {
                 uint32_t k = 0, tile = 0;
                 for (int i = first; i < end && ok; i += step, ++tile) {
-                    const typename W::Item I = work.item(i);
-                    const bool a_mn = work.a_mn(I), b_mn = work.b_mn(I);
-                    const uint32_t idesc = work.idesc(I), acc = tile & 1, use = tile >> 1;
-                    // 16 inner elements: 32 bytes along K, two groups of eight K rows along MN
-                    const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+                    typename W::Item I;
+                    ok = take(work, i, tile, I, false);
+                    if (!ok) break;
+                    const uint32_t acc = tile & 1, use = tile >> 1;
                     if (use > 0 && !mbar_wait(acc_empty0 + 8 * acc, (use - 1) & 1, kGemmWaitNs)) {
                         ok = false;
                         break;
@@ -357,6 +390,10 @@ struct Tiles {
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const uint32_t a = base + s * S::kStageBytes;
+                        const bool a_mn = work.a_mn(I, kb), b_mn = work.b_mn(I, kb);
+                        const uint32_t idesc = work.idesc(I, kb);
+                        // 16 inner elements: 32 bytes along K, two groups of eight K rows along MN
+                        const uint64_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
                         const uint64_t da = smem_desc(a, a_mn), db = smem_desc(a + S::kABytes, b_mn);
 #pragma unroll
                         for (int j = 0; j < kBK / 16; ++j)
@@ -367,6 +404,30 @@ struct Tiles {
                     mma_commit<CG>(acc_full0 + 8 * acc);
                 }
             }
+        } else if (W::kScout && warp == 3) {
+            // ---- scout: one thread
+            if constexpr (W::kScout) {
+                if (lane == 0) {
+                    typename W::Seen seen = {};
+                    uint32_t tile = 0;
+                    for (int i = first; i < end && ok; i += step, ++tile) {
+                        const uint32_t slot = tile % kQueue, use = tile / kQueue, at = queue0 + slot * kItemBytes;
+                        const typename W::Item I = work.item(i);
+                        if (use > 0 && !mbar_wait(queue_empty0 + 8 * slot, (use - 1) & 1, kGemmWaitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        uint32_t w[kItemBytes / 4];
+                        memcpy(w, &I, sizeof(I));
+#pragma unroll
+                        for (int j = 0; j < kItemBytes / 16; ++j)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16 * j), "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3]) : "memory");
+                        ok = work.begin(I, seen);
+                        if (!ok) break;
+                        mbar_arrive(queue_full0 + 8 * slot);
+                    }
+                }
+            }
         } else if (warp >= 4) {
             // ---- epilogue: warp w reads TMEM lanes 32 (w % 4) on; the two warps of a lane group take alternate
             // columns
@@ -375,7 +436,10 @@ struct Tiles {
             const uint32_t acc_empty_leader = CG == 2 ? leader_address(acc_empty0) : acc_empty0;
             uint32_t tile = 0;
             for (int i = first; i < end && ok; i += step, ++tile) {
-                const typename W::Item I = work.item(i);
+                typename W::Item I;
+                ok = take(work, i, tile, I, true);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
                 const uint32_t acc = tile & 1, use = tile >> 1;
                 typename W::Ahead ahead;
                 work.prepare(I, quad, half, (int)rank, lane, ahead);
@@ -495,10 +559,9 @@ __device__ __forceinline__ void load_tile16(uint32_t stage, int lane, const Matr
     }
 }
 
-// x: row `lane` of a tile at (row0, col0), rounded once; turned through shared memory, so that a store instruction
-// writes whole sectors.
+// x: row `lane` of the tile in shared memory, rounded once.
 template <int DT>
-__device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
+__device__ __forceinline__ void write_tile16(uint32_t stage, int lane, const float (&x)[32])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -506,9 +569,41 @@ __device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (
                      "r"(narrow2<DT>(x[8 * i + 2], x[8 * i + 3])), "r"(narrow2<DT>(x[8 * i + 4], x[8 * i + 5])),
                      "r"(narrow2<DT>(x[8 * i + 6], x[8 * i + 7]))
                      : "memory");
+}
+
+// The same tile at (row0, col0) of a matrix, through shared memory, so that a store instruction writes whole sectors.
+template <int DT>
+__device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
+{
+    write_tile16<DT>(stage, lane, x);
     __syncwarp();
     store_tile16(stage, lane, D, row0, col0);
     __syncwarp();
+}
+
+// The tile in shared memory (tile16_at's exchange is the 64-byte swizzle; 512-byte aligned) to a tensor map's matrix,
+// by a copy that lane 0 starts and that belongs to its bulk group; what is past the matrix is left out.
+__device__ __forceinline__ void send_tile16(uint32_t stage, int lane, const CUtensorMap* map, int64_t row0, int64_t col0)
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(map), "r"((int)col0), "r"((int)row0), "r"(stage)
+            : "memory");
+}
+
+// Lane 0: until all but `LEFT` of its copies have read their tiles; and until all have written.
+template <int LEFT>
+__device__ __forceinline__ void sent_read(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+    __syncwarp();
+}
+__device__ __forceinline__ void sent_all(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // x += the tile that is there.
@@ -630,18 +725,25 @@ inline EncodeFn encode_fn()
     return fn;
 }
 
-inline zero_status_t encode(CUtensorMap* map, const Operand& o, int dtype16, int box_rows, const char* who)
+inline zero_status_t encode_box(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int dtype16, int box_rows, int box_cols,
+                                const char* who)
 {
     EncodeFn fn = encode_fn();
     if (!fn) return fail(ZERO_ECUDA, std::string(who) + ": the driver has no cuTensorMapEncodeTiled");
-    const cuuint64_t dims[2] = {(cuuint64_t)(o.mn ? o.rows : o.inner), (cuuint64_t)(o.mn ? o.inner : o.rows)};
-    const cuuint64_t strides[1] = {(cuuint64_t)o.ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)(o.mn ? kBK : box_rows)};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t unit[2] = {1, 1};
     const CUresult r = fn(map, dtype16 == ZERO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                          const_cast<void*>(o.p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          const_cast<void*>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ZERO_OK : fail(ZERO_ECUDA, std::string(who) + ": a tensor map was refused (" + std::to_string((int)r) + ")");
+}
+
+inline zero_status_t encode(CUtensorMap* map, const Operand& o, int dtype16, int box_rows, const char* who)
+{
+    return encode_box(map, o.p, o.mn ? o.inner : o.rows, o.mn ? o.rows : o.inner, o.ld, dtype16, o.mn ? kBK : box_rows, 64, who);
 }
 
 inline int grid_of(int64_t items, int sms, int per_sm) { return (int)std::max<int64_t>(1, std::min<int64_t>(div_up(items, 256), (int64_t)sms * per_sm)); }

@@ -6,9 +6,9 @@
 //   p <- p - lr wd p;  p <- p - lr s X
 //
 // A pass over the contributions forms m' and the norms, one over the momentum the first X; then each iteration is three
-// products on the tensor cores: G and the polynomial of it, of which the upper triangle's tiles are multiplied and
-// written twice, and the polynomial times X.  Nothing is transposed in memory: a tensor map takes X along its rows or
-// along its columns.  All products of all matrices are one cooperative launch: a matrix's next product begins when
+// products on the tensor cores: G and the polynomial of it, of which only the upper triangle's tiles are multiplied and
+// kept, and the polynomial times X.  Nothing is transposed in memory: a tensor map takes X, or a symmetric matrix's tile
+// in place of the one across the diagonal, along its rows or along its columns.  All products of all matrices are one cooperative launch: a matrix's next product begins when
 // the one before it is complete, whatever the other matrices do, so that no round of tiles has to be full.
 //
 // Operands are fp16 whatever the gradients' type, times powers of two that keep them in its range (the iterates' are
@@ -54,9 +54,14 @@ struct MuonState {
 };
 static_assert(sizeof(MuonState) <= 256, "MuonState fits its slot");
 
+// A matrix's tensor maps.  Along K and along the rows of operands: X's two buffers, the symmetric matrices; to write
+// tiles of 32 x 32: the same and X's low part.
+enum { kMapX = 0, kMapXAcross = 2, kMapSquare = 4, kMapSquareAcross = 4 + kSquares, kMapOutX = 4 + 2 * kSquares,
+       kMapOutLow = kMapOutX + 2, kMapOutSquare = kMapOutX + 3, kMaps = kMapOutSquare + kSquares };
+static_assert(kMaps <= 32, "a bit a map");
+
 struct alignas(128) MuonTensor {
-    CUtensorMap xk[2], xm[2];    // X's two buffers, taken along their rows and along their columns
-    CUtensorMap sq[kSquares];    // the symmetric matrices
+    CUtensorMap map[kMaps];
     uint16_t *x[2], *low;        // rows x ldx
     uint16_t* square[kSquares];  // m x ldm
     float* p;                    // NULL: no parameters
@@ -327,30 +332,25 @@ __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p)
     return v;
 }
 
-// row `lane` of a tile: x, written as its transpose at (col0, row0)
-__device__ __forceinline__ void put_tile_across(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
-{
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile16_at(stage, j, lane >> 3) + (lane & 7) * 2), "h"(narrow1<ZERO_FP16>(x[j])) : "memory");
-    __syncwarp();
-    store_tile16(stage, lane, D, col0, row0);
-    __syncwarp();
-}
-
 template <int CG, int BN>
 struct MuonWork {
     const ProductParams& P;
-    struct Item {
-        const MuonTensor* T;
+    struct alignas(16) Item {
         const Op* op;
         const uint32_t* before;  // the matrix's counter of the product before, or NULL
         uint32_t* counter;       // and of this one
-        const CUtensorMap *map_a, *map_b;
-        int m, n, kb, kind;
+        const CUtensorMap* maps; // the matrix's
+        const uint16_t* add[2];
+        int32_t ld, rows, cols;  // of the result and the addends
+        int32_t m, n, kb, kind, tensor;
         uint32_t want;           // of `before`
-        bool a_along, b_along;   // operands taken along their own rows
+        int8_t a, b, out;        // maps: operands along K, or along their own rows where `along` says so; the result
+        int8_t along;            // 1: a is, 2: b is
+        int8_t square;           // 1: a, 2: b is symmetric: tiles below the diagonal are taken from above it
+        int8_t reserved[3];
+        int32_t more[3];
     };
+    static constexpr bool kScout = true;
 
     __device__ __forceinline__ void range(int worker, int, int& i, int& end, int& step) const
     {
@@ -363,33 +363,49 @@ struct MuonWork {
     {
         const Piece t = P.tiles[i];
         const int tensor = t.tensor & 0xFFFF, phase = (t.tensor >> 16) - P.first;
+        const MuonTensor& T = P.tensors[tensor];
         Item I;
-        I.T = P.tensors + tensor;
         I.op = &P.ops[phase];
+        I.maps = T.map;
+        I.tensor = tensor;
         I.m = t.at >> 16;
         I.n = t.at & 0xFFFF;
         I.kind = I.op->kind;
         I.counter = P.counters + tensor * kMaxPhases + phase;
         I.before = phase > 0 ? I.counter - 1 : nullptr;
         I.want = 0;
-        if (phase > 0) I.want = (uint32_t)I.T->tiles[P.ops[phase - 1].kind == kNext] * (kEpiWarps * CG);
-        const MuonTensor& T = *I.T;
+        if (phase > 0) I.want = (uint32_t)T.tiles[P.ops[phase - 1].kind == kNext] * (kEpiWarps * CG);
         const Op& O = *I.op;
         const bool wide = T.wide;
         int inner = T.m;
+        if (I.kind == kNext) {
+            I.out = kMapOutX + (O.src ^ 1);
+            I.add[0] = T.x[O.src];
+            I.add[1] = T.low;
+            I.ld = I.cols = T.ldx;
+            I.rows = T.rows;
+        } else {
+            I.out = kMapOutSquare + O.out;
+            I.add[0] = T.square[O.add[0]];
+            I.add[1] = T.square[O.add[1]];
+            I.ld = I.cols = T.ldm;
+            I.rows = T.m;
+        }
         if (I.kind == kGram) {
-            I.map_a = I.map_b = wide ? &T.xk[O.src] : &T.xm[O.src];
-            I.a_along = I.b_along = !wide;
+            I.a = I.b = (wide ? kMapX : kMapXAcross) + O.src;
+            I.along = wide ? 0 : 3;
+            I.square = 0;
             inner = wide ? T.cols : T.rows;
         } else if (I.kind == kSquare) {
-            I.map_a = &T.sq[O.left];
-            I.map_b = &T.sq[O.right];
-            I.a_along = I.b_along = false;
+            I.a = kMapSquare + O.left;
+            I.b = kMapSquare + O.right;
+            I.along = 0;
+            I.square = 3;
         } else {
-            I.map_a = wide ? &T.sq[O.left] : &T.xk[O.src];
-            I.map_b = wide ? &T.xm[O.src] : &T.sq[O.left];
-            I.a_along = false;
-            I.b_along = wide;
+            I.a = wide ? kMapSquare + O.left : kMapX + O.src;
+            I.b = wide ? kMapXAcross + O.src : kMapSquare + O.left;
+            I.along = wide ? 2 : 0;
+            I.square = wide ? 1 : 2;
         }
         I.kb = (inner + kBK - 1) / kBK;
         return I;
@@ -400,8 +416,10 @@ struct MuonWork {
     {
         if (!I.before || load_acquire(I.before) >= I.want) return true;
         const uint64_t t0 = global_ns();
-        for (uint32_t i = 0; i < kWaitIterCap && global_ns() - t0 < kGemmWaitNs; ++i)
+        for (uint32_t i = 0; i < kWaitIterCap; ++i) {
             if (load_acquire(I.before) >= I.want) return true;
+            if (i % 16 == 15 && global_ns() - t0 > kGemmWaitNs) break;
+        }
         return false;
     }
 
@@ -410,29 +428,48 @@ struct MuonWork {
     {
         asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
     }
-    __device__ __forceinline__ bool begin(const Item& I) const
+    // What a block has waited for last, and the tensor maps that it has seen (a bit each, of the first matrices).
+    struct Seen {
+        static constexpr int kMatrices = 64;
+        const uint32_t* before;
+        uint32_t maps[kMatrices];
+    };
+    __device__ __forceinline__ bool begin(const Item& I, Seen& S) const
     {
-        see(I.map_a);
-        see(I.map_b);
-        if (!wait_before(I)) return false;
-        // what other blocks stored is read by copies from here on
-        asm volatile("fence.proxy.async;" ::: "memory");
+        uint32_t use = 1u << I.a | 1u << I.b | 1u << I.out;
+        if (I.square & 1) use |= 1u << (I.a + kSquares);
+        if (I.square & 2) use |= 1u << (I.b + kSquares);
+        if (I.op->keep_low) use |= 1u << kMapOutLow;
+        if (I.tensor < Seen::kMatrices) {
+            const uint32_t old = S.maps[I.tensor];
+            S.maps[I.tensor] = old | use;
+            use &= ~old;
+        }
+        for (; use; use &= use - 1) see(I.maps + (__ffs(use) - 1));
+        if (I.before != S.before) {
+            if (!wait_before(I)) return false;
+            // what other blocks' copies wrote is read by copies from here on
+            asm volatile("fence.proxy.async;" ::: "memory");
+            S.before = I.before;
+        }
         return true;
     }
-    // Each lane's stores, then the warp's one release of them all.
+    // Lane 0 has sent the warp's tiles: once they are written, one release of them all.
     __device__ __forceinline__ void done(const Item& I, int lane) const
     {
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
+        sent_all(lane);
+        if (lane == 0) asm volatile("fence.proxy.async;\n\tfence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
     }
 
+    // Is an inner block of a symmetric operand's tile row below the diagonal?
+    __device__ __forceinline__ static bool below(int row_tile, int kb) { return kb / (kBM * CG / kBK) < row_tile; }
+
     __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (kBM + BN / CG) * (kBK * 2); }
-    __device__ __forceinline__ bool a_mn(const Item& I) const { return I.a_along; }
-    __device__ __forceinline__ bool b_mn(const Item& I) const { return I.b_along; }
-    __device__ __forceinline__ uint32_t idesc(const Item& I) const
+    __device__ __forceinline__ bool a_mn(const Item& I, int kb) const { return (I.along & 1) || ((I.square & 1) && below(I.m, kb)); }
+    __device__ __forceinline__ bool b_mn(const Item& I, int kb) const { return (I.along & 2) || ((I.square & 2) && below(I.n, kb)); }
+    __device__ __forceinline__ uint32_t idesc(const Item& I, int kb) const
     {
-        return (1u << 4) | ((I.a_along ? 1u : 0u) << 15) | ((I.b_along ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((kBM * CG) >> 4) << 24);
+        return (1u << 4) | ((a_mn(I, kb) ? 1u : 0u) << 15) | ((b_mn(I, kb) ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((kBM * CG) >> 4) << 24);
     }
 
     // 128 rows of an operand: along K in one box, along its own rows in two
@@ -448,8 +485,10 @@ struct MuonWork {
 
     __device__ __forceinline__ void load(const Item& I, int kb, uint32_t a, uint32_t b, uint32_t bar, int rank) const
     {
-        bring(I.map_a, I.a_along, a, (I.m * CG + rank) * kBM, kb * kBK, bar);
-        bring(I.map_b, I.b_along, b, I.n * BN + rank * (BN / CG), kb * kBK, bar);
+        const bool a_mn_ = a_mn(I, kb), b_mn_ = b_mn(I, kb);
+        const int map_a = I.a + ((I.square & 1) && a_mn_ ? kSquares : 0), map_b = I.b + ((I.square & 2) && b_mn_ ? kSquares : 0);
+        bring(I.maps + map_a, a_mn_, a, (I.m * CG + rank) * kBM, kb * kBK, bar);
+        bring(I.maps + map_b, b_mn_, b, I.n * BN + rank * (BN / CG), kb * kBK, bar);
     }
 
     // ---- a tile's end.  The addends of a 32 x 32 part are loaded while the one before it is finished, the first
@@ -457,35 +496,9 @@ struct MuonWork {
     struct Ahead {
         uint4 v[2][4];
     };
-    struct Place {
-        uint16_t *out, *add[2];
-        int32_t ld, rows, cols;
-    };
-
-    __device__ __forceinline__ Place place(const Item& I) const
-    {
-        const MuonTensor& T = *I.T;
-        const Op& O = *I.op;
-        Place L;
-        if (I.kind == kNext) {
-            L.out = T.x[O.src ^ 1];
-            L.add[0] = T.x[O.src];
-            L.add[1] = T.low;
-            L.ld = L.cols = T.ldx;
-            L.rows = T.rows;
-        } else {
-            L.out = T.square[O.out];
-            L.add[0] = T.square[O.add[0]];
-            L.add[1] = T.square[O.add[1]];
-            L.ld = L.cols = T.ldm;
-            L.rows = T.m;
-        }
-        return L;
-    }
-
     // Rows of a multiple of eight columns that start on 16 bytes: all eight of a piece are there, or none.  From L2:
     // other blocks write these buffers while this kernel runs.
-    __device__ __forceinline__ static void fetch(uint4 (&v)[4], const uint16_t* p, const Place& L, int64_t row0, int64_t col0, int lane)
+    __device__ __forceinline__ static void fetch(uint4 (&v)[4], const uint16_t* p, const Item& L, int64_t row0, int64_t col0, int lane)
     {
         const int64_t col = col0 + (lane & 3) * 8;
 #pragma unroll
@@ -517,57 +530,58 @@ struct MuonWork {
         }
     }
 
-    __device__ __forceinline__ void fetch_adds(const Item& I, const Place& L, Ahead& A, int64_t row0, int c, int lane) const
+    __device__ __forceinline__ void fetch_adds(const Item& I, Ahead& A, int64_t row0, int c, int lane) const
     {
         const int adds = I.op->adds;
-        if (adds > 0) fetch(A.v[0], L.add[0], L, row0, (int64_t)I.n * BN + c, lane);
-        if (adds > 1) fetch(A.v[1], L.add[1], L, row0, (int64_t)I.n * BN + c, lane);
+        if (adds > 0) fetch(A.v[0], I.add[0], I, row0, (int64_t)I.n * BN + c, lane);
+        if (adds > 1) fetch(A.v[1], I.add[1], I, row0, (int64_t)I.n * BN + c, lane);
     }
 
     __device__ __forceinline__ void prepare(const Item& I, int quad, int half, int rank, int lane, Ahead& A) const
     {
-        if (I.op->adds == 0) return;
-        // a wait that runs out here does so for the copies too, which say so
-        wait_before(I);
-        __syncwarp();
-        fetch_adds(I, place(I), A, ((int64_t)I.m * CG + rank) * kBM + quad * 32, half * kEpiCols, lane);
+        fetch_adds(I, A, ((int64_t)I.m * CG + rank) * kBM + quad * 32, half * kEpiCols, lane);
     }
 
     __device__ __forceinline__ void finish(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
-        const Place L = place(I);
         const Op& O = *I.op;
-        const Matrix16 D{L.out, L.ld, L.rows, L.cols, 1};
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
-        for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
+        uint32_t turn = 0;
+        for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols, turn ^= kTile16Bytes) {
             const int64_t col0 = (int64_t)I.n * BN + c;
-            if (col0 >= D.cols || row0 >= D.rows) break;
-            if (O.adds > 0) stash(stage, A.v[0], lane);
-            if (O.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
-            __syncwarp();
-            if (c + 2 * kEpiCols < BN) fetch_adds(I, L, A, row0, c + 2 * kEpiCols, lane);
+            if (col0 >= I.cols || row0 >= I.rows) break;
             float x[32];
             tmem_load32(acc + c, x);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] *= O.scale;
-            if (O.adds > 0) add_row(stage, O.lin[0], x, lane);
-            if (O.adds > 1) add_row(stage + kTile16Bytes, O.lin[1], x, lane);
-            __syncwarp();
-            if (I.kind == kNext) {
-                put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
-                if (O.keep_low) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
-                    put_tile<ZERO_FP16>(stage + kTile16Bytes, lane, x, Matrix16{L.add[1], L.ld, L.rows, L.cols, 1}, row0, col0);
-                }
+            // the tile that is sent: the two of the warp's in turn, where no addend and no low part needs one
+            uint32_t at = stage;
+            if (O.adds > 0) {
+                sent_read<0>(lane);
+                stash(stage, A.v[0], lane);
+                if (O.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
+                __syncwarp();
+                if (c + 2 * kEpiCols < BN) fetch_adds(I, A, row0, c + 2 * kEpiCols, lane);
+                add_row(stage, O.lin[0], x, lane);
+                if (O.adds > 1) add_row(stage + kTile16Bytes, O.lin[1], x, lane);
+                __syncwarp();
+            } else if (O.keep_low) {
+                sent_read<0>(lane);
             } else {
-                if (row0 == col0) {
+                sent_read<1>(lane);
+                at = stage + turn;
+            }
+            if (I.kind != kNext && row0 == col0) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] += j == lane ? O.diag : 0.0f;
-                }
-                put_tile<ZERO_FP16>(stage, lane, x, D, row0, col0);
-                // the tile on the other side of the diagonal is this one's transpose
-                if (I.m != I.n) put_tile_across(stage + kTile16Bytes, lane, x, D, row0, col0);
+                for (int j = 0; j < 32; ++j) x[j] += j == lane ? O.diag : 0.0f;
+            }
+            write_tile16<ZERO_FP16>(at, lane, x);
+            send_tile16(at, lane, I.maps + I.out, row0, col0);
+            if (O.keep_low) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
+                write_tile16<ZERO_FP16>(stage + kTile16Bytes, lane, x);
+                send_tile16(stage + kTile16Bytes, lane, I.maps + kMapOutLow, row0, col0);
             }
         }
     }
@@ -579,7 +593,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) mu
 {
     extern __shared__ unsigned char smem_raw[];
     Tiles<CG, BN> T;
-    T.open(smem_raw);
+    T.template open<true>(smem_raw);
     after_earlier_work();
     T.run(MuonWork<CG, BN>{P}, &g_muon_error);
 }
@@ -888,13 +902,13 @@ zero_status_t launch_reduce(const zero_muon* h, MuonParams P, cudaStream_t s)
 template <int CG, int BN>
 zero_status_t launch_products(const zero_muon* h, const ProductParams& P, cudaStream_t s)
 {
-    using S = GemmShape<CG, BN>;
-    const cudaError_t set = allow_shared<muon_product_kernel<CG, BN>>(S::kSmem);
+    constexpr int kShared = Tiles<CG, BN>::kScoutSmem;
+    const cudaError_t set = allow_shared<muon_product_kernel<CG, BN>>(kShared);
     if (set != cudaSuccess) return cuda_fail(set, "zero_muon: shared memory");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(CG * h->workers));
     cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = kShared;
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeCooperative;
@@ -1170,12 +1184,23 @@ try {
             for (int k = 0; k < kSquares; ++k) T.square[k] = q + 3 * x + k * g;
             data += 2 * (3 * x + kSquares * g);
             zero_status_t st = ZERO_OK;
-            for (int k = 0; k < 2 && st == ZERO_OK; ++k) {
-                st = encode(&T.xk[k], Operand{T.x[k], r, c, T.ldx, false}, ZERO_FP16, kBM, "zero_muon_bind");
-                if (st == ZERO_OK) st = encode(&T.xm[k], Operand{T.x[k], c, r, T.ldx, true}, ZERO_FP16, kBM, "zero_muon_bind");
+            auto map = [&](int which, const Operand& o) {
+                if (st == ZERO_OK) st = encode(&T.map[which], o, ZERO_FP16, kBM, "zero_muon_bind");
+            };
+            auto out = [&](int which, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+                if (st == ZERO_OK) st = encode_box(&T.map[which], p, rows, cols, ld, ZERO_FP16, 32, 32, "zero_muon_bind");
+            };
+            for (int k = 0; k < 2; ++k) {
+                map(kMapX + k, Operand{T.x[k], r, c, T.ldx, false});
+                map(kMapXAcross + k, Operand{T.x[k], c, r, T.ldx, true});
+                out(kMapOutX + k, T.x[k], r, c, T.ldx);
             }
-            for (int k = 0; k < kSquares && st == ZERO_OK; ++k)
-                st = encode(&T.sq[k], Operand{T.square[k], m, m, T.ldm, false}, ZERO_FP16, kBM, "zero_muon_bind");
+            out(kMapOutLow, T.low, r, c, T.ldx);
+            for (int k = 0; k < kSquares; ++k) {
+                map(kMapSquare + k, Operand{T.square[k], m, m, T.ldm, false});
+                map(kMapSquareAcross + k, Operand{T.square[k], m, m, T.ldm, true});
+                out(kMapOutSquare + k, T.square[k], m, m, T.ldm);
+            }
             if (st != ZERO_OK) return st;
             at += up(r * c, kStateBlock);
         }
