@@ -260,6 +260,14 @@ struct GemmShape {
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
+// mbar_wait with the clock read rarely: reading it twice before the first try costs more than most waits here take.
+__device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity)
+{
+    for (int i = 0; i < 8; ++i)
+        if (mbar_try(bar, parity)) return true;
+    return mbar_wait(bar, parity, kGemmWaitNs);
+}
+
 template <int CG, int BN>
 struct Tiles {
     using S = GemmShape<CG, BN>;
@@ -324,7 +332,7 @@ struct Tiles {
     {
         if constexpr (W::kScout) {
             const uint32_t slot = tile % kQueue, at = queue0 + slot * kItemBytes;
-            if (!mbar_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1, kGemmWaitNs)) return false;
+            if (!stage_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1)) return false;
             uint32_t w[kItemBytes / 4];
 #pragma unroll
             for (int j = 0; j < kItemBytes / 16; ++j)
@@ -356,7 +364,7 @@ struct Tiles {
                     const uint32_t bytes = work.bytes(I);
                     for (int kb = 0; kb < I.kb; ++kb, ++k) {
                         const uint32_t s = k % S::kStages, use = k / S::kStages;
-                        if (use > 0 && !mbar_wait(empty0 + 8 * s, (use - 1) & 1, kGemmWaitNs)) {
+                        if (use > 0 && !stage_wait(empty0 + 8 * s, (use - 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -377,14 +385,14 @@ struct Tiles {
                     ok = take(work, i, tile, I, false);
                     if (!ok) break;
                     const uint32_t acc = tile & 1, use = tile >> 1;
-                    if (use > 0 && !mbar_wait(acc_empty0 + 8 * acc, (use - 1) & 1, kGemmWaitNs)) {
+                    if (use > 0 && !stage_wait(acc_empty0 + 8 * acc, (use - 1) & 1)) {
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     for (int kb = 0; kb < I.kb; ++kb, ++k) {
                         const uint32_t s = k % S::kStages;
-                        if (!mbar_wait(full0 + 8 * s, (k / S::kStages) & 1, kGemmWaitNs)) {
+                        if (!stage_wait(full0 + 8 * s, (k / S::kStages) & 1)) {
                             ok = false;
                             break;
                         }
@@ -413,7 +421,7 @@ struct Tiles {
                     for (int i = first; i < end && ok; i += step, ++tile) {
                         const uint32_t slot = tile % kQueue, use = tile / kQueue, at = queue0 + slot * kItemBytes;
                         const typename W::Item I = work.item(i);
-                        if (use > 0 && !mbar_wait(queue_empty0 + 8 * slot, (use - 1) & 1, kGemmWaitNs)) {
+                        if (use > 0 && !stage_wait(queue_empty0 + 8 * slot, (use - 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -443,7 +451,7 @@ struct Tiles {
                 const uint32_t acc = tile & 1, use = tile >> 1;
                 typename W::Ahead ahead;
                 work.prepare(I, quad, half, (int)rank, lane, ahead);
-                ok = mbar_wait(acc_full0 + 8 * acc, use & 1, kGemmWaitNs);
+                ok = stage_wait(acc_full0 + 8 * acc, use & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -303,6 +303,9 @@ __global__ void __launch_bounds__(kThreads, 6) muon_start_kernel(const __grid_co
 
 // ------------------------------------------------------------------ the products
 
+// Rows of a box of an operand taken along K.
+constexpr int box_rows(int bn) { return bn == 64 ? 64 : 128; }
+
 // X X^T (or X^T X); a product of two symmetric matrices that commute, so that it is one too; one times X.
 enum { kGram = 0, kSquare = 1, kNext = 2 };
 
@@ -458,28 +461,31 @@ struct MuonWork {
     __device__ __forceinline__ void done(const Item& I, int lane) const
     {
         sent_all(lane);
-        if (lane == 0) asm volatile("fence.proxy.async;\n\tfence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
+        if (lane == 0) asm volatile("fence.proxy.async;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
     }
 
-    // Is an inner block of a symmetric operand's tile row below the diagonal?
-    __device__ __forceinline__ static bool below(int row_tile, int kb) { return kb / (kBM * CG / kBK) < row_tile; }
+    // Is an inner block below the diagonal block (kBM * CG wide) of a symmetric operand's rows from `row` on?
+    __device__ __forceinline__ static bool below(int row, int kb) { return kb / (kBM * CG / kBK) < row / (kBM * CG); }
 
     __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (kBM + BN / CG) * (kBK * 2); }
-    __device__ __forceinline__ bool a_mn(const Item& I, int kb) const { return (I.along & 1) || ((I.square & 1) && below(I.m, kb)); }
-    __device__ __forceinline__ bool b_mn(const Item& I, int kb) const { return (I.along & 2) || ((I.square & 2) && below(I.n, kb)); }
+    __device__ __forceinline__ bool a_mn(const Item& I, int kb) const { return (I.along & 1) || ((I.square & 1) && below(I.m * (kBM * CG), kb)); }
+    __device__ __forceinline__ bool b_mn(const Item& I, int kb) const { return (I.along & 2) || ((I.square & 2) && below(I.n * BN, kb)); }
     __device__ __forceinline__ uint32_t idesc(const Item& I, int kb) const
     {
         return (1u << 4) | ((a_mn(I, kb) ? 1u : 0u) << 15) | ((b_mn(I, kb) ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((kBM * CG) >> 4) << 24);
     }
 
-    // 128 rows of an operand: along K in one box, along its own rows in two
+    // ROWS rows of an operand: along K in boxes of kBox rows, along its own rows in boxes of 64
+    static constexpr int kBox = box_rows(BN);
+    template <int ROWS>
     __device__ __forceinline__ static void bring(const CUtensorMap* map, bool mn, uint32_t at, int row, int k, uint32_t bar)
     {
         if (mn) {
-            tma_load_2d<CG>(at, map, row, k, bar);
-            tma_load_2d<CG>(at + kBK * 128, map, row + 64, k, bar);
+#pragma unroll
+            for (int i = 0; i < ROWS / 64; ++i) tma_load_2d<CG>(at + i * (kBK * 128), map, row + 64 * i, k, bar);
         } else {
-            tma_load_2d<CG>(at, map, k, row, bar);
+#pragma unroll
+            for (int i = 0; i < ROWS / kBox; ++i) tma_load_2d<CG>(at + i * (kBox * kBK * 2), map, k, row + kBox * i, bar);
         }
     }
 
@@ -487,8 +493,8 @@ struct MuonWork {
     {
         const bool a_mn_ = a_mn(I, kb), b_mn_ = b_mn(I, kb);
         const int map_a = I.a + ((I.square & 1) && a_mn_ ? kSquares : 0), map_b = I.b + ((I.square & 2) && b_mn_ ? kSquares : 0);
-        bring(I.maps + map_a, a_mn_, a, (I.m * CG + rank) * kBM, kb * kBK, bar);
-        bring(I.maps + map_b, b_mn_, b, I.n * BN + rank * (BN / CG), kb * kBK, bar);
+        bring<kBM>(I.maps + map_a, a_mn_, a, (I.m * CG + rank) * kBM, kb * kBK, bar);
+        bring<BN / CG>(I.maps + map_b, b_mn_, b, I.n * BN + rank * (BN / CG), kb * kBK, bar);
     }
 
     // ---- a tile's end.  The addends of a 32 x 32 part are loaded while the one before it is finished, the first
@@ -554,22 +560,19 @@ struct MuonWork {
             tmem_load32(acc + c, x);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] *= O.scale;
-            // the tile that is sent: the two of the warp's in turn, where no addend and no low part needs one
-            uint32_t at = stage;
+            // The tile that is sent: the warp's two in turn, unless there is a second addend or a low part for the
+            // other.  A lane's row of it is where its row of the addend was.
+            const bool both = O.adds > 1 || O.keep_low;
+            const uint32_t at = both ? stage : stage + turn;
+            if (both) sent_read<0>(lane);
+            else sent_read<1>(lane);
             if (O.adds > 0) {
-                sent_read<0>(lane);
-                stash(stage, A.v[0], lane);
+                stash(at, A.v[0], lane);
                 if (O.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
                 __syncwarp();
                 if (c + 2 * kEpiCols < BN) fetch_adds(I, A, row0, c + 2 * kEpiCols, lane);
-                add_row(stage, O.lin[0], x, lane);
+                add_row(at, O.lin[0], x, lane);
                 if (O.adds > 1) add_row(stage + kTile16Bytes, O.lin[1], x, lane);
-                __syncwarp();
-            } else if (O.keep_low) {
-                sent_read<0>(lane);
-            } else {
-                sent_read<1>(lane);
-                at = stage + turn;
             }
             if (I.kind != kNext && row0 == col0) {
 #pragma unroll
@@ -681,7 +684,7 @@ struct zero_muon {
     int n_d = 0, dtype16 = 0;
     std::vector<int64_t> rows, cols;
     int64_t elems = 0, state_elems = 0;
-    int cg = 1;                  // tiles of 128 on a block, or of 256 on a pair
+    int cg = 1, bn = 128;        // tiles of 128 x 64 or 128 x 128 on a block, or of 256 x 256 on a pair
     bool pair = false;
     std::vector<zero::Piece> chunks, groups, tiles;   // tiles: each worker's, in the order of the products
     std::vector<int32_t> bounds;
@@ -766,23 +769,39 @@ int phase_kind(bool pair, int phase)
 }
 int phase_count(bool pair, int steps) { return pair ? kPairPhases + 3 * (steps - 2) : 3 * steps; }
 
-// Tiles along a side.
-int64_t tiles_of(int64_t side, int cg) { return div_up(side, 128 * cg); }
+// How tiles are cut: what a pair or block takes, and the estimated time of an inner block of it: zero_linear's.
+struct Shape {
+    int cg, bn;
+    double block_us;
+};
+constexpr Shape kShapes[] = {{2, 256, 0.336}, {1, 128, 0.29}, {1, 64, 0.20}};
+
+// Of a symmetric product: the tiles with anything on or above the diagonal, in whole diagonal blocks.
+bool kept(const Shape& S, int64_t a, int64_t b) { return b * S.bn >= a * 128 * S.cg; }
+int64_t tile_rows(const Shape& S, int64_t rows) { return div_up(rows, 128 * S.cg); }
+int64_t tile_cols(const Shape& S, int64_t cols) { return div_up(cols, S.bn); }
+int64_t square_tiles(const Shape& S, int64_t m)
+{
+    int64_t n = 0;
+    for (int64_t a = 0; a < tile_rows(S, m); ++a) n += tile_cols(S, m) - a * 128 * S.cg / S.bn;
+    return n;
+}
 
 // Every product's tiles dealt to the workers (blocks, or pairs), each to the one that is free first once the product
-// before is complete: as many whole steps as a call may ask for, since the list of fewer is its beginning.  The
-// estimated time of an inner block is zero_linear's; what a tile costs besides, and the wait for the product before, were
-// measured at sides of 256.  Returns the time that five steps take.
-double deal_tiles(const zero_muon* h, int cg, std::vector<Piece>* out, std::vector<int32_t>* bounds)
+// before is complete: as many whole steps as a call may ask for, since the list of fewer is its beginning.  What a tile
+// costs besides its inner blocks, and the way from a product's end to the next one's first block, were measured at
+// sides of 256.  Returns the time that five steps take.
+double deal_tiles(const zero_muon* h, const Shape& S, std::vector<Piece>* out, std::vector<int32_t>* bounds)
 {
-    const double block_us = cg == 2 ? 0.336 : 0.29, tile_us = 1.0, join_us = 3.0;
+    const double tile_us = 0.6, join_us = 4.0;
+    const int cg = S.cg;
     const size_t n = h->rows.size();
     std::vector<size_t> order;                // longest inner dimension first
     int64_t most = 0;
     for (size_t i = 0; i < n; ++i) {
         if (h->rows[i] * h->cols[i] == 0) continue;
         order.push_back(i);
-        most += tiles_of(h->rows[i], cg) * tiles_of(h->cols[i], cg);
+        most += tile_rows(S, h->rows[i]) * tile_cols(S, h->cols[i]);
     }
     std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return std::max(h->rows[a], h->cols[a]) > std::max(h->rows[b], h->cols[b]); });
     const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(kGb300Sms / cg, most));
@@ -797,14 +816,14 @@ double deal_tiles(const zero_muon* h, int cg, std::vector<Piece>* out, std::vect
         const int kind = phase_kind(h->pair, phase);
         for (const size_t i : order) {
             const int64_t r = h->rows[i], c = h->cols[i], m = std::min(r, c), inner = kind == kGram ? std::max(r, c) : m;
-            const int64_t tm = tiles_of(kind == kNext ? r : m, cg), tn = tiles_of(kind == kNext ? c : m, cg);
-            const double each = div_up(inner, kBK) * block_us + tile_us;
+            const int64_t tm = tile_rows(S, kind == kNext ? r : m), tn = tile_cols(S, kind == kNext ? c : m);
+            const double each = div_up(inner, kBK) * S.block_us + tile_us;
             double last = 0.0;
             // groups of eight tile rows, column by column, so that what runs at one time shares its operands
             for (int64_t g = 0; g < tm; g += 8)
                 for (int64_t b = 0; b < tn; ++b)
                     for (int64_t a = g; a < std::min(tm, g + 8); ++a) {
-                        if (kind != kNext && a > b) continue;
+                        if (kind != kNext && !kept(S, a, b)) continue;
                         std::pop_heap(heap.begin(), heap.end(), std::greater<Free>());
                         Free& f = heap.back();
                         f.first = std::max(f.first, complete[i]) + each;
@@ -1000,7 +1019,7 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
             square(kG, kG, kPoly, c[2], twice ? 0.0 : c[0], {{kG, c[1]}});
             next(kPoly, twice ? c[0] : 0.0, twice && k + 1 < kTwice && k + 1 < hyper.steps);
         }
-        const zero_status_t st = h->cg == 2 ? launch_products<2, 256>(h, Q, s) : launch_products<1, 128>(h, Q, s);
+        const zero_status_t st = h->cg == 2 ? launch_products<2, 256>(h, Q, s) : h->bn == 128 ? launch_products<1, 128>(h, Q, s) : launch_products<1, 64>(h, Q, s);
         if (st != ZERO_OK) return st;
         P.src = src;
     }
@@ -1065,11 +1084,15 @@ try {
     for (int64_t i = 0; i < n_matrices; ++i)
         if (rows[i] * cols[i] > 0 && std::min(rows[i], cols[i]) < kPairSide) h->pair = false;
     if (h->elems > 0) {
-        std::vector<Piece> tiles;
-        std::vector<int32_t> bounds;
-        const double us1 = deal_tiles(h.get(), 1, &h->tiles, &h->bounds), us2 = deal_tiles(h.get(), 2, &tiles, &bounds);
-        if (us2 < us1) {
-            h->cg = 2;
+        double best = 1e30;
+        for (const Shape& S : kShapes) {
+            std::vector<Piece> tiles;
+            std::vector<int32_t> bounds;
+            const double us = deal_tiles(h.get(), S, &tiles, &bounds);
+            if (us >= best) continue;
+            best = us;
+            h->cg = S.cg;
+            h->bn = S.bn;
             h->tiles.swap(tiles);
             h->bounds.swap(bounds);
         }
@@ -1154,9 +1177,9 @@ try {
             T.ldm = (int32_t)up(m, 8);
             T.wide = r <= c;
             T.at = at;
-            const int64_t side = tiles_of(m, h->cg);
-            T.tiles[0] = (int32_t)(side * (side + 1) / 2);
-            T.tiles[1] = (int32_t)(tiles_of(r, h->cg) * tiles_of(c, h->cg));
+            const Shape cut{h->cg, h->bn, 0.0};
+            T.tiles[0] = (int32_t)square_tiles(cut, m);
+            T.tiles[1] = (int32_t)(tile_rows(cut, r) * tile_cols(cut, c));
             T.chunks = (int32_t)div_up(r * c, kChunk);
             T.aspect = (float)std::sqrt(std::max(1.0, (double)r / (double)c));
             T.rms = (float)(0.2 * std::sqrt((double)std::max(r, c)));
@@ -1185,7 +1208,7 @@ try {
             data += 2 * (3 * x + kSquares * g);
             zero_status_t st = ZERO_OK;
             auto map = [&](int which, const Operand& o) {
-                if (st == ZERO_OK) st = encode(&T.map[which], o, ZERO_FP16, kBM, "zero_muon_bind");
+                if (st == ZERO_OK) st = encode(&T.map[which], o, ZERO_FP16, box_rows(h->bn), "zero_muon_bind");
             };
             auto out = [&](int which, const void* p, int64_t rows, int64_t cols, int64_t ld) {
                 if (st == ZERO_OK) st = encode_box(&T.map[which], p, rows, cols, ld, ZERO_FP16, 32, 32, "zero_muon_bind");
