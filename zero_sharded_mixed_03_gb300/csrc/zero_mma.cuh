@@ -260,6 +260,16 @@ struct GemmShape {
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
+// One lane of a whole warp, in a form that the compiler knows to be one: copies and products are then issued from
+// uniform registers.  Behind `lane == 0` it has to expect several, and two copies cost 470 cycles, more than the
+// products of an inner block take (128 x 128 tiles).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // mbar_wait with the clock read rarely: reading it twice before the first try costs more than most waits here take.
 __device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity)
 {
@@ -355,7 +365,7 @@ struct Tiles {
         bool ok = true;
         if (warp == 0) {
             // ---- producer: one thread
-            if (lane == 0) {
+            if (elect_one()) {
                 uint32_t k = 0, tile = 0;
                 for (int i = first; i < end && ok; i += step, ++tile) {
                     typename W::Item I;
@@ -378,7 +388,7 @@ struct Tiles {
             }
         } else if (warp == 1) {
             // ---- products: one thread of the leading block
-            if (lane == 0 && rank == 0) {
+            if (rank == 0 && elect_one()) {
                 uint32_t k = 0, tile = 0;
                 for (int i = first; i < end && ok; i += step, ++tile) {
                     typename W::Item I;
@@ -468,7 +478,7 @@ struct Tiles {
         if (!ok) {
             // A wait ran out: say so, and give copies and products in flight time to end before the block's memory
             // is given back.
-            if (lane == 0) atomicOr(error, 1u);
+            atomicOr(error, 1u);
             const uint64_t t0 = global_ns();
             for (uint32_t i = 0; i < kWaitIterCap && global_ns() - t0 < 100000000ull; ++i) __nanosleep(1000);
         }
