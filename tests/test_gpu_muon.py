@@ -248,17 +248,17 @@ def test_exact(r, c, k):
         mu = Muon([(r, c)], n_d, "bf16")
         for g in mu.g:
             g[0].copy_(v)
-        # singular values 2^-k: x -> x (1.5 - 0.5 x^2), then x (1 + 0.25 x^2 + 0.25 x^4), of few bits each
-        abc = [(1.5, -0.5, 0.0), (1.0, 0.25, 0.25)]
+        # singular values 2^-k: x -> x (1.5 - 0.5 x^2), then (two steps where k < 2) x (1 + 0.25 x^2): from 1/2 11/16 and
+        # 11/16 (1 + 121/1024), the polynomials' parts of at most 7 bits
+        abc = [(1.5, -0.5, 0.0), (1.0, 0.25, 0.0)]
         hyper = Z.muon_hyper(lr=1.0, weight_decay=0.0, momentum=0.0, eps=1e-12, steps=1 if k > 1 else 2, coefficients=abc, scale=0)
         mu.p[0].zero_()
         mu.step(hyper)
         x = v.double().cuda() * 2.0 ** -(k + 3)
         for a, b, d in abc[:hyper.steps]:
             x = x * (a + b * x ** 2 + d * x ** 4)
-        x = x.to(torch.float16).double()
         assert torch.equal(mu.p[0].double(), -x), float((mu.p[0].double() + x).abs().max())
-        assert torch.equal(mu.x[0], x.to(torch.bfloat16))
+        assert torch.equal(mu.x[0], x.float().to(torch.bfloat16))
         mu.guards_stand()
         mu.close()
 
@@ -271,7 +271,7 @@ def test_exact_two_at_once(r, c):
     mu.p[0].zero_()
     # singular values 1/2: G 1/4, R1 1/8, W 1/32, the second G 81/256 and R 81/512, Q 1241/4096
     mu.step(Z.muon_hyper(lr=1.0, weight_decay=0.0, momentum=0.0, eps=1e-12, steps=2, coefficients=(1.0, 0.5, 0.0), scale=0))
-    x = (v.double().cuda() / 16 * (5337 / 4096)).to(torch.float16).double()
+    x = v.double().cuda() / 16 * (5337 / 4096)
     assert torch.equal(mu.p[0].double(), -x)
     mu.close()
 

@@ -9,7 +9,8 @@
 // products on the tensor cores: G and the polynomial of it, of which only the upper triangle's tiles are multiplied and
 // kept, and the polynomial times X.  Nothing is transposed in memory: a tensor map takes X, or a symmetric matrix's tile
 // in place of the one across the diagonal, along its rows or along its columns.  All products of all matrices are one cooperative launch: a matrix's next product begins when
-// the one before it is complete, whatever the other matrices do, so that no round of tiles has to be full.
+// the one before it is complete, whatever the other matrices do, so that no round of tiles has to be full.  The last
+// product's tiles go into the parameters and are never stored.
 //
 // Operands are fp16 whatever the gradients' type, times powers of two that keep them in its range (the iterates' are
 // bounded: ||X||_2 <= 1 at first, and the coefficients give the rest).  Rounding to bf16's 8 bits costs 1 to 3 % of the
@@ -70,7 +71,7 @@ struct alignas(128) MuonTensor {
     float aspect, rms;           // factors of the update
     int32_t rows, cols, m, ldx, ldm;
     int32_t wide;                // rows <= cols: G = X X^T
-    int32_t vec_g, vec_p;        // 16-byte accesses to the contributions; to p, p16 and update
+    int32_t vec_g, vec_p;        // 16-byte accesses to the contributions; four elements at once of p, p16 and update
     int32_t chunks;              // of the first pass
     int32_t tiles[2];            // of a symmetric product, and of one with X
 };
@@ -92,8 +93,8 @@ struct MuonParams {
     uint32_t* tickets;           // [tensor]
     uint32_t* counters;          // [tensor][kMaxPhases]: warps that have stored their part of a product's tile
     int32_t n_counters;
-    int32_t count, n_d, nesterov, src, how;
-    float inv, mu, nu, sigma, lr, decay;   // nu = 1 - mu; sigma: X's factor in fp16
+    int32_t count, n_d, nesterov;
+    float inv, mu, nu, sigma;    // nu = 1 - mu; sigma: X's factor in fp16
     double eps;
 };
 
@@ -301,6 +302,48 @@ __global__ void __launch_bounds__(kThreads, 6) muon_start_kernel(const __grid_co
     }
 }
 
+// ------------------------------------------------------------------ the parameters
+
+// Is the step left out?
+__device__ __forceinline__ bool left_out(const MuonState* st, const DevState* plan)
+{
+    if (!plan) return *(const volatile uint32_t*)&st->flag != 0;
+    const volatile DevState* p = plan;
+    return (p->flag | p->error) != 0;
+}
+
+// By the last block, when every block has read the flag.
+__device__ __forceinline__ void close_step(MuonState* state, bool skip)
+{
+    volatile MuonState* st = state;
+    st->closed = 0;
+    st->flag = 0;
+    st->finished = st->finished + 1;
+    st->last_skipped = skip ? 1u : 0u;
+    if (skip) {
+        st->skipped = st->skipped + 1;
+    } else {
+        st->t = st->t + 1;
+        st->cur = (st->cur & 1) ^ 1;
+    }
+}
+
+// A step without elements.
+__global__ void __launch_bounds__(32) muon_close_kernel(MuonState* st, DevState* plan)
+{
+    after_earlier_work();
+    if (threadIdx.x == 0) close_step(st, left_out(st, plan));
+}
+
+__device__ __forceinline__ uint16_t narrow_to(float x, bool bf) { return bf ? narrow1<ZERO_BF16>(x) : narrow1<ZERO_FP16>(x); }
+__device__ __forceinline__ uint2 narrow_to(const float4& x, bool bf)
+{
+    return bf ? make_uint2(narrow2<ZERO_BF16>(x.x, x.y), narrow2<ZERO_BF16>(x.z, x.w)) : make_uint2(narrow2<ZERO_FP16>(x.x, x.y), narrow2<ZERO_FP16>(x.z, x.w));
+}
+
+// p - decay p - step x
+__device__ __forceinline__ float moved(float p, float x, float step, float decay) { return fmaf(-step, x, fmaf(-decay, p, p)); }
+
 // ------------------------------------------------------------------ the products
 
 // Rows of a box of an operand taken along K.
@@ -316,6 +359,7 @@ struct Op {
     int32_t left, right, out;    // operands and result; kNext: left is the polynomial
     int32_t adds, add[2];
     int32_t keep_low;            // kNext: the successor's low part is wanted
+    int32_t final;               // kNext: the result is the update, for the parameters
     float scale, lin[2], diag;
 };
 
@@ -324,6 +368,10 @@ struct ProductParams {
     const Piece* tiles;          // each worker's, in the order of the products: tensor | product << 16
     const int32_t* bounds;       // [worker][kMaxPhases]: where its tiles of each product begin
     uint32_t* counters;
+    MuonState* st;
+    DevState* plan;              // a sharded step that this one is part of, or NULL
+    int32_t how, bf;             // ZERO_MUON_SCALE_*; the 16-bit type is bf16
+    float lr, decay;             // lr weight_decay
     int32_t first, last;         // products that are made
     Op ops[kMaxPhases];          // ops[i - first] is product i
 };
@@ -543,14 +591,127 @@ struct MuonWork {
         if (adds > 1) fetch(A.v[1], I.add[1], I, row0, (int64_t)I.n * BN + c, lane);
     }
 
+    // The last product's end: x goes into the parameters, in fp32 through shared memory, so that a warp reads and writes
+    // neighbours; the parameters of the next part are loaded as this one's are stored.
+    struct Target {
+        float* p;
+        uint16_t *p16, *update;
+        int32_t rows, cols;
+        bool vec;
+        float step;
+    };
+    __device__ __forceinline__ Target target(const Item& I) const
+    {
+        const MuonTensor& T = P.tensors[I.tensor];
+        const float s = P.how == ZERO_MUON_SCALE_RMS ? T.rms : P.how == ZERO_MUON_SCALE_ASPECT ? T.aspect : 1.0f;
+        return Target{T.p, T.p16, T.update, T.rows, T.cols, T.vec_p != 0, P.lr * s};
+    }
+    // Four parameters: row i * 4 + lane / 8 of the part, columns 4 (lane % 8) on.
+    __device__ __forceinline__ static uint4 parameters(const Target& G, int64_t row0, int64_t col0, int i, int lane)
+    {
+        const int64_t row = row0 + i * 4 + (lane >> 3), col = col0 + (lane & 7) * 4;
+        if (!G.p || row >= G.rows || col >= G.cols) return make_uint4(0u, 0u, 0u, 0u);
+        return __ldcs(reinterpret_cast<const uint4*>(G.p + row * G.cols + col));
+    }
+    __device__ __forceinline__ static uint32_t turned_at(uint32_t stage, int row, int piece) { return stage + row * 128 + ((piece ^ (row & 7)) << 4); }
+
+    __device__ __forceinline__ void apply(const Target& G, Ahead& A, bool more, int64_t row0, int64_t col0, int lane, uint32_t stage, const float (&x)[32]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(turned_at(stage, lane, i)), "f"(x[4 * i]), "f"(x[4 * i + 1]), "f"(x[4 * i + 2]), "f"(x[4 * i + 3]) : "memory");
+        __syncwarp();
+        if (G.vec) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint4& w = A.v[i >> 2][i & 3];
+                const int r = i * 4 + (lane >> 3);
+                const int64_t row = row0 + r, col = col0 + (lane & 7) * 4;
+                float4 z, p = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(z.x), "=f"(z.y), "=f"(z.z), "=f"(z.w) : "r"(turned_at(stage, r, lane & 7)) : "memory");
+                if (more) w = parameters(G, row0, col0 + 2 * kEpiCols, i, lane);
+                if (row >= G.rows || col >= G.cols) continue;
+                const int64_t e = row * G.cols + col;
+                if (G.update) __stcs(reinterpret_cast<uint2*>(G.update + e), narrow_to(z, P.bf));
+                if (!G.p) continue;
+                p = make_float4(moved(p.x, z.x, G.step, P.decay), moved(p.y, z.y, G.step, P.decay), moved(p.z, z.z, G.step, P.decay), moved(p.w, z.w, G.step, P.decay));
+                __stcs(reinterpret_cast<float4*>(G.p + e), p);
+                if (G.p16) __stcs(reinterpret_cast<uint2*>(G.p16 + e), narrow_to(p, P.bf));
+            }
+        } else if (col0 + lane < G.cols) {
+            // a column a lane; eight rows loaded before any is stored
+            const int rows = (int)min((int64_t)32, G.rows - row0);
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+                float p[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = G.p && r0 + j < rows ? G.p[(row0 + r0 + j) * G.cols + col0 + lane] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (r0 + j >= rows) break;
+                    const int64_t e = (row0 + r0 + j) * G.cols + col0 + lane;
+                    float z;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z) : "r"(turned_at(stage, r0 + j, lane >> 2) + (lane & 3) * 4) : "memory");
+                    if (G.update) G.update[e] = narrow_to(z, P.bf);
+                    if (!G.p) continue;
+                    const float q = moved(p[j], z, G.step, P.decay);
+                    G.p[e] = q;
+                    if (G.p16) G.p16[e] = narrow_to(q, P.bf);
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void finish_final(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    {
+        const Op& O = *I.op;
+        if (left_out(P.st, P.plan)) return;
+        const Target G = target(I);
+        const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
+        for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
+            const int64_t col0 = (int64_t)I.n * BN + c;
+            if (col0 >= I.cols || row0 >= I.rows) break;
+            float x[32];
+            tmem_load32(acc + c, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] *= O.scale;
+            if (O.adds > 0) {
+                // one or two steps in all: the addends and the parameters are loaded here
+                fetch_adds(I, A, row0, c, lane);
+                stash(stage, A.v[0], lane);
+                stash(stage + kTile16Bytes, A.v[1], lane);
+                __syncwarp();
+                add_row(stage, O.lin[0], x, lane);
+                add_row(stage + kTile16Bytes, O.lin[1], x, lane);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (G.vec) A.v[i >> 2][i & 3] = parameters(G, row0, col0, i, lane);
+            }
+            apply(G, A, O.adds == 0 && c + 2 * kEpiCols < BN, row0, col0, lane, stage, x);
+        }
+    }
+
     __device__ __forceinline__ void prepare(const Item& I, int quad, int half, int rank, int lane, Ahead& A) const
     {
+        if (I.op->final) {
+            if (I.op->adds > 0) return;
+            const Target G = target(I);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (G.vec) A.v[i >> 2][i & 3] = parameters(G, ((int64_t)I.m * CG + rank) * kBM + quad * 32, (int64_t)I.n * BN + half * kEpiCols, i, lane);
+            return;
+        }
         fetch_adds(I, A, ((int64_t)I.m * CG + rank) * kBM + quad * 32, half * kEpiCols, lane);
     }
 
     __device__ __forceinline__ void finish(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
         const Op& O = *I.op;
+        if (O.final) {
+            finish_final(I, A, acc, quad, half, stage, rank, lane);
+            return;
+        }
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
         uint32_t turn = 0;
         for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols, turn ^= kTile16Bytes) {
@@ -599,79 +760,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) mu
     T.template open<true>(smem_raw);
     after_earlier_work();
     T.run(MuonWork<CG, BN>{P}, &g_muon_error);
-}
-
-// ------------------------------------------------------------------ the parameters
-
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 5) muon_apply_kernel(const __grid_constant__ MuonParams P)
-{
-    after_earlier_work();
-    bool skip = (*(const volatile uint32_t*)&P.st->flag) != 0;
-    if (P.plan) {
-        const volatile DevState* plan = P.plan;
-        skip = (plan->flag | plan->error) != 0;
-    }
-    if (!skip) {
-        const float unit = 1.0f / P.sigma;      // a power of two
-        Piece next = P.count > 0 ? P.pieces[min((int)blockIdx.x, P.count - 1)] : Piece{0, 0};
-        for (int i = blockIdx.x; i < P.count; i += gridDim.x) {
-            const Piece piece = next;
-            next = P.pieces[min(i + (int)gridDim.x, P.count - 1)];
-            const MuonTensor& T = P.tensors[piece.tensor];
-            const Eight E = eight_at(T, piece.at);
-            if (E.n == 0) continue;
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(T.x[P.src] + E.x));
-            float* const q = T.p ? T.p + E.e : nullptr;
-            uint16_t *const q16 = T.p16 ? T.p16 + E.e : nullptr, *const update = T.update ? T.update + E.e : nullptr;
-            const bool vec = T.vec_p;
-            const float step = P.lr * (P.how == ZERO_MUON_SCALE_RMS ? T.rms : P.how == ZERO_MUON_SCALE_ASPECT ? T.aspect : 1.0f);
-            float x[8], p[8];
-            if (q && vec) {
-                load_floats(q, p);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = q && j < E.n ? q[j] : 0.0f;
-            }
-            widen2<ZERO_FP16>(w.x, x[0], x[1]);
-            widen2<ZERO_FP16>(w.y, x[2], x[3]);
-            widen2<ZERO_FP16>(w.z, x[4], x[5]);
-            widen2<ZERO_FP16>(w.w, x[6], x[7]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] *= unit;
-                p[j] = fmaf(-step, x[j], fmaf(-P.decay, p[j], p[j]));
-            }
-            if (update) store8<DT>(update, vec, E.n, x);
-            if (!q) continue;
-            if (vec) {
-                reinterpret_cast<float4*>(q)[0] = make_float4(p[0], p[1], p[2], p[3]);
-                reinterpret_cast<float4*>(q)[1] = make_float4(p[4], p[5], p[6], p[7]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < E.n) q[j] = p[j];
-            }
-            if (q16) store8<DT>(q16, vec, E.n, p);
-        }
-    }
-    // the last block to finish closes the step: every block has read the flag by then
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        if (atomicAdd(&P.st->closed, 1u) == gridDim.x - 1) {
-            volatile MuonState* st = P.st;
-            st->closed = 0;
-            st->flag = 0;
-            st->finished = st->finished + 1;
-            st->last_skipped = skip ? 1u : 0u;
-            if (skip) {
-                st->skipped = st->skipped + 1;
-            } else {
-                st->t = st->t + 1;
-                st->cur = (st->cur & 1) ^ 1;
-            }
-        }
-    }
+    if (threadIdx.x == 0 && atomicAdd(&P.st->closed, 1u) == gridDim.x - 1) close_step(P.st, left_out(P.st, P.plan));
 }
 
 }  // namespace
@@ -895,13 +984,10 @@ MuonParams params(const zero_muon* h, const zero_muon_hyper_t& hyper, double los
     P.n_counters = (int32_t)h->rows.size() * kMaxPhases;
     P.n_d = h->n_d;
     P.nesterov = (hyper.flags & ZERO_MUON_NESTEROV) != 0;
-    P.how = hyper.scale;
     P.inv = (float)(1.0 / ((double)h->n_d * loss_scale));
     P.mu = (float)hyper.momentum;
     P.nu = (float)(1.0 - hyper.momentum);
     P.sigma = (float)range.sigma;
-    P.lr = (float)hyper.lr;
-    P.decay = (float)(hyper.lr * hyper.weight_decay);
     P.eps = hyper.eps;
     return P;
 }
@@ -955,6 +1041,12 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
         Q.tiles = reinterpret_cast<const Piece*>(ws + h->at_tiles);
         Q.bounds = reinterpret_cast<const int32_t*>(ws + h->at_bounds);
         Q.counters = P.counters;
+        Q.st = P.st;
+        Q.plan = P.plan;
+        Q.how = hyper.scale;
+        Q.bf = h->dtype16 == ZERO_BF16;
+        Q.lr = (float)hyper.lr;
+        Q.decay = (float)(hyper.lr * hyper.weight_decay);
         // one step alone of a handle that makes two at once is the first of the single ones
         const bool pair = h->pair && hyper.steps >= 2;
         Q.first = h->pair && !pair ? kPairPhases : 0;
@@ -1019,12 +1111,14 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
             square(kG, kG, kPoly, c[2], twice ? 0.0 : c[0], {{kG, c[1]}});
             next(kPoly, twice ? c[0] : 0.0, twice && k + 1 < kTwice && k + 1 < hyper.steps);
         }
-        const zero_status_t st = h->cg == 2 ? launch_products<2, 256>(h, Q, s) : h->bn == 128 ? launch_products<1, 128>(h, Q, s) : launch_products<1, 64>(h, Q, s);
-        if (st != ZERO_OK) return st;
-        P.src = src;
+        Op& end = Q.ops[ops - 1];
+        end.final = 1;
+        end.scale /= (float)R.sigma;
+        end.lin[0] /= (float)R.sigma;
+        end.lin[1] /= (float)R.sigma;
+        return h->cg == 2 ? launch_products<2, 256>(h, Q, s) : h->bn == 128 ? launch_products<1, 128>(h, Q, s) : launch_products<1, 64>(h, Q, s);
     }
-    e = h->dtype16 == ZERO_BF16 ? launch_after(muon_apply_kernel<ZERO_BF16>, grid, kThreads, 0, s, P)
-                                : launch_after(muon_apply_kernel<ZERO_FP16>, grid, kThreads, 0, s, P);
+    e = launch_after(muon_close_kernel, 1, 32, 0, s, P.st, P.plan);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
 }
 
@@ -1198,7 +1292,7 @@ try {
                 T.vec_g = T.vec_g && aligned(g, 16);
                 table[i * (size_t)h->n_d + (size_t)k] = g;
             }
-            T.vec_p = c % 8 == 0 && aligned(T.p, 16) && aligned(T.p16, 16) && aligned(T.update, 16);
+            T.vec_p = c % 4 == 0 && aligned(T.p, 16) && aligned(T.p16, 8) && aligned(T.update, 8);
             uint16_t* q = reinterpret_cast<uint16_t*>(ws + data);
             const int64_t x = x_elems(r, c), g = g_elems(m);
             T.x[0] = q;
