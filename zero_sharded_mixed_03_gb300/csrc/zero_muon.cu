@@ -40,6 +40,7 @@ constexpr int kThreads = 256;
 constexpr int kChunk = 8 * kThreads;
 constexpr int kPassBlocks = 6;            // blocks an SM of a pass over the elements
 constexpr int kStateBlock = 256;          // each matrix's momentum starts on a multiple of it
+constexpr int kRowElems = 16;             // rows of X and of the symmetric matrices are a multiple of it: 32 bytes
 constexpr int kSquares = 4;               // symmetric matrices beside each X
 constexpr int kMaxPhases = 32;            // products of a step, at most 25
 constexpr int kTwice = 2;                 // iterations whose X is the sum of two fp16 numbers
@@ -263,7 +264,7 @@ __device__ __forceinline__ Eight eight_at(const MuonTensor& T, int at)
     } else if (T.cols != T.ldx) {
         const int64_t row = i / groups, col = (i - row * groups) * 8;
         E.e = row * T.cols + col;
-        E.n = (int)min((int64_t)8, T.cols - col);
+        E.n = (int)max((int64_t)0, min((int64_t)8, T.cols - col));
     }
     return E;
 }
@@ -280,10 +281,11 @@ __global__ void __launch_bounds__(kThreads, 6) muon_start_kernel(const __grid_co
         const MuonTensor& T = P.tensors[piece.tensor];
         const Eight E = eight_at(T, piece.at);
         if (E.n == 0) continue;
+        const bool vec = T.cols % 8 == 0;
         const float scale = P.scale[piece.tensor];
         const float *old = P.momentum[cur & 1] + T.at + E.e, *now = P.momentum[(cur & 1) ^ 1] + T.at + E.e;
         float m0[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, m1[8], x[8];
-        if (T.cols == T.ldx) {
+        if (vec) {
             load_floats(now, m1);
             if (P.nesterov) load_floats(old, m0);
         } else {
@@ -550,45 +552,41 @@ struct MuonWork {
     struct Ahead {
         uint4 v[2][4];
     };
-    // Rows of a multiple of eight columns that start on 16 bytes: all eight of a piece are there, or none.  From L2:
-    // other blocks write these buffers while this kernel runs.
-    __device__ __forceinline__ static void fetch(uint4 (&v)[4], const uint16_t* p, const Item& L, int64_t row0, int64_t col0, int lane)
+    // Row `lane` of a 32 x 32 part: two loads of 32 bytes, as rows are of a multiple of 16 columns and start on 32 bytes.
+    // A load touches 32 rows, but what it brings needs no turning: through shared memory, which the products read
+    // all the time, a tile with two addends took 10 us to finish.  From L2: other blocks write these buffers while this
+    // kernel runs.
+    __device__ __forceinline__ static void fetch(uint4 (&v)[4], const uint16_t* p, const Item& L, int64_t row, int64_t col0)
     {
-        const int64_t col = col0 + (lane & 3) * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = row0 + i * 8 + (lane >> 2);
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < L.rows && col < L.cols) v[i] = __ldcg(reinterpret_cast<const uint4*>(p + row * L.ld + col));
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = v[2 * i + 1] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < L.rows && col0 + 16 * i < L.ld)
+                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(v[2 * i].x), "=r"(v[2 * i].y), "=r"(v[2 * i].z), "=r"(v[2 * i].w), "=r"(v[2 * i + 1].x), "=r"(v[2 * i + 1].y),
+                               "=r"(v[2 * i + 1].z), "=r"(v[2 * i + 1].w)
+                             : "l"(p + row * L.ld + col0 + 16 * i)
+                             : "memory");
         }
     }
-    __device__ __forceinline__ static void stash(uint32_t stage, const uint4 (&v)[4], int lane)
+    __device__ __forceinline__ static void add_row(const uint4 (&v)[4], float lin, float (&x)[32])
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile16_at(stage, i * 8 + (lane >> 2), lane & 3)), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
-    }
-    __device__ __forceinline__ static void add_row(uint32_t stage, float lin, float (&x)[32], int lane)
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tile16_at(stage, lane, i)) : "memory");
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float a, b;
-                widen2<ZERO_FP16>(w[j], a, b);
+                widen2<ZERO_FP16>(word(v[i], j), a, b);
                 x[8 * i + 2 * j] = fmaf(lin, a, x[8 * i + 2 * j]);
                 x[8 * i + 2 * j + 1] = fmaf(lin, b, x[8 * i + 2 * j + 1]);
             }
-        }
     }
 
     __device__ __forceinline__ void fetch_adds(const Item& I, Ahead& A, int64_t row0, int c, int lane) const
     {
         const int adds = I.op->adds;
-        if (adds > 0) fetch(A.v[0], I.add[0], I, row0, (int64_t)I.n * BN + c, lane);
-        if (adds > 1) fetch(A.v[1], I.add[1], I, row0, (int64_t)I.n * BN + c, lane);
+        if (adds > 0) fetch(A.v[0], I.add[0], I, row0 + lane, (int64_t)I.n * BN + c);
+        if (adds > 1) fetch(A.v[1], I.add[1], I, row0 + lane, (int64_t)I.n * BN + c);
     }
 
     // The last product's end: x goes into the parameters, in fp32 through shared memory, so that a warp reads and writes
@@ -678,12 +676,8 @@ struct MuonWork {
             if (O.adds > 0) {
                 // one or two steps in all: the addends and the parameters are loaded here
                 fetch_adds(I, A, row0, c, lane);
-                stash(stage, A.v[0], lane);
-                stash(stage + kTile16Bytes, A.v[1], lane);
-                __syncwarp();
-                add_row(stage, O.lin[0], x, lane);
-                add_row(stage + kTile16Bytes, O.lin[1], x, lane);
-                __syncwarp();
+                add_row(A.v[0], O.lin[0], x);
+                if (O.adds > 1) add_row(A.v[1], O.lin[1], x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (G.vec) A.v[i >> 2][i & 3] = parameters(G, row0, col0, i, lane);
@@ -721,20 +715,13 @@ struct MuonWork {
             tmem_load32(acc + c, x);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] *= O.scale;
-            // The tile that is sent: the warp's two in turn, unless there is a second addend or a low part for the
-            // other.  A lane's row of it is where its row of the addend was.
-            const bool both = O.adds > 1 || O.keep_low;
-            const uint32_t at = both ? stage : stage + turn;
-            if (both) sent_read<0>(lane);
+            if (O.adds > 0) add_row(A.v[0], O.lin[0], x);
+            if (O.adds > 1) add_row(A.v[1], O.lin[1], x);
+            if (c + 2 * kEpiCols < BN) fetch_adds(I, A, row0, c + 2 * kEpiCols, lane);
+            // the warp's two tiles in turn, unless the low part needs one
+            const uint32_t at = O.keep_low ? stage : stage + turn;
+            if (O.keep_low) sent_read<0>(lane);
             else sent_read<1>(lane);
-            if (O.adds > 0) {
-                stash(at, A.v[0], lane);
-                if (O.adds > 1) stash(stage + kTile16Bytes, A.v[1], lane);
-                __syncwarp();
-                if (c + 2 * kEpiCols < BN) fetch_adds(I, A, row0, c + 2 * kEpiCols, lane);
-                add_row(at, O.lin[0], x, lane);
-                if (O.adds > 1) add_row(stage + kTile16Bytes, O.lin[1], x, lane);
-            }
             if (I.kind != kNext && row0 == col0) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] += j == lane ? O.diag : 0.0f;
@@ -1133,8 +1120,8 @@ zero_status_t plan_ready(const zero_muon* h, const zero_plan* plan, const char* 
 }
 
 // Elements of X, and of G, in the workspace: each buffer starts on 256 bytes.
-int64_t x_elems(int64_t rows, int64_t cols) { return up(rows * up(cols, 8), 128); }
-int64_t g_elems(int64_t m) { return up(m * up(m, 8), 128); }
+int64_t x_elems(int64_t rows, int64_t cols) { return up(rows * up(cols, kRowElems), 128); }
+int64_t g_elems(int64_t m) { return up(m * up(m, kRowElems), 128); }
 
 }  // namespace
 }  // namespace zero
@@ -1170,7 +1157,7 @@ try {
     for (int64_t i = 0; i < n_matrices; ++i) {
         const int64_t r = rows[i], c = cols[i];
         for (int64_t k = 0; k < div_up(r * c, kChunk); ++k) h->chunks.push_back(Piece{(int32_t)i, (int32_t)k});
-        for (int64_t k = 0; k < div_up(r * up(c, 8), kChunk); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
+        for (int64_t k = 0; k < div_up(r * up(c, kRowElems), kChunk); ++k) h->groups.push_back(Piece{(int32_t)i, (int32_t)k});
     }
     // Two iterations at once replace two passes over X by products of the smaller side, and are as exact from sides of
     // 64 on; for small sides the second G's largest values, differences of larger terms, are not.
@@ -1267,8 +1254,8 @@ try {
         T.cols = (int32_t)c;
         T.m = (int32_t)m;
         if (m > 0) {
-            T.ldx = (int32_t)up(c, 8);
-            T.ldm = (int32_t)up(m, 8);
+            T.ldx = (int32_t)up(c, kRowElems);
+            T.ldm = (int32_t)up(m, kRowElems);
             T.wide = r <= c;
             T.at = at;
             const Shape cut{h->cg, h->bn, 0.0};
