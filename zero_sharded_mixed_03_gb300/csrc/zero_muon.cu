@@ -38,7 +38,9 @@ constexpr int kThreads = 256;
 // what runs at one time reads a few MB of each contribution: with 32768 in a row the contributions' pages are too many
 // (16 of 100M elements: 895 us; with 8192 816).
 constexpr int kChunk = 8 * kThreads;
-constexpr int kPassBlocks = 6;            // blocks an SM of a pass over the elements
+// Blocks an SM of the passes over the elements: as many as run at one time.  With six of the first pass, of which five
+// run, 16 contributions of 50M elements took 360 us instead of 304 (6.6 TB/s).
+constexpr int kReduceBlocks = 5, kStartBlocks = 6;
 constexpr int kStateBlock = 256;          // each matrix's momentum starts on a multiple of it
 constexpr int kRowElems = 16;             // rows of X and of the symmetric matrices are a multiple of it: 32 bytes
 constexpr int kSquares = 4;               // symmetric matrices beside each X
@@ -160,7 +162,7 @@ __device__ __forceinline__ void sum_contributions(const void* const* grads, int 
 // A block's sum of squares of a matrix goes to the slot of its first piece of it; the last of the blocks that have any
 // sums them, in order.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 5) muon_reduce_kernel(const __grid_constant__ MuonParams P)
+__global__ void __launch_bounds__(kThreads, kReduceBlocks) muon_reduce_kernel(const __grid_constant__ MuonParams P)
 {
     after_earlier_work();
     __shared__ double warp_sum[kThreads / 32];
@@ -203,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 5) muon_reduce_kernel(const __grid_c
                 sum = fmaf(u, u, sum);
             }
             float4* o = reinterpret_cast<float4*>(to + at + e);
-            o[0] = make_float4(m1[0], m1[1], m1[2], m1[3]);
-            o[1] = make_float4(m1[4], m1[5], m1[6], m1[7]);
+            __stcs(o, make_float4(m1[0], m1[1], m1[2], m1[3]));
+            __stcs(o + 1, make_float4(m1[4], m1[5], m1[6], m1[7]));
         }
         const int sharers = min(chunks, (int)gridDim.x);
         const double s = block_sum_fixed<kThreads>((double)sum, warp_sum);
@@ -269,7 +271,7 @@ __device__ __forceinline__ Eight eight_at(const MuonTensor& T, int at)
     return E;
 }
 
-__global__ void __launch_bounds__(kThreads, 6) muon_start_kernel(const __grid_constant__ MuonParams P)
+__global__ void __launch_bounds__(kThreads, kStartBlocks) muon_start_kernel(const __grid_constant__ MuonParams P)
 {
     after_earlier_work();
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < P.n_counters; i += gridDim.x * kThreads) P.counters[i] = 0;
@@ -795,36 +797,63 @@ struct Range {
 
 double power_below(double limit) { return std::exp2(std::floor(std::log2(limit))); }
 
-// Bounds of the singular values of all of them from the coefficients, by sampling the functions of one singular value
-// that they are, with slack for what lies between the samples and for rounding.  False: they grow too far.
+// The largest of |f| on [0, hi], f(g) = k0 + k1 g + k2 g^2: at an end or where the slope is 0.
+double largest(double k0, double k1, double k2, double hi)
+{
+    auto f = [&](double g) { return std::fabs(k0 + g * (k1 + g * k2)); };
+    double m = std::max(f(0.0), f(hi));
+    const double g = k2 != 0.0 ? -k1 / (2.0 * k2) : -1.0;
+    return g > 0.0 && g < hi ? std::max(m, f(g)) : m;
+}
+
+// The largest of |a s + b s^3 + c s^5| on [0, hi].
+double largest_step(const double* k, double hi)
+{
+    auto f = [&](double s) { return std::fabs(s * (k[0] + s * s * (k[1] + s * s * k[2]))); };
+    double m = f(hi);
+    // a + 3 b g + 5 c g^2 = 0, g = s^2
+    const double root = 9.0 * k[1] * k[1] - 20.0 * k[0] * k[2];
+    double g[2] = {-1.0, -1.0};
+    if (k[2] == 0.0) {
+        if (k[1] != 0.0) g[0] = -k[0] / (3.0 * k[1]);
+    } else if (root >= 0.0) {
+        g[0] = (-3.0 * k[1] - std::sqrt(root)) / (10.0 * k[2]);
+        g[1] = (-3.0 * k[1] + std::sqrt(root)) / (10.0 * k[2]);
+    }
+    for (const double x : g)
+        if (x > 0.0 && x < hi * hi) m = std::max(m, f(std::sqrt(x)));
+    return m;
+}
+
+// Bounds of the singular values of all of them from the coefficients, with slack for rounding.  False: they grow too
+// far.
 bool find_range(const zero_muon_hyper_t& hyper, bool pair, Range* r)
 {
-    constexpr int kSamples = 4096;
     double hi = 1.0, x = 1.0, most[kRoles];
     for (double& m : most) m = 1e-6;
     auto see = [&](Role role, double v) { most[role] = std::max(most[role], std::fabs(v)); };
     for (int k = 0; k < hyper.steps; ++k) {
         const double* c = hyper.coefficients[k];
-        double next = 0.0;
-        for (int i = 0; i <= kSamples; ++i) {
-            const double s = hi * i / kSamples, g = s * s, rest = c[1] * g + c[2] * g * g, poly = c[0] + rest;
-            next = std::max(next, std::fabs(s * poly));
-            see(kG, g);
-            see(kPoly, poly);
-            see(kPoly, rest);
-            if (k == 0 && pair && hyper.steps > 1) {
-                const double* e = hyper.coefficients[1];
-                const double g2 = g * poly * poly, rest2 = e[1] * g2 + e[2] * g2 * g2;
-                see(kR1, rest);
-                see(kW, rest * g);
-                see(kG2, g2);
-                see(kR2, rest2);
-                see(kQ, poly * (e[0] + rest2) - c[0] * e[0]);
-            }
-        }
-        hi = std::max(1.01 * next, 1e-6);
+        see(kG, hi * hi);
+        see(kPoly, largest(c[0], c[1], c[2], hi * hi));
+        see(kPoly, largest(0.0, c[1], c[2], hi * hi));
+        hi = std::max(1.01 * largest_step(c, hi), 1e-6);
         if (!(hi <= 8.0)) return false;
         x = std::max(x, hi);
+    }
+    if (pair && hyper.steps > 1) {
+        // functions of one singular value, at most 1: by samples, as the factors' room is more than what lies between them
+        constexpr int kSamples = 256;
+        const double *c = hyper.coefficients[0], *e = hyper.coefficients[1];
+        for (int i = 0; i <= kSamples; ++i) {
+            const double s = 1.01 * i / kSamples, g = s * s, rest = c[1] * g + c[2] * g * g, poly = c[0] + rest;
+            const double g2 = g * poly * poly, rest2 = e[1] * g2 + e[2] * g2 * g2;
+            see(kR1, rest);
+            see(kW, rest * g);
+            see(kG2, g2);
+            see(kR2, rest2);
+            see(kQ, poly * (e[0] + rest2) - c[0] * e[0]);
+        }
     }
     r->sigma = power_below(24000.0 / x);
     for (int i = 0; i < kRoles; ++i) {
@@ -845,12 +874,16 @@ int phase_kind(bool pair, int phase)
 }
 int phase_count(bool pair, int steps) { return pair ? kPairPhases + 3 * (steps - 2) : 3 * steps; }
 
-// How tiles are cut: what a pair or block takes, and the estimated time of an inner block of it: zero_linear's.
+// How tiles are cut: what a pair or block takes; the time of an inner block of it, what a tile costs besides, and the
+// way from a product's end to the next one's first block.  Fitted to steps of three layers of a 256-wide network, four
+// 512 wide, one 1024 and one 2048 wide, and eight matrices of mixed sizes, each cut all three ways (within 25 %, most
+// 10): 256 x 256 tiles are best from 2048 on (1,120 us, 128 x 128 1,430), 128 x 128 at 512 (308; 340 and 365) and 1024
+// (344; 385 and 410), 128 x 64 at 256 (105; 175 and 130).
 struct Shape {
     int cg, bn;
-    double block_us;
+    double block_us, tile_us, join_us;
 };
-constexpr Shape kShapes[] = {{2, 256, 0.336}, {1, 128, 0.29}, {1, 64, 0.20}};
+constexpr Shape kShapes[] = {{2, 256, 0.40, 3.0, 8.0}, {1, 128, 0.22, 4.0, 3.0}, {1, 64, 0.19, 3.0, 3.0}};
 
 // Of a symmetric product: the tiles with anything on or above the diagonal, in whole diagonal blocks.
 bool kept(const Shape& S, int64_t a, int64_t b) { return b * S.bn >= a * 128 * S.cg; }
@@ -864,12 +897,10 @@ int64_t square_tiles(const Shape& S, int64_t m)
 }
 
 // Every product's tiles dealt to the workers (blocks, or pairs), each to the one that is free first once the product
-// before is complete: as many whole steps as a call may ask for, since the list of fewer is its beginning.  What a tile
-// costs besides its inner blocks, and the way from a product's end to the next one's first block, were measured at
-// sides of 256.  Returns the time that five steps take.
-double deal_tiles(const zero_muon* h, const Shape& S, std::vector<Piece>* out, std::vector<int32_t>* bounds)
+// before is complete: as many whole steps as a call may ask for, since the list of fewer is its beginning.  Returns the
+// time that five steps take; nothing is dealt where the work alone would take `limit`.
+double deal_tiles(const zero_muon* h, const Shape& S, double limit, std::vector<Piece>* out, std::vector<int32_t>* bounds)
 {
-    const double tile_us = 0.6, join_us = 4.0;
     const int cg = S.cg;
     const size_t n = h->rows.size();
     std::vector<size_t> order;                // longest inner dimension first
@@ -881,19 +912,29 @@ double deal_tiles(const zero_muon* h, const Shape& S, std::vector<Piece>* out, s
     }
     std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return std::max(h->rows[a], h->cols[a]) > std::max(h->rows[b], h->cols[b]); });
     const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(kGb300Sms / cg, most));
+    const int phases = phase_count(h->pair, ZERO_MUON_MAX_STEPS), five = phase_count(h->pair, 5);
+    double work = 0.0;
+    for (const size_t i : order) {
+        const int64_t r = h->rows[i], c = h->cols[i], m = std::min(r, c);
+        const double whole = (double)(tile_rows(S, r) * tile_cols(S, c)), half = (double)square_tiles(S, m);
+        for (int phase = 0; phase < five; ++phase) {
+            const int kind = phase_kind(h->pair, phase);
+            work += (kind == kNext ? whole : half) * ((double)div_up(kind == kGram ? std::max(r, c) : m, kBK) * S.block_us + S.tile_us);
+        }
+    }
+    if (work / workers >= limit) return limit;
     std::vector<std::vector<Piece>> mine((size_t)workers);
     using Free = std::pair<double, int>;
     std::vector<Free> heap;
     for (int w = 0; w < workers; ++w) heap.push_back(Free(0.0, w));
     std::vector<double> complete(n, 0.0);
     double at_five = 0.0, end = 0.0;
-    const int phases = phase_count(h->pair, ZERO_MUON_MAX_STEPS), five = phase_count(h->pair, 5);
     for (int phase = 0; phase < phases; ++phase) {
         const int kind = phase_kind(h->pair, phase);
         for (const size_t i : order) {
             const int64_t r = h->rows[i], c = h->cols[i], m = std::min(r, c), inner = kind == kGram ? std::max(r, c) : m;
             const int64_t tm = tile_rows(S, kind == kNext ? r : m), tn = tile_cols(S, kind == kNext ? c : m);
-            const double each = div_up(inner, kBK) * S.block_us + tile_us;
+            const double each = div_up(inner, kBK) * S.block_us + S.tile_us;
             double last = 0.0;
             // groups of eight tile rows, column by column, so that what runs at one time shares its operands
             for (int64_t g = 0; g < tm; g += 8)
@@ -907,7 +948,7 @@ double deal_tiles(const zero_muon* h, const Shape& S, std::vector<Piece>* out, s
                         mine[(size_t)f.second].push_back(Piece{(int32_t)((int64_t)i | (int64_t)phase << 16), (int32_t)(a << 16 | b)});
                         std::push_heap(heap.begin(), heap.end(), std::greater<Free>());
                     }
-            complete[i] = last + join_us;
+            complete[i] = last + S.join_us;
             end = std::max(end, complete[i]);
         }
         if (phase == five - 1) at_five = end;
@@ -979,15 +1020,15 @@ MuonParams params(const zero_muon* h, const zero_muon_hyper_t& hyper, double los
     return P;
 }
 
-int pass_grid(int64_t pieces) { return (int)std::max<int64_t>(1, std::min<int64_t>(pieces, kPassBlocks * kGb300Sms)); }
+int pass_grid(int64_t pieces, int per_sm) { return (int)std::max<int64_t>(1, std::min<int64_t>(pieces, per_sm * kGb300Sms)); }
 
 zero_status_t launch_reduce(const zero_muon* h, MuonParams P, cudaStream_t s)
 {
     if (h->chunks.empty()) return ZERO_OK;
     P.pieces = reinterpret_cast<const Piece*>(static_cast<char*>(h->workspace) + h->at_chunks);
     P.count = (int32_t)h->chunks.size();
-    const cudaError_t e = h->dtype16 == ZERO_BF16 ? launch_after(muon_reduce_kernel<ZERO_BF16>, pass_grid(P.count), kThreads, 0, s, P)
-                                                  : launch_after(muon_reduce_kernel<ZERO_FP16>, pass_grid(P.count), kThreads, 0, s, P);
+    const cudaError_t e = h->dtype16 == ZERO_BF16 ? launch_after(muon_reduce_kernel<ZERO_BF16>, pass_grid(P.count, kReduceBlocks), kThreads, 0, s, P)
+                                                  : launch_after(muon_reduce_kernel<ZERO_FP16>, pass_grid(P.count, kReduceBlocks), kThreads, 0, s, P);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
 }
 
@@ -1016,7 +1057,7 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
 {
     P.pieces = reinterpret_cast<const Piece*>(static_cast<char*>(h->workspace) + h->at_groups);
     P.count = (int32_t)h->groups.size();
-    const int grid = pass_grid(P.count);
+    const int grid = pass_grid(P.count, kStartBlocks);
     cudaError_t e = cudaSuccess;
     if (P.count > 0) {
         e = launch_after(muon_start_kernel, grid, kThreads, 0, s, P);
@@ -1169,7 +1210,7 @@ try {
         for (const Shape& S : kShapes) {
             std::vector<Piece> tiles;
             std::vector<int32_t> bounds;
-            const double us = deal_tiles(h.get(), S, &tiles, &bounds);
+            const double us = deal_tiles(h.get(), S, best, &tiles, &bounds);
             if (us >= best) continue;
             best = us;
             h->cg = S.cg;
@@ -1258,7 +1299,7 @@ try {
             T.ldm = (int32_t)up(m, kRowElems);
             T.wide = r <= c;
             T.at = at;
-            const Shape cut{h->cg, h->bn, 0.0};
+            const Shape cut{h->cg, h->bn, 0.0, 0.0, 0.0};
             T.tiles[0] = (int32_t)square_tiles(cut, m);
             T.tiles[1] = (int32_t)(tile_rows(cut, r) * tile_cols(cut, c));
             T.chunks = (int32_t)div_up(r * c, kChunk);
