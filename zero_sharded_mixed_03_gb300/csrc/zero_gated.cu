@@ -5,9 +5,9 @@
 // Both projections are one product on the tensor cores: half of a tile's columns are Wg's and half Wu's, at the same
 // place, so that x is staged once for both and a thread of the epilogue holds g and u of the same elements; h leaves
 // it without g and u having been to memory (they are written where the gradients will want them).  dx is one product
-// too, its inner dimension Wg's columns and then Wu's, and the weights' two gradients are tiles of one launch.
-// dg and du are formed by a pass of their own, as both products need them in two layouts and the biases' gradients
-// their sums.
+// too, its inner dimension Wg's columns and then Wu's; its tiles, those of the weights' two gradients and the sums of
+// the biases' are one launch, so that no round of tiles has to be full.  dg and du are formed by a pass of their own, as
+// the products need them in two layouts and the biases their sums.
 #include <cmath>
 #include <cstring>
 
@@ -20,18 +20,37 @@ namespace {
 __device__ uint32_t g_gated_error;
 
 // What a launch's tiles are.
-enum { kForward = 0, kInput = 1, kWeights = 2 };   // g and u; dx; dWg and dWu
+enum { kForward = 0, kBackward = 1 };   // g and u; dx, then dWg and dWu
+
+// One product of the backward pass.  dx (the first): a and b of both pairs, its inner blocks of the first and then the
+// second; a weight's gradient: the first of each.
+struct Product {
+    CUtensorMap a[2], b[2];
+    Matrix16 out;
+    int32_t tiles_m, tiles_n, k_blocks, k_first;
+    int32_t a_mn, b_mn;          // operand stored along its own rows instead of along K
+    uint32_t idesc;
+};
+
+// Tiles of two kinds dealt to w workers: every w-th of n1, then of n2 `more` to each of the first `ahead` workers (those
+// with one of the first kind more) and `rest` to each of the others, as even as that goes.
+struct Deal {
+    int32_t n1, n2, w, ahead, more, rest;
+};
 
 struct GatedParams {
-    CUtensorMap a[2], b[2];      // forward: x and -, Wg and Wu; dx: dg and du, Wg and Wu; weights: a and b of each
-    Matrix16 out[3];             // forward: h, g, u (p NULL: not kept); dx; dWg, dWu
+    Product part[3];             // forward: x, Wg and Wu (a[0], b[0], b[1]); backward: dx, dWg, dWu, those that are there
+    Matrix16 out[3];             // forward: h, g, u (p NULL: not kept)
     const uint16_t* bias[2];     // forward: of g and u, or NULL
-    int32_t count, tiles_m, tiles_n, per_problem;   // per_problem: tiles of one product
-    int32_t k_blocks, k_first;   // dx: inner blocks in all, and of the first pair
+    Deal deal;                   // backward: n1 tiles of dx (part[0]), n2 of the others
+    int32_t count;               // forward: tiles
+    int32_t parts_at;            // backward: the first part that is a weight's gradient: 1 after dx, or 0
     int32_t a_rows;              // rows of A that a copy brings (kBM, or fewer where A has no more)
-    int32_t a_mn, b_mn;          // operand stored along its own rows instead of along K
     int32_t act, accumulate, bias_vec;
-    uint32_t idesc;
+    // backward: the biases' gradients from the sums of `workers` workers, [worker][2][ld]
+    const float* sums;
+    uint16_t* db[2];
+    int64_t ld, workers, cols;
 };
 
 // g becomes act(g) u.
@@ -67,73 +86,129 @@ __device__ __forceinline__ void add_bias(float (&x)[32], const uint16_t* bias, b
     }
 }
 
+// One column's sum over the workers, eight at a time, in a fixed order.
+template <int DT>
+__device__ __forceinline__ void add_workers(const float* from, int64_t ld, int64_t workers, uint16_t* out, int accumulate)
+{
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t w = 0;
+    for (; w + 16 <= workers; w += 16) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = from[(w + j) * 2 * ld];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[j & 7] += v[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (w + j < workers) s[j & 7] += from[(w + j) * 2 * ld];
+    float x = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+    if (accumulate) x += widen1<DT>(*out);
+    *out = narrow1<DT>(x);
+}
+
 template <int CG, int BN, int MODE, int DT>
 struct GatedWork {
     const GatedParams& P;
     static constexpr int kBRows = BN / CG;
     struct Item {
-        int m, n, kb, problem;
+        int m, n, kb, part;
     };
     struct Ahead {};
     __device__ __forceinline__ void prepare(const Item&, int, int, int, int, Ahead&) const {}
+    static constexpr bool kScout = false;
+    __device__ __forceinline__ void done(const Item&, int) const {}
+
+    __device__ __forceinline__ void range(int worker, int workers, int& i, int& end, int& step) const
+    {
+        i = MODE == kForward ? worker : 0;
+        step = MODE == kForward ? workers : 1;
+        end = P.count;
+        if constexpr (MODE == kBackward) {
+            const Deal& D = P.deal;
+            const int n1 = worker < D.n1 ? (D.n1 - worker + D.w - 1) / D.w : 0;
+            // of the second kind: the places that it has, up to the last tile
+            const int first = worker < D.ahead ? worker : D.ahead * D.more + worker - D.ahead;
+            const int stride = worker < D.ahead ? D.ahead : D.w - D.ahead, most = worker < D.ahead ? D.more : D.rest;
+            end = n1 + (first < D.n2 ? min(most, (D.n2 - first + stride - 1) / stride) : 0);
+        }
+    }
 
     __device__ __forceinline__ Item item(int i) const
     {
         Item I;
-        I.problem = MODE == kWeights && i >= P.per_problem;
-        tile_at(P.tiles_m, P.tiles_n, I.problem ? i - P.per_problem : i, I.m, I.n);
-        I.kb = P.k_blocks;
+        I.part = 0;
+        int tile = i;
+        if constexpr (MODE == kBackward) {
+            const Deal& D = P.deal;
+            const int worker = blockIdx.x / CG, n1 = worker < D.n1 ? (D.n1 - worker + D.w - 1) / D.w : 0;
+            if (i < n1) {
+                tile = worker + i * D.w;
+            } else {
+                const int stride = worker < D.ahead ? D.ahead : D.w - D.ahead;
+                tile = (worker < D.ahead ? worker : D.ahead * D.more + worker - D.ahead) + (i - n1) * stride;
+                I.part = P.parts_at;
+                const int per = P.part[I.part].tiles_m * P.part[I.part].tiles_n;
+                if (tile >= per) {
+                    tile -= per;
+                    ++I.part;
+                }
+            }
+        }
+        const Product& Q = P.part[I.part];
+        tile_at(Q.tiles_m, Q.tiles_n, tile, I.m, I.n);
+        I.kb = Q.k_blocks;
         return I;
     }
-    __device__ __forceinline__ void range(int worker, int workers, int& i, int& end, int& step) const
+    __device__ __forceinline__ uint32_t bytes(const Item& I) const { return CG * ((P.part[I.part].a_mn ? kBM : P.a_rows) + kBRows) * (kBK * 2); }
+    __device__ __forceinline__ bool a_mn(const Item& I, int) const { return P.part[I.part].a_mn; }
+    __device__ __forceinline__ bool b_mn(const Item& I, int) const { return P.part[I.part].b_mn; }
+    __device__ __forceinline__ uint32_t idesc(const Item& I, int) const { return P.part[I.part].idesc; }
+
+    // ROWS rows of an operand: along K in one box, along its own rows in boxes of 64
+    template <int ROWS>
+    __device__ __forceinline__ static void bring(const CUtensorMap* map, bool mn, uint32_t at, int row, int k, uint32_t bar)
     {
-        i = worker;
-        end = P.count;
-        step = workers;
+        if (mn) {
+#pragma unroll
+            for (int i = 0; i < ROWS / 64; ++i) tma_load_2d<CG>(at + i * (kBK * 128), map, row + 64 * i, k, bar);
+        } else {
+            tma_load_2d<CG>(at, map, k, row, bar);
+        }
     }
-    static constexpr bool kScout = false;
-    __device__ __forceinline__ void done(const Item&, int) const {}
-    __device__ __forceinline__ uint32_t bytes(const Item&) const { return CG * (P.a_rows + kBRows) * (kBK * 2); }
-    __device__ __forceinline__ bool a_mn(const Item&, int) const { return MODE == kWeights; }
-    __device__ __forceinline__ bool b_mn(const Item&, int) const { return P.b_mn; }
-    __device__ __forceinline__ uint32_t idesc(const Item&, int) const { return P.idesc; }
 
     __device__ __forceinline__ void load(const Item& I, int kb, uint32_t a, uint32_t b, uint32_t bar, int rank) const
     {
+        const Product& Q = P.part[I.part];
         const int row_a = (I.m * CG + rank) * kBM;
-        int pair = I.problem;
-        if constexpr (MODE == kInput) {
-            if (kb >= P.k_first) {
-                pair = 1;
-                kb -= P.k_first;
-            }
-        }
-        const int k = kb * kBK;
-        if constexpr (MODE == kWeights) {
-            for (int i = 0; i < kBM / 64; ++i) tma_load_2d<CG>(a + i * (kBK * 128), &P.a[pair], row_a + 64 * i, k, bar);
-        } else {
-            tma_load_2d<CG>(a, &P.a[pair], k, row_a, bar);
-        }
-        if constexpr (MODE == kForward && CG == 2) {
-            // the pair's first block brings Wg's half of the columns and the second Wu's
-            const int row_b = I.n * kBRows;
-            const CUtensorMap* map = &P.b[rank];
-            if (P.b_mn) {
-                for (int i = 0; i < kBRows / 64; ++i) tma_load_2d<CG>(b + i * (kBK * 128), map, row_b + 64 * i, k, bar);
+        if constexpr (MODE == kForward) {
+            const int k = kb * kBK;
+            bring<kBM>(&Q.a[0], false, a, row_a, k, bar);
+            if constexpr (CG == 2) {
+                // the pair's first block brings Wg's half of the columns and the second Wu's
+                bring<kBRows>(&Q.b[rank], Q.b_mn, b, I.n * kBRows, k, bar);
             } else {
-                tma_load_2d<CG>(b, map, k, row_b, bar);
-            }
-        } else if constexpr (MODE == kForward) {
-            for (int i = 0; i < 2; ++i) {
-                if (P.b_mn) tma_load_2d<CG>(b + i * (kBK * 128), &P.b[i], I.n * 64, k, bar);
-                else tma_load_2d<CG>(b + i * (64 * kBK * 2), &P.b[i], k, I.n * 64, bar);
+                for (int i = 0; i < 2; ++i) bring<64>(&Q.b[i], Q.b_mn, b + i * (64 * kBK * 2), I.n * 64, k, bar);
             }
         } else {
-            const int row_b = I.n * BN + rank * kBRows;
-            if (P.b_mn) {
-                for (int i = 0; i < kBRows / 64; ++i) tma_load_2d<CG>(b + i * (kBK * 128), &P.b[pair], row_b + 64 * i, k, bar);
-            } else {
-                tma_load_2d<CG>(b, &P.b[pair], k, row_b, bar);
+            const bool second = kb >= Q.k_first;
+            const int pair = second ? 1 : 0, k = (second ? kb - Q.k_first : kb) * kBK;
+            bring<kBM>(&Q.a[pair], Q.a_mn, a, row_a, k, bar);
+            bring<kBRows>(&Q.b[pair], Q.b_mn, b, I.n * BN + rank * kBRows, k, bar);
+        }
+    }
+
+    // The biases' gradients: 32 columns of one of them a warp, the workers' sums in a fixed order, in fp32.
+    __device__ __forceinline__ void aside(int lane) const
+    {
+        if constexpr (MODE == kBackward) {
+            if (!P.sums) return;
+            const int64_t parts = (P.cols + 31) / 32;
+            for (int64_t i = blockIdx.x; i < 2 * parts; i += gridDim.x) {
+                const int which = i >= parts;
+                const int64_t c = (i - which * parts) * 32 + lane;
+                uint16_t* db = P.db[which];
+                if (db && c < P.cols) add_workers<DT>(P.sums + which * P.ld + c, P.ld, P.workers, db + c, P.accumulate);
             }
         }
     }
@@ -158,13 +233,14 @@ struct GatedWork {
                 put_tile<DT>(stage, lane, g, H, row0, col0);
             }
         } else {
-            const Matrix16& D = P.out[I.problem];
+            const Matrix16& D = P.part[I.part].out;
+            const bool add = P.accumulate && I.part >= P.parts_at;
             for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
                 const int64_t col0 = (int64_t)I.n * BN + c;
                 if (col0 >= D.cols || row0 >= D.rows) break;
                 float x[32];
                 tmem_load32(acc + c, x);
-                if (MODE == kWeights && P.accumulate) add_tile<DT>(stage + kTile16Bytes, lane, 1.0f, x, D, row0, col0);
+                if (add) add_tile<DT>(stage + kTile16Bytes, lane, 1.0f, x, D, row0, col0);
                 put_tile<DT>(stage, lane, x, D, row0, col0);
             }
         }
@@ -323,30 +399,14 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ S
     q[1] = make_float4(su[4], su[5], su[6], su[7]);
 }
 
-// Sums over the workers, in a fixed order, in fp32: 32 columns by 8 workers at a time; the second half of the grid
-// is du's.
+// The biases' gradients where no product is asked for.
 template <int DT>
-__global__ void __launch_bounds__(256) gated_bias_kernel(const float* sums, int64_t ld, int64_t workers, int64_t cols,
-                                                         uint16_t* db_gate, uint16_t* db_up, int accumulate)
+__global__ void __launch_bounds__(128) gated_bias_kernel(const __grid_constant__ GatedParams P)
 {
     after_earlier_work();
-    __shared__ float part[8][33];
-    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    uint16_t* out = blockIdx.y ? db_up : db_gate;
-    const float* from = sums + blockIdx.y * ld;
-    float s = 0.0f;
-    if (c < cols && out) {
-#pragma unroll 8
-        for (int64_t w = threadIdx.y; w < workers; w += 8) s += from[w * 2 * ld + c];
-    }
-    part[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y != 0 || c >= cols || !out) return;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
-    if (accumulate) s += widen1<DT>(out[c]);
-    out[c] = narrow1<DT>(s);
+    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    uint16_t* db = P.db[blockIdx.y];
+    if (db && c < P.cols) add_workers<DT>(P.sums + blockIdx.y * P.ld + c, P.ld, P.workers, db + c, P.accumulate);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -523,33 +583,32 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewResident) gated_few_deep_k
 
 // ------------------------------------------------------------------ host
 
-// The shape of a product's tiles: 256 x 256 on a pair of SMs, an inner block of which takes 0.336 us (94 % of the tensor
-// cores' measured rate), or 128 x 128 on one (0.29, what the loads into an SM take), whichever is sooner done.
+// The shape of the tiles: 256 x 256 on a pair of SMs, an inner block of which takes 0.31 us, or 128 x 128 on one, 0.23,
+// whichever is sooner done.
 struct Shape {
-    int cg = 2, bn = 256;
-    int64_t tiles_m = 0, tiles_n = 0;
+    int cg, bn;
+    double block_us;
+    int workers() const { return kGb300Sms / cg; }
+    int64_t rows(int64_t m) const { return div_up(m, kBM * cg); }
+    int64_t cols(int64_t n) const { return div_up(n, bn); }
 };
+constexpr Shape kShapes[] = {{2, 256, 0.31}, {1, 128, 0.23}};
 
-Shape choose_shape(int64_t M, int64_t N, int64_t products)
+// n1 tiles of k1 inner blocks and n2 of k2 dealt so that the worker with most has least; *blocks: what it has.
+Deal deal_out(const Shape& S, int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t* blocks)
 {
-    Shape best;
-    double best_us = 1e30;
-    static const struct {
-        int cg, bn;
-        double block_us;
-    } shapes[] = {{2, 256, 0.336}, {1, 128, 0.29}};
-    for (const auto& c : shapes) {
-        Shape s;
-        s.cg = c.cg;
-        s.bn = c.bn;
-        s.tiles_m = div_up(M, kBM * c.cg);
-        s.tiles_n = div_up(N, c.bn);
-        const double us = div_up(products * s.tiles_m * s.tiles_n, kGb300Sms / c.cg) * c.block_us;
-        if (us < best_us) {
-            best_us = us;
-            best = s;
-        }
+    const int64_t w = std::min<int64_t>(S.workers(), std::max<int64_t>(1, n1 + n2)), q = n1 / w, ahead = n1 % w;
+    Deal best{(int32_t)n1, (int32_t)n2, (int32_t)w, (int32_t)ahead, 0, 0};
+    int64_t least = INT64_MAX;
+    for (int64_t more = 0; more <= div_up(n2, w); ++more) {
+        const int64_t left = std::max<int64_t>(0, n2 - more * ahead), rest = div_up(left, w - ahead);
+        const int64_t most = std::max(ahead > 0 ? (q + 1) * k1 + more * k2 : 0, q * k1 + rest * k2);
+        if (most >= least) continue;
+        least = most;
+        best.more = (int32_t)more;
+        best.rest = (int32_t)rest;
     }
+    *blocks = least;
     return best;
 }
 
@@ -559,7 +618,7 @@ zero_status_t launch_gated(const GatedParams& P, cudaStream_t s)
     using S = GemmShape<CG, BN>;
     const cudaError_t set = allow_shared<gated_kernel<CG, BN, MODE, DT>>(S::kSmem);
     if (set != cudaSuccess) return cuda_fail(set, "zero_gated: shared memory");
-    const int grid = CG * (int)std::min<int64_t>(kGb300Sms / CG, P.count);
+    const int grid = CG * (MODE == kForward ? (int)std::min<int64_t>(kGb300Sms / CG, P.count) : P.deal.w);
     const cudaError_t e = launch_after(gated_kernel<CG, BN, MODE, DT>, grid, kGemmThreads, S::kSmem, s, P);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
 }
@@ -844,19 +903,28 @@ try {
     plan_copies(L, static_cast<char*>(workspace), operand, &S);
     st = launch_split(L, S, s);
     if (st != ZERO_OK) return st;
-    const Shape c = choose_shape(a.rows, 2 * a.out_features, 1);
+    Shape c = kShapes[0];
+    double best = 1e30;
+    for (const Shape& S : kShapes) {
+        const double us = (double)div_up(S.rows(a.rows) * S.cols(2 * a.out_features), S.workers()) * S.block_us;
+        if (us < best) {
+            best = us;
+            c = S;
+        }
+    }
+    Product& Q = P.part[0];
     // few rows: no zeros are copied for the rest, whose results are not stored
     P.a_rows = c.cg == 1 && a.rows < kBM ? (int32_t)up(a.rows, 8) : kBM;
-    st = encode(&P.a[0], Operand{operand[0], a.rows, a.in_features, L.ld8[0], false}, a.dtype16, P.a_rows, "zero_gated");
+    st = encode(&Q.a[0], Operand{operand[0], a.rows, a.in_features, L.ld8[0], false}, a.dtype16, P.a_rows, "zero_gated");
     for (int i = 0; i < 2 && st == ZERO_OK; ++i)
-        st = encode(&P.b[i], Operand{operand[1 + i], a.out_features, a.in_features, L.ld8[1 + i], in_out}, a.dtype16, c.cg == 2 ? kBM : kBM / 2, "zero_gated");
+        st = encode(&Q.b[i], Operand{operand[1 + i], a.out_features, a.in_features, L.ld8[1 + i], in_out}, a.dtype16, c.cg == 2 ? kBM : kBM / 2, "zero_gated");
     if (st != ZERO_OK) return st;
-    P.tiles_m = (int32_t)c.tiles_m;
-    P.tiles_n = (int32_t)div_up(a.out_features, c.bn / 2);
-    P.count = P.per_problem = P.tiles_m * P.tiles_n;
-    P.k_blocks = (int32_t)div_up(a.in_features, kBK);
-    P.b_mn = in_out;
-    P.idesc = product_desc(L.bf, false, in_out, c);
+    Q.tiles_m = (int32_t)c.rows(a.rows);
+    Q.tiles_n = (int32_t)div_up(a.out_features, c.bn / 2);
+    Q.k_blocks = (int32_t)div_up(a.in_features, kBK);
+    Q.b_mn = in_out;
+    Q.idesc = product_desc(L.bf, false, in_out, c);
+    P.count = Q.tiles_m * Q.tiles_n;
     return launch_gated<kForward>(P, c, L.bf, s);
 }
 catch (...) {
@@ -910,65 +978,70 @@ try {
     }
     st = launch_split(L, S, s);
     if (st != ZERO_OK) return st;
+    GatedParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.accumulate = accumulate;
     if (L.make_sums) {
-        const dim3 grid((unsigned)div_up(n, 32), 2), threads(32, 8);
-        uint16_t *dbg = static_cast<uint16_t*>(a.db_gate), *dbu = static_cast<uint16_t*>(a.db_up);
-        const cudaError_t e = L.bf ? launch_after(gated_bias_kernel<ZERO_BF16>, grid, threads, 0, s, sums, L.ld_d, L.cut.workers, n, dbg, dbu, (int)accumulate)
-                                   : launch_after(gated_bias_kernel<ZERO_FP16>, grid, threads, 0, s, sums, L.ld_d, L.cut.workers, n, dbg, dbu, (int)accumulate);
-        if (e != cudaSuccess) return cuda_fail(e, "zero_gated_backward: launch");
+        P.sums = sums;
+        P.db[0] = static_cast<uint16_t*>(a.db_gate);
+        P.db[1] = static_cast<uint16_t*>(a.db_up);
+        P.ld = L.ld_d;
+        P.workers = L.cut.workers;
+        P.cols = n;
     }
-    if (!L.make_d) return ZERO_OK;
-    const Operand dg{ws + L.at_dg, m, n, L.ld_d, false}, du{ws + L.at_du, m, n, L.ld_d, false};
+    if (!L.make_d) {
+        if (!L.make_sums) return ZERO_OK;
+        const dim3 grid((unsigned)div_up(n, 128), 2);
+        const cudaError_t e = L.bf ? launch_after(gated_bias_kernel<ZERO_BF16>, grid, 128, 0, s, P) : launch_after(gated_bias_kernel<ZERO_FP16>, grid, 128, 0, s, P);
+        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated_backward: launch");
+    }
+    // dx, then the weights' gradients that are asked for
+    const int weights = (a.dw_gate != nullptr) + (a.dw_up != nullptr);
+    const int64_t kb_n = div_up(n, kBK), kb_m = div_up(m, kBK);
+    Shape c = kShapes[0];
+    double best = 1e30;
+    for (const Shape& S : kShapes) {
+        int64_t blocks = 0;
+        const Deal D = deal_out(S, a.dx ? S.rows(m) * S.cols(k) : 0, 2 * kb_n, weights * S.rows(L.w_rows) * S.cols(L.w_cols), kb_m, &blocks);
+        if (blocks * S.block_us >= best) continue;
+        best = blocks * S.block_us;
+        c = S;
+        P.deal = D;
+    }
+    P.a_rows = c.cg == 1 && m < kBM ? (int32_t)up(m, 8) : kBM;
+    const Operand d[2] = {{ws + L.at_dg, m, n, L.ld_d, false}, {ws + L.at_du, m, n, L.ld_d, false}};
+    int part = 0;
     if (a.dx) {
-        const Shape c = choose_shape(m, k, 1);
-        GatedParams P;
-        std::memset(&P, 0, sizeof(P));
-        P.out[0] = matrix(a.dx, a.ld_dx, m, k);
-        P.a_rows = c.cg == 1 && m < kBM ? (int32_t)up(m, 8) : kBM;
-        const Operand* d[2] = {&dg, &du};
+        Product& Q = P.part[part++];
+        Q.out = matrix(a.dx, a.ld_dx, m, k);
         for (int i = 0; i < 2 && st == ZERO_OK; ++i) {
-            st = encode(&P.a[i], *d[i], a.dtype16, P.a_rows, "zero_gated_backward");
-            if (st == ZERO_OK) st = encode(&P.b[i], Operand{operand[1 + i], k, n, L.ld8[1 + i], out_in}, a.dtype16, c.bn / c.cg, "zero_gated_backward");
+            st = encode(&Q.a[i], d[i], a.dtype16, P.a_rows, "zero_gated_backward");
+            if (st == ZERO_OK) st = encode(&Q.b[i], Operand{operand[1 + i], k, n, L.ld8[1 + i], out_in}, a.dtype16, c.bn / c.cg, "zero_gated_backward");
         }
-        if (st != ZERO_OK) return st;
-        P.tiles_m = (int32_t)c.tiles_m;
-        P.tiles_n = (int32_t)c.tiles_n;
-        P.count = P.per_problem = P.tiles_m * P.tiles_n;
-        P.k_first = (int32_t)div_up(n, kBK);
-        P.k_blocks = 2 * P.k_first;
-        P.b_mn = out_in;
-        P.idesc = product_desc(L.bf, false, out_in, c);
-        st = launch_gated<kInput>(P, c, L.bf, s);
-        if (st != ZERO_OK) return st;
+        Q.tiles_m = (int32_t)c.rows(m);
+        Q.tiles_n = (int32_t)c.cols(k);
+        Q.k_first = (int32_t)kb_n;
+        Q.k_blocks = 2 * Q.k_first;
+        Q.b_mn = out_in;
+        Q.idesc = product_desc(L.bf, false, out_in, c);
     }
-    if (a.dw_gate || a.dw_up) {
-        GatedParams P;
-        std::memset(&P, 0, sizeof(P));
-        const int problems = (a.dw_gate != nullptr) + (a.dw_up != nullptr);
-        const Shape c = choose_shape(L.w_rows, L.w_cols, problems);
-        const Operand x{operand[0], k, m, L.ld8[0], true};
-        int i = 0;
-        for (int which = 0; which < 2; ++which) {
-            void* dw = which ? a.dw_up : a.dw_gate;
-            if (!dw) continue;
-            const Operand z{ws + (which ? L.at_du : L.at_dg), n, m, L.ld_d, true};
-            P.out[i] = matrix(dw, which ? a.ld_dw_up : a.ld_dw_gate, L.w_rows, L.w_cols);
-            st = encode(&P.a[i], out_in ? z : x, a.dtype16, kBM, "zero_gated_backward");
-            if (st == ZERO_OK) st = encode(&P.b[i], out_in ? x : z, a.dtype16, kBM, "zero_gated_backward");
-            if (st != ZERO_OK) return st;
-            ++i;
-        }
-        P.a_rows = kBM;
-        P.tiles_m = (int32_t)c.tiles_m;
-        P.tiles_n = (int32_t)c.tiles_n;
-        P.per_problem = P.tiles_m * P.tiles_n;
-        P.count = problems * P.per_problem;
-        P.k_blocks = (int32_t)div_up(m, kBK);
-        P.b_mn = 1;
-        P.accumulate = accumulate;
-        P.idesc = product_desc(L.bf, true, true, c);
-        st = launch_gated<kWeights>(P, c, L.bf, s);
+    P.parts_at = part;
+    const Operand x{operand[0], k, m, L.ld8[0], true};
+    for (int which = 0; which < 2 && st == ZERO_OK; ++which) {
+        void* dw = which ? a.dw_up : a.dw_gate;
+        if (!dw) continue;
+        Product& Q = P.part[part++];
+        const Operand z{d[which].p, n, m, L.ld_d, true};
+        Q.out = matrix(dw, which ? a.ld_dw_up : a.ld_dw_gate, L.w_rows, L.w_cols);
+        st = encode(&Q.a[0], out_in ? z : x, a.dtype16, kBM, "zero_gated_backward");
+        if (st == ZERO_OK) st = encode(&Q.b[0], out_in ? x : z, a.dtype16, kBM, "zero_gated_backward");
+        Q.tiles_m = (int32_t)c.rows(L.w_rows);
+        Q.tiles_n = (int32_t)c.cols(L.w_cols);
+        Q.k_blocks = Q.k_first = (int32_t)kb_m;
+        Q.a_mn = Q.b_mn = 1;
+        Q.idesc = product_desc(L.bf, true, true, c);
     }
+    if (st == ZERO_OK) st = launch_gated<kBackward>(P, c, L.bf, s);
     return st;
 }
 catch (...) {

@@ -251,6 +251,7 @@ struct GemmShape {
 //   range(worker, workers, i, end, step)    the tiles of a block or pair
 //   Item item(int)                          where a tile is; Item::kb: its inner blocks, at least one
 //   uint32_t bytes(Item)                    what a stage's copies bring, to both blocks of a pair
+//   aside(lane)                             without a scout: what that warp does
 //   kScout, bool begin(Item, Seen&)         true: a warp of its own finds the items and waits for what they wait for
 //                                           (false: given up), ahead of the others, which take them from a queue
 //   load(Item, kb, a, b, bar, rank)      those copies
@@ -422,9 +423,11 @@ struct Tiles {
                     mma_commit<CG>(acc_full0 + 8 * acc);
                 }
             }
-        } else if (W::kScout && warp == 3) {
+        } else if (warp == 3) {
             // ---- scout: one thread
-            if constexpr (W::kScout) {
+            if constexpr (!W::kScout) {
+                work.aside(lane);
+            } else {
                 if (lane == 0) {
                     typename W::Seen seen = {};
                     uint32_t tile = 0;

@@ -380,10 +380,10 @@ struct ProductParams {
     Op ops[kMaxPhases];          // ops[i - first] is product i
 };
 
-__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p)
+__device__ __forceinline__ uint32_t load_relaxed(const uint32_t* p)
 {
     uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
 
@@ -466,13 +466,13 @@ struct MuonWork {
         return I;
     }
 
-    // Until every part of the product before is stored: a bounded wait.
+    // Until every part of the product before is stored: a bounded wait.  A fence follows it.
     __device__ __forceinline__ static bool wait_before(const Item& I)
     {
-        if (!I.before || load_acquire(I.before) >= I.want) return true;
+        if (!I.before || load_relaxed(I.before) >= I.want) return true;
         const uint64_t t0 = global_ns();
         for (uint32_t i = 0; i < kWaitIterCap; ++i) {
-            if (load_acquire(I.before) >= I.want) return true;
+            if (load_relaxed(I.before) >= I.want) return true;
             if (i % 16 == 15 && global_ns() - t0 > kGemmWaitNs) break;
         }
         return false;
@@ -503,17 +503,17 @@ struct MuonWork {
         for (; use; use &= use - 1) see(I.maps + (__ffs(use) - 1));
         if (I.before != S.before) {
             if (!wait_before(I)) return false;
-            // what other blocks' copies wrote is read by copies from here on
-            asm volatile("fence.proxy.async;" ::: "memory");
+            // with the writers' releases: what their copies wrote is read here, by loads and by copies
+            asm volatile("fence.acq_rel.gpu;\n\tfence.proxy.async;" ::: "memory");
             S.before = I.before;
         }
         return true;
     }
-    // Lane 0 has sent the warp's tiles: once they are written, one release of them all.
+    // Lane 0 has sent the warp's tiles: once they are written, and so visible to it, one release of them all.
     __device__ __forceinline__ void done(const Item& I, int lane) const
     {
         sent_all(lane);
-        if (lane == 0) asm volatile("fence.proxy.async;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
+        if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
     }
 
     // Is an inner block below the diagonal block (kBM * CG wide) of a symmetric operand's rows from `row` on?
