@@ -847,7 +847,8 @@ zero_status_t zero_muon_bind(zero_muon_t* h, float* const* params, void* const* 
 
 /* One step over every matrix.  Where the sum of squares of a matrix's u is not finite (a contribution is not, or fp32's
  * range is left) the whole step is left out: parameters, copies, updates and the current momentum stay.  ZERO_ERANGE
- * for coefficients that let singular values of at most 1 grow beyond 8. */
+ * for coefficients that let singular values of at most 1 grow beyond 8, or a step's polynomial of them beyond 16384.
+ * The products are one cooperative launch, whose blocks (up to one on each SM) run when all of them can. */
 zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, double loss_scale, void* stream);
 
 /* A step that h makes together with a plan's, applied or left out as one, with the plan's loss scale (as

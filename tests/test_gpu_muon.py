@@ -359,6 +359,41 @@ def test_streams_graphs_and_repeats():
         mu.close()
 
 
+def test_more_matrices_and_contributions():
+    """More matrices than a block keeps marks of, and the most contributions."""
+    for shapes, n_d in (([(40 + i % 7, 90 - i % 11) for i in range(70)], 2), ([(150, 130 + i) for i in range(66)], 1),
+                        ([(33, 47), (130, 256)], 128)):
+        mu = Muon(shapes, n_d).fill(n_d)
+        check(mu, Z.muon_hyper())
+        mu.close()
+
+
+def test_calls_at_once():
+    """Two optimizers and a linear layer's products on three streams."""
+    shapes = [(700, 900), (260, 1300)]
+    hyper = Z.muon_hyper(lr=0.01)
+    alone, first, second = (Muon(shapes, 2, "bf16").fill(11) for _ in range(3))
+    for _ in range(4):
+        alone.step(hyper)
+    x, w, y = (torch.randn(1024, 1024, device="cuda").bfloat16() for _ in range(3))
+    args = Z.zero_linear_t(rows=1024, in_features=1024, out_features=1024, dtype16=Z.ZERO_BF16,
+                           layout=Z.ZERO_WEIGHT_OUT_IN, x=x.data_ptr(), w=w.data_ptr(), y=y.data_ptr())
+    n = Z.zero_linear_workspace(args)
+    ws = torch.empty(max(16, n), dtype=torch.uint8, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        Z.zero_muon_step(first.h, hyper, 1.0, streams[0].cuda_stream)
+        Z.zero_linear(args, ws.data_ptr(), n, streams[2].cuda_stream)
+        Z.zero_muon_step(second.h, hyper, 1.0, streams[1].cuda_stream)
+    torch.cuda.synchronize()
+    for other in (first, second):
+        assert all(torch.equal(a, b) for a, b in zip(alone.p + alone.halves, other.p + other.halves))
+    Z.zero_operators_check(stream())
+    for mu in (alone, first, second):
+        mu.close()
+
+
 def test_no_matrices():
     mu = Muon([(0, 4)])
     assert mu.step(Z.muon_hyper()).t == 1

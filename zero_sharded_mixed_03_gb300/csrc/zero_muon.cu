@@ -980,7 +980,7 @@ zero_status_t check_hyper(const zero_muon* h, const zero_muon_hyper_t* hyper, Ra
     for (int k = 0; k < hyper->steps; ++k)
         for (int j = 0; j < 3; ++j)
             if (!std::isfinite(hyper->coefficients[k][j])) return fail(ZERO_EINVAL, w + "a coefficient is not finite");
-    if (!find_range(*hyper, h && h->pair, range)) return fail(ZERO_ERANGE, w + "the coefficients let singular values of at most 1 grow beyond 8");
+    if (!find_range(*hyper, h && h->pair, range)) return fail(ZERO_ERANGE, w + "the coefficients let singular values of at most 1 grow beyond 8, or a polynomial of them beyond 16384");
     return ZERO_OK;
 }
 
