@@ -178,9 +178,21 @@ def test_backward(m, k, n, layout):
 
 
 @pytest.mark.parametrize("layout", ["out_in", "in_out"])
+@pytest.mark.parametrize("m,k,n", [(40, 4096, 72), (130, 5000, 130), (300, 96, 5000), (129, 70, 6400), (4000, 72, 136),
+                                   (2500, 130, 64), (6000, 64, 2000)])
+def test_few_tiles_and_a_long_sum(m, k, n, layout):
+    """Parts of the inner dimension as tiles of their own, of one product or of two; narrow and wide columns' sums."""
+    for pad in (0, 8, 3):
+        b = Block(m, k, n, "bf16", layout, pad=pad, seed=k)
+        b.check_forward()
+        b.check_backward()
+    b.check_backward(accumulate=True)
+
+
+@pytest.mark.parametrize("layout", ["out_in", "in_out"])
 def test_whole_numbers_are_exact(layout):
     for act in ("none", "relu"):
-        for m, k, n in ((1, 64, 72), (2, 512, 64), (200, 96, 300), (513, 64, 520)):
+        for m, k, n in ((1, 64, 72), (2, 512, 64), (200, 96, 300), (513, 64, 520), (130, 64, 4000)):
             b = Block(m, k, n, "bf16", layout, act, whole=True, seed=k)
             b.check_forward(exact=k <= 64)
             b = Block(m, k, n, "bf16", layout, act, whole=True, seed=k)      # dg, du: whole numbers of at most 4

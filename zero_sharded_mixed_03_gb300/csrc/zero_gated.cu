@@ -7,7 +7,8 @@
 // it without g and u having been to memory (they are written where the gradients will want them).  dx is one product
 // too, its inner dimension Wg's columns and then Wu's; its tiles, those of the weights' two gradients and the sums of
 // the biases' are one launch, so that no round of tiles has to be full.  dg and du are formed by a pass of their own, as
-// the products need them in two layouts and the biases their sums.
+// the products need them in two layouts and the biases their sums.  Where there are few tiles and a long inner
+// dimension, parts of it are tiles of their own, summed in order by the warp that ends last.
 #include <cmath>
 #include <cstring>
 
@@ -28,6 +29,8 @@ struct Product {
     CUtensorMap a[2], b[2];
     Matrix16 out;
     int32_t tiles_m, tiles_n, k_blocks, k_first;
+    int32_t splits, k_per_split; // parts of the inner dimension, and the inner blocks of one (the last may have fewer)
+    int32_t tile0, part0;        // of the products in parts: the tiles, and the parts, before this product's
     int32_t a_mn, b_mn;          // operand stored along its own rows instead of along K
     uint32_t idesc;
 };
@@ -38,12 +41,15 @@ struct Deal {
     int32_t n1, n2, w, ahead, more, rest;
 };
 
+template <int MODE>
 struct GatedParams {
-    Product part[3];             // forward: x, Wg and Wu (a[0], b[0], b[1]); backward: dx, dWg, dWu, those that are there
+    Product part[MODE == kForward ? 1 : 3];   // forward: x, Wg and Wu (a[0], b[0], b[1]); backward: dx, dWg, dWu, those that are there
     Matrix16 out[3];             // forward: h, g, u (p NULL: not kept)
     const uint16_t* bias[2];     // forward: of g and u, or NULL
-    Deal deal;                   // backward: n1 tiles of dx (part[0]), n2 of the others
-    int32_t count;               // forward: tiles
+    Deal deal;                   // backward: n1 tiles of dx (part[0]), n2 of the others, parts counted each
+    int32_t count;               // forward: tiles, parts counted each
+    float4* partial;             // a part's sums: [tile][part][warp][..]
+    uint32_t* tickets;           // [tile][warp]: parts that are there; 0 at first
     int32_t parts_at;            // backward: the first part that is a weight's gradient: 1 after dx, or 0
     int32_t a_rows;              // rows of A that a copy brings (kBM, or fewer where A has no more)
     int32_t act, accumulate, bias_vec;
@@ -72,50 +78,102 @@ __device__ __forceinline__ void gate_values(float (&g)[32], const float (&u)[32]
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void add_bias(float (&x)[32], const uint16_t* bias, bool vec, int64_t col0, int64_t cols)
+// 32 columns of a bias from col0 on, packed; zeros past the last and without one.
+__device__ __forceinline__ void fetch_bias(uint4 (&v)[4], const uint16_t* bias, bool vec, int64_t col0, int64_t cols)
 {
-    if (!bias) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int n = (int)max((int64_t)0, min((int64_t)8, cols - col0 - 8 * i));
-        float b[8];
-        load8<DT>(bias + col0 + 8 * i, vec, n, b);
+        const int n = bias ? (int)max((int64_t)0, min((int64_t)8, cols - col0 - 8 * i)) : 0;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (n == 8 && vec) {
+            v[i] = *reinterpret_cast<const uint4*>(bias + col0 + 8 * i);
+        } else if (n > 0) {
+            const uint16_t* p = bias + col0 + 8 * i;
+            uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[8 * i + j] += b[j];
+            for (int j = 0; j < 4; ++j) w[j] = (2 * j < n ? p[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)p[2 * j + 1] : 0u) << 16);
+            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
-// One column's sum over the workers, eight at a time, in a fixed order.
 template <int DT>
-__device__ __forceinline__ void add_workers(const float* from, int64_t ld, int64_t workers, uint16_t* out, int accumulate)
+__device__ __forceinline__ void add_bias(float (&x)[32], const uint4 (&v)[4])
 {
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    int64_t w = 0;
-    for (; w + 16 <= workers; w += 16) {
-        float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = from[(w + j) * 2 * ld];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[j & 7] += v[j];
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            widen2<DT>(word(v[i], j), a, b);
+            x[8 * i + 2 * j] += a;
+            x[8 * i + 2 * j + 1] += b;
+        }
+}
+
+// Sums over the workers of 32 columns from c0 on, by a warp: eight lanes of four columns each, each eight a quarter of
+// the workers, in a fixed order.
+template <int DT>
+__device__ __forceinline__ void add_workers(const float* sums, int64_t ld, int64_t workers, int64_t c0, int64_t cols, uint16_t* out, int accumulate, int lane)
+{
+    if (!out) return;
+    const int64_t c = c0 + (lane & 7) * 4;
+    const bool mine = c < cols;                  // rows of a multiple of eight: four columns are there, or none
+    float4 s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int64_t w = lane >> 3; mine && w < workers; w += 32) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = w + 4 * j < workers ? *reinterpret_cast<const float4*>(sums + (w + 4 * j) * 2 * ld + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            s[j & 3].x += v[j].x;
+            s[j & 3].y += v[j].y;
+            s[j & 3].z += v[j].z;
+            s[j & 3].w += v[j].w;
+        }
     }
+    float x[4] = {(s[0].x + s[1].x) + (s[2].x + s[3].x), (s[0].y + s[1].y) + (s[2].y + s[3].y), (s[0].z + s[1].z) + (s[2].z + s[3].z),
+                  (s[0].w + s[1].w) + (s[2].w + s[3].w)};
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if (w + j < workers) s[j & 7] += from[(w + j) * 2 * ld];
-    float x = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-    if (accumulate) x += widen1<DT>(*out);
-    *out = narrow1<DT>(x);
+    for (int o = 8; o < 32; o *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += __shfl_xor_sync(0xFFFFFFFFu, x[j], o);
+    if (lane >= 8) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (c + j >= cols) break;
+        if (accumulate) x[j] += widen1<DT>(out[c + j]);
+        out[c + j] = narrow1<DT>(x[j]);
+    }
 }
 
 template <int CG, int BN, int MODE, int DT>
 struct GatedWork {
-    const GatedParams& P;
+    const GatedParams<MODE>& P;
     static constexpr int kBRows = BN / CG;
     struct Item {
         int m, n, kb, part;
+        int k0, slice, tile;     // the first inner block; which part; its tile among those in parts
     };
-    struct Ahead {};
-    __device__ __forceinline__ void prepare(const Item&, int, int, int, int, Ahead&) const {}
+    // The biases of a tile's first part are loaded while its products run.
+    struct Ahead {
+        uint4 bias[MODE == kForward ? 2 : 1][4];
+    };
+    __device__ __forceinline__ void biases(const Item& I, int c, Ahead& A) const
+    {
+        if constexpr (MODE == kForward) {
+            const int64_t col0 = (int64_t)I.n * (BN / 2) + c;
+            fetch_bias(A.bias[0], P.bias[0], P.bias_vec & 1, col0, P.out[0].cols);
+            fetch_bias(A.bias[1], P.bias[1], P.bias_vec & 2, col0, P.out[0].cols);
+        }
+    }
+    __device__ __forceinline__ void prepare(const Item& I, int, int half, int, int, Ahead& A) const
+    {
+        if (P.bias[0] || P.bias[1]) biases(I, half * kEpiCols, A);
+    }
     static constexpr bool kScout = false;
     __device__ __forceinline__ void done(const Item&, int) const {}
 
@@ -148,7 +206,7 @@ struct GatedWork {
                 const int stride = worker < D.ahead ? D.ahead : D.w - D.ahead;
                 tile = (worker < D.ahead ? worker : D.ahead * D.more + worker - D.ahead) + (i - n1) * stride;
                 I.part = P.parts_at;
-                const int per = P.part[I.part].tiles_m * P.part[I.part].tiles_n;
+                const int per = P.part[I.part].tiles_m * P.part[I.part].tiles_n * P.part[I.part].splits;
                 if (tile >= per) {
                     tile -= per;
                     ++I.part;
@@ -156,8 +214,15 @@ struct GatedWork {
             }
         }
         const Product& Q = P.part[I.part];
+        I.slice = 0;
+        if (Q.splits > 1) {
+            I.slice = tile % Q.splits;
+            tile /= Q.splits;
+        }
+        I.tile = Q.tile0 + tile;
         tile_at(Q.tiles_m, Q.tiles_n, tile, I.m, I.n);
-        I.kb = Q.k_blocks;
+        I.k0 = I.slice * Q.k_per_split;
+        I.kb = min(Q.k_blocks - I.k0, Q.k_per_split);
         return I;
     }
     __device__ __forceinline__ uint32_t bytes(const Item& I) const { return CG * ((P.part[I.part].a_mn ? kBM : P.a_rows) + kBRows) * (kBK * 2); }
@@ -181,6 +246,7 @@ struct GatedWork {
     {
         const Product& Q = P.part[I.part];
         const int row_a = (I.m * CG + rank) * kBM;
+        kb += I.k0;
         if constexpr (MODE == kForward) {
             const int k = kb * kBK;
             bring<kBM>(&Q.a[0], false, a, row_a, k, bar);
@@ -198,7 +264,8 @@ struct GatedWork {
         }
     }
 
-    // The biases' gradients: 32 columns of one of them a warp, the workers' sums in a fixed order, in fp32.
+    // The biases' gradients: 32 columns of one of them a warp, four a lane and every fourth worker; the workers' sums in
+    // a fixed order, in fp32.
     __device__ __forceinline__ void aside(int lane) const
     {
         if constexpr (MODE == kBackward) {
@@ -206,40 +273,103 @@ struct GatedWork {
             const int64_t parts = (P.cols + 31) / 32;
             for (int64_t i = blockIdx.x; i < 2 * parts; i += gridDim.x) {
                 const int which = i >= parts;
-                const int64_t c = (i - which * parts) * 32 + lane;
-                uint16_t* db = P.db[which];
-                if (db && c < P.cols) add_workers<DT>(P.sums + which * P.ld + c, P.ld, P.workers, db + c, P.accumulate);
+                add_workers<DT>(P.sums + which * P.ld, P.ld, P.workers, (i - which * parts) * 32, P.cols, P.db[which], P.accumulate, lane);
             }
         }
     }
 
-    __device__ __forceinline__ void finish(const Item& I, Ahead&, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
+    // ---- a tile's end
+    static constexpr int kParts = BN / 64;                     // 32 x 32 results of a warp
+    static constexpr int kWidth = MODE == kForward ? BN / 2 : BN;   // columns of the result
+
+    // Where this warp's sums of part `slice` are: kParts of eight rows of 16 bytes a lane.
+    __device__ __forceinline__ float4* sums_at(const Item& I, int slice, int warp, int rank) const
+    {
+        const Product& Q = P.part[I.part];
+        const int64_t part = Q.part0 + (int64_t)(I.tile - Q.tile0) * Q.splits + slice;
+        return P.partial + ((part * CG + rank) * kEpiWarps + warp) * (kParts * 8 * 32);
+    }
+
+    // The warp's results are kept beside the other parts'; is it the last of them?
+    __device__ __forceinline__ bool keep_part(const Item& I, uint32_t acc, int half, int warp, int rank, int lane) const
+    {
+        float4* q = sums_at(I, I.slice, warp, rank) + lane;
+        for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols)
+            for (int k = 0; k < (MODE == kForward ? 2 : 1); ++k) {
+                float x[32];
+                tmem_load32(acc + k * kWidth + c, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) __stcg(q + j * 32, make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+                q += 8 * 32;
+            }
+        __threadfence();
+        __syncwarp();
+        uint32_t before = 0;
+        if (lane == 0) before = atomicAdd(P.tickets + ((int64_t)I.tile * CG + rank) * kEpiWarps + warp, 1u);
+        before = __shfl_sync(0xFFFFFFFFu, before, 0);
+        __threadfence();
+        return before == (uint32_t)P.part[I.part].splits - 1;
+    }
+
+    // Results `part` of the warp: from TMEM, or the sum of all parts.
+    __device__ __forceinline__ void results(const Item& I, uint32_t at, int part, int warp, int rank, int lane, float (&x)[32]) const
+    {
+        const int splits = P.part[I.part].splits;
+        if (splits == 1) {
+            tmem_load32(at, x);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+        const float4* q = sums_at(I, 0, warp, rank) + part * (8 * 32) + lane;
+        const int64_t next = (int64_t)CG * kEpiWarps * (kParts * 8 * 32);
+        for (int s = 0; s < splits; ++s, q += next) {
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __ldcg(q + j * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[4 * j] += v[j].x;
+                x[4 * j + 1] += v[j].y;
+                x[4 * j + 2] += v[j].z;
+                x[4 * j + 3] += v[j].w;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
+        const int warp = quad + 4 * half;
+        if (P.part[I.part].splits > 1 && !keep_part(I, acc, half, warp, rank, lane)) return;
+        int part = 0;
         if constexpr (MODE == kForward) {
-            constexpr int kWidth = BN / 2;
             const Matrix16& H = P.out[0];
-            for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols) {
+            for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols, part += 2) {
                 const int64_t col0 = (int64_t)I.n * kWidth + c;
                 if (col0 >= H.cols || row0 >= H.rows) break;
                 float g[32], u[32];
-                tmem_load32(acc + c, g);
-                tmem_load32(acc + kWidth + c, u);
-                add_bias<DT>(g, P.bias[0], P.bias_vec & 1, col0, H.cols);
-                add_bias<DT>(u, P.bias[1], P.bias_vec & 2, col0, H.cols);
+                results(I, acc + c, part, warp, rank, lane, g);
+                results(I, acc + kWidth + c, part + 1, warp, rank, lane, u);
+                if (P.bias[0] || P.bias[1]) {
+                    add_bias<DT>(g, A.bias[0]);
+                    add_bias<DT>(u, A.bias[1]);
+                    if (c + 2 * kEpiCols < kWidth) biases(I, c + 2 * kEpiCols, A);
+                }
                 if (P.out[1].p) put_tile<DT>(stage, lane, g, P.out[1], row0, col0);
                 if (P.out[2].p) put_tile<DT>(stage + kTile16Bytes, lane, u, P.out[2], row0, col0);
                 gate_values(g, u, P.act);
                 put_tile<DT>(stage, lane, g, H, row0, col0);
             }
         } else {
-            const Matrix16& D = P.part[I.part].out;
+            const Product& Q = P.part[I.part];
+            const Matrix16& D = Q.out;
             const bool add = P.accumulate && I.part >= P.parts_at;
-            for (int c = half * kEpiCols; c < BN; c += 2 * kEpiCols) {
+            for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols, ++part) {
                 const int64_t col0 = (int64_t)I.n * BN + c;
                 if (col0 >= D.cols || row0 >= D.rows) break;
                 float x[32];
-                tmem_load32(acc + c, x);
+                results(I, acc + c, part, warp, rank, lane, x);
                 if (add) add_tile<DT>(stage + kTile16Bytes, lane, 1.0f, x, D, row0, col0);
                 put_tile<DT>(stage, lane, x, D, row0, col0);
             }
@@ -248,7 +378,7 @@ struct GatedWork {
 };
 
 template <int CG, int BN, int MODE, int DT>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) gated_kernel(const __grid_constant__ GatedParams P)
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) gated_kernel(const __grid_constant__ GatedParams<MODE> P)
 {
     extern __shared__ unsigned char smem_raw[];
     Tiles<CG, BN> T;
@@ -259,7 +389,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) ga
 
 // The block over an empty inner dimension: g = bg, u = bu.
 template <int DT>
-__global__ void __launch_bounds__(256) gated_empty_kernel(const __grid_constant__ GatedParams P)
+__global__ void __launch_bounds__(256) gated_empty_kernel(const __grid_constant__ GatedParams<kForward> P)
 {
     after_earlier_work();
     const Matrix16 &H = P.out[0], &G = P.out[1], &U = P.out[2];
@@ -281,7 +411,9 @@ struct SplitParams {
     int32_t copy_blocks[3];
     const uint16_t *dh, *gate, *up;
     uint16_t *dg, *du;           // rows of ld elements, 16-byte aligned; NULL: only the sums
-    float* sums;                 // [worker][2][ld] column sums, or NULL
+    float* sums;                 // [block of workers][2][ld] column sums, or NULL
+    uint32_t* tickets;           // set to 0
+    int32_t n_tickets;
     int64_t rows, cols, ld_dh, ld_gate, ld_up, ld;
     int32_t act, vec, chunk;     // vec: every row starts on 16 bytes; chunk: consecutive rows a worker takes
 };
@@ -370,6 +502,9 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ S
 {
     after_earlier_work();
     constexpr int kFlight = 2;
+    __shared__ float4 turned[256][4];
+    const int thread = threadIdx.y * blockDim.x + threadIdx.x;
+    for (int i = blockIdx.x * 256 + thread; i < P.n_tickets; i += gridDim.x * 256) P.tickets[i] = 0;
     if ((int)blockIdx.x >= P.blocks) {
         int b = blockIdx.x - P.blocks, which = 0;
         while (b >= P.copy_blocks[which]) b -= P.copy_blocks[which++];
@@ -382,31 +517,45 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ S
     const int64_t worker = (int64_t)by * blockDim.y + threadIdx.y;
     const int64_t r1 = min(P.rows, (worker + 1) * P.chunk);
     int64_t r = worker * P.chunk;
-    if (n == 0 || r >= r1) return;
     float sg[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, su[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (n == 8 && P.vec) {
         for (; r + kFlight <= r1; r += kFlight) split_rows<DT, true, kFlight>(P, col, n, r, sg, su);
         for (; r < r1; ++r) split_rows<DT, true, 1>(P, col, n, r, sg, su);
-    } else {
+    } else if (n > 0) {
         for (; r < r1; ++r) split_rows<DT, false, 1>(P, col, n, r, sg, su);
     }
     if (!P.sums) return;
-    float4* q = reinterpret_cast<float4*>(P.sums + worker * 2 * P.ld + col);
-    q[0] = make_float4(sg[0], sg[1], sg[2], sg[3]);
-    q[1] = make_float4(sg[4], sg[5], sg[6], sg[7]);
-    q = reinterpret_cast<float4*>(P.sums + (worker * 2 + 1) * P.ld + col);
-    q[0] = make_float4(su[0], su[1], su[2], su[3]);
-    q[1] = make_float4(su[4], su[5], su[6], su[7]);
+    float4 s[4] = {make_float4(sg[0], sg[1], sg[2], sg[3]), make_float4(sg[4], sg[5], sg[6], sg[7]), make_float4(su[0], su[1], su[2], su[3]),
+                   make_float4(su[4], su[5], su[6], su[7])};
+    if (blockDim.y > 1) {
+        // the block's workers, in order
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turned[thread][j] = s[j];
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 1; y < blockDim.y; ++y)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 v = turned[y * blockDim.x + threadIdx.x][j];
+                s[j] = make_float4(s[j].x + v.x, s[j].y + v.y, s[j].z + v.z, s[j].w + v.w);
+            }
+    }
+    if (n == 0) return;
+    float4* q = reinterpret_cast<float4*>(P.sums + (int64_t)by * 2 * P.ld + col);
+    q[0] = s[0];
+    q[1] = s[1];
+    q = reinterpret_cast<float4*>(P.sums + ((int64_t)by * 2 + 1) * P.ld + col);
+    q[0] = s[2];
+    q[1] = s[3];
 }
 
-// The biases' gradients where no product is asked for.
+// The biases' gradients where no product is asked for: a warp 32 columns.
 template <int DT>
-__global__ void __launch_bounds__(128) gated_bias_kernel(const __grid_constant__ GatedParams P)
+__global__ void __launch_bounds__(128) gated_bias_kernel(const __grid_constant__ GatedParams<kBackward> P)
 {
     after_earlier_work();
-    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    uint16_t* db = P.db[blockIdx.y];
-    if (db && c < P.cols) add_workers<DT>(P.sums + blockIdx.y * P.ld + c, P.ld, P.workers, db + c, P.accumulate);
+    const int64_t c0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * 32;
+    if (c0 < P.cols) add_workers<DT>(P.sums + blockIdx.y * P.ld, P.ld, P.workers, c0, P.cols, P.db[blockIdx.y], P.accumulate, threadIdx.x & 31);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -594,26 +743,75 @@ struct Shape {
 };
 constexpr Shape kShapes[] = {{2, 256, 0.31}, {1, 128, 0.23}};
 
-// n1 tiles of k1 inner blocks and n2 of k2 dealt so that the worker with most has least; *blocks: what it has.
-Deal deal_out(const Shape& S, int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t* blocks)
+// n1 items of us1 and n2 of us2 dealt so that the worker with most has least; *us: its time.
+Deal deal_out(const Shape& S, int64_t n1, double us1, int64_t n2, double us2, double* us)
 {
     const int64_t w = std::min<int64_t>(S.workers(), std::max<int64_t>(1, n1 + n2)), q = n1 / w, ahead = n1 % w;
     Deal best{(int32_t)n1, (int32_t)n2, (int32_t)w, (int32_t)ahead, 0, 0};
-    int64_t least = INT64_MAX;
+    if (n2 == 0) {
+        *us = (q + (ahead > 0)) * us1;
+        return best;
+    }
+    *us = 1e30;
     for (int64_t more = 0; more <= div_up(n2, w); ++more) {
         const int64_t left = std::max<int64_t>(0, n2 - more * ahead), rest = div_up(left, w - ahead);
-        const int64_t most = std::max(ahead > 0 ? (q + 1) * k1 + more * k2 : 0, q * k1 + rest * k2);
-        if (most >= least) continue;
-        least = most;
+        const double most = std::max(ahead > 0 ? (q + 1) * us1 + more * us2 : 0.0, q * us1 + rest * us2);
+        if (most >= *us) continue;
+        *us = most;
         best.more = (int32_t)more;
         best.rest = (int32_t)rest;
     }
-    *blocks = least;
+    return best;
+}
+
+// How a launch is cut: the tiles' shape, and the parts of the inner dimension of either kind of product.
+struct Cut {
+    Shape shape = kShapes[0];
+    int64_t tiles1 = 0, tiles2 = 0;
+    int splits1 = 1, splits2 = 1, per1 = 1, per2 = 1;
+    Deal deal{0, 0, 1, 0, 0, 0};
+    int64_t tiles_in_parts() const { return (splits1 > 1 ? tiles1 : 0) + (splits2 > 1 ? tiles2 : 0); }
+    int64_t partial_bytes() const { return (splits1 > 1 ? tiles1 * splits1 : 0) * tile_bytes() + (splits2 > 1 ? tiles2 * splits2 : 0) * tile_bytes(); }
+    int64_t tile_bytes() const { return 4ll * kBM * shape.cg * shape.bn; }
+    int64_t tickets() const { return tiles_in_parts() * kEpiWarps * shape.cg; }
+};
+
+// Products of m1 x n1 over kb1 inner blocks and `count2` of m2 x n2 over kb2.  A tile costs 1.2 us beside its inner blocks, a
+// part of one 2 us and a part's share of the sum more.
+Cut choose_cut(int64_t m1, int64_t n1, int64_t kb1, int64_t count2, int64_t m2, int64_t n2, int64_t kb2)
+{
+    static const int kWays[] = {1, 2, 4, 8, 16, 32};
+    Cut best;
+    double least = 1e30;
+    for (const Shape& S : kShapes) {
+        const int64_t tiles1 = S.rows(m1) * S.cols(n1), tiles2 = count2 * S.rows(m2) * S.cols(n2);
+        auto each = [&](int64_t kb, int splits) { return (double)kb * S.block_us + 1.2 + (splits > 1 ? 2.0 + 0.1 * splits : 0.0); };
+        for (const int ways1 : kWays) {
+            const int64_t per1 = div_up(std::max<int64_t>(kb1, 1), ways1);
+            if (ways1 > 1 && (tiles1 == 0 || per1 < 4 || div_up(kb1, per1) != ways1 || tiles1 >= S.workers())) continue;
+            for (const int ways2 : kWays) {
+                const int64_t per2 = div_up(std::max<int64_t>(kb2, 1), ways2);
+                if (ways2 > 1 && (tiles2 == 0 || per2 < 4 || div_up(kb2, per2) != ways2 || tiles2 >= S.workers())) continue;
+                double us = 0.0;
+                const Deal D = deal_out(S, tiles1 * ways1, each(per1, ways1), tiles2 * ways2, each(per2, ways2), &us);
+                if (us >= least) continue;
+                least = us;
+                best.shape = S;
+                best.tiles1 = tiles1;
+                best.tiles2 = tiles2;
+                best.splits1 = ways1;
+                best.splits2 = ways2;
+                best.per1 = (int)per1;
+                best.per2 = (int)per2;
+                best.deal = D;
+            }
+        }
+    }
     return best;
 }
 
 template <int CG, int BN, int MODE, int DT>
-zero_status_t launch_gated(const GatedParams& P, cudaStream_t s)
+zero_status_t launch_gated(const GatedParams<MODE>& P, cudaStream_t s)
 {
     using S = GemmShape<CG, BN>;
     const cudaError_t set = allow_shared<gated_kernel<CG, BN, MODE, DT>>(S::kSmem);
@@ -624,7 +822,7 @@ zero_status_t launch_gated(const GatedParams& P, cudaStream_t s)
 }
 
 template <int MODE>
-zero_status_t launch_gated(const GatedParams& P, const Shape& c, bool bf, cudaStream_t s)
+zero_status_t launch_gated(const GatedParams<MODE>& P, const Shape& c, bool bf, cudaStream_t s)
 {
     if (c.cg == 2) return bf ? launch_gated<2, 256, MODE, ZERO_BF16>(P, s) : launch_gated<2, 256, MODE, ZERO_FP16>(P, s);
     return bf ? launch_gated<1, 128, MODE, ZERO_BF16>(P, s) : launch_gated<1, 128, MODE, ZERO_FP16>(P, s);
@@ -667,6 +865,7 @@ zero_status_t launch_few(const FewParams& P, bool in_out, cudaStream_t s)
 struct SplitCut {
     int tx = 256, ty = 1, chunk = 1;
     int64_t workers = 0;
+    int64_t groups() const { return div_up(workers, ty); }   // blocks across the rows, each of which writes its sums
 };
 
 SplitCut split_cut(int64_t rows, int64_t cols)
@@ -690,8 +889,10 @@ struct Gated {
     int64_t w_rows = 0, w_cols = 0;        // as stored
     int64_t ld8[3] = {0, 0, 0}, at_copy[3] = {0, 0, 0};
     int64_t ld_d = 0, at_dg = 0, at_du = 0, at_sums = 0, bytes = 0;
+    int64_t at_partial = 0, at_tickets = 0;
     bool make_d = false, make_sums = false;
     SplitCut cut;
+    Cut tiles;
 };
 
 zero_status_t lay_out(const zero_gated_t* in, bool back, Gated* L, const char* who)
@@ -770,7 +971,17 @@ zero_status_t lay_out(const zero_gated_t* in, bool back, Gated* L, const char* w
             L->at_dg = take(2 * a.rows * L->ld_d);
             L->at_du = take(2 * a.rows * L->ld_d);
         }
-        if (L->make_sums) L->at_sums = take(8 * L->cut.workers * L->ld_d);
+        if (L->make_sums) L->at_sums = take(8 * L->cut.groups() * L->ld_d);
+    }
+    if (any_in && !L->few && (!back || L->make_d)) {
+        const int weights = (a.dw_gate != nullptr) + (a.dw_up != nullptr);
+        const int64_t kb_k = div_up(a.in_features, kBK), kb_n = div_up(a.out_features, kBK), kb_m = div_up(a.rows, kBK);
+        L->tiles = back ? choose_cut(a.dx ? a.rows : 0, a.in_features, 2 * kb_n, weights, L->w_rows, L->w_cols, kb_m)
+                        : choose_cut(a.rows, 2 * a.out_features, kb_k, 0, 0, 0, 0);
+        if (L->tiles.partial_bytes() > 0) {
+            L->at_partial = take(L->tiles.partial_bytes());
+            L->at_tickets = take(4 * L->tiles.tickets());
+        }
     }
     L->bytes = at;
     return ZERO_OK;
@@ -821,6 +1032,18 @@ zero_status_t launch_split(const Gated& L, const SplitParams& S, cudaStream_t s)
 Matrix16 matrix(void* p, int64_t ld, int64_t rows, int64_t cols)
 {
     return Matrix16{static_cast<uint16_t*>(p), ld, rows, cols, vec_flag(p, ld, 1)};
+}
+
+// The product's parts, after *tiles tiles and *parts parts of others.
+void set_parts(Product* Q, int splits, int per, int64_t* tiles, int64_t* parts)
+{
+    Q->splits = splits;
+    Q->k_per_split = per;
+    Q->tile0 = (int32_t)*tiles;
+    Q->part0 = (int32_t)*parts;
+    if (splits == 1) return;
+    *tiles += (int64_t)Q->tiles_m * Q->tiles_n;
+    *parts += (int64_t)Q->tiles_m * Q->tiles_n * splits;
 }
 
 // Zeros for a gradient that sums over nothing.
@@ -884,7 +1107,7 @@ try {
         P.act = a.activation;
         return L.bf ? launch_few<ZERO_BF16>(P, in_out, s) : launch_few<ZERO_FP16>(P, in_out, s);
     }
-    GatedParams P;
+    GatedParams<kForward> P;
     std::memset(&P, 0, sizeof(P));
     P.out[0] = matrix(a.h, a.ld_h, a.rows, a.out_features);
     P.out[1] = matrix(a.gate, a.ld_gate, a.rows, a.out_features);
@@ -903,15 +1126,7 @@ try {
     plan_copies(L, static_cast<char*>(workspace), operand, &S);
     st = launch_split(L, S, s);
     if (st != ZERO_OK) return st;
-    Shape c = kShapes[0];
-    double best = 1e30;
-    for (const Shape& S : kShapes) {
-        const double us = (double)div_up(S.rows(a.rows) * S.cols(2 * a.out_features), S.workers()) * S.block_us;
-        if (us < best) {
-            best = us;
-            c = S;
-        }
-    }
+    const Shape c = L.tiles.shape;
     Product& Q = P.part[0];
     // few rows: no zeros are copied for the rest, whose results are not stored
     P.a_rows = c.cg == 1 && a.rows < kBM ? (int32_t)up(a.rows, 8) : kBM;
@@ -924,7 +1139,16 @@ try {
     Q.k_blocks = (int32_t)div_up(a.in_features, kBK);
     Q.b_mn = in_out;
     Q.idesc = product_desc(L.bf, false, in_out, c);
-    P.count = Q.tiles_m * Q.tiles_n;
+    P.count = Q.tiles_m * Q.tiles_n * L.tiles.splits1;
+    int64_t tiles = 0, parts = 0;
+    set_parts(&Q, L.tiles.splits1, L.tiles.per1, &tiles, &parts);
+    if (L.tiles.splits1 > 1) {
+        char* ws = static_cast<char*>(workspace);
+        P.partial = reinterpret_cast<float4*>(ws + L.at_partial);
+        P.tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
+        const cudaError_t e = cudaMemsetAsync(P.tickets, 0, (size_t)(4 * L.tiles.tickets()), s);
+        if (e != cudaSuccess) return cuda_fail(e, "zero_gated: memset");
+    }
     return launch_gated<kForward>(P, c, L.bf, s);
 }
 catch (...) {
@@ -974,11 +1198,13 @@ try {
         S.vec = vec_flag(a.dh, a.ld_dh, 1) && vec_flag(a.gate, a.ld_gate, 1) && vec_flag(a.up, a.ld_up, 1);
         S.chunk = L.cut.chunk;
         S.across = (int32_t)div_up(n, (int64_t)L.cut.tx * 8);
-        S.blocks = (int32_t)(S.across * div_up(L.cut.workers, L.cut.ty));
+        S.blocks = (int32_t)(S.across * L.cut.groups());
+        S.tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
+        S.n_tickets = (int32_t)L.tiles.tickets();
     }
     st = launch_split(L, S, s);
     if (st != ZERO_OK) return st;
-    GatedParams P;
+    GatedParams<kBackward> P;
     std::memset(&P, 0, sizeof(P));
     P.accumulate = accumulate;
     if (L.make_sums) {
@@ -986,7 +1212,7 @@ try {
         P.db[0] = static_cast<uint16_t*>(a.db_gate);
         P.db[1] = static_cast<uint16_t*>(a.db_up);
         P.ld = L.ld_d;
-        P.workers = L.cut.workers;
+        P.workers = L.cut.groups();
         P.cols = n;
     }
     if (!L.make_d) {
@@ -996,18 +1222,13 @@ try {
         return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated_backward: launch");
     }
     // dx, then the weights' gradients that are asked for
-    const int weights = (a.dw_gate != nullptr) + (a.dw_up != nullptr);
     const int64_t kb_n = div_up(n, kBK), kb_m = div_up(m, kBK);
-    Shape c = kShapes[0];
-    double best = 1e30;
-    for (const Shape& S : kShapes) {
-        int64_t blocks = 0;
-        const Deal D = deal_out(S, a.dx ? S.rows(m) * S.cols(k) : 0, 2 * kb_n, weights * S.rows(L.w_rows) * S.cols(L.w_cols), kb_m, &blocks);
-        if (blocks * S.block_us >= best) continue;
-        best = blocks * S.block_us;
-        c = S;
-        P.deal = D;
-    }
+    const Cut& T = L.tiles;
+    const Shape c = T.shape;
+    P.deal = T.deal;
+    P.partial = reinterpret_cast<float4*>(ws + L.at_partial);
+    P.tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
+    int64_t tiles = 0, parts = 0;
     P.a_rows = c.cg == 1 && m < kBM ? (int32_t)up(m, 8) : kBM;
     const Operand d[2] = {{ws + L.at_dg, m, n, L.ld_d, false}, {ws + L.at_du, m, n, L.ld_d, false}};
     int part = 0;
@@ -1024,6 +1245,7 @@ try {
         Q.k_blocks = 2 * Q.k_first;
         Q.b_mn = out_in;
         Q.idesc = product_desc(L.bf, false, out_in, c);
+        set_parts(&Q, T.splits1, T.per1, &tiles, &parts);
     }
     P.parts_at = part;
     const Operand x{operand[0], k, m, L.ld8[0], true};
@@ -1040,6 +1262,7 @@ try {
         Q.k_blocks = Q.k_first = (int32_t)kb_m;
         Q.a_mn = Q.b_mn = 1;
         Q.idesc = product_desc(L.bf, true, true, c);
+        set_parts(&Q, T.splits2, T.per2, &tiles, &parts);
     }
     if (st == ZERO_OK) st = launch_gated<kBackward>(P, c, L.bf, s);
     return st;

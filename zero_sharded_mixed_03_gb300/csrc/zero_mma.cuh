@@ -244,6 +244,156 @@ struct GemmShape {
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 256;
 };
 
+// ------------------------------------------------------------------ tiles of 16 bits
+
+// A 16-bit matrix that tiles are read from or written to.
+struct Matrix16 {
+    uint16_t* p;
+    int64_t ld, rows, cols;
+    int32_t vec;             // rows start on 16 bytes
+};
+
+// Where a warp keeps a 32 x 32 tile of 16 bits: rows of 64 bytes, their 16-byte pieces exchanged so that neither
+// eight rows' same pieces nor two rows' four conflict.
+constexpr int kTile16Bytes = 32 * 64;
+
+__device__ __forceinline__ uint32_t tile16_at(uint32_t stage, int row, int piece) { return stage + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
+
+// The tile in shared memory to global memory; what is past the matrix is left out.
+__device__ __forceinline__ void store_tile16(uint32_t stage, int lane, const Matrix16& D, int64_t row0, int64_t col0)
+{
+    if (D.vec) {
+        const int64_t col = col0 + (lane & 3) * 8;
+        const int n = (int)max((int64_t)0, min((int64_t)8, D.cols - col));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tile16_at(stage, r, lane & 3)) : "memory");
+            if (row0 + r >= D.rows || n == 0) continue;
+            uint16_t* q = D.p + (row0 + r) * D.ld + col;
+            if (n == 8) {
+                *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < n) q[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+            }
+        }
+    } else if (col0 + lane < D.cols) {
+        // a column a lane, so that a warp writes neighbours
+        const int rows = (int)min((int64_t)32, D.rows - row0);
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(tile16_at(stage, r, lane >> 3) + (lane & 7) * 2) : "memory");
+            D.p[(row0 + r) * D.ld + col0 + lane] = v;
+        }
+    }
+}
+
+// The tile of global memory into shared memory; zeros past the matrix.
+__device__ __forceinline__ void load_tile16(uint32_t stage, int lane, const Matrix16& D, int64_t row0, int64_t col0)
+{
+    if (D.vec) {
+        const int64_t col = col0 + (lane & 3) * 8;
+        const int n = (int)max((int64_t)0, min((int64_t)8, D.cols - col));
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = row0 + i * 8 + (lane >> 2);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row >= D.rows || n == 0) continue;
+            const uint16_t* q = D.p + row * D.ld + col;
+            if (n == 8) {
+                v[i] = *reinterpret_cast<const uint4*>(q);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = (2 * j < n ? q[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)q[2 * j + 1] : 0u) << 16);
+                v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile16_at(stage, i * 8 + (lane >> 2), lane & 3)), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
+    } else {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            const uint16_t v = row0 + r < D.rows && col0 + lane < D.cols ? D.p[(row0 + r) * D.ld + col0 + lane] : (uint16_t)0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile16_at(stage, r, lane >> 3) + (lane & 7) * 2), "h"(v) : "memory");
+        }
+    }
+}
+
+// x: row `lane` of the tile in shared memory, rounded once.
+template <int DT>
+__device__ __forceinline__ void write_tile16(uint32_t stage, int lane, const float (&x)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile16_at(stage, lane, i)), "r"(narrow2<DT>(x[8 * i], x[8 * i + 1])),
+                     "r"(narrow2<DT>(x[8 * i + 2], x[8 * i + 3])), "r"(narrow2<DT>(x[8 * i + 4], x[8 * i + 5])),
+                     "r"(narrow2<DT>(x[8 * i + 6], x[8 * i + 7]))
+                     : "memory");
+}
+
+// The same tile at (row0, col0) of a matrix, through shared memory, so that a store instruction writes whole sectors.
+template <int DT>
+__device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
+{
+    write_tile16<DT>(stage, lane, x);
+    __syncwarp();
+    store_tile16(stage, lane, D, row0, col0);
+    __syncwarp();
+}
+
+// The tile in shared memory (tile16_at's exchange is the 64-byte swizzle; 512-byte aligned) to a tensor map's matrix,
+// by a copy that lane 0 starts and that belongs to its bulk group; what is past the matrix is left out.
+__device__ __forceinline__ void send_tile16(uint32_t stage, int lane, const CUtensorMap* map, int64_t row0, int64_t col0)
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(map), "r"((int)col0), "r"((int)row0), "r"(stage)
+            : "memory");
+}
+
+// Lane 0: until all but `LEFT` of its copies have read their tiles; and until all have written.
+template <int LEFT>
+__device__ __forceinline__ void sent_read(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+    __syncwarp();
+}
+__device__ __forceinline__ void sent_all(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// x += scale times the tile that is there.
+template <int DT>
+__device__ __forceinline__ void add_tile(uint32_t stage, int lane, float scale, float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
+{
+    load_tile16(stage, lane, D, row0, col0);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tile16_at(stage, lane, i)) : "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            widen2<DT>(w[j], a, b);
+            x[8 * i + 2 * j] += scale * a;
+            x[8 * i + 2 * j + 1] += scale * b;
+        }
+    }
+    __syncwarp();
+}
+
 // ------------------------------------------------------------------ a kernel of tiles
 //
 // One thread copies operand tiles into the ring, one issues the products, eight warps finish a tile while the next
@@ -257,8 +407,8 @@ struct GemmShape {
 //   load(Item, kb, a, b, bar, rank)      those copies
 //   a_mn(Item, kb), b_mn(Item, kb), idesc(Item, kb)   how a stage's operands lie, and the product's descriptor
 //   prepare(Item, quad, half, rank, lane, Ahead&)      what a tile's end may load before its products are done
-//   done(Item, lane)                                   by each of those warps once its part is stored
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
+//   done(Item, lane)                                   by each of those warps after it
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
 // One lane of a whole warp, in a form that the compiler knows to be one: copies and products are then issued from
@@ -457,11 +607,11 @@ struct Tiles {
             const uint32_t acc_empty_leader = CG == 2 ? leader_address(acc_empty0) : acc_empty0;
             uint32_t tile = 0;
             for (int i = first; i < end && ok; i += step, ++tile) {
+                const uint32_t acc = tile & 1, use = tile >> 1;
                 typename W::Item I;
                 ok = take(work, i, tile, I, true);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                const uint32_t acc = tile & 1, use = tile >> 1;
                 typename W::Ahead ahead;
                 work.prepare(I, quad, half, (int)rank, lane, ahead);
                 ok = stage_wait(acc_full0 + 8 * acc, use & 1);
@@ -477,6 +627,7 @@ struct Tiles {
                 }
                 work.done(I, lane);
             }
+            sent_all(lane);          // the block's memory outlives the copies from it
         }
         if (!ok) {
             // A wait ran out: say so, and give copies and products in flight time to end before the block's memory
@@ -498,155 +649,6 @@ struct Tiles {
         }
     }
 };
-
-// A 16-bit matrix that tiles are read from or written to.
-struct Matrix16 {
-    uint16_t* p;
-    int64_t ld, rows, cols;
-    int32_t vec;             // rows start on 16 bytes
-};
-
-// Where a warp keeps a 32 x 32 tile of 16 bits: rows of 64 bytes, their 16-byte pieces exchanged so that neither
-// eight rows' same pieces nor two rows' four conflict.
-constexpr int kTile16Bytes = 32 * 64;
-
-__device__ __forceinline__ uint32_t tile16_at(uint32_t stage, int row, int piece) { return stage + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
-
-// The tile in shared memory to global memory; what is past the matrix is left out.
-__device__ __forceinline__ void store_tile16(uint32_t stage, int lane, const Matrix16& D, int64_t row0, int64_t col0)
-{
-    if (D.vec) {
-        const int64_t col = col0 + (lane & 3) * 8;
-        const int n = (int)max((int64_t)0, min((int64_t)8, D.cols - col));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tile16_at(stage, r, lane & 3)) : "memory");
-            if (row0 + r >= D.rows || n == 0) continue;
-            uint16_t* q = D.p + (row0 + r) * D.ld + col;
-            if (n == 8) {
-                *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) q[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-            }
-        }
-    } else if (col0 + lane < D.cols) {
-        // a column a lane, so that a warp writes neighbours
-        const int rows = (int)min((int64_t)32, D.rows - row0);
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r) {
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(tile16_at(stage, r, lane >> 3) + (lane & 7) * 2) : "memory");
-            D.p[(row0 + r) * D.ld + col0 + lane] = v;
-        }
-    }
-}
-
-// The tile of global memory into shared memory; zeros past the matrix.
-__device__ __forceinline__ void load_tile16(uint32_t stage, int lane, const Matrix16& D, int64_t row0, int64_t col0)
-{
-    if (D.vec) {
-        const int64_t col = col0 + (lane & 3) * 8;
-        const int n = (int)max((int64_t)0, min((int64_t)8, D.cols - col));
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = row0 + i * 8 + (lane >> 2);
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row >= D.rows || n == 0) continue;
-            const uint16_t* q = D.p + row * D.ld + col;
-            if (n == 8) {
-                v[i] = *reinterpret_cast<const uint4*>(q);
-            } else {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = (2 * j < n ? q[2 * j] : 0u) | ((2 * j + 1 < n ? (uint32_t)q[2 * j + 1] : 0u) << 16);
-                v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile16_at(stage, i * 8 + (lane >> 2), lane & 3)), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
-    } else {
-#pragma unroll 8
-        for (int r = 0; r < 32; ++r) {
-            const uint16_t v = row0 + r < D.rows && col0 + lane < D.cols ? D.p[(row0 + r) * D.ld + col0 + lane] : (uint16_t)0;
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile16_at(stage, r, lane >> 3) + (lane & 7) * 2), "h"(v) : "memory");
-        }
-    }
-}
-
-// x: row `lane` of the tile in shared memory, rounded once.
-template <int DT>
-__device__ __forceinline__ void write_tile16(uint32_t stage, int lane, const float (&x)[32])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile16_at(stage, lane, i)), "r"(narrow2<DT>(x[8 * i], x[8 * i + 1])),
-                     "r"(narrow2<DT>(x[8 * i + 2], x[8 * i + 3])), "r"(narrow2<DT>(x[8 * i + 4], x[8 * i + 5])),
-                     "r"(narrow2<DT>(x[8 * i + 6], x[8 * i + 7]))
-                     : "memory");
-}
-
-// The same tile at (row0, col0) of a matrix, through shared memory, so that a store instruction writes whole sectors.
-template <int DT>
-__device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
-{
-    write_tile16<DT>(stage, lane, x);
-    __syncwarp();
-    store_tile16(stage, lane, D, row0, col0);
-    __syncwarp();
-}
-
-// The tile in shared memory (tile16_at's exchange is the 64-byte swizzle; 512-byte aligned) to a tensor map's matrix,
-// by a copy that lane 0 starts and that belongs to its bulk group; what is past the matrix is left out.
-__device__ __forceinline__ void send_tile16(uint32_t stage, int lane, const CUtensorMap* map, int64_t row0, int64_t col0)
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
-            "cp.async.bulk.commit_group;" ::"l"(map), "r"((int)col0), "r"((int)row0), "r"(stage)
-            : "memory");
-}
-
-// Lane 0: until all but `LEFT` of its copies have read their tiles; and until all have written.
-template <int LEFT>
-__device__ __forceinline__ void sent_read(int lane)
-{
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
-    __syncwarp();
-}
-__device__ __forceinline__ void sent_all(int lane)
-{
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-// x += the tile that is there.
-template <int DT>
-__device__ __forceinline__ void add_tile(uint32_t stage, int lane, float scale, float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
-{
-    load_tile16(stage, lane, D, row0, col0);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tile16_at(stage, lane, i)) : "memory");
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float a, b;
-            widen2<DT>(w[j], a, b);
-            x[8 * i + 2 * j] += scale * a;
-            x[8 * i + 2 * j + 1] += scale * b;
-        }
-    }
-    __syncwarp();
-}
 
 // ------------------------------------------------------------------ aligned copies
 

@@ -391,7 +391,6 @@ template <int CG, int BN>
 struct MuonWork {
     const ProductParams& P;
     struct alignas(16) Item {
-        const Op* op;
         const uint32_t* before;  // the matrix's counter of the product before, or NULL
         uint32_t* counter;       // and of this one
         const CUtensorMap* maps; // the matrix's
@@ -399,11 +398,12 @@ struct MuonWork {
         int32_t ld, rows, cols;  // of the result and the addends
         int32_t m, n, kb, kind, tensor;
         uint32_t want;           // of `before`
+        float scale, lin[2], diag;
+        int8_t adds, keep_low, final;
         int8_t a, b, out;        // maps: operands along K, or along their own rows where `along` says so; the result
         int8_t along;            // 1: a is, 2: b is
         int8_t square;           // 1: a, 2: b is symmetric: tiles below the diagonal are taken from above it
-        int8_t reserved[3];
-        int32_t more[3];
+        int32_t reserved[2];
     };
     static constexpr bool kScout = true;
 
@@ -420,17 +420,23 @@ struct MuonWork {
         const int tensor = t.tensor & 0xFFFF, phase = (t.tensor >> 16) - P.first;
         const MuonTensor& T = P.tensors[tensor];
         Item I;
-        I.op = &P.ops[phase];
+        const Op& O = P.ops[phase];
+        I.scale = O.scale;
+        I.lin[0] = O.lin[0];
+        I.lin[1] = O.lin[1];
+        I.diag = O.diag;
+        I.adds = (int8_t)O.adds;
+        I.keep_low = (int8_t)O.keep_low;
+        I.final = (int8_t)O.final;
         I.maps = T.map;
         I.tensor = tensor;
         I.m = t.at >> 16;
         I.n = t.at & 0xFFFF;
-        I.kind = I.op->kind;
+        I.kind = O.kind;
         I.counter = P.counters + tensor * kMaxPhases + phase;
         I.before = phase > 0 ? I.counter - 1 : nullptr;
         I.want = 0;
         if (phase > 0) I.want = (uint32_t)T.tiles[P.ops[phase - 1].kind == kNext] * (kEpiWarps * CG);
-        const Op& O = *I.op;
         const bool wide = T.wide;
         int inner = T.m;
         if (I.kind == kNext) {
@@ -494,7 +500,7 @@ struct MuonWork {
         uint32_t use = 1u << I.a | 1u << I.b | 1u << I.out;
         if (I.square & 1) use |= 1u << (I.a + kSquares);
         if (I.square & 2) use |= 1u << (I.b + kSquares);
-        if (I.op->keep_low) use |= 1u << kMapOutLow;
+        if (I.keep_low) use |= 1u << kMapOutLow;
         if (I.tensor < Seen::kMatrices) {
             const uint32_t old = S.maps[I.tensor];
             S.maps[I.tensor] = old | use;
@@ -586,7 +592,7 @@ struct MuonWork {
 
     __device__ __forceinline__ void fetch_adds(const Item& I, Ahead& A, int64_t row0, int c, int lane) const
     {
-        const int adds = I.op->adds;
+        const int adds = I.adds;
         if (adds > 0) fetch(A.v[0], I.add[0], I, row0 + lane, (int64_t)I.n * BN + c);
         if (adds > 1) fetch(A.v[1], I.add[1], I, row0 + lane, (int64_t)I.n * BN + c);
     }
@@ -664,7 +670,6 @@ struct MuonWork {
 
     __device__ __forceinline__ void finish_final(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
-        const Op& O = *I.op;
         if (left_out(P.st, P.plan)) return;
         const Target G = target(I);
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
@@ -674,24 +679,24 @@ struct MuonWork {
             float x[32];
             tmem_load32(acc + c, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] *= O.scale;
-            if (O.adds > 0) {
+            for (int j = 0; j < 32; ++j) x[j] *= I.scale;
+            if (I.adds > 0) {
                 // one or two steps in all: the addends and the parameters are loaded here
                 fetch_adds(I, A, row0, c, lane);
-                add_row(A.v[0], O.lin[0], x);
-                if (O.adds > 1) add_row(A.v[1], O.lin[1], x);
+                add_row(A.v[0], I.lin[0], x);
+                if (I.adds > 1) add_row(A.v[1], I.lin[1], x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (G.vec) A.v[i >> 2][i & 3] = parameters(G, row0, col0, i, lane);
             }
-            apply(G, A, O.adds == 0 && c + 2 * kEpiCols < BN, row0, col0, lane, stage, x);
+            apply(G, A, I.adds == 0 && c + 2 * kEpiCols < BN, row0, col0, lane, stage, x);
         }
     }
 
     __device__ __forceinline__ void prepare(const Item& I, int quad, int half, int rank, int lane, Ahead& A) const
     {
-        if (I.op->final) {
-            if (I.op->adds > 0) return;
+        if (I.final) {
+            if (I.adds > 0) return;
             const Target G = target(I);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -703,8 +708,7 @@ struct MuonWork {
 
     __device__ __forceinline__ void finish(const Item& I, Ahead& A, uint32_t acc, int quad, int half, uint32_t stage, int rank, int lane) const
     {
-        const Op& O = *I.op;
-        if (O.final) {
+        if (I.final) {
             finish_final(I, A, acc, quad, half, stage, rank, lane);
             return;
         }
@@ -716,26 +720,26 @@ struct MuonWork {
             float x[32];
             tmem_load32(acc + c, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] *= O.scale;
-            if (O.adds > 0) add_row(A.v[0], O.lin[0], x);
-            if (O.adds > 1) add_row(A.v[1], O.lin[1], x);
+            for (int j = 0; j < 32; ++j) x[j] *= I.scale;
+            if (I.adds > 0) add_row(A.v[0], I.lin[0], x);
+            if (I.adds > 1) add_row(A.v[1], I.lin[1], x);
             if (c + 2 * kEpiCols < BN) fetch_adds(I, A, row0, c + 2 * kEpiCols, lane);
             // the warp's two tiles in turn, unless the low part needs one
-            const uint32_t at = O.keep_low ? stage : stage + turn;
-            if (O.keep_low) sent_read<0>(lane);
+            const uint32_t at = I.keep_low ? stage : stage + turn;
+            if (I.keep_low) sent_read<0>(lane);
             else sent_read<1>(lane);
             if (I.kind != kNext && row0 == col0) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] += j == lane ? O.diag : 0.0f;
+                for (int j = 0; j < 32; ++j) x[j] += j == lane ? I.diag : 0.0f;
             }
             write_tile16<ZERO_FP16>(at, lane, x);
             send_tile16(at, lane, I.maps + I.out, row0, col0);
-            if (O.keep_low) {
+            if (I.keep_low) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
                 write_tile16<ZERO_FP16>(stage + kTile16Bytes, lane, x);
                 send_tile16(stage + kTile16Bytes, lane, I.maps + kMapOutLow, row0, col0);
-            }
+                }
         }
     }
 };
