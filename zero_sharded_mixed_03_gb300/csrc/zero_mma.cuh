@@ -244,6 +244,16 @@ struct GemmShape {
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kEpiBytes + 256;
 };
 
+// One lane of a whole warp, in a form that the compiler knows to be one: copies and products are then issued from
+// uniform registers.  Behind `lane == 0` it has to expect several, and two copies cost 470 cycles, more than the
+// products of an inner block take (128 x 128 tiles).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ tiles of 16 bits
 
 // A 16-bit matrix that tiles are read from or written to.
@@ -350,28 +360,29 @@ __device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (
 }
 
 // The tile in shared memory (tile16_at's exchange is the 64-byte swizzle; 512-byte aligned) to a tensor map's matrix,
-// by a copy that lane 0 starts and that belongs to its bulk group; what is past the matrix is left out.
-__device__ __forceinline__ void send_tile16(uint32_t stage, int lane, const CUtensorMap* map, int64_t row0, int64_t col0)
+// by a copy that one lane, always the same, starts and that belongs to its bulk group; what is past the matrix is left
+// out.
+__device__ __forceinline__ void send_tile16(uint32_t stage, const CUtensorMap* map, int64_t row0, int64_t col0)
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (lane == 0)
+    if (elect_one())
         asm volatile(
             "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
             "cp.async.bulk.commit_group;" ::"l"(map), "r"((int)col0), "r"((int)row0), "r"(stage)
             : "memory");
 }
 
-// Lane 0: until all but `LEFT` of its copies have read their tiles; and until all have written.
+// That lane: until all but `LEFT` of its copies have read their tiles; and until all have written.
 template <int LEFT>
-__device__ __forceinline__ void sent_read(int lane)
+__device__ __forceinline__ void sent_read()
 {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
     __syncwarp();
 }
-__device__ __forceinline__ void sent_all(int lane)
+__device__ __forceinline__ void sent_all()
 {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 // x += scale times the tile that is there.
 template <int DT>
@@ -411,16 +422,6 @@ __device__ __forceinline__ void add_tile(uint32_t stage, int lane, float scale, 
 //   done(Item, lane)                                   by each of those warps after it
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
-// One lane of a whole warp, in a form that the compiler knows to be one: copies and products are then issued from
-// uniform registers.  Behind `lane == 0` it has to expect several, and two copies cost 470 cycles, more than the
-// products of an inner block take (128 x 128 tiles).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // mbar_wait with the clock read rarely: reading it twice before the first try costs more than most waits here take.
 __device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity)
 {
@@ -627,7 +628,7 @@ struct Tiles {
                 }
                 work.done(I, lane);
             }
-            sent_all(lane);          // the block's memory outlives the copies from it
+            sent_all();          // the block's memory outlives the copies from it
         }
         if (!ok) {
             // A wait ran out: say so, and give copies and products in flight time to end before the block's memory

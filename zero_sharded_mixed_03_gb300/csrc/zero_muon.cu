@@ -515,11 +515,11 @@ struct MuonWork {
         }
         return true;
     }
-    // Lane 0 has sent the warp's tiles: once they are written, and so visible to it, one release of them all.
+    // One lane has sent the warp's tiles: once they are written, and so visible to it, its one release of them all.
     __device__ __forceinline__ void done(const Item& I, int lane) const
     {
-        sent_all(lane);
-        if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
+        sent_all();
+        if (elect_one()) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
     }
 
     // Is an inner block below the diagonal block (kBM * CG wide) of a symmetric operand's rows from `row` on?
@@ -726,19 +726,19 @@ struct MuonWork {
             if (c + 2 * kEpiCols < BN) fetch_adds(I, A, row0, c + 2 * kEpiCols, lane);
             // the warp's two tiles in turn, unless the low part needs one
             const uint32_t at = I.keep_low ? stage : stage + turn;
-            if (I.keep_low) sent_read<0>(lane);
-            else sent_read<1>(lane);
+            if (I.keep_low) sent_read<0>();
+            else sent_read<1>();
             if (I.kind != kNext && row0 == col0) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] += j == lane ? I.diag : 0.0f;
             }
             write_tile16<ZERO_FP16>(at, lane, x);
-            send_tile16(at, lane, I.maps + I.out, row0, col0);
+            send_tile16(at, I.maps + I.out, row0, col0);
             if (I.keep_low) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] = (x[j] - widen1<ZERO_FP16>(narrow1<ZERO_FP16>(x[j]))) * kLow;
                 write_tile16<ZERO_FP16>(stage + kTile16Bytes, lane, x);
-                send_tile16(stage + kTile16Bytes, lane, I.maps + kMapOutLow, row0, col0);
+                send_tile16(stage + kTile16Bytes, I.maps + kMapOutLow, row0, col0);
                 }
         }
     }
