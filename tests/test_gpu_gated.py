@@ -268,8 +268,9 @@ def test_gradient_against_differences():
         assert abs(got - want) <= 3.1 * 2.0 ** -11 * float((big[name] * v.abs()).sum()) + 1e-6, name
 
 
-def test_streams_and_graphs():
-    b = Block(90, 136, 200, "bf16", "in_out", pad=1, seed=5)       # rows off the 16-byte grid: copies as well
+@pytest.mark.parametrize("m,k,n", [(90, 136, 200), (40, 4096, 72), (130, 70, 6400)])
+def test_streams_and_graphs(m, k, n):
+    b = Block(m, k, n, "bf16", "in_out", pad=1, seed=5)            # rows off the 16-byte grid: copies as well
     call(b.args, False)
     call(b.args, True)
     torch.cuda.synchronize()
@@ -294,8 +295,9 @@ def test_streams_and_graphs():
     assert all(torch.equal(want[k], getattr(b, k)) for k in names)
 
 
-def test_repeats_are_the_same_bits():
-    b = Block(500, 1024, 1100, seed=6)
+@pytest.mark.parametrize("m,k,n", [(500, 1024, 1100), (40, 4096, 72), (3000, 70, 6400)])
+def test_repeats_are_the_same_bits(m, k, n):
+    b = Block(m, k, n, seed=6)
     out = []
     for _ in range(3):
         call(b.args, False)

@@ -384,6 +384,7 @@ __device__ __forceinline__ void sent_all()
 {
     if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
+
 // x += scale times the tile that is there.
 template <int DT>
 __device__ __forceinline__ void add_tile(uint32_t stage, int lane, float scale, float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
@@ -415,13 +416,14 @@ __device__ __forceinline__ void add_tile(uint32_t stage, int lane, float scale, 
 //   aside(lane)                             without a scout: what that warp does
 //   kScout, bool begin(Item, Seen&)         true: a warp of its own finds the items and waits for what they wait for
 //                                           (false: given up), ahead of the others, which take them from a queue
-//   load(Item, kb, a, b, bar, rank)      those copies
+//   load(Item, kb, a, b, bar, rank)         those copies
 //   a_mn(Item, kb), b_mn(Item, kb), idesc(Item, kb)   how a stage's operands lie, and the product's descriptor
 //   prepare(Item, quad, half, rank, lane, Ahead&)      what a tile's end may load before its products are done
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
-//   done(Item, lane)                                   by each of those warps after it
+//   done(Item)                                         by each of those warps after it
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
+
 // mbar_wait with the clock read rarely: reading it twice before the first try costs more than most waits here take.
 __device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity)
 {
@@ -488,7 +490,7 @@ struct Tiles {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
     }
 
-    // Item number `tile` of this block; every lane that `reads` it. One lane says that the warp has it.
+    // Item number `tile` of this block, to every lane that calls; one of them says that the warp has it.
     template <class W>
     __device__ __forceinline__ bool take(const W& work, int i, uint32_t tile, typename W::Item& I, bool whole_warp) const
     {
@@ -626,7 +628,7 @@ struct Tiles {
                     if constexpr (CG == 2) arrive_cluster(acc_empty_leader + 8 * acc);
                     else mbar_arrive(acc_empty0 + 8 * acc);
                 }
-                work.done(I, lane);
+                work.done(I);
             }
             sent_all();          // the block's memory outlives the copies from it
         }
