@@ -501,6 +501,28 @@ __device__ __forceinline__ void split_rows(const SplitParams& P, int64_t col, in
     }
 }
 
+// Rows copied to rows that start on 16 bytes, by block b of n: kCopies times eight elements a thread, all loaded before
+// any is stored.
+constexpr int kCopies = 2;
+
+__device__ __forceinline__ void copy_rows(const AlignJob& J, int b, int n, int thread)
+{
+    const int64_t per_row = (J.cols + 7) / 8, total = J.rows * per_row, step = (int64_t)n * 256;
+    for (int64_t i0 = (int64_t)b * 256 + thread; i0 < total; i0 += kCopies * step) {
+        uint4 v[kCopies];
+        int64_t to[kCopies];
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) {
+            const int64_t i = i0 + k * step, row = total < INT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row, col = (i - row * per_row) * 8;
+            to[k] = row * J.ld + col;
+            v[k] = i < total ? fetch8<false>(J.src + row * J.ld_src + col, (int)min((int64_t)8, J.cols - col)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k)
+            if (i0 + k * step < total) *reinterpret_cast<uint4*>(J.dst + to[k]) = v[k];
+    }
+}
+
 // A thread takes eight columns of a worker's rows (blocks of up to 2048 columns; narrower ones hold several
 // workers), so that the sums need no exchange.
 template <int DT>
@@ -514,7 +536,7 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ S
     if ((int)blockIdx.x >= P.blocks) {
         int b = blockIdx.x - P.blocks, which = 0;
         while (b >= P.copy_blocks[which]) b -= P.copy_blocks[which++];
-        align_rows(P.copy[which], b, P.copy_blocks[which]);
+        copy_rows(P.copy[which], b, P.copy_blocks[which], thread);
         return;
     }
     const int by = blockIdx.x / P.across, bx = blockIdx.x - by * P.across;
@@ -782,22 +804,24 @@ struct Cut {
     int64_t tickets() const { return tiles_in_parts() * kEpiWarps * shape.cg; }
 };
 
-// Products of m1 x n1 over kb1 inner blocks and `count2` of m2 x n2 over kb2.  A tile costs 1.2 us beside its inner blocks, a
-// part of one 2 us and a part's share of the sum more.
+// Products of m1 x n1 over kb1 inner blocks and `count2` of m2 x n2 over kb2.  A tile costs 3.8 us beside its inner blocks
+// (128 x 128: 1.5), a part of one 5 us (2.5) and a part's share of the sum more (with 1.2 for either tile, 300 tokens 2048 -> 2048
+// took 24.5 us instead of 12.3, gradients of 500 tokens 1024 -> 1024 22.8 instead of 16.6).
 Cut choose_cut(int64_t m1, int64_t n1, int64_t kb1, int64_t count2, int64_t m2, int64_t n2, int64_t kb2)
 {
     static const int kWays[] = {1, 2, 4, 8, 16, 32};
+    constexpr int kMostParts = 8;            // a worker: at most 160 MB of sums
     Cut best;
     double least = 1e30;
     for (const Shape& S : kShapes) {
         const int64_t tiles1 = S.rows(m1) * S.cols(n1), tiles2 = count2 * S.rows(m2) * S.cols(n2);
-        auto each = [&](int64_t kb, int splits) { return (double)kb * S.block_us + 1.2 + (splits > 1 ? 2.0 + 0.1 * splits : 0.0); };
+        auto each = [&](int64_t kb, int splits) { return (double)kb * S.block_us + (S.cg == 2 ? 3.8 : 1.5) + (splits > 1 ? (S.cg == 2 ? 5.0 : 2.5) + 0.15 * splits : 0.0); };
         for (const int ways1 : kWays) {
             const int64_t per1 = div_up(std::max<int64_t>(kb1, 1), ways1);
-            if (ways1 > 1 && (tiles1 == 0 || per1 < 4 || div_up(kb1, per1) != ways1 || tiles1 >= S.workers())) continue;
+            if (ways1 > 1 && (tiles1 == 0 || per1 < 4 || div_up(kb1, per1) != ways1 || tiles1 * ways1 >= kMostParts * S.workers())) continue;
             for (const int ways2 : kWays) {
                 const int64_t per2 = div_up(std::max<int64_t>(kb2, 1), ways2);
-                if (ways2 > 1 && (tiles2 == 0 || per2 < 4 || div_up(kb2, per2) != ways2 || tiles2 >= S.workers())) continue;
+                if (ways2 > 1 && (tiles2 == 0 || per2 < 4 || div_up(kb2, per2) != ways2 || tiles2 * ways2 >= kMostParts * S.workers())) continue;
                 double us = 0.0;
                 const Deal D = deal_out(S, tiles1 * ways1, each(per1, ways1), tiles2 * ways2, each(per2, ways2), &us);
                 if (us >= least) continue;
@@ -1020,7 +1044,7 @@ void plan_copies(const Gated& L, char* ws, const void* (&operand)[3], SplitParam
         J.ld = L.ld8[i];
         J.rows = i == 0 ? a.rows : L.w_rows;
         J.cols = i == 0 ? a.in_features : L.w_cols;
-        S->copy_blocks[i] = grid_of(J.rows * div_up(J.cols, 8), kGb300Sms, 8);
+        S->copy_blocks[i] = grid_of(div_up(J.rows * div_up(J.cols, 8), kCopies), kGb300Sms, 8);
         operand[i] = J.dst;
     }
 }
