@@ -654,14 +654,14 @@ typedef struct {
 } zero_gated_t;
 
 /* Bytes of device workspace that zero_gated (backward == 0) or zero_gated_backward needs for these sizes, strides
- * and pointers (their alignment counts): dg and du, their sums, and copies of operands whose rows do not start on 16
- * bytes.  Host-only.  0 is possible. */
+ * and pointers (their alignment counts): dg and du, their sums, partial sums of a long inner dimension where there are few
+ * tiles, and copies of operands whose rows do not start on 16 bytes.  Host-only.  0 is possible. */
 zero_status_t zero_gated_workspace(const zero_gated_t* a, int backward, int64_t* bytes);
 
 /* Forward of one gated block.  workspace: at least zero_gated_workspace bytes, 16-byte aligned (NULL if that is 0);
  * its contents need not survive between calls, but calls that may overlap on the GPU need one each.  ZERO_EINVAL /
- * ZERO_EALIGN / ZERO_ERANGE (a size beyond ZERO_LINEAR_MAX_SIZE, or a workspace that is too small) before anything is
- * enqueued.  rows == 0 does nothing; in_features == 0 gives g = bg and u = bu. */
+ * ZERO_EALIGN / ZERO_ERANGE (a size beyond ZERO_LINEAR_MAX_SIZE, a matrix of more than 2^42 elements, or a workspace that
+ * is too small) before anything is enqueued.  rows == 0 does nothing; in_features == 0 gives g = bg and u = bu. */
 zero_status_t zero_gated(const zero_gated_t* a, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Gradients of one gated block (see zero_gated_t); at least one of dx, dw_gate, dw_up, db_gate, db_up.  rows == 0

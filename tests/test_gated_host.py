@@ -54,6 +54,18 @@ def test_backward_refusals():
     refused(Z.ZERO_EINVAL, True, db_gate=1 << 23)
 
 
+@pytest.mark.timeout(20)
+@pytest.mark.parametrize("back", [False, True])
+def test_largest_sizes_are_laid_out_at_once(back):
+    """A size is refused where its matrices are beyond any memory, and the tiles of the largest are dealt without
+    looking at every way."""
+    refused(Z.ZERO_ERANGE, back, rows=1 << 30, in_features=1 << 30, out_features=1 << 30)
+    refused(Z.ZERO_ERANGE, back, rows=1, in_features=1 << 30, out_features=1 << 13)
+    large = args(rows=1 << 20, in_features=1 << 21, out_features=1 << 21)
+    # dg and du are 2^41 elements each
+    assert Z.zero_gated_workspace(large, back) >= (2 * 2 * (1 << 41) if back else 0)
+
+
 def test_workspace():
     assert Z.zero_gated_workspace(args()) == 0
     # rows that do not start on 16 bytes are copied: 2 bytes an element, rows rounded up to 8

@@ -781,7 +781,9 @@ Deal deal_out(const Shape& S, int64_t n1, double us1, int64_t n2, double us2, do
         return best;
     }
     *us = 1e30;
-    for (int64_t more = 0; more <= div_up(n2, w); ++more) {
+    // where both kinds of workers would end together, and whole numbers around it
+    const int64_t even = std::max<int64_t>(0, (int64_t)(((double)n2 - (double)(w - ahead) * us1 / us2) / (double)w) - 1);
+    for (int64_t more = even; more <= even + 3; ++more) {
         const int64_t left = std::max<int64_t>(0, n2 - more * ahead), rest = div_up(left, w - ahead);
         const double most = std::max(ahead > 0 ? (q + 1) * us1 + more * us2 : 0.0, q * us1 + rest * us2);
         if (most >= *us) continue;
@@ -911,6 +913,7 @@ SplitCut split_cut(int64_t rows, int64_t cols)
 }
 
 constexpr int64_t kMaxSize = ZERO_LINEAR_MAX_SIZE;   // tile coordinates stay 32-bit
+constexpr int64_t kMaxElements = (int64_t)1 << 42;   // so do counts of tiles
 
 // Everything a call needs, checked: strides filled in, and where its pieces lie in the workspace.
 struct Gated {
@@ -934,6 +937,8 @@ zero_status_t lay_out(const zero_gated_t* in, bool back, Gated* L, const char* w
     if (a.rows < 0 || a.in_features < 0 || a.out_features < 0) return fail(ZERO_EINVAL, w + "negative size");
     if (a.rows > kMaxSize || a.in_features > kMaxSize || a.out_features > kMaxSize)
         return fail(ZERO_ERANGE, w + "a size beyond ZERO_LINEAR_MAX_SIZE");
+    for (const int64_t n : {a.rows * a.in_features, a.rows * a.out_features, a.in_features * a.out_features})
+        if (n > kMaxElements) return fail(ZERO_ERANGE, w + "a matrix beyond 2^42 elements");
     if (a.dtype16 != ZERO_BF16 && a.dtype16 != ZERO_FP16) return fail(ZERO_EINVAL, w + "bad dtype16");
     if (a.layout != ZERO_WEIGHT_OUT_IN && a.layout != ZERO_WEIGHT_IN_OUT) return fail(ZERO_EINVAL, w + "bad layout");
     if (a.activation < ZERO_ACT_NONE || a.activation > ZERO_ACT_SILU) return fail(ZERO_EINVAL, w + "bad activation");
