@@ -856,8 +856,8 @@ zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, dou
  * stream: zero_muon_check, then zero_step of every bucket/unit, then zero_muon_step_with, then zero_step_finish.
  * zero_muon_check forms the momentum and marks the plan's step where it is not finite; it may come later, but before
  * zero_muon_step_with, in a step that is not offloaded.  The matrices' gradients are no part of the plan's norm and
- * are not clipped: a common factor of the gradients leaves X as it is.  ZERO_ESTATE out of this order; ZERO_EINVAL
- * where the two calls differ in momentum or flags. */
+ * are not clipped: a common factor of the gradients leaves X as it is.  ZERO_ESTATE out of this order, and where a
+ * zero_muon_step or a bind came between; ZERO_EINVAL where the two calls differ in momentum or flags. */
 zero_status_t zero_muon_check(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);
 zero_status_t zero_muon_step_with(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);
 

@@ -513,3 +513,24 @@ def test_joined_order():
         assert abs(norm - float(g.norm())) <= 1e-3 * norm
     finally:
         j.close()
+
+
+def test_joined_order_after_a_step_or_a_bind():
+    """What zero_muon_check formed is gone with a step of the handle's own or another bind."""
+    j, muon, s = Joined(), Z.muon_hyper(), stream()
+    try:
+        plan, mu, ptrs = j.g.plan, j.mu, [c.data_ptr() for c in j.c]
+        for spoil in (lambda: Z.zero_muon_step(mu.h, muon, 1.0, s), lambda: mu.bind(-1)):
+            Z.zero_muon_check(mu.h, plan, muon, s)
+            Z.zero_step(plan, ptrs, -1, Z.hyper(), s)
+            spoil()
+            with pytest.raises(Z.ZeroError) as e:
+                Z.zero_muon_step_with(mu.h, plan, muon, s)
+            assert e.value.status == Z.ZERO_ESTATE
+            # it joins the step again
+            Z.zero_muon_check(mu.h, plan, muon, s)
+            Z.zero_muon_step_with(mu.h, plan, muon, s)
+            Z.zero_step_finish(plan, s)
+        assert Z.zero_muon_read(mu.h, s).t == 3
+    finally:
+        j.close()

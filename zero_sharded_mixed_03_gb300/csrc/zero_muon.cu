@@ -1379,6 +1379,7 @@ try {
     if (e != cudaSuccess) return cuda_fail(e, "zero_muon_bind: the workspace's tables");
     for (int k = 0; k < 2; ++k) h->momentum[k] = momentum ? momentum[k] : nullptr;
     h->workspace = workspace;
+    h->checked_in = 0;                           // what a check left there is gone
     h->device = dev;
     h->bound = true;
     return ZERO_OK;
@@ -1398,6 +1399,7 @@ try {
     if (st != ZERO_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const MuonParams P = params(h, *hyper, loss_scale, R);
+    h->checked_in = 0;                           // the other half of the momentum is this step's now
     st = launch_reduce(h, P, s);
     return st == ZERO_OK ? launch_rest(h, P, *hyper, R, s) : st;
 }
