@@ -190,6 +190,14 @@ def test_few_tiles_and_a_long_sum(m, k, n, layout):
 
 
 @pytest.mark.parametrize("layout", ["out_in", "in_out"])
+@pytest.mark.parametrize("m,k,n", [(16, 4096, 9856), (140, 4096, 4900), (500, 8192, 4992), (1000, 4160, 2500)])
+def test_tiles_past_a_full_round(m, k, n, layout):
+    """Whole tiles, and the few that would not fill a round of the SMs in parts."""
+    for pad, keep in ((0, True), (3, False)):
+        Block(m, k, n, "bf16", layout, pad=pad, keep=keep, seed=k).check_forward()
+
+
+@pytest.mark.parametrize("layout", ["out_in", "in_out"])
 def test_whole_numbers_are_exact(layout):
     for act in ("none", "relu"):
         for m, k, n in ((1, 64, 72), (2, 512, 64), (200, 96, 300), (513, 64, 520), (130, 64, 4000)):

@@ -13,7 +13,7 @@
 // Measured on one GB300 (cuBLAS bf16: 1,939 TFLOP/s in a burst, 1,731 sustained under the power cap): 8192 tokens
 // 4096 -> 11008 with g and u kept 862 to 884 us, 1,690 TFLOP/s; their gradients 1,909 to 1,945, 1,530, of which 133 are dg
 // and du (HBM); 2048 tokens 2048 -> 8192 193 (dg and du 26, the rest 145 alone, tensor cores busy 89 %); 777 tokens
-// 1001 -> 1603, every row off the 16-byte grid, 36 to 38; one token 4096 -> 11008 29.5 (6.1 TB/s), 24 tokens 2048 -> 8192
+// 1001 -> 1603, every row off the 16-byte grid, 36; one token 4096 -> 11008 29.5 (6.1 TB/s), 24 tokens 2048 -> 8192
 // 14.7.  Tiles of few inner blocks are bound by their ends: 256 x 256 take 5 us with g and u kept, as long as 16 blocks.
 #include <cmath>
 #include <cstring>
@@ -52,8 +52,7 @@ struct GatedParams {
     Product part[MODE == kForward ? 1 : 3];   // forward: x, Wg and Wu (a[0], b[0], b[1]); backward: dx, dWg, dWu, those that are there
     Matrix16 out[3];             // forward: h, g, u (p NULL: not kept)
     const uint16_t* bias[2];     // forward: of g and u, or NULL
-    Deal deal;                   // backward: n1 tiles of dx (part[0]), n2 of the others, parts counted each
-    int32_t count;               // forward: tiles, parts counted each
+    Deal deal;                   // parts counted each.  Forward: n1 whole tiles, n2 parts of the others; backward: dx's (part[0]), the others'
     float4* partial;             // a part's sums: [tile][part][warp][..]
     uint32_t* tickets;           // [tile][warp]: parts that are there; 0 at first
     int32_t parts_at;            // backward: the first part that is a weight's gradient: 1 after dx, or 0
@@ -162,7 +161,7 @@ struct GatedWork {
     static constexpr int kBRows = BN / CG;
     struct Item {
         int m, n, kb, part;
-        int k0, slice, tile;     // the first inner block; which part; its tile among those in parts
+        int splits, k0, slice, tile;   // parts of the tile; the first inner block; which part; its tile among those in parts
     };
     // The biases of a tile's first part are loaded while its products run.
     struct Ahead {
@@ -183,33 +182,40 @@ struct GatedWork {
     static constexpr bool kScout = false;
     __device__ __forceinline__ void done(const Item&) const {}
 
-    __device__ __forceinline__ void range(int worker, int workers, int& i, int& end, int& step) const
+    __device__ __forceinline__ void range(int worker, int, int& i, int& end, int& step) const
     {
-        i = MODE == kForward ? worker : 0;
-        step = MODE == kForward ? workers : 1;
-        end = P.count;
-        if constexpr (MODE == kBackward) {
-            const Deal& D = P.deal;
-            const int n1 = worker < D.n1 ? (D.n1 - worker + D.w - 1) / D.w : 0;
+        const Deal& D = P.deal;
+        if constexpr (MODE == kForward) {
+            // in turn: the tiles of the first kind are whole rounds, or all there are
+            i = worker;
+            step = D.w;
+            end = D.n1 + D.n2;
+        } else {
+            i = 0;
+            step = 1;
+            end = worker < D.n1 ? (D.n1 - worker + D.w - 1) / D.w : 0;
             // of the second kind: the places that it has, up to the last tile
             const int first = worker < D.ahead ? worker : D.ahead * D.more + worker - D.ahead;
             const int stride = worker < D.ahead ? D.ahead : D.w - D.ahead, most = worker < D.ahead ? D.more : D.rest;
-            end = n1 + (first < D.n2 ? min(most, (D.n2 - first + stride - 1) / stride) : 0);
+            if (first < D.n2) end += min(most, (D.n2 - first + stride - 1) / stride);
         }
     }
 
     __device__ __forceinline__ Item item(int i) const
     {
+        const Deal& D = P.deal;
         Item I;
         I.part = 0;
-        int tile = i;
-        if constexpr (MODE == kBackward) {
-            const Deal& D = P.deal;
-            const int worker = blockIdx.x / CG, n1 = worker < D.n1 ? (D.n1 - worker + D.w - 1) / D.w : 0;
-            if (i < n1) {
-                tile = worker + i * D.w;
-            } else {
-                const int stride = worker < D.ahead ? D.ahead : D.w - D.ahead;
+        int tile, splits = P.part[0].splits;
+        if constexpr (MODE == kForward) {
+            tile = i;
+            if (i < D.n1) splits = 1;
+            else tile -= D.n1;
+        } else {
+            const int worker = blockIdx.x / CG;
+            tile = worker + i * D.w;
+            if (tile >= D.n1) {
+                const int n1 = worker < D.n1 ? (D.n1 - worker + D.w - 1) / D.w : 0, stride = worker < D.ahead ? D.ahead : D.w - D.ahead;
                 tile = (worker < D.ahead ? worker : D.ahead * D.more + worker - D.ahead) + (i - n1) * stride;
                 I.part = P.parts_at;
                 const int per = P.part[I.part].tiles_m * P.part[I.part].tiles_n * P.part[I.part].splits;
@@ -217,18 +223,22 @@ struct GatedWork {
                     tile -= per;
                     ++I.part;
                 }
+                splits = P.part[I.part].splits;
             }
         }
         const Product& Q = P.part[I.part];
+        I.splits = splits;
         I.slice = 0;
-        if (Q.splits > 1) {
-            I.slice = tile % Q.splits;
-            tile /= Q.splits;
+        I.kb = Q.k_blocks;
+        if (splits > 1) {
+            I.slice = tile % splits;
+            tile /= splits;
+            I.kb = min(Q.k_blocks - I.slice * Q.k_per_split, Q.k_per_split);
         }
-        I.tile = Q.tile0 + tile;
-        tile_at(Q.tiles_m, Q.tiles_n, tile, I.m, I.n);
         I.k0 = I.slice * Q.k_per_split;
-        I.kb = min(Q.k_blocks - I.k0, Q.k_per_split);
+        I.tile = Q.tile0 + tile;
+        if (MODE == kForward && i >= D.n1) tile += D.n1;
+        tile_at(Q.tiles_m, Q.tiles_n, tile, I.m, I.n);
         return I;
     }
     __device__ __forceinline__ uint32_t bytes(const Item& I) const { return CG * ((P.part[I.part].a_mn ? kBM : P.a_rows) + kBRows) * (kBK * 2); }
@@ -292,7 +302,7 @@ struct GatedWork {
     __device__ __forceinline__ float4* sums_at(const Item& I, int slice, int warp, int rank) const
     {
         const Product& Q = P.part[I.part];
-        const int64_t part = Q.part0 + (int64_t)(I.tile - Q.tile0) * Q.splits + slice;
+        const int64_t part = Q.part0 + (int64_t)(I.tile - Q.tile0) * I.splits + slice;
         return P.partial + ((part * CG + rank) * kEpiWarps + warp) * (kParts * 8 * 32);
     }
 
@@ -314,14 +324,13 @@ struct GatedWork {
         if (lane == 0) before = atomicAdd(P.tickets + ((int64_t)I.tile * CG + rank) * kEpiWarps + warp, 1u);
         before = __shfl_sync(0xFFFFFFFFu, before, 0);
         __threadfence();
-        return before == (uint32_t)P.part[I.part].splits - 1;
+        return before == (uint32_t)I.splits - 1;
     }
 
     // Results `part` of the warp: from TMEM, or the sum of all parts.
     __device__ __forceinline__ void results(const Item& I, uint32_t at, int part, int warp, int rank, int lane, float (&x)[32]) const
     {
-        const int splits = P.part[I.part].splits;
-        if (splits == 1) {
+        if (I.splits == 1) {
             tmem_load32(at, x);
             return;
         }
@@ -329,10 +338,7 @@ struct GatedWork {
         for (int j = 0; j < 32; ++j) x[j] = 0.0f;
         const float4* q = sums_at(I, 0, warp, rank) + part * (8 * 32) + lane;
         const int64_t next = (int64_t)CG * kEpiWarps * (kParts * 8 * 32);
-        for (int s = 0; s < splits; ++s, q += next) {
-            float4 v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __ldcg(q + j * 32);
+        auto add = [&](const float4 (&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[4 * j] += v[j].x;
@@ -340,6 +346,23 @@ struct GatedWork {
                 x[4 * j + 2] += v[j].z;
                 x[4 * j + 3] += v[j].w;
             }
+        };
+        // in order, two at a time: what a part costs is the way to L2
+        int s = 0;
+        for (; s + 2 <= I.splits; s += 2, q += 2 * next) {
+            float4 v[8], w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __ldcg(q + j * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __ldcg(q + next + j * 32);
+            add(v);
+            add(w);
+        }
+        if (s < I.splits) {
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __ldcg(q + j * 32);
+            add(v);
         }
     }
 
@@ -347,13 +370,14 @@ struct GatedWork {
     {
         const int64_t row0 = ((int64_t)I.m * CG + rank) * kBM + quad * 32;
         const int warp = quad + 4 * half;
-        if (P.part[I.part].splits > 1 && !keep_part(I, acc, half, warp, rank, lane)) return;
+        if (row0 >= (MODE == kForward ? P.out[0].rows : P.part[I.part].out.rows)) return;
+        if (I.splits > 1 && !keep_part(I, acc, half, warp, rank, lane)) return;
         int part = 0;
         if constexpr (MODE == kForward) {
             const Matrix16& H = P.out[0];
             for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols, part += 2) {
                 const int64_t col0 = (int64_t)I.n * kWidth + c;
-                if (col0 >= H.cols || row0 >= H.rows) break;
+                if (col0 >= H.cols) break;
                 float g[32], u[32];
                 results(I, acc + c, part, warp, rank, lane, g);
                 results(I, acc + kWidth + c, part + 1, warp, rank, lane, u);
@@ -373,7 +397,7 @@ struct GatedWork {
             const bool add = P.accumulate && I.part >= P.parts_at;
             for (int c = half * kEpiCols; c < kWidth; c += 2 * kEpiCols, ++part) {
                 const int64_t col0 = (int64_t)I.n * BN + c;
-                if (col0 >= D.cols || row0 >= D.rows) break;
+                if (col0 >= D.cols) break;
                 float x[32];
                 results(I, acc + c, part, warp, rank, lane, x);
                 if (add) add_tile<DT>(stage + kTile16Bytes, lane, 1.0f, x, D, row0, col0);
@@ -575,6 +599,13 @@ __global__ void __launch_bounds__(256, 3) split_kernel(const __grid_constant__ S
     q = reinterpret_cast<float4*>(P.sums + ((int64_t)by * 2 + 1) * P.ld + col);
     q[0] = s[2];
     q[1] = s[3];
+}
+
+// The tickets alone, where nothing else precedes the products.
+__global__ void __launch_bounds__(256) gated_tickets_kernel(uint32_t* tickets, int n)
+{
+    after_earlier_work();
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) tickets[i] = 0;
 }
 
 // The biases' gradients where no product is asked for: a warp 32 columns.
@@ -794,50 +825,80 @@ Deal deal_out(const Shape& S, int64_t n1, double us1, int64_t n2, double us2, do
     return best;
 }
 
-// How a launch is cut: the tiles' shape, and the parts of the inner dimension of either kind of product.
+// How a launch is cut: the tiles' shape, and of either kind how many there are and the parts of their inner dimension.
 struct Cut {
     Shape shape = kShapes[0];
     int64_t tiles1 = 0, tiles2 = 0;
     int splits1 = 1, splits2 = 1, per1 = 1, per2 = 1;
     Deal deal{0, 0, 1, 0, 0, 0};
+    double us = 1e30;
     int64_t tiles_in_parts() const { return (splits1 > 1 ? tiles1 : 0) + (splits2 > 1 ? tiles2 : 0); }
     int64_t partial_bytes() const { return (splits1 > 1 ? tiles1 * splits1 : 0) * tile_bytes() + (splits2 > 1 ? tiles2 * splits2 : 0) * tile_bytes(); }
     int64_t tile_bytes() const { return 4ll * kBM * shape.cg * shape.bn; }
     int64_t tickets() const { return tiles_in_parts() * kEpiWarps * shape.cg; }
 };
 
-// Products of m1 x n1 over kb1 inner blocks and `count2` of m2 x n2 over kb2.  A tile costs 3.8 us beside its inner blocks
-// (128 x 128: 1.5), a part of one 5 us (2.5) and a part's share of the sum more (with 1.2 for either tile, 300 tokens 2048 -> 2048
-// took 24.5 us instead of 12.3, gradients of 500 tokens 1024 -> 1024 22.8 instead of 16.6).
+// One tile, or one part of `splits`, of kb inner blocks: 256 x 256 cost 3.8 us beside them (128 x 128: 1.5), a part 5 us (2.5)
+// more and its share of the sum (with 1.2 for either tile, 300 tokens 2048 -> 2048 took 24.5 us instead of 12.3,
+// gradients of 500 tokens 1024 -> 1024 22.8 instead of 16.6).
+double tile_us(const Shape& S, int64_t kb, int splits)
+{
+    return (double)kb * S.block_us + (S.cg == 2 ? 3.8 : 1.5) + (splits > 1 ? (S.cg == 2 ? 5.0 : 2.5) + 0.15 * splits : 0.0);
+}
+
+// May n tiles of kb inner blocks be in `ways` parts?  Each has four blocks at least; a worker at most 8 parts, 160 MB of
+// sums in all.
+bool divides(const Shape& S, int64_t n, int64_t kb, int ways, int64_t* per)
+{
+    *per = div_up(std::max<int64_t>(kb, 1), ways);
+    return ways == 1 || (n > 0 && *per >= 4 && div_up(kb, *per) == ways && n * ways < 8 * S.workers());
+}
+
+// Tiles of two kinds, in parts or whole, and end_us after them, where that is sooner done than *best.
+void consider(const Shape& S, int64_t n1, int64_t kb1, int ways1, int64_t n2, int64_t kb2, int ways2, double end_us, Cut* best)
+{
+    int64_t per1, per2;
+    if (!divides(S, n1, kb1, ways1, &per1) || !divides(S, n2, kb2, ways2, &per2)) return;
+    double us = 0.0;
+    const Deal D = deal_out(S, n1 * ways1, tile_us(S, per1, ways1), n2 * ways2, tile_us(S, per2, ways2), &us);
+    us += end_us;
+    if (us >= best->us) return;
+    best->us = us;
+    best->shape = S;
+    best->tiles1 = n1;
+    best->tiles2 = n2;
+    best->splits1 = ways1;
+    best->splits2 = ways2;
+    best->per1 = (int)per1;
+    best->per2 = (int)per2;
+    best->deal = D;
+}
+
+// Products of m1 x n1 over kb1 inner blocks and `count2` of m2 x n2 over kb2.
 Cut choose_cut(int64_t m1, int64_t n1, int64_t kb1, int64_t count2, int64_t m2, int64_t n2, int64_t kb2)
 {
     static const int kWays[] = {1, 2, 4, 8, 16, 32};
-    constexpr int kMostParts = 8;            // a worker: at most 160 MB of sums
     Cut best;
-    double least = 1e30;
+    for (const Shape& S : kShapes)
+        for (const int ways1 : kWays)
+            for (const int ways2 : kWays)
+                consider(S, S.rows(m1) * S.cols(n1), kb1, ways1, count2 * S.rows(m2) * S.cols(n2), kb2, ways2, 0.0, &best);
+    return best;
+}
+
+// One product: whole tiles, and parts of those that would not fill a round (or of all).  The last sums are nothing's to
+// hide behind: 0.25 us a part (256 x 256 tiles 0.55) and 0.03 (0.08) for each tile in parts.  16 tokens 4096 -> 11008,
+// 172 tiles for 152 workers, 42 -> 37 us; 64 tokens 8192 -> 256, four tiles, 30 -> 13.7.
+Cut choose_cut(int64_t m, int64_t n, int64_t kb)
+{
+    constexpr int kMostWays = 32;
+    Cut best;
     for (const Shape& S : kShapes) {
-        const int64_t tiles1 = S.rows(m1) * S.cols(n1), tiles2 = count2 * S.rows(m2) * S.cols(n2);
-        auto each = [&](int64_t kb, int splits) { return (double)kb * S.block_us + (S.cg == 2 ? 3.8 : 1.5) + (splits > 1 ? (S.cg == 2 ? 5.0 : 2.5) + 0.15 * splits : 0.0); };
-        for (const int ways1 : kWays) {
-            const int64_t per1 = div_up(std::max<int64_t>(kb1, 1), ways1);
-            if (ways1 > 1 && (tiles1 == 0 || per1 < 4 || div_up(kb1, per1) != ways1 || tiles1 * ways1 >= kMostParts * S.workers())) continue;
-            for (const int ways2 : kWays) {
-                const int64_t per2 = div_up(std::max<int64_t>(kb2, 1), ways2);
-                if (ways2 > 1 && (tiles2 == 0 || per2 < 4 || div_up(kb2, per2) != ways2 || tiles2 * ways2 >= kMostParts * S.workers())) continue;
-                double us = 0.0;
-                const Deal D = deal_out(S, tiles1 * ways1, each(per1, ways1), tiles2 * ways2, each(per2, ways2), &us);
-                if (us >= least) continue;
-                least = us;
-                best.shape = S;
-                best.tiles1 = tiles1;
-                best.tiles2 = tiles2;
-                best.splits1 = ways1;
-                best.splits2 = ways2;
-                best.per1 = (int)per1;
-                best.per2 = (int)per2;
-                best.deal = D;
-            }
-        }
+        const int64_t tiles = S.rows(m) * S.cols(n), over = tiles % S.workers();
+        consider(S, tiles, kb, 1, 0, 0, 1, 0.0, &best);
+        for (const int64_t parted : {over, tiles})
+            for (int ways = 2; ways <= kMostWays; ++ways)
+                consider(S, tiles - parted, kb, 1, parted, kb, ways, ways * (S.cg == 2 ? 0.55 + 0.08 * (double)parted : 0.25 + 0.03 * (double)parted), &best);
     }
     return best;
 }
@@ -848,8 +909,7 @@ zero_status_t launch_gated(const GatedParams<MODE>& P, cudaStream_t s)
     using S = GemmShape<CG, BN>;
     const cudaError_t set = allow_shared<gated_kernel<CG, BN, MODE, DT>>(S::kSmem);
     if (set != cudaSuccess) return cuda_fail(set, "zero_gated: shared memory");
-    const int grid = CG * (MODE == kForward ? (int)std::min<int64_t>(kGb300Sms / CG, P.count) : P.deal.w);
-    const cudaError_t e = launch_after(gated_kernel<CG, BN, MODE, DT>, grid, kGemmThreads, S::kSmem, s, P);
+    const cudaError_t e = launch_after(gated_kernel<CG, BN, MODE, DT>, CG * P.deal.w, kGemmThreads, S::kSmem, s, P);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
 }
 
@@ -1012,7 +1072,7 @@ zero_status_t lay_out(const zero_gated_t* in, bool back, Gated* L, const char* w
         const int weights = (a.dw_gate != nullptr) + (a.dw_up != nullptr);
         const int64_t kb_k = div_up(a.in_features, kBK), kb_n = div_up(a.out_features, kBK), kb_m = div_up(a.rows, kBK);
         L->tiles = back ? choose_cut(a.dx ? a.rows : 0, a.in_features, 2 * kb_n, weights, L->w_rows, L->w_cols, kb_m)
-                        : choose_cut(a.rows, 2 * a.out_features, kb_k, 0, 0, 0, 0);
+                        : choose_cut(a.rows, 2 * a.out_features, kb_k);
         if (L->tiles.partial_bytes() > 0) {
             L->at_partial = take(L->tiles.partial_bytes());
             L->at_tickets = take(4 * L->tiles.tickets());
@@ -1032,11 +1092,13 @@ zero_status_t check_workspace(const Gated& L, const void* workspace, int64_t byt
     return ZERO_OK;
 }
 
-// The copies that the call needs, into S; the operands become theirs.
+// The copies that the call needs, and its tickets, into S; the operands become theirs.
 void plan_copies(const Gated& L, char* ws, const void* (&operand)[3], SplitParams* S)
 {
     const zero_gated_t& a = L.a;
     std::memset(S, 0, sizeof(*S));
+    S->tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
+    S->n_tickets = (int32_t)L.tiles.tickets();
     const int64_t ld[3] = {a.ld_x, a.ld_w_gate, a.ld_w_up};
     const void* source[3] = {a.x, a.w_gate, a.w_up};
     for (int i = 0; i < 3; ++i) {
@@ -1057,10 +1119,14 @@ void plan_copies(const Gated& L, char* ws, const void* (&operand)[3], SplitParam
 zero_status_t launch_split(const Gated& L, const SplitParams& S, cudaStream_t s)
 {
     const int64_t blocks = (int64_t)S.blocks + S.copy_blocks[0] + S.copy_blocks[1] + S.copy_blocks[2];
-    if (blocks == 0) return ZERO_OK;
+    cudaError_t e = cudaSuccess;
+    if (blocks == 0) {
+        if (S.n_tickets > 0) e = launch_after(gated_tickets_kernel, grid_of(S.n_tickets, kGb300Sms, 1), 256, 0, s, S.tickets, (int)S.n_tickets);
+        return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
+    }
     const dim3 threads(L.cut.tx, L.cut.ty);
-    const cudaError_t e = L.bf ? launch_after(split_kernel<ZERO_BF16>, (unsigned)blocks, threads, 0, s, S)
-                               : launch_after(split_kernel<ZERO_FP16>, (unsigned)blocks, threads, 0, s, S);
+    e = L.bf ? launch_after(split_kernel<ZERO_BF16>, (unsigned)blocks, threads, 0, s, S)
+             : launch_after(split_kernel<ZERO_FP16>, (unsigned)blocks, threads, 0, s, S);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
 }
 
@@ -1156,9 +1222,10 @@ try {
         const cudaError_t e = L.bf ? launch_after(gated_empty_kernel<ZERO_BF16>, grid, 256, 0, s, P) : launch_after(gated_empty_kernel<ZERO_FP16>, grid, 256, 0, s, P);
         return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_gated: launch");
     }
+    char* ws = static_cast<char*>(workspace);
     const void* operand[3];
     SplitParams S;
-    plan_copies(L, static_cast<char*>(workspace), operand, &S);
+    plan_copies(L, ws, operand, &S);
     st = launch_split(L, S, s);
     if (st != ZERO_OK) return st;
     const Shape c = L.tiles.shape;
@@ -1174,16 +1241,11 @@ try {
     Q.k_blocks = (int32_t)div_up(a.in_features, kBK);
     Q.b_mn = in_out;
     Q.idesc = product_desc(L.bf, false, in_out, c);
-    P.count = Q.tiles_m * Q.tiles_n * L.tiles.splits1;
-    int64_t tiles = 0, parts = 0;
-    set_parts(&Q, L.tiles.splits1, L.tiles.per1, &tiles, &parts);
-    if (L.tiles.splits1 > 1) {
-        char* ws = static_cast<char*>(workspace);
-        P.partial = reinterpret_cast<float4*>(ws + L.at_partial);
-        P.tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
-        const cudaError_t e = cudaMemsetAsync(P.tickets, 0, (size_t)(4 * L.tiles.tickets()), s);
-        if (e != cudaSuccess) return cuda_fail(e, "zero_gated: memset");
-    }
+    Q.splits = L.tiles.splits2;
+    Q.k_per_split = L.tiles.per2;
+    P.deal = L.tiles.deal;
+    P.partial = reinterpret_cast<float4*>(ws + L.at_partial);
+    P.tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
     return launch_gated<kForward>(P, c, L.bf, s);
 }
 catch (...) {
@@ -1234,8 +1296,6 @@ try {
         S.chunk = L.cut.chunk;
         S.across = (int32_t)div_up(n, (int64_t)L.cut.tx * 8);
         S.blocks = (int32_t)(S.across * L.cut.groups());
-        S.tickets = reinterpret_cast<uint32_t*>(ws + L.at_tickets);
-        S.n_tickets = (int32_t)L.tiles.tickets();
     }
     st = launch_split(L, S, s);
     if (st != ZERO_OK) return st;
