@@ -401,7 +401,8 @@ struct GatedWork {
                 float x[32];
                 results(I, acc + c, part, warp, rank, lane, x);
                 if (add) add_tile<DT>(stage + kTile16Bytes, lane, 1.0f, x, D, row0, col0);
-                put_tile<DT>(stage, lane, x, D, row0, col0);
+                // of few rows, the weights' gradients are little but this: 128 tokens, 4096 -> 11008, 73 -> 62 us for both
+                put_tile<DT, true>(stage, lane, x, D, row0, col0);
             }
         }
     }
@@ -791,8 +792,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewResident) gated_few_deep_k
 
 // ------------------------------------------------------------------ host
 
-// The shape of the tiles: 256 x 256 on a pair of SMs, an inner block of which takes 0.31 us, or 128 x 128 on one, 0.23,
-// whichever is sooner done.
+// The shape of the tiles: 256 x 256 on a pair of SMs, an inner block of which takes 0.31 us, or 128 x 128 on one, 0.22 to
+// 0.3, the more SMs load the more, whichever is sooner done (with 0.23 gradients of 300 tokens 2000 -> 5000 took 57 us
+// instead of 46, of 2500 tokens 768 -> 2048 45 instead of 41).
 struct Shape {
     int cg, bn;
     double block_us;
@@ -800,7 +802,7 @@ struct Shape {
     int64_t rows(int64_t m) const { return div_up(m, kBM * cg); }
     int64_t cols(int64_t n) const { return div_up(n, bn); }
 };
-constexpr Shape kShapes[] = {{2, 256, 0.31}, {1, 128, 0.23}};
+constexpr Shape kShapes[] = {{2, 256, 0.31}, {1, 128, 0.25}};
 
 // n1 items of us1 and n2 of us2 dealt so that the worker with most has least; *us: its time.
 Deal deal_out(const Shape& S, int64_t n1, double us1, int64_t n2, double us2, double* us)

@@ -269,10 +269,20 @@ constexpr int kTile16Bytes = 32 * 64;
 
 __device__ __forceinline__ uint32_t tile16_at(uint32_t stage, int row, int piece) { return stage + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
 
-// The tile in shared memory to global memory; what is past the matrix is left out.
+// The tile in shared memory to global memory; what is past the matrix is left out.  WHOLE: with a way for tiles that are
+// all inside (loads, then stores, and no branch between them), for kernels that little else bounds: more instructions.
+template <bool WHOLE>
 __device__ __forceinline__ void store_tile16(uint32_t stage, int lane, const Matrix16& D, int64_t row0, int64_t col0)
 {
-    if (D.vec) {
+    if (WHOLE && D.vec && row0 + 32 <= D.rows && col0 + 32 <= D.cols) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w) : "r"(tile16_at(stage, i * 8 + (lane >> 2), lane & 3)) : "memory");
+        uint16_t* q = D.p + (row0 + (lane >> 2)) * D.ld + col0 + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i, q += 8 * D.ld) *reinterpret_cast<uint4*>(q) = v[i];
+    } else if (D.vec) {
         const int64_t col = col0 + (lane & 3) * 8;
         const int n = (int)max((int64_t)0, min((int64_t)8, D.cols - col));
 #pragma unroll
@@ -350,12 +360,12 @@ __device__ __forceinline__ void write_tile16(uint32_t stage, int lane, const flo
 }
 
 // The same tile at (row0, col0) of a matrix, through shared memory, so that a store instruction writes whole sectors.
-template <int DT>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void put_tile(uint32_t stage, int lane, const float (&x)[32], const Matrix16& D, int64_t row0, int64_t col0)
 {
     write_tile16<DT>(stage, lane, x);
     __syncwarp();
-    store_tile16(stage, lane, D, row0, col0);
+    store_tile16<WHOLE>(stage, lane, D, row0, col0);
     __syncwarp();
 }
 
