@@ -890,7 +890,8 @@ Cut choose_cut(int64_t m1, int64_t n1, int64_t kb1, int64_t count2, int64_t m2, 
 
 // One product: whole tiles, and parts of those that would not fill a round (or of all).  The last sums are nothing's to
 // hide behind: 0.25 us a part (256 x 256 tiles 0.55) and 0.03 (0.08) for each tile in parts.  16 tokens 4096 -> 11008,
-// 172 tiles for 152 workers, 42 -> 37 us; 64 tokens 8192 -> 256, four tiles, 30 -> 13.7.
+// 172 tiles for 152 workers, 42 -> 37 us; 64 tokens 8192 -> 256, four tiles, 30 -> 13.7.  Less than a hundredth is not
+// worth the sums: 8192 tokens 4096 -> 11008, 16 tiles beyond 36 rounds, lose 10 us by them.
 Cut choose_cut(int64_t m, int64_t n, int64_t kb)
 {
     constexpr int kMostWays = 32;
@@ -898,9 +899,10 @@ Cut choose_cut(int64_t m, int64_t n, int64_t kb)
     for (const Shape& S : kShapes) {
         const int64_t tiles = S.rows(m) * S.cols(n), over = tiles % S.workers();
         consider(S, tiles, kb, 1, 0, 0, 1, 0.0, &best);
+        const double margin = 0.01 * tile_us(S, kb, 1) * (double)div_up(tiles, S.workers());
         for (const int64_t parted : {over, tiles})
             for (int ways = 2; ways <= kMostWays; ++ways)
-                consider(S, tiles - parted, kb, 1, parted, kb, ways, ways * (S.cg == 2 ? 0.55 + 0.08 * (double)parted : 0.25 + 0.03 * (double)parted), &best);
+                consider(S, tiles - parted, kb, 1, parted, kb, ways, margin + ways * (S.cg == 2 ? 0.55 + 0.08 * (double)parted : 0.25 + 0.03 * (double)parted), &best);
     }
     return best;
 }
