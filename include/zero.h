@@ -775,8 +775,9 @@ zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double
  *   zero_step_finish
  * zero_adamw_check reads h's gradients over the plan's loss scale and adds their sum of squares to the plan's norm,
  * where that is formed; a sum that is not finite marks the plan's step, which is then skipped whole (and its loss
- * scale backed off) as for a gradient of the plan's that is not.  It may come later, but before
- * zero_adamw_step_with, in a step that neither clips nor is offloaded.  zero_adamw_step_with applies h's update, gradients over the plan's
+ * scale backed off) as for a gradient of the plan's that is not.  It may come later in a step that neither clips nor
+ * is offloaded, but before every zero_adamw_step_with and zero_muon_step_with of it: what those have moved could not be
+ * left out any more.  zero_adamw_step_with applies h's update, gradients over the plan's
  * loss scale and times its clipping coefficient, unless the plan's step is marked or a bounded wait of it ran out.
  * zero_adamw_read: grad_norm is -1, the plan's result has the norm of both.  ZERO_ESTATE out of this order.  Not
  * with zero_step_units_overlapped, which finishes the step itself. */
@@ -854,8 +855,8 @@ zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, dou
 /* A step that h makes together with a plan's, applied or left out as one, with the plan's loss scale (as
  * zero_adamw_check and zero_adamw_step_with, of which both may be part of the same step).  In the plan's step, on its
  * stream: zero_muon_check, then zero_step of every bucket/unit, then zero_muon_step_with, then zero_step_finish.
- * zero_muon_check forms the momentum and marks the plan's step where it is not finite; it may come later, but before
- * zero_muon_step_with, in a step that is not offloaded.  The matrices' gradients are no part of the plan's norm and
+ * zero_muon_check forms the momentum and marks the plan's step where it is not finite; it may come later in a step that
+ * is not offloaded, but before every zero_muon_step_with and zero_adamw_step_with of it.  The matrices' gradients are no part of the plan's norm and
  * are not clipped: a common factor of the gradients leaves X as it is.  ZERO_ESTATE out of this order, and where a
  * zero_muon_step or a bind came between; ZERO_EINVAL where the two calls differ in momentum or flags. */
 zero_status_t zero_muon_check(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);

@@ -1132,6 +1132,7 @@ try {
     if (h->checked_in == plan->step_no) return fail(ZERO_ESTATE, "zero_adamw_check: already part of this step");
     if (plan->in_step && (plan->offload || plan->step_hyper.max_grad_norm > 0.0))
         return fail(ZERO_ESTATE, "zero_adamw_check: must precede the first bucket/unit of a step that clips or is offloaded");
+    if (plan->moved_in == plan->step_no) return fail(ZERO_ESTATE, "zero_adamw_check: a part of this step, which it could not leave out, is enqueued");
     AdamParams P = adam_params(h);
     P.plan = reinterpret_cast<DevState*>(plan->workspace);
     launch_norm<true>(h, P, static_cast<cudaStream_t>(stream));
@@ -1160,6 +1161,7 @@ try {
     AdamParams P = adam_params(h);
     set_hyper(P, *hyper, 1.0);
     P.plan = reinterpret_cast<DevState*>(plan->workspace);
+    plan->moved_in = plan->step_no;
     launch_adamw(h, P, static_cast<cudaStream_t>(stream));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "zero_adamw_step_with: launch");

@@ -146,6 +146,7 @@ struct zero_plan {
     bool in_step = false;
     bool stepped = false;               // a step has been enqueued since the plan was bound
     int64_t step_no = zero::next_step_number();   // the open or coming step's (zero_adamw_check)
+    int64_t moved_in = 0;               // the last step of which a zero_*_step_with was enqueued
     std::vector<char> covered;          // per bucket / unit in the open step
     std::vector<char> norm_covered;     // per bucket / unit: gradient-norm pre-pass done
     bool norm_open = false;             // a norm pre-pass of the next step has been issued

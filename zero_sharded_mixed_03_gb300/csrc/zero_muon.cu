@@ -1416,6 +1416,7 @@ try {
     if (h->checked_in == plan->step_no) return fail(ZERO_ESTATE, "zero_muon_check: already part of this step");
     if (plan->in_step && plan->offload)
         return fail(ZERO_ESTATE, "zero_muon_check: must precede the first bucket/unit of a step that is offloaded");
+    if (plan->moved_in == plan->step_no) return fail(ZERO_ESTATE, "zero_muon_check: a part of this step, which it could not leave out, is enqueued");
     MuonParams P = params(h, *hyper, 1.0, R);
     P.plan = reinterpret_cast<DevState*>(plan->workspace);
     st = launch_reduce(h, P, static_cast<cudaStream_t>(stream));
@@ -1444,6 +1445,7 @@ try {
         return fail(ZERO_EINVAL, "zero_muon_step_with: one step has one momentum and one set of flags");
     MuonParams P = params(h, *hyper, 1.0, R);
     P.plan = reinterpret_cast<DevState*>(plan->workspace);
+    plan->moved_in = plan->step_no;
     st = launch_rest(h, P, *hyper, R, static_cast<cudaStream_t>(stream));
     if (st != ZERO_OK) return st;
     h->stepped_in = plan->step_no;
