@@ -456,7 +456,8 @@ __device__ __forceinline__ void split_each(const float (&d)[8], float (&g)[8], f
     for (int j = 0; j < 8; ++j) {
         const float a = act_value(g[j], ACT), s = act_slope(g[j], ACT), up = u[j];
         u[j] = d[j] * a;
-        g[j] = d[j] * up * s;
+        // the slope, at most 1.2, before dh: dh u alone may leave fp32's range in bf16 (and a slope of 0 then made it NaN)
+        g[j] = d[j] * (up * s);
     }
 }
 
