@@ -506,7 +506,11 @@ struct Tiles {
     {
         if constexpr (W::kScout) {
             const uint32_t slot = tile % kQueue, at = queue0 + slot * kItemBytes;
-            if (!stage_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1)) return false;
+            bool there = stage_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1);
+            // a warp has the item or gives up as one: the item may come as some lanes' waits run out, and the others
+            // would wait for them below
+            if (whole_warp) there = __all_sync(0xFFFFFFFFu, there);
+            if (!there) return false;
             uint32_t w[kItemBytes / 4];
 #pragma unroll
             for (int j = 0; j < kItemBytes / 16; ++j)
@@ -623,7 +627,6 @@ struct Tiles {
                 const uint32_t acc = tile & 1, use = tile >> 1;
                 typename W::Item I;
                 ok = take(work, i, tile, I, true);
-                ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 typename W::Ahead ahead;
                 work.prepare(I, quad, half, (int)rank, lane, ahead);
