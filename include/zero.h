@@ -280,8 +280,9 @@ zero_status_t zero_grad_norm(zero_plan_t* plan, const void* const* grad_contribs
 zero_status_t zero_step_finish(zero_plan_t* plan, void* stream, zero_step_result_t* out);
 
 /* Read the device-resident step state (synchronises `stream`).  zero_read_state and
- * zero_step_finish (out != NULL) return ZERO_ETIMEOUT, with *out filled, when a wait of a
- * bulk-staged kernel (step or gather) ran out since the state was last read: every step
+ * the finishes (out != NULL) return ZERO_ETIMEOUT, with *out filled, when a wait of a
+ * bulk-staged kernel (step or gather), or of another optimizer's part of a step
+ * (zero_muon_step_with), ran out since the state was last read: every step
  * finished since then was discarded (state, t, loss scale and counters unchanged; 16-bit
  * parameters rewritten from the current master).  Reading the state clears the condition. */
 zero_status_t zero_read_state(zero_plan_t* plan, void* stream, zero_step_result_t* out);
@@ -716,12 +717,13 @@ zero_status_t zero_block_norm_backward(const zero_block_norm_t* a, void* workspa
                                        void* stream);
 
 /* Waits of the operators' kernels.  Those on shared-memory barriers are bounded, each by itself (zero_linear,
- * zero_gated and zero_muon 2 s, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
+ * zero_gated and zero_muon 2 s, zero_muon's for other blocks' tiles as ZERO_MUON_OPT_WAIT_LIMIT_NS says, and up to 2 s
+ * more for those that wait behind it, zero_block_norm 1 s; a block that meets one makes no more of them but to drain its copies, and a
  * product's block then gives its own 0.1 s).  Without a limit of their own are the hardware's: a cluster's barrier, which
  * every block of it reaches on every path, the allocation of tensor memory while another block on the SM
  * holds it, and the wait for the earlier work of the stream.  ZERO_ETIMEOUT if a bounded one ran out on the current device
- * since the last call, and clears that: nothing else tells of outputs that are not final.  Synchronises
- * `stream`. */
+ * since the last call, and clears that: nothing else tells of outputs that are not final, but for zero_muon_read.
+ * Synchronises `stream`. */
 zero_status_t zero_operators_check(void* stream);
 
 /* Elements of one tensor that share a pair of 8-bit scales; the moments' buffers hold every
@@ -835,6 +837,14 @@ zero_status_t zero_muon_create(const int64_t* rows, const int64_t* cols, int64_t
                                zero_muon_t** out);
 zero_status_t zero_muon_info(const zero_muon_t* h, zero_muon_info_t* out);
 
+/* Of the steps enqueued from now on. */
+#define ZERO_MUON_MAX_WAIT_NS 30000000000
+enum {
+    ZERO_MUON_OPT_WAIT_LIMIT_NS = 0  /* bound on a product's wait for the one before it, whose tiles other blocks make, in ns
+                                        up to ZERO_MUON_MAX_WAIT_NS (2e9; 0: no longer than it takes to look a few times) */
+};
+zero_status_t zero_muon_set_option(zero_muon_t* h, int option, int64_t value);
+
 /* Bind the caller's device buffers: per matrix the parameters (updated in place; params or an entry NULL: none), a
  * 16-bit copy (params16 or an entry NULL: none) and where X goes (updates or an entry NULL: nowhere; one of
  * parameters and update is needed); grads[r * n_matrices + i]: contribution r of matrix i; the momentum's two halves
@@ -862,7 +872,11 @@ zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, dou
 zero_status_t zero_muon_check(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);
 zero_status_t zero_muon_step_with(zero_muon_t* h, zero_plan_t* plan, const zero_muon_hyper_t* hyper, void* stream);
 
-/* t, skipped, skipped_total, finished and current after the work on `stream`, which it synchronises; grad_norm is -1. */
+/* t, skipped, skipped_total, finished and current after the work on `stream`, which it synchronises; grad_norm is -1.
+ * ZERO_ETIMEOUT, with *out filled, if a bounded wait of a step ran out since the last read, and clears that: that step's
+ * parameters, copies and updates may be partly written.  It counts as skipped, as do the handle's own steps until the read,
+ * and the current momentum is the one before it.  A plan's step that it was part of is discarded, and reports ZERO_ETIMEOUT
+ * itself; what other zero_*_step_with calls had moved in it stays moved.  Restore all of it from what was saved. */
 zero_status_t zero_muon_read(zero_muon_t* h, void* stream, zero_step_result_t* out);
 
 /* NULL is ignored. */

@@ -45,6 +45,8 @@ ZERO_MUON_MAX_MATRICES = 65536
 ZERO_MUON_MAX_SIZE = 4194304
 ZERO_MUON_MAX_SIDE = 65536
 ZERO_MUON_BLOCK = 256
+ZERO_MUON_OPT_WAIT_LIMIT_NS = 0
+ZERO_MUON_MAX_WAIT_NS = 30_000_000_000
 STATUS_NAMES = {0: "ZERO_OK", 1: "ZERO_EINVAL", 2: "ZERO_EALIGN", 3: "ZERO_ECUDA",
                 4: "ZERO_ESTATE", 5: "ZERO_ERANGE", 6: "ZERO_ETIMEOUT", 7: "ZERO_ENOMEM"}
 
@@ -62,8 +64,8 @@ EXPORTED = ["zero_plan_create", "zero_plan_create_per_param", "zero_plan_info", 
             "zero_block_norm", "zero_block_norm_workspace", "zero_block_norm_backward",
             "zero_adamw_create", "zero_adamw_info", "zero_adamw_bind", "zero_adamw_step",
             "zero_adamw_check", "zero_adamw_step_with", "zero_adamw_export", "zero_adamw_read", "zero_adamw_destroy",
-            "zero_muon_create", "zero_muon_info", "zero_muon_bind", "zero_muon_step", "zero_muon_check",
-            "zero_muon_step_with", "zero_muon_read", "zero_muon_destroy"]
+            "zero_muon_create", "zero_muon_info", "zero_muon_set_option", "zero_muon_bind", "zero_muon_step",
+            "zero_muon_check", "zero_muon_step_with", "zero_muon_read", "zero_muon_destroy"]
 ZERO_NOALLOC_SCRATCH_BYTES = 256
 
 
@@ -282,13 +284,14 @@ def lib() -> ctypes.CDLL:
         L.zero_adamw_destroy.argtypes = [_vp]
         L.zero_muon_create.argtypes = [_vp, _vp, _i64, _int, _int, ctypes.POINTER(_vp)]
         L.zero_muon_info.argtypes = [_vp, ctypes.POINTER(zero_muon_info_t)]
+        L.zero_muon_set_option.argtypes = [_vp, _int, _i64]
         L.zero_muon_bind.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
         L.zero_muon_step.argtypes = [_vp, ctypes.POINTER(zero_muon_hyper_t), ctypes.c_double, _vp]
         L.zero_muon_check.argtypes = [_vp, _vp, ctypes.POINTER(zero_muon_hyper_t), _vp]
         L.zero_muon_step_with.argtypes = [_vp, _vp, ctypes.POINTER(zero_muon_hyper_t), _vp]
         L.zero_muon_read.argtypes = [_vp, _vp, ctypes.POINTER(zero_step_result_t)]
-        for f in (L.zero_muon_create, L.zero_muon_info, L.zero_muon_bind, L.zero_muon_step, L.zero_muon_check,
-                  L.zero_muon_step_with, L.zero_muon_read):
+        for f in (L.zero_muon_create, L.zero_muon_info, L.zero_muon_set_option, L.zero_muon_bind, L.zero_muon_step,
+                  L.zero_muon_check, L.zero_muon_step_with, L.zero_muon_read):
             f.restype = st
         L.zero_muon_destroy.restype = None
         L.zero_muon_destroy.argtypes = [_vp]
@@ -427,7 +430,7 @@ def zero_offload_finish(plan: int, threads: int, stream: int = 0,
                         wait: bool = True) -> Optional[zero_step_result_t]:
     res = zero_step_result_t() if wait else None
     _check(lib().zero_offload_finish(plan, threads, stream or None,
-                                     ctypes.byref(res) if res is not None else None))
+                                     ctypes.byref(res) if res is not None else None), res)
     return res
 
 
@@ -652,6 +655,11 @@ def zero_muon_info(handle: int) -> zero_muon_info_t:
     info = zero_muon_info_t()
     _check(lib().zero_muon_info(handle, ctypes.byref(info)))
     return info
+
+
+def zero_muon_set_option(handle: int, option: int, value: int) -> None:
+    """ZERO_MUON_OPT_WAIT_LIMIT_NS; see include/zero.h."""
+    _check(lib().zero_muon_set_option(handle, option, int(value)))
 
 
 def zero_muon_bind(handle: int, params: Optional[Sequence[Optional[int]]], params16: Optional[Sequence[Optional[int]]],

@@ -128,7 +128,8 @@ struct DevState {
     uint32_t norm_valid;    // open step computed a norm
     uint32_t last_norm_valid;
     uint32_t error;         // bit 0: a barrier wait of the staged step ran out; bit 1: a drain
-                            // ran out; bit 2: a barrier wait of the staged gather ran out
+                            // ran out; bit 2: a barrier wait of the staged gather ran out; bit 3: a
+                            // wait of another optimizer's part of the step ran out
                             // (sticky until read; every step finished meanwhile is discarded)
     uint32_t pad32;
     int64_t pad;

@@ -181,6 +181,7 @@ struct GatedWork {
     }
     static constexpr bool kScout = false;
     __device__ __forceinline__ void done(const Item&) const {}
+    __device__ __forceinline__ void gave_up() const {}
 
     __device__ __forceinline__ void range(int worker, int, int& i, int& end, int& step) const
     {

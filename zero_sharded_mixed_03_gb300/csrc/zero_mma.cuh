@@ -426,20 +426,22 @@ __device__ __forceinline__ void add_tile(uint32_t stage, int lane, float scale, 
 //   aside(lane)                             without a scout: what that warp does
 //   kScout, bool begin(Item, Seen&)         true: a warp of its own finds the items and waits for what they wait for
 //                                           (false: given up), ahead of the others, which take them from a queue
+//   queue_ns()                              bound on their wait for an item there
 //   load(Item, kb, a, b, bar, rank)         those copies
 //   a_mn(Item, kb), b_mn(Item, kb), idesc(Item, kb)   how a stage's operands lie, and the product's descriptor
 //   prepare(Item, quad, half, rank, lane, Ahead&)      what a tile's end may load before its products are done
 //   finish(Item, Ahead&, acc, quad, half, stage, rank, lane)   TMEM lanes 32 quad on; alternate 32 columns a half
 //   done(Item)                                         by each of those warps after it
+//   gave_up()                                          by a thread whose wait ran out
 // CG = 2: the two blocks of a cluster form one 256 x BN tile: each stages 128 rows of A and BN / 2 of B, the first
 // one issues products that read both, and each keeps the accumulators of its own 128 rows.  CG = 1: 128 x BN.
 
 // mbar_wait with the clock read rarely: reading it twice before the first try costs more than most waits here take.
-__device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns = kGemmWaitNs)
 {
     for (int i = 0; i < 8; ++i)
         if (mbar_try(bar, parity)) return true;
-    return mbar_wait(bar, parity, kGemmWaitNs);
+    return mbar_wait(bar, parity, limit_ns);
 }
 
 template <int CG, int BN>
@@ -506,7 +508,7 @@ struct Tiles {
     {
         if constexpr (W::kScout) {
             const uint32_t slot = tile % kQueue, at = queue0 + slot * kItemBytes;
-            bool there = stage_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1);
+            bool there = stage_wait(queue_full0 + 8 * slot, (tile / kQueue) & 1, work.queue_ns());
             // a warp has the item or gives up as one: the item may come as some lanes' waits run out, and the others
             // would wait for them below
             if (whole_warp) there = __all_sync(0xFFFFFFFFu, there);
@@ -649,6 +651,7 @@ struct Tiles {
             // A wait ran out: say so, and give copies and products in flight time to end before the block's memory
             // is given back.
             atomicOr(error, 1u);
+            work.gave_up();
             const uint64_t t0 = global_ns();
             for (uint32_t i = 0; i < kWaitIterCap && global_ns() - t0 < 100000000ull; ++i) __nanosleep(1000);
         }

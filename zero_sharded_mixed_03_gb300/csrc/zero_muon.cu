@@ -63,6 +63,7 @@ struct MuonState {
     uint32_t last_skipped;
     uint32_t closed;        // blocks of the last pass that are done
     int64_t t, skipped, finished;
+    uint32_t timeout;       // a wait of a step ran out since the last read, and its parameters may be partly moved
 };
 static_assert(sizeof(MuonState) <= 256, "MuonState fits its slot");
 
@@ -316,10 +317,13 @@ __global__ void __launch_bounds__(kThreads, kStartBlocks) muon_start_kernel(cons
 
 // ------------------------------------------------------------------ the parameters
 
-// Is the step left out?
+// Is the step left out?  A wait that runs out says so to it too (gave_up), and to the steps that follow until it is read.
 __device__ __forceinline__ bool left_out(const MuonState* st, const DevState* plan)
 {
-    if (!plan) return *(const volatile uint32_t*)&st->flag != 0;
+    if (!plan) {
+        const volatile MuonState* s = st;
+        return (s->flag | s->timeout) != 0;
+    }
     const volatile DevState* p = plan;
     return (p->flag | p->error) != 0;
 }
@@ -384,6 +388,7 @@ struct ProductParams {
     DevState* plan;              // a sharded step that this one is part of, or NULL
     int32_t how, bf;             // ZERO_MUON_SCALE_*; the 16-bit type is bf16
     float lr, decay;             // lr weight_decay
+    uint64_t wait_ns;            // bound on a wait for the product before
     int32_t first, last;         // products that are made
     Op ops[kMaxPhases];          // ops[i - first] is product i
 };
@@ -481,13 +486,13 @@ struct MuonWork {
     }
 
     // Until every part of the product before is stored: a bounded wait.  A fence follows it.
-    __device__ __forceinline__ static bool wait_before(const Item& I)
+    __device__ __forceinline__ bool wait_before(const Item& I) const
     {
         if (!I.before || load_relaxed(I.before) >= I.want) return true;
         const uint64_t t0 = global_ns();
         for (uint32_t i = 0; i < kWaitIterCap; ++i) {
             if (load_relaxed(I.before) >= I.want) return true;
-            if (i % 16 == 15 && global_ns() - t0 > kGemmWaitNs) break;
+            if (i % 16 == 15 && global_ns() - t0 > P.wait_ns) break;
         }
         return false;
     }
@@ -528,6 +533,17 @@ struct MuonWork {
     {
         sent_all();
         if (elect_one()) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(I.counter) : "memory");
+    }
+
+    // The scout's wait and what may keep it from the next.
+    __device__ __forceinline__ uint64_t queue_ns() const { return P.wait_ns + kGemmWaitNs; }
+
+    // Before this block counts itself as done (muon_product_kernel), so that what closes the step sees it.
+    __device__ __forceinline__ void gave_up() const
+    {
+        atomicOr(&P.st->timeout, 1u);
+        if (P.plan) atomicOr(&P.plan->error, 8u);
+        __threadfence();
     }
 
     // Is an inner block below the diagonal block (kBM * CG wide) of a symmetric operand's rows from `row` on?
@@ -760,7 +776,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kGemmThreads, 1) mu
     T.template open<true>(smem_raw);
     after_earlier_work();
     T.run(MuonWork<CG, BN>{P}, &g_muon_error);
-    if (threadIdx.x == 0 && atomicAdd(&P.st->closed, 1u) == gridDim.x - 1) close_step(P.st, left_out(P.st, P.plan));
+    if (threadIdx.x == 0 && atomicAdd(&P.st->closed, 1u) == gridDim.x - 1) {
+        __threadfence();
+        close_step(P.st, left_out(P.st, P.plan));
+    }
 }
 
 }  // namespace
@@ -790,6 +809,7 @@ struct zero_muon {
     int64_t checked_in = 0, stepped_in = 0;
     double checked_mu = 0.0;
     int64_t checked_flags = 0;
+    int64_t wait_ns = (int64_t)zero::kGemmWaitNs;    // ZERO_MUON_OPT_WAIT_LIMIT_NS
 };
 
 namespace zero {
@@ -1086,6 +1106,7 @@ zero_status_t launch_rest(const zero_muon* h, MuonParams P, const zero_muon_hype
         Q.bf = h->dtype16 == ZERO_BF16;
         Q.lr = (float)hyper.lr;
         Q.decay = (float)(hyper.lr * hyper.weight_decay);
+        Q.wait_ns = (uint64_t)h->wait_ns;
         // one step alone of a handle that makes two at once is the first of the single ones
         const bool pair = h->pair && hyper.steps >= 2;
         Q.first = h->pair && !pair ? kPairPhases : 0;
@@ -1273,6 +1294,21 @@ catch (...) {
     return exception_status("zero_muon_info");
 }
 
+zero_status_t zero_muon_set_option(zero_muon_t* h, int option, int64_t value)
+try {
+    if (!h) return fail(ZERO_EINVAL, "zero_muon_set_option: NULL handle");
+    switch (option) {
+    case ZERO_MUON_OPT_WAIT_LIMIT_NS:
+        if (value < 0 || value > ZERO_MUON_MAX_WAIT_NS) return fail(ZERO_EINVAL, "zero_muon_set_option: the wait limit must be in 0 .. ZERO_MUON_MAX_WAIT_NS");
+        h->wait_ns = value;
+        return ZERO_OK;
+    default: return fail(ZERO_EINVAL, "zero_muon_set_option: unknown option");
+    }
+}
+catch (...) {
+    return exception_status("zero_muon_set_option");
+}
+
 zero_status_t zero_muon_bind(zero_muon_t* h, float* const* params, void* const* params16, void* const* updates, const void* const* grads,
                              float* const momentum[2], void* workspace, int64_t t, void* stream)
 try {
@@ -1448,6 +1484,11 @@ try {
     plan->moved_in = plan->step_no;
     st = launch_rest(h, P, *hyper, R, static_cast<cudaStream_t>(stream));
     if (st != ZERO_OK) return st;
+    if (plan->offload) {
+        // the host's update reads the step's state behind this event, and a wait that runs out here discards the step
+        const cudaError_t e = cudaEventRecord((cudaEvent_t)plan->off_flag_event, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "zero_muon_step_with: event");
+    }
     h->stepped_in = plan->step_no;
     return ZERO_OK;
 }
@@ -1474,6 +1515,12 @@ try {
     out->skipped_total = state.skipped;
     out->finished = state.finished;
     out->grad_norm = -1.0;
+    if (state.timeout) {
+        e = cudaMemsetAsync(&static_cast<MuonState*>(h->workspace)->timeout, 0, sizeof(state.timeout), s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e != cudaSuccess) return cuda_fail(e, "zero_muon_read: clearing the state");
+        return fail(ZERO_ETIMEOUT, "zero_muon_read: a wait of a step's products ran out; its parameters may be partly moved, and the steps since then were left out");
+    }
     return ZERO_OK;
 }
 catch (...) {

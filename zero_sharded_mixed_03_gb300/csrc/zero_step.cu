@@ -578,7 +578,10 @@ zero_status_t read_state(zero_plan* p, cudaStream_t s, zero_step_result_t* out)
         e = cudaMemsetAsync(&dev_state(p)->error, 0, sizeof(host.error), s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
         if (e != cudaSuccess) return cuda_fail(e, "clearing the error word");
-        return fail(ZERO_ETIMEOUT, (host.error & 2u)
+        return fail(ZERO_ETIMEOUT, (host.error & 8u)
+                                       ? "a wait of another optimizer's part of the step ran out, whose parameters may be "
+                                         "partly moved; the steps finished since the last read were discarded"
+                                   : (host.error & 2u)
                                        ? "a barrier wait and the drain of the bulk-staged step ran out; "
                                          "the steps finished since the last read were discarded"
                                        : "a barrier wait of the bulk-staged step ran out; the steps "
@@ -1702,8 +1705,9 @@ try {
     }
     // deferred reductions (ZERO_OPT_OFFLOAD_DEFER): the decision is known; a clean step streams
     // every call's gradient to the host now, a skipped one needs none of it
+    const bool left_out = (host.flag | host.error) != 0;      // as the commit decides
     if (!p->off_deferred.empty()) {
-        if (host.flag == 0)
+        if (!left_out)
             for (const zero_plan::OffloadCall& c : p->off_deferred) {
                 e = offload_reduce_groups(p, c.contribs.data(), c.segs, p->off_segs.size(), s);
                 if (e != cudaSuccess) return cuda_fail(e, "zero_offload_finish: reduce-to-host launch");
@@ -1739,8 +1743,8 @@ try {
         p->host_pool = worker_pool_create(nt);
         p->release_hook = release_plan_resources;
     }
-    if (host.flag != 0) {
-        // skipped step: every gradient lands first, then the re-cast of the unchanged master
+    if (left_out) {
+        // skipped or discarded step: every gradient lands first, then the re-cast of the unchanged master
         e = cudaStreamSynchronize(s);
         if (e != cudaSuccess) return cuda_fail(e, "zero_offload_finish: waiting for the reductions");
         cpu_adamw(p->host_pool, spans, k9, p->dtype16, true, nt);
