@@ -837,11 +837,14 @@ zero_status_t zero_muon_create(const int64_t* rows, const int64_t* cols, int64_t
                                zero_muon_t** out);
 zero_status_t zero_muon_info(const zero_muon_t* h, zero_muon_info_t* out);
 
-/* Of the steps enqueued from now on. */
 #define ZERO_MUON_MAX_WAIT_NS 30000000000
 enum {
-    ZERO_MUON_OPT_WAIT_LIMIT_NS = 0  /* bound on a product's wait for the one before it, whose tiles other blocks make, in ns
-                                        up to ZERO_MUON_MAX_WAIT_NS (2e9; 0: no longer than it takes to look a few times) */
+    ZERO_MUON_OPT_WAIT_LIMIT_NS = 0, /* bound on a product's wait for the one before it, whose tiles other blocks make, in ns
+                                        up to ZERO_MUON_MAX_WAIT_NS (2e9; 0: no longer than it takes to look a few times), of
+                                        the steps enqueued from now on */
+    ZERO_MUON_OPT_SMS = 1            /* SMs that the products take at most, from the next zero_muon_bind on: 0 (default) as
+                                        many as they have use for, else at least 2.  The same results; graphs of steps
+                                        that were captured before that bind are captured anew */
 };
 zero_status_t zero_muon_set_option(zero_muon_t* h, int option, int64_t value);
 
@@ -859,7 +862,8 @@ zero_status_t zero_muon_bind(zero_muon_t* h, float* const* params, void* const* 
 /* One step over every matrix.  Where the sum of squares of a matrix's u is not finite (a contribution is not, or fp32's
  * range is left) the whole step is left out: parameters, copies, updates and the current momentum stay.  ZERO_ERANGE
  * for coefficients that let singular values of at most 1 grow beyond 8, or a step's polynomial of them beyond 16384.
- * The products are one cooperative launch, whose blocks (up to one on each SM) run when all of them can. */
+ * The products are one cooperative launch, whose blocks (up to one on each SM that zero_muon_bind found room on) run when
+ * all of them can. */
 zero_status_t zero_muon_step(zero_muon_t* h, const zero_muon_hyper_t* hyper, double loss_scale, void* stream);
 
 /* A step that h makes together with a plan's, applied or left out as one, with the plan's loss scale (as

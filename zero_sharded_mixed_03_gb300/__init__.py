@@ -45,7 +45,7 @@ ZERO_MUON_MAX_MATRICES = 65536
 ZERO_MUON_MAX_SIZE = 4194304
 ZERO_MUON_MAX_SIDE = 65536
 ZERO_MUON_BLOCK = 256
-ZERO_MUON_OPT_WAIT_LIMIT_NS = 0
+ZERO_MUON_OPT_WAIT_LIMIT_NS, ZERO_MUON_OPT_SMS = range(2)
 ZERO_MUON_MAX_WAIT_NS = 30_000_000_000
 STATUS_NAMES = {0: "ZERO_OK", 1: "ZERO_EINVAL", 2: "ZERO_EALIGN", 3: "ZERO_ECUDA",
                 4: "ZERO_ESTATE", 5: "ZERO_ERANGE", 6: "ZERO_ETIMEOUT", 7: "ZERO_ENOMEM"}
@@ -658,7 +658,7 @@ def zero_muon_info(handle: int) -> zero_muon_info_t:
 
 
 def zero_muon_set_option(handle: int, option: int, value: int) -> None:
-    """ZERO_MUON_OPT_WAIT_LIMIT_NS; see include/zero.h."""
+    """ZERO_MUON_OPT_WAIT_LIMIT_NS, ZERO_MUON_OPT_SMS; see include/zero.h."""
     _check(lib().zero_muon_set_option(handle, option, int(value)))
 
 

@@ -796,7 +796,9 @@ struct zero_muon {
     bool pair = false;
     std::vector<zero::Piece> chunks, groups, tiles;   // tiles: each worker's, in the order of the products
     std::vector<int32_t> bounds;
-    int workers = 0;
+    int workers = 0;             // that the tiles are dealt to where every SM can be had
+    int running = 0;             // the bound ones: as many as are resident at one time, or as the option says
+    int64_t most_sms = 0;        // ZERO_MUON_OPT_SMS
     // the workspace's pieces
     int64_t at_tensors = 0, at_grads = 0, at_chunks = 0, at_groups = 0, at_tiles = 0, at_bounds = 0, at_counters = 0, at_slots = 0, at_scale = 0, at_tickets = 0,
             at_data = 0, bytes = 0;
@@ -929,10 +931,10 @@ int64_t square_tiles(const Shape& S, int64_t m)
 
 // Every product's tiles dealt to the workers (blocks, or pairs), each to the one that is free first once the product
 // before is complete: as many whole steps as a call may ask for, since the list of fewer is its beginning.  Returns the
-// time that five steps take; nothing is dealt where the work alone would take `limit`.
-double deal_tiles(const zero_muon* h, const Shape& S, double limit, std::vector<Piece>* out, std::vector<int32_t>* bounds)
+// time that five steps take; nothing is dealt where the work alone would take `limit`.  A tile's result does not depend
+// on who makes it.
+double deal_tiles(const zero_muon* h, const Shape& S, int64_t most_workers, double limit, std::vector<Piece>* out, std::vector<int32_t>* bounds)
 {
-    const int cg = S.cg;
     const size_t n = h->rows.size();
     std::vector<size_t> order;                // longest inner dimension first
     int64_t most = 0;
@@ -942,7 +944,7 @@ double deal_tiles(const zero_muon* h, const Shape& S, double limit, std::vector<
         most += tile_rows(S, h->rows[i]) * tile_cols(S, h->cols[i]);
     }
     std::stable_sort(order.begin(), order.end(), [&](size_t a, size_t b) { return std::max(h->rows[a], h->cols[a]) > std::max(h->rows[b], h->cols[b]); });
-    const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(kGb300Sms / cg, most));
+    const int workers = (int)std::max<int64_t>(1, std::min(most_workers, most));
     const int phases = phase_count(h->pair, ZERO_MUON_MAX_STEPS), five = phase_count(h->pair, 5);
     double work = 0.0;
     for (const size_t i : order) {
@@ -1070,7 +1072,7 @@ zero_status_t launch_products(const zero_muon* h, const ProductParams& P, cudaSt
     const cudaError_t set = allow_shared<muon_product_kernel<CG, BN>>(kShared);
     if (set != cudaSuccess) return cuda_fail(set, "zero_muon: shared memory");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CG * h->workers));
+    cfg.gridDim = dim3((unsigned)(CG * h->running));
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = kShared;
     cfg.stream = s;
@@ -1081,6 +1083,20 @@ zero_status_t launch_products(const zero_muon* h, const ProductParams& P, cudaSt
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, muon_product_kernel<CG, BN>, P);
     return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "zero_muon: launch");
+}
+
+// Workers of the products that the current device has room for at one time: a cooperative launch of more is refused.
+template <int CG, int BN>
+cudaError_t resident_workers(int* workers)
+{
+    constexpr int kShared = Tiles<CG, BN>::kScoutSmem;
+    cudaError_t e = allow_shared<muon_product_kernel<CG, BN>>(kShared);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)CG);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kShared;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(workers, muon_product_kernel<CG, BN>, &cfg);
+    return e;
 }
 
 // The first X, the iterations and the parameters.
@@ -1242,7 +1258,7 @@ try {
         for (const Shape& S : kShapes) {
             std::vector<Piece> tiles;
             std::vector<int32_t> bounds;
-            const double us = deal_tiles(h.get(), S, best, &tiles, &bounds);
+            const double us = deal_tiles(h.get(), S, kGb300Sms / S.cg, best, &tiles, &bounds);
             if (us >= best) continue;
             best = us;
             h->cg = S.cg;
@@ -1301,6 +1317,10 @@ try {
     case ZERO_MUON_OPT_WAIT_LIMIT_NS:
         if (value < 0 || value > ZERO_MUON_MAX_WAIT_NS) return fail(ZERO_EINVAL, "zero_muon_set_option: the wait limit must be in 0 .. ZERO_MUON_MAX_WAIT_NS");
         h->wait_ns = value;
+        return ZERO_OK;
+    case ZERO_MUON_OPT_SMS:
+        if (value < 0 || value == 1) return fail(ZERO_EINVAL, "zero_muon_set_option: SMs must be 0 (all) or at least 2");
+        h->most_sms = value;
         return ZERO_OK;
     default: return fail(ZERO_EINVAL, "zero_muon_set_option: unknown option");
     }
@@ -1403,11 +1423,29 @@ try {
     };
     put(h->at_chunks, h->chunks);
     put(h->at_groups, h->groups);
-    put(h->at_tiles, h->tiles);
-    if (!h->bounds.empty()) std::memcpy(image.data() + h->at_bounds, h->bounds.data(), h->bounds.size() * sizeof(int32_t));
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "zero_muon_bind: cudaGetDevice");
+    int running = h->workers;
+    if (running > 0) {
+        int resident = 0;
+        e = h->cg == 2 ? resident_workers<2, 256>(&resident) : h->bn == 128 ? resident_workers<1, 128>(&resident) : resident_workers<1, 64>(&resident);
+        if (e != cudaSuccess) return cuda_fail(e, "zero_muon_bind: the blocks that the device has room for");
+        if (resident < 1) return fail(ZERO_ECUDA, "zero_muon_bind: the device has no room for a block of the products");
+        running = std::min(running, resident);
+        if (h->most_sms > 0) running = std::min(running, (int)std::max<int64_t>(1, std::min<int64_t>(h->most_sms, kGb300Sms) / h->cg));
+    }
+    std::vector<Piece> fewer_tiles;
+    std::vector<int32_t> fewer_bounds;
+    const bool fewer = running < h->workers;
+    if (fewer) {
+        // the same tiles among the workers that there are
+        for (const Shape& S : kShapes)
+            if (S.cg == h->cg && S.bn == h->bn) deal_tiles(h, S, running, 1e30, &fewer_tiles, &fewer_bounds);
+    }
+    put(h->at_tiles, fewer ? fewer_tiles : h->tiles);
+    const std::vector<int32_t>& bounds = fewer ? fewer_bounds : h->bounds;
+    if (!bounds.empty()) std::memcpy(image.data() + h->at_bounds, bounds.data(), bounds.size() * sizeof(int32_t));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t skip = t == -1 ? 256 : 0;       // -1: the state's slot stays
     e = cudaMemcpyAsync(ws + skip, image.data() + skip, image.size() - skip, cudaMemcpyHostToDevice, s);
@@ -1417,6 +1455,7 @@ try {
     h->workspace = workspace;
     h->checked_in = 0;                           // what a check left there is gone
     h->device = dev;
+    h->running = running;
     h->bound = true;
     return ZERO_OK;
 }
