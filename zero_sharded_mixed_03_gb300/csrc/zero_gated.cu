@@ -850,8 +850,8 @@ double tile_us(const Shape& S, int64_t kb, int splits)
     return (double)kb * S.block_us + (S.cg == 2 ? 3.8 : 1.5) + (splits > 1 ? (S.cg == 2 ? 5.0 : 2.5) + 0.15 * splits : 0.0);
 }
 
-// May n tiles of kb inner blocks be in `ways` parts?  Each has four blocks at least; a worker at most 8 parts, 160 MB of
-// sums in all.
+// May n tiles of kb inner blocks be in `ways` parts?  Each has four blocks at least; a worker at most 8 parts of either
+// kind of tile, so that the sums take at most 160 MB for each kind: 320 where dx and the weights' gradients are both in parts.
 bool divides(const Shape& S, int64_t n, int64_t kb, int ways, int64_t* per)
 {
     *per = div_up(std::max<int64_t>(kb, 1), ways);
