@@ -831,8 +831,10 @@ typedef struct {
  *   p <- p - lr weight_decay p;  p <- p - lr s X            (s: ZERO_MUON_SCALE_*)
  * fp32 parameters, row-major and dense, and momentum; contributions, an optional copy of each parameter and an
  * optional copy of X in dtype16.  The products' operands are fp16 whatever dtype16 is, in its range by powers of two,
- * with fp32 sums: X is within about 0.3 % (2-norm) of the formula's where its smallest singular values are not far
- * below rounding.  Host memory only; zero_muon_destroy. */
+ * with fp32 sums.  With the usual five steps X is within about 0.3 % (2-norm) of the formula's for dense matrices whose
+ * sides are 64 and more, 1.1 % where few singular values are all there is (3 x 512; 4 rows of 256 not zero); one direction
+ * over noise of 1e-3 of it and less, whose singular values are near rounding, 0.5 %, and 1.4 % in the Frobenius norm.
+ * Host memory only; zero_muon_destroy. */
 zero_status_t zero_muon_create(const int64_t* rows, const int64_t* cols, int64_t n_matrices, int n_contribs, int dtype16,
                                zero_muon_t** out);
 zero_status_t zero_muon_info(const zero_muon_t* h, zero_muon_info_t* out);

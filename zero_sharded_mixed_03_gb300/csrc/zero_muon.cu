@@ -17,8 +17,10 @@
 // bounded: ||X||_2 <= 1 at first, and the coefficients give the rest).  Rounding to bf16's 8 bits costs 1 to 3 % of the
 // result, as small singular values grow by a^steps (485) and what rounding adds to them grows with them; fp16's 11 bits
 // 0.13 to 0.4 %, and with the first iterates as sums of two fp16 numbers (the products take the first; a X, which is
-// nearly all of small singular values' growth, both) 0.1 to 0.3 %.  tf32 has fp16's 11 bits at half its rate.  Sums are
-// fp32.
+// nearly all of small singular values' growth, both) 0.1 to 0.3 % (2-norm, dense matrices with sides of 64 and more).  One
+// direction over 1 % of noise, 512 x 512: 0.26 % instead of 2.7, for which the second number is there.  Few singular values
+// have up to 1.1 % either way: 3 x 512, or 4 rows of 256 that are not zero.  tf32 has fp16's 11 bits at half its rate.
+// Sums are fp32.
 //
 // Measured on one GB300: two layers of a 2048-wide GPT's matrices (101M elements) from 16 contributions 2,913 us: the
 // contributions 575 (7.0 TB/s), the first X 177 (6.8 TB/s), the products 1,900 as long as the clocks hold; a 4096 x 4096
