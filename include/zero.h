@@ -781,8 +781,8 @@ zero_status_t zero_adamw_step(zero_adamw_t* h, const zero_hyper_t* hyper, double
  * is offloaded, but before every zero_adamw_step_with and zero_muon_step_with of it: what those have moved could not be
  * left out any more.  zero_adamw_step_with applies h's update, gradients over the plan's
  * loss scale and times its clipping coefficient, unless the plan's step is marked or a bounded wait of it ran out.
- * zero_adamw_read: grad_norm is -1, the plan's result has the norm of both.  ZERO_ESTATE out of this order.  Not
- * with zero_step_units_overlapped, which finishes the step itself. */
+ * zero_adamw_read: grad_norm is -1, the plan's result has the norm of both.  ZERO_ESTATE out of this order, and where a
+ * bind came between.  Not with zero_step_units_overlapped, which finishes the step itself. */
 zero_status_t zero_adamw_check(zero_adamw_t* h, zero_plan_t* plan, void* stream);
 zero_status_t zero_adamw_step_with(zero_adamw_t* h, zero_plan_t* plan, const zero_hyper_t* hyper, void* stream);
 

@@ -33,8 +33,11 @@ class Tensors:
         info = Z.zero_adamw_info(self.h)
         self.m, self.v, self.ws = (torch.zeros(max(16, n), dtype=torch.uint8, device="cuda")
                                    for n in (info.moment_bytes, info.moment_bytes, info.workspace_bytes))
+        self.bind(0)
+
+    def bind(self, t):
         Z.zero_adamw_bind(self.h, [t.data_ptr() for t in self.p], None, [t.data_ptr() for t in self.g],
-                          self.m.data_ptr(), self.v.data_ptr(), None, self.ws.data_ptr(), 0, stream())
+                          self.m.data_ptr(), self.v.data_ptr(), None, self.ws.data_ptr(), t, stream())
 
     def state(self):
         torch.cuda.synchronize()
@@ -161,3 +164,25 @@ def test_a_check_after_a_part_is_refused(bad):
     finally:
         j.close()
         other.close()
+
+
+def test_a_bind_after_the_check_is_another_check():
+    """A bind may bring gradients that the check has not seen."""
+    j, alone, h, s = Three(), Tensors(), Z.hyper(), stream()
+    plan = j.g.plan
+    try:
+        Z.zero_adamw_check(j.tensors.h, plan, s)
+        Z.zero_step(plan, j.ptrs, -1, h, s)
+        j.tensors.bind(-1)
+        refused(Z.zero_adamw_step_with, j.tensors.h, plan, h, s)
+        Z.zero_adamw_check(j.tensors.h, plan, s)
+        Z.zero_adamw_step_with(j.tensors.h, plan, h, s)
+        j.tensors.bind(-1)
+        refused(Z.zero_adamw_check, j.tensors.h, plan, s)
+        refused(Z.zero_adamw_step_with, j.tensors.h, plan, h, s)
+        assert Z.zero_step_finish(plan, s).t == 1
+        Z.zero_adamw_step(alone.h, h, 1.0, s)
+        assert all(torch.equal(a, b) for a, b in zip(alone.state(), j.tensors.state()))
+    finally:
+        j.close()
+        alone.close()

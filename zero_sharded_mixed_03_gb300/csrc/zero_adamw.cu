@@ -1095,6 +1095,7 @@ try {
     h->v = v;
     h->scales = scales;
     h->workspace = workspace;
+    h->checked_in = 0;                           // other gradients than a check saw
     h->device = dev;
     h->bound = true;
     return ZERO_OK;
