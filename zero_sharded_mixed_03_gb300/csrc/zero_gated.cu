@@ -11,8 +11,8 @@
 // dimension, parts of it are tiles of their own, summed in order by the warp that ends last.
 //
 // Measured on one GB300 (cuBLAS bf16: 1,939 TFLOP/s in a burst, 1,731 sustained under the power cap): 8192 tokens
-// 4096 -> 11008 with g and u kept 825 to 884 us, 1,670 to 1,790 TFLOP/s; their gradients 1,853 to 1,948, of which 133 are dg
-// and du (HBM); 2048 tokens 2048 -> 8192 193 (dg and du 26, the rest 145 alone, tensor cores busy 89 %); 777 tokens
+// 4096 -> 11008 with g and u kept 825 to 888 us, 1,660 to 1,790 TFLOP/s; their gradients 1,853 to 1,966, of which 133 are dg
+// and du (HBM); 2048 tokens 2048 -> 8192 192 to 197 (dg and du 26, the rest 145 alone, tensor cores busy 89 %); 777 tokens
 // 1001 -> 1603, every row off the 16-byte grid, 36; one token 4096 -> 11008 29.5 (6.1 TB/s), 24 tokens 2048 -> 8192
 // 14.7.  Tiles of few inner blocks are bound by their ends: 256 x 256 take 5 us with g and u kept, as long as 16 blocks.
 #include <cmath>

@@ -22,9 +22,9 @@
 // have up to 1.1 % either way: 3 x 512, or 4 rows of 256 that are not zero.  tf32 has fp16's 11 bits at half its rate.
 // Sums are fp32.
 //
-// Measured on one GB300: two layers of a 2048-wide GPT's matrices (101M elements) from 16 contributions 2,913 us: the
-// contributions 575 (7.0 TB/s), the first X 177 (6.8 TB/s), the products 1,900 as long as the clocks hold; a 4096 x 4096
-// and an 11008 x 4096 matrix from 8 3,030; three layers 256 wide from four 131, 16 products of 5.6 us one after another.
+// Measured on one GB300: two layers of a 2048-wide GPT's matrices (101M elements) from 16 contributions 2,913 to 2,978
+// us: the contributions 575 (7.0 TB/s), the first X 177 (6.8 TB/s), the products 1,900 as long as the clocks hold; a 4096 x 4096
+// and an 11008 x 4096 matrix from 8 3,012 to 3,112; three layers 256 wide from four 131, 16 products of 5.6 us one after another.
 // The products are bound by power: of the library's fp16 products of normal numbers (1,629 TFLOP/s sustained; 1,731 in
 // bf16) they make 0.9, and the tensor cores are busy 81 % of the cycles.
 #include <cmath>
